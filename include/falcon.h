@@ -225,6 +225,107 @@ int falcon_bwd(int variant, const void* q, const void* k, const void* v, const f
  * and 3 KiB of per-token scalars); 0 for invalid or unsupported arguments. */
 size_t falcon_bwd_workspace_bytes(int variant, const falcon_dims_t* dims, int chunk);
 
+/* ------------------------------------------------------------------------------------------------
+ * Operators beside the scan, on the same [B,H,T,d] tensors: a gated linear recurrence (the diagonal
+ * counterpart of the fast-weight update) and the group norm of a head's channels with an activation
+ * and a gate (the normalisation of a denominator-free read before the output projection).
+ *
+ * Layout: a tensor [B,H,T,d] has d contiguous channels; `strides` (host memory) gives its batch, head
+ * and token strides in elements, three int64 per tensor in the order each function lists, or is NULL
+ * when every tensor is dense. So the projection's layout [B,T,H,d] and column blocks of one wider
+ * product are passed as they are. Strides are >= 0; that of an axis of length 1 is ignored; an input's
+ * may be 0 (one row read for many places: a gradient is then that of every place, not their sum).
+ * A written tensor has every element at an address of its own. Written tensors may interleave with
+ * other arguments in one buffer (column blocks); two that could share an element are
+ * FALCON_ERR_INVALID_ARG. Pointers are aligned to their element; where pointers, strides and d are also
+ * multiples of 16 bytes (8 for bf16 in the recurrence) the kernels move vectors, else single elements.
+ * lengths: NULL, or device int32 [B]: sequence b has min(max(lengths[b], 0), T) tokens. Rows behind them
+ * are not read (they may hold anything) and are written as zeros.
+ * The calls use the current device, keep no scratch of their own and may run at the same time on any
+ * streams. Sums run in a fixed order: the same call gives the same bits.
+ */
+typedef struct {
+    int64_t batch;   /* B >= 0                                                        */
+    int64_t heads;   /* H >= 0                                                        */
+    int64_t seqlen;  /* 0 <= T < 2^30                                                 */
+    int64_t d;       /* channels of a head, 1 <= d < 2^31 (group norm: d <= 1024)     */
+    int32_t dtype;   /* falcon_dtype_t of every tensor that has strides               */
+    int32_t reserved; /* 0                                                            */
+} falcon_seq_dims_t;
+
+typedef enum {
+    FALCON_GATE_DECAY = 0,   /* a = exp(g),     u = x          (g <= 0: a log decay)  */
+    FALCON_GATE_SIGMOID = 1, /* a = sigmoid(g), u = x                                 */
+    FALCON_GATE_MIX = 2      /* a = sigmoid(g), u = (1 - a) x                         */
+} falcon_gate_t;
+
+/*
+ * falcon_glr_fwd — gated linear recurrence: per channel h_t = a_t h_{t-1} + u_t, out_t = h_t.
+ * A gate g = -inf (a = 0) starts a new document in the middle of a sequence.
+ *   x, g      [B,H,T,d] dtype         input and gate
+ *   h0        fp32 [B,H,d] or NULL (zero state)
+ *   lengths   see above
+ *   out       [B,H,T,d] dtype
+ *   h_final   fp32 [B,H,d] or NULL: the state behind each sequence's last token (h0 when it has none);
+ *             may be the same pointer as h0
+ *   strides   of x, g, out (9 values) or NULL
+ * T = 1 is a decoding step; calls that continue from h_final equal one call over all tokens.
+ */
+int falcon_glr_fwd(int gate, const void* x, const void* g, const float* h0, const int32_t* lengths, void* out,
+                   float* h_final, const falcon_seq_dims_t* dims, const int64_t* strides, void* stream);
+
+/*
+ * falcon_glr_bwd — gradients of L = sum(out * dout) + sum(h_final * dh_final) of one falcon_glr_fwd call.
+ *   x, g, h0, lengths   as passed to falcon_glr_fwd (x may be NULL unless the gate is FALCON_GATE_MIX)
+ *   out       [B,H,T,d] dtype         what falcon_glr_fwd wrote: h_{t-1} is read from it
+ *   dout      [B,H,T,d] dtype
+ *   dh_final  fp32 [B,H,d] or NULL (zero)
+ *   dx, dg    [B,H,T,d] dtype         (rounded once, to the inputs' type)
+ *   dh0       fp32 [B,H,d] or NULL
+ *   strides   of x, g, out, dout, dx, dg (18 values) or NULL
+ */
+int falcon_glr_bwd(int gate, const void* x, const void* g, const void* out, const float* h0, const int32_t* lengths,
+                   const void* dout, const float* dh_final, void* dx, void* dg, float* dh0,
+                   const falcon_seq_dims_t* dims, const int64_t* strides, void* stream);
+
+typedef enum {
+    FALCON_ACT_NONE = 0,
+    FALCON_ACT_SILU = 1,
+    FALCON_ACT_GELU = 2,    /* v Phi(v), Phi the normal distribution function         */
+    FALCON_ACT_SIGMOID = 3
+} falcon_act_t;
+
+/*
+ * falcon_gn_fwd — per token and head, over its d channels: n = weight (x - mean) / sqrt(var + eps) + bias;
+ * y = act(n), or n * act(z) with a gate z. The group is one token's head (each output depends on its own
+ * token alone); with x in the scan's layout and y in the projection's the call also transposes.
+ *   x, y      [B,H,T,d] dtype
+ *   z         [B,H,T,d] dtype or NULL
+ *   weight, bias  fp32 [H,d] or NULL (1 and 0)
+ *   strides   of x, z, y (9 values; z's ignored without a gate) or NULL
+ *   eps       > 0
+ */
+int falcon_gn_fwd(int act, const void* x, const void* z, const float* weight, const float* bias,
+                  const int32_t* lengths, void* y, const falcon_seq_dims_t* dims, const int64_t* strides, float eps,
+                  void* stream);
+
+/*
+ * falcon_gn_bwd — gradients of L = sum(y * dy) of one falcon_gn_fwd call.
+ *   dx        [B,H,T,d] dtype
+ *   dz        [B,H,T,d] dtype; NULL if and only if z is
+ *   dweight, dbias  fp32 [H,d] or NULL: written, not added to
+ *   strides   of x, z, dy, dx, dz (15 values) or NULL
+ *   workspace at least falcon_gn_bwd_workspace_bytes(dims) bytes, 256-byte aligned; may be NULL when
+ *             dweight and dbias are
+ */
+int falcon_gn_bwd(int act, const void* x, const void* z, const float* weight, const float* bias,
+                  const int32_t* lengths, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                  const falcon_seq_dims_t* dims, const int64_t* strides, float eps, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of falcon_gn_bwd (partial sums of dweight and dbias); 0 for invalid dims. Host only. */
+size_t falcon_gn_bwd_workspace_bytes(const falcon_seq_dims_t* dims);
+
 /* ABI version of this header: 4. */
 int falcon_abi_version(void);
 

@@ -25,6 +25,9 @@ FALCON_ERR_MISALIGNED = 3
 FALCON_ERR_CUDA = 4
 FALCON_ERR_DEVICE_TIMEOUT = 5
 
+GLR_GATES = {"decay": 0, "sigmoid": 1, "mix": 2}
+GN_ACTS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
+
 VARIANTS = {"falcon1": FALCON_1, "falcon1a": FALCON_1A, "falcon2": FALCON_2, "falcon2a": FALCON_2A,
             "falcon3": FALCON_3, "falcon3a": FALCON_3A}
 
@@ -46,12 +49,29 @@ class FalconDims(ctypes.Structure):
 
 assert ctypes.sizeof(FalconDims) == 64
 
+
+class FalconSeqDims(ctypes.Structure):
+    """falcon_seq_dims_t: the sizes of the strided [B,H,T,d] operators."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(FalconSeqDims) == 40
+
 _lock = threading.Lock()
 _lib = None
 
 EXPORTED = ("falcon_fwd", "falcon_workspace_bytes", "falcon_fwd_static", "falcon_tail_bytes",
             "falcon_status_string", "falcon_device_status", "falcon_kernel_for", "falcon_abi_version",
-            "falcon_bwd", "falcon_bwd_workspace_bytes")
+            "falcon_bwd", "falcon_bwd_workspace_bytes", "falcon_glr_fwd", "falcon_glr_bwd", "falcon_gn_fwd",
+            "falcon_gn_bwd", "falcon_gn_bwd_workspace_bytes")
 STATIC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -99,6 +119,15 @@ def load(path: str | None = None):
                                                                 ctypes.c_size_t, vp]
         lib.falcon_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.falcon_bwd_workspace_bytes.argtypes = [ctypes.c_int, ctypes.POINTER(FalconDims), ctypes.c_int]
+        dims_p, i32, f32 = ctypes.POINTER(FalconSeqDims), ctypes.c_int, ctypes.c_float
+        for name, args in (("falcon_glr_fwd", [i32] + [vp] * 6 + [dims_p, vp, vp]),
+                           ("falcon_glr_bwd", [i32] + [vp] * 10 + [dims_p, vp, vp]),
+                           ("falcon_gn_fwd", [i32] + [vp] * 6 + [dims_p, vp, f32, vp]),
+                           ("falcon_gn_bwd", [i32] + [vp] * 10 + [dims_p, vp, f32, vp, ctypes.c_size_t, vp])):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = args
+        lib.falcon_gn_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.falcon_gn_bwd_workspace_bytes.argtypes = [dims_p]
         if path is None:
             _lib = lib
         return lib
@@ -268,3 +297,202 @@ def join_tail(keys, vals):
 
     B, H = keys.shape[:2]
     return torch.cat([keys.reshape(B, H, -1), vals.reshape(B, H, -1)], dim=-1).reshape(-1).contiguous()
+
+
+# ---- the strided [B,H,T,d] operators: gated linear recurrence and head norm
+
+
+def make_seq_dims(batch, heads, seqlen, d, *, dtype=FALCON_BF16) -> FalconSeqDims:
+    return FalconSeqDims(int(batch), int(heads), int(seqlen), int(d), int(dtype), 0)
+
+
+def _strides(strides):
+    """A flat sequence of (batch, head, token) strides per tensor as an int64 array, or None (dense)."""
+    return None if strides is None else (ctypes.c_int64 * len(strides))(*strides)
+
+
+def falcon_glr_fwd(gate, x, g, h0, lengths, out, h_final, dims: FalconSeqDims, strides=None, stream=None) -> int:
+    """The C entry point with the same argument order; tensors or raw device pointers, `strides` 9 values or
+    None. Returns the status."""
+    return int(load().falcon_glr_fwd(int(gate), _ptr(x), _ptr(g), _ptr(h0), _ptr(lengths), _ptr(out), _ptr(h_final),
+                                     ctypes.byref(dims), _strides(strides), _stream_handle(stream)))
+
+
+def falcon_glr_bwd(gate, x, g, out, h0, lengths, dout, dh_final, dx, dg, dh0, dims: FalconSeqDims, strides=None,
+                   stream=None) -> int:
+    """The C entry point (`strides` 18 values or None); returns the status."""
+    return int(load().falcon_glr_bwd(int(gate), _ptr(x), _ptr(g), _ptr(out), _ptr(h0), _ptr(lengths), _ptr(dout),
+                                     _ptr(dh_final), _ptr(dx), _ptr(dg), _ptr(dh0), ctypes.byref(dims),
+                                     _strides(strides), _stream_handle(stream)))
+
+
+def falcon_gn_fwd(act, x, z, weight, bias, lengths, y, dims: FalconSeqDims, strides=None, eps=1e-5,
+                  stream=None) -> int:
+    """The C entry point (`strides` 9 values or None); returns the status."""
+    return int(load().falcon_gn_fwd(int(act), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(y),
+                                    ctypes.byref(dims), _strides(strides), float(eps), _stream_handle(stream)))
+
+
+def falcon_gn_bwd(act, x, z, weight, bias, lengths, dy, dx, dz, dweight, dbias, dims: FalconSeqDims, strides=None,
+                  eps=1e-5, workspace=None, workspace_bytes=None, stream=None) -> int:
+    """The C entry point (`strides` 15 values or None); returns the status."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    return int(load().falcon_gn_bwd(int(act), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(dy),
+                                    _ptr(dx), _ptr(dz), _ptr(dweight), _ptr(dbias), ctypes.byref(dims),
+                                    _strides(strides), float(eps), _ptr(workspace), int(workspace_bytes),
+                                    _stream_handle(stream)))
+
+
+def falcon_gn_bwd_workspace_bytes(dims: FalconSeqDims) -> int:
+    return int(load().falcon_gn_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+class _SeqCall:
+    """Checks and marshals the tensors of one call: [B,H,T,d] views in x's dtype on x's device."""
+
+    def __init__(self, x, stream):
+        import torch
+
+        self.torch, self.x = torch, x
+        if x.dim() != 4:
+            raise ValueError(f"x must be [B,H,T,d], got {tuple(x.shape)}")
+        if not x.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if x.dtype is torch.bfloat16:
+            dt = FALCON_BF16
+        elif x.dtype is torch.float32:
+            dt = FALCON_F32
+        else:
+            raise ValueError(f"unsupported dtype {x.dtype}: float32 or bfloat16")
+        self.shape = B, H, T, d = x.shape
+        self.device = x.device
+        self.dims = FalconSeqDims(B, H, T, d, dt, 0)
+        self.strides = []
+        self.stream = stream
+
+    def view(self, t, name):
+        """The pointer of a [B,H,T,d] tensor (None: absent); notes its strides."""
+        if t is None:
+            self.strides += (0, 0, 0)
+            return None
+        if t.shape != self.shape or t.dtype is not self.x.dtype or t.device != self.device:
+            raise ValueError(f"{name} must be {tuple(self.shape)} {self.x.dtype} on {self.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+        sb, sh, st, sd = t.stride()
+        if sd != 1 and self.shape[3] > 1:
+            raise ValueError(f"{name}'s channels must be contiguous (stride 1), got stride {sd}")
+        self.strides += (sb, sh, st)
+        return t.data_ptr()
+
+    def dense(self, t, name, shape, dtype=None):
+        """The pointer of a contiguous array (None: absent)."""
+        if t is None:
+            return None
+        dtype = dtype or self.torch.float32
+        if tuple(t.shape) != shape or t.dtype is not dtype or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {shape} {dtype} on {self.device}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+        return t.data_ptr()
+
+    def empty(self, shape, dtype=None):
+        return self.torch.empty(shape, dtype=dtype or self.torch.float32, device=self.device)
+
+    def run(self, what, *args):
+        """Calls lib.<what>(*args, stream) on the tensors' device; raises on a nonzero status."""
+        cuda, index = self.torch.cuda, self.device.index
+        if index != cuda.current_device():
+            with cuda.device(index):
+                return self.run(what, *args)
+        stream = cuda.current_stream(index) if self.stream is None else self.stream
+        st = getattr(load(), what)(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+        if st != FALCON_OK:
+            raise FalconError(st, what)
+
+
+def _choice(table, value, what):
+    if value not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {value!r}")
+    return table[value]
+
+
+def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, want_state=True, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t per channel; returns (out, h_final or None).
+
+    gate: "decay" (a = exp(g), u = x), "sigmoid" (a = sigmoid(g), u = x) or "mix" (a = sigmoid(g),
+    u = (1 - a) x). x, g: [B,H,T,d], float32 or bfloat16, any strides with contiguous channels (so
+    `proj.view(B, T, H, d).transpose(1, 2)` and column blocks are passed as they are). h0: fp32 [B,H,d] or
+    None (zero). lengths: int32 [B] or None; rows behind them come back as zeros. out (a [B,H,T,d] view) and
+    h_final (may be h0: updated in place) are written where given, else allocated dense."""
+    c = _SeqCall(x, stream)
+    B, H, T, d = c.shape
+    if out is None:
+        out = c.empty((B, H, T, d), x.dtype)
+    if h_final is None and want_state:
+        h_final = c.empty((B, H, d))
+    xp, gp, op = c.view(x, "x"), c.view(g, "g"), c.view(out, "out")
+    c.run("falcon_glr_fwd", _choice(GLR_GATES, gate, "gate"), xp, gp, c.dense(h0, "h0", (B, H, d)),
+          c.dense(lengths, "lengths", (B,), c.torch.int32), op, c.dense(h_final, "h_final", (B, H, d)), c.dims,
+          _strides(c.strides))
+    return out, h_final
+
+
+def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None, dx=None, dg=None, dh0=None,
+                 stream=None):
+    """Gradients of one glr_forward call, from its inputs, its output `out` and the adjoints of out and
+    h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated."""
+    c = _SeqCall(x, stream)
+    B, H, T, d = c.shape
+    dx = c.empty((B, H, T, d), x.dtype) if dx is None else dx
+    dg = c.empty((B, H, T, d), x.dtype) if dg is None else dg
+    dh0 = c.empty((B, H, d)) if dh0 is None else dh0
+    p = [c.view(t, n) for t, n in ((x, "x"), (g, "g"), (out, "out"), (dout, "dout"), (dx, "dx"), (dg, "dg"))]
+    c.run("falcon_glr_bwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[2], c.dense(h0, "h0", (B, H, d)),
+          c.dense(lengths, "lengths", (B,), c.torch.int32), p[3], c.dense(dh_final, "dh_final", (B, H, d)), p[4], p[5],
+          c.dense(dh0, "dh0", (B, H, d)), c.dims, _strides(c.strides))
+    return {"dx": dx, "dg": dg, "dh0": dh0}
+
+
+def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5, lengths=None, y=None, stream=None):
+    """Group norm of each token's head over its d channels: n = weight (x - mean) / sqrt(var + eps) + bias,
+    y = act(n), or n * act(z) with a gate z.
+
+    x, z: [B,H,T,d] views as for glr_forward; weight, bias: fp32 [H,d] or None; act: "none", "silu", "gelu"
+    (erf) or "sigmoid". y is written where given, else allocated in the output projection's layout: a [B,H,T,d]
+    view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free."""
+    c = _SeqCall(x, stream)
+    B, H, T, d = c.shape
+    if y is None:
+        y = c.empty((B, T, H, d), x.dtype).transpose(1, 2)
+    xp, zp, yp = c.view(x, "x"), c.view(z, "z"), c.view(y, "y")
+    c.run("falcon_gn_fwd", _choice(GN_ACTS, act, "act"), xp, zp, c.dense(weight, "weight", (H, d)),
+          c.dense(bias, "bias", (H, d)), c.dense(lengths, "lengths", (B,), c.torch.int32), yp, c.dims,
+          _strides(c.strides), float(eps))
+    return y
+
+
+def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps=1e-5, lengths=None, dx=None,
+                       dz=None, dweight=None, dbias=None, workspace=None, want_params=True, stream=None):
+    """Gradients of one groupnorm_forward call. Returns a dict dx, dz (None without a gate), dweight, dbias
+    (fp32 [H,d]; None unless want_params or given). dx is written where given, else allocated dense; the
+    workspace (falcon_gn_bwd_workspace_bytes) is allocated unless given."""
+    c = _SeqCall(x, stream)
+    B, H, T, d = c.shape
+    dx = c.empty((B, H, T, d), x.dtype) if dx is None else dx
+    if z is not None and dz is None:
+        dz = c.empty((B, H, T, d), x.dtype)
+    if want_params:
+        dweight = c.empty((H, d)) if dweight is None else dweight
+        dbias = c.empty((H, d)) if dbias is None else dbias
+    if workspace is None and (dweight is not None or dbias is not None):
+        n = falcon_gn_bwd_workspace_bytes(c.dims)
+        workspace = c.empty((n,), c.torch.uint8) if n > 0 else None
+    if workspace is not None and workspace.device != c.device:
+        raise ValueError(f"workspace must be on {c.device}, got {workspace.device}")
+    p = [c.view(t, n) for t, n in ((x, "x"), (z, "z"), (dy, "dy"), (dx, "dx"), (dz, "dz"))]
+    c.run("falcon_gn_bwd", _choice(GN_ACTS, act, "act"), p[0], p[1], c.dense(weight, "weight", (H, d)),
+          c.dense(bias, "bias", (H, d)), c.dense(lengths, "lengths", (B,), c.torch.int32), p[2], p[3], p[4],
+          c.dense(dweight, "dweight", (H, d)), c.dense(dbias, "dbias", (H, d)), c.dims, _strides(c.strides),
+          float(eps), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
