@@ -9,6 +9,7 @@
 
 #include "falcon.h"
 #include "falcon_internal.h"
+#include "falcon_seq.h"
 
 // Scratch of falcon_fwd_static: a file-scope device array (one per device), never allocated.
 static __device__ __align__(256) uint8_t g_static_workspace[FALCON_STATIC_WORKSPACE_BYTES];
@@ -308,12 +309,12 @@ int falcon_bwd(int variant, const void* q, const void* k, const void* v, const f
 
 int falcon_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FALCON_ERR_CUDA;
-    int f = 0, g = 0, h = 0, k = 0, b = 0;
+    int f = 0, g = 0, h = 0, k = 0, b = 0, r = 0;
     if (falcon::fused_consume_timeout_flag(&f) != 0 || falcon::colw_consume_timeout_flag(&g) != 0 ||
         falcon::f3map_consume_timeout_flag(&h) != 0 || falcon::scan_tc_consume_timeout_flag(&k) != 0 ||
-        falcon::bwd_consume_timeout_flag(&b) != 0)
+        falcon::bwd_consume_timeout_flag(&b) != 0 || falcon::glr_consume_timeout_flag(&r) != 0)
         return FALCON_ERR_CUDA;
-    return f || g || h || k || b ? FALCON_ERR_DEVICE_TIMEOUT : FALCON_OK;
+    return f || g || h || k || b || r ? FALCON_ERR_DEVICE_TIMEOUT : FALCON_OK;
 }
 
 }  // extern "C"

@@ -2,9 +2,12 @@
 // logistic function with its complement, and the cluster primitives of the recurrence.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include "sm103_f32x2.cuh"
 
 namespace falcon {
 namespace seq {
@@ -102,18 +105,50 @@ __device__ __forceinline__ void logistic(float v, float& s, float& c) {
 }
 
 // e^v. Close to 0 (a log decay of a long memory) the hardware's base-2 exponential is off by up to two
-// units, always on one side for a given argument, which a memory of n tokens multiplies by n: there the
-// Taylor series to the sixth degree (remainder below 0.25^7 / 7! = 1.3e-8), whose one large rounding is
-// that of the last sum.
+// units, the same for the same argument, which a memory of n tokens multiplies by n: there the Taylor
+// series to the fourth degree (remainder below 16^-5 / 5! = 8e-9), whose one large rounding is that of the
+// last sum.
 __device__ __forceinline__ float decay_exp(float v) {
-    float p = fmaf(v, 1.f / 720, 1.f / 120);
-    p = fmaf(p, v, 1.f / 24);
-    p = fmaf(p, v, 1.f / 6);
+    float p = fmaf(v, 1.f / 24, 1.f / 6);
     p = fmaf(p, v, 0.5f);
     p = fmaf(p, v, 1.f);
     p = fmaf(p, v, 1.f);
-    return fabsf(v) < 0.25f ? p : ex2(kLog2e * v);
+    return fabsf(v) < 0.0625f ? p : ex2(kLog2e * v);
 }
+
+// ---- pairs of channels: the same functions on two values, packed where the hardware can
+__device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
+
+// s = 1 / (1 + e^-v), c = 1 - s. With e = e^-|v| <= 1 the smaller of the two is e / (1 + e).
+__device__ __forceinline__ void logistic2(float2 v, float2& s, float2& c) {
+    const float2 e = pair(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
+    const float2 d = ptx::add2(e, pair(1.f, 1.f));
+    const float2 small = ptx::mul2(e, pair(rcp(d.x), rcp(d.y)));
+    const float2 large = ptx::fma2(small, pair(-1.f, -1.f), pair(1.f, 1.f));
+    const bool px = v.x > 0.f, py = v.y > 0.f;
+    s = pair(px ? large.x : small.x, py ? large.y : small.y);
+    c = pair(px ? small.x : large.x, py ? small.y : large.y);
+}
+__device__ __forceinline__ float2 decay_exp2(float2 v) {
+    float2 p = ptx::fma2(v, pair(1.f / 24, 1.f / 24), pair(1.f / 6, 1.f / 6));
+    p = ptx::fma2(p, v, pair(0.5f, 0.5f));
+    p = ptx::fma2(p, v, pair(1.f, 1.f));
+    p = ptx::fma2(p, v, pair(1.f, 1.f));
+    const float2 k = ptx::mul2(v, pair(kLog2e, kLog2e));
+    return pair(fabsf(v.x) < 0.0625f ? p.x : ex2(k.x), fabsf(v.y) < 0.0625f ? p.y : ex2(k.y));
+}
+
+// ---- asynchronous copies of CB bytes, global to shared; `in` false writes zeros and reads nothing
+template <int CB>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
+    if (CB == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // ---- thread-block clusters
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -124,12 +159,24 @@ __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Four floats into a peer's shared memory, counted as 16 bytes by the mbarrier `bar` of that peer.
+__device__ __forceinline__ void st_async4(uint32_t addr, const float* v, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+        ::"r"(addr), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+        "r"(__float_as_uint(v[3])), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_peer4(uint32_t addr, const float* v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+
+// ---- TMA boxes of a [B,H,T,d] tensor (coordinates: channel, token, head, sequence)
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c, int t, int h, int b,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(tm), "r"(c), "r"(t), "r"(h), "r"(b), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, uint32_t src, int c, int t, int h, int b) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+                 ::"l"(tm), "r"(src), "r"(c), "r"(t), "r"(h), "r"(b) : "memory");
 }
 
 }  // namespace seq

@@ -34,6 +34,8 @@ struct GlrArgs {
 };
 int launch_glr_fwd(const GlrArgs& a, cudaStream_t s);
 int launch_glr_bwd(const GlrArgs& a, cudaStream_t s);
+// Reads and clears the kernels' timeout flag (synchronous).
+int glr_consume_timeout_flag(int* flag);
 
 struct GnArgs {
     int act;

@@ -11,7 +11,9 @@ PyTorch is used only to hand over device pointers and the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -119,15 +121,15 @@ def load(path: str | None = None):
                                                                 ctypes.c_size_t, vp]
         lib.falcon_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.falcon_bwd_workspace_bytes.argtypes = [ctypes.c_int, ctypes.POINTER(FalconDims), ctypes.c_int]
-        dims_p, i32, f32 = ctypes.POINTER(FalconSeqDims), ctypes.c_int, ctypes.c_float
-        for name, args in (("falcon_glr_fwd", [i32] + [vp] * 6 + [dims_p, vp, vp]),
-                           ("falcon_glr_bwd", [i32] + [vp] * 10 + [dims_p, vp, vp]),
-                           ("falcon_gn_fwd", [i32] + [vp] * 6 + [dims_p, vp, f32, vp]),
-                           ("falcon_gn_bwd", [i32] + [vp] * 10 + [dims_p, vp, f32, vp, ctypes.c_size_t, vp])):
+        i32, f32 = ctypes.c_int, ctypes.c_float
+        for name, args in (("falcon_glr_fwd", [i32] + [vp] * 6 + [vp, vp, vp]),
+                           ("falcon_glr_bwd", [i32] + [vp] * 10 + [vp, vp, vp]),
+                           ("falcon_gn_fwd", [i32] + [vp] * 6 + [vp, vp, f32, vp]),
+                           ("falcon_gn_bwd", [i32] + [vp] * 10 + [vp, vp, f32, vp, ctypes.c_size_t, vp])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = args
         lib.falcon_gn_bwd_workspace_bytes.restype = ctypes.c_size_t
-        lib.falcon_gn_bwd_workspace_bytes.argtypes = [dims_p]
+        lib.falcon_gn_bwd_workspace_bytes.argtypes = [vp]
         if path is None:
             _lib = lib
         return lib
@@ -349,66 +351,80 @@ def falcon_gn_bwd_workspace_bytes(dims: FalconSeqDims) -> int:
     return int(load().falcon_gn_bwd_workspace_bytes(ctypes.byref(dims)))
 
 
-class _SeqCall:
-    """Checks and marshals the tensors of one call: [B,H,T,d] views in x's dtype on x's device."""
+_DIMS, _STRIDES = struct.Struct("=4q2i"), {n: struct.Struct(f"={3 * n}q") for n in (3, 5, 6)}
 
-    def __init__(self, x, stream):
-        import torch
 
-        self.torch, self.x = torch, x
-        if x.dim() != 4:
-            raise ValueError(f"x must be [B,H,T,d], got {tuple(x.shape)}")
-        if not x.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if x.dtype is torch.bfloat16:
-            dt = FALCON_BF16
-        elif x.dtype is torch.float32:
-            dt = FALCON_F32
-        else:
-            raise ValueError(f"unsupported dtype {x.dtype}: float32 or bfloat16")
-        self.shape = B, H, T, d = x.shape
-        self.device = x.device
-        self.dims = FalconSeqDims(B, H, T, d, dt, 0)
-        self.strides = []
-        self.stream = stream
+def _sizes(x):
+    if x.dim() != 4:
+        raise ValueError(f"x must be [B,H,T,d], got {tuple(x.shape)}")
+    return x.shape
 
-    def view(self, t, name):
-        """The pointer of a [B,H,T,d] tensor (None: absent); notes its strides."""
+
+def _seq_call(x, views, arrays, stream):
+    """Checks the tensors of one call and marshals them: `views`, pairs (tensor or None, name), are [B,H,T,d] like x
+    in x's dtype; `arrays`, (tensor or None, name, shape, dtype), are contiguous. Returns their pointers (views,
+    then arrays), the packed falcon_seq_dims_t, the packed strides, x's device index and the stream's handle."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    code = _dtype_codes().get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    pointers, strides = [], []
+    for t, name in views:
         if t is None:
-            self.strides += (0, 0, 0)
-            return None
-        if t.shape != self.shape or t.dtype is not self.x.dtype or t.device != self.device:
-            raise ValueError(f"{name} must be {tuple(self.shape)} {self.x.dtype} on {self.device}, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+            pointers.append(None)
+            strides += (0, 0, 0)
+            continue
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+            raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {x.device}, got {tuple(t.shape)} {t.dtype} on "
+                             f"{t.device}")
         sb, sh, st, sd = t.stride()
-        if sd != 1 and self.shape[3] > 1:
+        if sd != 1 and shape[3] > 1:
             raise ValueError(f"{name}'s channels must be contiguous (stride 1), got stride {sd}")
-        self.strides += (sb, sh, st)
-        return t.data_ptr()
-
-    def dense(self, t, name, shape, dtype=None):
-        """The pointer of a contiguous array (None: absent)."""
+        strides += (sb, sh, st)
+        pointers.append(t.data_ptr())
+    for t, name, want, dt in arrays:
         if t is None:
-            return None
-        dtype = dtype or self.torch.float32
-        if tuple(t.shape) != shape or t.dtype is not dtype or t.device != self.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {shape} {dtype} on {self.device}, got {tuple(t.shape)} "
+            pointers.append(None)
+            continue
+        if t.shape != want or t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {tuple(want)} {dt} on {x.device}, got {tuple(t.shape)} "
                              f"{t.dtype} on {t.device}")
-        return t.data_ptr()
+        pointers.append(t.data_ptr())
+    if stream is None:
+        stream = _raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    return pointers, _DIMS.pack(*shape, code, 0), _STRIDES[len(views)].pack(*strides), index, stream
 
-    def empty(self, shape, dtype=None):
-        return self.torch.empty(shape, dtype=dtype or self.torch.float32, device=self.device)
 
-    def run(self, what, *args):
-        """Calls lib.<what>(*args, stream) on the tensors' device; raises on a nonzero status."""
-        cuda, index = self.torch.cuda, self.device.index
-        if index != cuda.current_device():
-            with cuda.device(index):
-                return self.run(what, *args)
-        stream = cuda.current_stream(index) if self.stream is None else self.stream
-        st = getattr(load(), what)(*args, stream if isinstance(stream, int) else stream.cuda_stream)
-        if st != FALCON_OK:
-            raise FalconError(st, what)
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
+    import torch
+
+    return {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32}
+
+
+def _raw_stream(index):
+    """The handle of the device's current stream."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_device(index, what, *args):
+    """Calls lib.<what>(*args) with device `index` current; raises on a nonzero status."""
+    import torch
+
+    fn = getattr(_lib or load(), what)
+    if index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != FALCON_OK:
+        raise FalconError(st, what)
 
 
 def _choice(table, value, what):
@@ -425,16 +441,19 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
     `proj.view(B, T, H, d).transpose(1, 2)` and column blocks are passed as they are). h0: fp32 [B,H,d] or
     None (zero). lengths: int32 [B] or None; rows behind them come back as zeros. out (a [B,H,T,d] view) and
     h_final (may be h0: updated in place) are written where given, else allocated dense."""
-    c = _SeqCall(x, stream)
-    B, H, T, d = c.shape
+    import torch
+
+    B, H, T, d = _sizes(x)
     if out is None:
-        out = c.empty((B, H, T, d), x.dtype)
+        out = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
     if h_final is None and want_state:
-        h_final = c.empty((B, H, d))
-    xp, gp, op = c.view(x, "x"), c.view(g, "g"), c.view(out, "out")
-    c.run("falcon_glr_fwd", _choice(GLR_GATES, gate, "gate"), xp, gp, c.dense(h0, "h0", (B, H, d)),
-          c.dense(lengths, "lengths", (B,), c.torch.int32), op, c.dense(h_final, "h_final", (B, H, d)), c.dims,
-          _strides(c.strides))
+        h_final = torch.empty((B, H, d), dtype=torch.float32, device=x.device)
+    f32, state = torch.float32, (B, H, d)
+    p, dims, strides, index, stream = _seq_call(
+        x, ((x, "x"), (g, "g"), (out, "out")),
+        ((h0, "h0", state, f32), (lengths, "lengths", (B,), torch.int32), (h_final, "h_final", state, f32)), stream)
+    _on_device(index, "falcon_glr_fwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[3], p[4], p[2], p[5], dims,
+               strides, stream)
     return out, h_final
 
 
@@ -442,15 +461,22 @@ def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None,
                  stream=None):
     """Gradients of one glr_forward call, from its inputs, its output `out` and the adjoints of out and
     h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated."""
-    c = _SeqCall(x, stream)
-    B, H, T, d = c.shape
-    dx = c.empty((B, H, T, d), x.dtype) if dx is None else dx
-    dg = c.empty((B, H, T, d), x.dtype) if dg is None else dg
-    dh0 = c.empty((B, H, d)) if dh0 is None else dh0
-    p = [c.view(t, n) for t, n in ((x, "x"), (g, "g"), (out, "out"), (dout, "dout"), (dx, "dx"), (dg, "dg"))]
-    c.run("falcon_glr_bwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[2], c.dense(h0, "h0", (B, H, d)),
-          c.dense(lengths, "lengths", (B,), c.torch.int32), p[3], c.dense(dh_final, "dh_final", (B, H, d)), p[4], p[5],
-          c.dense(dh0, "dh0", (B, H, d)), c.dims, _strides(c.strides))
+    import torch
+
+    B, H, T, d = _sizes(x)
+    f32, state = torch.float32, (B, H, d)
+    if dx is None:
+        dx = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+    if dg is None:
+        dg = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+    if dh0 is None:
+        dh0 = torch.empty(state, dtype=f32, device=x.device)
+    p, dims, strides, index, stream = _seq_call(
+        x, ((x, "x"), (g, "g"), (out, "out"), (dout, "dout"), (dx, "dx"), (dg, "dg")),
+        ((h0, "h0", state, f32), (lengths, "lengths", (B,), torch.int32), (dh_final, "dh_final", state, f32),
+         (dh0, "dh0", state, f32)), stream)
+    _on_device(index, "falcon_glr_bwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[2], p[6], p[7], p[3], p[8],
+               p[4], p[5], p[9], dims, strides, stream)
     return {"dx": dx, "dg": dg, "dh0": dh0}
 
 
@@ -461,38 +487,49 @@ def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5
     x, z: [B,H,T,d] views as for glr_forward; weight, bias: fp32 [H,d] or None; act: "none", "silu", "gelu"
     (erf) or "sigmoid". y is written where given, else allocated in the output projection's layout: a [B,H,T,d]
     view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free."""
-    c = _SeqCall(x, stream)
-    B, H, T, d = c.shape
+    import torch
+
+    B, H, T, d = _sizes(x)
     if y is None:
-        y = c.empty((B, T, H, d), x.dtype).transpose(1, 2)
-    xp, zp, yp = c.view(x, "x"), c.view(z, "z"), c.view(y, "y")
-    c.run("falcon_gn_fwd", _choice(GN_ACTS, act, "act"), xp, zp, c.dense(weight, "weight", (H, d)),
-          c.dense(bias, "bias", (H, d)), c.dense(lengths, "lengths", (B,), c.torch.int32), yp, c.dims,
-          _strides(c.strides), float(eps))
+        y = torch.empty((B, T, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
+    f32, chans = torch.float32, (H, d)
+    p, dims, strides, index, stream = _seq_call(
+        x, ((x, "x"), (z, "z"), (y, "y")),
+        ((weight, "weight", chans, f32), (bias, "bias", chans, f32), (lengths, "lengths", (B,), torch.int32)), stream)
+    _on_device(index, "falcon_gn_fwd", _choice(GN_ACTS, act, "act"), p[0], p[1], p[3], p[4], p[5], p[2], dims, strides,
+               float(eps), stream)
     return y
 
 
 def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps=1e-5, lengths=None, dx=None,
                        dz=None, dweight=None, dbias=None, workspace=None, want_params=True, stream=None):
     """Gradients of one groupnorm_forward call. Returns a dict dx, dz (None without a gate), dweight, dbias
-    (fp32 [H,d]; None unless want_params or given). dx is written where given, else allocated dense; the
-    workspace (falcon_gn_bwd_workspace_bytes) is allocated unless given."""
-    c = _SeqCall(x, stream)
-    B, H, T, d = c.shape
-    dx = c.empty((B, H, T, d), x.dtype) if dx is None else dx
+    (fp32 [H,d]; None unless want_params or given). Each is written where given, else allocated dense; so is the
+    workspace, uint8 of falcon_gn_bwd_workspace_bytes, which dweight and dbias need."""
+    import torch
+
+    B, H, T, d = _sizes(x)
+    f32, chans = torch.float32, (H, d)
+    if dx is None:
+        dx = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
     if z is not None and dz is None:
-        dz = c.empty((B, H, T, d), x.dtype)
+        dz = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
     if want_params:
-        dweight = c.empty((H, d)) if dweight is None else dweight
-        dbias = c.empty((H, d)) if dbias is None else dbias
-    if workspace is None and (dweight is not None or dbias is not None):
-        n = falcon_gn_bwd_workspace_bytes(c.dims)
-        workspace = c.empty((n,), c.torch.uint8) if n > 0 else None
-    if workspace is not None and workspace.device != c.device:
-        raise ValueError(f"workspace must be on {c.device}, got {workspace.device}")
-    p = [c.view(t, n) for t, n in ((x, "x"), (z, "z"), (dy, "dy"), (dx, "dx"), (dz, "dz"))]
-    c.run("falcon_gn_bwd", _choice(GN_ACTS, act, "act"), p[0], p[1], c.dense(weight, "weight", (H, d)),
-          c.dense(bias, "bias", (H, d)), c.dense(lengths, "lengths", (B,), c.torch.int32), p[2], p[3], p[4],
-          c.dense(dweight, "dweight", (H, d)), c.dense(dbias, "dbias", (H, d)), c.dims, _strides(c.strides),
-          float(eps), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+        dweight = torch.empty(chans, dtype=f32, device=x.device) if dweight is None else dweight
+        dbias = torch.empty(chans, dtype=f32, device=x.device) if dbias is None else dbias
+    p, dims, strides, index, stream = _seq_call(
+        x, ((x, "x"), (z, "z"), (dy, "dy"), (dx, "dx"), (dz, "dz")),
+        ((weight, "weight", chans, f32), (bias, "bias", chans, f32), (lengths, "lengths", (B,), torch.int32),
+         (dweight, "dweight", chans, f32), (dbias, "dbias", chans, f32)), stream)
+    size = 0
+    if dweight is not None or dbias is not None:
+        size = load().falcon_gn_bwd_workspace_bytes(dims)
+        if workspace is None and size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        if workspace is not None:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
+            size = workspace.numel() * workspace.element_size()
+    _on_device(index, "falcon_gn_bwd", _choice(GN_ACTS, act, "act"), p[0], p[1], p[5], p[6], p[7], p[2], p[3], p[4],
+               p[8], p[9], dims, strides, float(eps), _ptr(workspace), size, stream)
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
