@@ -7,9 +7,9 @@
 // scan's direction: position n is token n forward and token len - 1 - n backward.
 //
 // One pass over the data. A CTA works through tiles of kTile positions x 2 LC channels; a thread owns two
-// channels of R consecutive positions. Each warp keeps its own ring of tiles in shared memory, filled ahead
-// by TMA (by cp.async, or through registers, where addresses do not allow it), evaluates the gates once
-// into registers and reduces its tokens to their map; maps are composed over the warp (shuffles), the CTA
+// channels of R consecutive positions. Tiles lie in a ring in shared memory, filled ahead and emptied by TMA (where addresses do not allow that, each warp copies its rows by cp.async, or
+// through registers, and stores them itself). A warp evaluates the gates of its rows once into registers and
+// reduces its tokens to their map; maps are composed over the warp (shuffles), the CTA
 // (shared memory) and, for long sequences, the CTAs of a cluster that lie side by side along the tokens:
 // each CTA sends its tile's map into its peers' shared memory (st.async, counted by an mbarrier there: no
 // fence that would wait for the outputs on their way to memory), and every CTA composes them all in the
@@ -24,7 +24,9 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <stdlib.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "falcon_internal.h"
 #include "falcon_seq.cuh"
@@ -38,7 +40,8 @@ using namespace seq;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
+template <int LC>
+constexpr int kMaxCluster = LC == 32 ? 8 : 16;  // CTAs of a cluster; a fuller tile has more maps to hold
 constexpr long long kTimeoutCycles = 4000000000LL;  // ~2 s
 
 __device__ int g_glr_timeout_flag = 0;
@@ -56,7 +59,7 @@ struct Params {
     float* h_out;        // forward: h_final; backward: dh0
     const int32_t* lengths;
     long long sb[6], sh[6], st[6];  // x, g, out_in, dout, out, dg
-    long long items;                // sequences x channel tiles
+    int items;                      // sequences x channel tiles
     int H, T, d, tiles;             // tiles: channel tiles of a head
 };
 enum { kX, kG, kOutIn, kDout, kOut, kDg };
@@ -87,6 +90,14 @@ __device__ __forceinline__ Map shfl_up(const Map& m, int o) {
     r.H.y = __shfl_up_sync(0xffffffffu, m.H.y, o);
     return r;
 }
+__device__ __forceinline__ Map shfl(const Map& m, int from) {
+    Map r;
+    r.A.x = __shfl_sync(0xffffffffu, m.A.x, from);
+    r.A.y = __shfl_sync(0xffffffffu, m.A.y, from);
+    r.H.x = __shfl_sync(0xffffffffu, m.H.x, from);
+    r.H.y = __shfl_sync(0xffffffffu, m.H.y, from);
+    return r;
+}
 // first `before`, then `m`
 __device__ __forceinline__ Map compose(const Map& before, const Map& m) {
     return Map{ptx::mul2(m.A, before.A), ptx::fma2(m.A, before.H, m.H)};
@@ -94,17 +105,28 @@ __device__ __forceinline__ Map compose(const Map& before, const Map& m) {
 __device__ __forceinline__ float2 apply(const Map& m, float2 h) { return ptx::fma2(m.A, h, m.H); }
 
 template <int LC>
-struct Maps {
+struct __align__(16) Maps {
     Map warp[2][kWarps][LC];
-    Map cta[2][kMaxCluster][LC];
-    uint64_t ready[2];  // the maps of a cluster-wide tile have arrived
+    Map cta[2][kMaxCluster<LC>][LC];
+    float2 state[2][LC];  // behind a tile, where there is no cluster
+    uint64_t ready[2];    // the maps of a cluster-wide tile have arrived
 };
 
-// Bounded wait of a whole warp. After a wait that ran out the following ones are skipped: the outputs are
+// Waits for a phase for at most about kTimeoutCycles; false when that runs out.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity) {
+    const uint32_t at = ptx::smem_u32(bar);
+    if (ptx::mbar_try(at, parity)) return true;
+    const long long t0 = clock64();
+    do {
+        if (ptx::mbar_try(at, parity)) return true;
+    } while (clock64() - t0 <= kTimeoutCycles);
+    return false;
+}
+// The same for a whole warp. After a wait that ran out the following ones are skipped: the outputs are
 // lost, the flag tells, and the kernel comes to its end.
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, bool& dead) {
     if (dead) return;
-    if (!ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity, kTimeoutCycles)) {
+    if (!bounded_wait(bar, parity)) {
         dead = true;
         atomicExch(&g_glr_timeout_flag, 1);
     }
@@ -112,11 +134,13 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, bool& d
 }
 
 // The state that enters this thread's positions: composes the thread's map over the warp, the CTA and the
-// cluster; `carry` is the state entering the cluster's tile on entry and leaving it on return. Called by all
+// cluster. `carry` is the state entering the cluster's tile (without a cluster only for an item's first tile,
+// `fresh`; then sm.state has it) and, in a cluster, the one leaving it on return. Called by all scanning
 // threads of the cluster the same number of times; `it` counts the calls.
-template <int LC>
-__device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, int cs, int rank, const Map& own, float2& carry,
-                                            bool& dead) {
+// `behind_barrier` runs when every thread of the CTA has left the tile before this one.
+template <int LC, typename F>
+__device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, bool fresh, int cs, int rank, const Map& own,
+                                            float2& carry, bool& dead, F behind_barrier) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lc = lane % LC;
     const int buf = it & 1;
     Map inc = own;  // over the segments up to this one
@@ -125,7 +149,7 @@ __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, int cs, int ra
         const Map m = shfl_up(inc, o);
         if (lane >= o) inc = compose(m, inc);
     }
-    if (lane >= 32 - LC) sm.warp[buf][warp][lc] = inc;
+    if (lane >= 32 - LC && warp < kWarps - 1) sm.warp[buf][warp][lc] = inc;
     Map exc = {pair(1.f, 1.f), pair(0.f, 0.f)};  // over the segments before it
     if (LC < 32) {
         const Map m = shfl_up(inc, LC);
@@ -135,47 +159,61 @@ __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, int cs, int ra
     // before the last tile's state may be written over it
     asm volatile("" ::"f"(carry.x), "f"(carry.y) : "memory");
     __syncthreads();
-    Map before = {pair(1.f, 1.f), pair(0.f, 0.f)}, all = before;
+    behind_barrier();
+    Map before = {pair(1.f, 1.f), pair(0.f, 0.f)};  // over the warps before this one
+    {
+        for (int w0 = 0; w0 < warp; w0 += 3) {
+            Map m[3];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = all;
-        all = compose(all, sm.warp[buf][w][lc]);
+            for (int w = 0; w < 3; ++w) m[w] = sm.warp[buf][w0 + w][lc];  // those from `warp` on are not used
+            before = compose(before, m[0]);
+            if (w0 + 1 < warp) before = compose(before, m[1]);
+            if (w0 + 2 < warp) before = compose(before, m[2]);
+        }
     }
-    float2 in;  // the state entering this CTA's tile
+    float2 in = carry;  // the state entering this CTA's tile
     if (cs > 1) {
-        if (it == 0) cluster_wait();  // every peer runs and has set up its mbarriers
         const uint32_t bar = ptx::smem_u32(&sm.ready[buf]);
         if (threadIdx.x == 0) ptx::mbar_expect_tx(bar, cs * LC * (uint32_t)sizeof(Map));
-        if (warp < cs && lane < LC)
-            st_async4(peer(ptx::smem_u32(&sm.cta[buf][rank][lc]), warp), &all.A.x, peer(bar, warp));
-        // A peer writes this buffer again two tiles on, after this CTA's map of the tile between has
-        // reached it; that is sent behind the __syncthreads above, so behind the reads below.
-        wait_for(&sm.ready[buf], (it >> 1) & 1, dead);
-        in = carry;
-#pragma unroll 4
-        for (int r = 0; r < cs; ++r) {
-            if (r == rank) in = carry;
-            carry = apply(sm.cta[buf][r][lc], carry);
+        if (warp == kWarps - 1) {  // the CTA's map, to every peer: the lanes of a segment send to every kSegs-th
+            Map all = compose(before, inc);
+            if (LC < 32) all = shfl(all, 32 - LC + lc);
+            const uint32_t at = ptx::smem_u32(&sm.cta[buf][rank][lc]);
+            for (int r = lane / LC; r < cs; r += 32 / LC) st_async4(peer(at, r), &all.A.x, peer(bar, r));
         }
-    } else {
-        in = carry;
-        carry = apply(all, carry);
+        // A peer writes this buffer again two tiles on, after this CTA's map of the tile between has
+        // reached it; that is sent behind the barrier above, so behind the reads below.
+        wait_for(&sm.ready[buf], (it >> 1) & 1, dead);
+#pragma unroll
+        for (int r0 = 0; r0 < kMaxCluster<LC>; r0 += 4) {
+            if (r0 >= cs) break;
+            Map m[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[r] = sm.cta[buf][r0 + r][lc];  // those behind cs are not used
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (r0 + r == rank) in = carry;
+                const float2 next = apply(m[r], carry);
+                carry = pair(r0 + r < cs ? next.x : carry.x, r0 + r < cs ? next.y : carry.y);
+            }
+        }
+    } else if (!fresh) {
+        in = sm.state[buf ^ 1][lc];
     }
     return apply(exc, apply(before, in));
 }
 
 // ---- the work list: items (sequence, channel tile) dealt to the clusters in turn, each of one or more tiles
 struct Cursor {
-    long long item;
-    long long b, h;
+    int item, b, h;
     int c0, n0, len;  // first channel; first position of the cluster's tile; positions in all
 };
 template <int CHANS>
 __device__ __forceinline__ void enter(const Params& p, Cursor& c) {
     c.n0 = 0;
     if (c.item >= p.items) return;
-    const long long bh = c.item / p.tiles;
-    c.c0 = (int)(c.item - bh * p.tiles) * CHANS;
+    const int bh = c.item / p.tiles;
+    c.c0 = (c.item - bh * p.tiles) * CHANS;
     c.b = bh / p.H;
     c.h = bh - c.b * p.H;
     c.len = length_of(p, c.b);
@@ -184,7 +222,7 @@ template <int CHANS>
 __device__ __forceinline__ void advance(const Params& p, Cursor& c, int step, int clusters) {
     c.n0 += step;  // far below 2^31: the host refuses T >= 2^30
     if (c.n0 >= c.len) {
-        c.item += clusters;
+        c.item += clusters;  // so does this: fewer than 2^30 items
         enter<CHANS>(p, c);
     }
 }
@@ -197,7 +235,7 @@ __device__ __forceinline__ void copy_rows(const Params& p, uint32_t dst, uint8_t
     constexpr int RB = Geo<LC, R>::kChans * sizeof(E), PAD = Geo<LC, R>::kSegs > 1 ? RB : 0;  // as Ring's
     constexpr int CPR = RB / CB, N = Geo<LC, R>::kRows * CPR / 32, EPC = CB / sizeof(E);
     const int lane = threadIdx.x & 31;
-    const long long off = c.b * p.sb[k] + c.h * p.sh[k] + c.c0;
+    const long long off = (long long)c.b * p.sb[k] + (long long)c.h * p.sh[k] + c.c0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int q = lane + 32 * j, row = q / CPR, col = q % CPR;
@@ -244,6 +282,13 @@ __device__ __forceinline__ void st_state2(float* s, long long off, float2 v, boo
     if (second) s[off + 1] = v.y;
 }
 
+// A gate that keeps the state and adds nothing: a is 1 and 1 - a is 0, exactly.
+template <int GATE>
+__device__ __forceinline__ float2 idle_gate() {
+    const float g = GATE == kGateDecay ? 0.f : __uint_as_float(0x7f800000u);
+    return pair(g, g);
+}
+
 template <typename E, int GATE>
 __device__ __forceinline__ void gates(float2 g, float2& a, float2& om) {
     if (GATE == kGateDecay) {
@@ -254,151 +299,215 @@ __device__ __forceinline__ void gates(float2 g, float2& a, float2& om) {
     }
 }
 
-// How a kernel moves its rows: TMA boxes, or copies of 16, 4 or 2 bytes.
+// How a kernel moves its rows: TMA boxes, or copies of 8, 4 or 2 bytes.
 constexpr int kTma = 0;
 
 template <typename E, int LC, int R, int CB>
 struct Ring {
     using G = Geo<LC, R>;
     static constexpr bool kBoxes = CB == kTma;
-    static constexpr bool VS = CB == kTma || CB == 16 || (CB == 4 && sizeof(E) == 2);
+    static constexpr bool VS = CB == kTma || CB == 2 * sizeof(E) || CB == 8;  // pairs of channels are aligned
     static constexpr int RB = G::kChans * sizeof(E);                     // bytes of a row
     static constexpr int PAD = G::kSegs > 1 && !kBoxes ? RB : 0;         // between segments, against bank conflicts
     static constexpr int WB = G::kRows * RB + G::kSegs * PAD;            // one warp's rows of one tensor
+    static constexpr int TB = kWarps * WB;                               // a tile's
+    static constexpr int kBoxes1 = (G::kTile + 255) / 256, kBoxRows = G::kTile / kBoxes1;  // boxes of a tile, rows of a box
+    static_assert(kBoxRows * kBoxes1 == G::kTile, "a tile is whole boxes");
     // where row r of segment seg lies
     static __device__ __forceinline__ int at(int seg, int r) { return (seg * R + r) * RB + seg * PAD; }
 };
 
-template <typename E, int GATE, int LC, int R, int CB, int S>
-__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_constant__ Params p, int cs) {
-    using G = Geo<LC, R>;
-    using Q = Ring<E, LC, R, CB>;
-    __shared__ Maps<LC> sm;
-    __shared__ uint64_t full[S][kWarps];
-    extern __shared__ __align__(128) uint8_t ring[];  // [S][warp][x, g][rows]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / LC, lc = lane % LC;
-    const int rank = blockIdx.x % cs, clusters = gridDim.x / cs, step = cs * G::kTile;
-    const int row0 = (rank * kWarps + warp) * G::kRows;  // of the warp, in the cluster's tile
-    uint8_t* const mine = ring + warp * 2 * Q::WB;
+// A tile's rows of one tensor, as boxes: from shared memory (`mine` its address) or to it.
+template <typename Q>
+__device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* tm, const Cursor& c, int t, uint32_t bar) {
+#pragma unroll
+    for (int i = 0; i < Q::G::kTile; i += Q::kBoxRows)
+        tma_load_4d(to + i * Q::RB, tm, c.c0, t + i, c.h, c.b, bar);
+}
+template <typename Q>
+__device__ __forceinline__ void store_tile(const CUtensorMap* tm, uint32_t from, const Cursor& c, int t, int T) {
+#pragma unroll
+    for (int i = 0; i < Q::G::kTile; i += Q::kBoxRows)  // a box that reaches behind T is cut there
+        if (t + i < T) tma_store_4d(tm, from + i * Q::RB, c.c0, t + i, c.h, c.b);
+}
+
+// Behind a tile: the thread with the last positions hands the state `h` on, or the cluster's rank 0 knows it
+// as `carry`; after an item's last tile it goes to memory.
+template <int LC>
+__device__ __forceinline__ void leave_tile(const Params& p, Maps<LC>& sm, int it, int cs, int rank, const Cursor& c,
+                                           int step, float2 h, float2 carry, bool first, bool second) {
+    const int lc = threadIdx.x % LC;
+    if (cs == 1 ? threadIdx.x < kThreads - LC : rank > 0 || threadIdx.x >= LC) return;
+    if (cs == 1) sm.state[it & 1][lc] = h;
+    if (p.h_out && c.n0 + step >= c.len)
+        st_state2(p.h_out, ((long long)c.b * p.H + c.h) * p.d + c.c0 + 2 * lc, cs == 1 ? h : carry, first, second);
+}
+
+// What thread 0 keeps of a ring of boxes: a stage's boxes have landed (a barrier for each stage); the tile to be
+// loaded next, the tile whose outputs lie in the ring.
+template <int S>
+struct Mover {
+    uint64_t full[S];
+    Cursor next, held;
+    int loaded;
+};
+template <int LC, int S>
+__device__ __forceinline__ void set_up(Mover<S>& mv, Maps<LC>& sm) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S * kWarps; ++i) ptx::mbar_init(ptx::smem_u32(&full[0][0] + i), 1);
+        for (int i = 0; i < S; ++i) ptx::mbar_init(ptx::smem_u32(&mv.full[i]), 1);
         ptx::mbar_init(ptx::smem_u32(&sm.ready[0]), 1);
         ptx::mbar_init(ptx::smem_u32(&sm.ready[1]), 1);
         ptx::mbar_init_fence();
     }
     __syncthreads();
-    if (cs > 1) cluster_arrive();
+}
 
+template <typename E, int GATE, int LC, int R, int CB, int S>
+__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_constant__ Params p, int cs) {
+    using G = Geo<LC, R>;
+    using Q = Ring<E, LC, R, CB>;
+    constexpr int SB = 2 * Q::TB;  // a stage: x, g
+    __shared__ Maps<LC> sm;
+    __shared__ Mover<S> mv;
+    extern __shared__ __align__(128) uint8_t ring[];  // [S][x, g][warp][rows]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / LC, lc = lane % LC;
+    const int rank = blockIdx.x % cs, clusters = gridDim.x / cs, step = cs * G::kTile;
+    const int row0 = (rank * kWarps + warp) * G::kRows;  // of the warp, in the cluster's tile
+    set_up(mv, sm);
+    if (cs > 1) cluster_arrive();
     Cursor pre = {};
     pre.item = blockIdx.x / cs;
     enter<G::kChans>(p, pre);
-    Cursor cur = pre;
-    bool dead = false;
-    int fetched = 0, landed = 0;
-    auto fetch = [&](int stage) {
-        if (pre.item < p.items && !dead) {
-            uint8_t* to = mine + stage * kWarps * 2 * Q::WB;
-            const uint32_t dst = ptx::smem_u32(to);
-            const int n = pre.n0 + row0;
-            if constexpr (Q::kBoxes) {
-                if (lane == 0) {
-                    const uint32_t bar = ptx::smem_u32(&full[stage][warp]);
-                    ptx::bulk_wait_read<0>();  // outputs that lie in the stage have left it
-                    ptx::mbar_expect_tx(bar, 2 * Q::WB);
-                    tma_load_4d(dst, &p.tm[kX], pre.c0, n, (int)pre.h, (int)pre.b, bar);
-                    tma_load_4d(dst + Q::WB, &p.tm[kG], pre.c0, n, (int)pre.h, (int)pre.b, bar);
-                }
-            } else {
-                copy_rows<E, LC, R, CB>(p, dst, to, p.x, kX, pre, n, 0, 1, 0);
-                copy_rows<E, LC, R, CB>(p, dst + Q::WB, to + Q::WB, p.g, kG, pre, n, 0, 1, 0);
-            }
-            advance<G::kChans>(p, pre, step, clusters);
-            ++fetched;
+
+    // thread 0 moves the boxes
+    auto load = [&](int stage, const Cursor& c) {
+        const uint32_t to = ptx::smem_u32(ring + stage * SB), bar = ptx::smem_u32(&mv.full[stage]);
+        ptx::mbar_expect_tx(bar, SB);
+        load_tile<Q>(to, &p.tm[kX], c, c.n0 + rank * G::kTile, bar);
+        load_tile<Q>(to + Q::TB, &p.tm[kG], c, c.n0 + rank * G::kTile, bar);
+    };
+    auto store = [&](int stage, const Cursor& c) {
+        store_tile<Q>(&p.tm[kOut], ptx::smem_u32(ring + stage * SB), c, c.n0 + rank * G::kTile, p.T);
+        ptx::bulk_commit();
+    };
+    if (Q::kBoxes && threadIdx.x == 0) {
+        Cursor c = pre;
+        int n = 0;
+        for (; n < S && c.item < p.items; ++n) {
+            load(n, c);
+            advance<G::kChans>(p, c, step, clusters);
         }
-        if constexpr (!Q::kBoxes) copy_commit();
+        mv.next = c;
+        mv.loaded = n;
+    }
+
+    Cursor cur = pre;
+    auto fetch = [&](int stage) {
+        if constexpr (!Q::kBoxes) {
+            if (pre.item < p.items) {
+                uint8_t* to = ring + stage * SB + warp * Q::WB;
+                const int n = pre.n0 + row0;
+                copy_rows<E, LC, R, CB>(p, ptx::smem_u32(to), to, p.x, kX, pre, n, 0, 1, 0);
+                copy_rows<E, LC, R, CB>(p, ptx::smem_u32(to) + Q::TB, to + Q::TB, p.g, kG, pre, n, 0, 1, 0);
+                advance<G::kChans>(p, pre, step, clusters);
+            }
+            copy_commit();
+        }
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(i);
+    if (cs > 1) cluster_wait();  // every peer runs and has set up its mbarriers
 
     float2 carry = pair(0.f, 0.f);
+    bool dead = false;
     int it = 0, stage = 0;
     for (; cur.item < p.items; ++it) {
         const int c = cur.c0 + 2 * lc;
         const bool first = c < p.d, second = c + 1 < p.d;
-        const long long s0 = (cur.b * p.H + cur.h) * p.d + c;
-        if (cur.n0 == 0) carry = ld_state2(p.h_in, s0, first, second);
+        if (cur.n0 == 0) carry = ld_state2(p.h_in, ((long long)cur.b * p.H + cur.h) * p.d + c, first, second);
         if constexpr (Q::kBoxes) {
-            wait_for(&full[stage][warp], it / S & 1, dead);
-            landed += !dead;
+            wait_for(&mv.full[stage], it / S & 1, dead);
         } else {
             copy_wait<S - 2>();
             __syncwarp();
         }
         const int t0 = cur.n0 + row0 + seg * R, left = cur.len - t0;  // this thread's rows inside the sequence
-        uint8_t* const from = mine + stage * kWarps * 2 * Q::WB + Q::at(seg, 0) + lc * 2 * sizeof(E);
+        uint8_t* const from = ring + stage * SB + warp * Q::WB + Q::at(seg, 0) + lc * 2 * sizeof(E);
+        const bool whole = left >= R;
+        if (!whole) {  // rows behind the end change nothing, whatever they hold
+#pragma unroll 1
+            for (int r = max(left, 0); r < R; ++r) {
+                st_pair<E, true>(from + r * Q::RB, 0, pair(0.f, 0.f), true);
+                st_pair<E, true>(from + Q::TB + r * Q::RB, 0, idle_gate<GATE>(), true);
+            }
+        }
         float2 a[R], u[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float2 x = ld_pair(reinterpret_cast<const E*>(from + r * Q::RB));
             float2 om;
-            gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + Q::WB + r * Q::RB)), a[r], om);
+            gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + Q::TB + r * Q::RB)), a[r], om);
             u[r] = GATE == kGateMix ? ptx::mul2(om, x) : x;
-        }
-        if (left < R) {  // rows behind the end change nothing, whatever they hold
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r >= left) a[r] = pair(1.f, 1.f), u[r] = pair(0.f, 0.f);
         }
         Map own = {a[0], u[0]};
 #pragma unroll
         for (int r = 1; r < R; ++r) own = compose(own, Map{a[r], u[r]});
         __syncwarp();  // every lane has read the stage before this one, which is filled again
         fetch(stage == 0 ? S - 1 : stage - 1);
-        float2 h = scan_tile<LC>(sm, it, cs, rank, own, carry, dead);
-        const long long o0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c;
+        float2 h = scan_tile<LC>(sm, it, cur.n0 == 0, cs, rank, own, carry, dead, [&] {
+            if (Q::kBoxes && threadIdx.x == 0 && it > 0 && !dead) store(stage == 0 ? S - 1 : stage - 1, mv.held);
+        });
+        if (Q::kBoxes && threadIdx.x == 0 && !dead) {
+            mv.held = cur;
+            if (it > 0 && mv.next.item < p.items) {
+                Cursor n = mv.next;
+                ptx::bulk_wait_read<0>();  // the outputs have left the stage
+                load(stage == 0 ? S - 1 : stage - 1, n);
+                advance<G::kChans>(p, n, step, clusters);
+                mv.next = n;
+                ++mv.loaded;
+            }
+        }
         if constexpr (Q::kBoxes) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = ptx::fma2(a[r], h, u[r]);
                 st_pair<E, true>(from + r * Q::RB, 0, h, true);
             }
-            if (left < R) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (r >= left) st_pair<E, true>(from + r * Q::RB, 0, pair(0.f, 0.f), true);
+            if (!whole) {
+#pragma unroll 1
+                for (int r = max(left, 0); r < R; ++r) st_pair<E, true>(from + r * Q::RB, 0, pair(0.f, 0.f), true);
             }
             ptx::fence_async_smem();
-            __syncwarp();
-            if (lane == 0 && cur.n0 + row0 < p.T) {  // a box that ends behind T is cut there
-                tma_store_4d(&p.tm[kOut], ptx::smem_u32(mine + stage * kWarps * 2 * Q::WB), cur.c0, cur.n0 + row0,
-                             (int)cur.h, (int)cur.b);
-                ptx::bulk_commit();
-            }
         } else if (first) {
+            const long long o0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = ptx::fma2(a[r], h, u[r]);
                 if (r < left) st_pair<E, Q::VS>(p.out, o0 + (t0 + r) * p.st[kOut], h, second);
             }
         }
+        leave_tile<LC>(p, sm, it, cs, rank, cur, step, h, carry, first, second);
         if (cur.n0 + step >= cur.len) {
-            if (p.h_out && rank == 0 && threadIdx.x < LC) st_state2(p.h_out, s0, carry, first, second);
             // zeros behind the end; boxes have reached the end of the cluster's tile
-            const int t1 = Q::kBoxes ? cur.n0 + step : cur.len;
+            const long long o0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c;
             if (first)
-                for (int t = t1 + (rank * kWarps + warp) * G::kSegs + seg; t < p.T; t += cs * kWarps * G::kSegs)
+                for (int t = (Q::kBoxes ? cur.n0 + step : cur.len) + (rank * kWarps + warp) * G::kSegs + seg; t < p.T;
+                     t += cs * kWarps * G::kSegs)
                     st_pair<E, Q::VS>(p.out, o0 + t * p.st[kOut], pair(0.f, 0.f), second);
         }
         advance<G::kChans>(p, cur, step, clusters);
         stage = stage == S - 1 ? 0 : stage + 1;
     }
     if constexpr (Q::kBoxes) {
-        for (; landed < fetched; ++landed)  // after a wait that ran out: the loads on their way, once more
-            ptx::mbar_wait_bounded(ptx::smem_u32(&full[landed % S][warp]), landed / S & 1, kTimeoutCycles);
-        if (lane == 0) ptx::bulk_wait_all();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (it > 0 && !dead) store((it - 1) % S, mv.held);
+            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+            ptx::bulk_wait_all();
+        }
     }
     if (cs > 1) {  // no CTA leaves while a peer may still write to it
-        if (it == 0) cluster_wait();
         cluster_arrive();
         cluster_wait();
     }
@@ -408,133 +517,156 @@ template <typename E, int GATE, int LC, int R, int CB, int S>
 __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_constant__ Params p, int cs) {
     using G = Geo<LC, R>;
     using Q = Ring<E, LC, R, CB>;
-    constexpr int NT = GATE == kGateMix ? 4 : 3;  // g, dout, out, x
+    constexpr int NT = GATE == kGateMix ? 4 : 3, SB = NT * Q::TB;  // a stage: g, dout, out, x
     __shared__ Maps<LC> sm;
-    __shared__ uint64_t full[S][kWarps];
-    extern __shared__ __align__(128) uint8_t ring[];  // [S][warp][tensor][rows]
+    __shared__ Mover<S> mv;
+    extern __shared__ __align__(128) uint8_t ring[];  // [S][tensor][warp][rows]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / LC, lc = lane % LC;
     const int rank = blockIdx.x % cs, clusters = gridDim.x / cs, step = cs * G::kTile;
     const int row0 = (rank * kWarps + warp) * G::kRows;
-    uint8_t* const mine = ring + warp * NT * Q::WB;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S * kWarps; ++i) ptx::mbar_init(ptx::smem_u32(&full[0][0] + i), 1);
-        ptx::mbar_init(ptx::smem_u32(&sm.ready[0]), 1);
-        ptx::mbar_init(ptx::smem_u32(&sm.ready[1]), 1);
-        ptx::mbar_init_fence();
-    }
-    __syncthreads();
+    set_up(mv, sm);
     if (cs > 1) cluster_arrive();
-
     Cursor pre = {};
     pre.item = blockIdx.x / cs;
     enter<G::kChans>(p, pre);
-    Cursor cur = pre;
-    bool dead = false;
-    int fetched = 0, landed = 0;
-    auto fetch = [&](int stage) {
-        if (pre.item < p.items && !dead) {
-            uint8_t* to = mine + stage * kWarps * NT * Q::WB;
-            const uint32_t dst = ptx::smem_u32(to);
-            const int n = pre.n0 + row0, last = pre.len - 1;
-            if constexpr (Q::kBoxes) {
-                if (lane == 0) {
-                    // a box holds its tokens in ascending order; it may start before the first one
-                    const int t = pre.len - n - G::kRows, h = (int)pre.h, b = (int)pre.b;
-                    const uint32_t bar = ptx::smem_u32(&full[stage][warp]);
-                    ptx::bulk_wait_read<0>();
-                    ptx::mbar_expect_tx(bar, NT * Q::WB);
-                    tma_load_4d(dst, &p.tm[kG], pre.c0, t, h, b, bar);
-                    tma_load_4d(dst + Q::WB, &p.tm[kDout], pre.c0, t, h, b, bar);
-                    tma_load_4d(dst + 2 * Q::WB, &p.tm[kOutIn], pre.c0, t - 1, h, b, bar);
-                    if (GATE == kGateMix) tma_load_4d(dst + 3 * Q::WB, &p.tm[kX], pre.c0, t, h, b, bar);
-                }
-            } else {
-                copy_rows<E, LC, R, CB>(p, dst, to, p.g, kG, pre, n, last, -1, 0);
-                copy_rows<E, LC, R, CB>(p, dst + Q::WB, to + Q::WB, p.dout, kDout, pre, n, last, -1, 0);
-                // h before the token; the first token's is h0
-                copy_rows<E, LC, R, CB>(p, dst + 2 * Q::WB, to + 2 * Q::WB, p.out_in, kOutIn, pre, n, last, -1, -1);
-                if (GATE == kGateMix)
-                    copy_rows<E, LC, R, CB>(p, dst + 3 * Q::WB, to + 3 * Q::WB, p.x, kX, pre, n, last, -1, 0);
-            }
-            advance<G::kChans>(p, pre, step, clusters);
-            ++fetched;
+    // the first token of a CTA's tile, whose rows lie in ascending order; negative where the sequence begins
+    // inside the tile
+    auto low = [&](const Cursor& c) { return c.len - (c.n0 + rank * G::kTile) - G::kTile; };
+
+    // thread 0 moves the boxes
+    auto load = [&](int stage, const Cursor& c) {
+        const uint32_t to = ptx::smem_u32(ring + stage * SB), bar = ptx::smem_u32(&mv.full[stage]);
+        const int t = low(c);
+        ptx::mbar_expect_tx(bar, SB);
+        load_tile<Q>(to, &p.tm[kG], c, t, bar);
+        load_tile<Q>(to + Q::TB, &p.tm[kDout], c, t, bar);
+        load_tile<Q>(to + 2 * Q::TB, &p.tm[kOutIn], c, t - 1, bar);  // h before the token
+        if (GATE == kGateMix) load_tile<Q>(to + 3 * Q::TB, &p.tm[kX], c, t, bar);
+    };
+    auto store = [&](int stage, const Cursor& c) {
+        if (low(c) < 0) return;  // the warps have stored such a tile themselves
+        const uint32_t from = ptx::smem_u32(ring + stage * SB);
+        store_tile<Q>(&p.tm[kOut], from, c, low(c), p.T);
+        store_tile<Q>(&p.tm[kDg], from + Q::TB, c, low(c), p.T);
+        ptx::bulk_commit();
+    };
+    if (Q::kBoxes && threadIdx.x == 0) {
+        Cursor c = pre;
+        int n = 0;
+        for (; n < S && c.item < p.items; ++n) {
+            load(n, c);
+            advance<G::kChans>(p, c, step, clusters);
         }
-        if constexpr (!Q::kBoxes) copy_commit();
+        mv.next = c;
+        mv.loaded = n;
+    }
+
+    Cursor cur = pre;
+    auto fetch = [&](int stage) {
+        if constexpr (!Q::kBoxes) {
+            if (pre.item < p.items) {
+                uint8_t* to = ring + stage * SB + warp * Q::WB;
+                const uint32_t dst = ptx::smem_u32(to);
+                const int n = pre.n0 + row0, last = pre.len - 1;
+                copy_rows<E, LC, R, CB>(p, dst, to, p.g, kG, pre, n, last, -1, 0);
+                copy_rows<E, LC, R, CB>(p, dst + Q::TB, to + Q::TB, p.dout, kDout, pre, n, last, -1, 0);
+                copy_rows<E, LC, R, CB>(p, dst + 2 * Q::TB, to + 2 * Q::TB, p.out_in, kOutIn, pre, n, last, -1, -1);
+                if (GATE == kGateMix)
+                    copy_rows<E, LC, R, CB>(p, dst + 3 * Q::TB, to + 3 * Q::TB, p.x, kX, pre, n, last, -1, 0);
+                advance<G::kChans>(p, pre, step, clusters);
+            }
+            copy_commit();
+        }
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(i);
+    if (cs > 1) cluster_wait();
 
     float2 carry = pair(0.f, 0.f);
+    bool dead = false;
     int it = 0, stage = 0;
     for (; cur.item < p.items; ++it) {
         const int c = cur.c0 + 2 * lc;
         const bool first = c < p.d, second = c + 1 < p.d;
-        const long long s0 = (cur.b * p.H + cur.h) * p.d + c;
-        if (cur.n0 == 0) carry = ld_state2(p.h_in, s0, first, second);
+        if (cur.n0 == 0) carry = ld_state2(p.h_in, ((long long)cur.b * p.H + cur.h) * p.d + c, first, second);
         if constexpr (Q::kBoxes) {
-            wait_for(&full[stage][warp], it / S & 1, dead);
-            landed += !dead;
+            wait_for(&mv.full[stage], it / S & 1, dead);
         } else {
             copy_wait<S - 2>();
             __syncwarp();
         }
         const int n0 = cur.n0 + row0 + seg * R, left = cur.len - n0, t0 = left - 1;  // tokens t0, t0 - 1, ..
-        uint8_t* const base = mine + stage * kWarps * NT * Q::WB + lc * 2 * sizeof(E);
         // boxes lie in ascending order of the tokens, copied rows in the scan's
-        uint8_t* const from = base + (Q::kBoxes ? (G::kRows - 1 - seg * R) * Q::RB : Q::at(seg, 0));
+        uint8_t* const from = ring + stage * SB + lc * 2 * sizeof(E) +
+                              (Q::kBoxes ? (G::kTile - 1 - warp * G::kRows - seg * R) * Q::RB
+                                         : warp * Q::WB + Q::at(seg, 0));
         constexpr int RS = Q::kBoxes ? -Q::RB : Q::RB;
-        float2 a[R], f[R], d[R], om[GATE == kGateMix ? R : 1];
+        const bool whole = left >= R;
+        if (!whole) {  // positions behind the last: dout and out read as zeros there
+#pragma unroll 1
+            for (int r = max(left, 0); r < R; ++r) st_pair<E, true>(from + r * RS, 0, idle_gate<GATE>(), true);
+        }
+        auto d_of = [&](int r) { return ld_pair(reinterpret_cast<const E*>(from + Q::TB + r * RS)); };
+        float2 a[R], f[R], om[GATE == kGateMix ? R : 1];
+        Map own = {pair(1.f, 1.f), pair(0.f, 0.f)};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float2 o, before = ld_pair(reinterpret_cast<const E*>(from + 2 * Q::WB + r * RS));
+            float2 o, before = ld_pair(reinterpret_cast<const E*>(from + 2 * Q::TB + r * RS));
             gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + r * RS)), a[r], o);
-            d[r] = ld_pair(reinterpret_cast<const E*>(from + Q::WB + r * RS));
-            if (t0 - r == 0) before = ld_state2(p.h0, s0, first, second);
+            if (GATE == kGateMix)
+                before = ptx::fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f), before);
             f[r] = ptx::mul2(a[r], before);
-            if (GATE == kGateSigmoid) f[r] = ptx::mul2(f[r], o);
-            if (GATE == kGateMix) {
-                const float2 x = ld_pair(reinterpret_cast<const E*>(from + 3 * Q::WB + r * RS));
-                f[r] = ptx::mul2(ptx::mul2(a[r], o), ptx::fma2(x, pair(-1.f, -1.f), before));
-                om[r] = o;
-            }
-        }
-        if (left < R) {  // positions behind the last: their rows are zeros
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r >= left) a[r] = pair(1.f, 1.f);
-        }
-        Map own = {a[0], ptx::mul2(a[0], d[0])};
-#pragma unroll
-        for (int r = 1; r < R; ++r) {
-            own.H = ptx::mul2(a[r], ptx::add2(own.H, d[r]));
+            if (GATE != kGateDecay) f[r] = ptx::mul2(f[r], o);
+            if (GATE == kGateMix) om[r] = o;
+            own.H = ptx::mul2(a[r], ptx::add2(own.H, d_of(r)));
             own.A = ptx::mul2(own.A, a[r]);
+        }
+        if (t0 >= 0 && t0 < R) {  // the sequence's first token: h0 comes before it
+            const float2 h0 = ld_state2(p.h0, ((long long)cur.b * p.H + cur.h) * p.d + c, first, second);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r != t0) continue;
+                float2 ga, o, before = h0;
+                gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + r * RS)), ga, o);
+                if (GATE == kGateMix)
+                    before = ptx::fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f),
+                                       before);
+                f[r] = ptx::mul2(ga, before);
+                if (GATE != kGateDecay) f[r] = ptx::mul2(f[r], o);
+            }
         }
         __syncwarp();
         fetch(stage == 0 ? S - 1 : stage - 1);
-        float2 g = scan_tile<LC>(sm, it, cs, rank, own, carry, dead);
+        float2 g = scan_tile<LC>(sm, it, cur.n0 == 0, cs, rank, own, carry, dead, [&] {
+            if (Q::kBoxes && threadIdx.x == 0 && it > 0 && !dead) store(stage == 0 ? S - 1 : stage - 1, mv.held);
+        });
+        if (Q::kBoxes && threadIdx.x == 0 && !dead) {
+            mv.held = cur;
+            if (it > 0 && mv.next.item < p.items) {
+                Cursor n = mv.next;
+                ptx::bulk_wait_read<0>();  // the outputs have left the stage
+                load(stage == 0 ? S - 1 : stage - 1, n);
+                advance<G::kChans>(p, n, step, clusters);
+                mv.next = n;
+                ++mv.loaded;
+            }
+        }
         const long long x0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c, g0 = cur.b * p.sb[kDg] + cur.h * p.sh[kDg] + c;
-        const int low = cur.len - (cur.n0 + row0) - G::kRows;  // the warp's first token, if there are as many
-        if (Q::kBoxes && low >= 0) {
+        const bool boxes = Q::kBoxes && low(cur) >= 0;
+        if (boxes) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = ptx::add2(d[r], g);
+                const float2 dh = ptx::add2(d_of(r), g);
                 g = ptx::mul2(a[r], dh);
                 st_pair<E, true>(from + r * RS, 0, GATE == kGateMix ? ptx::mul2(om[GATE == kGateMix ? r : 0], dh) : dh,
                                  true);
-                st_pair<E, true>(from + Q::WB + r * RS, 0, ptx::mul2(dh, f[r]), true);
+                st_pair<E, true>(from + Q::TB + r * RS, 0, ptx::mul2(dh, f[r]), true);
             }
             ptx::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                const uint32_t src = ptx::smem_u32(mine + stage * kWarps * NT * Q::WB);
-                tma_store_4d(&p.tm[kOut], src, cur.c0, low, (int)cur.h, (int)cur.b);
-                tma_store_4d(&p.tm[kDg], src + Q::WB, cur.c0, low, (int)cur.h, (int)cur.b);
-                ptx::bulk_commit();
-            }
         } else if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = ptx::add2(d[r], g);
+                const float2 dh = ptx::add2(d_of(r), g);
                 g = ptx::mul2(a[r], dh);
                 if (r < left) {
                     st_pair<E, Q::VS>(p.out, x0 + (t0 - r) * p.st[kOut],
@@ -543,8 +675,10 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
                 }
             }
         }
+        if constexpr (Q::kBoxes) {
+        }
+        leave_tile<LC>(p, sm, it, cs, rank, cur, step, g, carry, first, second);
         if (cur.n0 + step >= cur.len) {
-            if (p.h_out && rank == 0 && threadIdx.x < LC) st_state2(p.h_out, s0, carry, first, second);
             if (first)
                 for (int t = cur.len + (rank * kWarps + warp) * G::kSegs + seg; t < p.T; t += cs * kWarps * G::kSegs) {
                     st_pair<E, Q::VS>(p.out, x0 + t * p.st[kOut], pair(0.f, 0.f), second);
@@ -555,17 +689,21 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         stage = stage == S - 1 ? 0 : stage + 1;
     }
     if constexpr (Q::kBoxes) {
-        for (; landed < fetched; ++landed)  // after a wait that ran out: the loads on their way, once more
-            ptx::mbar_wait_bounded(ptx::smem_u32(&full[landed % S][warp]), landed / S & 1, kTimeoutCycles);
-        if (lane == 0) ptx::bulk_wait_all();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (it > 0 && !dead) store((it - 1) % S, mv.held);
+            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+            ptx::bulk_wait_all();
+        }
     }
     if (cs > 1) {
-        if (it == 0) cluster_wait();
         cluster_arrive();
         cluster_wait();
     }
 }
 
+// ---- few tokens (a decoding step, short sequences): one thread per VW channels walks them, its rows loaded U at
+// a time
 template <int VW>
 __device__ __forceinline__ void ld_state(const float* s, long long off, float (&v)[VW]) {
 #pragma unroll
@@ -582,62 +720,128 @@ __device__ __forceinline__ void st_state(float* s, long long off, const float (&
     store(s, off, w);
 }
 
-// Few tokens (a decoding step): one thread per VW channels walks them.
-template <typename E, int GATE, int VW>
-__global__ void __launch_bounds__(128) glr_step_kernel(const __grid_constant__ Params p, long long lanes) {
+constexpr int kWalkThreads = 128;
+
+// The channels of one walking thread.
+struct Lane {
+    long long b, h, s0;  // s0: the state's offset
+    int c;
+};
+template <int VW>
+__device__ __forceinline__ Lane lane_of(const Params& p, long long i) {
+    const int per = p.d / VW;
+    const long long bh = i / per;
+    Lane l;
+    l.c = (int)(i - bh * per) * VW;
+    l.b = bh / p.H;
+    l.h = bh - l.b * p.H;
+    l.s0 = bh * p.d + l.c;
+    return l;
+}
+__device__ __forceinline__ long long offset(const Params& p, const Lane& l, int k) {
+    return l.b * p.sb[k] + l.h * p.sh[k] + l.c;
+}
+
+template <typename E, int GATE, int VW, int U>
+__global__ void __launch_bounds__(kWalkThreads) glr_walk_kernel(const __grid_constant__ Params p, long long lanes) {
     // a decoding loop's previous step wrote the state: wait for the grid before this one
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
     if (i >= lanes) return;
-    const int per = p.d / VW;
-    const long long bh = i / per;
-    const int c = (int)(i % per) * VW;
-    const long long b = bh / p.H, hd = bh % p.H;
-    const long long s0 = bh * p.d + c;
+    const Lane l = lane_of<VW>(p, i);
+    const long long x0 = offset(p, l, kX), g0 = offset(p, l, kG), o0 = offset(p, l, kOut);
+    const int len = length_of(p, l.b);
     float h[VW];
-    ld_state<VW>(p.h_in, s0, h);
-    const int len = length_of(p, b);
-    const long long x0 = b * p.sb[kX] + hd * p.sh[kX] + c, g0 = b * p.sb[kG] + hd * p.sh[kG] + c,
-                    o0 = b * p.sb[kOut] + hd * p.sh[kOut] + c;
-    for (int t = 0; t < p.T; ++t) {
-        Pack<E, VW> po;
-        zero(po);
-        if (t < len) {
-            const Pack<E, VW> px = load<E, VW>(p.x, x0 + t * p.st[kX]), pg = load<E, VW>(p.g, g0 + t * p.st[kG]);
+    ld_state<VW>(p.h_in, l.s0, h);
+    for (int t0 = 0; t0 < p.T; t0 += U) {
+        Pack<E, VW> px[U], pg[U];
 #pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                float ga, gc = 1.f;
-                if (GATE == kGateDecay) ga = decay_exp(elem(pg, j));
-                else logistic(elem(pg, j), ga, gc);
-                h[j] = fmaf(ga, h[j], GATE == kGateMix ? gc * elem(px, j) : elem(px, j));
+        for (int u = 0; u < U; ++u)
+            if (t0 + u < len) {
+                px[u] = load<E, VW>(p.x, x0 + (t0 + u) * p.st[kX]);
+                pg[u] = load<E, VW>(p.g, g0 + (t0 + u) * p.st[kG]);
             }
-            pack(po, h);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t0 + u >= p.T) break;
+            Pack<E, VW> po;
+            zero(po);
+            if (t0 + u < len) {
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    float ga, gc = 1.f;
+                    if (GATE == kGateDecay) ga = decay_exp(elem(pg[u], j));
+                    else logistic(elem(pg[u], j), ga, gc);
+                    h[j] = fmaf(ga, h[j], GATE == kGateMix ? gc * elem(px[u], j) : elem(px[u], j));
+                }
+                pack(po, h);
+            }
+            store(p.out, o0 + (t0 + u) * p.st[kOut], po);
         }
-        store(p.out, o0 + t * p.st[kOut], po);
     }
-    if (p.h_out) st_state<VW>(p.h_out, s0, h);
+    if (p.h_out) st_state<VW>(p.h_out, l.s0, h);
 }
 
-constexpr int kStepTokens = 4;  // up to this length the step kernel runs
+template <typename E, int GATE, int VW, int U>
+__global__ void __launch_bounds__(kWalkThreads) glr_walk_bwd_kernel(const __grid_constant__ Params p, long long lanes) {
+    const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
+    if (i >= lanes) return;
+    const Lane l = lane_of<VW>(p, i);
+    const long long x0 = offset(p, l, kX), g0 = offset(p, l, kG), h0 = offset(p, l, kOutIn), d0 = offset(p, l, kDout),
+                    ox = offset(p, l, kOut), og = offset(p, l, kDg);
+    const int len = length_of(p, l.b);
+    float c[VW];
+    ld_state<VW>(p.h_in, l.s0, c);
+    for (int t1 = p.T - 1; t1 >= 0; t1 -= U) {
+        Pack<E, VW> px[GATE == kGateMix ? U : 1], pg[U], ph[U], pd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t1 - u;
+            if (t >= 0 && t < len) {
+                pg[u] = load<E, VW>(p.g, g0 + t * p.st[kG]);
+                pd[u] = load<E, VW>(p.dout, d0 + t * p.st[kDout]);
+                if (t > 0) ph[u] = load<E, VW>(p.out_in, h0 + (t - 1) * p.st[kOutIn]);
+                if (GATE == kGateMix) px[GATE == kGateMix ? u : 0] = load<E, VW>(p.x, x0 + t * p.st[kX]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t1 - u;
+            if (t < 0) break;
+            Pack<E, VW> po, pq;
+            zero(po);
+            zero(pq);
+            if (t < len) {
+                float before[VW], dx[VW], dg[VW];
+#pragma unroll
+                for (int j = 0; j < VW; ++j) before[j] = elem(ph[u], j);
+                if (t == 0) ld_state<VW>(p.h0, l.s0, before);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    float ga, gc = 1.f;
+                    if (GATE == kGateDecay) ga = decay_exp(elem(pg[u], j));
+                    else logistic(elem(pg[u], j), ga, gc);
+                    float f = ga * (GATE == kGateMix ? before[j] - elem(px[GATE == kGateMix ? u : 0], j) : before[j]);
+                    if (GATE != kGateDecay) f *= gc;
+                    const float dh = elem(pd[u], j) + c[j];
+                    dx[j] = GATE == kGateMix ? gc * dh : dh;
+                    dg[j] = dh * f;
+                    c[j] = ga * dh;
+                }
+                pack(po, dx);
+                pack(pq, dg);
+            }
+            store(p.out, ox + t * p.st[kOut], po);
+            store(p.dg, og + t * p.st[kDg], pq);
+        }
+    }
+    if (p.h_out) st_state<VW>(p.h_out, l.s0, c);
+}
+
 constexpr long long kMaxGrid = 0x7fffffffLL;
-
-// A kernel's shared memory beyond the default 48 KB, once per device.
-bool allow_smem(const void* fn, int bytes) {
-    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
-struct Shape {
-    int lc, cs;
-};
-
-template <int R>
-Shape shape_of(long long seqs, int d, int T, bool narrow) {
-    Shape s = {32, 1};
-    if (getenv("GLR_LC")) s.lc = atoi(getenv("GLR_LC"));
-    if (getenv("GLR_CS")) s.cs = atoi(getenv("GLR_CS"));
-    return s;
-}
+constexpr int kSms = 152;
+constexpr int kMaxDevices = 64;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -680,86 +884,210 @@ struct Call {
     bool used[6];
     long long B;
     int gate, es;
-    bool bwd;
 };
 
-template <typename E, int LC, int R, int CB, int S>
-int launch_scan_kernel(void (*fn)(Params, int), const Call& c, int cs, int tensors, cudaStream_t s) {
-    Params p = c.p;
-    p.tiles = (p.d + 2 * LC - 1) / (2 * LC);
-    p.items = c.B * p.H * p.tiles;
-    const int bytes = S * kWarps * tensors * Ring<E, LC, R, CB>::WB;
-    if (p.items > kMaxGrid / cs) return 2;
-    if (CB == kTma)
-        for (int i = 0; i < 6; ++i)
-            if (c.used[i] && !encode_view(&p.tm[i], c.view[i], p, c.B, c.es, 2 * LC, Geo<LC, R>::kRows)) return -1;
-    if (!allow_smem(reinterpret_cast<const void*>(fn), bytes)) return 4;
-    long long clusters = p.items;
-    int per = getenv("GLR_PER") ? atoi(getenv("GLR_PER")) : 2;
-    if (clusters > 152 * per / cs) clusters = 152 * per / cs;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * cs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cs;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, p, cs) == cudaSuccess ? 0 : 4;
+// What is known of one kernel on each device: its shared memory allowed, and how many clusters of each size run
+// at once (0: not asked yet). Both are the same whoever asks first.
+struct KernelInfo {
+    std::atomic<int> ready[kMaxDevices];
+    std::atomic<int> clusters[kMaxDevices][17];
+};
+
+void describe(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int cs, int bytes) {
+    cfg->blockDim = dim3(kThreads);
+    cfg->dynamicSmemBytes = bytes;
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = cs;
+    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg->attrs = at;
+    cfg->numAttrs = 1;
 }
 
-template <typename E, int GATE, int VW>
-int launch_step(const Params& p, long long B, cudaStream_t s) {
-    const long long lanes = B * p.H * (p.d / VW), blocks = (lanes + 127) / 128;
+// Clusters of cs CTAs that run at once on device `dev`, two CTAs an SM; 0 on an error.
+template <typename Fn>
+int resident(Fn fn, KernelInfo& info, int dev, int cs, int bytes) {
+    if (!info.ready[dev].load(std::memory_order_acquire)) {
+        const void* f = reinterpret_cast<const void*>(fn);
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+            cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return 0;
+        info.ready[dev].store(1, std::memory_order_release);
+    }
+    int n = info.clusters[dev][cs].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        cfg.gridDim = dim3(cs);
+        describe(&cfg, at, cs, bytes);
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return 0;
+        info.clusters[dev][cs].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// A launch of one of the two tile shapes, and what it would cost.
+struct Plan {
+    int cs = 0;           // 0: the kernel cannot run
+    long long clusters = 0, cost = 0;
+};
+
+// The cluster size for a tile shape. A sequence's tiles are dealt to the cs CTAs of its cluster; every round of
+// cluster-wide tiles lasts as long as a tile on the fullest SM: measured (bf16 forward, tiles of 8192 elements)
+// 1.0 us where each SM holds one CTA, 1.75 us (narrow tiles 1.9 us) where one holds two, and 0.38 us more for the
+// exchange in a cluster. The costs are those, in eighths of a microsecond.
+template <int LC, typename Fn>
+Plan plan_for(Fn fn, KernelInfo& info, int dev, int bytes, long long items, int T, int rows) {
+    Plan best;
+    const long long tiles = ((long long)T + rows - 1) / rows;
+    for (int cs = 1; cs <= kMaxCluster<LC> && cs <= tiles; ++cs) {
+        const long long most = resident(fn, info, dev, cs, bytes);
+        if (most == 0) continue;
+        const long long clusters = items < most ? items : most;
+        const long long rounds = (items + clusters - 1) / clusters * ((tiles + cs - 1) / cs);
+        const long long cost = rounds * ((clusters * cs <= kSms ? 8 : LC < 32 ? 15 : 14) + (cs > 1 ? 3 : 0));
+        if (best.cs == 0 || cost < best.cost) {
+            best.cs = cs;
+            best.clusters = clusters;
+            best.cost = cost;
+        }
+    }
+    return best;
+}
+
+template <int LC>
+bool items_of(const Call& c, int* tiles, long long* items) {
+    *tiles = (int)(((long long)c.p.d + 2 * LC - 1) / (2 * LC));
+    *items = c.B * c.p.H * *tiles;
+    return *items < 1LL << 30;
+}
+
+// R: rows of a thread. Forward 16 (two fp32 values a row and channel stay in registers), backward 8 (four); half
+// for fp32, whose tiles take twice the shared memory. In the narrow tiles one less: the segments of a warp then
+// start in different banks (118 against 141 us for [1,12,131072,64] bf16).
+template <typename E, int LC, bool BWD>
+constexpr int kR = (BWD ? 8 : 16) / (int)(sizeof(E) / 2) - (LC < 32 && sizeof(E) == 2 ? 1 : 0);
+constexpr int kStages = 3;
+
+template <typename E, int GATE, int LC, int CB, bool BWD>
+struct Kernel {
+    static constexpr int R = kR<E, LC, BWD>;
+    using Q = Ring<E, LC, R, CB>;
+    static constexpr int kBytes = kStages * (BWD ? (GATE == kGateMix ? 4 : 3) : 2) * Q::TB;
+    static KernelInfo& info() {
+        static KernelInfo k;
+        return k;
+    }
+    static void (*fn())(Params, int) {
+        if constexpr (BWD) return glr_bwd_kernel<E, GATE, LC, R, CB, kStages>;
+        else return glr_fwd_kernel<E, GATE, LC, R, CB, kStages>;
+    }
+    static Plan plan(const Call& c, int dev) {
+        int tiles;
+        long long items;
+        if (!items_of<LC>(c, &tiles, &items)) return Plan{};
+        return plan_for<LC>(fn(), info(), dev, kBytes, items, c.p.T, Q::G::kTile);
+    }
+    // 0, a status, or -1: TMA does not take these tensors
+    static int launch(const Call& c, const Plan& plan, cudaStream_t s) {
+        Params p = c.p;
+        long long items;
+        if (!items_of<LC>(c, &p.tiles, &items)) return 2;
+        p.items = (int)items;
+        if (CB == kTma)
+            for (int i = 0; i < 6; ++i)
+                if (c.used[i] && !encode_view(&p.tm[i], c.view[i], p, c.B, c.es, 2 * LC, Q::kBoxRows)) return -1;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        describe(&cfg, at, plan.cs, kBytes);
+        cfg.gridDim = dim3((unsigned)(plan.clusters * plan.cs));
+        cfg.stream = s;
+        return cudaLaunchKernelEx(&cfg, fn(), p, plan.cs) == cudaSuccess ? 0 : 4;
+    }
+};
+
+// U: rows loaded at a time.
+template <typename E, int GATE, int VW, int U, bool BWD>
+int launch_walk_rows(const Call& c, cudaStream_t s) {
+    const long long lanes = c.B * c.p.H * (c.p.d / VW), blocks = (lanes + kWalkThreads - 1) / kWalkThreads;
     if (blocks > kMaxGrid) return 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, glr_step_kernel<E, GATE, VW>, p, lanes) == cudaSuccess ? 0 : 4;
+    if constexpr (BWD) {
+        glr_walk_bwd_kernel<E, GATE, VW, U><<<(unsigned)blocks, kWalkThreads, 0, s>>>(c.p, lanes);
+        return cudaGetLastError() == cudaSuccess ? 0 : 4;
+    } else {
+        // programmatic stream serialisation: consecutive steps overlap one's launch with the other's tail
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kWalkThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, glr_walk_kernel<E, GATE, VW, U>, c.p, lanes) == cudaSuccess ? 0 : 4;
+    }
 }
 
-template <typename E, int GATE, int LC, int CB>
-int launch_lc(const Call& c, int cs, cudaStream_t s) {
-    constexpr int RF = sizeof(E) == 2 ? 16 : 8, RB = sizeof(E) == 2 ? 8 : 4, S = 3;
-    if (!c.bwd) return launch_scan_kernel<E, LC, RF, CB, S>(glr_fwd_kernel<E, GATE, LC, RF, CB, S>, c, cs, 2, s);
-    return launch_scan_kernel<E, LC, RB, CB, S>(glr_bwd_kernel<E, GATE, LC, RB, CB, S>, c, cs, GATE == kGateMix ? 4 : 3, s);
+template <typename E, int GATE, int VW, bool BWD>
+int launch_walk(const Call& c, cudaStream_t s) {
+    if (c.p.T == 1) return launch_walk_rows<E, GATE, VW, 1, BWD>(c, s);
+    return launch_walk_rows<E, GATE, VW, VW == 1 || !BWD ? 8 : 4, BWD>(c, s);
 }
 
-template <typename E, int GATE>
-int launch_gate(const Call& c, int cb, bool vec4, cudaStream_t s) {
-    const Params& p = c.p;
-    if (!c.bwd && p.T <= kStepTokens) return vec4 ? launch_step<E, GATE, 4>(p, c.B, s) : launch_step<E, GATE, 1>(p, c.B, s);
-    const Shape sh = shape_of<16>(c.B * p.H, p.d, p.T, cb == 16);
+// Whether walking costs less than the plan. A token takes a walking thread 0.25 us forward and 0.63 us backward
+// (half a load's latency, and a third of one's of four tensors) up to about 40,000 threads on the GPU, then in
+// proportion to them; a plan has about 1 us of filling and emptying to it.
+template <bool BWD>
+bool walks(const Call& c, int vw, const Plan& plan) {
+    const long long lanes = c.B * c.p.H * (c.p.d / vw);
+    const long long token = BWD ? std::max(5LL, lanes / 9400) : std::max(2LL, lanes / 18600);
+    return c.p.T <= 256 && c.p.T * token <= plan.cost + 8;
+}
+
+// The plan's kernel, unless walking is cheaper.
+template <typename K, bool BWD, typename Walk>
+int launch_copied(const Call& c, int dev, int vw, Walk walk, cudaStream_t s) {
+    const Plan k = K::plan(c, dev);
+    if (k.cs == 0) return 4;
+    return walks<BWD>(c, vw, k) ? walk() : K::launch(c, k, s);
+}
+
+template <typename E, int GATE, bool BWD>
+int launch_scan(const Call& c, int cb, int vw, cudaStream_t s) {
+    auto walk = [&] { return vw == 4 ? launch_walk<E, GATE, 4, BWD>(c, s) : launch_walk<E, GATE, 1, BWD>(c, s); };
+    if (c.p.T <= 8) return walk();
+    int dev = 0, tiles;
+    long long items;
+    if (!items_of<32>(c, &tiles, &items)) return 2;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 4;
     if (cb == 16) {
-        const int st = sh.lc == 8    ? launch_lc<E, GATE, 8, kTma>(c, sh.cs, s)
-                       : sh.lc == 16 ? launch_lc<E, GATE, 16, kTma>(c, sh.cs, s)
-                                     : launch_lc<E, GATE, 32, kTma>(c, sh.cs, s);
-        return st >= 0 ? st : launch_lc<E, GATE, 32, 16>(c, sh.cs, s);
+        using Wide = Kernel<E, GATE, 32, kTma, BWD>;
+        using Narrow = Kernel<E, GATE, 8, kTma, BWD>;
+        const Plan w = Wide::plan(c, dev), n = Narrow::plan(c, dev);
+        if (w.cs == 0 && n.cs == 0) return 4;
+        // narrow tiles split the channels where sequences are few and long
+        const bool narrow = n.cs > 0 && (w.cs == 0 || n.cost < w.cost);
+        if (walks<BWD>(c, vw, narrow ? n : w)) return walk();
+        const int st = narrow ? Narrow::launch(c, n, s) : Wide::launch(c, w, s);
+        if (st >= 0) return st;
+        cb = 8;
     }
-    if (cb >= 4) return launch_lc<E, GATE, 32, 4>(c, sh.cs, s);
-    if constexpr (sizeof(E) == 2) return launch_lc<E, GATE, 32, 2>(c, sh.cs, s);
-    return 2;
+    if (cb == 8) return launch_copied<Kernel<E, GATE, 32, 8, BWD>, BWD>(c, dev, vw, walk, s);
+    if (cb == 4) return launch_copied<Kernel<E, GATE, 32, 4, BWD>, BWD>(c, dev, vw, walk, s);
+    if constexpr (sizeof(E) == 2) return launch_copied<Kernel<E, GATE, 32, 2, BWD>, BWD>(c, dev, vw, walk, s);
+    return 4;
 }
 
-template <typename E>
-int launch_type(const Call& c, int cb, bool vec4, cudaStream_t s) {
+template <typename E, bool BWD>
+int launch_gate(const Call& c, int cb, int vw, cudaStream_t s) {
     switch (c.gate) {
-        case kGateDecay: return launch_gate<E, kGateDecay>(c, cb, vec4, s);
-        case kGateSigmoid: return launch_gate<E, kGateSigmoid>(c, cb, vec4, s);
-        default: return launch_gate<E, kGateMix>(c, cb, vec4, s);
+        case kGateDecay: return launch_scan<E, kGateDecay, BWD>(c, cb, vw, s);
+        case kGateSigmoid: return launch_scan<E, kGateSigmoid, BWD>(c, cb, vw, s);
+        default: return launch_scan<E, kGateMix, BWD>(c, cb, vw, s);
     }
 }
 
+template <bool BWD>
 int launch(Call& c, const GlrArgs& a, cudaStream_t s) {
     Params& p = c.p;
     p.H = (int)a.n.H, p.T = a.n.T, p.d = a.n.d, p.lengths = a.lengths;
@@ -772,11 +1100,12 @@ int launch(Call& c, const GlrArgs& a, cudaStream_t s) {
         p.sb[i] = v.sb, p.sh[i] = v.sh, p.st[i] = v.st;
         vec4 = vec4 && (!c.used[i] || seq_vec_ok(v, c.es, 4 * c.es));
         while (cb > c.es && (((long long)p.d * c.es) % cb != 0 || (c.used[i] && !seq_vec_ok(v, c.es, cb))))
-            cb = cb == 16 ? 4 : cb / 2;
+            cb /= 2;
     }
     for (const void* st : {(const void*)p.h_in, (const void*)p.h0, (const void*)p.h_out})
         vec4 = vec4 && reinterpret_cast<uintptr_t>(st) % 16 == 0;
-    return a.n.bf16 ? launch_type<bf16>(c, cb, vec4, s) : launch_type<float>(c, cb, vec4, s);
+    const int vw = vec4 ? 4 : 1;
+    return a.n.bf16 ? launch_gate<bf16, BWD>(c, cb, vw, s) : launch_gate<float, BWD>(c, cb, vw, s);
 }
 
 }  // namespace
@@ -787,7 +1116,7 @@ int launch_glr_fwd(const GlrArgs& a, cudaStream_t s) {
     Params& p = c.p;
     p.x = a.x.p, p.g = a.g.p, p.out = a.out.p;
     p.h_in = a.h0, p.h_out = a.h_final;
-    return launch(c, a, s);
+    return launch<false>(c, a, s);
 }
 
 int launch_glr_bwd(const GlrArgs& a, cudaStream_t s) {
@@ -799,13 +1128,12 @@ int launch_glr_bwd(const GlrArgs& a, cudaStream_t s) {
         return e == cudaSuccess ? 0 : 4;
     }
     Call c = {};
-    c.bwd = true;
     c.view[kX] = a.x, c.view[kG] = a.g, c.view[kOutIn] = a.out, c.view[kDout] = a.dout, c.view[kOut] = a.dx,
     c.view[kDg] = a.dg;
     Params& p = c.p;
     p.x = a.x.p, p.g = a.g.p, p.out_in = a.out.p, p.dout = a.dout.p, p.out = a.dx.p, p.dg = a.dg.p;
     p.h_in = a.dh_final, p.h0 = a.h0, p.h_out = a.dh0;
-    return launch(c, a, s);
+    return launch<true>(c, a, s);
 }
 
 int glr_consume_timeout_flag(int* flag) {

@@ -20,6 +20,9 @@ namespace {
 using namespace gn;
 
 constexpr int kThreads = 256;
+#ifndef GN_UNR
+#define GN_UNR (NCH == 1 ? 2 : 1)
+#endif
 
 struct FwdParams {
     const void* x;
@@ -36,31 +39,31 @@ struct FwdParams {
     float inv_d, eps;
 };
 
-template <int N>
-__device__ __forceinline__ void act_all(int a, const float (&v)[N], float (&f)[N]) {
+template <int P>
+__device__ __forceinline__ void act_all(int a, const float2 (&v)[P], float2 (&f)[P]) {
     switch (a) {  // the same for the whole grid
         case kActNone:
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act<kActNone>(v[i]);
+            for (int i = 0; i < P; ++i) f[i] = act<kActNone>(v[i]);
             break;
         case kActSilu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act<kActSilu>(v[i]);
+            for (int i = 0; i < P; ++i) f[i] = act<kActSilu>(v[i]);
             break;
         case kActGelu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act<kActGelu>(v[i]);
+            for (int i = 0; i < P; ++i) f[i] = act<kActGelu>(v[i]);
             break;
         default:
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = act<kActSigmoid>(v[i]);
+            for (int i = 0; i < P; ++i) f[i] = act<kActSigmoid>(v[i]);
     }
 }
 
-template <typename E, int VW, int LPR, int NCH, int UNR, bool GATED>
+template <typename E, int VW, int LPR, int NCH, int UNR, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const __grid_constant__ FwdParams p) {
-    constexpr int N = NCH * VW;
-    const int l = threadIdx.x % LPR;
+    using Q = Row<VW, LPR, NCH, FULL>;
+    const Q q = {(int)threadIdx.x % LPR, p.d};
     const uint32_t i = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
     const bool have = i < p.total;  // a group without rows still takes part in the shuffles
     const uint32_t blk = have ? i : p.total - 1;
@@ -70,84 +73,57 @@ __global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const __grid_constant_
     const uint32_t h = p.heads_first ? f0 : f1;
     const int t0 = (int)((p.heads_first ? f1 : f0) * UNR);
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+    const int c0 = q.chan(0);
+    const E* x0 = static_cast<const E*>(p.x) + b * p.xb + h * p.xh + t0 * p.xt + c0;
+    const E* z0 = static_cast<const E*>(p.z) + (GATED ? b * p.zb + h * p.zh + t0 * p.zt + c0 : 0);
+    E* y0 = static_cast<E*>(p.y) + b * p.yb + h * p.yh + t0 * p.yt + c0;
 
-    bool live[N];
-    int c[NCH];
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-        c[k] = (l + LPR * k) * VW;
-#pragma unroll
-        for (int j = 0; j < VW; ++j) live[k * VW + j] = c[k] < p.d;
-    }
     Pack<E, VW> px[UNR][NCH], pz[UNR][GATED ? NCH : 1];
 #pragma unroll
     for (int u = 0; u < UNR; ++u)
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
-            const bool in = have && t0 + u < len && c[k] < p.d;
             zero(px[u][k]);
             if (GATED) zero(pz[u][k]);
-            if (in) {
-                px[u][k] = load<E, VW>(p.x, b * p.xb + h * p.xh + (t0 + u) * p.xt + c[k]);
-                if (GATED) pz[u][k] = load<E, VW>(p.z, b * p.zb + h * p.zh + (t0 + u) * p.zt + c[k]);
+            if (have && t0 + u < len && q.live(k)) {
+                px[u][k] = load<E, VW>(x0, u * p.xt + LPR * k * VW);
+                if (GATED) pz[u][k] = load<E, VW>(z0, u * p.zt + LPR * k * VW);
             }
         }
-    float w[N], bias[N];
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-        constexpr int FW = VW < 4 ? VW : 4;
-#pragma unroll
-        for (int j = 0; j < VW; j += FW) {
-            Pack<float, FW> pw, pb;
-            zero(pw);
-            zero(pb);
-            const bool in = c[k] < p.d;
-            if (p.w && in) pw = load<float, FW>(p.w, (long long)h * p.d + c[k] + j);
-            if (p.b && in) pb = load<float, FW>(p.b, (long long)h * p.d + c[k] + j);
-#pragma unroll
-            for (int m = 0; m < FW; ++m) {
-                w[k * VW + j + m] = p.w ? elem(pw, m) : 1.f;
-                bias[k * VW + j + m] = elem(pb, m);
-            }
-        }
-    }
+    float2 w[Q::P], bias[Q::P];
+    constexpr int FW = VW < 4 ? VW : 4;
+    q.template params<FW>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
+    q.template params<FW>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
-        float x[N], f[N];
+        float2 x[Q::P], f[Q::P];
+        q.get(px[u], x);
+        q.normalise(x, p.inv_d, p.eps);
 #pragma unroll
-        for (int k = 0; k < NCH; ++k)
+        for (int j = 0; j < Q::P; ++j) x[j] = ptx::fma2(x[j], w[j], bias[j]);
+        if constexpr (GATED) {
+            float2 z[Q::P];
+            q.get(pz[u], z);
+            act_all<Q::P>(p.act, z, f);
 #pragma unroll
-            for (int j = 0; j < VW; ++j) x[k * VW + j] = elem(px[u][k], j);
-        normalise<LPR, N>(x, live, p.d, p.inv_d, p.eps);
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = fmaf(x[j], w[j], bias[j]);
-        if (GATED) {
-            float z[N];
-#pragma unroll
-            for (int k = 0; k < NCH; ++k)
-#pragma unroll
-                for (int j = 0; j < VW; ++j) z[k * VW + j] = elem(pz[u][GATED ? k : 0], j);
-            act_all<N>(p.act, z, f);
-#pragma unroll
-            for (int j = 0; j < N; ++j) f[j] *= x[j];
+            for (int j = 0; j < Q::P; ++j) f[j] = ptx::mul2(f[j], x[j]);
         } else {
-            act_all<N>(p.act, x, f);
+            act_all<Q::P>(p.act, x, f);
         }
         const int t = t0 + u;
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
-            if (!have || t >= p.T || c[k] >= p.d) continue;
-            Pack<E, VW> po;
-            if (t < len) pack(po, f + k * VW);
-            else zero(po);
-            store(p.y, b * p.yb + h * p.yh + t * p.yt + c[k], po);
+            if (!have || t >= p.T || !q.live(k)) continue;
+            Pack<E, VW> po = q.template put<E>(f, k);
+            if (t >= len) zero(po);
+            store(y0, u * p.yt + LPR * k * VW, po);
         }
     }
 }
 
 template <typename E, int VW, int LPR, int NCH>
-int launch(const GnArgs& a, FwdParams p, long long B, long long H, cudaStream_t s) {
-    constexpr int UNR = NCH == 1 ? 4 : NCH == 2 ? 2 : 1;
+int launch(FwdParams p, long long B, long long H, cudaStream_t s) {
+    constexpr int UNR = GN_UNR;
     const long long TB = (p.T + UNR - 1) / UNR;
     const unsigned __int128 total = (unsigned __int128)B * H * TB;
     if (total >= ((unsigned __int128)1 << 31)) return 2;
@@ -157,25 +133,28 @@ int launch(const GnArgs& a, FwdParams p, long long B, long long H, cudaStream_t 
     p.slow = fast_div((uint32_t)(p.heads_first ? TB : H));
     constexpr int per = kThreads / LPR;
     const unsigned grid = (p.total + per - 1) / per;
-    if (p.z) gn_fwd_kernel<E, VW, LPR, NCH, UNR, true><<<grid, kThreads, 0, s>>>(p);
-    else gn_fwd_kernel<E, VW, LPR, NCH, UNR, false><<<grid, kThreads, 0, s>>>(p);
+    const bool full = p.d == VW * LPR * NCH;
+    if (p.z && full) gn_fwd_kernel<E, VW, LPR, NCH, UNR, true, true><<<grid, kThreads, 0, s>>>(p);
+    else if (p.z) gn_fwd_kernel<E, VW, LPR, NCH, UNR, true, false><<<grid, kThreads, 0, s>>>(p);
+    else if (full) gn_fwd_kernel<E, VW, LPR, NCH, UNR, false, true><<<grid, kThreads, 0, s>>>(p);
+    else gn_fwd_kernel<E, VW, LPR, NCH, UNR, false, false><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 template <typename E, int VW>
-int by_width(const GnArgs& a, const FwdParams& p, long long B, long long H, cudaStream_t s) {
+int by_width(const FwdParams& p, long long B, long long H, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
     if constexpr (VW > 1) {
-        if (nv <= 4) return launch<E, VW, 4, 1>(a, p, B, H, s);
-        if (nv <= 8) return launch<E, VW, 8, 1>(a, p, B, H, s);
-        if (nv <= 16) return launch<E, VW, 16, 1>(a, p, B, H, s);
+        if (nv <= 4) return launch<E, VW, 4, 1>(p, B, H, s);
+        if (nv <= 8) return launch<E, VW, 8, 1>(p, B, H, s);
+        if (nv <= 16) return launch<E, VW, 16, 1>(p, B, H, s);
+        if (nv <= 32) return launch<E, VW, 32, 1>(p, B, H, s);
     }
-    if (nv <= 32) return launch<E, VW, 32, 1>(a, p, B, H, s);
-    if (nv <= 64) return launch<E, VW, 32, 2>(a, p, B, H, s);
-    if (nv <= 128) return launch<E, VW, 32, 4>(a, p, B, H, s);
+    if (nv <= 64) return launch<E, VW, 32, 2>(p, B, H, s);
+    if (nv <= 128) return launch<E, VW, 32, 4>(p, B, H, s);
     if constexpr (VW * 256 <= kGnMaxD)
-        if (nv <= 256) return launch<E, VW, 32, 8>(a, p, B, H, s);
-    if constexpr (VW == 1) return launch<E, VW, 32, 32>(a, p, B, H, s);
+        if (nv <= 256) return launch<E, VW, 32, 8>(p, B, H, s);
+    if constexpr (VW == 1) return launch<E, VW, 32, 32>(p, B, H, s);
     return 2;
 }
 
@@ -199,8 +178,8 @@ int launch_gn_fwd(const GnArgs& a, cudaStream_t s) {
     const bool vec = a.n.d % (16 / es) == 0 && seq_vec_ok(a.x, es, 16) && seq_vec_ok(a.z, es, 16) &&
                      seq_vec_ok(a.y, es, 16) && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.b) % 16 == 0;
-    if (a.n.bf16) return vec ? by_width<bf16, 8>(a, p, B, a.n.H, s) : by_width<bf16, 1>(a, p, B, a.n.H, s);
-    return vec ? by_width<float, 4>(a, p, B, a.n.H, s) : by_width<float, 1>(a, p, B, a.n.H, s);
+    if (a.n.bf16) return vec ? by_width<bf16, 8>(p, B, a.n.H, s) : by_width<bf16, 1>(p, B, a.n.H, s);
+    return vec ? by_width<float, 4>(p, B, a.n.H, s) : by_width<float, 1>(p, B, a.n.H, s);
 }
 
 }  // namespace falcon

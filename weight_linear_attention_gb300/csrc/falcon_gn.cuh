@@ -11,58 +11,121 @@ namespace gn {
 
 using namespace seq;
 
-// ---- activations: v -> f(v), and its derivative
-template <int ACT>
-__device__ __forceinline__ float act(float v) {
-    if (ACT == kActNone) return v;
-    if (ACT == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    float s, c;
-    logistic(v, s, c);
-    return ACT == kActSilu ? v * s : s;
+// ---- activations. e^-v is cut at 2^126 (far below any type's resolution of the results), so that
+// s = 1 / (1 + e) and 1 - s = e s are both finite and exact to a few units; NaN stays NaN.
+__device__ __forceinline__ float2 exp_neg(float2 v) {
+    const float2 k = ptx::mul2(v, pair(-kLog2e, -kLog2e));
+    float2 e;
+    asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.x) : "f"(k.x));
+    asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.y) : "f"(k.y));
+    return pair(ex2(e.x), ex2(e.y));
 }
+__device__ __forceinline__ float2 rcp2(float2 v) { return pair(rcp(v.x), rcp(v.y)); }
+
 template <int ACT>
-__device__ __forceinline__ void act_slope(float v, float& f, float& df) {
+__device__ __forceinline__ float2 act(float2 v) {
+    if (ACT == kActNone) return v;
+    if (ACT == kActGelu) {
+        constexpr float r = 0.70710678118654752f;
+        return pair(0.5f * v.x * erfcf(-r * v.x), 0.5f * v.y * erfcf(-r * v.y));
+    }
+    const float2 s = rcp2(ptx::add2(exp_neg(v), pair(1.f, 1.f)));
+    return ACT == kActSilu ? ptx::mul2(v, s) : s;
+}
+// f(v) and f'(v)
+template <int ACT>
+__device__ __forceinline__ void act_slope(float2 v, float2& f, float2& df) {
     if (ACT == kActNone) {
         f = v;
-        df = 1.f;
+        df = pair(1.f, 1.f);
     } else if (ACT == kActGelu) {
-        const float phi = 0.5f * erfcf(-0.70710678118654752f * v);
-        f = v * phi;
-        df = fmaf(v * 0.39894228040143268f, expf(-0.5f * v * v), phi);
+        constexpr float r = 0.70710678118654752f, q = 0.39894228040143268f;
+        const float2 phi = pair(0.5f * erfcf(-r * v.x), 0.5f * erfcf(-r * v.y));
+        f = ptx::mul2(v, phi);
+        df = pair(fmaf(v.x * q, expf(-0.5f * v.x * v.x), phi.x), fmaf(v.y * q, expf(-0.5f * v.y * v.y), phi.y));
     } else {
-        float s, c;
-        logistic(v, s, c);
-        f = ACT == kActSilu ? v * s : s;
-        df = ACT == kActSilu ? fmaf(v * s, c, s) : s * c;
+        const float2 e = exp_neg(v), s = rcp2(ptx::add2(e, pair(1.f, 1.f))), c = ptx::mul2(e, s);
+        f = ACT == kActSilu ? ptx::mul2(v, s) : s;
+        df = ACT == kActSilu ? ptx::fma2(f, c, s) : ptx::mul2(s, c);
     }
 }
 
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(float2 p) {
+    float v = p.x + p.y;
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// x -> (x - mean) rstd in place, rows of d channels; elements behind d hold 0 on entry and return.
-// Two passes over the registers: the variance is that of the centred values.
-template <int LPR, int N>
-__device__ __forceinline__ float normalise(float (&x)[N], const bool (&live)[N], int d, float inv_d, float eps) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += x[i];
-    const float mean = row_sum<LPR>(s) * inv_d;
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = live[i] ? x[i] - mean : 0.f;
-        s = fmaf(x[i], x[i], s);
+// A thread's share of a row: NCH chunks of VW channels as P pairs. FULL: every lane's channels exist.
+template <int VW, int LPR, int NCH, bool FULL>
+struct Row {
+    static constexpr int P = NCH * VW / 2;
+    static_assert(NCH * VW % 2 == 0, "pairs");
+    int l;     // the lane of the row
+    int d;
+    __device__ __forceinline__ int chan(int k) const { return (l + LPR * k) * VW; }  // first of chunk k
+    __device__ __forceinline__ bool live(int k) const { return FULL || chan(k) < d; }
+    // the value of element e in pairs, 0 where it does not exist
+    __device__ __forceinline__ float2 keep(int i, float2 v) const {
+        return FULL ? v : pair(live(2 * i / VW) ? v.x : 0.f, live((2 * i + 1) / VW) ? v.y : 0.f);
     }
-    const float rstd = rsqrtf(row_sum<LPR>(s) * inv_d + eps);
+    template <typename E>
+    __device__ __forceinline__ void get(const Pack<E, VW> (&p)[NCH], float2 (&v)[P]) const {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] *= rstd;
-    return rstd;
-}
+        for (int i = 0; i < P; ++i)
+            v[i] = pair(elem(p[2 * i / VW], 2 * i % VW), elem(p[(2 * i + 1) / VW], (2 * i + 1) % VW));
+    }
+    // chunk k of pairs, in memory's form
+    template <typename E>
+    __device__ __forceinline__ Pack<E, VW> put(const float2 (&v)[P], int k) const {
+        float w[VW];
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            const int e = k * VW + j;
+            w[j] = e % 2 ? v[e / 2].y : v[e / 2].x;
+        }
+        Pack<E, VW> p;
+        pack(p, w);
+        return p;
+    }
+    // fp32 values per channel, `none` where there are none
+    template <int FW>
+    __device__ __forceinline__ void params(const float* s, float none, float2 (&v)[P]) const {
+        float w[NCH * VW];
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+#pragma unroll
+            for (int j = 0; j < VW; j += FW) {
+                Pack<float, FW> q;
+                zero(q);
+                if (s && live(k)) q = load<float, FW>(s, chan(k) + j);
+#pragma unroll
+                for (int m = 0; m < FW; ++m) w[k * VW + j + m] = s ? elem(q, m) : live(k) ? none : 0.f;
+            }
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = pair(w[2 * i], w[2 * i + 1]);
+    }
+    // x -> (x - mean) rstd in place; elements that do not exist hold 0 on entry and return. Two passes over the
+    // registers: the variance is that of the centred values.
+    __device__ __forceinline__ float normalise(float2 (&x)[P], float inv_d, float eps) const {
+        float2 s = x[0];
+#pragma unroll
+        for (int i = 1; i < P; ++i) s = ptx::add2(s, x[i]);
+        const float mean = row_sum<LPR>(s) * inv_d;
+        s = pair(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            x[i] = keep(i, ptx::add2(x[i], pair(-mean, -mean)));
+            s = ptx::fma2(x[i], x[i], s);
+        }
+        const float rstd = rsqrtf(row_sum<LPR>(s) * inv_d + eps);
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = ptx::mul2(x[i], pair(rstd, rstd));
+        return rstd;
+    }
+};
 
 // n / d for 0 <= n < 2^31 by a multiplication: q = (n mul) >> 32 >> shift, with mul = ceil(2^(32+shift)/d)
 // and 2^shift >= d / 2 (the error n (mul d - 2^(32+shift)) / (d 2^(32+shift)) stays below 1 / d).

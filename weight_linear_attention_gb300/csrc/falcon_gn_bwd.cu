@@ -19,7 +19,12 @@ using namespace gn;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 2;  // rows in flight of a group
+#ifndef GNB_U
+#define GNB_U 2
+#endif
+#ifndef GNB_PER
+#define GNB_PER 4
+#endif
 
 struct BwdParams {
     const void* x;
@@ -38,149 +43,121 @@ struct BwdParams {
     float inv_d, eps;
 };
 
-template <int N>
-__device__ __forceinline__ void slope_all(int a, const float (&v)[N], float (&f)[N], float (&df)[N]) {
+template <int P>
+__device__ __forceinline__ void slope_all(int a, const float2 (&v)[P], float2 (&f)[P], float2 (&df)[P]) {
     switch (a) {  // the same for the whole grid
         case kActNone:
 #pragma unroll
-            for (int i = 0; i < N; ++i) act_slope<kActNone>(v[i], f[i], df[i]);
+            for (int i = 0; i < P; ++i) act_slope<kActNone>(v[i], f[i], df[i]);
             break;
         case kActSilu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) act_slope<kActSilu>(v[i], f[i], df[i]);
+            for (int i = 0; i < P; ++i) act_slope<kActSilu>(v[i], f[i], df[i]);
             break;
         case kActGelu:
 #pragma unroll
-            for (int i = 0; i < N; ++i) act_slope<kActGelu>(v[i], f[i], df[i]);
+            for (int i = 0; i < P; ++i) act_slope<kActGelu>(v[i], f[i], df[i]);
             break;
         default:
 #pragma unroll
-            for (int i = 0; i < N; ++i) act_slope<kActSigmoid>(v[i], f[i], df[i]);
+            for (int i = 0; i < P; ++i) act_slope<kActSigmoid>(v[i], f[i], df[i]);
     }
 }
 
-template <typename E, int VW, int LPR, int NCH, bool GATED>
+template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const __grid_constant__ BwdParams p) {
-    constexpr int N = NCH * VW;
+    using Q = Row<VW, LPR, NCH, FULL>;
+    constexpr int P = Q::P;
     constexpr int G = kThreads / LPR;  // rows side by side
-    constexpr int U = NCH <= 2 ? kUnroll : 1;
-    __shared__ float part[kWarps][LPR * N];
-    const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    const uint32_t h = blockIdx.y;
-    bool live[N];
-    int c[NCH];
+    constexpr int U = NCH == 1 ? GNB_U : 1;
+    __shared__ float part[kWarps][LPR * NCH * VW];
+    const Q q = {(int)threadIdx.x % LPR, p.d};
+    const uint32_t grp = threadIdx.x / LPR, h = blockIdx.y;
+    float2 w[P], bias[P], aw[P], ab[P];
+    q.template params<1>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
+    q.template params<1>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-        c[k] = (l + LPR * k) * VW;
-#pragma unroll
-        for (int j = 0; j < VW; ++j) live[k * VW + j] = c[k] < p.d;
-    }
-    float w[N], bias[N], aw[N], ab[N];
-#pragma unroll
-    for (int k = 0; k < NCH; ++k)
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-            const long long at = (long long)h * p.d + c[k] + j;
-            w[k * VW + j] = p.w && c[k] < p.d ? p.w[at] : c[k] < p.d ? 1.f : 0.f;
-            bias[k * VW + j] = p.b && c[k] < p.d ? p.b[at] : 0.f;
-            aw[k * VW + j] = ab[k * VW + j] = 0.f;
-        }
+    for (int i = 0; i < P; ++i) aw[i] = ab[i] = pair(0.f, 0.f);
+    const E* x0 = static_cast<const E*>(p.x) + h * p.xh + q.chan(0);
+    const E* z0 = static_cast<const E*>(p.z) + (GATED ? h * p.zh + q.chan(0) : 0);
+    const E* d0 = static_cast<const E*>(p.dy) + h * p.yh + q.chan(0);
+    E* ox = static_cast<E*>(p.dx) + h * p.dxh + q.chan(0);
+    E* oz = static_cast<E*>(p.dz) + (GATED ? h * p.dzh + q.chan(0) : 0);
     const uint32_t step = gridDim.x * G * U;
     for (uint32_t r0 = blockIdx.x * G * U; r0 < p.rows; r0 += step) {  // the same count for a whole CTA
         Pack<E, VW> px[U][NCH], pz[U][GATED ? NCH : 1], pd[U][NCH];
-        long long b[U];
-        int t[U];
+        uint32_t b[U], t[U];
         bool have[U], in[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t r = r0 + u * G + grp;
             have[u] = r < p.rows;
-            const uint32_t q = div(have[u] ? r : 0, p.tokens);
-            b[u] = q;
-            t[u] = (int)((have[u] ? r : 0) - q * p.tokens.d);
-            in[u] = have[u] && (!p.lengths || t[u] < p.lengths[b[u]]);
+            b[u] = div(have[u] ? r : 0, p.tokens);
+            t[u] = (have[u] ? r : 0) - b[u] * p.tokens.d;
+            in[u] = have[u] && (!p.lengths || (int)t[u] < p.lengths[b[u]]);
 #pragma unroll
             for (int k = 0; k < NCH; ++k) {
                 zero(px[u][k]);
                 zero(pd[u][k]);
                 if (GATED) zero(pz[u][k]);
-                if (in[u] && c[k] < p.d) {
-                    px[u][k] = load<E, VW>(p.x, b[u] * p.xb + h * p.xh + t[u] * p.xt + c[k]);
-                    pd[u][k] = load<E, VW>(p.dy, b[u] * p.yb + h * p.yh + t[u] * p.yt + c[k]);
-                    if (GATED) pz[u][k] = load<E, VW>(p.z, b[u] * p.zb + h * p.zh + t[u] * p.zt + c[k]);
+                if (in[u] && q.live(k)) {
+                    px[u][k] = load<E, VW>(x0, b[u] * p.xb + t[u] * p.xt + LPR * k * VW);
+                    pd[u][k] = load<E, VW>(d0, b[u] * p.yb + t[u] * p.yt + LPR * k * VW);
+                    if (GATED) pz[u][k] = load<E, VW>(z0, b[u] * p.zb + t[u] * p.zt + LPR * k * VW);
                 }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float x[N], dn[N], f[N], df[N];
+            float2 x[P], dn[P], f[P], df[P];
+            q.get(px[u], x);
+            q.get(pd[u], dn);
+            const float rstd = q.normalise(x, p.inv_d, p.eps);
+            if constexpr (GATED) {
+                float2 z[P];
+                q.get(pz[u], z);
+                slope_all<P>(p.act, z, f, df);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    df[i] = ptx::mul2(ptx::mul2(dn[i], ptx::fma2(x[i], w[i], bias[i])), df[i]);  // dz
+                    dn[i] = ptx::mul2(dn[i], f[i]);
+                }
+#pragma unroll
+                for (int k = 0; k < NCH; ++k)
+                    if (have[u] && q.live(k)) {
+                        Pack<E, VW> po = q.template put<E>(df, k);
+                        if (!in[u]) zero(po);
+                        store(oz, b[u] * p.dzb + t[u] * p.dzt + LPR * k * VW, po);
+                    }
+            } else {
+                float2 n[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) n[i] = ptx::fma2(x[i], w[i], bias[i]);
+                slope_all<P>(p.act, n, f, df);
+#pragma unroll
+                for (int i = 0; i < P; ++i) dn[i] = ptx::mul2(dn[i], df[i]);
+            }
+            // rows behind the end were read as zeros: dy = 0, and no activation's slope at 0 is infinite
+            float2 s1 = pair(0.f, 0.f), s2 = s1;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                aw[i] = ptx::fma2(dn[i], x[i], aw[i]);
+                ab[i] = ptx::add2(ab[i], dn[i]);
+                dn[i] = ptx::mul2(dn[i], w[i]);  // p; 0 behind d
+                s1 = ptx::add2(s1, dn[i]);
+                s2 = ptx::fma2(dn[i], x[i], s2);
+            }
+            const float m1 = -row_sum<LPR>(s1) * p.inv_d, m2 = -row_sum<LPR>(s2) * p.inv_d;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                dn[i] = ptx::mul2(ptx::fma2(x[i], pair(m2, m2), ptx::add2(dn[i], pair(m1, m1))), pair(rstd, rstd));
 #pragma unroll
             for (int k = 0; k < NCH; ++k)
-#pragma unroll
-                for (int j = 0; j < VW; ++j) x[k * VW + j] = elem(px[u][k], j);
-            const float rstd = normalise<LPR, N>(x, live, p.d, p.inv_d, p.eps);
-            if (GATED) {
-                float z[N];
-#pragma unroll
-                for (int k = 0; k < NCH; ++k)
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) z[k * VW + j] = elem(pz[u][GATED ? k : 0], j);
-                slope_all<N>(p.act, z, f, df);
-#pragma unroll
-                for (int k = 0; k < NCH; ++k) {
-                    float dz[VW];
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) {
-                        const int e = k * VW + j;
-                        const float dy = elem(pd[u][k], j);
-                        dn[e] = dy * f[e];
-                        dz[j] = dy * fmaf(x[e], w[e], bias[e]) * df[e];
-                    }
-                    if (have[u] && c[k] < p.d) {
-                        Pack<E, VW> po;
-                        if (in[u]) pack(po, dz);
-                        else zero(po);
-                        store(p.dz, b[u] * p.dzb + h * p.dzh + t[u] * p.dzt + c[k], po);
-                    }
+                if (have[u] && q.live(k)) {
+                    Pack<E, VW> po = q.template put<E>(dn, k);
+                    if (!in[u]) zero(po);
+                    store(ox, b[u] * p.dxb + t[u] * p.dxt + LPR * k * VW, po);
                 }
-            } else {
-                float n[N];
-#pragma unroll
-                for (int e = 0; e < N; ++e) n[e] = fmaf(x[e], w[e], bias[e]);
-                slope_all<N>(p.act, n, f, df);
-#pragma unroll
-                for (int k = 0; k < NCH; ++k)
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) dn[k * VW + j] = elem(pd[u][k], j) * df[k * VW + j];
-            }
-            float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (in[u]) {  // rows behind the end hold zeros that a NaN of the gate's slope must not reach
-                    aw[e] = fmaf(dn[e], x[e], aw[e]);
-                    ab[e] += dn[e];
-                }
-                dn[e] *= w[e];  // p; 0 behind d
-                s1 += dn[e];
-                s2 = fmaf(dn[e], x[e], s2);
-            }
-            s1 = row_sum<LPR>(s1) * p.inv_d;
-            s2 = row_sum<LPR>(s2) * p.inv_d;
-#pragma unroll
-            for (int k = 0; k < NCH; ++k) {
-                float dx[VW];
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    const int e = k * VW + j;
-                    dx[j] = rstd * (dn[e] - s1 - x[e] * s2);
-                }
-                if (have[u] && c[k] < p.d) {
-                    Pack<E, VW> po;
-                    if (in[u]) pack(po, dx);
-                    else zero(po);
-                    store(p.dx, b[u] * p.dxb + h * p.dxh + t[u] * p.dxt + c[k], po);
-                }
-            }
         }
     }
     if (!p.ws) return;
@@ -189,14 +166,13 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_kernel(const __grid_constant_
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
-        for (int k = 0; k < NCH; ++k)
+        for (int e = 0; e < 2 * P; ++e) {
+            const float2 a = which ? ab[e / 2] : aw[e / 2];
+            float v = e % 2 ? a.y : a.x;
 #pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                float v = which ? ab[k * VW + j] : aw[k * VW + j];
-#pragma unroll
-                for (int o = 16; o >= LPR; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (threadIdx.x % 32 < LPR) part[threadIdx.x / 32][c[k] + j] = v;
-            }
+            for (int o = 16; o >= LPR; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (threadIdx.x % 32 < LPR) part[threadIdx.x / 32][q.chan(e / VW) + e % VW] = v;
+        }
         __syncthreads();
         for (int e = threadIdx.x; e < p.d; e += kThreads) {
             float v = 0.f;
@@ -237,8 +213,11 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
 template <typename E, int VW, int LPR, int NCH>
 int launch(const BwdParams& p, int splits, cudaStream_t s) {
     const dim3 grid((unsigned)splits, (unsigned)p.H);
-    if (p.z) gn_bwd_kernel<E, VW, LPR, NCH, true><<<grid, kThreads, 0, s>>>(p);
-    else gn_bwd_kernel<E, VW, LPR, NCH, false><<<grid, kThreads, 0, s>>>(p);
+    const bool full = p.d == VW * LPR * NCH;
+    if (p.z && full) gn_bwd_kernel<E, VW, LPR, NCH, true, true><<<grid, kThreads, 0, s>>>(p);
+    else if (p.z) gn_bwd_kernel<E, VW, LPR, NCH, true, false><<<grid, kThreads, 0, s>>>(p);
+    else if (full) gn_bwd_kernel<E, VW, LPR, NCH, false, true><<<grid, kThreads, 0, s>>>(p);
+    else gn_bwd_kernel<E, VW, LPR, NCH, false, false><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
@@ -249,8 +228,8 @@ int by_width(const BwdParams& p, int splits, cudaStream_t s) {
         if (nv <= 4) return launch<E, VW, 4, 1>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 8, 1>(p, splits, s);
         if (nv <= 16) return launch<E, VW, 16, 1>(p, splits, s);
+        if (nv <= 32) return launch<E, VW, 32, 1>(p, splits, s);
     }
-    if (nv <= 32) return launch<E, VW, 32, 1>(p, splits, s);
     if (nv <= 64) return launch<E, VW, 32, 2>(p, splits, s);
     if (nv <= 128) return launch<E, VW, 32, 4>(p, splits, s);
     if constexpr (VW * 256 <= kGnMaxD)
@@ -264,7 +243,7 @@ int by_width(const BwdParams& p, int splits, cudaStream_t s) {
 // As many CTAs as run at once (4 per SM), over the heads; no more than there are rows for.
 int gn_bwd_splits(const SeqSizes& n) {
     const long long rows = n.B * n.T;
-    long long s = (152 * 4 + n.H - 1) / n.H;
+    long long s = (152 * GNB_PER + n.H - 1) / n.H;
     const long long most = (rows + 31) / 32;
     if (s > most) s = most;
     return s < 1 ? 1 : (int)s;

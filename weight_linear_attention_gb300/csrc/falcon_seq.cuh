@@ -141,10 +141,7 @@ __device__ __forceinline__ float2 decay_exp2(float2 v) {
 // ---- asynchronous copies of CB bytes, global to shared; `in` false writes zeros and reads nothing
 template <int CB>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
-    if (CB == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(CB), "r"(in ? CB : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
