@@ -4,13 +4,14 @@
 //
 // A memory-bound transposition with arithmetic on the way: 2 (3 with a gate) tensors' bytes per element.
 // LPR lanes hold a row in registers (16 bytes a lane), so the row is read once and the variance is that
-// of the centred values; a thread takes UNR tokens of one head, so that weight and bias are fetched once
-// for them and UNR (2 UNR) vector loads are in flight. Row blocks go over the heads first where y's heads
-// are its closer axis (the projection's layout), else over the tokens, so that neighbouring CTAs write
-// neighbouring memory.
+// of the centred values. A group of lanes keeps one head, so that weight and bias stay in registers, and
+// steps over the tokens, the next row's loads on their way while it works on this one; neighbouring groups
+// have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <numeric>
 
 #include "falcon_gn.cuh"
 
@@ -20,22 +21,16 @@ namespace {
 using namespace gn;
 
 constexpr int kThreads = 256;
-#ifndef GN_UNR
-#define GN_UNR (NCH == 1 ? 2 : 1)
-#endif
+
+enum { kX, kZ, kY };
 
 struct FwdParams {
-    const void* x;
-    const void* z;
-    void* y;
+    Tensors<3> s;
     const float* w;
     const float* b;
     const int32_t* lengths;
-    long long xb, xh, xt, zb, zh, zt, yb, yh, yt;
-    uint32_t total;      // row blocks
-    FastDiv fast, slow;  // the sizes of the block index's fastest axis and of the next
-    int heads_first;
-    int T, d, act;
+    uint32_t rows, H;  // B T, heads
+    int d, act;
     float inv_d, eps;
 };
 
@@ -60,126 +55,145 @@ __device__ __forceinline__ void act_all(int a, const float2 (&v)[P], float2 (&f)
     }
 }
 
-template <typename E, int VW, int LPR, int NCH, int UNR, bool GATED, bool FULL>
-__global__ void __launch_bounds__(kThreads) gn_fwd_kernel(const __grid_constant__ FwdParams p) {
-    using Q = Row<VW, LPR, NCH, FULL>;
-    const Q q = {(int)threadIdx.x % LPR, p.d};
-    const uint32_t i = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
-    const bool have = i < p.total;  // a group without rows still takes part in the shuffles
-    const uint32_t blk = have ? i : p.total - 1;
-    const uint32_t q1 = div(blk, p.fast), f0 = blk - q1 * p.fast.d;
-    const uint32_t q2 = div(q1, p.slow), f1 = q1 - q2 * p.slow.d;
-    const long long b = q2;
-    const uint32_t h = p.heads_first ? f0 : f1;
-    const int t0 = (int)((p.heads_first ? f1 : f0) * UNR);
-    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    const int c0 = q.chan(0);
-    const E* x0 = static_cast<const E*>(p.x) + b * p.xb + h * p.xh + t0 * p.xt + c0;
-    const E* z0 = static_cast<const E*>(p.z) + (GATED ? b * p.zb + h * p.zh + t0 * p.zt + c0 : 0);
-    E* y0 = static_cast<E*>(p.y) + b * p.yb + h * p.yh + t0 * p.yt + c0;
+// CTAs that an SM is given: what the registers of the row's width allow.
+template <int VW, int NCH>
+constexpr int kPerSm = NCH * VW <= 4 ? 4 : NCH * VW <= 8 ? 3 : NCH * VW <= 24 ? 2 : 1;
 
-    Pack<E, VW> px[UNR][NCH], pz[UNR][GATED ? NCH : 1];
+template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
+__global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const __grid_constant__ FwdParams p) {
+    using Q = Row<VW, LPR, NCH, FULL>;
+    constexpr int P = Q::P, G = kThreads / LPR;
+    constexpr bool kAhead = NCH * VW <= 16;  // the registers take the next row too
+    const Q q = {(int)threadIdx.x % LPR, p.d};
+    const uint32_t first = blockIdx.x * G, i = first + threadIdx.x / LPR;
+    const uint32_t h = i % p.H;
+    const int c0 = q.chan(0) * (int)sizeof(E);
+    constexpr int CB = LPR * VW * sizeof(E);  // from one chunk of a lane to its next
+    using V = Pack<E, VW>;
+    V px[NCH], pz[GATED ? NCH : 1];
+    Walk<3> at;
+    at.start(p.s, i / p.H, h, c0);
+    bool in;  // the row at hand lies inside its sequence; others are worked on with what the registers hold
 #pragma unroll
-    for (int u = 0; u < UNR; ++u)
+    for (int k = 0; k < NCH; ++k) {
+        zero(px[k]);
+        if (GATED) zero(pz[k]);
+    }
+    auto fetch = [&] {
+        in = at.r < p.rows;
+        if (in && p.lengths) in = (int)at.t < p.lengths[div(at.r, p.s.tokens)];
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
-            zero(px[u][k]);
-            if (GATED) zero(pz[u][k]);
-            if (have && t0 + u < len && q.live(k)) {
-                px[u][k] = load<E, VW>(x0, u * p.xt + LPR * k * VW);
-                if (GATED) pz[u][k] = load<E, VW>(z0, u * p.zt + LPR * k * VW);
+            if (in && q.live(k)) {
+                px[k] = at.template get<V>(kX, k * CB);
+                if (GATED) pz[k] = at.template get<V>(kZ, k * CB);
             }
         }
-    float2 w[Q::P], bias[Q::P];
+    };
+    if (kAhead) fetch();
+    float2 w[P], bias[P];
     constexpr int FW = VW < 4 ? VW : 4;
     q.template params<FW>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
     q.template params<FW>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
-#pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-        float2 x[Q::P], f[Q::P];
-        q.get(px[u], x);
+    // the CTA's first group has the first rows: all take as many turns as it has
+    for (uint32_t r = first / p.H; r < p.rows; r += p.s.by) {
+        if (!kAhead) fetch();
+        float2 x[P], z[GATED ? P : 1], f[P];
+        q.get(px, x);
+        if constexpr (GATED) q.get(pz, z);
+        const bool mine = at.r < p.rows, was_in = in;
+        char* const out = at.at[kY];
+        if (r + p.s.by < p.rows) {
+            at.step(p.s, h, c0);
+            if (kAhead) fetch();
+        }
         q.normalise(x, p.inv_d, p.eps);
 #pragma unroll
-        for (int j = 0; j < Q::P; ++j) x[j] = ptx::fma2(x[j], w[j], bias[j]);
+        for (int j = 0; j < P; ++j) x[j] = ptx::fma2(x[j], w[j], bias[j]);
         if constexpr (GATED) {
-            float2 z[Q::P];
-            q.get(pz[u], z);
-            act_all<Q::P>(p.act, z, f);
+            act_all<P>(p.act, z, f);
 #pragma unroll
-            for (int j = 0; j < Q::P; ++j) f[j] = ptx::mul2(f[j], x[j]);
+            for (int j = 0; j < P; ++j) f[j] = ptx::mul2(f[j], x[j]);
         } else {
-            act_all<Q::P>(p.act, x, f);
+            act_all<P>(p.act, x, f);
         }
-        const int t = t0 + u;
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
-            if (!have || t >= p.T || !q.live(k)) continue;
-            Pack<E, VW> po = q.template put<E>(f, k);
-            if (t >= len) zero(po);
-            store(y0, u * p.yt + LPR * k * VW, po);
+            if (!mine || !q.live(k)) continue;
+            V po;
+            if (was_in) po = q.template put<E>(f, k);
+            else zero(po);
+            *reinterpret_cast<V*>(out + k * CB) = po;
         }
     }
 }
 
 template <typename E, int VW, int LPR, int NCH>
-int launch(FwdParams p, long long B, long long H, cudaStream_t s) {
-    constexpr int UNR = GN_UNR;
-    const long long TB = (p.T + UNR - 1) / UNR;
-    const unsigned __int128 total = (unsigned __int128)B * H * TB;
-    if (total >= ((unsigned __int128)1 << 31)) return 2;
-    p.total = (uint32_t)total;
-    p.heads_first = p.yh < p.yt || p.T == 1;
-    p.fast = fast_div((uint32_t)(p.heads_first ? H : TB));
-    p.slow = fast_div((uint32_t)(p.heads_first ? TB : H));
-    constexpr int per = kThreads / LPR;
-    const unsigned grid = (p.total + per - 1) / per;
-    const bool full = p.d == VW * LPR * NCH;
-    if (p.z && full) gn_fwd_kernel<E, VW, LPR, NCH, UNR, true, true><<<grid, kThreads, 0, s>>>(p);
-    else if (p.z) gn_fwd_kernel<E, VW, LPR, NCH, UNR, true, false><<<grid, kThreads, 0, s>>>(p);
-    else if (full) gn_fwd_kernel<E, VW, LPR, NCH, UNR, false, true><<<grid, kThreads, 0, s>>>(p);
-    else gn_fwd_kernel<E, VW, LPR, NCH, UNR, false, false><<<grid, kThreads, 0, s>>>(p);
+int launch(FwdParams p, cudaStream_t s) {
+    constexpr int G = kThreads / LPR;
+    const unsigned __int128 groups = (unsigned __int128)p.rows * p.H;
+    if (groups >= ((unsigned __int128)1 << 31)) return 2;
+    // the grid's groups are a multiple of the heads, so that a group keeps its head; no more CTAs than run at once
+    const uint32_t unit = p.H / std::gcd(p.H, (uint32_t)G);
+    const uint32_t most = ((uint32_t)groups + G - 1) / G, slots = kSms * kPerSm<VW, NCH>;
+    const uint32_t grid = most <= slots ? (most + unit - 1) / unit * unit : std::max(slots / unit, 1u) * unit;
+    p.s.by = (uint32_t)((unsigned long long)grid * G / p.H);
+    for (int k = 0; k < 3; ++k) p.s.inc[k] = p.s.by * p.s.st[k];
+    const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
+    if (gated && full) gn_fwd_kernel<E, VW, LPR, NCH, true, true><<<grid, kThreads, 0, s>>>(p);
+    else if (gated) gn_fwd_kernel<E, VW, LPR, NCH, true, false><<<grid, kThreads, 0, s>>>(p);
+    else if (full) gn_fwd_kernel<E, VW, LPR, NCH, false, true><<<grid, kThreads, 0, s>>>(p);
+    else gn_fwd_kernel<E, VW, LPR, NCH, false, false><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 template <typename E, int VW>
-int by_width(const FwdParams& p, long long B, long long H, cudaStream_t s) {
+int by_width(const FwdParams& p, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
     if constexpr (VW > 1) {
-        if (nv <= 4) return launch<E, VW, 4, 1>(p, B, H, s);
-        if (nv <= 8) return launch<E, VW, 8, 1>(p, B, H, s);
-        if (nv <= 16) return launch<E, VW, 16, 1>(p, B, H, s);
-        if (nv <= 32) return launch<E, VW, 32, 1>(p, B, H, s);
+        if (nv <= 4) return launch<E, VW, 4, 1>(p, s);
+        if (nv <= 8) return launch<E, VW, 8, 1>(p, s);
+        if (nv <= 16) return launch<E, VW, 16, 1>(p, s);
+        if (nv <= 32) return launch<E, VW, 32, 1>(p, s);
     }
-    if (nv <= 64) return launch<E, VW, 32, 2>(p, B, H, s);
-    if (nv <= 128) return launch<E, VW, 32, 4>(p, B, H, s);
+    if (nv <= 64) return launch<E, VW, 32, 2>(p, s);
+    if constexpr (VW > 1)
+        if (nv <= 96) return launch<E, VW, 32, 3>(p, s);
+    if (nv <= 128) return launch<E, VW, 32, 4>(p, s);
+    if constexpr (VW == 4)
+        if (nv <= 192) return launch<E, VW, 32, 6>(p, s);
     if constexpr (VW * 256 <= kGnMaxD)
-        if (nv <= 256) return launch<E, VW, 32, 8>(p, B, H, s);
-    if constexpr (VW == 1) return launch<E, VW, 32, 32>(p, B, H, s);
+        if (nv <= 256) return launch<E, VW, 32, 8>(p, s);
+    if constexpr (VW == 1) return launch<E, VW, 32, 32>(p, s);
     return 2;
 }
 
 }  // namespace
 
 int launch_gn_fwd(const GnArgs& a, cudaStream_t s) {
+    if ((unsigned __int128)a.n.B * a.n.T >= ((unsigned __int128)1 << 31) || a.n.H >= 1LL << 30) return 2;
     FwdParams p = {};
-    p.x = a.x.p, p.z = a.z.p, p.y = a.y.p;
     p.w = a.w, p.b = a.b, p.lengths = a.lengths;
-    p.xb = a.x.sb, p.xh = a.x.sh, p.xt = a.x.st;
-    p.zb = a.z.sb, p.zh = a.z.sh, p.zt = a.z.st;
-    p.yb = a.y.sb, p.yh = a.y.sh, p.yt = a.y.st;
-    p.T = a.n.T, p.d = a.n.d, p.act = a.act;
-    p.inv_d = 1.f / a.n.d, p.eps = a.eps;
-    long long B = a.n.B;
-    if (p.T == 1 && !p.lengths && B < (1LL << 30)) {  // single tokens: the batch takes the tokens' place
-        p.T = (int)B, B = 1;
-        p.xt = p.xb, p.zt = p.zb, p.yt = p.yb;
-    }
+    const SeqView* v[] = {&a.x, &a.z, &a.y};
     const int es = a.n.bf16 ? 2 : 4;
-    const bool vec = a.n.d % (16 / es) == 0 && seq_vec_ok(a.x, es, 16) && seq_vec_ok(a.z, es, 16) &&
-                     seq_vec_ok(a.y, es, 16) && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.b) % 16 == 0;
-    if (a.n.bf16) return vec ? by_width<bf16, 8>(p, B, a.n.H, s) : by_width<bf16, 1>(p, B, a.n.H, s);
-    return vec ? by_width<float, 4>(p, B, a.n.H, s) : by_width<float, 1>(p, B, a.n.H, s);
+    int vw = 16 / es;  // elements that every access can move at a time: 16 bytes, or 8, else one
+    while (vw > 1 && a.n.d % vw) vw /= 2;
+    for (int k = 0; k < 3; ++k) {
+        p.s.base[k] = static_cast<char*>(v[k]->p);
+        p.s.sb[k] = v[k]->sb * es, p.s.sh[k] = v[k]->sh * es, p.s.st[k] = v[k]->st * es;
+        while (vw > 1 && !seq_vec_ok(*v[k], es, vw * es)) vw /= 2;
+    }
+    p.d = a.n.d, p.act = a.act, p.H = (uint32_t)a.n.H;
+    p.rows = (uint32_t)(a.n.B * a.n.T);
+    p.s.tokens = fast_div((uint32_t)a.n.T);
+    p.inv_d = 1.f / a.n.d, p.eps = a.eps;
+    if (a.n.T == 1 && !p.lengths) {  // single tokens: the batch takes the tokens' place
+        p.s.tokens = fast_div(p.rows);
+        for (int k = 0; k < 3; ++k) p.s.st[k] = p.s.sb[k];
+    }
+    if (reinterpret_cast<uintptr_t>(a.w) % 16 || reinterpret_cast<uintptr_t>(a.b) % 16) vw = 1;
+    if (a.n.bf16) return vw == 8 ? by_width<bf16, 8>(p, s) : vw == 4 ? by_width<bf16, 4>(p, s) : by_width<bf16, 1>(p, s);
+    return vw == 4 ? by_width<float, 4>(p, s) : by_width<float, 1>(p, s);
 }
 
 }  // namespace falcon

@@ -22,12 +22,31 @@ __device__ __forceinline__ float2 exp_neg(float2 v) {
 }
 __device__ __forceinline__ float2 rcp2(float2 v) { return pair(rcp(v.x), rcp(v.y)); }
 
+// The normal distribution function and e = exp(-v^2 / 2). With x = |v| / sqrt 2 and t = 1 / (1 + 0.45 x),
+// exp(x^2) erfc(x) = t P(t); P is a least-squares fit of degree 9 over t in (0, 1], its weights moved until the
+// relative error was level at 3.2e-8. The lower tail keeps its relative accuracy; the upper is one minus it.
+__device__ __forceinline__ void normal2(float2 v, float2& phi, float2& e) {
+    constexpr float kT = 0.45f * 0.70710678118654752f, kE = -0.5f * kLog2e;
+    const float2 t = pair(rcp(fmaf(kT, fabsf(v.x), 1.f)), rcp(fmaf(kT, fabsf(v.y), 1.f)));
+    constexpr float c[10] = {0.25388533f, 0.25388315f, 0.22827165f, 0.17525212f, 0.11995047f,
+                             -0.02235809f, 0.14240131f, -0.30058289f, 0.19068813f, -0.04139117f};
+    float2 p = pair(c[9], c[9]);
+#pragma unroll
+    for (int k = 8; k >= 0; --k) p = ptx::fma2(p, t, pair(c[k], c[k]));
+    const float2 s = ptx::mul2(ptx::mul2(v, v), pair(kE, kE));
+    e = pair(ex2(s.x), ex2(s.y));
+    const float2 low = ptx::mul2(ptx::mul2(t, pair(0.5f, 0.5f)), ptx::mul2(p, e));
+    const float2 high = ptx::fma2(low, pair(-1.f, -1.f), pair(1.f, 1.f));
+    phi = pair(v.x > 0.f ? high.x : low.x, v.y > 0.f ? high.y : low.y);
+}
+
 template <int ACT>
 __device__ __forceinline__ float2 act(float2 v) {
     if (ACT == kActNone) return v;
     if (ACT == kActGelu) {
-        constexpr float r = 0.70710678118654752f;
-        return pair(0.5f * v.x * erfcf(-r * v.x), 0.5f * v.y * erfcf(-r * v.y));
+        float2 phi, e;
+        normal2(v, phi, e);
+        return ptx::mul2(v, phi);
     }
     const float2 s = rcp2(ptx::add2(exp_neg(v), pair(1.f, 1.f)));
     return ACT == kActSilu ? ptx::mul2(v, s) : s;
@@ -39,10 +58,11 @@ __device__ __forceinline__ void act_slope(float2 v, float2& f, float2& df) {
         f = v;
         df = pair(1.f, 1.f);
     } else if (ACT == kActGelu) {
-        constexpr float r = 0.70710678118654752f, q = 0.39894228040143268f;
-        const float2 phi = pair(0.5f * erfcf(-r * v.x), 0.5f * erfcf(-r * v.y));
+        constexpr float q = 0.39894228040143268f;  // 1 / sqrt(2 pi)
+        float2 phi, e;
+        normal2(v, phi, e);
         f = ptx::mul2(v, phi);
-        df = pair(fmaf(v.x * q, expf(-0.5f * v.x * v.x), phi.x), fmaf(v.y * q, expf(-0.5f * v.y * v.y), phi.y));
+        df = ptx::fma2(ptx::mul2(v, pair(q, q)), e, phi);
     } else {
         const float2 e = exp_neg(v), s = rcp2(ptx::add2(e, pair(1.f, 1.f))), c = ptx::mul2(e, s);
         f = ACT == kActSilu ? ptx::mul2(v, s) : s;
@@ -142,6 +162,45 @@ inline FastDiv fast_div(uint32_t d) {
 __device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv& f) {
     return f.mul ? __umulhi(n, f.mul) >> f.shift : n;
 }
+
+// Where a group of lanes is: row r = b T + t, and its place in K tensors. A grid of groups steps `by` rows at a
+// time; inside a sequence the addresses grow by inc = by st bytes.
+template <int K>
+struct Tensors {
+    char* base[K];
+    long long sb[K], sh[K], st[K], inc[K];  // bytes
+    FastDiv tokens;
+    uint32_t by;
+};
+template <int K>
+struct Walk {
+    uint32_t r, t;
+    char* at[K];
+    // row r of head h, byte `c` of it
+    __device__ __forceinline__ void start(const Tensors<K>& s, uint32_t row, uint32_t h, int c) {
+        const uint32_t b = div(row, s.tokens);
+        r = row;
+        t = row - b * s.tokens.d;
+#pragma unroll
+        for (int k = 0; k < K; ++k) at[k] = s.base[k] + (b * s.sb[k] + h * s.sh[k] + t * s.st[k] + c);
+    }
+    __device__ __forceinline__ void step(const Tensors<K>& s, uint32_t h, int c) {
+        if (t + s.by < s.tokens.d) {
+            r += s.by;
+            t += s.by;
+#pragma unroll
+            for (int k = 0; k < K; ++k) at[k] += s.inc[k];
+        } else {
+            start(s, r + s.by, h, c);
+        }
+    }
+    template <typename P>
+    __device__ __forceinline__ P get(int k, int off) const {
+        return *reinterpret_cast<const P*>(at[k] + off);
+    }
+};
+
+constexpr int kSms = 152;
 
 }  // namespace gn
 }  // namespace falcon
