@@ -237,12 +237,14 @@ size_t falcon_bwd_workspace_bytes(int variant, const falcon_dims_t* dims, int ch
  * may be 0 (one row read for many places: a gradient is then that of every place, not their sum).
  * A written tensor has every element at an address of its own. Written tensors may interleave with
  * other arguments in one buffer (column blocks); two that could share an element are
- * FALCON_ERR_INVALID_ARG. Pointers are aligned to their element; where pointers, strides and d are also
- * multiples of 16 bytes (8 for bf16 in the recurrence) the kernels move vectors, else single elements.
+ * FALCON_ERR_INVALID_ARG. Pointers are aligned to their element; calls are fastest where pointers, strides
+ * and d are multiples of 16 bytes, then of 8 (the recurrence also of 4), else elements move one by one.
  * lengths: NULL, or device int32 [B]: sequence b has min(max(lengths[b], 0), T) tokens. Rows behind them
  * are not read (they may hold anything) and are written as zeros.
  * The calls use the current device, keep no scratch of their own and may run at the same time on any
  * streams. Sums run in a fixed order: the same call gives the same bits.
+ * FALCON_ERR_UNSUPPORTED beyond the sizes below and from B*H*ceil(d/64) = 2^30 (recurrence), B*H*T = 2^31 rows
+ * (norm) or 65536 heads (norm's backward) on.
  */
 typedef struct {
     int64_t batch;   /* B >= 0                                                        */

@@ -486,6 +486,165 @@ def test_falcon_read_through_the_norm_and_back():
         assert abs(a - want[k]).max() <= 2e-4 * abs(want[k]).max(), k
 
 
+def test_out_beside_its_inputs_in_one_buffer():
+    """x, g and out as column blocks of one buffer, and one tensor as both inputs."""
+    shape = (2, 3, 700, 64)
+    x, g, h0 = glr_inputs("mix", shape, torch.bfloat16, 90)
+    xd, gd, od = place("blocks", x, g, torch.full(shape, math.nan).to(torch.bfloat16))
+    out, h = F.glr_forward("mix", xd, gd, h0.cuda(), out=od)
+    (ro, rh), (eo, eh) = R.glr_forward("mix", x, g, h0)
+    _close("out", out, ro, eo)
+    _close("h_final", h, rh, eh)
+    assert torch.equal(xd.cpu(), x) and torch.equal(gd.cpu(), g)  # the neighbours are as they were
+    out, _ = F.glr_forward("mix", gd, gd, h0.cuda())
+    _close("out", out, *[v[0] for v in R.glr_forward("mix", g, g, h0)])
+    y = F.groupnorm_forward(xd, None, None, gd, act="silu", y=od)
+    _close("y", y, *R.gn_forward(x, None, None, g, "silu"))
+    assert torch.equal(xd.cpu(), x) and torch.equal(gd.cpu(), g)
+
+
+def test_writes_stay_inside():
+    """Outputs inside a larger buffer: every byte around them is as it was (cut channel tiles and last tiles)."""
+    for shape in ((2, 1, 131, 40), (1, 2, 1, 72), (3, 1, 1300, 8)):
+        B, H, T, d = shape
+        x, g, h0 = glr_inputs("sigmoid", shape, torch.bfloat16, 91)
+        w = Draw(92)(H, d).cuda()
+        buf = torch.full((B, T + 3, H, d + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+        view = buf[:, 1:T + 1, :, 8:8 + d].transpose(1, 2)
+        xd, gd = x.cuda(), g.cuda()
+        n = torch.tensor([T, 0, T // 2][:B], dtype=torch.int32, device="cuda")
+        for write in (lambda: F.glr_forward("sigmoid", xd, gd, h0.cuda(), lengths=n, out=view),
+                      lambda: F.groupnorm_forward(xd, w, None, gd, act="gelu", lengths=n, y=view),
+                      lambda: F.glr_backward("sigmoid", xd, gd, xd, gd, lengths=n, dx=view),
+                      lambda: F.groupnorm_backward(xd, gd, w, None, gd, act="gelu", lengths=n, dz=view)):
+            buf.fill_(7.0)
+            write()
+            view.fill_(7.0)
+            assert bool((buf == 7.0).all()), shape
+
+
+def test_states_and_parameters_at_single_element_alignment():
+    shape = (2, 3, 260, 64)
+    x, g, h0 = glr_inputs("mix", shape, torch.bfloat16, 93)
+
+    def off(t):
+        return torch.empty(t.numel() + 1, device="cuda")[1:].view(t.shape).copy_(t)
+
+    for T in (1, 260):
+        xs, gs = x[:, :, :T].contiguous(), g[:, :, :T].contiguous()
+        s = off(h0)
+        out, h = F.glr_forward("mix", xs.cuda(), gs.cuda(), s, h_final=s)
+        (ro, rh), (eo, eh) = R.glr_forward("mix", xs, gs, h0)
+        _close("out", out, ro, eo)
+        _close("h_final", h, rh, eh)
+        got = F.glr_backward("mix", xs.cuda(), gs.cuda(), out, gs.cuda(), off(h0), dh0=off(h0))
+        ref, e = R.glr_backward("mix", xs, gs, out.cpu(), gs, h0)
+        for k, r, b in zip(("dx", "dg", "dh0"), ref, e):
+            _close(k, got[k], r, b)
+    w, b = Draw(94)(3, 64), Draw(95)(3, 64)
+    _close("y", F.groupnorm_forward(x.cuda(), off(w), off(b)), *R.gn_forward(x, w, b))
+    got = F.groupnorm_backward(x.cuda(), g.cuda(), off(w), off(b), dweight=off(w), dbias=off(b))
+    ref, e = R.gn_backward(x, g, w, b)
+    for k in ref:
+        _close(k, got[k], ref[k], e[k])
+
+
+def test_broadcast_norm_gate():
+    """One gate row for all heads (stride 0): dz is that of every place."""
+    shape = (2, 4, 33, 64)
+    x, _, w, b, dy = gn_inputs(shape, torch.bfloat16, 96, False)
+    z = Draw(97)(2, 1, 33, 64).to(torch.bfloat16)
+    zd = z.cuda().expand(shape)
+    y = F.groupnorm_forward(x.cuda(), w.cuda(), b.cuda(), zd, act="sigmoid")
+    _close("y", y, *R.gn_forward(x, w, b, z.expand(shape), "sigmoid"))
+    got = F.groupnorm_backward(x.cuda(), dy.cuda(), w.cuda(), b.cuda(), zd, act="sigmoid")
+    ref, e = R.gn_backward(x, dy, w, b, z.expand(shape), "sigmoid")
+    for k in ref:
+        _close(k, got[k], ref[k], e[k])
+
+
+@pytest.mark.parametrize("B,H,T", [(40, 6, 20), (300, 4, 50), (2, 2, 9), (64, 12, 16), (1, 1, 64)])
+@pytest.mark.parametrize("gate", GATES)
+def test_glr_short_sequences(gate, B, H, T):
+    """Lengths around which the kernel changes, many sequences and few."""
+    shape = (B, H, T, 64)
+    x, g, h0 = glr_inputs(gate, shape, torch.bfloat16, 98)
+    n = torch.tensor([(T * (i % 7)) // 6 for i in range(B)], dtype=torch.int32)
+    out, h = run_fwd(gate, x, g, h0, n)
+    (ro, rh), (eo, eh) = R.glr_forward(gate, x, g, h0, n)
+    _close("out", out, ro, eo)
+    _close("h_final", h, rh, eh)
+    dout = Draw(99)(*shape).to(torch.bfloat16)
+    dx, dg = poison("bthd", 2, shape, torch.bfloat16)
+    got = F.glr_backward(gate, x.cuda(), g.cuda(), out, dout.cuda(), h0.cuda(), h0.cuda(), lengths=n.cuda(), dx=dx, dg=dg)
+    ref, e = R.glr_backward(gate, x, g, out.cpu(), dout, h0, h0, n)
+    for k, r, b in zip(("dx", "dg", "dh0"), ref, e):
+        _close(k, got[k], r, b)
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """Nothing that a first call sets up breaks a capture."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from weight_linear_attention_gb300 import falcon as F
+x = torch.randn(2, 3, 1500, 64, device="cuda").bfloat16()
+z, h0 = torch.randn_like(x), torch.zeros(2, 3, 64, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out, h = F.glr_forward("sigmoid", x, z, h0)
+    y = F.groupnorm_forward(out, None, None, z, act="silu")
+    d = F.groupnorm_backward(out, z, None, None, z, act="silu")
+    e = F.glr_backward("sigmoid", x, z, out, d["dx"], h0)
+graph.replay()
+torch.cuda.synchronize()
+want, _ = F.glr_forward("sigmoid", x, z, h0)
+assert torch.equal(out, want) and torch.equal(y, F.groupnorm_forward(out, None, None, z, act="silu"))
+assert torch.equal(e["dg"], F.glr_backward("sigmoid", x, z, out, d["dx"], h0)["dg"])
+assert F.falcon_device_status() == F.FALCON_OK
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_host_threads():
+    """Calls of two threads on streams of their own give what one thread's do."""
+    import threading
+
+    shape = (2, 3, 1200, 64)
+    ins = [glr_inputs("mix", shape, torch.bfloat16, 100 + i) for i in range(2)]
+    dev = [[t.cuda() for t in v] for v in ins]
+    want = [F.glr_forward("mix", *v)[0] for v in dev]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    out, _ = F.glr_forward("mix", *dev[i])
+                    F.groupnorm_forward(out, act="silu")
+            s.synchronize()
+            got[i] = out
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert F.falcon_device_status() == F.FALCON_OK
+
+
 def test_wrappers_refuse():
     x = torch.zeros(2, 2, 3, 8, device="cuda")
     for bad in (x[:, :, :, ::2], x.double(), x.cpu(), x[:, :1], x.transpose(2, 3)):

@@ -85,6 +85,15 @@ def test_choices():
     assert gn(dims=_dims(d=1025)) == UNS and gn_b(dims=_dims(d=1025)) == UNS
 
 
+def test_sizes_without_a_kernel():
+    far = dict(x=A, g=A + (1 << 50), out=A + (2 << 50))
+    assert glr(dims=_dims(b=1 << 30, h=4, t=16, d=64), **far) == UNS           # more channel tiles than a grid takes
+    assert glr(dims=_dims(b=1 << 30, h=1 << 20, t=1, d=64), x=A, g=A + (1 << 60), out=A + (2 << 60)) == UNS
+    assert gn(dims=_dims(b=1 << 20, h=1 << 10, t=1 << 10), z=None, y=A + (1 << 50)) == UNS  # 2^40 rows
+    assert gn_b(dims=_dims(h=70000), z=None, dz=None, dy=A + (1 << 40), dx=A + (2 << 40), dweight=None,
+                dbias=None) == UNS
+
+
 def test_missing_tensors():
     for k in ("x", "g", "out"):
         assert glr(**{k: None}) == INV, k

@@ -375,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
     const int row0 = (rank * kWarps + warp) * G::kRows;  // of the warp, in the cluster's tile
     set_up(mv, sm);
     if (cs > 1) cluster_arrive();
+    ptx::pdl_wait();  // what the grids before this one wrote may be read from here on
+    ptx::pdl_launch_dependents();
     Cursor pre = {};
     pre.item = blockIdx.x / cs;
     enter<G::kChans>(p, pre);
@@ -526,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
     const int row0 = (rank * kWarps + warp) * G::kRows;
     set_up(mv, sm);
     if (cs > 1) cluster_arrive();
+    ptx::pdl_wait();  // what the grids before this one wrote may be read from here on
+    ptx::pdl_launch_dependents();
     Cursor pre = {};
     pre.item = blockIdx.x / cs;
     enter<G::kChans>(p, pre);
@@ -785,6 +789,8 @@ __global__ void __launch_bounds__(kWalkThreads) glr_walk_kernel(const __grid_con
 
 template <typename E, int GATE, int VW, int U>
 __global__ void __launch_bounds__(kWalkThreads) glr_walk_bwd_kernel(const __grid_constant__ Params p, long long lanes) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const long long i = (long long)blockIdx.x * kWalkThreads + threadIdx.x;
     if (i >= lanes) return;
     const Lane l = lane_of<VW>(p, i);
@@ -893,14 +899,17 @@ struct KernelInfo {
     std::atomic<int> clusters[kMaxDevices][17];
 };
 
-void describe(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int cs, int bytes) {
+// With programmatic stream serialisation: a call's launch and set-up overlap the end of the one before it.
+void describe(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&at)[2], int cs, int bytes) {
     cfg->blockDim = dim3(kThreads);
     cfg->dynamicSmemBytes = bytes;
-    at->id = cudaLaunchAttributeClusterDimension;
-    at->val.clusterDim.x = cs;
-    at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cs;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg->attrs = at;
-    cfg->numAttrs = 1;
+    cfg->numAttrs = 2;
 }
 
 // Clusters of cs CTAs that run at once on device `dev`, two CTAs an SM; 0 on an error.
@@ -916,7 +925,7 @@ int resident(Fn fn, KernelInfo& info, int dev, int cs, int bytes) {
     int n = info.clusters[dev][cs].load(std::memory_order_relaxed);
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute at[1];
+        cudaLaunchAttribute at[2];
         cfg.gridDim = dim3(cs);
         describe(&cfg, at, cs, bytes);
         if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return 0;
@@ -932,11 +941,13 @@ struct Plan {
 };
 
 // The cluster size for a tile shape. A sequence's tiles are dealt to the cs CTAs of its cluster; every round of
-// cluster-wide tiles lasts as long as a tile on the fullest SM: measured (bf16 forward, tiles of 8192 elements)
-// 1.0 us where each SM holds one CTA, 1.75 us (narrow tiles 1.9 us) where one holds two, and 0.38 us more for the
-// exchange in a cluster. The costs are those, in eighths of a microsecond.
-template <int LC, typename Fn>
+// cluster-wide tiles lasts as long as a tile on the fullest SM: measured (bf16, 8192 elements forward, 4096
+// backward) 1.0 to 1.15 us where each SM holds one CTA, 1.75 us (narrow tiles 1.9 to 2 us) where one holds two, and
+// 0.38 us more for the exchange in a cluster; fp32 tiles, of half the elements, are a little quicker. The costs are
+// those, in eighths of a microsecond.
+template <int LC, bool F32, typename Fn>
 Plan plan_for(Fn fn, KernelInfo& info, int dev, int bytes, long long items, int T, int rows) {
+    constexpr int kAlone = F32 ? 7 : 9, kShared = F32 ? 13 : LC < 32 ? 16 : 14, kExchange = 3;
     Plan best;
     const long long tiles = ((long long)T + rows - 1) / rows;
     for (int cs = 1; cs <= kMaxCluster<LC> && cs <= tiles; ++cs) {
@@ -944,7 +955,7 @@ Plan plan_for(Fn fn, KernelInfo& info, int dev, int bytes, long long items, int 
         if (most == 0) continue;
         const long long clusters = items < most ? items : most;
         const long long rounds = (items + clusters - 1) / clusters * ((tiles + cs - 1) / cs);
-        const long long cost = rounds * ((clusters * cs <= kSms ? 8 : LC < 32 ? 15 : 14) + (cs > 1 ? 3 : 0));
+        const long long cost = rounds * ((clusters * cs <= kSms ? kAlone : kShared) + (cs > 1 ? kExchange : 0));
         if (best.cs == 0 || cost < best.cost) {
             best.cs = cs;
             best.clusters = clusters;
@@ -985,7 +996,7 @@ struct Kernel {
         int tiles;
         long long items;
         if (!items_of<LC>(c, &tiles, &items)) return Plan{};
-        return plan_for<LC>(fn(), info(), dev, kBytes, items, c.p.T, Q::G::kTile);
+        return plan_for<LC, sizeof(E) == 4>(fn(), info(), dev, kBytes, items, c.p.T, Q::G::kTile);
     }
     // 0, a status, or -1: TMA does not take these tensors
     static int launch(const Call& c, const Plan& plan, cudaStream_t s) {
@@ -997,7 +1008,7 @@ struct Kernel {
             for (int i = 0; i < 6; ++i)
                 if (c.used[i] && !encode_view(&p.tm[i], c.view[i], p, c.B, c.es, 2 * LC, Q::kBoxRows)) return -1;
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute at[1];
+        cudaLaunchAttribute at[2];
         describe(&cfg, at, plan.cs, kBytes);
         cfg.gridDim = dim3((unsigned)(plan.clusters * plan.cs));
         cfg.stream = s;
@@ -1010,22 +1021,19 @@ template <typename E, int GATE, int VW, int U, bool BWD>
 int launch_walk_rows(const Call& c, cudaStream_t s) {
     const long long lanes = c.B * c.p.H * (c.p.d / VW), blocks = (lanes + kWalkThreads - 1) / kWalkThreads;
     if (blocks > kMaxGrid) return 2;
-    if constexpr (BWD) {
-        glr_walk_bwd_kernel<E, GATE, VW, U><<<(unsigned)blocks, kWalkThreads, 0, s>>>(c.p, lanes);
-        return cudaGetLastError() == cudaSuccess ? 0 : 4;
-    } else {
-        // programmatic stream serialisation: consecutive steps overlap one's launch with the other's tail
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(kWalkThreads);
-        cfg.stream = s;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, glr_walk_kernel<E, GATE, VW, U>, c.p, lanes) == cudaSuccess ? 0 : 4;
-    }
+    void (*fn)(Params, long long);
+    if constexpr (BWD) fn = glr_walk_bwd_kernel<E, GATE, VW, U>;
+    else fn = glr_walk_kernel<E, GATE, VW, U>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kWalkThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, c.p, lanes) == cudaSuccess ? 0 : 4;
 }
 
 template <typename E, int GATE, int VW, bool BWD>

@@ -61,6 +61,8 @@ constexpr int kPerSm = NCH * VW <= 4 ? 4 : NCH * VW <= 8 ? 3 : NCH * VW <= 24 ? 
 
 template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const __grid_constant__ FwdParams p) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P, G = kThreads / LPR;
     constexpr bool kAhead = NCH * VW <= 16;  // the registers take the next row too
@@ -140,11 +142,10 @@ int launch(FwdParams p, cudaStream_t s) {
     p.s.by = (uint32_t)((unsigned long long)grid * G / p.H);
     for (int k = 0; k < 3; ++k) p.s.inc[k] = p.s.by * p.s.st[k];
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
-    if (gated && full) gn_fwd_kernel<E, VW, LPR, NCH, true, true><<<grid, kThreads, 0, s>>>(p);
-    else if (gated) gn_fwd_kernel<E, VW, LPR, NCH, true, false><<<grid, kThreads, 0, s>>>(p);
-    else if (full) gn_fwd_kernel<E, VW, LPR, NCH, false, true><<<grid, kThreads, 0, s>>>(p);
-    else gn_fwd_kernel<E, VW, LPR, NCH, false, false><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : 4;
+    if (gated && full) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, true>, dim3(grid), kThreads, s, p);
+    if (gated) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, false>, dim3(grid), kThreads, s, p);
+    if (full) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, true>, dim3(grid), kThreads, s, p);
+    return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, false>, dim3(grid), kThreads, s, p);
 }
 
 template <typename E, int VW>

@@ -5,6 +5,7 @@
 
 #include "falcon_seq.cuh"
 #include "falcon_seq.h"
+#include "sm103_ptx.cuh"
 
 namespace falcon {
 namespace gn {
@@ -201,6 +202,22 @@ struct Walk {
 };
 
 constexpr int kSms = 152;
+
+// Launches with programmatic stream serialisation: the kernel's launch overlaps the end of the one before it, so
+// it waits (pdl_wait) before it reads or writes.
+template <typename... Args>
+inline int launch_ahead(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? 0 : 4;
+}
 
 }  // namespace gn
 }  // namespace falcon

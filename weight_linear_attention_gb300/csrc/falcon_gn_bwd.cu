@@ -57,6 +57,8 @@ __device__ __forceinline__ void slope_all(int a, const float2 (&v)[P], float2 (&
 
 template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 2 : 1) gn_bwd_kernel(const __grid_constant__ BwdParams p) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P;
     constexpr int G = kThreads / LPR;  // rows side by side
@@ -159,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 
                 *reinterpret_cast<V*>(to_x + k * CB) = po;
             }
     }
-    ptx::pdl_launch_dependents();
     if (!p.ws) return;
     // the warp's groups, then the CTA's warps; first dw, then db
     float* to = p.ws + (long long)blockIdx.x * 2 * p.H * p.d + (long long)h * p.d;
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
     gn_sum_kernel(const float* __restrict__ ws, int splits, long long n, float* __restrict__ dw,
                   float* __restrict__ db) {
     __shared__ float part[kSumSlices][kSumChannels];
-    ptx::pdl_wait();  // launched while the CTAs before it still run
+    ptx::pdl_wait();  // launched while the CTAs whose sums it adds still run
+    ptx::pdl_launch_dependents();
     const int lane = threadIdx.x % kSumChannels, slice = threadIdx.x / kSumChannels;
     const long long c = (long long)blockIdx.x * kSumChannels + lane;
     float v = 0.f;
@@ -217,11 +219,10 @@ int launch(BwdParams p, int splits, cudaStream_t s) {
     for (int k = 0; k < 5; ++k) p.s.inc[k] = p.s.by * p.s.st[k];
     const dim3 grid((unsigned)splits, (unsigned)p.H);
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
-    if (gated && full) gn_bwd_kernel<E, VW, LPR, NCH, true, true><<<grid, kThreads, 0, s>>>(p);
-    else if (gated) gn_bwd_kernel<E, VW, LPR, NCH, true, false><<<grid, kThreads, 0, s>>>(p);
-    else if (full) gn_bwd_kernel<E, VW, LPR, NCH, false, true><<<grid, kThreads, 0, s>>>(p);
-    else gn_bwd_kernel<E, VW, LPR, NCH, false, false><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : 4;
+    if (gated && full) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, true, true>, grid, kThreads, s, p);
+    if (gated) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, true, false>, grid, kThreads, s, p);
+    if (full) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, true>, grid, kThreads, s, p);
+    return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, false>, grid, kThreads, s, p);
 }
 
 template <typename E, int VW>
@@ -289,17 +290,8 @@ int launch_gn_bwd(const GnArgs& a, cudaStream_t s) {
         st = vw == 4 ? by_width<float, 4>(p, splits, s) : by_width<float, 1>(p, splits, s);
     if (st != 0 || !a.ws) return st;
     const long long n = a.n.H * a.n.d;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((2 * n + kSumChannels - 1) / kSumChannels));
-    cfg.blockDim = dim3(kSumChannels * kSumSlices);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gn_sum_kernel, (const float*)a.ws, splits, n, a.dw, a.db);
-    return e == cudaSuccess ? 0 : 4;
+    return launch_ahead(gn_sum_kernel, dim3((unsigned)((2 * n + kSumChannels - 1) / kSumChannels)),
+                        kSumChannels * kSumSlices, s, (const float*)a.ws, splits, n, a.dw, a.db);
 }
 
 }  // namespace falcon

@@ -351,7 +351,80 @@ def falcon_gn_bwd_workspace_bytes(dims: FalconSeqDims) -> int:
     return int(load().falcon_gn_bwd_workspace_bytes(ctypes.byref(dims)))
 
 
-_DIMS, _STRIDES = struct.Struct("=4q2i"), {n: struct.Struct(f"={3 * n}q") for n in (3, 5, 6)}
+_PACK_DIMS = struct.Struct("=4q2i").pack
+_PACK_STRIDES = {n: struct.Struct(f"={3 * n}q").pack for n in (3, 5, 6)}
+
+
+@functools.lru_cache(maxsize=None)
+def _t():
+    """torch, the types' codes, and how to ask for the current stream and device; looked up once."""
+    import torch
+
+    return (torch, {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32}, torch._C._cuda_getCurrentRawStream,
+            torch.cuda.current_device)
+
+
+def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
+    """Checks the tensors of one call and marshals them. `views` (tensors or None) are [B,H,T,d] like x in x's type,
+    `arrays` (tensors or None) contiguous fp32 of `shape`; `names` has the views' names, then the arrays'. Returns
+    the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides, and the function that calls
+    the library's `what` on x's device and stream."""
+    torch, codes, raw_stream, current_device = _t()
+    full, dtype, index = x.shape, x.dtype, x.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    code = codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    if choice is None:
+        raise ValueError(f"{what}: no such gate or activation")
+    pointers, strides = [], []
+    for i, t in enumerate(views):
+        if t is None:
+            pointers.append(None)
+            strides += (0, 0, 0)
+            continue
+        if t.shape != full or t.dtype is not dtype or t.get_device() != index:
+            raise ValueError(f"{names[i]} must be {tuple(full)} {dtype} on {x.device}, got {tuple(t.shape)} {t.dtype} "
+                             f"on {t.device}")
+        sb, sh, st, sd = t.stride()
+        if sd != 1 and full[3] > 1:
+            raise ValueError(f"{names[i]}'s channels must be contiguous (stride 1), got stride {sd}")
+        strides += (sb, sh, st)
+        pointers.append(t.data_ptr())
+    f32 = torch.float32
+    for i, t in enumerate(arrays, len(views)):
+        if t is None:
+            pointers.append(None)
+            continue
+        if t.shape != shape or t.dtype is not f32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{names[i]} must be contiguous {tuple(shape)} {f32} on {x.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+        pointers.append(t.data_ptr())
+    if lengths is None:
+        pointers.append(None)
+    else:
+        if lengths.shape != full[:1] or lengths.dtype is not torch.int32 or lengths.get_device() != index or \
+                not lengths.is_contiguous():
+            raise ValueError(f"lengths must be contiguous ({full[0]},) torch.int32 on {x.device}, got "
+                             f"{tuple(lengths.shape)} {lengths.dtype} on {lengths.device}")
+        pointers.append(lengths.data_ptr())
+    if stream is None:
+        stream = raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or load(), what)
+
+    def call(*args):
+        if index == current_device():
+            status = fn(choice, *args, stream)
+        else:
+            with torch.cuda.device(index):
+                status = fn(choice, *args, stream)
+        if status != FALCON_OK:
+            raise FalconError(status, what)
+
+    return pointers, _PACK_DIMS(*full, code, 0), _PACK_STRIDES[len(views)](*strides), call
 
 
 def _sizes(x):
@@ -360,77 +433,9 @@ def _sizes(x):
     return x.shape
 
 
-def _seq_call(x, views, arrays, stream):
-    """Checks the tensors of one call and marshals them: `views`, pairs (tensor or None, name), are [B,H,T,d] like x
-    in x's dtype; `arrays`, (tensor or None, name, shape, dtype), are contiguous. Returns their pointers (views,
-    then arrays), the packed falcon_seq_dims_t, the packed strides, x's device index and the stream's handle."""
-    shape, dtype, index = x.shape, x.dtype, x.get_device()
-    if not x.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    code = _dtype_codes().get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
-    pointers, strides = [], []
-    for t, name in views:
-        if t is None:
-            pointers.append(None)
-            strides += (0, 0, 0)
-            continue
-        if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-            raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {x.device}, got {tuple(t.shape)} {t.dtype} on "
-                             f"{t.device}")
-        sb, sh, st, sd = t.stride()
-        if sd != 1 and shape[3] > 1:
-            raise ValueError(f"{name}'s channels must be contiguous (stride 1), got stride {sd}")
-        strides += (sb, sh, st)
-        pointers.append(t.data_ptr())
-    for t, name, want, dt in arrays:
-        if t is None:
-            pointers.append(None)
-            continue
-        if t.shape != want or t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {tuple(want)} {dt} on {x.device}, got {tuple(t.shape)} "
-                             f"{t.dtype} on {t.device}")
-        pointers.append(t.data_ptr())
-    if stream is None:
-        stream = _raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    return pointers, _DIMS.pack(*shape, code, 0), _STRIDES[len(views)].pack(*strides), index, stream
-
-
-@functools.lru_cache(maxsize=None)
-def _dtype_codes():
-    import torch
-
-    return {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32}
-
-
-def _raw_stream(index):
-    """The handle of the device's current stream."""
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _on_device(index, what, *args):
-    """Calls lib.<what>(*args) with device `index` current; raises on a nonzero status."""
-    import torch
-
-    fn = getattr(_lib or load(), what)
-    if index == torch.cuda.current_device():
-        st = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args)
-    if st != FALCON_OK:
-        raise FalconError(st, what)
-
-
-def _choice(table, value, what):
-    if value not in table:
-        raise ValueError(f"{what} must be one of {', '.join(table)}, got {value!r}")
-    return table[value]
+def _empty(x, shape, dtype=None):
+    torch = _t()[0]
+    return torch.empty(shape, dtype=dtype or torch.float32, device=x.device)
 
 
 def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, want_state=True, stream=None):
@@ -441,19 +446,14 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
     `proj.view(B, T, H, d).transpose(1, 2)` and column blocks are passed as they are). h0: fp32 [B,H,d] or
     None (zero). lengths: int32 [B] or None; rows behind them come back as zeros. out (a [B,H,T,d] view) and
     h_final (may be h0: updated in place) are written where given, else allocated dense."""
-    import torch
-
     B, H, T, d = _sizes(x)
     if out is None:
-        out = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+        out = _empty(x, x.shape, x.dtype)
     if h_final is None and want_state:
-        h_final = torch.empty((B, H, d), dtype=torch.float32, device=x.device)
-    f32, state = torch.float32, (B, H, d)
-    p, dims, strides, index, stream = _seq_call(
-        x, ((x, "x"), (g, "g"), (out, "out")),
-        ((h0, "h0", state, f32), (lengths, "lengths", (B,), torch.int32), (h_final, "h_final", state, f32)), stream)
-    _on_device(index, "falcon_glr_fwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[3], p[4], p[2], p[5], dims,
-               strides, stream)
+        h_final = _empty(x, (B, H, d))
+    p, dims, strides, call = _seq_call("falcon_glr_fwd", GLR_GATES.get(gate), x, (x, g, out), (h0, h_final), (B, H, d),
+                                       lengths, ("x", "g", "out", "h0", "h_final"), stream)
+    call(p[0], p[1], p[3], p[5], p[2], p[4], dims, strides)
     return out, h_final
 
 
@@ -461,22 +461,14 @@ def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None,
                  stream=None):
     """Gradients of one glr_forward call, from its inputs, its output `out` and the adjoints of out and
     h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated."""
-    import torch
-
     B, H, T, d = _sizes(x)
-    f32, state = torch.float32, (B, H, d)
-    if dx is None:
-        dx = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
-    if dg is None:
-        dg = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
-    if dh0 is None:
-        dh0 = torch.empty(state, dtype=f32, device=x.device)
-    p, dims, strides, index, stream = _seq_call(
-        x, ((x, "x"), (g, "g"), (out, "out"), (dout, "dout"), (dx, "dx"), (dg, "dg")),
-        ((h0, "h0", state, f32), (lengths, "lengths", (B,), torch.int32), (dh_final, "dh_final", state, f32),
-         (dh0, "dh0", state, f32)), stream)
-    _on_device(index, "falcon_glr_bwd", _choice(GLR_GATES, gate, "gate"), p[0], p[1], p[2], p[6], p[7], p[3], p[8],
-               p[4], p[5], p[9], dims, strides, stream)
+    dx = _empty(x, x.shape, x.dtype) if dx is None else dx
+    dg = _empty(x, x.shape, x.dtype) if dg is None else dg
+    dh0 = _empty(x, (B, H, d)) if dh0 is None else dh0
+    p, dims, strides, call = _seq_call(
+        "falcon_glr_bwd", GLR_GATES.get(gate), x, (x, g, out, dout, dx, dg), (h0, dh_final, dh0), (B, H, d), lengths,
+        ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"), stream)
+    call(p[0], p[1], p[2], p[6], p[9], p[3], p[7], p[4], p[5], p[8], dims, strides)
     return {"dx": dx, "dg": dg, "dh0": dh0}
 
 
@@ -487,17 +479,12 @@ def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5
     x, z: [B,H,T,d] views as for glr_forward; weight, bias: fp32 [H,d] or None; act: "none", "silu", "gelu"
     (erf) or "sigmoid". y is written where given, else allocated in the output projection's layout: a [B,H,T,d]
     view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free."""
-    import torch
-
     B, H, T, d = _sizes(x)
     if y is None:
-        y = torch.empty((B, T, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
-    f32, chans = torch.float32, (H, d)
-    p, dims, strides, index, stream = _seq_call(
-        x, ((x, "x"), (z, "z"), (y, "y")),
-        ((weight, "weight", chans, f32), (bias, "bias", chans, f32), (lengths, "lengths", (B,), torch.int32)), stream)
-    _on_device(index, "falcon_gn_fwd", _choice(GN_ACTS, act, "act"), p[0], p[1], p[3], p[4], p[5], p[2], dims, strides,
-               float(eps), stream)
+        y = _empty(x, (B, T, H, d), x.dtype).transpose(1, 2)
+    p, dims, strides, call = _seq_call("falcon_gn_fwd", GN_ACTS.get(act), x, (x, z, y), (weight, bias), (H, d), lengths,
+                                       ("x", "z", "y", "weight", "bias"), stream)
+    call(p[0], p[1], p[3], p[4], p[5], p[2], dims, strides, eps)
     return y
 
 
@@ -506,30 +493,25 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
     """Gradients of one groupnorm_forward call. Returns a dict dx, dz (None without a gate), dweight, dbias
     (fp32 [H,d]; None unless want_params or given). Each is written where given, else allocated dense; so is the
     workspace, uint8 of falcon_gn_bwd_workspace_bytes, which dweight and dbias need."""
-    import torch
-
     B, H, T, d = _sizes(x)
-    f32, chans = torch.float32, (H, d)
-    if dx is None:
-        dx = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+    dx = _empty(x, x.shape, x.dtype) if dx is None else dx
     if z is not None and dz is None:
-        dz = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+        dz = _empty(x, x.shape, x.dtype)
     if want_params:
-        dweight = torch.empty(chans, dtype=f32, device=x.device) if dweight is None else dweight
-        dbias = torch.empty(chans, dtype=f32, device=x.device) if dbias is None else dbias
-    p, dims, strides, index, stream = _seq_call(
-        x, ((x, "x"), (z, "z"), (dy, "dy"), (dx, "dx"), (dz, "dz")),
-        ((weight, "weight", chans, f32), (bias, "bias", chans, f32), (lengths, "lengths", (B,), torch.int32),
-         (dweight, "dweight", chans, f32), (dbias, "dbias", chans, f32)), stream)
+        dweight = _empty(x, (H, d)) if dweight is None else dweight
+        dbias = _empty(x, (H, d)) if dbias is None else dbias
+    p, dims, strides, call = _seq_call(
+        "falcon_gn_bwd", GN_ACTS.get(act), x, (x, z, dy, dx, dz), (weight, bias, dweight, dbias), (H, d), lengths,
+        ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"), stream)
     size = 0
     if dweight is not None or dbias is not None:
-        size = load().falcon_gn_bwd_workspace_bytes(dims)
-        if workspace is None and size > 0:
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-        if workspace is not None:
-            if workspace.get_device() != index or not workspace.is_contiguous():
+        if workspace is None:
+            size = load().falcon_gn_bwd_workspace_bytes(dims)
+            if size > 0:
+                workspace = _empty(x, size, _t()[0].uint8)
+        else:
+            if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
             size = workspace.numel() * workspace.element_size()
-    _on_device(index, "falcon_gn_bwd", _choice(GN_ACTS, act, "act"), p[0], p[1], p[5], p[6], p[7], p[2], p[3], p[4],
-               p[8], p[9], dims, strides, float(eps), _ptr(workspace), size, stream)
+    call(p[0], p[1], p[5], p[6], p[9], p[2], p[3], p[4], p[7], p[8], dims, strides, eps, _ptr(workspace), size)
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
