@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
         if (GATED) zero(pz[k]);
     }
     auto fetch = [&] {
-        in = at.r < p.rows;
-        if (in && p.lengths) in = (int)at.t < p.lengths[div(at.r, p.s.tokens)];
+        in = at.exists(p.s);
+        if (in && p.lengths) in = (int)at.t < p.lengths[at.b];
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
             if (in && q.live(k)) {
@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
         float2 x[P], z[GATED ? P : 1], f[P];
         q.get(px, x);
         if constexpr (GATED) q.get(pz, z);
-        const bool mine = at.r < p.rows, was_in = in;
+        const bool mine = at.exists(p.s), was_in = in;
         char* const out = at.at[kY];
         if (r + p.s.by < p.rows) {
-            at.step(p.s, h, c0);
+            at.step(p.s);
             if (kAhead) fetch();
         }
         q.normalise(x, p.inv_d, p.eps);
@@ -139,8 +139,7 @@ int launch(FwdParams p, cudaStream_t s) {
     const uint32_t unit = p.H / std::gcd(p.H, (uint32_t)G);
     const uint32_t most = ((uint32_t)groups + G - 1) / G, slots = kSms * kPerSm<VW, NCH>;
     const uint32_t grid = most <= slots ? (most + unit - 1) / unit * unit : std::max(slots / unit, 1u) * unit;
-    p.s.by = (uint32_t)((unsigned long long)grid * G / p.H);
-    for (int k = 0; k < 3; ++k) p.s.inc[k] = p.s.by * p.s.st[k];
+    set_step(p.s, (uint32_t)((unsigned long long)grid * G / p.H));
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
     if (gated && full) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, true>, dim3(grid), kThreads, s, p);
     if (gated) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, false>, dim3(grid), kThreads, s, p);
@@ -187,9 +186,11 @@ int launch_gn_fwd(const GnArgs& a, cudaStream_t s) {
     p.d = a.n.d, p.act = a.act, p.H = (uint32_t)a.n.H;
     p.rows = (uint32_t)(a.n.B * a.n.T);
     p.s.tokens = fast_div((uint32_t)a.n.T);
+    p.s.B = (uint32_t)a.n.B;
     p.inv_d = 1.f / a.n.d, p.eps = a.eps;
     if (a.n.T == 1 && !p.lengths) {  // single tokens: the batch takes the tokens' place
         p.s.tokens = fast_div(p.rows);
+        p.s.B = 1;
         for (int k = 0; k < 3; ++k) p.s.st[k] = p.s.sb[k];
     }
     if (reinterpret_cast<uintptr_t>(a.w) % 16 || reinterpret_cast<uintptr_t>(a.b) % 16) vw = 1;

@@ -164,37 +164,49 @@ __device__ __forceinline__ uint32_t div(uint32_t n, const FastDiv& f) {
     return f.mul ? __umulhi(n, f.mul) >> f.shift : n;
 }
 
-// Where a group of lanes is: row r = b T + t, and its place in K tensors. A grid of groups steps `by` rows at a
-// time; inside a sequence the addresses grow by inc = by st bytes.
+// Where a group of lanes is: token t of sequence b, and its place in K tensors. A grid of groups steps `by` rows
+// (of B T) at a time: qb sequences and qt tokens, inc = qb sb + qt st bytes, and where that leaves the sequence
+// one sequence more, wrap = sb - T st bytes.
 template <int K>
 struct Tensors {
     char* base[K];
-    long long sb[K], sh[K], st[K], inc[K];  // bytes
-    FastDiv tokens;
-    uint32_t by;
+    long long sb[K], sh[K], st[K], inc[K], wrap[K];  // bytes
+    FastDiv tokens;                                  // T
+    uint32_t B, by, qb, qt;
 };
 template <int K>
+inline void set_step(Tensors<K>& s, uint32_t by) {
+    const uint32_t T = s.tokens.d;
+    s.by = by, s.qb = by / T, s.qt = by % T;
+    for (int k = 0; k < K; ++k) {
+        s.inc[k] = (long long)s.qb * s.sb[k] + (long long)s.qt * s.st[k];
+        s.wrap[k] = s.sb[k] - (long long)T * s.st[k];
+    }
+}
+template <int K>
 struct Walk {
-    uint32_t r, t;
+    uint32_t b, t;
     char* at[K];
     // row r of head h, byte `c` of it
-    __device__ __forceinline__ void start(const Tensors<K>& s, uint32_t row, uint32_t h, int c) {
-        const uint32_t b = div(row, s.tokens);
-        r = row;
-        t = row - b * s.tokens.d;
+    __device__ __forceinline__ void start(const Tensors<K>& s, uint32_t r, uint32_t h, int c) {
+        b = div(r, s.tokens);
+        t = r - b * s.tokens.d;
 #pragma unroll
         for (int k = 0; k < K; ++k) at[k] = s.base[k] + (b * s.sb[k] + h * s.sh[k] + t * s.st[k] + c);
     }
-    __device__ __forceinline__ void step(const Tensors<K>& s, uint32_t h, int c) {
-        if (t + s.by < s.tokens.d) {
-            r += s.by;
-            t += s.by;
+    __device__ __forceinline__ void step(const Tensors<K>& s) {
+        b += s.qb;
+        t += s.qt;
 #pragma unroll
-            for (int k = 0; k < K; ++k) at[k] += s.inc[k];
-        } else {
-            start(s, r + s.by, h, c);
+        for (int k = 0; k < K; ++k) at[k] += s.inc[k];
+        if (t >= s.tokens.d) {
+            ++b;
+            t -= s.tokens.d;
+#pragma unroll
+            for (int k = 0; k < K; ++k) at[k] += s.wrap[k];
         }
     }
+    __device__ __forceinline__ bool exists(const Tensors<K>& s) const { return b < s.B; }
     template <typename P>
     __device__ __forceinline__ P get(int k, int off) const {
         return *reinterpret_cast<const P*>(at[k] + off);

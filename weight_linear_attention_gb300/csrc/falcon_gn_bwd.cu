@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 
         if (GATED) zero(pz[k]);
     }
     auto fetch = [&] {
-        in = at.r < p.rows;
-        if (in && p.lengths) in = (int)at.t < p.lengths[div(at.r, p.s.tokens)];
+        in = at.exists(p.s);
+        if (in && p.lengths) in = (int)at.t < p.lengths[at.b];
 #pragma unroll
         for (int k = 0; k < NCH; ++k) {
             if (in && q.live(k)) {
@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 
         q.get(px, x);
         q.get(pd, dn);
         if constexpr (GATED) q.get(pz, z);
-        const bool mine = at.r < p.rows, was_in = in;
+        const bool mine = at.exists(p.s), was_in = in;
         char *const to_x = at.at[kDx], *const to_z = at.at[kDz];
         if (r + p.s.by < p.rows) {
-            at.step(p.s, h, c0);
+            at.step(p.s);
             if (kAhead) fetch();
         }
         const float rstd = q.normalise(x, p.inv_d, p.eps);
@@ -215,8 +215,7 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
 
 template <typename E, int VW, int LPR, int NCH>
 int launch(BwdParams p, int splits, cudaStream_t s) {
-    p.s.by = (uint32_t)splits * (kThreads / LPR);
-    for (int k = 0; k < 5; ++k) p.s.inc[k] = p.s.by * p.s.st[k];
+    set_step(p.s, (uint32_t)splits * (kThreads / LPR));
     const dim3 grid((unsigned)splits, (unsigned)p.H);
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
     if (gated && full) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, true, true>, grid, kThreads, s, p);
@@ -274,10 +273,12 @@ int launch_gn_bwd(const GnArgs& a, cudaStream_t s) {
     }
     p.rows = (uint32_t)(a.n.B * a.n.T);
     p.s.tokens = fast_div((uint32_t)a.n.T);
+    p.s.B = (uint32_t)a.n.B;
     p.d = a.n.d, p.H = (int)a.n.H, p.act = a.act;
     p.inv_d = 1.f / a.n.d, p.eps = a.eps;
     if (a.n.T == 1 && !p.lengths) {  // single tokens: the batch takes the tokens' place
         p.s.tokens = fast_div(p.rows);
+        p.s.B = 1;
         for (int k = 0; k < 5; ++k) p.s.st[k] = p.s.sb[k];
     }
     const int splits = gn_bwd_splits(a.n);
