@@ -318,7 +318,8 @@ int falcon_gn_fwd(int act, const void* x, const void* z, const float* weight, co
  *   dweight, dbias  fp32 [H,d] or NULL: written, not added to
  *   strides   of x, z, dy, dx, dz (15 values) or NULL
  *   workspace at least falcon_gn_bwd_workspace_bytes(dims) bytes, 256-byte aligned; may be NULL when
- *             dweight and dbias are
+ *             dweight and dbias are. Contents ignored on entry, unspecified on return; calls that may run at
+ *             the same time must not share one
  */
 int falcon_gn_bwd(int act, const void* x, const void* z, const float* weight, const float* bias,
                   const int32_t* lengths, const void* dy, void* dx, void* dz, float* dweight, float* dbias,

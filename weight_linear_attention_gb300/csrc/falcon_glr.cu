@@ -7,19 +7,23 @@
 // scan's direction: position n is token n forward and token len - 1 - n backward.
 //
 // One pass over the data. A CTA works through tiles of kTile positions x 2 LC channels; a thread owns two
-// channels of R consecutive positions. Tiles lie in a ring in shared memory, filled ahead and emptied by TMA (where addresses do not allow that, each warp copies its rows by cp.async, or
-// through registers, and stores them itself). A warp evaluates the gates of its rows once into registers and
-// reduces its tokens to their map; maps are composed over the warp (shuffles), the CTA
-// (shared memory) and, for long sequences, the CTAs of a cluster that lie side by side along the tokens:
-// each CTA sends its tile's map into its peers' shared memory (st.async, counted by an mbarrier there: no
-// fence that would wait for the outputs on their way to memory), and every CTA composes them all in the
-// same order, so that the state that enters the next cluster-wide tile is known everywhere without another
-// exchange. Then each thread replays its tokens from its entering state into the ring, whence a TMA store
-// takes them. No scratch in global memory, no atomics on data; the order of every sum is fixed by the
-// sizes. Waits are bounded: one that runs out raises a flag (falcon_device_status) and is not repeated.
+// channels of R consecutive positions. Tiles lie in a ring in shared memory, filled ahead and emptied by TMA
+// (where addresses do not allow that, each warp copies its rows by cp.async, or through registers, and stores
+// them itself). A warp evaluates the gates of its rows once into registers and reduces its tokens to their map;
+// maps are composed over the warp (shuffles), the CTA (shared memory) and, for long sequences, the CTAs of a
+// cluster that lie side by side along the tokens: each CTA sends its tile's map into its peers' shared memory
+// (st.async, counted by an mbarrier there: no fence that would wait for the outputs on their way to memory), and
+// every CTA composes them all in the same order, so that the state that enters the next cluster-wide tile is
+// known everywhere without another exchange. Then each thread replays its tokens from its entering state into
+// the ring, whence a TMA store takes them. No scratch in global memory, no atomics on data; the order of every
+// sum is fixed by the sizes. Waits are bounded: one that runs out raises a flag (falcon_device_status) and is
+// not repeated.
 //
-// What bounds it: 3 tensors' bytes per element forward, 5 or 6 backward; the thread instructions per
-// element, of which an SM has about 33 (bf16, forward) at the memory rate.
+// What bounds it: 3 tensors' bytes per element forward, 5 or 6 backward, where there are tiles enough to hide
+// the rest ([16,16,4096,64] bf16: 65 us forward, 91 % of the copy rate; 20 to 26 thread instructions per
+// element, of which an SM has 33 at that rate). One long sequence ([1,12,131072,64] decay: 119 us, 75 %) is bound
+// by the exchange (95 us without it), a training batch ([8,12,1024,64] mix: 12.5 us, 45 %) by filling and emptying
+// three tiles per CTA (the same boxes without arithmetic: 8.5 us).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -100,9 +104,9 @@ __device__ __forceinline__ Map shfl(const Map& m, int from) {
 }
 // first `before`, then `m`
 __device__ __forceinline__ Map compose(const Map& before, const Map& m) {
-    return Map{ptx::mul2(m.A, before.A), ptx::fma2(m.A, before.H, m.H)};
+    return Map{mul2(m.A, before.A), fma2(m.A, before.H, m.H)};
 }
-__device__ __forceinline__ float2 apply(const Map& m, float2 h) { return ptx::fma2(m.A, h, m.H); }
+__device__ __forceinline__ float2 apply(const Map& m, float2 h) { return fma2(m.A, h, m.H); }
 
 template <int LC>
 struct __align__(16) Maps {
@@ -161,15 +165,16 @@ __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, bool fresh, in
     __syncthreads();
     behind_barrier();
     Map before = {pair(1.f, 1.f), pair(0.f, 0.f)};  // over the warps before this one
-    {
-        for (int w0 = 0; w0 < warp; w0 += 3) {
-            Map m[3];
 #pragma unroll
-            for (int w = 0; w < 3; ++w) m[w] = sm.warp[buf][w0 + w][lc];  // those from `warp` on are not used
-            before = compose(before, m[0]);
-            if (w0 + 1 < warp) before = compose(before, m[1]);
-            if (w0 + 2 < warp) before = compose(before, m[2]);
-        }
+    for (int w0 = 0; w0 < kWarps - 1; w0 += 4) {
+        if (w0 >= warp) break;
+        Map m[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (w0 + w < kWarps - 1) m[w] = sm.warp[buf][w0 + w][lc];  // those from `warp` on are not used
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (w0 + w < kWarps - 1 && w0 + w < warp) before = compose(before, m[w]);
     }
     float2 in = carry;  // the state entering this CTA's tile
     if (cs > 1) {
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
             const float2 x = ld_pair(reinterpret_cast<const E*>(from + r * Q::RB));
             float2 om;
             gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + Q::TB + r * Q::RB)), a[r], om);
-            u[r] = GATE == kGateMix ? ptx::mul2(om, x) : x;
+            u[r] = GATE == kGateMix ? mul2(om, x) : x;
         }
         Map own = {a[0], u[0]};
 #pragma unroll
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
         if constexpr (Q::kBoxes) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                h = ptx::fma2(a[r], h, u[r]);
+                h = fma2(a[r], h, u[r]);
                 st_pair<E, true>(from + r * Q::RB, 0, h, true);
             }
             if (!whole) {
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
             const long long o0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                h = ptx::fma2(a[r], h, u[r]);
+                h = fma2(a[r], h, u[r]);
                 if (r < left) st_pair<E, Q::VS>(p.out, o0 + (t0 + r) * p.st[kOut], h, second);
             }
         }
@@ -618,12 +623,12 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
             float2 o, before = ld_pair(reinterpret_cast<const E*>(from + 2 * Q::TB + r * RS));
             gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + r * RS)), a[r], o);
             if (GATE == kGateMix)
-                before = ptx::fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f), before);
-            f[r] = ptx::mul2(a[r], before);
-            if (GATE != kGateDecay) f[r] = ptx::mul2(f[r], o);
+                before = fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f), before);
+            f[r] = mul2(a[r], before);
+            if (GATE != kGateDecay) f[r] = mul2(f[r], o);
             if (GATE == kGateMix) om[r] = o;
-            own.H = ptx::mul2(a[r], ptx::add2(own.H, d_of(r)));
-            own.A = ptx::mul2(own.A, a[r]);
+            own.H = mul2(a[r], add2(own.H, d_of(r)));
+            own.A = mul2(own.A, a[r]);
         }
         if (t0 >= 0 && t0 < R) {  // the sequence's first token: h0 comes before it
             const float2 h0 = ld_state2(p.h0, ((long long)cur.b * p.H + cur.h) * p.d + c, first, second);
@@ -633,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
                 float2 ga, o, before = h0;
                 gates<E, GATE>(ld_pair(reinterpret_cast<const E*>(from + r * RS)), ga, o);
                 if (GATE == kGateMix)
-                    before = ptx::fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f),
+                    before = fma2(ld_pair(reinterpret_cast<const E*>(from + 3 * Q::TB + r * RS)), pair(-1.f, -1.f),
                                        before);
-                f[r] = ptx::mul2(ga, before);
-                if (GATE != kGateDecay) f[r] = ptx::mul2(f[r], o);
+                f[r] = mul2(ga, before);
+                if (GATE != kGateDecay) f[r] = mul2(f[r], o);
             }
         }
         __syncwarp();
@@ -660,22 +665,22 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         if (boxes) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = ptx::add2(d_of(r), g);
-                g = ptx::mul2(a[r], dh);
-                st_pair<E, true>(from + r * RS, 0, GATE == kGateMix ? ptx::mul2(om[GATE == kGateMix ? r : 0], dh) : dh,
+                const float2 dh = add2(d_of(r), g);
+                g = mul2(a[r], dh);
+                st_pair<E, true>(from + r * RS, 0, GATE == kGateMix ? mul2(om[GATE == kGateMix ? r : 0], dh) : dh,
                                  true);
-                st_pair<E, true>(from + Q::TB + r * RS, 0, ptx::mul2(dh, f[r]), true);
+                st_pair<E, true>(from + Q::TB + r * RS, 0, mul2(dh, f[r]), true);
             }
             ptx::fence_async_smem();
         } else if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = ptx::add2(d_of(r), g);
-                g = ptx::mul2(a[r], dh);
+                const float2 dh = add2(d_of(r), g);
+                g = mul2(a[r], dh);
                 if (r < left) {
                     st_pair<E, Q::VS>(p.out, x0 + (t0 - r) * p.st[kOut],
-                                      GATE == kGateMix ? ptx::mul2(om[GATE == kGateMix ? r : 0], dh) : dh, second);
-                    st_pair<E, Q::VS>(p.dg, g0 + (t0 - r) * p.st[kDg], ptx::mul2(dh, f[r]), second);
+                                      GATE == kGateMix ? mul2(om[GATE == kGateMix ? r : 0], dh) : dh, second);
+                    st_pair<E, Q::VS>(p.dg, g0 + (t0 - r) * p.st[kDg], mul2(dh, f[r]), second);
                 }
             }
         }

@@ -7,6 +7,10 @@
 // of the centred values. A group of lanes keeps one head, so that weight and bias stay in registers, and
 // steps over the tokens, the next row's loads on their way while it works on this one; neighbouring groups
 // have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
+//
+// What bounds it: issue slots at bf16 ([8,12,2048,64] with a SiLU gate: 16.8 us, 66 % of the copy rate,
+// [16,16,4096,64] 73 to 78 us, 76 to 82 %; 22 thread instructions per element, of which an SM has 33 at that rate),
+// memory at fp32 ([8,1,8192,768]: 101 us, 89 %).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -111,11 +115,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
         }
         q.normalise(x, p.inv_d, p.eps);
 #pragma unroll
-        for (int j = 0; j < P; ++j) x[j] = ptx::fma2(x[j], w[j], bias[j]);
+        for (int j = 0; j < P; ++j) x[j] = fma2(x[j], w[j], bias[j]);
         if constexpr (GATED) {
             act_all<P>(p.act, z, f);
 #pragma unroll
-            for (int j = 0; j < P; ++j) f[j] = ptx::mul2(f[j], x[j]);
+            for (int j = 0; j < P; ++j) f[j] = mul2(f[j], x[j]);
         } else {
             act_all<P>(p.act, x, f);
         }

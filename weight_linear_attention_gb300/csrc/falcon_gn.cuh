@@ -15,7 +15,7 @@ using namespace seq;
 // ---- activations. e^-v is cut at 2^126 (far below any type's resolution of the results), so that
 // s = 1 / (1 + e) and 1 - s = e s are both finite and exact to a few units; NaN stays NaN.
 __device__ __forceinline__ float2 exp_neg(float2 v) {
-    const float2 k = ptx::mul2(v, pair(-kLog2e, -kLog2e));
+    const float2 k = mul2(v, pair(-kLog2e, -kLog2e));
     float2 e;
     asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.x) : "f"(k.x));
     asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.y) : "f"(k.y));
@@ -33,11 +33,11 @@ __device__ __forceinline__ void normal2(float2 v, float2& phi, float2& e) {
                              -0.02235809f, 0.14240131f, -0.30058289f, 0.19068813f, -0.04139117f};
     float2 p = pair(c[9], c[9]);
 #pragma unroll
-    for (int k = 8; k >= 0; --k) p = ptx::fma2(p, t, pair(c[k], c[k]));
-    const float2 s = ptx::mul2(ptx::mul2(v, v), pair(kE, kE));
+    for (int k = 8; k >= 0; --k) p = fma2(p, t, pair(c[k], c[k]));
+    const float2 s = mul2(mul2(v, v), pair(kE, kE));
     e = pair(ex2(s.x), ex2(s.y));
-    const float2 low = ptx::mul2(ptx::mul2(t, pair(0.5f, 0.5f)), ptx::mul2(p, e));
-    const float2 high = ptx::fma2(low, pair(-1.f, -1.f), pair(1.f, 1.f));
+    const float2 low = mul2(mul2(t, pair(0.5f, 0.5f)), mul2(p, e));
+    const float2 high = fma2(low, pair(-1.f, -1.f), pair(1.f, 1.f));
     phi = pair(v.x > 0.f ? high.x : low.x, v.y > 0.f ? high.y : low.y);
 }
 
@@ -47,10 +47,10 @@ __device__ __forceinline__ float2 act(float2 v) {
     if (ACT == kActGelu) {
         float2 phi, e;
         normal2(v, phi, e);
-        return ptx::mul2(v, phi);
+        return mul2(v, phi);
     }
-    const float2 s = rcp2(ptx::add2(exp_neg(v), pair(1.f, 1.f)));
-    return ACT == kActSilu ? ptx::mul2(v, s) : s;
+    const float2 s = rcp2(add2(exp_neg(v), pair(1.f, 1.f)));
+    return ACT == kActSilu ? mul2(v, s) : s;
 }
 // f(v) and f'(v)
 template <int ACT>
@@ -62,12 +62,12 @@ __device__ __forceinline__ void act_slope(float2 v, float2& f, float2& df) {
         constexpr float q = 0.39894228040143268f;  // 1 / sqrt(2 pi)
         float2 phi, e;
         normal2(v, phi, e);
-        f = ptx::mul2(v, phi);
-        df = ptx::fma2(ptx::mul2(v, pair(q, q)), e, phi);
+        f = mul2(v, phi);
+        df = fma2(mul2(v, pair(q, q)), e, phi);
     } else {
-        const float2 e = exp_neg(v), s = rcp2(ptx::add2(e, pair(1.f, 1.f))), c = ptx::mul2(e, s);
-        f = ACT == kActSilu ? ptx::mul2(v, s) : s;
-        df = ACT == kActSilu ? ptx::fma2(f, c, s) : ptx::mul2(s, c);
+        const float2 e = exp_neg(v), s = rcp2(add2(e, pair(1.f, 1.f))), c = mul2(e, s);
+        f = ACT == kActSilu ? mul2(v, s) : s;
+        df = ACT == kActSilu ? fma2(f, c, s) : mul2(s, c);
     }
 }
 
@@ -133,17 +133,17 @@ struct Row {
     __device__ __forceinline__ float normalise(float2 (&x)[P], float inv_d, float eps) const {
         float2 s = x[0];
 #pragma unroll
-        for (int i = 1; i < P; ++i) s = ptx::add2(s, x[i]);
+        for (int i = 1; i < P; ++i) s = add2(s, x[i]);
         const float mean = row_sum<LPR>(s) * inv_d;
         s = pair(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            x[i] = keep(i, ptx::add2(x[i], pair(-mean, -mean)));
-            s = ptx::fma2(x[i], x[i], s);
+            x[i] = keep(i, add2(x[i], pair(-mean, -mean)));
+            s = fma2(x[i], x[i], s);
         }
         const float rstd = rsqrtf(row_sum<LPR>(s) * inv_d + eps);
 #pragma unroll
-        for (int i = 0; i < P; ++i) x[i] = ptx::mul2(x[i], pair(rstd, rstd));
+        for (int i = 0; i < P; ++i) x[i] = mul2(x[i], pair(rstd, rstd));
         return rstd;
     }
 };

@@ -6,6 +6,10 @@
 // thread's channels stay the same and it sums dw and db in registers; the CTA adds its threads' sums up
 // in shared memory and leaves one partial sum per split of the rows, which a second, small kernel adds
 // in the order of the splits. Every order depends on the sizes alone: no atomics.
+//
+// What bounds it: issue slots at bf16 ([8,12,1024,64] with a SiLU gate: 17 us with the sums' kernel, 55 % of the
+// copy rate, [16,16,4096,64] 127 us, 78 %; 39 thread instructions per element, of which an SM has 55 at that rate),
+// memory at fp32 ([4,12,8192,64]: 71 us, 84 %).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -115,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 
             slope_all<P>(p.act, z, f, df);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                df[i] = ptx::mul2(ptx::mul2(dn[i], ptx::fma2(x[i], w[i], bias[i])), df[i]);  // dz
-                dn[i] = ptx::mul2(dn[i], f[i]);
+                df[i] = mul2(mul2(dn[i], fma2(x[i], w[i], bias[i])), df[i]);  // dz
+                dn[i] = mul2(dn[i], f[i]);
             }
 #pragma unroll
             for (int k = 0; k < NCH; ++k)
@@ -129,29 +133,29 @@ __global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 
         } else {
             float2 n[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) n[i] = ptx::fma2(x[i], w[i], bias[i]);
+            for (int i = 0; i < P; ++i) n[i] = fma2(x[i], w[i], bias[i]);
             slope_all<P>(p.act, n, f, df);
 #pragma unroll
-            for (int i = 0; i < P; ++i) dn[i] = ptx::mul2(dn[i], df[i]);
+            for (int i = 0; i < P; ++i) dn[i] = mul2(dn[i], df[i]);
         }
         float2 s1 = pair(0.f, 0.f), s2 = s1;
         if (was_in) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                aw[i] = ptx::fma2(dn[i], x[i], aw[i]);
-                ab[i] = ptx::add2(ab[i], dn[i]);
+                aw[i] = fma2(dn[i], x[i], aw[i]);
+                ab[i] = add2(ab[i], dn[i]);
             }
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            dn[i] = ptx::mul2(dn[i], w[i]);  // p; 0 behind d
-            s1 = ptx::add2(s1, dn[i]);
-            s2 = ptx::fma2(dn[i], x[i], s2);
+            dn[i] = mul2(dn[i], w[i]);  // p; 0 behind d
+            s1 = add2(s1, dn[i]);
+            s2 = fma2(dn[i], x[i], s2);
         }
         const float m1 = -row_sum<LPR>(s1) * p.inv_d, m2 = -row_sum<LPR>(s2) * p.inv_d;
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            dn[i] = ptx::mul2(ptx::fma2(x[i], pair(m2, m2), ptx::add2(dn[i], pair(m1, m1))), pair(rstd, rstd));
+            dn[i] = mul2(fma2(x[i], pair(m2, m2), add2(dn[i], pair(m1, m1))), pair(rstd, rstd));
 #pragma unroll
         for (int k = 0; k < NCH; ++k)
             if (mine && q.live(k)) {

@@ -7,8 +7,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "sm103_f32x2.cuh"
-
 namespace falcon {
 namespace seq {
 
@@ -118,23 +116,26 @@ __device__ __forceinline__ float decay_exp(float v) {
 
 // ---- pairs of channels: the same functions on two values, packed where the hardware can
 __device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }  // a b + c
 
 // s = 1 / (1 + e^-v), c = 1 - s. With e = e^-|v| <= 1 the smaller of the two is e / (1 + e).
 __device__ __forceinline__ void logistic2(float2 v, float2& s, float2& c) {
     const float2 e = pair(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
-    const float2 d = ptx::add2(e, pair(1.f, 1.f));
-    const float2 small = ptx::mul2(e, pair(rcp(d.x), rcp(d.y)));
-    const float2 large = ptx::fma2(small, pair(-1.f, -1.f), pair(1.f, 1.f));
+    const float2 d = add2(e, pair(1.f, 1.f));
+    const float2 small = mul2(e, pair(rcp(d.x), rcp(d.y)));
+    const float2 large = fma2(small, pair(-1.f, -1.f), pair(1.f, 1.f));
     const bool px = v.x > 0.f, py = v.y > 0.f;
     s = pair(px ? large.x : small.x, py ? large.y : small.y);
     c = pair(px ? small.x : large.x, py ? small.y : large.y);
 }
 __device__ __forceinline__ float2 decay_exp2(float2 v) {
-    float2 p = ptx::fma2(v, pair(1.f / 24, 1.f / 24), pair(1.f / 6, 1.f / 6));
-    p = ptx::fma2(p, v, pair(0.5f, 0.5f));
-    p = ptx::fma2(p, v, pair(1.f, 1.f));
-    p = ptx::fma2(p, v, pair(1.f, 1.f));
-    const float2 k = ptx::mul2(v, pair(kLog2e, kLog2e));
+    float2 p = fma2(v, pair(1.f / 24, 1.f / 24), pair(1.f / 6, 1.f / 6));
+    p = fma2(p, v, pair(0.5f, 0.5f));
+    p = fma2(p, v, pair(1.f, 1.f));
+    p = fma2(p, v, pair(1.f, 1.f));
+    const float2 k = mul2(v, pair(kLog2e, kLog2e));
     return pair(fabsf(v.x) < 0.0625f ? p.x : ex2(k.x), fabsf(v.y) < 0.0625f ? p.y : ex2(k.y));
 }
 

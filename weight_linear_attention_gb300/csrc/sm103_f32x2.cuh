@@ -15,10 +15,5 @@ __device__ __forceinline__ void fma2(float& x0, float& x1, float g0, float g1, f
         : "f"(g0), "f"(g1), "f"(v));
 }
 
-// ---- packed fp32 pairs by value
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }  // a b + c
-
 }  // namespace ptx
 }  // namespace falcon
