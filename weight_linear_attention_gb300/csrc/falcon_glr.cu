@@ -7,7 +7,7 @@
 // scan's direction: position n is token n forward and token len - 1 - n backward.
 //
 // One pass over the data. A CTA works through tiles of kTile positions x 2 LC channels; a thread owns two
-// channels of R consecutive positions. Tiles lie in a ring in shared memory, filled ahead and emptied by TMA
+// channels of R consecutive positions. Tiles lie in a ring in shared memory, filled ahead by TMA
 // (where addresses do not allow that, each warp copies its rows by cp.async, or through registers, and stores
 // them itself). A warp evaluates the gates of its rows once into registers and reduces its tokens to their map;
 // maps are composed over the warp (shuffles), the CTA (shared memory) and, for long sequences, the CTAs of a
@@ -15,7 +15,7 @@
 // (st.async, counted by an mbarrier there: no fence that would wait for the outputs on their way to memory), and
 // every CTA composes them all in the same order, so that the state that enters the next cluster-wide tile is
 // known everywhere without another exchange. Then each thread replays its tokens from its entering state into
-// the ring, whence a TMA store takes them. No scratch in global memory, no atomics on data; the order of every
+// a buffer of their own, whence a TMA store takes them while the next tile is worked on. No scratch in global memory, no atomics on data; the order of every
 // sum is fixed by the sizes. Waits are bounded: one that runs out raises a flag (falcon_device_status) and is
 // not repeated.
 //
@@ -46,6 +46,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 template <int LC>
 constexpr int kMaxCluster = LC == 32 ? 8 : 16;  // CTAs of a cluster; a fuller tile has more maps to hold
+constexpr int kStorer = 0, kLoader = 32;        // the threads that move boxes, in two warps: an issue takes ~130 cycles
 constexpr long long kTimeoutCycles = 4000000000LL;  // ~2 s
 
 __device__ int g_glr_timeout_flag = 0;
@@ -126,22 +127,20 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity) {
     } while (clock64() - t0 <= kTimeoutCycles);
     return false;
 }
-// The same for a whole warp. After a wait that ran out the following ones are skipped: the outputs are
-// lost, the flag tells, and the kernel comes to its end.
+// After a wait that ran out the thread skips its following ones: the outputs are lost, the flag tells, and the
+// kernel comes to its end.
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, bool& dead) {
-    if (dead) return;
-    if (!bounded_wait(bar, parity)) {
+    if (!dead && !bounded_wait(bar, parity)) {
         dead = true;
         atomicExch(&g_glr_timeout_flag, 1);
     }
-    dead = __any_sync(0xffffffffu, dead);
 }
 
 // The state that enters this thread's positions: composes the thread's map over the warp, the CTA and the
 // cluster. `carry` is the state entering the cluster's tile (without a cluster only for an item's first tile,
 // `fresh`; then sm.state has it) and, in a cluster, the one leaving it on return. Called by all scanning
 // threads of the cluster the same number of times; `it` counts the calls.
-// `behind_barrier` runs when every thread of the CTA has left the tile before this one.
+// `behind_barrier` runs when every thread of the CTA has evaluated its gates and left the tile before this one.
 template <int LC, typename F>
 __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, bool fresh, int cs, int rank, const Map& own,
                                             float2& carry, bool& dead, F behind_barrier) {
@@ -197,9 +196,9 @@ __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, bool fresh, in
             for (int r = 0; r < 4; ++r) m[r] = sm.cta[buf][r0 + r][lc];  // those behind cs are not used
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
+                if (r0 + r >= cs) break;
                 if (r0 + r == rank) in = carry;
-                const float2 next = apply(m[r], carry);
-                carry = pair(r0 + r < cs ? next.x : carry.x, r0 + r < cs ? next.y : carry.y);
+                carry = apply(m[r], carry);
             }
         }
     } else if (!fresh) {
@@ -348,7 +347,7 @@ __device__ __forceinline__ void leave_tile(const Params& p, Maps<LC>& sm, int it
         st_state2(p.h_out, ((long long)c.b * p.H + c.h) * p.d + c.c0 + 2 * lc, cs == 1 ? h : carry, first, second);
 }
 
-// What thread 0 keeps of a ring of boxes: a stage's boxes have landed (a barrier for each stage); the tile to be
+// What the threads that move boxes keep: a stage's boxes have landed (a barrier for each stage); the tile to be
 // loaded next, the tile whose outputs lie in the ring.
 template <int S>
 struct Mover {
@@ -374,7 +373,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
     constexpr int SB = 2 * Q::TB;  // a stage: x, g
     __shared__ Maps<LC> sm;
     __shared__ Mover<S> mv;
-    extern __shared__ __align__(128) uint8_t ring[];  // [S][x, g][warp][rows]
+    extern __shared__ __align__(128) uint8_t ring[];  // [S][x, g][warp][rows], then with boxes [2][out][warp][rows]
+    constexpr int OB = Q::TB;
+    uint8_t* const outs = ring + S * SB;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / LC, lc = lane % LC;
     const int rank = blockIdx.x % cs, clusters = gridDim.x / cs, step = cs * G::kTile;
     const int row0 = (rank * kWarps + warp) * G::kRows;  // of the warp, in the cluster's tile
@@ -386,18 +387,18 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
     pre.item = blockIdx.x / cs;
     enter<G::kChans>(p, pre);
 
-    // thread 0 moves the boxes
+    // one thread fills the ring with boxes, another stores the outputs
     auto load = [&](int stage, const Cursor& c) {
         const uint32_t to = ptx::smem_u32(ring + stage * SB), bar = ptx::smem_u32(&mv.full[stage]);
         ptx::mbar_expect_tx(bar, SB);
         load_tile<Q>(to, &p.tm[kX], c, c.n0 + rank * G::kTile, bar);
         load_tile<Q>(to + Q::TB, &p.tm[kG], c, c.n0 + rank * G::kTile, bar);
     };
-    auto store = [&](int stage, const Cursor& c) {
-        store_tile<Q>(&p.tm[kOut], ptx::smem_u32(ring + stage * SB), c, c.n0 + rank * G::kTile, p.T);
+    auto store = [&](int tile, const Cursor& c) {
+        store_tile<Q>(&p.tm[kOut], ptx::smem_u32(outs + (tile & 1) * OB), c, c.n0 + rank * G::kTile, p.T);
         ptx::bulk_commit();
     };
-    if (Q::kBoxes && threadIdx.x == 0) {
+    if (Q::kBoxes && threadIdx.x == kLoader) {
         Cursor c = pre;
         int n = 0;
         for (; n < S && c.item < p.items; ++n) {
@@ -447,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
                 st_pair<E, true>(from + r * Q::RB, 0, pair(0.f, 0.f), true);
                 st_pair<E, true>(from + Q::TB + r * Q::RB, 0, idle_gate<GATE>(), true);
             }
+            if (Q::kBoxes) ptx::fence_async_smem();  // before boxes overwrite it
         }
         float2 a[R], u[R];
 #pragma unroll
@@ -461,29 +463,31 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
         for (int r = 1; r < R; ++r) own = compose(own, Map{a[r], u[r]});
         __syncwarp();  // every lane has read the stage before this one, which is filled again
         fetch(stage == 0 ? S - 1 : stage - 1);
+        if (Q::kBoxes && threadIdx.x == kStorer) ptx::bulk_wait_read<0>();  // this tile's outputs go where those two back lay
         float2 h = scan_tile<LC>(sm, it, cur.n0 == 0, cs, rank, own, carry, dead, [&] {
-            if (Q::kBoxes && threadIdx.x == 0 && it > 0 && !dead) store(stage == 0 ? S - 1 : stage - 1, mv.held);
-        });
-        if (Q::kBoxes && threadIdx.x == 0 && !dead) {
-            mv.held = cur;
-            if (it > 0 && mv.next.item < p.items) {
+            if (!Q::kBoxes || dead) return;
+            if (threadIdx.x == kStorer) {
+                if (it > 0) store(it - 1, mv.held);
+                mv.held = cur;
+            }
+            if (threadIdx.x == kLoader && mv.next.item < p.items) {  // into the stage that every warp has read
                 Cursor n = mv.next;
-                ptx::bulk_wait_read<0>();  // the outputs have left the stage
-                load(stage == 0 ? S - 1 : stage - 1, n);
+                load(stage, n);
                 advance<G::kChans>(p, n, step, clusters);
                 mv.next = n;
                 ++mv.loaded;
             }
-        }
+        });
         if constexpr (Q::kBoxes) {
+            uint8_t* const to = outs + (it & 1) * OB + warp * Q::WB + Q::at(seg, 0) + lc * 2 * sizeof(E);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = fma2(a[r], h, u[r]);
-                st_pair<E, true>(from + r * Q::RB, 0, h, true);
+                st_pair<E, true>(to + r * Q::RB, 0, h, true);
             }
             if (!whole) {
 #pragma unroll 1
-                for (int r = max(left, 0); r < R; ++r) st_pair<E, true>(from + r * Q::RB, 0, pair(0.f, 0.f), true);
+                for (int r = max(left, 0); r < R; ++r) st_pair<E, true>(to + r * Q::RB, 0, pair(0.f, 0.f), true);
             }
             ptx::fence_async_smem();
         } else if (first) {
@@ -508,11 +512,12 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
     }
     if constexpr (Q::kBoxes) {
         __syncthreads();
-        if (threadIdx.x == 0) {
-            if (it > 0 && !dead) store((it - 1) % S, mv.held);
-            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+        if (threadIdx.x == kStorer) {
+            if (it > 0 && !dead) store(it - 1, mv.held);
             ptx::bulk_wait_all();
         }
+        if (threadIdx.x == kLoader)  // loads that a wait that ran out has left behind
+            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
     }
     if (cs > 1) {  // no CTA leaves while a peer may still write to it
         cluster_arrive();
@@ -527,7 +532,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
     constexpr int NT = GATE == kGateMix ? 4 : 3, SB = NT * Q::TB;  // a stage: g, dout, out, x
     __shared__ Maps<LC> sm;
     __shared__ Mover<S> mv;
-    extern __shared__ __align__(128) uint8_t ring[];  // [S][tensor][warp][rows]
+    extern __shared__ __align__(128) uint8_t ring[];  // [S][tensor][warp][rows], then with boxes [2][dx, dg][..][..]
+    constexpr int OB = 2 * Q::TB;
+    uint8_t* const outs = ring + S * SB;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = lane / LC, lc = lane % LC;
     const int rank = blockIdx.x % cs, clusters = gridDim.x / cs, step = cs * G::kTile;
     const int row0 = (rank * kWarps + warp) * G::kRows;
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
     // inside the tile
     auto low = [&](const Cursor& c) { return c.len - (c.n0 + rank * G::kTile) - G::kTile; };
 
-    // thread 0 moves the boxes
+    // one thread fills the ring with boxes, another stores the outputs
     auto load = [&](int stage, const Cursor& c) {
         const uint32_t to = ptx::smem_u32(ring + stage * SB), bar = ptx::smem_u32(&mv.full[stage]);
         const int t = low(c);
@@ -552,14 +559,14 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         load_tile<Q>(to + 2 * Q::TB, &p.tm[kOutIn], c, t - 1, bar);  // h before the token
         if (GATE == kGateMix) load_tile<Q>(to + 3 * Q::TB, &p.tm[kX], c, t, bar);
     };
-    auto store = [&](int stage, const Cursor& c) {
+    auto store = [&](int tile, const Cursor& c) {
         if (low(c) < 0) return;  // the warps have stored such a tile themselves
-        const uint32_t from = ptx::smem_u32(ring + stage * SB);
+        const uint32_t from = ptx::smem_u32(outs + (tile & 1) * OB);
         store_tile<Q>(&p.tm[kOut], from, c, low(c), p.T);
         store_tile<Q>(&p.tm[kDg], from + Q::TB, c, low(c), p.T);
         ptx::bulk_commit();
     };
-    if (Q::kBoxes && threadIdx.x == 0) {
+    if (Q::kBoxes && threadIdx.x == kLoader) {
         Cursor c = pre;
         int n = 0;
         for (; n < S && c.item < p.items; ++n) {
@@ -614,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         if (!whole) {  // positions behind the last: dout and out read as zeros there
 #pragma unroll 1
             for (int r = max(left, 0); r < R; ++r) st_pair<E, true>(from + r * RS, 0, idle_gate<GATE>(), true);
+            if (Q::kBoxes) ptx::fence_async_smem();
         }
-        auto d_of = [&](int r) { return ld_pair(reinterpret_cast<const E*>(from + Q::TB + r * RS)); };
-        float2 a[R], f[R], om[GATE == kGateMix ? R : 1];
+        float2 a[R], f[R], d[R], om[GATE == kGateMix ? R : 1];
         Map own = {pair(1.f, 1.f), pair(0.f, 0.f)};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -627,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
             f[r] = mul2(a[r], before);
             if (GATE != kGateDecay) f[r] = mul2(f[r], o);
             if (GATE == kGateMix) om[r] = o;
-            own.H = mul2(a[r], add2(own.H, d_of(r)));
+            d[r] = ld_pair(reinterpret_cast<const E*>(from + Q::TB + r * RS));
+            own.H = mul2(a[r], add2(own.H, d[r]));
             own.A = mul2(own.A, a[r]);
         }
         if (t0 >= 0 && t0 < R) {  // the sequence's first token: h0 comes before it
@@ -646,36 +654,38 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         }
         __syncwarp();
         fetch(stage == 0 ? S - 1 : stage - 1);
+        if (Q::kBoxes && threadIdx.x == kStorer) ptx::bulk_wait_read<0>();
         float2 g = scan_tile<LC>(sm, it, cur.n0 == 0, cs, rank, own, carry, dead, [&] {
-            if (Q::kBoxes && threadIdx.x == 0 && it > 0 && !dead) store(stage == 0 ? S - 1 : stage - 1, mv.held);
-        });
-        if (Q::kBoxes && threadIdx.x == 0 && !dead) {
-            mv.held = cur;
-            if (it > 0 && mv.next.item < p.items) {
+            if (!Q::kBoxes || dead) return;
+            if (threadIdx.x == kStorer) {
+                if (it > 0) store(it - 1, mv.held);
+                mv.held = cur;
+            }
+            if (threadIdx.x == kLoader && mv.next.item < p.items) {  // into the stage that every warp has read
                 Cursor n = mv.next;
-                ptx::bulk_wait_read<0>();  // the outputs have left the stage
-                load(stage == 0 ? S - 1 : stage - 1, n);
+                load(stage, n);
                 advance<G::kChans>(p, n, step, clusters);
                 mv.next = n;
                 ++mv.loaded;
             }
-        }
+        });
         const long long x0 = cur.b * p.sb[kOut] + cur.h * p.sh[kOut] + c, g0 = cur.b * p.sb[kDg] + cur.h * p.sh[kDg] + c;
         const bool boxes = Q::kBoxes && low(cur) >= 0;
         if (boxes) {
+            uint8_t* const to = outs + (it & 1) * OB + lc * 2 * sizeof(E) + (G::kTile - 1 - warp * G::kRows - seg * R) * Q::RB;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = add2(d_of(r), g);
+                const float2 dh = add2(d[r], g);
                 g = mul2(a[r], dh);
-                st_pair<E, true>(from + r * RS, 0, GATE == kGateMix ? mul2(om[GATE == kGateMix ? r : 0], dh) : dh,
+                st_pair<E, true>(to + r * RS, 0, GATE == kGateMix ? mul2(om[GATE == kGateMix ? r : 0], dh) : dh,
                                  true);
-                st_pair<E, true>(from + Q::TB + r * RS, 0, mul2(dh, f[r]), true);
+                st_pair<E, true>(to + Q::TB + r * RS, 0, mul2(dh, f[r]), true);
             }
             ptx::fence_async_smem();
         } else if (first) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float2 dh = add2(d_of(r), g);
+                const float2 dh = add2(d[r], g);
                 g = mul2(a[r], dh);
                 if (r < left) {
                     st_pair<E, Q::VS>(p.out, x0 + (t0 - r) * p.st[kOut],
@@ -699,11 +709,12 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
     }
     if constexpr (Q::kBoxes) {
         __syncthreads();
-        if (threadIdx.x == 0) {
-            if (it > 0 && !dead) store((it - 1) % S, mv.held);
-            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+        if (threadIdx.x == kStorer) {
+            if (it > 0 && !dead) store(it - 1, mv.held);
             ptx::bulk_wait_all();
         }
+        if (threadIdx.x == kLoader)  // loads that a wait that ran out has left behind
+            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
     }
     if (cs > 1) {
         cluster_arrive();
@@ -982,13 +993,15 @@ bool items_of(const Call& c, int* tiles, long long* items) {
 // start in different banks (118 against 141 us for [1,12,131072,64] bf16).
 template <typename E, int LC, bool BWD>
 constexpr int kR = (BWD ? 8 : 16) / (int)(sizeof(E) / 2) - (LC < 32 && sizeof(E) == 2 ? 1 : 0);
-constexpr int kStages = 3;
 
 template <typename E, int GATE, int LC, int CB, bool BWD>
 struct Kernel {
     static constexpr int R = kR<E, LC, BWD>;
     using Q = Ring<E, LC, R, CB>;
-    static constexpr int kBytes = kStages * (BWD ? (GATE == kGateMix ? 4 : 3) : 2) * Q::TB;
+    // two tiles of inputs and two of outputs (boxes), or three of inputs: about 96 KB, two CTAs an SM
+    static constexpr int kStages = Q::kBoxes ? 2 : 3;
+    static constexpr int kBytes =
+        (kStages * (BWD ? (GATE == kGateMix ? 4 : 3) : 2) + (Q::kBoxes ? (BWD ? 4 : 2) : 0)) * Q::TB;
     static KernelInfo& info() {
         static KernelInfo k;
         return k;
