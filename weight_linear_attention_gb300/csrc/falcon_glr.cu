@@ -950,20 +950,21 @@ int resident(Fn fn, KernelInfo& info, int dev, int cs, int bytes) {
     return n;
 }
 
-// A launch of one of the two tile shapes, and what it would cost.
+// A launch of one of the tile shapes, and what it would cost (sixteenths of a microsecond).
 struct Plan {
     int cs = 0;           // 0: the kernel cannot run
     long long clusters = 0, cost = 0;
 };
 
 // The cluster size for a tile shape. A sequence's tiles are dealt to the cs CTAs of its cluster; every round of
-// cluster-wide tiles lasts as long as a tile on the fullest SM: measured (bf16, 8192 elements forward, 4096
-// backward) 1.0 to 1.15 us where each SM holds one CTA, 1.75 us (narrow tiles 1.9 to 2 us) where one holds two, and
-// 0.38 us more for the exchange in a cluster; fp32 tiles, of half the elements, are a little quicker. The costs are
-// those, in eighths of a microsecond.
-template <int LC, bool F32, typename Fn>
+// cluster-wide tiles lasts as long as a tile on the fullest SM, and in a cluster the exchange longer. Measured, in
+// sixteenths of a microsecond (bf16; fp32 tiles, of half the elements, are a little quicker): a tile takes 16
+// forward and 18 backward where each SM holds one CTA, 28 to 31 and 25 to 26 (the narrower the more: a box moves a
+// row at a time) where one holds two; the exchange 6, and 7 and 12 where no second CTA covers it.
+template <int LC, bool BWD, bool F32, typename Fn>
 Plan plan_for(Fn fn, KernelInfo& info, int dev, int bytes, long long items, int T, int rows) {
-    constexpr int kAlone = F32 ? 7 : 9, kShared = F32 ? 13 : LC < 32 ? 16 : 14, kExchange = 3;
+    constexpr int kAlone = F32 ? 14 : BWD ? 18 : 16, kExchangeAlone = BWD ? 12 : 7, kExchange = 6;
+    constexpr int kShared = (BWD ? LC == 8 ? 26 : 25 : LC == 8 ? 31 : LC == 16 ? 29 : 28) - (F32 ? 2 : 0);
     Plan best;
     const long long tiles = ((long long)T + rows - 1) / rows;
     for (int cs = 1; cs <= kMaxCluster<LC> && cs <= tiles; ++cs) {
@@ -971,7 +972,9 @@ Plan plan_for(Fn fn, KernelInfo& info, int dev, int bytes, long long items, int 
         if (most == 0) continue;
         const long long clusters = items < most ? items : most;
         const long long rounds = (items + clusters - 1) / clusters * ((tiles + cs - 1) / cs);
-        const long long cost = rounds * ((clusters * cs <= kSms ? kAlone : kShared) + (cs > 1 ? kExchange : 0));
+        const bool alone = clusters * cs <= kSms;
+        const long long cost =
+            rounds * ((alone ? kAlone : kShared) + (cs == 1 ? 0 : alone ? kExchangeAlone : kExchange));
         if (best.cs == 0 || cost < best.cost) {
             best.cs = cs;
             best.clusters = clusters;
@@ -990,7 +993,7 @@ bool items_of(const Call& c, int* tiles, long long* items) {
 
 // R: rows of a thread. Forward 16 (two fp32 values a row and channel stay in registers), backward 8 (four); half
 // for fp32, whose tiles take twice the shared memory. In the narrow tiles one less: the segments of a warp then
-// start in different banks (118 against 141 us for [1,12,131072,64] bf16).
+// start in different banks (118 against 141 us for [1,12,131072,64] bf16 in tiles of 16 channels).
 template <typename E, int LC, bool BWD>
 constexpr int kR = (BWD ? 8 : 16) / (int)(sizeof(E) / 2) - (LC < 32 && sizeof(E) == 2 ? 1 : 0);
 
@@ -1014,7 +1017,7 @@ struct Kernel {
         int tiles;
         long long items;
         if (!items_of<LC>(c, &tiles, &items)) return Plan{};
-        return plan_for<LC, sizeof(E) == 4>(fn(), info(), dev, kBytes, items, c.p.T, Q::G::kTile);
+        return plan_for<LC, BWD, sizeof(E) == 4>(fn(), info(), dev, kBytes, items, c.p.T, Q::G::kTile);
     }
     // 0, a status, or -1: TMA does not take these tensors
     static int launch(const Call& c, const Plan& plan, cudaStream_t s) {
@@ -1066,8 +1069,8 @@ int launch_walk(const Call& c, cudaStream_t s) {
 template <bool BWD>
 bool walks(const Call& c, int vw, const Plan& plan) {
     const long long lanes = c.B * c.p.H * (c.p.d / vw);
-    const long long token = BWD ? std::max(5LL, lanes / 9400) : std::max(2LL, lanes / 18600);
-    return c.p.T <= 256 && c.p.T * token <= plan.cost + 8;
+    const long long token = BWD ? std::max(10LL, lanes / 4700) : std::max(4LL, lanes / 9300);
+    return c.p.T <= 256 && c.p.T * token <= plan.cost + 16;
 }
 
 // The plan's kernel, unless walking is cheaper.
@@ -1087,14 +1090,19 @@ int launch_scan(const Call& c, int cb, int vw, cudaStream_t s) {
     if (!items_of<32>(c, &tiles, &items)) return 2;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 4;
     if (cb == 16) {
+        // narrower tiles split the channels where sequences are few and long
         using Wide = Kernel<E, GATE, 32, kTma, BWD>;
+        using Half = Kernel<E, GATE, 16, kTma, BWD>;
         using Narrow = Kernel<E, GATE, 8, kTma, BWD>;
-        const Plan w = Wide::plan(c, dev), n = Narrow::plan(c, dev);
-        if (w.cs == 0 && n.cs == 0) return 4;
-        // narrow tiles split the channels where sequences are few and long
-        const bool narrow = n.cs > 0 && (w.cs == 0 || n.cost < w.cost);
-        if (walks<BWD>(c, vw, narrow ? n : w)) return walk();
-        const int st = narrow ? Narrow::launch(c, n, s) : Wide::launch(c, w, s);
+        const Plan plans[3] = {Wide::plan(c, dev), Half::plan(c, dev), Narrow::plan(c, dev)};
+        int k = 0;
+        for (int i = 1; i < 3; ++i)
+            if (plans[i].cs > 0 && (plans[k].cs == 0 || plans[i].cost < plans[k].cost)) k = i;
+        if (plans[k].cs == 0) return 4;
+        if (walks<BWD>(c, vw, plans[k])) return walk();
+        const int st = k == 0   ? Wide::launch(c, plans[0], s)
+                       : k == 1 ? Half::launch(c, plans[1], s)
+                                : Narrow::launch(c, plans[2], s);
         if (st >= 0) return st;
         cb = 8;
     }
