@@ -360,45 +360,41 @@ def _t():
     """torch, the types' codes, and how to ask for the current stream and device; looked up once."""
     import torch
 
-    return (torch, {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32}, torch._C._cuda_getCurrentRawStream,
-            torch.cuda.current_device)
+    return (torch, torch.float32, {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32},
+            torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
 
 
 def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
     """Checks the tensors of one call and marshals them. `views` (tensors or None) are [B,H,T,d] like x in x's type,
     `arrays` (tensors or None) contiguous fp32 of `shape`; `names` has the views' names, then the arrays'. Returns
-    the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides, and the function that calls
-    the library's `what` on x's device and stream."""
-    torch, codes, raw_stream, current_device = _t()
+    the library's function `what`, the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides,
+    and the stream."""
+    torch, f32, codes, raw_stream, current_device = _t()
     full, dtype, index = x.shape, x.dtype, x.get_device()
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    code = codes.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
     if choice is None:
         raise ValueError(f"{what}: no such gate or activation")
+    if dtype not in codes:
+        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
     pointers, strides = [], []
-    for i, t in enumerate(views):
+    for t in views:
         if t is None:
             pointers.append(None)
             strides += (0, 0, 0)
             continue
-        if t.shape != full or t.dtype is not dtype or t.get_device() != index:
-            raise ValueError(f"{names[i]} must be {tuple(full)} {dtype} on {x.device}, got {tuple(t.shape)} {t.dtype} "
-                             f"on {t.device}")
-        sb, sh, st, sd = t.stride()
-        if sd != 1 and full[3] > 1:
-            raise ValueError(f"{names[i]}'s channels must be contiguous (stride 1), got stride {sd}")
+        sb, sh, st, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+        if t.shape != full or t.dtype is not dtype or t.get_device() != index or sd != 1 and full[3] > 1:
+            raise ValueError(f"{names[len(pointers)]} must be {tuple(full)} {dtype} on {x.device} with contiguous "
+                             f"channels, got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
         strides += (sb, sh, st)
         pointers.append(t.data_ptr())
-    f32 = torch.float32
-    for i, t in enumerate(arrays, len(views)):
+    for t in arrays:
         if t is None:
             pointers.append(None)
             continue
         if t.shape != shape or t.dtype is not f32 or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{names[i]} must be contiguous {tuple(shape)} {f32} on {x.device}, got "
+            raise ValueError(f"{names[len(pointers)]} must be contiguous {tuple(shape)} {f32} on {x.device}, got "
                              f"{tuple(t.shape)} {t.dtype} on {t.device}")
         pointers.append(t.data_ptr())
     if lengths is None:
@@ -414,17 +410,19 @@ def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     fn = getattr(_lib or load(), what)
+    if index != current_device():
+        fn = _on_device(fn, index)
+    return fn, pointers, _PACK_DIMS(*full, codes[dtype], 0), _PACK_STRIDES[len(views)](*strides), stream
+
+
+def _on_device(fn, index):
+    """fn with device `index` current."""
 
     def call(*args):
-        if index == current_device():
-            status = fn(choice, *args, stream)
-        else:
-            with torch.cuda.device(index):
-                status = fn(choice, *args, stream)
-        if status != FALCON_OK:
-            raise FalconError(status, what)
+        with _t()[0].cuda.device(index):
+            return fn(*args)
 
-    return pointers, _PACK_DIMS(*full, code, 0), _PACK_STRIDES[len(views)](*strides), call
+    return call
 
 
 def _sizes(x):
@@ -451,9 +449,12 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
         out = _empty(x, x.shape, x.dtype)
     if h_final is None and want_state:
         h_final = _empty(x, (B, H, d))
-    p, dims, strides, call = _seq_call("falcon_glr_fwd", GLR_GATES.get(gate), x, (x, g, out), (h0, h_final), (B, H, d),
-                                       lengths, ("x", "g", "out", "h0", "h_final"), stream)
-    call(p[0], p[1], p[3], p[5], p[2], p[4], dims, strides)
+    code = GLR_GATES.get(gate)
+    fn, p, dims, strides, stream = _seq_call("falcon_glr_fwd", code, x, (x, g, out), (h0, h_final), (B, H, d), lengths,
+                                             ("x", "g", "out", "h0", "h_final"), stream)
+    st = fn(code, p[0], p[1], p[3], p[5], p[2], p[4], dims, strides, stream)
+    if st != FALCON_OK:
+        raise FalconError(st, "falcon_glr_fwd")
     return out, h_final
 
 
@@ -465,10 +466,13 @@ def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None,
     dx = _empty(x, x.shape, x.dtype) if dx is None else dx
     dg = _empty(x, x.shape, x.dtype) if dg is None else dg
     dh0 = _empty(x, (B, H, d)) if dh0 is None else dh0
-    p, dims, strides, call = _seq_call(
-        "falcon_glr_bwd", GLR_GATES.get(gate), x, (x, g, out, dout, dx, dg), (h0, dh_final, dh0), (B, H, d), lengths,
+    code = GLR_GATES.get(gate)
+    fn, p, dims, strides, stream = _seq_call(
+        "falcon_glr_bwd", code, x, (x, g, out, dout, dx, dg), (h0, dh_final, dh0), (B, H, d), lengths,
         ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"), stream)
-    call(p[0], p[1], p[2], p[6], p[9], p[3], p[7], p[4], p[5], p[8], dims, strides)
+    st = fn(code, p[0], p[1], p[2], p[6], p[9], p[3], p[7], p[4], p[5], p[8], dims, strides, stream)
+    if st != FALCON_OK:
+        raise FalconError(st, "falcon_glr_bwd")
     return {"dx": dx, "dg": dg, "dh0": dh0}
 
 
@@ -482,9 +486,12 @@ def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5
     B, H, T, d = _sizes(x)
     if y is None:
         y = _empty(x, (B, T, H, d), x.dtype).transpose(1, 2)
-    p, dims, strides, call = _seq_call("falcon_gn_fwd", GN_ACTS.get(act), x, (x, z, y), (weight, bias), (H, d), lengths,
-                                       ("x", "z", "y", "weight", "bias"), stream)
-    call(p[0], p[1], p[3], p[4], p[5], p[2], dims, strides, eps)
+    code = GN_ACTS.get(act)
+    fn, p, dims, strides, stream = _seq_call("falcon_gn_fwd", code, x, (x, z, y), (weight, bias), (H, d), lengths,
+                                             ("x", "z", "y", "weight", "bias"), stream)
+    st = fn(code, p[0], p[1], p[3], p[4], p[5], p[2], dims, strides, eps, stream)
+    if st != FALCON_OK:
+        raise FalconError(st, "falcon_gn_fwd")
     return y
 
 
@@ -500,8 +507,9 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
     if want_params:
         dweight = _empty(x, (H, d)) if dweight is None else dweight
         dbias = _empty(x, (H, d)) if dbias is None else dbias
-    p, dims, strides, call = _seq_call(
-        "falcon_gn_bwd", GN_ACTS.get(act), x, (x, z, dy, dx, dz), (weight, bias, dweight, dbias), (H, d), lengths,
+    code = GN_ACTS.get(act)
+    fn, p, dims, strides, stream = _seq_call(
+        "falcon_gn_bwd", code, x, (x, z, dy, dx, dz), (weight, bias, dweight, dbias), (H, d), lengths,
         ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"), stream)
     size = 0
     if dweight is not None or dbias is not None:
@@ -513,5 +521,8 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
             if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
             size = workspace.numel() * workspace.element_size()
-    call(p[0], p[1], p[5], p[6], p[9], p[2], p[3], p[4], p[7], p[8], dims, strides, eps, _ptr(workspace), size)
+    st = fn(code, p[0], p[1], p[5], p[6], p[9], p[2], p[3], p[4], p[7], p[8], dims, strides, eps, _ptr(workspace), size,
+            stream)
+    if st != FALCON_OK:
+        raise FalconError(st, "falcon_gn_bwd")
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
