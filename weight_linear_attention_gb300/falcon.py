@@ -432,8 +432,13 @@ def _sizes(x):
 
 
 def _empty(x, shape, dtype=None):
-    torch = _t()[0]
-    return torch.empty(shape, dtype=dtype or torch.float32, device=x.device)
+    return x.new_empty(shape, dtype=dtype or _t()[1])
+
+
+@functools.lru_cache(maxsize=256)
+def _gn_bwd_bytes(dims):
+    """falcon_gn_bwd_workspace_bytes of a packed falcon_seq_dims_t (a function of the sizes alone)."""
+    return int(load().falcon_gn_bwd_workspace_bytes(dims))
 
 
 def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, want_state=True, stream=None):
@@ -514,7 +519,7 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
     size = 0
     if dweight is not None or dbias is not None:
         if workspace is None:
-            size = load().falcon_gn_bwd_workspace_bytes(dims)
+            size = _gn_bwd_bytes(dims)
             if size > 0:
                 workspace = _empty(x, size, _t()[0].uint8)
         else:
