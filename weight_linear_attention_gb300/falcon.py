@@ -361,7 +361,7 @@ def _t():
     import torch
 
     return (torch, torch.float32, {torch.bfloat16: FALCON_BF16, torch.float32: FALCON_F32},
-            torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+            torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty)
 
 
 def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
@@ -369,7 +369,7 @@ def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
     `arrays` (tensors or None) contiguous fp32 of `shape`; `names` has the views' names, then the arrays'. Returns
     the library's function `what`, the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides,
     and the stream."""
-    torch, f32, codes, raw_stream, current_device = _t()
+    torch, f32, codes, raw_stream, current_device, _ = _t()
     full, dtype, index = x.shape, x.dtype, x.get_device()
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
@@ -383,11 +383,11 @@ def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
             pointers.append(None)
             strides += (0, 0, 0)
             continue
-        sb, sh, st, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
-        if t.shape != full or t.dtype is not dtype or t.get_device() != index or sd != 1 and full[3] > 1:
+        layout = t.stride()
+        if t.shape != full or t.dtype is not dtype or t.get_device() != index or layout[3] != 1 and full[3] > 1:
             raise ValueError(f"{names[len(pointers)]} must be {tuple(full)} {dtype} on {x.device} with contiguous "
-                             f"channels, got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
-        strides += (sb, sh, st)
+                             f"channels, got {tuple(t.shape)} {t.dtype} on {t.device} with strides {layout}")
+        strides += layout[:3]
         pointers.append(t.data_ptr())
     for t in arrays:
         if t is None:
@@ -432,7 +432,7 @@ def _sizes(x):
 
 
 def _empty(x, shape, dtype=None):
-    return x.new_empty(shape, dtype=dtype or _t()[1])
+    return _t()[5](shape, dtype=dtype or _t()[1], device=x.device)
 
 
 @functools.lru_cache(maxsize=256)
@@ -521,7 +521,7 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
         if workspace is None:
             size = _gn_bwd_bytes(dims)
             if size > 0:
-                workspace = _empty(x, size, _t()[0].uint8)
+                workspace = _t()[5](size, dtype=_t()[0].uint8, device=x.device)
         else:
             if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
