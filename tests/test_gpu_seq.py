@@ -348,6 +348,28 @@ def test_groupnorm_layouts_and_lengths(layout, shape, ragged):
         _close(k, got[k], ref[k], e[k])
 
 
+# a width for every split of a row over lanes, and its neighbour that leaves lanes idle
+GN_LANES = [8, 15, 20, 24, 31, 32, 47, 48, 49, 60, 63, 80, 96, 99, 127, 129, 160, 255, 300, 520, 700]
+
+
+@pytest.mark.parametrize("layout", ["dense", "bthd", "odd"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", GN_LANES)
+def test_groupnorm_lanes(layout, dt, d):
+    shape = (3, 3, 157, d)
+    x, z, w, b, dy = gn_inputs(shape, DT[dt], 70 + d, True)
+    n = torch.tensor([157, 0, 80], dtype=torch.int32)
+    xd, zd, dd = place(layout, x, z, dy)
+    wd, bd = w.cuda(), b.cuda()
+    y, dx, dz = poison(layout, 3, shape, DT[dt])
+    y = F.groupnorm_forward(xd, wd, bd, zd, act="silu", lengths=n.cuda(), y=y)
+    _close("y", y, *R.gn_forward(x, w, b, z, "silu", 1e-5, n))
+    got = F.groupnorm_backward(xd, dd, wd, bd, zd, act="silu", lengths=n.cuda(), dx=dx, dz=dz)
+    ref, e = R.gn_backward(x, dy, w, b, z, "silu", 1e-5, n)
+    for k in ref:
+        _close(k, got[k], ref[k], e[k])
+
+
 def test_groupnorm_optional_parameters():
     x, z, w, b, dy = gn_inputs((2, 2, 9, 64), torch.float32, 60, True)
     xd, dd = x.cuda(), dy.cuda()

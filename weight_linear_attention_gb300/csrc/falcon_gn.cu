@@ -151,24 +151,43 @@ int launch(FwdParams p, cudaStream_t s) {
     return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, false>, dim3(grid), kThreads, s, p);
 }
 
+// Lanes and chunks of a row: up to 16 elements a lane. What a row costs beside its elements (the reductions' shuffles,
+// the walk, the loop) is paid once per lane, so few lanes with much each beat many with little: against 16 bytes a
+// lane [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead of 51, and rows of 100 or 33
+// elements, which leave lanes of a wide group idle, [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead
+// of 63. 32 elements a lane are slower again (the registers leave one CTA an SM: 35 against 16 us at d = 64).
 template <typename E, int VW>
 int by_width(const FwdParams& p, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
-    if constexpr (VW > 1) {
-        if (nv <= 4) return launch<E, VW, 4, 1>(p, s);
-        if (nv <= 8) return launch<E, VW, 8, 1>(p, s);
-        if (nv <= 16) return launch<E, VW, 16, 1>(p, s);
-        if (nv <= 32) return launch<E, VW, 32, 1>(p, s);
-    }
-    if (nv <= 64) return launch<E, VW, 32, 2>(p, s);
-    if constexpr (VW > 1)
+    if constexpr (VW == 8) {
+        if (nv <= 2) return launch<E, VW, 2, 1>(p, s);
+        if (nv <= 4) return launch<E, VW, 2, 2>(p, s);
+        if (nv <= 8) return launch<E, VW, 4, 2>(p, s);
+        if (nv <= 16) return launch<E, VW, 8, 2>(p, s);
+        if (nv <= 32) return launch<E, VW, 16, 2>(p, s);
+        if (nv <= 64) return launch<E, VW, 32, 2>(p, s);
         if (nv <= 96) return launch<E, VW, 32, 3>(p, s);
-    if (nv <= 128) return launch<E, VW, 32, 4>(p, s);
-    if constexpr (VW == 4)
+        if (nv <= 128) return launch<E, VW, 32, 4>(p, s);
+    } else if constexpr (VW == 4) {
+        if (nv <= 4) return launch<E, VW, 2, 2>(p, s);
+        if (nv <= 8) return launch<E, VW, 4, 2>(p, s);
+        if (nv <= 12) return launch<E, VW, 4, 3>(p, s);
+        if (nv <= 16) return launch<E, VW, 4, 4>(p, s);
+        if (nv <= 32) return launch<E, VW, 8, 4>(p, s);
+        if (nv <= 64) return launch<E, VW, 16, 4>(p, s);
+        if (nv <= 96) return launch<E, VW, 32, 3>(p, s);
+        if (nv <= 128) return launch<E, VW, 32, 4>(p, s);
         if (nv <= 192) return launch<E, VW, 32, 6>(p, s);
-    if constexpr (VW * 256 <= kGnMaxD)
         if (nv <= 256) return launch<E, VW, 32, 8>(p, s);
-    if constexpr (VW == 1) return launch<E, VW, 32, 32>(p, s);
+    } else {
+        if (nv <= 16) return launch<E, VW, 4, 4>(p, s);
+        if (nv <= 32) return launch<E, VW, 8, 4>(p, s);
+        if (nv <= 48) return launch<E, VW, 8, 6>(p, s);
+        if (nv <= 64) return launch<E, VW, 8, 8>(p, s);
+        if (nv <= 128) return launch<E, VW, 16, 8>(p, s);
+        if (nv <= 256) return launch<E, VW, 32, 8>(p, s);
+        if (nv <= 1024) return launch<E, VW, 32, 32>(p, s);
+    }
     return 2;
 }
 

@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "falcon_gn.cuh"
 #include "sm103_ptx.cuh"
 
@@ -59,8 +61,12 @@ __device__ __forceinline__ void slope_all(int a, const float2 (&v)[P], float2 (&
     }
 }
 
+// CTAs that an SM is given: what the registers of the row's width allow.
+template <int VW, int NCH>
+constexpr int kPerSm = NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 2 : 1;
+
 template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
-__global__ void __launch_bounds__(kThreads, NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 2 : 1) gn_bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const __grid_constant__ BwdParams p) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     using Q = Row<VW, LPR, NCH, FULL>;
@@ -217,8 +223,10 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
     }
 }
 
+// Launches the row's width with `splits` (as many as the workspace has room for), or fewer if fewer CTAs run at once.
 template <typename E, int VW, int LPR, int NCH>
-int launch(BwdParams p, int splits, cudaStream_t s) {
+int launch(BwdParams p, int& splits, cudaStream_t s) {
+    splits = std::max(1, std::min(splits, kSms * kPerSm<VW, NCH> / p.H));
     set_step(p.s, (uint32_t)splits * (kThreads / LPR));
     const dim3 grid((unsigned)splits, (unsigned)p.H);
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
@@ -228,24 +236,42 @@ int launch(BwdParams p, int splits, cudaStream_t s) {
     return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, false>, grid, kThreads, s, p);
 }
 
+// Lanes and chunks of a row: up to 8 elements a lane, of fp32 up to 4. The sums of dw and db take twice an element's
+// registers, so the forward's 16 leave one CTA an SM (d = 64: 30.6 against 28.9 us for [8,12,2048,64] bf16), while
+// fewer elements on more lanes pay a row's fixed part more often: [8,12,1310,100] bf16 takes 32 us with 8 on 16
+// lanes, 45 with 4 on 32; [8,12,3971,33] 46 us with 6 on 8 lanes, 109 with 2 on 32.
 template <typename E, int VW>
-int by_width(const BwdParams& p, int splits, cudaStream_t s) {
+int by_width(const BwdParams& p, int& splits, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
-    if constexpr (VW > 1) {
+    if constexpr (VW * sizeof(E) == 16) {
+        if (nv <= 2) return launch<E, VW, 2, 1>(p, splits, s);
         if (nv <= 4) return launch<E, VW, 4, 1>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 8, 1>(p, splits, s);
         if (nv <= 16) return launch<E, VW, 16, 1>(p, splits, s);
         if (nv <= 32) return launch<E, VW, 32, 1>(p, splits, s);
-    }
-    if (nv <= 64) return launch<E, VW, 32, 2>(p, splits, s);
-    if constexpr (VW > 1)
-        if (nv <= 96) return launch<E, VW, 32, 3>(p, splits, s);
-    if (nv <= 128) return launch<E, VW, 32, 4>(p, splits, s);
-    if constexpr (VW == 4)
-        if (nv <= 192) return launch<E, VW, 32, 6>(p, splits, s);
-    if constexpr (VW * 256 <= kGnMaxD)
+    } else if constexpr (VW == 4) {
+        if (nv <= 4) return launch<E, VW, 2, 2>(p, splits, s);
+        if (nv <= 8) return launch<E, VW, 4, 2>(p, splits, s);
+        if (nv <= 16) return launch<E, VW, 8, 2>(p, splits, s);
+        if (nv <= 32) return launch<E, VW, 16, 2>(p, splits, s);
+    } else {
+        if (nv <= 16) return launch<E, VW, 4, 4>(p, splits, s);
+        if (nv <= 32) return launch<E, VW, 8, 4>(p, splits, s);
+        if (nv <= 48) return launch<E, VW, 8, 6>(p, splits, s);
+        if (nv <= 64) return launch<E, VW, 8, 8>(p, splits, s);
+        if (nv <= 128) return launch<E, VW, 16, 8>(p, splits, s);
         if (nv <= 256) return launch<E, VW, 32, 8>(p, splits, s);
-    if constexpr (VW == 1) return launch<E, VW, 32, 32>(p, splits, s);
+        return launch<E, VW, 32, 32>(p, splits, s);
+    }
+    if constexpr (VW > 1) {
+        if (nv <= 64) return launch<E, VW, 32, 2>(p, splits, s);
+        if (nv <= 96) return launch<E, VW, 32, 3>(p, splits, s);
+        if (nv <= 128) return launch<E, VW, 32, 4>(p, splits, s);
+    }
+    if constexpr (VW == 4) {
+        if (nv <= 192) return launch<E, VW, 32, 6>(p, splits, s);
+        if (nv <= 256) return launch<E, VW, 32, 8>(p, splits, s);
+    }
     return 2;
 }
 
@@ -285,7 +311,7 @@ int launch_gn_bwd(const GnArgs& a, cudaStream_t s) {
         p.s.B = 1;
         for (int k = 0; k < 5; ++k) p.s.st[k] = p.s.sb[k];
     }
-    const int splits = gn_bwd_splits(a.n);
+    int splits = gn_bwd_splits(a.n);
     int st;
     if (a.n.bf16)
         st = vw == 8   ? by_width<bf16, 8>(p, splits, s)
