@@ -8,9 +8,8 @@
 // steps over the tokens, the next row's loads on their way while it works on this one; neighbouring groups
 // have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
 //
-// What bounds it: issue slots at bf16 ([8,12,2048,64] with a SiLU gate: 16.8 us, 66 % of the copy rate,
-// [16,16,4096,64] 73 to 78 us, 76 to 82 %; 22 thread instructions per element, of which an SM has 33 at that rate),
-// memory at fp32 ([8,1,8192,768]: 101 us, 89 %).
+// What bounds it: issue slots at bf16 ([8,12,2048,64] with a SiLU gate: 15.9 us, 70 % of the copy rate,
+// [16,16,4096,64] 67 to 72 us, 82 to 89 %), memory at fp32 ([4,12,8192,64]: 46 us, 97 %).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -69,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
     ptx::pdl_launch_dependents();
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P, G = kThreads / LPR;
-    constexpr bool kAhead = NCH * VW <= 16;  // the registers take the next row too
+    constexpr bool kAhead = NCH * VW * sizeof(E) <= 64;  // the registers take the next row too
+    constexpr bool kHeld = NCH * VW <= 16;               // and weight and bias, else these come from the L1 cache
     const Q q = {(int)threadIdx.x % LPR, p.d};
     const uint32_t first = blockIdx.x * G, i = first + threadIdx.x / LPR;
     const uint32_t h = i % p.H;
@@ -99,8 +99,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
     if (kAhead) fetch();
     float2 w[P], bias[P];
     constexpr int FW = VW < 4 ? VW : 4;
-    q.template params<FW>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
-    q.template params<FW>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
+    auto params = [&] {
+        q.template params<FW>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
+        q.template params<FW>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
+    };
+    if (kHeld) params();
     // the CTA's first group has the first rows: all take as many turns as it has
     for (uint32_t r = first / p.H; r < p.rows; r += p.s.by) {
         if (!kAhead) fetch();
@@ -114,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
             if (kAhead) fetch();
         }
         q.normalise(x, p.inv_d, p.eps);
+        if (!kHeld) params();
 #pragma unroll
         for (int j = 0; j < P; ++j) x[j] = fma2(x[j], w[j], bias[j]);
         if constexpr (GATED) {
@@ -151,20 +155,32 @@ int launch(FwdParams p, cudaStream_t s) {
     return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, false>, dim3(grid), kThreads, s, p);
 }
 
-// Lanes and chunks of a row: up to 16 elements a lane. What a row costs beside its elements (the reductions' shuffles,
-// the walk, the loop) is paid once per lane, so few lanes with much each beat many with little: against 16 bytes a
-// lane [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead of 51, and rows of 100 or 33
-// elements, which leave lanes of a wide group idle, [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead
-// of 63. 32 elements a lane are slower again (the registers leave one CTA an SM: 35 against 16 us at d = 64).
+// Lanes and chunks of a row: 16 elements a lane, or 24 where that leaves fewer lanes idle. What a row costs beside its
+// elements (the reductions' shuffles, the walk, the loop) is paid once per lane, so few lanes with much each beat many
+// with little: against 16 bytes a lane [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead
+// of 51, and rows whose length is no power of two [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead of
+// 63, [4,1,32768,192] 26 instead of 31. 32 elements a lane leave one CTA an SM: 35 against 16 us at d = 64. Few rows
+// (up to two CTAs an SM at 16 bytes a lane) are over sooner with a lane's least to fetch: single tokens
+// [256,12,1,64] bf16 1.6 against 2.0 us, [2,12,256,64] 1.9 against 2.0.
 template <typename E, int VW>
 int by_width(const FwdParams& p, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
+    if constexpr (VW * sizeof(E) == 16) {
+        const unsigned __int128 few = 2 * kSms * kThreads / ((unsigned __int128)p.rows * p.H);  // lanes a row may take
+        if (nv > 2 && nv <= 4 && few >= 4) return launch<E, VW, 4, 1>(p, s);
+        if (nv > 4 && nv <= 8 && few >= 8) return launch<E, VW, 8, 1>(p, s);
+        if (nv > 8 && nv <= 16 && few >= 16) return launch<E, VW, 16, 1>(p, s);
+        if (nv > 16 && nv <= 32 && few >= 32) return launch<E, VW, 32, 1>(p, s);
+    }
     if constexpr (VW == 8) {
         if (nv <= 2) return launch<E, VW, 2, 1>(p, s);
         if (nv <= 4) return launch<E, VW, 2, 2>(p, s);
         if (nv <= 8) return launch<E, VW, 4, 2>(p, s);
+        if (nv <= 12) return launch<E, VW, 4, 3>(p, s);
         if (nv <= 16) return launch<E, VW, 8, 2>(p, s);
+        if (nv <= 24) return launch<E, VW, 8, 3>(p, s);
         if (nv <= 32) return launch<E, VW, 16, 2>(p, s);
+        if (nv <= 48) return launch<E, VW, 16, 3>(p, s);
         if (nv <= 64) return launch<E, VW, 32, 2>(p, s);
         if (nv <= 96) return launch<E, VW, 32, 3>(p, s);
         if (nv <= 128) return launch<E, VW, 32, 4>(p, s);
@@ -173,7 +189,9 @@ int by_width(const FwdParams& p, cudaStream_t s) {
         if (nv <= 8) return launch<E, VW, 4, 2>(p, s);
         if (nv <= 12) return launch<E, VW, 4, 3>(p, s);
         if (nv <= 16) return launch<E, VW, 4, 4>(p, s);
+        if (nv <= 24) return launch<E, VW, 8, 3>(p, s);
         if (nv <= 32) return launch<E, VW, 8, 4>(p, s);
+        if (nv <= 48) return launch<E, VW, 16, 3>(p, s);
         if (nv <= 64) return launch<E, VW, 16, 4>(p, s);
         if (nv <= 96) return launch<E, VW, 32, 3>(p, s);
         if (nv <= 128) return launch<E, VW, 32, 4>(p, s);

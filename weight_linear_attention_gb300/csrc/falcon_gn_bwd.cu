@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P;
     constexpr int G = kThreads / LPR;  // rows side by side
-    constexpr bool kAhead = NCH * VW <= 16;  // the registers take the next row too
+    constexpr bool kAhead = NCH * VW * sizeof(E) <= 64;  // the registers take the next row too
+    constexpr bool kHeld = NCH * VW <= 24;               // and weight and bias, else these come from the L1 cache
     __shared__ float part[kWarps][LPR * NCH * VW];
     const Q q = {(int)threadIdx.x % LPR, p.d};
     const uint32_t h = blockIdx.y;
@@ -102,9 +103,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
         }
     };
     if (kAhead) fetch();
+    constexpr int FW = VW < 4 ? VW : 4;
     float2 w[P], bias[P], aw[P], ab[P];
-    q.template params<1>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
-    q.template params<1>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
+    auto params = [&] {
+        q.template params<FW>(p.w ? p.w + (long long)h * p.d : nullptr, 1.f, w);
+        q.template params<FW>(p.b ? p.b + (long long)h * p.d : nullptr, 0.f, bias);
+    };
+    if (kHeld) params();
 #pragma unroll
     for (int i = 0; i < P; ++i) aw[i] = ab[i] = pair(0.f, 0.f);
     // the same number of turns for a whole CTA; the next row's loads are on their way while this one is worked on
@@ -121,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
             if (kAhead) fetch();
         }
         const float rstd = q.normalise(x, p.inv_d, p.eps);
+        if (!kHeld) params();
         if constexpr (GATED) {
             slope_all<P>(p.act, z, f, df);
 #pragma unroll
@@ -236,10 +242,11 @@ int launch(BwdParams p, int& splits, cudaStream_t s) {
     return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, false>, grid, kThreads, s, p);
 }
 
-// Lanes and chunks of a row: up to 8 elements a lane, of fp32 up to 4. The sums of dw and db take twice an element's
-// registers, so the forward's 16 leave one CTA an SM (d = 64: 30.6 against 28.9 us for [8,12,2048,64] bf16), while
-// fewer elements on more lanes pay a row's fixed part more often: [8,12,1310,100] bf16 takes 32 us with 8 on 16
-// lanes, 45 with 4 on 32; [8,12,3971,33] 46 us with 6 on 8 lanes, 109 with 2 on 32.
+// Lanes and chunks of a row: 8 elements a lane (of fp32 4) with two or three CTAs an SM, or 24 with one where that
+// leaves fewer lanes idle. The sums of dw and db take twice an element's registers, so the forward's 16 are slower (d =
+// 64: 30.6 against 28.9 us for [8,12,2048,64] bf16), while fewer elements on more lanes pay a row's fixed part more
+// often: [8,12,1310,100] bf16 takes 32 us with 8 on 16 lanes, 45 with 4 on 32; [8,12,3971,33] 46 us with 6 on 8
+// lanes, 109 with 2 on 32; [4,1,32768,192] 49 us with 24 on 8 lanes, 60 with 8 on 32.
 template <typename E, int VW>
 int by_width(const BwdParams& p, int& splits, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
@@ -247,8 +254,12 @@ int by_width(const BwdParams& p, int& splits, cudaStream_t s) {
         if (nv <= 2) return launch<E, VW, 2, 1>(p, splits, s);
         if (nv <= 4) return launch<E, VW, 4, 1>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 8, 1>(p, splits, s);
+        if (VW == 8 && nv <= 12) return launch<E, VW, 4, 3>(p, splits, s);
         if (nv <= 16) return launch<E, VW, 16, 1>(p, splits, s);
+        if (VW == 8 && nv <= 24) return launch<E, VW, 8, 3>(p, splits, s);
         if (nv <= 32) return launch<E, VW, 32, 1>(p, splits, s);
+        if (nv <= 48) return launch<E, VW, 16, 3>(p, splits, s);
+        if (VW == 4 && nv <= 64) return launch<E, VW, 16, 4>(p, splits, s);
     } else if constexpr (VW == 4) {
         if (nv <= 4) return launch<E, VW, 2, 2>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 4, 2>(p, splits, s);
@@ -311,6 +322,7 @@ int launch_gn_bwd(const GnArgs& a, cudaStream_t s) {
         p.s.B = 1;
         for (int k = 0; k < 5; ++k) p.s.st[k] = p.s.sb[k];
     }
+    if (reinterpret_cast<uintptr_t>(a.w) % 16 || reinterpret_cast<uintptr_t>(a.b) % 16) vw = 1;
     int splits = gn_bwd_splits(a.n);
     int st;
     if (a.n.bf16)
