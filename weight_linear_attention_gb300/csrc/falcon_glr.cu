@@ -237,18 +237,27 @@ template <typename E, int LC, int R, int CB>
 __device__ __forceinline__ void copy_rows(const Params& p, uint32_t dst, uint8_t* dst_p, const void* base, int k,
                                           const Cursor& c, int n, int t0, int sign, int shift) {
     constexpr int RB = Geo<LC, R>::kChans * sizeof(E), PAD = Geo<LC, R>::kSegs > 1 ? RB : 0;  // as Ring's
-    constexpr int CPR = RB / CB, N = Geo<LC, R>::kRows * CPR / 32, EPC = CB / sizeof(E);
-    const int lane = threadIdx.x & 31;
-    const long long off = (long long)c.b * p.sb[k] + (long long)c.h * p.sh[k] + c.c0;
+    constexpr int CPR = RB / CB, EPC = CB / sizeof(E);
+    constexpr int RPS = CPR < 32 ? 32 / CPR : 1, CPL = CPR < 32 ? 1 : CPR / 32;  // rows a step, columns a lane
+    const int lane = threadIdx.x & 31, row0 = lane / CPR % RPS, col0 = lane % CPR;
+    int t = t0 + sign * (n + row0) + shift;
+    const int left = c.len - n - row0;  // rows from this lane's first to the end
+    const E* src = static_cast<const E*>(base) + ((long long)c.b * p.sb[k] + (long long)c.h * p.sh[k] + c.c0 +
+                                                  t * p.st[k] + col0 * EPC);
+    const long long inc = sign * RPS * p.st[k];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int q = lane + 32 * j, row = q / CPR, col = q % CPR;
-        const int t = t0 + sign * (n + row) + shift;
-        const bool in = n + row < c.len && t >= 0 && c.c0 + col * EPC < p.d;
-        const long long at = in ? off + t * p.st[k] + col * EPC : 0;
-        const uint32_t o = row * RB + row / R * PAD + col * CB;
-        if constexpr (CB >= 4) copy_async<CB>(dst + o, static_cast<const E*>(base) + at, in);
-        else *reinterpret_cast<uint16_t*>(dst_p + o) = in ? static_cast<const uint16_t*>(base)[at] : (uint16_t)0;
+    for (int r = 0; r < Geo<LC, R>::kRows; r += RPS) {
+        const bool row_in = r < left && t >= 0;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const bool in = row_in && c.c0 + (col0 + 32 * j) * EPC < p.d;
+            const E* at = in ? src + 32 * j * EPC : static_cast<const E*>(base);
+            const uint32_t o = (r + row0) * RB + (r + row0) / R * PAD + (col0 + 32 * j) * CB;
+            if constexpr (CB >= 4) copy_async<CB>(dst + o, at, in);
+            else *reinterpret_cast<uint16_t*>(dst_p + o) = in ? *reinterpret_cast<const uint16_t*>(at) : (uint16_t)0;
+        }
+        src += inc;
+        t += sign * RPS;
     }
 }
 __device__ __forceinline__ float2 ld_pair(const float* s) { return *reinterpret_cast<const float2*>(s); }
