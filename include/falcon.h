@@ -263,7 +263,9 @@ typedef enum {
 
 /*
  * falcon_glr_fwd — gated linear recurrence: per channel h_t = a_t h_{t-1} + u_t, out_t = h_t.
- * A gate g = -inf (a = 0) starts a new document in the middle of a sequence.
+ * A gate g = -inf (a = 0) starts a new document in the middle of a sequence. A decay g > 0 (a > 1) is taken as it is;
+ * products of consecutive a are formed over up to a few thousand tokens, so where one overflows fp32 the state is
+ * inf or NaN even if it would have stayed 0.
  *   x, g      [B,H,T,d] dtype         input and gate
  *   h0        fp32 [B,H,d] or NULL (zero state)
  *   lengths   see above

@@ -3,7 +3,7 @@
 // y = act(n), or n act(z).
 //
 // A memory-bound transposition with arithmetic on the way: 2 (3 with a gate) tensors' bytes per element.
-// LPR lanes hold a row in registers (16 bytes a lane), so the row is read once and the variance is that
+// LPR lanes hold a row in registers (16 or 24 elements a lane), so the row is read once and the variance is that
 // of the centred values. A group of lanes keeps one head, so that weight and bias stay in registers, and
 // steps over the tokens, the next row's loads on their way while it works on this one; neighbouring groups
 // have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
