@@ -5,11 +5,11 @@
 // A memory-bound transposition with arithmetic on the way: 2 (3 with a gate) tensors' bytes per element.
 // LPR lanes hold a row in registers (16 or 24 elements a lane), so the row is read once and the variance is that
 // of the centred values. A group of lanes keeps one head, so that weight and bias stay in registers, and
-// steps over the tokens, the next row's loads on their way while it works on this one; neighbouring groups
+// steps over the tokens, the next rows' loads on their way while it works on this one; neighbouring groups
 // have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
 //
-// What bounds it: issue slots at bf16 ([8,12,2048,64] with a SiLU gate: 15.9 us, 70 % of the copy rate,
-// [16,16,4096,64] 67 to 72 us, 82 to 89 %), memory at fp32 ([4,12,8192,64]: 46 us, 97 %).
+// What bounds it: memory ([16,16,4096,64] bf16 with a SiLU gate: 60 us, 99 % of the copy rate; [4,12,8192,64] fp32 46
+// us, 97 %); at [8,12,2048,64] bf16 (13.4 us, 83 %) filling and emptying; GELU's issue slots (14.8 us, 50 %, ungated).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,41 +62,31 @@ __device__ __forceinline__ void act_all(int a, const float2 (&v)[P], float2 (&f)
 template <int VW, int NCH>
 constexpr int kPerSm = NCH * VW <= 4 ? 4 : NCH * VW <= 8 ? 3 : NCH * VW <= 24 ? 2 : 1;
 
+// Bytes of a row of the CTA's groups, and the rows that its ring holds (0: registers). The ring keeps twice the bytes
+// on their way that the registers have room for: [16,16,4096,64] bf16 60 instead of 72 us, [8,12,2048,64] 13.4 instead of
+// 16.0. fp32 has as many on their way in registers ([4,12,8192,64] 46 us, with a ring 47); with 24 elements a lane the ring's
+// shared memory costs more than it gains ([4,1,8192,768] 28 against 26 us).
+template <typename E, int VW, int NCH, bool GATED>
+constexpr int kRow = (GATED ? 2 : 1) * NCH * VW * (int)sizeof(E) * kThreads;
+template <typename E, int VW, int NCH, bool GATED>
+constexpr int kRing =
+    VW == 1 || sizeof(E) == 4 || NCH * VW > 16 ? 0 : depth(kRow<E, VW, NCH, GATED>, kPerSm<VW, NCH>, 0);
+
 template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const __grid_constant__ FwdParams p) {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P, G = kThreads / LPR;
-    constexpr bool kAhead = NCH * VW * sizeof(E) <= 64;  // the registers take the next row too
-    constexpr bool kHeld = NCH * VW <= 16;               // and weight and bias, else these come from the L1 cache
+    constexpr bool kHeld = NCH * VW <= 16;  // weight and bias stay in registers, else they come from the L1 cache
+    using V = Pack<E, VW>;
+    constexpr int CB = LPR * VW * sizeof(E), D = kRing<E, VW, NCH, GATED>;
+    extern __shared__ __align__(16) uint8_t ring[];
     const Q q = {(int)threadIdx.x % LPR, p.d};
     const uint32_t first = blockIdx.x * G, i = first + threadIdx.x / LPR;
     const uint32_t h = i % p.H;
-    const int c0 = q.chan(0) * (int)sizeof(E);
-    constexpr int CB = LPR * VW * sizeof(E);  // from one chunk of a lane to its next
-    using V = Pack<E, VW>;
-    V px[NCH], pz[GATED ? NCH : 1];
-    Walk<3> at;
-    at.start(p.s, i / p.H, h, c0);
-    bool in;  // the row at hand lies inside its sequence; others are worked on with what the registers hold
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-        zero(px[k]);
-        if (GATED) zero(pz[k]);
-    }
-    auto fetch = [&] {
-        in = at.exists(p.s);
-        if (in && p.lengths) in = (int)at.t < p.lengths[at.b];
-#pragma unroll
-        for (int k = 0; k < NCH; ++k) {
-            if (in && q.live(k)) {
-                px[k] = at.template get<V>(kX, k * CB);
-                if (GATED) pz[k] = at.template get<V>(kZ, k * CB);
-            }
-        }
-    };
-    if (kAhead) fetch();
+    Rows<E, VW, LPR, NCH, FULL, GATED, 2, 3, kThreads, D, NCH * VW * sizeof(E) <= 64> row;
+    row.start(q, p.s, p.lengths, i / p.H, h, ring);
     float2 w[P], bias[P];
     constexpr int FW = VW < 4 ? VW : 4;
     auto params = [&] {
@@ -106,16 +96,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
     if (kHeld) params();
     // the CTA's first group has the first rows: all take as many turns as it has
     for (uint32_t r = first / p.H; r < p.rows; r += p.s.by) {
-        if (!kAhead) fetch();
         float2 x[P], z[GATED ? P : 1], f[P];
-        q.get(px, x);
-        if constexpr (GATED) q.get(pz, z);
-        const bool mine = at.exists(p.s), was_in = in;
-        char* const out = at.at[kY];
-        if (r + p.s.by < p.rows) {
-            at.step(p.s);
-            if (kAhead) fetch();
-        }
+        row.wait(q, p.s, p.lengths);
+        row.get(q, kX, x);
+        if constexpr (GATED) row.get(q, kZ, z);
+        const bool mine = row.mine, in = row.in;
+        char* const out = row.out[0];
+        if (D > 0 || r + p.s.by < p.rows) row.next(q, p.s, p.lengths);
         q.normalise(x, p.inv_d, p.eps);
         if (!kHeld) params();
 #pragma unroll
@@ -131,11 +118,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_fwd_kernel(const
         for (int k = 0; k < NCH; ++k) {
             if (!mine || !q.live(k)) continue;
             V po;
-            if (was_in) po = q.template put<E>(f, k);
+            if (in) po = q.template put<E>(f, k);
             else zero(po);
             *reinterpret_cast<V*>(out + k * CB) = po;
         }
     }
+}
+
+template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
+int run(const FwdParams& p, uint32_t grid, cudaStream_t s) {
+    constexpr int kBytes = kRing<E, VW, NCH, GATED> * kRow<E, VW, NCH, GATED>;
+    return launch_ahead<gn_fwd_kernel<E, VW, LPR, NCH, GATED, FULL>>(dim3(grid), kThreads, kBytes, s, p);
 }
 
 template <typename E, int VW, int LPR, int NCH>
@@ -149,15 +142,13 @@ int launch(FwdParams p, cudaStream_t s) {
     const uint32_t grid = most <= slots ? (most + unit - 1) / unit * unit : std::max(slots / unit, 1u) * unit;
     set_step(p.s, (uint32_t)((unsigned long long)grid * G / p.H));
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
-    if (gated && full) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, true>, dim3(grid), kThreads, s, p);
-    if (gated) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, true, false>, dim3(grid), kThreads, s, p);
-    if (full) return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, true>, dim3(grid), kThreads, s, p);
-    return launch_ahead(gn_fwd_kernel<E, VW, LPR, NCH, false, false>, dim3(grid), kThreads, s, p);
+    if (gated) return full ? run<E, VW, LPR, NCH, true, true>(p, grid, s) : run<E, VW, LPR, NCH, true, false>(p, grid, s);
+    return full ? run<E, VW, LPR, NCH, false, true>(p, grid, s) : run<E, VW, LPR, NCH, false, false>(p, grid, s);
 }
 
 // Lanes and chunks of a row: 16 elements a lane, or 24 where that leaves fewer lanes idle. What a row costs beside its
 // elements (the reductions' shuffles, the walk, the loop) is paid once per lane, so few lanes with much each beat many
-// with little: against 16 bytes a lane [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead
+// with little: against 16 bytes a lane, both without the ring, [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead
 // of 51, and rows whose length is no power of two [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead of
 // 63, [4,1,32768,192] 26 instead of 31. 32 elements a lane leave one CTA an SM: 35 against 16 us at d = 64. Few rows
 // (up to two CTAs an SM at 16 bytes a lane) are over sooner with a lane's least to fetch: single tokens

@@ -3,6 +3,9 @@
 // with elements (l + LPR k) VW .. + VW - 1 for k < NCH.
 #pragma once
 
+#include <atomic>
+#include <type_traits>
+
 #include "falcon_seq.cuh"
 #include "falcon_seq.h"
 #include "sm103_ptx.cuh"
@@ -183,52 +186,187 @@ inline void set_step(Tensors<K>& s, uint32_t by) {
         s.wrap[k] = s.sb[k] - (long long)T * s.st[k];
     }
 }
-template <int K>
+// A place in the N tensors from number FIRST on.
+template <int FIRST, int N>
 struct Walk {
     uint32_t b, t;
-    char* at[K];
+    char* at[N];
     // row r of head h, byte `c` of it
+    template <int K>
     __device__ __forceinline__ void start(const Tensors<K>& s, uint32_t r, uint32_t h, int c) {
         b = div(r, s.tokens);
         t = r - b * s.tokens.d;
 #pragma unroll
-        for (int k = 0; k < K; ++k) at[k] = s.base[k] + (b * s.sb[k] + h * s.sh[k] + t * s.st[k] + c);
+        for (int k = 0; k < N; ++k)
+            at[k] = s.base[FIRST + k] + (b * s.sb[FIRST + k] + h * s.sh[FIRST + k] + t * s.st[FIRST + k] + c);
     }
+    template <int K>
     __device__ __forceinline__ void step(const Tensors<K>& s) {
         b += s.qb;
         t += s.qt;
 #pragma unroll
-        for (int k = 0; k < K; ++k) at[k] += s.inc[k];
+        for (int k = 0; k < N; ++k) at[k] += s.inc[FIRST + k];
         if (t >= s.tokens.d) {
             ++b;
             t -= s.tokens.d;
 #pragma unroll
-            for (int k = 0; k < K; ++k) at[k] += s.wrap[k];
+            for (int k = 0; k < N; ++k) at[k] += s.wrap[FIRST + k];
         }
     }
+    template <int K>
     __device__ __forceinline__ bool exists(const Tensors<K>& s) const { return b < s.B; }
-    template <typename P>
-    __device__ __forceinline__ P get(int k, int off) const {
-        return *reinterpret_cast<const P*>(at[k] + off);
+    // the row lies inside its sequence
+    template <int K>
+    __device__ __forceinline__ bool in(const Tensors<K>& s, const int32_t* lengths) const {
+        return exists(s) && (!lengths || (int)t < lengths[b]);
+    }
+};
+
+// A group's rows: the first NT of K tensors (all where GATED, else without number 1) are read ahead of their use, into
+// a ring of D rows a thread in shared memory, each thread's bytes its own, or (D = 0) into registers, one row ahead where
+// AHEAD; the others are written. Rows outside their sequence are not read, their place holds what was there before.
+// Channels that do not exist are zero.
+template <typename E, int VW, int LPR, int NCH, bool FULL, bool GATED, int NT, int K, int THREADS, int D, bool AHEAD>
+struct Rows {
+    using V = Pack<E, VW>;
+    using Q = Row<VW, LPR, NCH, FULL>;
+    using Held = std::conditional_t<sizeof(V) == 2, uint32_t, V>;  // halves of registers would wait for their loads
+    static constexpr int CB = LPR * VW * sizeof(E);                // from one chunk of a lane to its next
+    static constexpr int kRow = (GATED ? NT : NT - 1) * NCH * THREADS;  // packs of a row of the ring
+    Walk<0, D ? NT : K> at;
+    Walk<NT, K - NT> dst;  // with a ring: the row at hand
+    Held reg[D ? 1 : NT][D ? 1 : NCH];
+    V* ring;
+    uint32_t to;
+    int head;           // the ring's row at hand
+    bool ahead_in;      // the row fetched last lies inside its sequence
+    bool mine, in;      // the row at hand exists, and lies inside its sequence
+    char* out[K - NT];  // where it is written
+
+    static __device__ __forceinline__ constexpr bool has(int k) { return GATED || k != 1; }
+    static __device__ __forceinline__ constexpr int slot(int k, int j) {
+        return ((GATED || k == 0 ? k : k - 1) * NCH + j) * THREADS;
+    }
+    __device__ __forceinline__ void fetch(const Q& q, const Tensors<K>& s, const int32_t* lengths, int row) {
+        ahead_in = at.in(s, lengths);
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            if (ahead_in && q.live(j)) {
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    if (!has(k)) continue;
+                    const char* from = at.at[k] + j * CB;
+                    if constexpr (D > 0) copy_async<sizeof(V)>(to + (row * kRow + slot(k, j)) * (int)sizeof(V), from, true);
+                    else if constexpr (sizeof(V) == 2) reg[k][j] = *reinterpret_cast<const uint16_t*>(from);
+                    else reg[k][j] = *reinterpret_cast<const V*>(from);
+                }
+            }
+        }
+        if constexpr (D > 0) {
+            at.step(s);
+            copy_commit();
+        }
+    }
+    __device__ __forceinline__ void start(const Q& q, const Tensors<K>& s, const int32_t* lengths, uint32_t r, uint32_t h,
+                                          void* shared) {
+        const int c0 = q.chan(0) * (int)sizeof(E);
+        at.start(s, r, h, c0);
+        if constexpr (D > 0) {
+            dst.start(s, r, h, c0);
+            ring = static_cast<V*>(shared) + threadIdx.x;
+            to = ptx::smem_u32(ring);
+            if (!FULL) {
+                V none;
+                zero(none);
+#pragma unroll 1
+                for (int i = 0; i < D * kRow / THREADS; ++i) ring[i * THREADS] = none;
+            }
+            head = 0;
+#pragma unroll
+            for (int i = 0; i < D - 1; ++i) fetch(q, s, lengths, i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int j = 0; j < NCH; ++j) reg[k][j] = Held{};
+            if (AHEAD) fetch(q, s, lengths, 0);
+        }
+    }
+    // Waits for the row at hand.
+    __device__ __forceinline__ void wait(const Q& q, const Tensors<K>& s, const int32_t* lengths) {
+        if constexpr (D > 0) {
+            copy_wait<D - 2>();
+            mine = dst.exists(s);
+            in = dst.in(s, lengths);
+#pragma unroll
+            for (int k = 0; k < K - NT; ++k) out[k] = dst.at[k];
+        } else {
+            if (!AHEAD) fetch(q, s, lengths, 0);
+            mine = at.exists(s);
+            in = ahead_in;
+#pragma unroll
+            for (int k = 0; k < K - NT; ++k) out[k] = at.at[NT + k];
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void get(const Q& q, int k, float2 (&v)[P]) const {
+        V w[NCH];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            if constexpr (D > 0) w[j] = ring[head * kRow + slot(k, j)];
+            else if constexpr (sizeof(V) == 2) w[j].w = (uint16_t)reg[k][j];
+            else w[j] = reg[k][j];
+        }
+        q.get(w, v);
+    }
+    // Behind the row's `get`s: on to the next, or the one that its place in the ring is for.
+    __device__ __forceinline__ void next(const Q& q, const Tensors<K>& s, const int32_t* lengths) {
+        if constexpr (D > 0) {
+            fetch(q, s, lengths, head == 0 ? D - 1 : head - 1);
+            head = head == D - 1 ? 0 : head + 1;
+            dst.step(s);
+        } else {
+            at.step(s);
+            if (AHEAD) fetch(q, s, lengths, 0);
+        }
     }
 };
 
 constexpr int kSms = 152;
 
-// Launches with programmatic stream serialisation: the kernel's launch overlaps the end of the one before it, so
+constexpr int kMaxDevices = 64;
+constexpr int kSmem = 220 * 1024;  // of an SM, for the CTAs that it is given
+
+// The rows a ring has: three (more gain nothing: 60.5 us either way for [16,16,4096,64] bf16 forward), or two where
+// that is too much for the shared memory of `ctas` CTAs with `other` bytes besides.
+constexpr int depth(int row, int ctas, int other) {
+    return ctas * (3 * row + other) <= kSmem ? 3 : ctas * (2 * row + other) <= kSmem ? 2 : 0;
+}
+
+// Launches kernel FN with programmatic stream serialisation: the launch overlaps the end of the kernel before it, so
 // it waits (pdl_wait) before it reads or writes.
-template <typename... Args>
-inline int launch_ahead(void (*fn)(Args...), dim3 grid, int threads, cudaStream_t s, Args... args) {
+template <auto FN, typename... Args>
+inline int launch_ahead(dim3 grid, int threads, int bytes, cudaStream_t s, Args... args) {
+    if (bytes > 0) {
+        static std::atomic<bool> ready[kMaxDevices];  // the kernel may have `bytes` of shared memory there
+        int dev;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 4;
+        if (!ready[dev].load(std::memory_order_acquire)) {
+            if (cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return 4;
+            ready[dev].store(true, std::memory_order_release);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? 0 : 4;
+    return cudaLaunchKernelEx(&cfg, FN, args...) == cudaSuccess ? 0 : 4;
 }
 
 }  // namespace gn

@@ -7,9 +7,8 @@
 // in shared memory and leaves one partial sum per split of the rows, which a second, small kernel adds
 // in the order of the splits. Every order depends on the sizes alone: no atomics.
 //
-// What bounds it: issue slots at bf16 ([8,12,1024,64] with a SiLU gate: 17 us with the sums' kernel, 55 % of the
-// copy rate, [16,16,4096,64] 127 us, 78 %; 39 thread instructions per element, of which an SM has 55 at that rate),
-// memory at fp32 ([4,12,8192,64]: 71 us, 84 %).
+// What bounds it: memory ([16,16,4096,64] bf16 with a SiLU gate: 104 us, 95 % of the copy rate; [4,12,8192,64] fp32
+// with a gate 82 us, 91 %); at [8,12,1024,64] bf16 (14.9 us with the sums' kernel, 62 %) filling, emptying and the sums.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -65,6 +64,16 @@ __device__ __forceinline__ void slope_all(int a, const float2 (&v)[P], float2 (&
 template <int VW, int NCH>
 constexpr int kPerSm = NCH * VW <= 4 ? 3 : NCH * VW <= 8 ? 2 : 1;
 
+// Bytes of a row of the CTA's groups, and the rows that its ring holds (0: registers). The ring keeps twice the bytes
+// on their way that the registers have room for: [16,16,4096,64] bf16 104 instead of 128 us, [8,12,1024,64] 14.9 instead
+// of 17.1. fp32 has as many on their way in registers up to 16 elements a lane ([4,12,8192,64] 82 us, with a ring 87).
+template <typename E, int VW, int NCH, bool GATED>
+constexpr int kRow = (GATED ? 3 : 2) * NCH * VW * (int)sizeof(E) * kThreads;
+template <typename E, int VW, int LPR, int NCH, bool GATED>
+constexpr int kRing = VW == 1 || (sizeof(E) == 4 && NCH * VW < 16)
+                          ? 0
+                          : depth(kRow<E, VW, NCH, GATED>, kPerSm<VW, NCH>, kWarps* LPR* NCH* VW * (int)sizeof(float));
+
 template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const __grid_constant__ BwdParams p) {
     ptx::pdl_wait();
@@ -72,37 +81,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
     using Q = Row<VW, LPR, NCH, FULL>;
     constexpr int P = Q::P;
     constexpr int G = kThreads / LPR;  // rows side by side
-    constexpr bool kAhead = NCH * VW * sizeof(E) <= 64;  // the registers take the next row too
-    constexpr bool kHeld = NCH * VW <= 24;               // and weight and bias, else these come from the L1 cache
+    constexpr bool kHeld = NCH * VW <= 24;  // weight and bias stay in registers, else they come from the L1 cache
+    using V = Pack<E, VW>;
+    constexpr int CB = LPR * VW * sizeof(E), D = kRing<E, VW, LPR, NCH, GATED>;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float part[kWarps][LPR * NCH * VW];
     const Q q = {(int)threadIdx.x % LPR, p.d};
-    const uint32_t h = blockIdx.y;
-    const int c0 = q.chan(0) * (int)sizeof(E);
-    constexpr int CB = LPR * VW * sizeof(E);  // from one chunk of a lane to its next
-    using V = Pack<E, VW>;
-    V px[NCH], pz[GATED ? NCH : 1], pd[NCH];
-    Walk<5> at;
-    at.start(p.s, blockIdx.x * G + threadIdx.x / LPR, h, c0);
-    bool in;  // the row at hand lies inside its sequence; others are worked on with what the registers hold
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-        zero(px[k]);
-        zero(pd[k]);
-        if (GATED) zero(pz[k]);
-    }
-    auto fetch = [&] {
-        in = at.exists(p.s);
-        if (in && p.lengths) in = (int)at.t < p.lengths[at.b];
-#pragma unroll
-        for (int k = 0; k < NCH; ++k) {
-            if (in && q.live(k)) {
-                px[k] = at.template get<V>(kX, k * CB);
-                pd[k] = at.template get<V>(kDy, k * CB);
-                if (GATED) pz[k] = at.template get<V>(kZ, k * CB);
-            }
-        }
-    };
-    if (kAhead) fetch();
+    const uint32_t h = blockIdx.y, i0 = blockIdx.x * G + threadIdx.x / LPR;
+    Rows<E, VW, LPR, NCH, FULL, GATED, 3, 5, kThreads, D, NCH * VW * sizeof(E) <= 64> row;
+    row.start(q, p.s, p.lengths, i0, h, ring);
     constexpr int FW = VW < 4 ? VW : 4;
     float2 w[P], bias[P], aw[P], ab[P];
     auto params = [&] {
@@ -114,17 +101,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
     for (int i = 0; i < P; ++i) aw[i] = ab[i] = pair(0.f, 0.f);
     // the same number of turns for a whole CTA; the next row's loads are on their way while this one is worked on
     for (uint32_t r = blockIdx.x * G; r < p.rows; r += p.s.by) {
-        if (!kAhead) fetch();
         float2 x[P], dn[P], f[P], df[P], z[GATED ? P : 1];
-        q.get(px, x);
-        q.get(pd, dn);
-        if constexpr (GATED) q.get(pz, z);
-        const bool mine = at.exists(p.s), was_in = in;
-        char *const to_x = at.at[kDx], *const to_z = at.at[kDz];
-        if (r + p.s.by < p.rows) {
-            at.step(p.s);
-            if (kAhead) fetch();
-        }
+        row.wait(q, p.s, p.lengths);
+        row.get(q, kX, x);
+        row.get(q, kDy, dn);
+        if constexpr (GATED) row.get(q, kZ, z);
+        const bool mine = row.mine, in = row.in;
+        char *const to_x = row.out[0], *const to_z = row.out[1];
+        if (D > 0 || r + p.s.by < p.rows) row.next(q, p.s, p.lengths);
         const float rstd = q.normalise(x, p.inv_d, p.eps);
         if (!kHeld) params();
         if constexpr (GATED) {
@@ -138,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
             for (int k = 0; k < NCH; ++k)
                 if (mine && q.live(k)) {
                     V po;
-                    if (was_in) po = q.template put<E>(df, k);
+                    if (in) po = q.template put<E>(df, k);
                     else zero(po);
                     *reinterpret_cast<V*>(to_z + k * CB) = po;
                 }
@@ -151,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
             for (int i = 0; i < P; ++i) dn[i] = mul2(dn[i], df[i]);
         }
         float2 s1 = pair(0.f, 0.f), s2 = s1;
-        if (was_in) {
+        if (in) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 aw[i] = fma2(dn[i], x[i], aw[i]);
@@ -172,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<VW, NCH>) gn_bwd_kernel(const
         for (int k = 0; k < NCH; ++k)
             if (mine && q.live(k)) {
                 V po;
-                if (was_in) po = q.template put<E>(dn, k);
+                if (in) po = q.template put<E>(dn, k);
                 else zero(po);
                 *reinterpret_cast<V*>(to_x + k * CB) = po;
             }
@@ -229,6 +213,12 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
     }
 }
 
+template <typename E, int VW, int LPR, int NCH, bool GATED, bool FULL>
+int run(const BwdParams& p, dim3 grid, cudaStream_t s) {
+    constexpr int kBytes = kRing<E, VW, LPR, NCH, GATED> * kRow<E, VW, NCH, GATED>;
+    return launch_ahead<gn_bwd_kernel<E, VW, LPR, NCH, GATED, FULL>>(grid, kThreads, kBytes, s, p);
+}
+
 // Launches the row's width with `splits` (as many as the workspace has room for), or fewer if fewer CTAs run at once.
 template <typename E, int VW, int LPR, int NCH>
 int launch(BwdParams p, int& splits, cudaStream_t s) {
@@ -236,10 +226,8 @@ int launch(BwdParams p, int& splits, cudaStream_t s) {
     set_step(p.s, (uint32_t)splits * (kThreads / LPR));
     const dim3 grid((unsigned)splits, (unsigned)p.H);
     const bool gated = p.s.base[kZ] != nullptr, full = p.d == VW * LPR * NCH;
-    if (gated && full) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, true, true>, grid, kThreads, s, p);
-    if (gated) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, true, false>, grid, kThreads, s, p);
-    if (full) return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, true>, grid, kThreads, s, p);
-    return launch_ahead(gn_bwd_kernel<E, VW, LPR, NCH, false, false>, grid, kThreads, s, p);
+    if (gated) return full ? run<E, VW, LPR, NCH, true, true>(p, grid, s) : run<E, VW, LPR, NCH, true, false>(p, grid, s);
+    return full ? run<E, VW, LPR, NCH, false, true>(p, grid, s) : run<E, VW, LPR, NCH, false, false>(p, grid, s);
 }
 
 // Lanes and chunks of a row: 8 elements a lane (of fp32 4) with two or three CTAs an SM, or 24 with one where that
@@ -254,12 +242,15 @@ int by_width(const BwdParams& p, int& splits, cudaStream_t s) {
         if (nv <= 2) return launch<E, VW, 2, 1>(p, splits, s);
         if (nv <= 4) return launch<E, VW, 4, 1>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 8, 1>(p, splits, s);
-        if (VW == 8 && nv <= 12) return launch<E, VW, 4, 3>(p, splits, s);
+        if constexpr (VW == 8)
+            if (nv <= 12) return launch<E, VW, 4, 3>(p, splits, s);
         if (nv <= 16) return launch<E, VW, 16, 1>(p, splits, s);
-        if (VW == 8 && nv <= 24) return launch<E, VW, 8, 3>(p, splits, s);
+        if constexpr (VW == 8)
+            if (nv > 16 && nv <= 24) return launch<E, VW, 8, 3>(p, splits, s);
         if (nv <= 32) return launch<E, VW, 32, 1>(p, splits, s);
         if (nv <= 48) return launch<E, VW, 16, 3>(p, splits, s);
-        if (VW == 4 && nv <= 64) return launch<E, VW, 16, 4>(p, splits, s);
+        if constexpr (VW == 4)
+            if (nv <= 64) return launch<E, VW, 16, 4>(p, splits, s);
     } else if constexpr (VW == 4) {
         if (nv <= 4) return launch<E, VW, 2, 2>(p, splits, s);
         if (nv <= 8) return launch<E, VW, 4, 2>(p, splits, s);
@@ -333,8 +324,8 @@ int launch_gn_bwd(const GnArgs& a, cudaStream_t s) {
         st = vw == 4 ? by_width<float, 4>(p, splits, s) : by_width<float, 1>(p, splits, s);
     if (st != 0 || !a.ws) return st;
     const long long n = a.n.H * a.n.d;
-    return launch_ahead(gn_sum_kernel, dim3((unsigned)((2 * n + kSumChannels - 1) / kSumChannels)),
-                        kSumChannels * kSumSlices, s, (const float*)a.ws, splits, n, a.dw, a.db);
+    return launch_ahead<gn_sum_kernel>(dim3((unsigned)((2 * n + kSumChannels - 1) / kSumChannels)),
+                                       kSumChannels * kSumSlices, 0, s, (const float*)a.ws, splits, n, a.dw, a.db);
 }
 
 }  // namespace falcon
