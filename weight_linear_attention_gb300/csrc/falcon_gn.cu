@@ -63,9 +63,9 @@ template <int VW, int NCH>
 constexpr int kPerSm = NCH * VW <= 4 ? 4 : NCH * VW <= 8 ? 3 : NCH * VW <= 24 ? 2 : 1;
 
 // Bytes of a row of the CTA's groups, and the rows that its ring holds (0: registers). The ring keeps twice the bytes
-// on their way that the registers have room for: [16,16,4096,64] bf16 60 instead of 72 us, [8,12,2048,64] 13.4 instead of
-// 16.0. fp32 has as many on their way in registers ([4,12,8192,64] 46 us, with a ring 47); with 24 elements a lane the ring's
-// shared memory costs more than it gains ([4,1,8192,768] 28 against 26 us).
+// on their way that the registers have room for: [16,16,4096,64] bf16 60 instead of 72 us, [8,12,2048,64] 13.4 instead
+// of 16.0. fp32 has as many on their way in registers ([4,12,8192,64] 46 us, with a ring 47); with 24 elements a lane
+// the ring's shared memory costs more than it gains ([4,1,8192,768] 28 against 26 us).
 template <typename E, int VW, int NCH, bool GATED>
 constexpr int kRow = (GATED ? 2 : 1) * NCH * VW * (int)sizeof(E) * kThreads;
 template <typename E, int VW, int NCH, bool GATED>
@@ -148,8 +148,8 @@ int launch(FwdParams p, cudaStream_t s) {
 
 // Lanes and chunks of a row: 16 elements a lane, or 24 where that leaves fewer lanes idle. What a row costs beside its
 // elements (the reductions' shuffles, the walk, the loop) is paid once per lane, so few lanes with much each beat many
-// with little: against 16 bytes a lane, both without the ring, [16,16,4096,64] bf16 takes 72 instead of 78 us, [4,12,8192,64] fp32 46 instead
-// of 51, and rows whose length is no power of two [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead of
+// with little: against 16 bytes a lane, both without the ring, [16,16,4096,64] bf16 takes 72 instead of 78 us,
+// [4,12,8192,64] fp32 46 instead of 51, and rows whose length is no power of two [8,12,1310,100] bf16 17 instead of 23, [8,12,3971,33] 26 instead of
 // 63, [4,1,32768,192] 26 instead of 31. 32 elements a lane leave one CTA an SM: 35 against 16 us at d = 64. Few rows
 // (up to two CTAs an SM at 16 bytes a lane) are over sooner with a lane's least to fetch: single tokens
 // [256,12,1,64] bf16 1.6 against 2.0 us, [2,12,256,64] 1.9 against 2.0.
