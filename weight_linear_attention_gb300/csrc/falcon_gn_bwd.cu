@@ -231,10 +231,10 @@ int launch(BwdParams p, int& splits, cudaStream_t s) {
 }
 
 // Lanes and chunks of a row: 8 elements a lane (of fp32 4) with two or three CTAs an SM, or 24 with one where that
-// leaves fewer lanes idle; the figures are without the ring. The sums of dw and db take twice an element's registers, so the forward's 16 are slower (d =
+// leaves fewer lanes idle. The sums of dw and db take twice an element's registers, so the forward's 16 are slower (d =
 // 64: 30.6 against 28.9 us for [8,12,2048,64] bf16), while fewer elements on more lanes pay a row's fixed part more
 // often: [8,12,1310,100] bf16 takes 32 us with 8 on 16 lanes, 45 with 4 on 32; [8,12,3971,33] 46 us with 6 on 8
-// lanes, 109 with 2 on 32; [4,1,32768,192] 49 us with 24 on 8 lanes, 60 with 8 on 32.
+// lanes, 109 with 2 on 32; [4,1,32768,192] 49 us with 24 on 8 lanes, 60 with 8 on 32 (all without the ring).
 template <typename E, int VW>
 int by_width(const BwdParams& p, int& splits, cudaStream_t s) {
     const int nv = (p.d + VW - 1) / VW;
