@@ -15,14 +15,20 @@ namespace gn {
 
 using namespace seq;
 
-// ---- activations. e^-v is cut at 2^126 (far below any type's resolution of the results), so that
-// s = 1 / (1 + e) and 1 - s = e s are both finite and exact to a few units; NaN stays NaN.
+// ---- activations, of s = 1 / (1 + e) with e = e^-v. Where e overflows s is 0 (a logistic below 2^-126 is flushed to
+// it), so that v s is 0 for every finite v down to the type's lowest, off by at most |v| 2^-126 where the exact value
+// is not yet below that. NaN stays NaN.
 __device__ __forceinline__ float2 exp_neg(float2 v) {
     const float2 k = mul2(v, pair(-kLog2e, -kLog2e));
-    float2 e;
-    asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.x) : "f"(k.x));
-    asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e.y) : "f"(k.y));
-    return pair(ex2(e.x), ex2(e.y));
+    return pair(ex2(k.x), ex2(k.y));
+}
+// 1 - s as e s, exact to a few units. The cut at 2^126 keeps infinity times 0 out of it: s is 0 there, and the slopes
+// multiply 1 - s by s or by v s.
+__device__ __forceinline__ float2 one_minus(float2 e, float2 s) {
+    float2 c;
+    asm("min.NaN.f32 %0, %1, 0f7E800000;" : "=f"(c.x) : "f"(e.x));
+    asm("min.NaN.f32 %0, %1, 0f7E800000;" : "=f"(c.y) : "f"(e.y));
+    return mul2(c, s);
 }
 __device__ __forceinline__ float2 rcp2(float2 v) { return pair(rcp(v.x), rcp(v.y)); }
 
@@ -68,7 +74,7 @@ __device__ __forceinline__ void act_slope(float2 v, float2& f, float2& df) {
         f = mul2(v, phi);
         df = fma2(mul2(v, pair(q, q)), e, phi);
     } else {
-        const float2 e = exp_neg(v), s = rcp2(add2(e, pair(1.f, 1.f))), c = mul2(e, s);
+        const float2 e = exp_neg(v), s = rcp2(add2(e, pair(1.f, 1.f))), c = one_minus(e, s);
         f = ACT == kActSilu ? mul2(v, s) : s;
         df = ACT == kActSilu ? fma2(f, c, s) : mul2(s, c);
     }
