@@ -183,6 +183,21 @@ def _stream_handle(stream):
     return stream.cuda_stream
 
 
+def _as_current(stream, device):
+    """A context in which `stream` (a torch stream, an object with its handle, or the handle) is the current one. What a
+    call allocates in it belongs to that stream: the allocator reuses a block behind the work of the stream that it
+    belongs to, so a workspace from another stream's pool could be handed out again while the kernels still use it."""
+    import torch
+
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 1 is cudaStreamLegacy, the default stream's other name, which torch knows as 0
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got one on {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def falcon_fwd(variant, q, k, v, beta, lam, S0, tail, out, S_final, tail_out, dims: FalconDims, chunk: int,
                workspace=None, workspace_bytes=None, stream=None) -> int:
     """The C entry point with the same argument order; tensors or raw device pointers. Returns the status.
@@ -224,9 +239,14 @@ def backward(variant, q, k, v, beta, lam, dout, S0=None, dS_final=None, tail=Non
              eps_gamma=1e-6, want_dS0=True, stream=None):
     """Allocate fp32 gradients and a workspace with torch on q's device and call falcon_bwd; raises
     FalconError on a nonzero status. Returns a dict dq, dk, dv, dbeta, dlam, dS0 (None unless
-    want_dS0), dtail (None unless pos > 0)."""
+    want_dS0), dtail (None unless pos > 0). With `stream` (a torch stream or a raw handle) the whole call, its
+    allocations too, is that stream's, as inside torch.cuda.stream(stream)."""
     import torch
 
+    if stream is not None:
+        with _as_current(stream, q.device):
+            return backward(variant, q, k, v, beta, lam, dout, S0, dS_final, tail, pos=pos, chunk=chunk, eps=eps,
+                            eps_gamma=eps_gamma, want_dS0=want_dS0)
     if isinstance(variant, str):
         variant = VARIANTS[variant]
     B, H, T, dk_ = q.shape
@@ -242,7 +262,7 @@ def backward(variant, q, k, v, beta, lam, dout, S0=None, dS_final=None, tail=Non
     n = falcon_bwd_workspace_bytes(variant, dims, chunk)
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n > 0 else None
     st = falcon_bwd(variant, q, k, v, beta, lam, S0, tail, dout, dS_final, g["dq"], g["dk"], g["dv"], g["dbeta"],
-                    g["dlam"], g["dS0"], g["dtail"], dims, chunk, ws, stream=stream)
+                    g["dlam"], g["dS0"], g["dtail"], dims, chunk, ws)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_bwd")
     return g
@@ -263,10 +283,15 @@ def forward(variant, q, k, v, beta, lam, S0=None, tail=None, *, pos=0, window=1,
     Returns (out, S_final or None, tail_out or None). tail/tail_out are flat byte-sized
     buffers in q's dtype, laid out per (b,h) as keys[window][dk] then vals[window-1][dv].
     ``split=True`` hands falcon_fwd a workspace whenever a path can use one; ``False`` runs the
-    single-pass kernels.
+    single-pass kernels. With `stream` (a torch stream or a raw handle) the whole call, its allocations too, is that
+    stream's, as inside torch.cuda.stream(stream).
     """
     import torch
 
+    if stream is not None:
+        with _as_current(stream, q.device):
+            return forward(variant, q, k, v, beta, lam, S0, tail, pos=pos, window=window, chunk=chunk, eps=eps,
+                           eps_gamma=eps_gamma, want_state=want_state, want_tail=want_tail, split=split)
     if isinstance(variant, str):
         variant = VARIANTS[variant]
     B, H, T, dk = q.shape
@@ -280,7 +305,7 @@ def forward(variant, q, k, v, beta, lam, S0=None, tail=None, *, pos=0, window=1,
         n = falcon_tail_bytes(dims) // q.element_size()
         tail_out = torch.empty(n, dtype=q.dtype, device=q.device)
     ws = workspace_for(variant, dims, chunk, q.device) if split else None
-    st = falcon_fwd(variant, q, k, v, beta, lam, S0, tail, out, S_final, tail_out, dims, chunk, ws, stream=stream)
+    st = falcon_fwd(variant, q, k, v, beta, lam, S0, tail, out, S_final, tail_out, dims, chunk, ws)
     if st != FALCON_OK:
         raise FalconError(st)
     return out, S_final, tail_out
@@ -364,11 +389,11 @@ def _t():
             torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty)
 
 
-def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
+def _seq_call(what, choice, x, views, arrays, shape, lengths, names):
     """Checks the tensors of one call and marshals them. `views` (tensors or None) are [B,H,T,d] like x in x's type,
     `arrays` (tensors or None) contiguous fp32 of `shape`; `names` has the views' names, then the arrays'. Returns
     the library's function `what`, the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides,
-    and the stream."""
+    and the current stream."""
     torch, f32, codes, raw_stream, current_device, _ = _t()
     full, dtype, index = x.shape, x.dtype, x.get_device()
     if index < 0:
@@ -405,14 +430,10 @@ def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
             raise ValueError(f"lengths must be contiguous ({full[0]},) torch.int32 on {x.device}, got "
                              f"{tuple(lengths.shape)} {lengths.dtype} on {lengths.device}")
         pointers.append(lengths.data_ptr())
-    if stream is None:
-        stream = raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
     fn = getattr(_lib or load(), what)
     if index != current_device():
         fn = _on_device(fn, index)
-    return fn, pointers, _PACK_DIMS(*full, codes[dtype], 0), _PACK_STRIDES[len(views)](*strides), stream
+    return fn, pointers, _PACK_DIMS(*full, codes[dtype], 0), _PACK_STRIDES[len(views)](*strides), raw_stream(index)
 
 
 def _on_device(fn, index):
@@ -448,16 +469,21 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
     u = (1 - a) x). x, g: [B,H,T,d], float32 or bfloat16, any strides with contiguous channels (so
     `proj.view(B, T, H, d).transpose(1, 2)` and column blocks are passed as they are). h0: fp32 [B,H,d] or
     None (zero). lengths: int32 [B] or None; rows behind them come back as zeros. out (a [B,H,T,d] view) and
-    h_final (may be h0: updated in place) are written where given, else allocated dense."""
+    h_final (may be h0: updated in place) are written where given, else allocated dense. With `stream` (a torch
+    stream or a raw handle) the whole call, its allocations too, is that stream's, as inside
+    torch.cuda.stream(stream)."""
+    if stream is not None:
+        with _as_current(stream, x.device):
+            return glr_forward(gate, x, g, h0, lengths=lengths, out=out, h_final=h_final, want_state=want_state)
     B, H, T, d = _sizes(x)
     if out is None:
         out = _empty(x, x.shape, x.dtype)
     if h_final is None and want_state:
         h_final = _empty(x, (B, H, d))
     code = GLR_GATES.get(gate)
-    fn, p, dims, strides, stream = _seq_call("falcon_glr_fwd", code, x, (x, g, out), (h0, h_final), (B, H, d), lengths,
-                                             ("x", "g", "out", "h0", "h_final"), stream)
-    st = fn(code, p[0], p[1], p[3], p[5], p[2], p[4], dims, strides, stream)
+    fn, p, dims, strides, current = _seq_call("falcon_glr_fwd", code, x, (x, g, out), (h0, h_final), (B, H, d), lengths,
+                                             ("x", "g", "out", "h0", "h_final"))
+    st = fn(code, p[0], p[1], p[3], p[5], p[2], p[4], dims, strides, current)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_glr_fwd")
     return out, h_final
@@ -466,16 +492,20 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
 def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None, dx=None, dg=None, dh0=None,
                  stream=None):
     """Gradients of one glr_forward call, from its inputs, its output `out` and the adjoints of out and
-    h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated."""
+    h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated.
+    stream: as for glr_forward."""
+    if stream is not None:
+        with _as_current(stream, x.device):
+            return glr_backward(gate, x, g, out, dout, h0, dh_final, lengths=lengths, dx=dx, dg=dg, dh0=dh0)
     B, H, T, d = _sizes(x)
     dx = _empty(x, x.shape, x.dtype) if dx is None else dx
     dg = _empty(x, x.shape, x.dtype) if dg is None else dg
     dh0 = _empty(x, (B, H, d)) if dh0 is None else dh0
     code = GLR_GATES.get(gate)
-    fn, p, dims, strides, stream = _seq_call(
+    fn, p, dims, strides, current = _seq_call(
         "falcon_glr_bwd", code, x, (x, g, out, dout, dx, dg), (h0, dh_final, dh0), (B, H, d), lengths,
-        ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"), stream)
-    st = fn(code, p[0], p[1], p[2], p[6], p[9], p[3], p[7], p[4], p[5], p[8], dims, strides, stream)
+        ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"))
+    st = fn(code, p[0], p[1], p[2], p[6], p[9], p[3], p[7], p[4], p[5], p[8], dims, strides, current)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_glr_bwd")
     return {"dx": dx, "dg": dg, "dh0": dh0}
@@ -487,14 +517,17 @@ def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5
 
     x, z: [B,H,T,d] views as for glr_forward; weight, bias: fp32 [H,d] or None; act: "none", "silu", "gelu"
     (erf) or "sigmoid". y is written where given, else allocated in the output projection's layout: a [B,H,T,d]
-    view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free."""
+    view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free. stream: as for glr_forward."""
+    if stream is not None:
+        with _as_current(stream, x.device):
+            return groupnorm_forward(x, weight, bias, z, act=act, eps=eps, lengths=lengths, y=y)
     B, H, T, d = _sizes(x)
     if y is None:
         y = _empty(x, (B, T, H, d), x.dtype).transpose(1, 2)
     code = GN_ACTS.get(act)
-    fn, p, dims, strides, stream = _seq_call("falcon_gn_fwd", code, x, (x, z, y), (weight, bias), (H, d), lengths,
-                                             ("x", "z", "y", "weight", "bias"), stream)
-    st = fn(code, p[0], p[1], p[3], p[4], p[5], p[2], dims, strides, eps, stream)
+    fn, p, dims, strides, current = _seq_call("falcon_gn_fwd", code, x, (x, z, y), (weight, bias), (H, d), lengths,
+                                             ("x", "z", "y", "weight", "bias"))
+    st = fn(code, p[0], p[1], p[3], p[4], p[5], p[2], dims, strides, eps, current)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_gn_fwd")
     return y
@@ -504,7 +537,11 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
                        dz=None, dweight=None, dbias=None, workspace=None, want_params=True, stream=None):
     """Gradients of one groupnorm_forward call. Returns a dict dx, dz (None without a gate), dweight, dbias
     (fp32 [H,d]; None unless want_params or given). Each is written where given, else allocated dense; so is the
-    workspace, uint8 of falcon_gn_bwd_workspace_bytes, which dweight and dbias need."""
+    workspace, uint8 of falcon_gn_bwd_workspace_bytes, which dweight and dbias need. stream: as for glr_forward."""
+    if stream is not None:
+        with _as_current(stream, x.device):
+            return groupnorm_backward(x, dy, weight, bias, z, act=act, eps=eps, lengths=lengths, dx=dx, dz=dz,
+                                      dweight=dweight, dbias=dbias, workspace=workspace, want_params=want_params)
     B, H, T, d = _sizes(x)
     dx = _empty(x, x.shape, x.dtype) if dx is None else dx
     if z is not None and dz is None:
@@ -513,9 +550,9 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
         dweight = _empty(x, (H, d)) if dweight is None else dweight
         dbias = _empty(x, (H, d)) if dbias is None else dbias
     code = GN_ACTS.get(act)
-    fn, p, dims, strides, stream = _seq_call(
+    fn, p, dims, strides, current = _seq_call(
         "falcon_gn_bwd", code, x, (x, z, dy, dx, dz), (weight, bias, dweight, dbias), (H, d), lengths,
-        ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"), stream)
+        ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"))
     size = 0
     if dweight is not None or dbias is not None:
         if workspace is None:
@@ -527,7 +564,7 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
                 raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
             size = workspace.numel() * workspace.element_size()
     st = fn(code, p[0], p[1], p[5], p[6], p[9], p[2], p[3], p[4], p[7], p[8], dims, strides, eps, _ptr(workspace), size,
-            stream)
+            current)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_gn_bwd")
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
