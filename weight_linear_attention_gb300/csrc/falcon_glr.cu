@@ -952,7 +952,10 @@ int resident(Fn fn, KernelInfo& info, int dev, int cs, int bytes) {
         cudaLaunchAttribute at[2];
         cfg.gridDim = dim3(cs);
         describe(&cfg, at, cs, bytes);
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();  // a size that does not run is no error of the call's
+            return 0;
+        }
         info.clusters[dev][cs].store(n, std::memory_order_relaxed);
     }
     return n;

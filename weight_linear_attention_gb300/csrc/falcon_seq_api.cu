@@ -192,6 +192,13 @@ void merge_heads(SeqSizes* n, SeqView** v, int nv) {
     n->H = 1;
 }
 
+// A call's status. What CUDA refused is told by it alone: the runtime's last error, which the program's other
+// launches are checked by, is cleared.
+int result(int status) {
+    if (status == FALCON_ERR_CUDA) (void)cudaGetLastError();
+    return status;
+}
+
 }  // namespace
 
 extern "C" {
@@ -221,7 +228,7 @@ int falcon_glr_fwd(int gate, const void* x, const void* g, const float* h0, cons
     a.h_final = h_final;
     SeqView* v[] = {&a.x, &a.g, &a.out};
     merge_heads(&a.n, v, 3);
-    return falcon::launch_glr_fwd(a, static_cast<cudaStream_t>(stream));
+    return result(falcon::launch_glr_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 int falcon_glr_bwd(int gate, const void* x, const void* g, const void* out, const float* h0, const int32_t* lengths,
@@ -256,7 +263,7 @@ int falcon_glr_bwd(int gate, const void* x, const void* g, const void* out, cons
     if (gate != FALCON_GATE_MIX) a.x.p = nullptr;  // not read
     SeqView* v[] = {&a.x, &a.g, &a.out, &a.dout, &a.dx, &a.dg};
     merge_heads(&a.n, v, 6);
-    return falcon::launch_glr_bwd(a, static_cast<cudaStream_t>(stream));
+    return result(falcon::launch_glr_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 // eps > 0, and not NaN or infinite
@@ -288,7 +295,7 @@ int falcon_gn_fwd(int act, const void* x, const void* z, const float* weight, co
     a.lengths = lengths;
     a.eps = eps;
     if (c.n.B * c.n.H == 0 || c.n.T == 0) return FALCON_OK;
-    return falcon::launch_gn_fwd(a, static_cast<cudaStream_t>(stream));
+    return result(falcon::launch_gn_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t falcon_gn_bwd_workspace_bytes(const falcon_seq_dims_t* dims) {
@@ -340,11 +347,11 @@ int falcon_gn_bwd(int act, const void* x, const void* z, const float* weight, co
     a.ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
     if (c.n.B * c.n.H == 0 || c.n.T == 0) {  // no rows: the sums are zero
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (dweight && chans && cudaMemsetAsync(dweight, 0, chans * 4, s) != cudaSuccess) return FALCON_ERR_CUDA;
-        if (dbias && chans && cudaMemsetAsync(dbias, 0, chans * 4, s) != cudaSuccess) return FALCON_ERR_CUDA;
+        for (float* p : {dweight, dbias})
+            if (p && chans && cudaMemsetAsync(p, 0, chans * 4, s) != cudaSuccess) return result(FALCON_ERR_CUDA);
         return FALCON_OK;
     }
-    return falcon::launch_gn_bwd(a, static_cast<cudaStream_t>(stream));
+    return result(falcon::launch_gn_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
