@@ -240,11 +240,16 @@ size_t falcon_bwd_workspace_bytes(int variant, const falcon_dims_t* dims, int ch
  * FALCON_ERR_INVALID_ARG. Pointers are aligned to their element; calls are fastest where pointers, strides
  * and d are multiples of 16 bytes, then of 8 (the recurrence also of 4), else elements move one by one.
  * lengths: NULL, or device int32 [B]: sequence b has min(max(lengths[b], 0), T) tokens. Rows behind them
- * are not read (they may hold anything) and are written as zeros.
+ * reach no result, whatever they hold (the recurrence's forward may load some and discards them), and are
+ * written as zeros.
  * The calls use the current device, keep no scratch of their own and may run at the same time on any
  * streams. Sums run in a fixed order: the same call gives the same bits.
- * FALCON_ERR_UNSUPPORTED beyond the sizes below and from B*H*ceil(d/64) = 2^30 (recurrence), B*H*T = 2^31 rows
- * (norm) or 65536 heads (norm's backward) on.
+ * FALCON_ERR_UNSUPPORTED beyond the sizes below, and for
+ *   the recurrence    where B*H*ceil(d/64) reaches 2^30 (heads that follow each other without a gap in every
+ *                     tensor count as one head of H*d channels; with up to 8 tokens only where B*H*d reaches
+ *                     2^38, or 2^40 if all is aligned to four elements);
+ *   the norm forward  from B*H*T = 2^31 rows or H = 2^30 on;
+ *   its backward      from B*T = 2^31 - 65536 or H = 65536 on.
  */
 typedef struct {
     int64_t batch;   /* B >= 0                                                        */
@@ -308,6 +313,8 @@ typedef enum {
  *   weight, bias  fp32 [H,d] or NULL (1 and 0)
  *   strides   of x, z, y (9 values; z's ignored without a gate) or NULL
  *   eps       > 0
+ * Statistics are fp32: where a row's sum or its centred squares' sum overflows (|x| beyond some 1e17), n is not the
+ * formula's (the bias alone, or NaN).
  */
 int falcon_gn_fwd(int act, const void* x, const void* z, const float* weight, const float* bias,
                   const int32_t* lengths, void* y, const falcon_seq_dims_t* dims, const int64_t* strides, float eps,
@@ -331,7 +338,8 @@ int falcon_gn_bwd(int act, const void* x, const void* z, const float* weight, co
 /* Workspace bytes of falcon_gn_bwd (partial sums of dweight and dbias); 0 for invalid dims. Host only. */
 size_t falcon_gn_bwd_workspace_bytes(const falcon_seq_dims_t* dims);
 
-/* ABI version of this header: 4. */
+/* ABI version of this header: 4. Functions that are added beside the others leave it as it is (falcon_glr_fwd and
+ * those behind it were): a caller that may meet an older library looks their symbols up. */
 int falcon_abi_version(void);
 
 #ifdef __cplusplus
