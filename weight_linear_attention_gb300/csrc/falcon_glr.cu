@@ -237,7 +237,7 @@ __device__ __forceinline__ void advance(const Params& p, Cursor& c, int step, in
 template <typename E, int LC, int R, int CB>
 __device__ __forceinline__ void copy_rows(const Params& p, uint32_t dst, uint8_t* dst_p, const void* base, int k,
                                           const Cursor& c, int n, int t0, int sign, int shift) {
-    constexpr int RB = Geo<LC, R>::kChans * sizeof(E), PAD = Geo<LC, R>::kSegs > 1 ? RB : 0;  // as Ring's
+    constexpr int RB = Geo<LC, R>::kChans * sizeof(E);
     constexpr int CPR = RB / CB, EPC = CB / sizeof(E);
     constexpr int RPS = CPR < 32 ? 32 / CPR : 1, CPL = CPR < 32 ? 1 : CPR / 32;  // rows a step, columns a lane
     const int lane = threadIdx.x & 31, row0 = lane / CPR % RPS, col0 = lane % CPR;
@@ -253,7 +253,7 @@ __device__ __forceinline__ void copy_rows(const Params& p, uint32_t dst, uint8_t
         for (int j = 0; j < CPL; ++j) {
             const bool in = row_in && c.c0 + (col0 + 32 * j) * EPC < p.d;
             const E* at = in ? src + 32 * j * EPC : static_cast<const E*>(base);
-            const uint32_t o = (r + row0) * RB + (r + row0) / R * PAD + (col0 + 32 * j) * CB;
+            const uint32_t o = (r + row0) * RB + (col0 + 32 * j) * CB;
             if constexpr (CB >= 4) copy_async<CB>(dst + o, at, in);
             else *reinterpret_cast<uint16_t*>(dst_p + o) = in ? *reinterpret_cast<const uint16_t*>(at) : (uint16_t)0;
         }
@@ -321,14 +321,12 @@ struct Ring {
     using G = Geo<LC, R>;
     static constexpr bool kBoxes = CB == kTma;
     static constexpr bool VS = CB == kTma || CB == 2 * sizeof(E) || CB == 8;  // pairs of channels are aligned
-    static constexpr int RB = G::kChans * sizeof(E);                     // bytes of a row
-    static constexpr int PAD = G::kSegs > 1 && !kBoxes ? RB : 0;         // between segments, against bank conflicts
-    static constexpr int WB = G::kRows * RB + G::kSegs * PAD;            // one warp's rows of one tensor
-    static constexpr int TB = kWarps * WB;                               // a tile's
+    static constexpr int RB = G::kChans * sizeof(E);  // bytes of a row
+    static constexpr int WB = G::kRows * RB;          // one warp's rows of one tensor
+    static constexpr int TB = kWarps * WB;            // a tile's
     static constexpr int kBoxes1 = (G::kTile + 255) / 256, kBoxRows = G::kTile / kBoxes1;  // boxes of a tile, rows of a box
     static_assert(kBoxRows * kBoxes1 == G::kTile, "a tile is whole boxes");
-    // where row r of segment seg lies
-    static __device__ __forceinline__ int at(int seg, int r) { return (seg * R + r) * RB + seg * PAD; }
+    static __device__ __forceinline__ int at(int seg) { return seg * R * RB; }  // a segment's first row
 };
 
 // A tile's rows of one tensor, as boxes: from shared memory (`mine` its address) or to it.
@@ -450,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
             __syncwarp();
         }
         const int t0 = cur.n0 + row0 + seg * R, left = cur.len - t0;  // this thread's rows inside the sequence
-        uint8_t* const from = ring + stage * SB + warp * Q::WB + Q::at(seg, 0) + lc * 2 * sizeof(E);
+        uint8_t* const from = ring + stage * SB + warp * Q::WB + Q::at(seg) + lc * 2 * sizeof(E);
         const bool whole = left >= R;
         if (!whole) {  // rows behind the end change nothing, whatever they hold
 #pragma unroll 1
@@ -489,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
             }
         });
         if constexpr (Q::kBoxes) {
-            uint8_t* const to = outs + (it & 1) * OB + warp * Q::WB + Q::at(seg, 0) + lc * 2 * sizeof(E);
+            uint8_t* const to = outs + (it & 1) * OB + warp * Q::WB + Q::at(seg) + lc * 2 * sizeof(E);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h = fma2(a[r], h, u[r]);
@@ -625,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
         // boxes lie in ascending order of the tokens, copied rows in the scan's
         uint8_t* const from = ring + stage * SB + lc * 2 * sizeof(E) +
                               (Q::kBoxes ? (G::kTile - 1 - warp * G::kRows - seg * R) * Q::RB
-                                         : warp * Q::WB + Q::at(seg, 0));
+                                         : warp * Q::WB + Q::at(seg));
         constexpr int RS = Q::kBoxes ? -Q::RB : Q::RB;
         const bool whole = left >= R;
         if (!whole) {  // positions behind the last: dout and out read as zeros there
