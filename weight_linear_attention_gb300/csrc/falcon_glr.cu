@@ -178,12 +178,14 @@ __device__ __forceinline__ float2 scan_tile(Maps<LC>& sm, int it, bool fresh, in
     float2 in = carry;  // the state entering this CTA's tile
     if (cs > 1) {
         const uint32_t bar = ptx::smem_u32(&sm.ready[buf]);
-        if (threadIdx.x == 0) ptx::mbar_expect_tx(bar, cs * LC * (uint32_t)sizeof(Map));
+        // a thread whose wait ran out neither arrives again (the phase before may be open) nor sends any more: its
+        // peers' waits run out as well, and all come to their end
+        if (threadIdx.x == 0 && !dead) ptx::mbar_expect_tx(bar, cs * LC * (uint32_t)sizeof(Map));
         if (warp == kWarps - 1) {  // the CTA's map, to every peer: the lanes of a segment send to every kSegs-th
             Map all = compose(before, inc);
             if (LC < 32) all = shfl(all, 32 - LC + lc);
             const uint32_t at = ptx::smem_u32(&sm.cta[buf][rank][lc]);
-            for (int r = lane / LC; r < cs; r += 32 / LC) st_async4(peer(at, r), &all.A.x, peer(bar, r));
+            for (int r = dead ? cs : lane / LC; r < cs; r += 32 / LC) st_async4(peer(at, r), &all.A.x, peer(bar, r));
         }
         // A peer writes this buffer again two tiles on, after this CTA's map of the tile between has
         // reached it; that is sent behind the barrier above, so behind the reads below.
@@ -374,6 +376,24 @@ __device__ __forceinline__ void set_up(Mover<S>& mv, Maps<LC>& sm) {
     __syncthreads();
 }
 
+// Behind a wait that ran out nothing is loaded any more and nothing waited for, so what is still on its way into this
+// CTA's shared memory is waited for at the end (each with the same limit). The boxes: each stage's last ones, whose
+// phase no later one has followed.
+template <int S>
+__device__ __forceinline__ void drain_loads(Mover<S>& mv) {
+    for (int i = max(mv.loaded - S, 0); i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+}
+// No CTA leaves while a peer may still write to it. Every map has been waited for, unless a wait ran out: then some may
+// be on their way that no phase will count, and what is sent is given the time of a wait to arrive.
+__device__ __forceinline__ void leave_cluster(int cs, bool dead) {
+    if (cs == 1) return;
+    cluster_arrive();
+    cluster_wait();
+    if (dead)
+        for (const long long t0 = clock64(); clock64() - t0 <= kTimeoutCycles;) {
+        }
+}
+
 template <typename E, int GATE, int LC, int R, int CB, int S>
 __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_constant__ Params p, int cs) {
     using G = Geo<LC, R>;
@@ -524,13 +544,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const __grid_const
             if (it > 0 && !dead) store(it - 1, mv.held);
             ptx::bulk_wait_all();
         }
-        if (threadIdx.x == kLoader)  // loads that a wait that ran out has left behind
-            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+        if (threadIdx.x == kLoader && dead) drain_loads(mv);
     }
-    if (cs > 1) {  // no CTA leaves while a peer may still write to it
-        cluster_arrive();
-        cluster_wait();
-    }
+    leave_cluster(cs, dead);
 }
 
 template <typename E, int GATE, int LC, int R, int CB, int S>
@@ -719,13 +735,9 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const __grid_const
             if (it > 0 && !dead) store(it - 1, mv.held);
             ptx::bulk_wait_all();
         }
-        if (threadIdx.x == kLoader)  // loads that a wait that ran out has left behind
-            for (int i = it; i < mv.loaded; ++i) bounded_wait(&mv.full[i % S], i / S & 1);
+        if (threadIdx.x == kLoader && dead) drain_loads(mv);
     }
-    if (cs > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
+    leave_cluster(cs, dead);
 }
 
 // ---- few tokens (a decoding step, short sequences): one thread per VW channels walks them, its rows loaded U at
