@@ -16,14 +16,15 @@
 // every CTA composes them all in the same order, so that the state that enters the next cluster-wide tile is
 // known everywhere without another exchange. Then each thread replays its tokens from its entering state into
 // a buffer of their own, whence a TMA store takes them while the next tile is worked on. No scratch in global memory,
-// no atomics on data; the order of every sum is fixed by the sizes. Waits are bounded: one that runs out raises a flag
-// (falcon_device_status) and is not repeated.
+// no atomics on data; the order of every sum is fixed by sizes and alignment. Waits are bounded: one that runs out
+// raises a flag (falcon_device_status) and is not repeated.
 //
 // What bounds it: 3 tensors' bytes per element forward, 5 or 6 backward, where there are tiles enough to hide
 // the rest ([16,16,4096,64] bf16: 65 us forward, 92 % of the copy rate, 133 us backward, 90 %; 20 to 26 thread
 // instructions per element, of which an SM has 33 at that rate). One long sequence ([1,12,131072,64] decay: 119 us,
 // 75 %) is bound by the exchange (95 us without it), a training batch ([8,12,1024,64] mix: 12.2 us forward, 46 %, 18.1
-// backward, 62 %) by filling and emptying three tiles per CTA (the same boxes without arithmetic: 8.5 us forward).
+// backward, 62 %) by filling and emptying three tiles per CTA (the same boxes without arithmetic: 8.5 us forward) and
+// by arithmetic that does not overlap them (the other 3.7).
 
 #include <cuda.h>
 #include <cuda_bf16.h>

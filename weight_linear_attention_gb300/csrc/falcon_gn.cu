@@ -9,7 +9,8 @@
 // have neighbouring heads, so that a CTA writes whole lines of the projection's layout.
 //
 // What bounds it: memory ([16,16,4096,64] bf16 with a SiLU gate: 60 us, 99 % of the copy rate; [4,12,8192,64] fp32 46
-// us, 97 %); at [8,12,2048,64] bf16 (13.4 us, 83 %) filling and emptying; GELU's issue slots (14.8 us, 50 %, ungated).
+// us, 97 %); at [8,12,2048,64] bf16 (13.4 us, 83 %) filling and emptying; without a gate GELU's arithmetic (the same 14.8
+// us, 50 %; [8,12,8192,64] 48.6 us, 61 %, with 63 % of the issue slots busy, where SiLU takes 36.4).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

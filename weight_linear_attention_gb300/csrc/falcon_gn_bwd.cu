@@ -5,7 +5,7 @@
 // Memory bound: 3 (5 with a gate) tensors' bytes per element. A CTA takes rows of one head only, so a
 // thread's channels stay the same and it sums dw and db in registers; the CTA adds its threads' sums up
 // in shared memory and leaves one partial sum per split of the rows, which a second, small kernel adds
-// in the order of the splits. Every order depends on the sizes alone: no atomics.
+// in the order of the splits. Every order depends on sizes and alignment alone: no atomics.
 //
 // What bounds it: memory ([16,16,4096,64] bf16 with a SiLU gate: 104 us, 95 % of the copy rate; [4,12,8192,64] fp32
 // with a gate 82 us, 91 %); at [8,12,1024,64] bf16 (14.9 us with the sums' kernel, 62 %) filling, emptying and the sums.
