@@ -210,3 +210,42 @@ def test_two_given_streams_without_a_workspace():
     for a, b in zip(got, want):
         for k in ("dx", "dweight", "dbias"):
             assert torch.equal(a[k], b[k]), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_given_stream_and_outputs(raw):
+    """With nothing to allocate the call still runs on the stream it is given, and only there."""
+    x, _, _, s, w = _tensors()
+    want, _ = F.glr_forward("mix", x[0], x[1], s)
+    norm = F.groupnorm_forward(want, w, w, x[1], act="silu")
+    out, y = torch.zeros_like(want), torch.zeros_like(norm)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    st = side.cuda_stream if raw else side
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(PENDING)
+    F.glr_forward("mix", x[0], x[1], s, out=out, want_state=False, stream=st)
+    F.groupnorm_forward(out, w, w, x[1], act="silu", y=y, stream=st)
+    before = [out.clone(), y.clone()]  # on the current stream, which waits for neither
+    torch.cuda.current_stream().synchronize()
+    assert not any(bool(t.any()) for t in before)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(y, norm)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_the_current_stream_as_an_argument(name):
+    call = gpu_calls()[name]
+    want = _leaves(call())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for st in (None, side):
+        with torch.cuda.stream(st):
+            now = torch.cuda.current_stream()
+            for arg in (now, now.cuda_stream):
+                got = _leaves(call(stream=arg))
+                torch.cuda.synchronize()
+                assert _same(name, got, want)
+                assert all(_owner(t) == now.cuda_stream for t in got)

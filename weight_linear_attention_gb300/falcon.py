@@ -11,6 +11,7 @@ PyTorch is used only to hand over device pointers and the current CUDA stream.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import functools
 import os
@@ -188,15 +189,24 @@ def _as_current(stream, device):
     """A context in which `stream` (a torch stream, an object with its handle, or the handle) is the current one. What a
     call allocates in it belongs to that stream: the allocator reuses a block behind the work of the stream that it
     belongs to, so a workspace from another stream's pool could be handed out again while the kernels still use it."""
-    import torch
+    t = _t()
+    handle = _handle(stream, device)
+    if handle == 1:  # cudaStreamLegacy, the default stream's other name, which torch knows as 0
+        handle = stream = 0
+    if device.index is not None and t.current_device() == device.index and t.raw_stream(device.index) == handle:
+        return contextlib.nullcontext()
+    if not isinstance(stream, t.torch.cuda.Stream):
+        stream = t.torch.cuda.ExternalStream(handle, device=device)
+    return t.torch.cuda.stream(stream)
 
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-        # 1 is cudaStreamLegacy, the default stream's other name, which torch knows as 0
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
-    if stream.device != device:
+
+def _handle(stream, device):
+    """The raw handle of a stream argument."""
+    if isinstance(stream, int):
+        return stream
+    if isinstance(stream, _t().torch.cuda.Stream) and stream.device != device:
         raise ValueError(f"stream must be on {device}, got one on {stream.device}")
-    return torch.cuda.stream(stream)
+    return stream.cuda_stream
 
 
 def falcon_fwd(variant, q, k, v, beta, lam, S0, tail, out, S_final, tail_out, dims: FalconDims, chunk: int,
@@ -395,11 +405,11 @@ def _t():
                   torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty)
 
 
-def _seq_call(what, choice, x, views, arrays, shape, lengths, names):
+def _seq_call(what, choice, x, views, arrays, shape, lengths, names, stream):
     """Checks the tensors of one call and marshals them. `views` (tensors or None) are [B,H,T,d] like x in x's type,
     `arrays` (tensors or None) contiguous fp32 of `shape`; `names` has the views' names, then the arrays'. Returns
     the library's function `what`, the pointers (views, arrays, lengths), the packed falcon_seq_dims_t and strides,
-    and the current stream."""
+    and the stream's handle (the current one's where `stream` is None)."""
     torch, f32, codes, raw_stream, current_device, _ = _t()
     full, dtype, index = x.shape, x.dtype, x.get_device()
     if index < 0:
@@ -439,7 +449,8 @@ def _seq_call(what, choice, x, views, arrays, shape, lengths, names):
     fn = getattr(_lib or load(), what)
     if index != current_device():
         fn = _on_device(fn, index)
-    return fn, pointers, _PACK_DIMS(*full, codes[dtype], 0), _PACK_STRIDES[len(views)](*strides), raw_stream(index)
+    return fn, pointers, _PACK_DIMS(*full, codes[dtype], 0), _PACK_STRIDES[len(views)](*strides), \
+        raw_stream(index) if stream is None else _handle(stream, x.device)
 
 
 def _on_device(fn, index):
@@ -458,9 +469,12 @@ def _sizes(x):
     return x.shape
 
 
-def _empty(x, shape, dtype=None):
-    t = _t()
-    return t.empty(shape, dtype=dtype or t.float32, device=x.device)
+def _empty(x, shape, dtype, stream):
+    """A tensor beside x whose memory belongs to `stream` (None: the current one)."""
+    if stream is None:
+        return _t().empty(shape, dtype=dtype, device=x.device)
+    with _as_current(stream, x.device):
+        return _t().empty(shape, dtype=dtype, device=x.device)
 
 
 @functools.lru_cache(maxsize=256)
@@ -477,21 +491,19 @@ def glr_forward(gate, x, g, h0=None, *, lengths=None, out=None, h_final=None, wa
     `proj.view(B, T, H, d).transpose(1, 2)` and column blocks are passed as they are). h0: fp32 [B,H,d] or
     None (zero). lengths: int32 [B] or None; rows behind them come back as zeros. out (a [B,H,T,d] view) and
     h_final (may be h0: updated in place) are written where given, else allocated dense. With `stream` (a torch
-    stream or a raw handle) the whole call, its allocations too, is that stream's, as inside
-    torch.cuda.stream(stream)."""
-    if stream is not None:
-        with _as_current(stream, x.device):
-            return glr_forward(gate, x, g, h0, lengths=lengths, out=out, h_final=h_final, want_state=want_state)
+    stream or a raw handle) the kernels run there and what is allocated belongs to it, as inside
+    torch.cuda.stream(stream); where all outputs are given that costs nothing."""
     B, H, T, d = _sizes(x)
     if out is None:
-        out = _empty(x, x.shape, x.dtype)
+        out = _empty(x, x.shape, x.dtype, stream)
     if h_final is None and want_state:
-        h_final = _empty(x, (B, H, d))
+        h_final = _empty(x, (B, H, d), _t().float32, stream)
     code = GLR_GATES.get(gate)
-    fn, pointers, dims, strides, current = _seq_call(
-        "falcon_glr_fwd", code, x, (x, g, out), (h0, h_final), (B, H, d), lengths, ("x", "g", "out", "h0", "h_final"))
+    fn, pointers, dims, strides, handle = _seq_call(
+        "falcon_glr_fwd", code, x, (x, g, out), (h0, h_final), (B, H, d), lengths, ("x", "g", "out", "h0", "h_final"),
+        stream)
     p_x, p_g, p_out, p_h0, p_h_final, p_lengths = pointers
-    st = fn(code, p_x, p_g, p_h0, p_lengths, p_out, p_h_final, dims, strides, current)
+    st = fn(code, p_x, p_g, p_h0, p_lengths, p_out, p_h_final, dims, strides, handle)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_glr_fwd")
     return out, h_final
@@ -502,19 +514,16 @@ def glr_backward(gate, x, g, out, dout, h0=None, dh_final=None, *, lengths=None,
     """Gradients of one glr_forward call, from its inputs, its output `out` and the adjoints of out and
     h_final. Returns a dict dx, dg (in x's dtype), dh0 (fp32); each is written where given, else allocated.
     stream: as for glr_forward."""
-    if stream is not None:
-        with _as_current(stream, x.device):
-            return glr_backward(gate, x, g, out, dout, h0, dh_final, lengths=lengths, dx=dx, dg=dg, dh0=dh0)
     B, H, T, d = _sizes(x)
-    dx = _empty(x, x.shape, x.dtype) if dx is None else dx
-    dg = _empty(x, x.shape, x.dtype) if dg is None else dg
-    dh0 = _empty(x, (B, H, d)) if dh0 is None else dh0
+    dx = _empty(x, x.shape, x.dtype, stream) if dx is None else dx
+    dg = _empty(x, x.shape, x.dtype, stream) if dg is None else dg
+    dh0 = _empty(x, (B, H, d), _t().float32, stream) if dh0 is None else dh0
     code = GLR_GATES.get(gate)
-    fn, pointers, dims, strides, current = _seq_call(
+    fn, pointers, dims, strides, handle = _seq_call(
         "falcon_glr_bwd", code, x, (x, g, out, dout, dx, dg), (h0, dh_final, dh0), (B, H, d), lengths,
-        ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"))
+        ("x", "g", "out", "dout", "dx", "dg", "h0", "dh_final", "dh0"), stream)
     p_x, p_g, p_out, p_dout, p_dx, p_dg, p_h0, p_dh_final, p_dh0, p_lengths = pointers
-    st = fn(code, p_x, p_g, p_out, p_h0, p_lengths, p_dout, p_dh_final, p_dx, p_dg, p_dh0, dims, strides, current)
+    st = fn(code, p_x, p_g, p_out, p_h0, p_lengths, p_dout, p_dh_final, p_dx, p_dg, p_dh0, dims, strides, handle)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_glr_bwd")
     return {"dx": dx, "dg": dg, "dh0": dh0}
@@ -527,17 +536,14 @@ def groupnorm_forward(x, weight=None, bias=None, z=None, *, act="none", eps=1e-5
     x, z: [B,H,T,d] views as for glr_forward; weight, bias: fp32 [H,d] or None; act: "none", "silu", "gelu"
     (erf) or "sigmoid". y is written where given, else allocated in the output projection's layout: a [B,H,T,d]
     view of a dense [B,T,H,d], so `y.transpose(1, 2).reshape(B, T, H * d)` is free. stream: as for glr_forward."""
-    if stream is not None:
-        with _as_current(stream, x.device):
-            return groupnorm_forward(x, weight, bias, z, act=act, eps=eps, lengths=lengths, y=y)
     B, H, T, d = _sizes(x)
     if y is None:
-        y = _empty(x, (B, T, H, d), x.dtype).transpose(1, 2)
+        y = _empty(x, (B, T, H, d), x.dtype, stream).transpose(1, 2)
     code = GN_ACTS.get(act)
-    fn, pointers, dims, strides, current = _seq_call(
-        "falcon_gn_fwd", code, x, (x, z, y), (weight, bias), (H, d), lengths, ("x", "z", "y", "weight", "bias"))
+    fn, pointers, dims, strides, handle = _seq_call(
+        "falcon_gn_fwd", code, x, (x, z, y), (weight, bias), (H, d), lengths, ("x", "z", "y", "weight", "bias"), stream)
     p_x, p_z, p_y, p_weight, p_bias, p_lengths = pointers
-    st = fn(code, p_x, p_z, p_weight, p_bias, p_lengths, p_y, dims, strides, eps, current)
+    st = fn(code, p_x, p_z, p_weight, p_bias, p_lengths, p_y, dims, strides, eps, handle)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_gn_fwd")
     return y
@@ -548,34 +554,30 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
     """Gradients of one groupnorm_forward call. Returns a dict dx, dz (None without a gate), dweight, dbias
     (fp32 [H,d]; None unless want_params or given). Each is written where given, else allocated dense; so is the
     workspace, uint8 of falcon_gn_bwd_workspace_bytes, which dweight and dbias need. stream: as for glr_forward."""
-    if stream is not None:
-        with _as_current(stream, x.device):
-            return groupnorm_backward(x, dy, weight, bias, z, act=act, eps=eps, lengths=lengths, dx=dx, dz=dz,
-                                      dweight=dweight, dbias=dbias, workspace=workspace, want_params=want_params)
     B, H, T, d = _sizes(x)
-    dx = _empty(x, x.shape, x.dtype) if dx is None else dx
+    dx = _empty(x, x.shape, x.dtype, stream) if dx is None else dx
     if z is not None and dz is None:
-        dz = _empty(x, x.shape, x.dtype)
+        dz = _empty(x, x.shape, x.dtype, stream)
     if want_params:
-        dweight = _empty(x, (H, d)) if dweight is None else dweight
-        dbias = _empty(x, (H, d)) if dbias is None else dbias
+        dweight = _empty(x, (H, d), _t().float32, stream) if dweight is None else dweight
+        dbias = _empty(x, (H, d), _t().float32, stream) if dbias is None else dbias
     code = GN_ACTS.get(act)
-    fn, pointers, dims, strides, current = _seq_call(
+    fn, pointers, dims, strides, handle = _seq_call(
         "falcon_gn_bwd", code, x, (x, z, dy, dx, dz), (weight, bias, dweight, dbias), (H, d), lengths,
-        ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"))
+        ("x", "z", "dy", "dx", "dz", "weight", "bias", "dweight", "dbias"), stream)
     size = 0
     if dweight is not None or dbias is not None:
         if workspace is None:
             size = _gn_bwd_bytes(dims)
             if size > 0:
-                workspace = _empty(x, size, _t().torch.uint8)
+                workspace = _empty(x, size, _t().torch.uint8, stream)
         else:
             if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
                 raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
             size = workspace.numel() * workspace.element_size()
     p_x, p_z, p_dy, p_dx, p_dz, p_weight, p_bias, p_dweight, p_dbias, p_lengths = pointers
     st = fn(code, p_x, p_z, p_weight, p_bias, p_lengths, p_dy, p_dx, p_dz, p_dweight, p_dbias, dims, strides, eps,
-            _ptr(workspace), size, current)
+            _ptr(workspace), size, handle)
     if st != FALCON_OK:
         raise FalconError(st, "falcon_gn_bwd")
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
