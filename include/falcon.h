@@ -338,6 +338,111 @@ int falcon_gn_bwd(int act, const void* x, const void* z, const float* weight, co
 /* Workspace bytes of falcon_gn_bwd (partial sums of dweight and dbias); 0 for invalid dims. Host only. */
 size_t falcon_gn_bwd_workspace_bytes(const falcon_seq_dims_t* dims);
 
+/* ------------------------------------------------------------------------------------------------
+ * The block around the read: the gated delta rule (the fast-weight update with a gain and a decay of its own a
+ * token, the key that is written and the one that predicts being the same) and the root-mean-square norm with the
+ * residual's addition. Strides, lengths, alignment, overlap, streams and errors are as for the operators above;
+ * where strides of q, k and v are given, those of beta and g are, too.
+ */
+typedef struct {
+    int64_t batch;     /* B >= 0                                                      */
+    int64_t heads;     /* H >= 0, of v                                                */
+    int64_t qk_heads;  /* Hk, of q and k: divides H; head h of v goes with h / (H/Hk) */
+    int64_t seqlen;    /* 0 <= T < 2^30                                               */
+    int64_t dk;        /* 1 <= dk <= 128                                              */
+    int64_t dv;        /* 1 <= dv <= 128                                              */
+    int32_t dtype;     /* falcon_dtype_t of q, k, v, out and their gradients          */
+    int32_t reserved;  /* 0                                                           */
+} falcon_gdr_dims_t;
+
+/*
+ * falcon_gdr_fwd — gated delta rule. Per sequence and head, with a_t = e^{g_t}:
+ *   S_t = a_t S_{t-1} + k_t (beta_t (v_t - a_t S_{t-1}^T k_t))^T,   out_t = scale S_t^T q_t.
+ *   q, k      [B,Hk,T,dk] dtype
+ *   v, out    [B,H,T,dv] dtype
+ *   beta, g   fp32 [B,H,T]            gain, and log decay (-inf forgets all before its token)
+ *   S0        fp32 [B,H,dk,dv] or NULL (zero state)
+ *   S_final   fp32 [B,H,dk,dv] or NULL: the state behind each sequence's last token (S0 when it has none);
+ *             may be the same pointer as S0
+ *   strides   of q, k, v, beta, g, out (18 values) or NULL
+ *   scale     any finite number (dk^-1/2 is usual)
+ *   workspace at least falcon_gdr_workspace_bytes(dims, 0) bytes, 256-byte aligned; may be NULL where that is 0
+ *             (up to 16 tokens). Contents ignored on entry, unspecified on return; calls that may run at the same
+ *             time must not share one
+ * Up to 16 tokens are walked one by one, in fp32. Longer sequences go in chunks of 64, whose maps of the state are
+ * formed first: their products, (I + N diag(beta))^-1 with N_ij = e^{..} k_i.k_j among them, have fp32's precision,
+ * and are as well conditioned as the update itself where beta |k|^2 stays below 2 (keys of unit length, a gain
+ * below 1). Sums over more than 2^24 log decays' worth are not formed: a chunk's are, in double.
+ * T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
+ * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or B*H*ceil(T/64) = 2^31.
+ */
+int falcon_gdr_fwd(const void* q, const void* k, const void* v, const float* beta, const float* g, const float* S0,
+                   const int32_t* lengths, void* out, float* S_final, const falcon_gdr_dims_t* dims,
+                   const int64_t* strides, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * falcon_gdr_bwd — gradients of L = sum(out * dout) + sum(S_final * dS_final) of one falcon_gdr_fwd call, from its
+ * inputs alone (the states are formed again).
+ *   dout      [B,H,T,dv] dtype
+ *   dS_final  fp32 [B,H,dk,dv] or NULL (zero)
+ *   dq, dk    [B,Hk,T,dk] dtype       summed over the heads that share them, rounded once
+ *   dv        [B,H,T,dv] dtype
+ *   dbeta, dg fp32 [B,H,T]            (dg is 0 where e^g is)
+ *   dS0       fp32 [B,H,dk,dv] or NULL
+ *   strides   of q, k, v, beta, g, dout, dq, dk, dv, dbeta, dg (33 values) or NULL
+ *   workspace at least falcon_gdr_workspace_bytes(dims, 1) bytes, as above
+ */
+int falcon_gdr_bwd(const void* q, const void* k, const void* v, const float* beta, const float* g, const float* S0,
+                   const int32_t* lengths, const void* dout, const float* dS_final, void* dq, void* dk, void* dv,
+                   float* dbeta, float* dg, float* dS0, const falcon_gdr_dims_t* dims, const int64_t* strides,
+                   float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of falcon_gdr_fwd (backward 0) or falcon_gdr_bwd (1); 0 where none is needed and for invalid
+ * dims. A function of the sizes alone. Host only. */
+size_t falcon_gdr_workspace_bytes(const falcon_gdr_dims_t* dims, int backward);
+
+#define FALCON_E4M3 2 /* out_dtype of falcon_rms_fwd: 8 bits, 4 of them exponent and 3 mantissa, up to 448 */
+
+typedef struct {
+    int64_t batch;     /* B >= 0                                                      */
+    int64_t seqlen;    /* T >= 0; B*T < 2^31                                          */
+    int64_t d;         /* channels of a token, 1 <= d <= 16384                        */
+    int32_t dtype;     /* falcon_dtype_t of x, residual, h and the gradients          */
+    int32_t out_dtype; /* of y: dtype, or FALCON_E4M3 (forward only)                  */
+} falcon_rms_dims_t;
+
+/*
+ * falcon_rms_fwd — per token: h = x + residual (x alone without one), y = weight h / sqrt(mean h^2 + eps), of h as it
+ * is rounded to dtype.
+ *   x, y      [B,T,d]                 d contiguous channels; strides are two values a tensor: batch, token
+ *   residual  [B,T,d] dtype or NULL
+ *   weight    fp32 [d] or NULL (1)
+ *   h         [B,T,d] dtype or NULL; only with a residual. May be x or residual (same pointer and strides)
+ *   scales    fp32 [B,T] if y is FALCON_E4M3, else NULL: a token's scale is its largest |y| / 448, and y holds the
+ *             nearest values of y / scale (ties to even; zeros, and scale 0, where all are 0; NaN stays NaN)
+ *   strides   of x, residual, h, y (8 values) or NULL
+ * Rows behind a sequence's length are written as zeros, their h and scales too. Statistics are fp32: where a row's
+ * squares' sum overflows, y is 0.
+ */
+int falcon_rms_fwd(const void* x, const void* residual, const float* weight, const int32_t* lengths, void* h, void* y,
+                   float* scales, const falcon_rms_dims_t* dims, const int64_t* strides, float eps, void* stream);
+
+/*
+ * falcon_rms_bwd — gradients of L = sum(y * dy) + sum(h * dh) of one falcon_rms_fwd call, its y unrounded.
+ *   h         [B,T,d] dtype           what was normalised: falcon_rms_fwd's h, or x without a residual
+ *   dh        [B,T,d] dtype or NULL   gradient that reaches h from elsewhere (the stream behind the block)
+ *   dx        [B,T,d] dtype           gradient of x and of residual alike; may be dh (same pointer and strides)
+ *   dweight   fp32 [d] or NULL: written, not added to
+ *   strides   of h, dy, dh, dx (8 values) or NULL
+ *   workspace at least falcon_rms_bwd_workspace_bytes(dims) bytes, 256-byte aligned; may be NULL when dweight is
+ */
+int falcon_rms_bwd(const void* h, const float* weight, const int32_t* lengths, const void* dy, const void* dh, void* dx,
+                   float* dweight, const falcon_rms_dims_t* dims, const int64_t* strides, float eps, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of falcon_rms_bwd (partial sums of dweight); 0 for invalid dims. Host only. */
+size_t falcon_rms_bwd_workspace_bytes(const falcon_rms_dims_t* dims);
+
 /* ABI version of this header: 4. Functions that are added beside the others leave it as it is (falcon_glr_fwd and
  * those behind it were): a caller that may meet an older library looks their symbols up. */
 int falcon_abi_version(void);

@@ -1,0 +1,307 @@
+// Gated delta rule, forward: the chunks' maps (gdr_prep), the scan over them (gdr_scan), the outputs (gdr_out), and
+// short sequences token by token (gdr_step). The algebra is in falcon_gdr.cuh.
+
+#include "falcon.h"
+#include "falcon_gdr.cuh"
+#include "falcon_gdr_bwd.cuh"
+
+namespace falcon {
+namespace gdr {
+namespace {
+
+// ---- outputs of one chunk: out = scale diag(e^G) Q S + P U, U = diag(beta) X (V - diag(e^G) K S). From bf16 inputs
+// every operand is rounded to tf32 once, whose steps are an eighth of the result's; from fp32 ones it is whole.
+template <typename E>
+struct OutArgs {
+    Sizes n;
+    Ten<const E> q, k, v;
+    Ten<E> out;
+    Ten<float> beta, g;
+    const float *X, *S;
+};
+
+template <typename E, int NK>
+__global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
+    constexpr int PI = sizeof(E) == 2 ? kExact : kFull;
+    constexpr int PW = PI;                                    // tiles that were rounded where they were written
+    constexpr int PR = sizeof(E) == 2 ? kRound : kFull;       // registers
+    extern __shared__ __align__(16) float smem[];
+    __shared__ Scal s;
+    float* K = smem;
+    float* Q = K + NK * kTile;
+    float* X = Q + NK * kTile;
+    float* W = X + kTile;
+    const Lane ln;
+    const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
+    const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
+    const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
+    const long long t0 = (long long)c * kC;
+    const int NV = (a.n.dv + kC - 1) / kC;
+    float acc[8][4];
+    if (live <= 0) {
+        zero(acc);
+        for (int sb = 0; sb < NV; ++sb)
+            write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, acc, ln, rows, 0, a.n.dv - sb * kC);
+        return;
+    }
+    const float* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * kTile);
+    copy_tile(W, St);
+    commit();
+    copy_tile(X, a.X + (bh * a.n.NC + c) * kTile);
+    commit();
+    load_scal(s, a.beta, a.g, b, h, t0, live);
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) {
+        load_tile(K + kb * kTile, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
+        load_tile(Q + kb * kTile, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
+    }
+    wait<1>();
+    __syncthreads();
+    float P[8][4];
+    zero(P);
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Q + kb * kTile, rb, K + kb * kTile, ln, 0, 8, 0, 2 * rb + 2);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
+            P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
+        }
+#pragma unroll 1
+    for (int sb = 0; sb < NV; ++sb) {
+        float o[8][4];
+        zero(acc);
+        zero(o);
+#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) {
+            if (sb + kb > 0) {
+                __syncthreads();
+                copy_tile(W, St + (sb * NK + kb) * kTile);
+                commit();
+                wait<0>();
+                __syncthreads();
+            }
+            mm<PI, PW, false, false>(acc, K + kb * kTile, rb, W, ln);
+            mm<PI, PW, false, false>(o, Q + kb * kTile, rb, W, ln);
+        }
+        wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int row = 16 * rb + ln.r + 8 * hf;
+            const float eG = s.eG[row];
+            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const int col = 8 * nt + 2 * ln.j;
+                const float2 v = row < live ? load2(pv + col, a.n.dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
+                float x = fmaf(-eG, acc[nt][2 * hf], v.x), y = fmaf(-eG, acc[nt][2 * hf + 1], v.y);
+                if (PI == kExact) x = __uint_as_float(tf32(x)), y = __uint_as_float(tf32(y));
+                acc[nt][2 * hf] = x;
+                acc[nt][2 * hf + 1] = y;
+                o[nt][2 * hf] *= eG * a.n.scale;
+                o[nt][2 * hf + 1] *= eG * a.n.scale;
+            }
+        }
+        put(W, rb, acc, ln);
+        __syncthreads();
+        zero(acc);
+        mm<PW, PW, false, true>(acc, X, rb, W, ln, 0, 2 * rb + 2);
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float u = acc[nt][e] * s.beta[16 * rb + ln.r + 8 * (e >> 1)];
+                acc[nt][e] = PI == kExact ? __uint_as_float(tf32(u)) : u;
+            }
+        put(W, rb, acc, ln);
+        __syncthreads();
+        mmr<PR, PW, true>(o, P, W, ln, 0, 2 * rb + 2);
+        write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, o, ln, rows, live, a.n.dv - sb * kC);
+    }
+}
+
+// ---- short sequences: a warp holds 16 columns of a head's state, 8 groups of R rows x 4 columns, and walks the
+// tokens. Bound by the state's bytes, read and written once; every load of them is in flight before the first use.
+template <typename E>
+struct StepArgs {
+    Sizes n;
+    Ten<const E> q, k, v;
+    Ten<E> out;
+    Ten<float> beta, g;
+    const float* S0;
+    float* S;
+    long long tiles;  // warps
+    int cols;         // of 16 a head
+    bool vec;         // states in 16-byte pieces
+};
+
+template <typename E, int R>
+__global__ void __launch_bounds__(kThreads) gdr_step(const StepArgs<E> a) {
+    const long long id = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (id >= a.tiles) return;
+    const int l = threadIdx.x & 31, c0 = 16 * (int)(id % a.cols) + 4 * (l & 3), rg = l >> 2;
+    const long long bh = id / a.cols, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const int live = length_of(a.n, b), dk = a.n.dk, dv = a.n.dv;
+    float S[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int row = 8 * i + rg;
+        S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
+        if (!a.S0 || row >= dk || c0 >= dv) continue;
+        const float* p = a.S0 + (bh * dk + row) * dv + c0;
+        if (a.vec) {
+            const float4 x = *reinterpret_cast<const float4*>(p);
+            S[i][0] = x.x, S[i][1] = x.y, S[i][2] = x.z, S[i][3] = x.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c0 + e < dv) S[i][e] = p[e];
+        }
+    }
+    for (int t = 0; t < a.n.T; ++t) {
+        E* po = a.out.row0(b, h, t) + c0;
+        if (t >= live) {
+            if (rg == 0) store2(po, 0.f, 0.f, dv - c0, a.out.pair), store2(po + 2, 0.f, 0.f, dv - c0 - 2, a.out.pair);
+            continue;
+        }
+        const E* pk = a.k.row0(b, hk, t);
+        const E* pq = a.q.row0(b, hk, t);
+        const E* pv = a.v.row0(b, h, t) + c0;
+        const float2 v0 = load2(pv, dv - c0, a.v.pair), v1 = load2(pv + 2, dv - c0 - 2, a.v.pair);
+        const float v[4] = {v0.x, v0.y, v1.x, v1.y};
+        const float beta = *a.beta.row0(b, h, t), dec = expf(*a.g.row0(b, h, t));
+        float k[R], x[9];  // S^T k, S^T q, k.q
+#pragma unroll
+        for (int e = 0; e < 9; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = 8 * i + rg;
+            k[i] = row < dk ? to_f(pk[row]) : 0.f;
+            const float q = row < dk ? to_f(pq[row]) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[i][e] *= dec;
+                x[e] = fmaf(S[i][e], k[i], x[e]);
+                x[4 + e] = fmaf(S[i][e], q, x[4 + e]);
+            }
+            x[8] = fmaf(k[i], q, x[8]);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int e = 0; e < 9; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], d);
+        float u[4], o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            u[e] = beta * (v[e] - x[e]);
+            o[e] = a.n.scale * fmaf(x[8], u[e], x[4 + e]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) S[i][e] = fmaf(k[i], u[e], S[i][e]);
+        }
+        if (rg == 0) store2(po, o[0], o[1], dv - c0, a.out.pair), store2(po + 2, o[2], o[3], dv - c0 - 2, a.out.pair);
+    }
+    if (!a.S) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int row = 8 * i + rg;
+        if (row >= dk || c0 >= dv) continue;
+        float* p = a.S + (bh * dk + row) * dv + c0;
+        if (a.vec) {
+            *reinterpret_cast<float4*>(p) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c0 + e < dv) p[e] = S[i][e];
+        }
+    }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename E>
+int launch_step(const GdrArgs& a, cudaStream_t st) {
+    StepArgs<E> p = {};
+    p.n = sizes_of(a, Layout{});
+    p.q = ten<const E>(a.q, a.n.dk);
+    p.k = ten<const E>(a.k, a.n.dk);
+    p.v = ten<const E>(a.v, a.n.dv);
+    p.out = ten<E>(a.out, a.n.dv);
+    p.beta = ten<float>(a.beta, 1);
+    p.g = ten<float>(a.g, 1);
+    p.S0 = a.S0;
+    p.S = a.S_final;
+    p.cols = (a.n.dv + 15) / 16;
+    p.tiles = p.n.BH * p.cols;
+    p.vec = a.n.dv % 4 == 0 && al16(a.S0) && al16(a.S_final);
+    const unsigned grid = (unsigned)((p.tiles + kThreads / 32 - 1) / (kThreads / 32));
+    if (a.n.dk <= 64) gdr_step<E, 8><<<grid, kThreads, 0, st>>>(p);
+    else gdr_step<E, 16><<<grid, kThreads, 0, st>>>(p);
+    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+template <typename E, int NK>
+int launch_chunks(const GdrArgs& a, const Layout& l, cudaStream_t st) {
+    const Sizes n = sizes_of(a, l);
+    PrepArgs<E> p = {};
+    p.n = n;
+    p.k = ten<const E>(a.k, a.n.dk);
+    p.v = ten<const E>(a.v, a.n.dv);
+    p.beta = ten<float>(a.beta, 1);
+    p.g = ten<float>(a.g, 1);
+    p.X = a.ws + l.X;
+    p.M = a.ws + l.M;
+    p.A = a.ws + l.S;
+    OutArgs<E> o = {};
+    o.n = n;
+    o.q = ten<const E>(a.q, a.n.dk);
+    o.k = p.k;
+    o.v = p.v;
+    o.out = ten<E>(a.out, a.n.dv);
+    o.beta = p.beta;
+    o.g = p.g;
+    o.X = p.X;
+    o.S = p.A;
+    const int prep = (NK + 2) * kTile * 4, out = (2 * NK + 2) * kTile * 4;
+    if (!want_smem(gdr_prep<E, NK, false>, prep) || !want_smem(gdr_out<E, NK>, out)) return FALCON_ERR_CUDA;
+    const unsigned grid = (unsigned)(n.BH * l.NC);
+    gdr_prep<E, NK, false><<<grid, kThreads, prep, st>>>(p);
+    if (!run_scan<NK, false>(n, l, a.ws, a.S0, a.S_final, false, sizeof(E) == 2, st)) return FALCON_ERR_CUDA;
+    gdr_out<E, NK><<<grid, kThreads, out, st>>>(o);
+    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+template <typename E>
+int launch_fwd(const GdrArgs& a, cudaStream_t st) {
+    if (a.n.T <= kGdrStepT) return launch_step<E>(a, st);
+    const Layout l = layout_of(a.n, false);
+    return l.NK == 1 ? launch_chunks<E, 1>(a, l, st) : launch_chunks<E, 2>(a, l, st);
+}
+
+}  // namespace
+}  // namespace gdr
+
+unsigned long long gdr_fwd_workspace(const GdrSizes& n) {
+    return n.T <= kGdrStepT ? 0 : (unsigned long long)gdr::layout_of(n, false).total * 4;
+}
+
+bool gdr_fits(const GdrSizes& n) {
+    const long long BH = n.B * n.H, most = 0x7fffffff;
+    const long long NC = (n.T + gdr::kC - 1) / gdr::kC;
+    return BH <= most / 8 && BH * (NC > 0 ? NC : 1) <= most;
+}
+
+int launch_gdr_fwd(const GdrArgs& a, cudaStream_t s) { return a.n.bf16 ? gdr::launch_fwd<gdr::bf16>(a, s) : gdr::launch_fwd<float>(a, s); }
+
+unsigned long long gdr_bwd_workspace(const GdrSizes& n) { return (unsigned long long)gdr::layout_of(n, true).total * 4; }
+
+int launch_gdr_bwd(const GdrArgs& a, cudaStream_t s) {
+    const bool one = a.n.dk <= gdr::kC;
+    if (a.n.bf16) return one ? gdr::launch_bwd<gdr::bf16, 1>(a, s) : gdr::launch_bwd<gdr::bf16, 2>(a, s);
+    return one ? gdr::launch_bwd<float, 1>(a, s) : gdr::launch_bwd<float, 2>(a, s);
+}
+
+}  // namespace falcon

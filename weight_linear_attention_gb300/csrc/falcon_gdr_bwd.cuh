@@ -1,0 +1,400 @@
+// Gated delta rule, backward. With the notation of falcon_gdr.cuh, dO the output's adjoint, dS' that of the state
+// behind a chunk:
+//   dU = P^T dO + diag(w) K dS',   Z = X^T diag(beta) dU = dV,
+//   dS = e^{G_C} dS' + scale Q^T diag(e^G) dO - K^T diag(e^G) Z = M^T dS' + dA,
+//   dP_ij = scale D_ij beta_j dO_i.E_j (j <= i),   H_ij = -D_ij beta_j Z_i.E_j (j < i), H symmetric,
+//   dQ = scale diag(e^G) dO S^T + dP K,
+//   dK = dP^T Q + H K - diag(e^G) Z S^T + diag(w beta) E dS'^T,
+//   dbeta_j = E_j.(dU - N^T Z)_j.
+// The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
+// writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
+// from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
+// gdr_grad takes the gradients, all chunks at once.
+
+#pragma once
+
+#include "falcon.h"
+#include "falcon_gdr.cuh"
+
+namespace falcon {
+namespace gdr {
+
+template <typename E>
+struct GradArgs {
+    Sizes n;
+    Ten<const E> q, k, v, dout;
+    Ten<float> beta, g, dbeta, dg;
+    Ten<E> dq, dk, dv;
+    float *pq, *pk;  // [B,H,T,dk] instead of dq and dk where heads share theirs, or null
+    const float *X, *S, *dS;
+};
+
+template <int NK, int NV>
+constexpr int grad_smem() { return (NK + 3 * NV + 2) * kTile * 4; }
+
+// x and y summed over the four lanes that hold a row.
+__device__ __forceinline__ float row_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+template <typename E, int NK, int NV>
+__global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
+    constexpr bool ONE = NK * NV == 1;  // one tile of S and dS': both stay
+    constexpr int PI = sizeof(E) == 2 ? kExact : kFull;
+    // operands that reach only dK, rounded to bf16: its steps are eight of tf32's
+    constexpr int PL = sizeof(E) == 2 ? kRound : kFull;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ Scal s;
+    __shared__ float own[kC], dbe[kC], part[kThreads / 32];
+    float* K = smem;
+    float* dO = K + NK * kTile;
+    float* Et = dO + NV * kTile;
+    float* Zt = Et + NV * kTile;
+    float* W0 = Zt + NV * kTile;
+    float* W1 = W0 + kTile;
+    const Lane ln;
+    const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
+    const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
+    const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
+    const int dk = a.n.dk, dv = a.n.dv;
+    const long long t0 = (long long)c * kC;
+    auto write_qk = [&](const Ten<E>& t, float* p, const float (&x)[8][4], int kb) {
+        if (p) write_rows(p + (bh * a.n.T + t0) * dk + kb * kC, (long long)dk, dk % 2 == 0, rb, x, ln, rows, live, dk - kb * kC);
+        else write_rows(t.row0(b, hk, t0) + kb * kC, t.st, t.pair, rb, x, ln, rows, live, dk - kb * kC);
+    };
+    float x[8][4], d[8][4];
+    if (live <= 0) {
+        zero(x);
+        for (int kb = 0; kb < NK; ++kb) {
+            write_qk(a.dq, a.pq, x, kb);
+            write_qk(a.dk, a.pk, x, kb);
+        }
+        for (int sb = 0; sb < NV; ++sb) write_rows(a.dv.row0(b, h, t0) + sb * kC, a.dv.st, a.dv.pair, rb, x, ln, rows, 0, dv - sb * kC);
+        if (threadIdx.x < rows) {
+            *a.dbeta.row0(b, h, t0 + threadIdx.x) = 0.f;
+            *a.dg.row0(b, h, t0 + threadIdx.x) = 0.f;
+        }
+        return;
+    }
+    const long long st = (long long)NV * NK * kTile;
+    const float* St = a.S + (bh * (a.n.NC + 1) + c) * st;  // the state behind the chunk lies st further
+    const float* dSt = a.dS + (bh * a.n.NC + c) * st;
+    const float* Xt = a.X + (bh * a.n.NC + c) * kTile;
+    copy_tile(W0, St);
+    copy_tile(W1, dSt);
+    commit();
+    load_scal(s, a.beta, a.g, b, h, t0, live);
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) load_tile(K + kb * kTile, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, dk - kb * kC, a.k.vec);
+#pragma unroll 1
+    for (int sb = 0; sb < NV; ++sb) load_tile(dO + sb * kTile, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
+    // P transposed: rows j, columns i >= j
+    float P[8][4];
+    zero(P);
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) {
+        if (kb > 0) __syncthreads();
+        load_tile(Et, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
+        __syncthreads();
+        mm<PI, PI, false, false>(P, K + kb * kTile, rb, Et, ln, 0, 8, 2 * rb, 8);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
+            P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
+        }
+    float ends = 0.f;                               // <dS', S'>
+    float sb_[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};  // the rows' dbeta and dV.V
+#pragma unroll 1
+    for (int sb = 0; sb < NV; ++sb) {
+        zero(x);
+        zero(d);
+#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) {
+            if (sb + kb > 0) {
+                __syncthreads();
+                copy_tile(W0, St + (sb * NK + kb) * kTile);
+                copy_tile(W1, dSt + (sb * NK + kb) * kTile);
+                commit();
+            }
+            wait<0>();
+            __syncthreads();
+            mm<PI, kFull, false, false>(x, K + kb * kTile, rb, W0, ln);
+            mm<PI, kFull, false, false>(d, K + kb * kTile, rb, W1, ln);
+            const float* S1 = St + st + (sb * NK + kb) * kTile;
+#pragma unroll
+            for (int i = 0; i < kTile / 4 / kThreads; ++i) {
+                const int o = 4 * (threadIdx.x + i * kThreads);
+                const float4 u = *reinterpret_cast<const float4*>(S1 + o), v = *reinterpret_cast<const float4*>(W1 + o);
+                ends += (u.x * v.x + u.y * v.y) + (u.z * v.z + u.w * v.w);
+            }
+        }
+        __syncthreads();  // Q in E's place, dS' and the states are read
+        copy_tile(W1, Xt);
+        commit();
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
+        mmr<kFull, PI, true>(d, P, dO + sb * kTile, ln, 2 * rb, 8);  // dU
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int row = 16 * rb + ln.r + 8 * hf;
+            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const int col = 8 * nt + 2 * ln.j;
+                const float2 v = row < live ? load2(pv + col, dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
+                x[nt][2 * hf] = fmaf(-s.eG[row], x[nt][2 * hf], v.x);
+                x[nt][2 * hf + 1] = fmaf(-s.eG[row], x[nt][2 * hf + 1], v.y);
+            }
+        }
+        float* Es = Et + sb * kTile;
+        float* Zs = Zt + sb * kTile;
+        put(Es, rb, x, ln);
+        float z[8][4];
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e] = d[nt][e] * s.beta[16 * rb + ln.r + 8 * (e >> 1)];
+        put(Zs, rb, z, ln);
+        wait<0>();
+        __syncthreads();
+        zero(x);
+        zero(z);
+        mm<kFull, kFull, false, true>(x, W1, rb, Es, ln, 0, 2 * rb + 2);  // E
+        mm<kFull, kFull, true, true>(z, W1, rb, Zs, ln, 2 * rb, 8);       // Z
+        __syncthreads();
+        put(Es, rb, x, ln);
+        put(Zs, rb, z, ln);
+        if (ONE) {
+            copy_tile(W1, dSt);
+            commit();
+        }
+        write_rows(a.dv.row0(b, h, t0) + sb * kC, a.dv.st, a.dv.pair, rb, z, ln, rows, live, dv - sb * kC);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int row = 16 * rb + ln.r + 8 * hf;
+            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const int col = 8 * nt + 2 * ln.j;
+                const float2 v = row < live ? load2(pv + col, dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
+                sv[hf] = fmaf(z[nt][2 * hf], v.x, fmaf(z[nt][2 * hf + 1], v.y, sv[hf]));
+            }
+        }
+        __syncthreads();
+        // N transposed: rows j, columns i > j
+        float N[8][4];
+        zero(N);
+#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(N, K + kb * kTile, rb, K + kb * kTile, ln, 0, 8, 2 * rb, 8);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
+                N[nt][e] = j < i ? N[nt][e] * decay(s, i, j) : 0.f;
+            }
+        zero(z);
+        mmr<kFull, kFull, true>(z, N, Zs, ln, 2 * rb, 8);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sb_[e >> 1] = fmaf(x[nt][e], d[nt][e] - z[nt][e], sb_[e >> 1]);
+    }
+    // dP, its transpose, and H
+    float A1[8][4], A3[8][4], H[8][4];
+    zero(A1);
+    zero(A3);
+    zero(H);
+    zero(x);
+#pragma unroll 1
+    for (int sb = 0; sb < NV; ++sb) {
+        const float *Es = Et + sb * kTile, *Zs = Zt + sb * kTile, *Os = dO + sb * kTile;
+        mm<PI, kFull, false, false>(A1, Os, rb, Es, ln, 0, 8, 0, 2 * rb + 2);
+        mm<PL, PI, false, false>(A3, Es, rb, Os, ln, 0, 8, 2 * rb, 8);
+        mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 8, 0, 2 * rb + 2);
+        mm<PL, PL, false, false>(x, Es, rb, Zs, ln, 0, 8, 2 * rb, 8);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int m = 16 * rb + ln.r + 8 * (e >> 1), n = 8 * nt + 2 * ln.j + (e & 1);
+            const float f = m >= n ? decay(s, m, n) * s.beta[n] : decay(s, n, m) * s.beta[m];
+            A1[nt][e] = m >= n ? A1[nt][e] * f * a.n.scale : 0.f;
+            A3[nt][e] = m <= n ? A3[nt][e] * f * a.n.scale : 0.f;
+            H[nt][e] = m == n ? 0.f : (m > n ? H[nt][e] : x[nt][e]) * -f;
+        }
+    float sq[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) {
+        zero(x);
+        zero(d);
+        float t[8][4];
+        zero(t);
+#pragma unroll 1
+        for (int sb = 0; sb < NV; ++sb) {
+            if (!ONE) {
+                __syncthreads();
+                copy_tile(W0, St + (sb * NK + kb) * kTile);
+                copy_tile(W1, dSt + (sb * NK + kb) * kTile);
+                commit();
+            }
+            wait<0>();
+            __syncthreads();
+            mm<PI, kFull, false, true>(x, dO + sb * kTile, rb, W0, ln);
+            mm<PL, PL, false, true>(d, Zt + sb * kTile, rb, W0, ln);
+            mm<PL, PL, false, true>(t, Et + sb * kTile, rb, W1, ln);
+        }
+        __syncthreads();
+        load_tile(W0, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * rb + ln.r + 8 * (e >> 1);
+                x[nt][e] *= s.eG[row] * a.n.scale;
+                d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
+            }
+        mmr<kFull, PI, true>(x, A1, K + kb * kTile, ln, 0, 2 * rb + 2);
+        write_qk(a.dq, a.pq, x, kb);
+        mmr<PL, PI, true>(d, H, K + kb * kTile, ln);
+        __syncthreads();
+        mmr<PL, PI, true>(d, A3, W0, ln, 2 * rb, 8);
+        write_qk(a.dk, a.pk, d, kb);
+        get(W0, rb, t, ln);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sq[e >> 1] = fmaf(x[nt][e], t[nt][e], sq[e >> 1]);
+    }
+    // the rows' sums: own = dQ.Q - dV.V, and the ends'
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int row = 16 * rb + ln.r + 8 * hf;
+        const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]);
+        if (ln.j == 0) own[row] = o, dbe[row] = e;
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) ends += __shfl_xor_sync(0xffffffffu, ends, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ends;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    const int l = threadIdx.x;
+    double sum = (double)own[2 * l] + own[2 * l + 1];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const double o = __shfl_down_sync(0xffffffffu, sum, m);
+        if (l + m < 32) sum += o;
+    }
+    const double all = ((double)part[0] + part[1]) + ((double)part[2] + part[3]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int t = 2 * l + e;
+        if (t >= rows) continue;
+        const bool in = t < live;
+        *a.dbeta.row0(b, h, t0 + t) = in ? dbe[t] : 0.f;
+        // a decay of 0 keeps nothing: its gradient is 0, not what rounding leaves of the sum
+        const bool kept = in && !(expf(*a.g.row0(b, h, t0 + t)) == 0.f);
+        *a.dg.row0(b, h, t0 + t) = kept ? (float)((e ? sum - own[2 * l] : sum) + all) : 0.f;
+    }
+}
+
+// ---- dq and dk of shared heads: the sums over the heads that share them, in their order
+template <typename E>
+struct SumArgs {
+    const float* part;  // [B,Hk,group,T,dk]
+    Ten<E> to;
+    long long count;    // rows: B Hk T
+    int Hk, group, T, dk;
+};
+template <typename E>
+__global__ void __launch_bounds__(256) gdr_sum(const SumArgs<E> a, const SumArgs<E> a2) {
+    const SumArgs<E>& p = blockIdx.y ? a2 : a;
+    const int l = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= p.count) return;
+    const long long bk = row / p.T, t = row % p.T;
+    const float* src = p.part + (bk * p.group * p.T + t) * p.dk;
+    E* dst = p.to.row0(bk / p.Hk, bk % p.Hk, t);
+    for (int i = 2 * l; i < p.dk; i += 64) {
+        float2 s = make_float2(0.f, 0.f);
+        for (int m = 0; m < p.group; ++m) {
+            const float2 v = load2(src + (long long)m * p.T * p.dk + i, p.dk - i, p.dk % 2 == 0);
+            s.x += v.x;
+            s.y += v.y;
+        }
+        store2(dst + i, s.x, s.y, p.dk - i, p.to.pair);
+    }
+}
+
+template <typename E, int NK>
+int launch_bwd(const GdrArgs& a, cudaStream_t st) {
+    const Layout l = layout_of(a.n, true);
+    const Sizes n = sizes_of(a, l);
+    const unsigned grid = (unsigned)(n.BH * l.NC);
+    PrepArgs<E> p = {};
+    p.n = n;
+    p.q = ten<const E>(a.q, a.n.dk);
+    p.k = ten<const E>(a.k, a.n.dk);
+    p.v = ten<const E>(a.v, a.n.dv);
+    p.dout = ten<const E>(a.dout, a.n.dv);
+    p.beta = ten<float>(a.beta, 1);
+    p.g = ten<float>(a.g, 1);
+    p.X = a.ws + l.X;
+    p.M = a.ws + l.M;
+    p.A = a.ws + l.S;
+    p.dA = a.ws + l.dA;
+    const int prep = (2 * NK + 3) * kTile * 4;
+    if (!want_smem(gdr_prep<E, NK, true>, prep)) return FALCON_ERR_CUDA;
+    if (grid) {
+        gdr_prep<E, NK, true><<<grid, kThreads, prep, st>>>(p);
+        if (!run_scan<NK, false>(n, l, a.ws, a.S0, nullptr, true, false, st)) return FALCON_ERR_CUDA;
+    }
+    if (!run_scan<NK, true>(n, l, a.ws, a.dS_final, a.dS0, false, false, st)) return FALCON_ERR_CUDA;
+    if (grid) {
+        GradArgs<E> g = {};
+        g.n = n;
+        g.q = p.q, g.k = p.k, g.v = p.v, g.dout = p.dout, g.beta = p.beta, g.g = p.g;
+        g.dbeta = ten<float>(a.dbeta, 1);
+        g.dg = ten<float>(a.dg, 1);
+        g.dq = ten<E>(a.dq, a.n.dk);
+        g.dk = ten<E>(a.dk, a.n.dk);
+        g.dv = ten<E>(a.dv, a.n.dv);
+        const bool shared = n.group > 1;
+        g.pq = shared ? a.ws + l.dq : nullptr;
+        g.pk = shared ? a.ws + l.dk : nullptr;
+        g.X = p.X;
+        g.S = p.A;
+        g.dS = p.dA;
+        if (l.NV == 1) {
+            if (!want_smem(gdr_grad<E, NK, 1>, grad_smem<NK, 1>())) return FALCON_ERR_CUDA;
+            gdr_grad<E, NK, 1><<<grid, kThreads, grad_smem<NK, 1>(), st>>>(g);
+        } else {
+            if (!want_smem(gdr_grad<E, NK, 2>, grad_smem<NK, 2>())) return FALCON_ERR_CUDA;
+            gdr_grad<E, NK, 2><<<grid, kThreads, grad_smem<NK, 2>(), st>>>(g);
+        }
+        if (shared) {
+            SumArgs<E> q = {a.ws + l.dq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
+            k.part = a.ws + l.dk;
+            k.to = g.dk;
+            gdr_sum<E><<<dim3((unsigned)((q.count + 7) / 8), 2), 256, 0, st>>>(q, k);
+        }
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+// One translation unit for each, to be compiled side by side.
+extern template int launch_bwd<bf16, 1>(const GdrArgs&, cudaStream_t);
+extern template int launch_bwd<bf16, 2>(const GdrArgs&, cudaStream_t);
+extern template int launch_bwd<float, 1>(const GdrArgs&, cudaStream_t);
+extern template int launch_bwd<float, 2>(const GdrArgs&, cudaStream_t);
+
+}  // namespace gdr
+}  // namespace falcon

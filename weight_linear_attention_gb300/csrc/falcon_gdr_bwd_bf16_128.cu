@@ -1,0 +1,11 @@
+// Gated delta rule, backward: bfloat16 inputs, dk up to 128. See falcon_gdr_bwd.cuh.
+
+#include "falcon_gdr_bwd.cuh"
+
+namespace falcon {
+namespace gdr {
+
+template int launch_bwd<bf16, 2>(const GdrArgs&, cudaStream_t);
+
+}  // namespace gdr
+}  // namespace falcon

@@ -1,0 +1,371 @@
+// Root-mean-square norm of a token's d channels with the residual's addition, forward and backward.
+//   h = x + residual (rounded to their type, as it is stored),  r = 1 / sqrt(mean h^2 + eps),  y = weight h r,
+//   y in their type or, with s = max |y| / 448, as e4m3 values y / s;
+//   p = weight dy,  dx = r (p - h r^2 mean(p h)) + dh,  dweight = sum over tokens of dy h r.
+// A token's channels stay in registers from their one read to their one write, in the lanes of one warp (up to 1024
+// of bf16) or of all warps of a CTA; the next token's are on their way meanwhile. Bound by the bytes.
+
+#include <cuda_fp8.h>
+
+#include "falcon.h"
+#include "falcon_rms.h"
+#include "falcon_seq.cuh"
+
+namespace falcon {
+namespace rms {
+namespace {
+
+using namespace seq;
+
+constexpr int kWarps = 4;       // of a CTA whose warps have a token each
+constexpr int kMost = 512;      // threads of a CTA that has one token
+constexpr int kSms = 152;
+
+struct Args {
+    RmsArgs a;
+    long long rows;
+};
+
+// The place of a token, and whether it lies inside its sequence.
+struct Row {
+    long long b;
+    int t;
+    bool live;
+};
+__device__ __forceinline__ Row row_of(const RmsArgs& a, long long row) {
+    Row r;
+    const unsigned q = (unsigned)row / (unsigned)a.T;
+    r.b = q;
+    r.t = (int)((unsigned)row - q * (unsigned)a.T);
+    r.live = !a.lengths || r.t < a.lengths[q];
+    return r;
+}
+__device__ __forceinline__ long long offset(const RowView& v, const Row& r) { return r.b * v.sb + r.t * v.st; }
+
+// NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sums (or, with MAX, maxima) over the lanes that hold a token: every one gets the same bits. `slot` of shared memory
+// is left alone until the next call but one.
+template <bool MULTI, bool MAX, int N>
+__device__ __forceinline__ void reduce(float (&v)[N], float* slot) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[i], m);
+            v[i] = MAX ? max_nan(v[i], o) : v[i] + o;
+        }
+    if (!MULTI) return;
+    const int w = threadIdx.x >> 5, n = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) slot[i * 32 + w] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float s = slot[i * 32];
+        for (int k = 1; k < n; ++k) s = MAX ? max_nan(s, slot[i * 32 + k]) : s + slot[i * 32 + k];
+        v[i] = s;
+    }
+}
+
+template <typename E, int W, int N>
+struct Line {
+    Pack<E, W> v[N];
+    // Vectors first, first + step, ... of the d / W of a token at p; nothing is read of one that is not live.
+    __device__ __forceinline__ void fetch(const void* p, long long off, int first, int step, int count, bool live) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (live && first + i * step < count) v[i] = load<E, W>(p, off + (long long)(first + i * step) * W);
+            else zero(v[i]);
+        }
+    }
+};
+
+template <int W>
+__device__ __forceinline__ void store8(uint8_t* p, const float* v) {
+    if (W == 1) {
+        *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint32_t u[W / 4 > 0 ? W / 4 : 1];
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+            u[i] = lo | hi << 16;
+        }
+        if (W == 8) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[W / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(p) = u[0];
+    }
+}
+
+template <typename E, int W, int N, bool MULTI, bool EIGHT>
+__global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Args g) {
+    __shared__ float slots[2][2][32];
+    const RmsArgs& a = g.a;
+    const int step = MULTI ? blockDim.x : 32, first = MULTI ? threadIdx.x : threadIdx.x & 31;
+    const int count = a.d / W;
+    const long long stride = MULTI ? gridDim.x : (long long)gridDim.x * kWarps;
+    long long row = MULTI ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (row >= g.rows) return;
+    float wt[N * W];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int c = (first + i * step) * W + e;
+            wt[i * W + e] = a.weight && c < a.d ? a.weight[c] : 1.f;
+        }
+    Line<E, W, N> x, r;
+    Row at = row_of(a, row);
+    x.fetch(a.x.p, offset(a.x, at), first, step, count, at.live);
+    if (a.residual.p) r.fetch(a.residual.p, offset(a.residual, at), first, step, count, at.live);
+    const float inv_d = 1.f / a.d;
+    for (int turn = 0;; turn ^= 1) {
+        float h[N * W], s[1] = {0.f};
+        if (a.residual.p) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) h[i * W + e] = elem(x.v[i], e) + elem(r.v[i], e);
+                pack(x.v[i], h + i * W);  // as it is stored is how it is normalised
+                if (a.h.p && first + i * step < count)
+                    store<E, W>(a.h.p, offset(a.h, at) + (long long)(first + i * step) * W, x.v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                h[i * W + e] = elem(x.v[i], e);
+                s[0] = fmaf(h[i * W + e], h[i * W + e], s[0]);
+            }
+        const Row now = at;
+        const long long here = row;
+        row += stride;
+        if (row < g.rows) {
+            at = row_of(a, row);
+            x.fetch(a.x.p, offset(a.x, at), first, step, count, at.live);
+            if (a.residual.p) r.fetch(a.residual.p, offset(a.residual, at), first, step, count, at.live);
+        }
+        reduce<MULTI, false>(s, slots[turn][0]);
+        const float rstd = 1.f / sqrtf(fmaf(s[0], inv_d, a.eps));
+        float top[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < N * W; ++i) {
+            h[i] = h[i] * rstd * wt[i];
+            if (EIGHT) top[0] = max_nan(top[0], fabsf(h[i]));
+        }
+        const long long oy = offset(a.y, now);
+        if (!EIGHT) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (first + i * step >= count) continue;
+                Pack<E, W> o;
+                if (now.live) pack(o, h + i * W);
+                else zero(o);
+                store<E, W>(a.y.p, oy + (long long)(first + i * step) * W, o);
+            }
+        } else {
+            reduce<MULTI, true>(top, slots[turn][1]);
+            const float scale = now.live ? top[0] * (1.f / 448.f) : 0.f;
+            if (first == 0) a.scales[here] = scale;
+            // 1 / scale where it is not near overflow (NaN too), else the quotients themselves; a row of zeros stays 0
+            const bool tiny = scale < 1e-37f;
+            const float inv = tiny ? 0.f : 1.f / scale;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (first + i * step >= count) continue;
+                float q[W];
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    q[e] = !now.live ? 0.f : !tiny ? h[i * W + e] * inv : scale > 0.f ? h[i * W + e] / scale : 0.f;
+                store8<W>(static_cast<uint8_t*>(a.y.p) + oy + (long long)(first + i * step) * W, q);
+            }
+        }
+        if (row >= g.rows) return;
+    }
+}
+
+// dweight's sums: a lane adds up its own channels over the CTA's tokens, then the CTA's warps in their order, and
+// rms_sum the CTAs in theirs.
+template <typename E, int W, int N, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_bwd(const Args g) {
+    extern __shared__ __align__(16) float sums[];
+    __shared__ float slots[2][2 * 32];
+    const RmsArgs& a = g.a;
+    const int step = MULTI ? blockDim.x : 32, first = MULTI ? threadIdx.x : threadIdx.x & 31;
+    const int count = a.d / W;
+    const long long stride = MULTI ? gridDim.x : (long long)gridDim.x * kWarps;
+    long long row = MULTI ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    float wt[N * W], acc[N * W];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const int c = (first + i * step) * W + e;
+            wt[i * W + e] = a.weight && c < a.d ? a.weight[c] : 1.f;
+            acc[i * W + e] = 0.f;
+        }
+    const float inv_d = 1.f / a.d;
+    Line<E, W, N> x, dy, dh;
+    Row at = {};
+    auto fetch = [&] {
+        if (row >= g.rows) return;
+        at = row_of(a, row);
+        x.fetch(a.x.p, offset(a.x, at), first, step, count, at.live);
+        dy.fetch(a.dy.p, offset(a.dy, at), first, step, count, at.live);
+        if (a.dh.p) dh.fetch(a.dh.p, offset(a.dh, at), first, step, count, at.live);
+    };
+    fetch();
+    for (int turn = 0; row < g.rows; turn ^= 1) {
+        const Line<E, W, N> cx = x, cy = dy, ch = dh;
+        const Row now = at;
+        row += stride;
+        fetch();
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float h = elem(cx.v[i], e), p = elem(cy.v[i], e) * wt[i * W + e];
+                s[0] = fmaf(h, h, s[0]);
+                s[1] = fmaf(p, h, s[1]);
+            }
+        reduce<MULTI, false>(s, slots[turn]);
+        const float rstd = 1.f / sqrtf(fmaf(s[0], inv_d, a.eps)), k = rstd * rstd * (s[1] * inv_d);
+        const long long o = offset(a.dx, now);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float h = elem(cx.v[i], e), y = elem(cy.v[i], e);
+                if (now.live) acc[i * W + e] = fmaf(y, h * rstd, acc[i * W + e]);
+                v[e] = rstd * fmaf(-h, k, y * wt[i * W + e]);
+                if (a.dh.p) v[e] += elem(ch.v[i], e);
+                if (!now.live) v[e] = 0.f;
+            }
+            if (first + i * step >= count) continue;
+            Pack<E, W> u;
+            pack(u, v);
+            store<E, W>(a.dx.p, o + (long long)(first + i * step) * W, u);
+        }
+    }
+    if (!a.ws) return;
+    float* to = a.ws + (long long)blockIdx.x * a.d;
+    if (!MULTI) {
+        for (int w = 0; w < kWarps; ++w) {
+            if ((int)(threadIdx.x >> 5) == w) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        const int c = (first + i * step) * W + e;
+                        if (c < a.d) sums[c] = (w > 0 ? sums[c] : 0.f) + acc[i * W + e];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.d; c += blockDim.x) to[c] = sums[c];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const int c = (first + i * step) * W + e;
+                if (c < a.d) to[c] = acc[i * W + e];
+            }
+    }
+}
+
+__global__ void __launch_bounds__(256) rms_sum(const float* part, int splits, int d, float* out) {
+    __shared__ float s[8][33];
+    const int l = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
+    float v = 0.f;
+    if (c < d)
+        for (int i = w; i < splits; i += 8) v += part[(long long)i * d + c];
+    s[w][l] = v;
+    __syncthreads();
+    if (w == 0 && c < d) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += s[i][l];
+        out[c] = v;
+    }
+}
+
+// Lanes of a token. A vector is 16 bytes where every access can be one, else an element, and a lane holds N of them: as
+// few as keep a token in one warp, or in a CTA's most threads.
+bool vec_ok(const RowView& v, int bytes, int es) {
+    const long long m = bytes / es;
+    return !v.p || (reinterpret_cast<uintptr_t>(v.p) % (uintptr_t)bytes == 0 && v.sb % m == 0 && v.st % m == 0);
+}
+int lanes_of(int d, int per) { return ((d + per - 1) / per + 31) / 32 * 32; }
+
+template <typename E, int W, int N>
+void fwd(const Args& g, cudaStream_t s) {
+    const int lanes = lanes_of(g.a.d, W * N);
+    const bool multi = lanes > 32;
+    const int threads = multi ? lanes : 32 * kWarps;
+    // as many CTAs as are resident at up to 128 registers a thread: each warp goes on to its next token
+    const long long most = (long long)kSms * (512 / threads);
+    const long long want = multi ? g.rows : (g.rows + kWarps - 1) / kWarps;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    if (g.a.eight) {
+        if (multi) rms_fwd<E, W, N, true, true><<<grid, threads, 0, s>>>(g);
+        else rms_fwd<E, W, N, false, true><<<grid, threads, 0, s>>>(g);
+    } else {
+        if (multi) rms_fwd<E, W, N, true, false><<<grid, threads, 0, s>>>(g);
+        else rms_fwd<E, W, N, false, false><<<grid, threads, 0, s>>>(g);
+    }
+}
+template <typename E, int W, int N>
+void bwd(const Args& g, cudaStream_t s) {
+    const int lanes = lanes_of(g.a.d, W * N);
+    const unsigned grid = (unsigned)rms_bwd_splits(g.rows);
+    if (lanes > 32) rms_bwd<E, W, N, true><<<grid, lanes, 0, s>>>(g);
+    else rms_bwd<E, W, N, false><<<grid, 32 * kWarps, g.a.d * 4, s>>>(g);
+}
+
+}  // namespace
+}  // namespace rms
+
+int rms_bwd_splits(long long rows) {
+    const long long most = 2 * rms::kSms;  // two CTAs an SM; what rms_sum reads grows with them
+    return (int)(rows < most ? rows : most);
+}
+
+int launch_rms_fwd(const RmsArgs& a, cudaStream_t s) {
+    using namespace rms;
+    const int es = a.bf16 ? 2 : 4, w = 16 / es;
+    const bool vec = a.d % w == 0 && vec_ok(a.x, 16, es) && vec_ok(a.residual, 16, es) && vec_ok(a.h, 16, es) &&
+                     (a.eight ? vec_ok(a.y, w, 1) : vec_ok(a.y, 16, es));
+    const Args g = {a, a.B * a.T};
+    const bool wide = a.d > kMost * 16;
+    if (a.bf16) vec ? fwd<bf16, 8, 4>(g, s) : wide ? fwd<bf16, 1, 32>(g, s) : fwd<bf16, 1, 16>(g, s);
+    else if (vec) wide ? fwd<float, 4, 8>(g, s) : fwd<float, 4, 4>(g, s);
+    else wide ? fwd<float, 1, 32>(g, s) : fwd<float, 1, 16>(g, s);
+    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+int launch_rms_bwd(const RmsArgs& a, cudaStream_t s) {
+    using namespace rms;
+    const int es = a.bf16 ? 2 : 4, w = 16 / es;
+    const bool vec = a.d % w == 0 && vec_ok(a.x, 16, es) && vec_ok(a.dy, 16, es) && vec_ok(a.dh, 16, es) && vec_ok(a.dx, 16, es);
+    const Args g = {a, a.B * a.T};
+    const bool wide = a.d > kMost * 16;
+    if (a.bf16 && vec) wide || a.d <= 1024 ? bwd<bf16, 8, 4>(g, s) : bwd<bf16, 8, 2>(g, s);
+    else if (a.bf16) wide ? bwd<bf16, 1, 32>(g, s) : bwd<bf16, 1, 16>(g, s);
+    else if (vec) wide ? bwd<float, 4, 8>(g, s) : bwd<float, 4, 4>(g, s);
+    else wide ? bwd<float, 1, 32>(g, s) : bwd<float, 1, 16>(g, s);
+    if (a.ws) rms_sum<<<(a.d + 31) / 32, 256, 0, s>>>(a.ws, rms_bwd_splits(g.rows), a.d, a.dweight);
+    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+}  // namespace falcon

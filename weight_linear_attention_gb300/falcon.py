@@ -22,6 +22,7 @@ from . import build as _build
 
 FALCON_1, FALCON_1A, FALCON_2, FALCON_2A, FALCON_3, FALCON_3A = 1, 2, 3, 4, 5, 6
 FALCON_F32, FALCON_BF16 = 0, 1
+FALCON_E4M3 = 2  # output of the root-mean-square norm only
 FALCON_OK = 0
 FALCON_ERR_INVALID_ARG = 1
 FALCON_ERR_UNSUPPORTED = 2
@@ -69,13 +70,47 @@ class FalconSeqDims(ctypes.Structure):
 
 assert ctypes.sizeof(FalconSeqDims) == 40
 
+
+class FalconGdrDims(ctypes.Structure):
+    """falcon_gdr_dims_t: the sizes of the gated delta rule."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("qk_heads", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("dk", ctypes.c_int64),
+        ("dv", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(FalconGdrDims) == 56
+
+
+class FalconRmsDims(ctypes.Structure):
+    """falcon_rms_dims_t: the sizes of the root-mean-square norm."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("seqlen", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(FalconRmsDims) == 32
+
 _lock = threading.Lock()
 _lib = None
 
 EXPORTED = ("falcon_fwd", "falcon_workspace_bytes", "falcon_fwd_static", "falcon_tail_bytes",
             "falcon_status_string", "falcon_device_status", "falcon_kernel_for", "falcon_abi_version",
             "falcon_bwd", "falcon_bwd_workspace_bytes", "falcon_glr_fwd", "falcon_glr_bwd", "falcon_gn_fwd",
-            "falcon_gn_bwd", "falcon_gn_bwd_workspace_bytes")
+            "falcon_gn_bwd", "falcon_gn_bwd_workspace_bytes", "falcon_gdr_fwd", "falcon_gdr_bwd",
+            "falcon_gdr_workspace_bytes", "falcon_rms_fwd", "falcon_rms_bwd", "falcon_rms_bwd_workspace_bytes")
 STATIC_WORKSPACE_BYTES = 16 << 20
 
 
@@ -127,9 +162,17 @@ def load(path: str | None = None):
         for name, args in (("falcon_glr_fwd", [i32] + [vp] * 6 + [vp, vp, vp]),
                            ("falcon_glr_bwd", [i32] + [vp] * 10 + [vp, vp, vp]),
                            ("falcon_gn_fwd", [i32] + [vp] * 6 + [vp, vp, f32, vp]),
-                           ("falcon_gn_bwd", [i32] + [vp] * 10 + [vp, vp, f32, vp, ctypes.c_size_t, vp])):
+                           ("falcon_gn_bwd", [i32] + [vp] * 10 + [vp, vp, f32, vp, ctypes.c_size_t, vp]),
+                           ("falcon_gdr_fwd", [vp] * 11 + [f32, vp, ctypes.c_size_t, vp]),
+                           ("falcon_gdr_bwd", [vp] * 17 + [f32, vp, ctypes.c_size_t, vp]),
+                           ("falcon_rms_fwd", [vp] * 9 + [f32, vp]),
+                           ("falcon_rms_bwd", [vp] * 9 + [f32, vp, ctypes.c_size_t, vp])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = args
+        lib.falcon_gdr_workspace_bytes.restype = ctypes.c_size_t
+        lib.falcon_gdr_workspace_bytes.argtypes = [vp, i32]
+        lib.falcon_rms_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.falcon_rms_bwd_workspace_bytes.argtypes = [vp]
         lib.falcon_gn_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.falcon_gn_bwd_workspace_bytes.argtypes = [vp]
         if path is None:
@@ -581,3 +624,315 @@ def groupnorm_backward(x, dy, weight=None, bias=None, z=None, *, act="none", eps
     if st != FALCON_OK:
         raise FalconError(st, "falcon_gn_bwd")
     return {"dx": dx, "dz": dz, "dweight": dweight, "dbias": dbias}
+
+
+# ---- the block around the read: gated delta rule, root-mean-square norm
+
+
+def make_gdr_dims(batch, heads, seqlen, dk, dv, *, qk_heads=None, dtype=FALCON_BF16) -> FalconGdrDims:
+    return FalconGdrDims(int(batch), int(heads), int(heads if qk_heads is None else qk_heads), int(seqlen), int(dk),
+                         int(dv), int(dtype), 0)
+
+
+def make_rms_dims(batch, seqlen, d, *, dtype=FALCON_BF16, out_dtype=None) -> FalconRmsDims:
+    return FalconRmsDims(int(batch), int(seqlen), int(d), int(dtype), int(dtype if out_dtype is None else out_dtype))
+
+
+def _ws_bytes(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        return 0 if workspace is None or isinstance(workspace, int) else workspace.numel() * workspace.element_size()
+    return int(workspace_bytes)
+
+
+def falcon_gdr_fwd(q, k, v, beta, g, S0, lengths, out, S_final, dims: FalconGdrDims, strides=None, scale=1.0,
+                   workspace=None, workspace_bytes=None, stream=None) -> int:
+    """The C entry point with the same argument order; tensors or raw device pointers, `strides` 18 values or None.
+    Returns the status."""
+    return int(load().falcon_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(S0), _ptr(lengths),
+                                     _ptr(out), _ptr(S_final), ctypes.byref(dims), _strides(strides), float(scale),
+                                     _ptr(workspace), _ws_bytes(workspace, workspace_bytes), _stream_handle(stream)))
+
+
+def falcon_gdr_bwd(q, k, v, beta, g, S0, lengths, dout, dS_final, dq, dk, dv, dbeta, dg, dS0, dims: FalconGdrDims,
+                   strides=None, scale=1.0, workspace=None, workspace_bytes=None, stream=None) -> int:
+    """The C entry point (`strides` 33 values or None); returns the status."""
+    return int(load().falcon_gdr_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(S0), _ptr(lengths),
+                                     _ptr(dout), _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(dg),
+                                     _ptr(dS0), ctypes.byref(dims), _strides(strides), float(scale), _ptr(workspace),
+                                     _ws_bytes(workspace, workspace_bytes), _stream_handle(stream)))
+
+
+def falcon_gdr_workspace_bytes(dims: FalconGdrDims, backward: bool = False) -> int:
+    return int(load().falcon_gdr_workspace_bytes(ctypes.byref(dims), int(backward)))
+
+
+def falcon_rms_fwd(x, residual, weight, lengths, h, y, scales, dims: FalconRmsDims, strides=None, eps=1e-6,
+                   stream=None) -> int:
+    """The C entry point (`strides` 8 values or None); returns the status."""
+    return int(load().falcon_rms_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(lengths), _ptr(h), _ptr(y),
+                                     _ptr(scales), ctypes.byref(dims), _strides(strides), float(eps),
+                                     _stream_handle(stream)))
+
+
+def falcon_rms_bwd(h, weight, lengths, dy, dh, dx, dweight, dims: FalconRmsDims, strides=None, eps=1e-6,
+                   workspace=None, workspace_bytes=None, stream=None) -> int:
+    """The C entry point (`strides` 8 values or None); returns the status."""
+    return int(load().falcon_rms_bwd(_ptr(h), _ptr(weight), _ptr(lengths), _ptr(dy), _ptr(dh), _ptr(dx),
+                                     _ptr(dweight), ctypes.byref(dims), _strides(strides), float(eps),
+                                     _ptr(workspace), _ws_bytes(workspace, workspace_bytes), _stream_handle(stream)))
+
+
+def falcon_rms_bwd_workspace_bytes(dims: FalconRmsDims) -> int:
+    return int(load().falcon_rms_bwd_workspace_bytes(ctypes.byref(dims)))
+
+
+_PACK_GDR = struct.Struct("=6q2i").pack
+_PACK_RMS = struct.Struct("=3q2i").pack
+_PACK_N = functools.lru_cache(maxsize=None)(lambda n: struct.Struct(f"={n}q").pack)
+
+
+def _refuse(name, t, shape, dtype, device, what="contiguous channels"):
+    raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device} with {what}, got {tuple(t.shape)} {t.dtype} on "
+                     f"{t.device} with strides {t.stride()}")
+
+
+def _view(name, t, shape, dtype, index, x, pointers, strides):
+    """Checks one strided tensor (the last axis contiguous) and notes its pointer and its other axes' strides."""
+    layout = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or layout[-1] != 1 and shape[-1] > 1:
+        _refuse(name, t, shape, dtype, x.device)
+    strides += layout[:-1]
+    pointers.append(t.data_ptr())
+
+
+def _gate_view(name, t, shape, index, x, pointers, strides):
+    """The same for an fp32 [B,H,T] tensor, whose tokens may lie apart."""
+    if t.shape != shape or t.dtype is not _t().float32 or t.get_device() != index:
+        _refuse(name, t, shape, "torch.float32", x.device, "any strides")
+    strides += t.stride()
+    pointers.append(t.data_ptr())
+
+
+def _dense(name, t, shape, dtype, index, x):
+    """The pointer of a contiguous array, None without one."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, x.device, "no gaps")
+    return t.data_ptr()
+
+
+def _launch(what, index, args):
+    fn = getattr(_lib or load(), what)
+    if index != _t().current_device():
+        fn = _on_device(fn, index)
+    st = fn(*args)
+    if st != FALCON_OK:
+        raise FalconError(st, what)
+
+
+def _workspace(workspace, need, x, stream):
+    """A workspace tensor of at least `need` bytes and its size; allocated beside x where none is given."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = _empty(x, need, _t().torch.uint8, stream)
+    elif workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {x.device}, got one on {workspace.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def _gdr_bytes(dims, backward):
+    return int(load().falcon_gdr_workspace_bytes(dims, backward))
+
+
+@functools.lru_cache(maxsize=256)
+def _rms_bytes(dims):
+    return int(load().falcon_rms_bwd_workspace_bytes(dims))
+
+
+def _gdr_sizes(q, v):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q and v must be [B,H,T,d], got {tuple(q.shape)} and {tuple(v.shape)}")
+    index, dtype = q.get_device(), q.dtype
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    code = _t().codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    if H > 0 and (Hk == 0 or H % Hk):
+        raise ValueError(f"the heads of q and k must divide those of v, got {Hk} and {H}")
+    return index, dtype, B, H, Hk, T, dk, dv, _PACK_GDR(B, H, Hk, T, dk, dv, code, 0)
+
+
+def gdr_forward(q, k, v, beta, g, S0=None, *, scale=None, lengths=None, out=None, S_final=None, want_state=True,
+                workspace=None, stream=None):
+    """Gated delta rule: S_t = a_t S_{t-1} + k_t (beta_t (v_t - a_t S_{t-1}^T k_t))^T with a_t = exp(g_t),
+    out_t = scale S_t^T q_t; returns (out, S_final or None).
+
+    q, k: [B,Hk,T,dk], v: [B,H,T,dv], float32 or bfloat16, any strides with contiguous channels (column blocks of one
+    projection are passed as they are); Hk divides H, and each head of q and k is shared by H / Hk heads of v that
+    follow each other. dk, dv up to 128. beta (gain), g (log decay): fp32 [B,H,T], any strides. S0: fp32 [B,H,dk,dv]
+    or None (zero). scale: dk ** -0.5 unless given. lengths: int32 [B] or None; rows behind them come back as zeros.
+    out (a [B,H,T,dv] view) and S_final (may be S0: updated in place) are written where given; out is else allocated
+    in the output projection's layout, a view of a dense [B,T,H,dv]. workspace: uint8 of falcon_gdr_workspace_bytes,
+    allocated unless given (up to 16 tokens need none). stream: as for glr_forward."""
+    index, dtype, B, H, Hk, T, dk, dv, dims = _gdr_sizes(q, v)
+    t = _t()
+    if out is None:
+        out = _empty(v, (B, T, H, dv), dtype, stream).transpose(1, 2)
+    if S_final is None and want_state:
+        S_final = _empty(v, (B, H, dk, dv), t.float32, stream)
+    pointers, strides = [], []
+    _view("q", q, (B, Hk, T, dk), dtype, index, q, pointers, strides)
+    _view("k", k, (B, Hk, T, dk), dtype, index, q, pointers, strides)
+    _view("v", v, (B, H, T, dv), dtype, index, q, pointers, strides)
+    _gate_view("beta", beta, (B, H, T), index, q, pointers, strides)
+    _gate_view("g", g, (B, H, T), index, q, pointers, strides)
+    _view("out", out, (B, H, T, dv), dtype, index, q, pointers, strides)
+    p_out = pointers.pop()
+    state = (B, H, dk, dv)
+    p_S0 = _dense("S0", S0, state, t.float32, index, q)
+    p_last = _dense("S_final", S_final, state, t.float32, index, q)
+    p_len = _dense("lengths", lengths, (B,), t.torch.int32, index, q)
+    workspace, size = _workspace(workspace, _gdr_bytes(dims, 0), q, stream)
+    _launch("falcon_gdr_fwd", index, (*pointers, p_S0, p_len, p_out, p_last, dims, _PACK_N(18)(*strides),
+                                      dk ** -0.5 if scale is None else scale, _ptr(workspace), size,
+                                      t.raw_stream(index) if stream is None else _handle(stream, q.device)))
+    return out, S_final
+
+
+def gdr_backward(q, k, v, beta, g, dout, S0=None, dS_final=None, *, scale=None, lengths=None, dq=None, dk=None,
+                 dv=None, dbeta=None, dg=None, dS0=None, workspace=None, stream=None):
+    """Gradients of one gdr_forward call, from its inputs and the adjoints of out and S_final. Returns a dict dq, dk,
+    dv (in q's type), dbeta, dg, dS0 (fp32); each is written where given, else allocated dense. workspace: as for
+    gdr_forward, of falcon_gdr_workspace_bytes(dims, backward=True). stream: as for glr_forward."""
+    index, dtype, B, H, Hk, T, n_k, n_v, dims = _gdr_sizes(q, v)
+    t = _t()
+    f32, state = t.float32, (B, H, n_k, n_v)
+    dq = _empty(q, (B, Hk, T, n_k), dtype, stream) if dq is None else dq
+    dk = _empty(q, (B, Hk, T, n_k), dtype, stream) if dk is None else dk
+    dv = _empty(q, (B, H, T, n_v), dtype, stream) if dv is None else dv
+    dbeta = _empty(q, (B, H, T), f32, stream) if dbeta is None else dbeta
+    dg = _empty(q, (B, H, T), f32, stream) if dg is None else dg
+    dS0 = _empty(q, state, f32, stream) if dS0 is None else dS0
+    pointers, strides = [], []
+    _view("q", q, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
+    _view("k", k, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
+    _view("v", v, (B, H, T, n_v), dtype, index, q, pointers, strides)
+    _gate_view("beta", beta, (B, H, T), index, q, pointers, strides)
+    _gate_view("g", g, (B, H, T), index, q, pointers, strides)
+    _view("dout", dout, (B, H, T, n_v), dtype, index, q, pointers, strides)
+    _view("dq", dq, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
+    _view("dk", dk, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
+    _view("dv", dv, (B, H, T, n_v), dtype, index, q, pointers, strides)
+    _gate_view("dbeta", dbeta, (B, H, T), index, q, pointers, strides)
+    _gate_view("dg", dg, (B, H, T), index, q, pointers, strides)
+    p_S0 = _dense("S0", S0, state, f32, index, q)
+    p_dS = _dense("dS_final", dS_final, state, f32, index, q)
+    p_dS0 = _dense("dS0", dS0, state, f32, index, q)
+    p_len = _dense("lengths", lengths, (B,), t.torch.int32, index, q)
+    workspace, size = _workspace(workspace, _gdr_bytes(dims, 1), q, stream)
+    _launch("falcon_gdr_bwd", index, (*pointers[:5], p_S0, p_len, pointers[5], p_dS, *pointers[6:], p_dS0, dims,
+                                      _PACK_N(33)(*strides), n_k ** -0.5 if scale is None else scale, _ptr(workspace),
+                                      size, t.raw_stream(index) if stream is None else _handle(stream, q.device)))
+    return {"dq": dq, "dk": dk, "dv": dv, "dbeta": dbeta, "dg": dg, "dS0": dS0}
+
+
+def _rms_sizes(x):
+    """[B,T,d], or [N,d] as one sequence of N tokens."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [B,T,d] or [N,d], got {tuple(x.shape)}")
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    code = _t().codes.get(x.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {x.dtype}: float32 or bfloat16")
+    return index, code, (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
+
+
+def _row_view(name, t, x, dtype, index, pointers, strides):
+    layout = t.stride()
+    if t.shape != x.shape or t.dtype is not dtype or t.get_device() != index or layout[-1] != 1 and x.shape[-1] > 1:
+        _refuse(name, t, x.shape, dtype, x.device)
+    strides += (0, *layout[:-1]) if len(layout) == 2 else layout[:-1]
+    pointers.append(t.data_ptr())
+
+
+def rmsnorm_forward(x, weight=None, residual=None, *, eps=1e-6, lengths=None, y=None, h=None, scales=None,
+                    out_dtype=None, stream=None):
+    """Root-mean-square norm with the residual's addition, per token: h = x + residual, y = weight h /
+    sqrt(mean h^2 + eps); returns (y, h, scales).
+
+    x, residual: [B,T,d] or [N,d], float32 or bfloat16, any strides with contiguous channels; weight: fp32 [d] or None.
+    h, in x's type, is what is normalised; it may be x or residual (updated in place), and without a residual it is x
+    itself. out_dtype (or y's type): x's, or torch.float8_e4m3fn, with fp32 scales [B,T] (or [N]): a token's largest
+    |y| / 448, of which y holds the multiples (else scales is None). lengths: int32 [B] or None; rows behind them come
+    back as zeros. y, h and scales are written where given, else allocated dense. stream: as for glr_forward."""
+    index, code, (B, T, d) = _rms_sizes(x)
+    t = _t()
+    torch = t.torch
+    kind = y.dtype if y is not None else x.dtype if out_dtype is None else out_dtype
+    if out_dtype is not None and kind is not out_dtype:
+        raise ValueError(f"y must be {out_dtype}, got {kind}")
+    eight = kind is torch.float8_e4m3fn
+    if not eight and kind is not x.dtype:
+        raise ValueError(f"y must be {x.dtype} or torch.float8_e4m3fn, got {kind}")
+    if residual is None and h is not None:
+        raise ValueError("h is written with a residual only: without one it is x")
+    if scales is not None and not eight:
+        raise ValueError("scales go with an output in 8 bits")
+    y = _empty(x, x.shape, kind, stream) if y is None else y
+    if residual is not None and h is None:
+        h = _empty(x, x.shape, x.dtype, stream)
+    if eight and scales is None:
+        scales = _empty(x, x.shape[:-1], t.float32, stream)
+    pointers, strides = [], []
+    for name, v in (("x", x), ("residual", residual), ("h", h)):
+        if v is None:
+            pointers.append(None)
+            strides += (0, 0)
+        else:
+            _row_view(name, v, x, x.dtype, index, pointers, strides)
+    _row_view("y", y, x, kind, index, pointers, strides)
+    p_x, p_r, p_h, p_y = pointers
+    _launch("falcon_rms_fwd", index, (
+        p_x, p_r, _dense("weight", weight, (d,), t.float32, index, x), _dense("lengths", lengths, (B,), torch.int32, index, x),
+        p_h, p_y, _dense("scales", scales, x.shape[:-1], t.float32, index, x),
+        _PACK_RMS(B, T, d, code, FALCON_E4M3 if eight else code), _PACK_N(8)(*strides), eps,
+        t.raw_stream(index) if stream is None else _handle(stream, x.device)))
+    return y, x if residual is None else h, scales
+
+
+def rmsnorm_backward(h, dy, weight=None, dh=None, *, eps=1e-6, lengths=None, dx=None, dweight=None, workspace=None,
+                     want_params=True, stream=None):
+    """Gradients of one rmsnorm_forward call, from what it normalised (its h, or x without a residual), the adjoint of y
+    and that of h (None: nothing else reads it). Returns a dict dx, the gradient of x and of the residual alike (in h's
+    type; may be dh, written in place), and dweight (fp32 [d]; None unless want_params or given). workspace: uint8 of
+    falcon_rms_bwd_workspace_bytes, which dweight needs, allocated unless given. stream: as for glr_forward."""
+    index, code, (B, T, d) = _rms_sizes(h)
+    t = _t()
+    dx = _empty(h, h.shape, h.dtype, stream) if dx is None else dx
+    if want_params and dweight is None:
+        dweight = _empty(h, (d,), t.float32, stream)
+    pointers, strides = [], []
+    for name, v in (("h", h), ("dy", dy), ("dh", dh), ("dx", dx)):
+        if v is None:
+            pointers.append(None)
+            strides += (0, 0)
+        else:
+            _row_view(name, v, h, h.dtype, index, pointers, strides)
+    p_h, p_dy, p_dh, p_dx = pointers
+    dims, size = _PACK_RMS(B, T, d, code, code), 0
+    if dweight is not None:
+        workspace, size = _workspace(workspace, _rms_bytes(dims), h, stream)
+    _launch("falcon_rms_bwd", index, (
+        p_h, _dense("weight", weight, (d,), t.float32, index, h),
+        _dense("lengths", lengths, (B,), t.torch.int32, index, h), p_dy, p_dh, p_dx,
+        _dense("dweight", dweight, (d,), t.float32, index, h), dims, _PACK_N(8)(*strides), eps, _ptr(workspace), size,
+        t.raw_stream(index) if stream is None else _handle(stream, h.device)))
+    return {"dx": dx, "dweight": dweight}
