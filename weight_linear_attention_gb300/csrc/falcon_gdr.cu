@@ -10,27 +10,29 @@ namespace gdr {
 namespace {
 
 // ---- outputs of one chunk: out = scale diag(e^G) Q S + P U, U = diag(beta) X (V - diag(e^G) K S). From bf16 inputs
-// every operand is rounded to tf32 once, whose steps are an eighth of the result's; from fp32 ones it is whole.
+// every fp32 operand enters in two planes, 16 bits where the result has 8; from fp32 ones in three.
 template <typename E>
 struct OutArgs {
     Sizes n;
     Ten<const E> q, k, v;
     Ten<E> out;
     Ten<float> beta, g;
-    const float *X, *S;
+    const uint8_t *X, *S;
 };
 
 template <typename E, int NK>
+__host__ __device__ constexpr int out_smem() { return (2 * NK * planes<E>() + 2 * state_planes<E, false>()) * kPlane; }
+
+template <typename E, int NK>
 __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
-    constexpr int PI = sizeof(E) == 2 ? kExact : kFull;
-    constexpr int PW = PI;                                    // tiles that were rounded where they were written
-    constexpr int PR = sizeof(E) == 2 ? kRound : kFull;       // registers
-    extern __shared__ __align__(16) float smem[];
+    constexpr int PI = planes<E>(), PS = state_planes<E, false>();
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
-    float* K = smem;
-    float* Q = K + NK * kTile;
-    float* X = Q + NK * kTile;
-    float* W = X + kTile;
+    uint8_t* K = smem;
+    uint8_t* Q = K + NK * PI * kPlane;
+    uint8_t* X = Q + NK * PI * kPlane;
+    uint8_t* W = X + PS * kPlane;
+    const uint32_t Ks = saddr(K), Qs = saddr(Q), Xs = saddr(X), Ws = saddr(W);
     const Lane ln;
     const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
@@ -45,23 +47,23 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
             write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, acc, ln, rows, 0, a.n.dv - sb * kC);
         return;
     }
-    const float* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * kTile);
-    copy_tile(W, St);
-    commit();
-    copy_tile(X, a.X + (bh * a.n.NC + c) * kTile);
-    commit();
-    load_scal(s, a.beta, a.g, b, h, t0, live);
+    const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * PS * kPlane);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
-        load_tile(K + kb * kTile, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
-        load_tile(Q + kb * kTile, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
+        load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
+        load_planes(Q + kb * PI * kPlane, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
     }
+    commit();
+    copy_planes<PS>(Ws, St);
+    copy_planes<PS>(Xs, a.X + (bh * a.n.NC + c) * (PS * kPlane));
+    commit();
+    load_scal(s, a.beta, a.g, b, h, t0, live);
     wait<1>();
     __syncthreads();
     float P[8][4];
     zero(P);
 #pragma unroll 1
-    for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Q + kb * kTile, rb, K + kb * kTile, ln, 0, 8, 0, 2 * rb + 2);
+    for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Qs + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -78,15 +80,14 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
         for (int kb = 0; kb < NK; ++kb) {
             if (sb + kb > 0) {
                 __syncthreads();
-                copy_tile(W, St + (sb * NK + kb) * kTile);
+                copy_planes<PS>(Ws, St + (sb * NK + kb) * (PS * kPlane));
                 commit();
-                wait<0>();
-                __syncthreads();
             }
-            mm<PI, PW, false, false>(acc, K + kb * kTile, rb, W, ln);
-            mm<PI, PW, false, false>(o, Q + kb * kTile, rb, W, ln);
+            wait<0>();
+            __syncthreads();
+            mm<PI, PS, false, false>(acc, Ks + kb * PI * kPlane, rb, Ws, ln);
+            mm<PI, PS, false, false>(o, Qs + kb * PI * kPlane, rb, Ws, ln);
         }
-        wait<0>();
         __syncthreads();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -97,29 +98,24 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
             for (int nt = 0; nt < 8; ++nt) {
                 const int col = 8 * nt + 2 * ln.j;
                 const float2 v = row < live ? load2(pv + col, a.n.dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
-                float x = fmaf(-eG, acc[nt][2 * hf], v.x), y = fmaf(-eG, acc[nt][2 * hf + 1], v.y);
-                if (PI == kExact) x = __uint_as_float(tf32(x)), y = __uint_as_float(tf32(y));
-                acc[nt][2 * hf] = x;
-                acc[nt][2 * hf + 1] = y;
+                acc[nt][2 * hf] = fmaf(-eG, acc[nt][2 * hf], v.x);
+                acc[nt][2 * hf + 1] = fmaf(-eG, acc[nt][2 * hf + 1], v.y);
                 o[nt][2 * hf] *= eG * a.n.scale;
                 o[nt][2 * hf + 1] *= eG * a.n.scale;
             }
         }
-        put(W, rb, acc, ln);
+        put_planes<PS>(W, rb, acc, ln);
         __syncthreads();
         zero(acc);
-        mm<PW, PW, false, true>(acc, X, rb, W, ln, 0, 2 * rb + 2);
+        mm<PS, PS, false, true>(acc, Xs, rb, Ws, ln, 0, rb + 1);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float u = acc[nt][e] * s.beta[16 * rb + ln.r + 8 * (e >> 1)];
-                acc[nt][e] = PI == kExact ? __uint_as_float(tf32(u)) : u;
-            }
-        put(W, rb, acc, ln);
+            for (int e = 0; e < 4; ++e) acc[nt][e] *= s.beta[16 * rb + ln.r + 8 * (e >> 1)];
+        put_planes<PS>(W, rb, acc, ln);
         __syncthreads();
-        mmr<PR, PW, true>(o, P, W, ln, 0, 2 * rb + 2);
+        mmr<PS, PS, true>(o, P, Ws, ln, 0, rb + 1);
         write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, o, ln, rows, live, a.n.dv - sb * kC);
     }
 }
@@ -252,9 +248,10 @@ int launch_chunks(const GdrArgs& a, const Layout& l, cudaStream_t st) {
     p.v = ten<const E>(a.v, a.n.dv);
     p.beta = ten<float>(a.beta, 1);
     p.g = ten<float>(a.g, 1);
-    p.X = a.ws + l.X;
-    p.M = a.ws + l.M;
-    p.A = a.ws + l.S;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
+    p.X = ws + l.X;
+    p.M = ws + l.M;
+    p.A = reinterpret_cast<float*>(ws + l.A);
     OutArgs<E> o = {};
     o.n = n;
     o.q = ten<const E>(a.q, a.n.dk);
@@ -264,12 +261,12 @@ int launch_chunks(const GdrArgs& a, const Layout& l, cudaStream_t st) {
     o.beta = p.beta;
     o.g = p.g;
     o.X = p.X;
-    o.S = p.A;
-    const int prep = (NK + 2) * kTile * 4, out = (2 * NK + 2) * kTile * 4;
+    o.S = ws + l.S;
+    constexpr int prep = prep_smem<E, NK, false>(), out = out_smem<E, NK>();
     if (!want_smem(gdr_prep<E, NK, false>, prep) || !want_smem(gdr_out<E, NK>, out)) return FALCON_ERR_CUDA;
     const unsigned grid = (unsigned)(n.BH * l.NC);
     gdr_prep<E, NK, false><<<grid, kThreads, prep, st>>>(p);
-    if (!run_scan<NK, false>(n, l, a.ws, a.S0, a.S_final, false, sizeof(E) == 2, st)) return FALCON_ERR_CUDA;
+    if (!run_scan<NK, false, state_planes<E, false>()>(n, l, ws, a.S0, a.S_final, false, st)) return FALCON_ERR_CUDA;
     gdr_out<E, NK><<<grid, kThreads, out, st>>>(o);
     return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
@@ -285,7 +282,7 @@ int launch_fwd(const GdrArgs& a, cudaStream_t st) {
 }  // namespace gdr
 
 unsigned long long gdr_fwd_workspace(const GdrSizes& n) {
-    return n.T <= kGdrStepT ? 0 : (unsigned long long)gdr::layout_of(n, false).total * 4;
+    return n.T <= kGdrStepT ? 0 : (unsigned long long)gdr::layout_of(n, false).total;
 }
 
 bool gdr_fits(const GdrSizes& n) {
@@ -296,7 +293,7 @@ bool gdr_fits(const GdrSizes& n) {
 
 int launch_gdr_fwd(const GdrArgs& a, cudaStream_t s) { return a.n.bf16 ? gdr::launch_fwd<gdr::bf16>(a, s) : gdr::launch_fwd<float>(a, s); }
 
-unsigned long long gdr_bwd_workspace(const GdrSizes& n) { return (unsigned long long)gdr::layout_of(n, true).total * 4; }
+unsigned long long gdr_bwd_workspace(const GdrSizes& n) { return (unsigned long long)gdr::layout_of(n, true).total; }
 
 int launch_gdr_bwd(const GdrArgs& a, cudaStream_t s) {
     const bool one = a.n.dk <= gdr::kC;

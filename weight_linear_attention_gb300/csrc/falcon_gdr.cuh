@@ -10,9 +10,11 @@
 // So S' = M S + A with M = e^{G_C} I - K^T diag(w beta) X diag(e^G) K and A = K^T diag(w beta) X V: the chunk
 // kernels run for all chunks at once, and only S' = M S + A goes along the sequence.
 //
-// Products: operands are fp32, a value x enters as x = h + l, h its nearest tf32, and a product as
-// l h + h l + h h with fp32 sums: what is left out is below 2^-22 of it. bf16 inputs are tf32 values, so
-// their l is nothing and the pass falls away.
+// Products: an fp32 operand x enters as bf16 planes, x = h + m + l (each the nearest bf16 of what the ones before
+// leave: 24 bits), and a product of two as h h + h m + m h + m m + h l + l h with fp32 sums, what is left out being
+// below 2^-24 of it; with two planes as h h + h m + m h (2^-16). bf16 inputs are their own single plane. An operand is
+// split once, where it is made, and the warps' products are loads of matrices and nothing else. (As tf32 pairs, split by
+// every warp that reads them, the same products took 2.2 to 3 times as long.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,133 +28,152 @@ namespace gdr {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kC = 64;          // tokens of a chunk, rows and columns of a tile
-constexpr int kTile = kC * kC;  // floats
+constexpr int kC = 64;              // tokens of a chunk, rows and columns of a tile
+constexpr int kTile = kC * kC;      // floats of an fp32 tile
+constexpr int kPlane = kC * kC * 2; // bytes of a bf16 plane
 constexpr int kThreads = 128;
 
-// A tile's element (row, col) lies at row * 64 + (col ^ 8 f(row)): reads of 4 consecutive rows x 8 columns and of
-// every other one of 8 rows x 8 columns both touch 32 different banks. Groups of 8 columns stay together, so a tile
-// is copied in pieces of 16 bytes, and lies in the workspace as it does in shared memory.
+// An fp32 tile's element (row, col) lies at row * 64 + (col ^ 8 f(row)): reads of 4 consecutive rows x 8 columns and of
+// every other one of 8 rows x 8 columns both touch 32 different banks. It lies in the workspace as in shared memory.
 __device__ __forceinline__ int fsw(int row) { return (row ^ ((row >> 2) & 1)) & 3; }
 __device__ __forceinline__ int at(int row, int col) { return row * kC + (col ^ (fsw(row) << 3)); }
+// A plane's element lies at this byte: rows of 128 bytes, their pieces of 16 in an order that puts a column of
+// pieces of 8 rows into 8 different bank groups.
+__device__ __forceinline__ int pat(int row, int col) { return row * 128 + ((((col >> 3) ^ row) & 7) << 4) + 2 * (col & 7); }
 
 struct Lane {
-    int r, j, fr, f0, f1;
+    int r, j, fr;       // of a product's result: rows r and r + 8, columns 2 j and 2 j + 1 of 8
+    int l7, l8, l16;    // of a load of four 8 x 8 matrices
     __device__ Lane() {
         const int l = threadIdx.x & 31;
         r = l >> 2;
         j = l & 3;
         fr = fsw(r);
-        f0 = fsw(2 * j);
-        f1 = fsw(2 * j + 1);
+        l7 = l & 7;
+        l8 = (l >> 3) & 1;
+        l16 = l >> 4;
     }
 };
 
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <bool TRANS>
+__device__ __forceinline__ void ldm(uint32_t (&v)[4], uint32_t addr) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t tf32(float x) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
-}
-// x = h + l. The carry of a NaN's mantissa may leave the NaN out of h, never out of l.
-__device__ __forceinline__ void split(float x, uint32_t& h, uint32_t& l) {
-    h = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    l = __float_as_uint(x - __uint_as_float(h));
-}
 
-// How an operand enters: kExact, a value that is tf32 as it is; kRound, its nearest tf32 alone; kFull, both parts.
-enum { kExact = 0, kRound = 1, kFull = 2 };
-template <int P>
-__device__ __forceinline__ void part(float x, uint32_t& h, uint32_t& l) {
-    if (P == kFull) split(x, h, l);
-    else h = P == kRound ? tf32(x) : __float_as_uint(x);
-}
-
-// Operand B of k step kk for four column groups: B[n][k] (COL false) or B[k][n] (COL true). Contraction index j of the
-// instruction is column 2j of the k step and j + 4 column 2j + 1, for A and B alike, so that a lane's two values
-// lie together in a row, and so that a product's own result can be the next one's A.
-template <int PB, bool COL>
-__device__ __forceinline__ void load_b(const float* B, const Lane& ln, int kk, int nt0, uint32_t (&h)[4][2], uint32_t (&l)[4][2]) {
+// Two values as N planes of packed pairs (x in the low half).
+template <int N>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&p)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int nt = nt0 + i;
-        float x, y;
-        if (!COL) {
-            const float2 v = *reinterpret_cast<const float2*>(B + (8 * nt + ln.r) * kC + (((kk & 3) ^ ln.fr) << 3) +
-                                                              ((kk >> 2) << 5) + 2 * ln.j);
-            x = v.x;
-            y = v.y;
-        } else {
-            const float* p = B + (8 * kk + 2 * ln.j) * kC + ((nt >> 2) << 5) + ln.r;
-            x = p[((nt & 3) ^ ln.f0) << 3];
-            y = p[kC + (((nt & 3) ^ ln.f1) << 3)];
+    for (int i = 0; i < N; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        p[i] = *reinterpret_cast<const uint32_t*>(&h);
+        if (i + 1 < N) {
+            x -= __uint_as_float(p[i] << 16);
+            y -= __uint_as_float(p[i] & 0xffff0000u);
         }
-        part<PB>(x, h[i][0], l[i][0]);
-        part<PB>(y, h[i][1], l[i][1]);
     }
 }
 
-// One k step: acc (16 rows x 64 columns, column groups [n0, n1)) += a B.
+// One k step of 16: acc (16 rows x 64 columns, column groups of 16 in [p0, p1)) += a B. B, its planes at `b`, is stored
+// [n][k], or [k][n] (BCOL).
 template <int PA, int PB, bool BCOL>
-__device__ __forceinline__ void step(float (&acc)[8][4], const float (&a)[4], const float* B, const Lane& ln, int kk, int n0, int n1) {
-    uint32_t ah[4], al[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part<PA>(a[i], ah[i], al[i]);
+__device__ __forceinline__ void step(float (&acc)[8][4], const uint32_t (&a)[PA][4], uint32_t b, const Lane& ln, int kk, int p0, int p1) {
+    const uint32_t row = BCOL ? b + (16 * kk + ln.l7 + 8 * ln.l8) * 128 : b + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        if (n1 <= 4 * q || n0 >= 4 * q + 4) continue;
-        uint32_t bh[4][2], bl[4][2];
-        load_b<PB, BCOL>(B, ln, kk, 4 * q, bh, bl);
-        if (PA == kFull) {
+        if (p1 <= 2 * q || p0 >= 2 * q + 2) continue;
+        uint32_t v[2][PB][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma(acc[4 * q + i], al, bh[i][0], bh[i][1]);
-        }
-        if (PB == kFull) {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma(acc[4 * q + i], ah, bl[i][0], bl[i][1]);
-        }
+            for (int m = 0; m < PB; ++m) {
+                const int p = 2 * q + i;
+                ldm<BCOL>(v[i][m], row + m * kPlane + (BCOL ? (((2 * p + ln.l16) ^ ln.l7) << 4) : p * 2048));
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma(acc[4 * q + i], ah, bh[i][0], bh[i][1]);
+        for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
+#pragma unroll
+            for (int ma = 0; ma < PA; ++ma) {
+                const int mb = s - ma;
+                if (mb < 0 || mb >= PB) continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mma(acc[4 * q + 2 * i], a[ma], v[i][mb][0], v[i][mb][1]);
+                    mma(acc[4 * q + 2 * i + 1], a[ma], v[i][mb][2], v[i][mb][3]);
+                }
+            }
     }
 }
 
-// acc += A[16 rb ..][k] B over k steps [k0, k1). ACOL: A is stored [k][m]. `scale`: a factor for each k, or null.
+// acc += A[16 rb ..][k] B over k steps [k0, k1). ACOL: A is stored [k][m].
 template <int PA, int PB, bool ACOL, bool BCOL>
-__device__ __forceinline__ void mm(float (&acc)[8][4], const float* A, int rb, const float* B, const Lane& ln, int k0 = 0,
-                                   int k1 = 8, int n0 = 0, int n1 = 8, const float* scale = nullptr) {
-#pragma unroll 2
+__device__ __forceinline__ void mm(float (&acc)[8][4], uint32_t A, int rb, uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4,
+                                   int p0 = 0, int p1 = 4) {
+#pragma unroll 1
     for (int kk = k0; kk < k1; ++kk) {
-        float a[4];
-        if (!ACOL) {
-            const float* p = A + (16 * rb + ln.r) * kC + (((kk & 3) ^ ln.fr) << 3) + ((kk >> 2) << 5) + 2 * ln.j;
-            const float2 x = *reinterpret_cast<const float2*>(p), y = *reinterpret_cast<const float2*>(p + 8 * kC);
-            a[0] = x.x, a[1] = y.x, a[2] = x.y, a[3] = y.y;
-        } else {
-            const int nt = 2 * rb;
-            const float* p = A + (8 * kk + 2 * ln.j) * kC + ((nt >> 2) << 5) + ln.r;
-            a[0] = p[((nt & 3) ^ ln.f0) << 3], a[1] = p[(((nt + 1) & 3) ^ ln.f0) << 3];
-            a[2] = p[kC + (((nt & 3) ^ ln.f1) << 3)], a[3] = p[kC + ((((nt + 1) & 3) ^ ln.f1) << 3)];
+        uint32_t a[PA][4];
+#pragma unroll
+        for (int m = 0; m < PA; ++m) {
+            const uint32_t p = ACOL ? A + (16 * kk + ln.l7 + 8 * ln.l16) * 128 + (((2 * rb + ln.l8) ^ ln.l7) << 4)
+                                    : A + (16 * rb + ln.l7 + 8 * ln.l8) * 128 + (((2 * kk + ln.l16) ^ ln.l7) << 4);
+            ldm<ACOL>(a[m], p + m * kPlane);
         }
-        if (scale) {
-            const float s0 = scale[8 * kk + 2 * ln.j], s1 = scale[8 * kk + 2 * ln.j + 1];
-            a[0] *= s0, a[1] *= s0, a[2] *= s1, a[3] *= s1;
-        }
-        step<PA, PB, BCOL>(acc, a, B, ln, kk, n0, n1);
+        step<PA, PB, BCOL>(acc, a, B, ln, kk, p0, p1);
     }
 }
 // The same with A in registers, as a product leaves it.
 template <int PA, int PB, bool BCOL>
-__device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], const float* B, const Lane& ln, int k0 = 0,
-                                    int k1 = 8) {
+__device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
+    for (int kk = 0; kk < 4; ++kk) {
         if (kk < k0 || kk >= k1) continue;
-        const float a[4] = {A[kk][0], A[kk][2], A[kk][1], A[kk][3]};
-        step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 8);
+        uint32_t a[PA][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t s[PA];
+            split<PA>(A[2 * kk + (i >> 1)][2 * (i & 1)], A[2 * kk + (i >> 1)][2 * (i & 1) + 1], s);
+#pragma unroll
+            for (int m = 0; m < PA; ++m) a[m][i] = s[m];
+        }
+        step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
+    }
+}
+// The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
+template <int PI, int PB, bool BCOL>
+__device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float* f, int rb, uint32_t B, const Lane& ln) {
+#pragma unroll 1
+    for (int kk = 0; kk < 4; ++kk) {
+        float x[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = 0.f;
+#pragma unroll
+        for (int m = PI - 1; m >= 0; --m) {
+            uint32_t v[4];
+            ldm<true>(v, A + m * kPlane + (16 * kk + ln.l7 + 8 * ln.l16) * 128 + (((2 * rb + ln.l8) ^ ln.l7) << 4));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i][0] += __uint_as_float(v[i] << 16), x[i][1] += __uint_as_float(v[i] & 0xffff0000u);
+        }
+        uint32_t a[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 s = *reinterpret_cast<const float2*>(f + 16 * kk + 8 * (i >> 1) + 2 * ln.j);
+            uint32_t p[3];
+            split<3>(x[i][0] * s.x, x[i][1] * s.y, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) a[m][i] = p[m];
+        }
+        step<3, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
     }
 }
 
@@ -162,7 +183,7 @@ __device__ __forceinline__ void zero(float (&acc)[8][4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 }
-// Rows 16 rb .. of a tile from and to a product's registers: acc[nt][e] is row 16 rb + r + 8 (e / 2), column
+// Rows 16 rb .. of an fp32 tile from and to a product's registers: acc[nt][e] is row 16 rb + r + 8 (e / 2), column
 // 8 nt + 2 j + e % 2.
 __device__ __forceinline__ void put(float* T, int rb, const float (&acc)[8][4], const Lane& ln) {
 #pragma unroll
@@ -180,15 +201,55 @@ __device__ __forceinline__ void get(const float* T, int rb, float (&acc)[8][4], 
         acc[nt][0] = x.x, acc[nt][1] = x.y, acc[nt][2] = y.x, acc[nt][3] = y.y;
     }
 }
-
-// ---- copies of whole tiles, global to shared
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_tile(float* dst, const float* src) {
+// The same transposed: acc's row is the tile's column.
+__device__ __forceinline__ void get_cols(const float* T, int rb, float (&acc)[8][4], const Lane& ln) {
 #pragma unroll
-    for (int i = 0; i < kTile / 4 / kThreads; ++i) {
-        const int o = 4 * (threadIdx.x + i * kThreads);
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][e] = T[at(8 * nt + 2 * ln.j + (e & 1), 16 * rb + ln.r + 8 * (e >> 1))];
+}
+// Rows 16 rb .. of N planes, in shared or global memory.
+template <int N>
+__device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc)[8][4], const Lane& ln) {
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p[N];
+            split<N>(acc[nt][2 * h], acc[nt][2 * h + 1], p);
+            uint8_t* to = T + (16 * rb + ln.r + 8 * h) * 128 + ((nt ^ ln.r) << 4) + 4 * ln.j;
+#pragma unroll
+            for (int m = 0; m < N; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
+        }
+}
+template <int N>
+__device__ __forceinline__ void get_planes(const uint8_t* T, int rb, float (&acc)[8][4], const Lane& ln) {
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* from = T + (16 * rb + ln.r + 8 * h) * 128 + ((nt ^ ln.r) << 4) + 4 * ln.j;
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int m = N - 1; m >= 0; --m) {
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(from + m * kPlane);
+                x += __uint_as_float(u << 16);
+                y += __uint_as_float(u & 0xffff0000u);
+            }
+            acc[nt][2 * h] = x, acc[nt][2 * h + 1] = y;
+        }
+}
+
+// ---- asynchronous copies, global to shared
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in = true) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+// N planes as they lie.
+template <int N>
+__device__ __forceinline__ void copy_planes(uint32_t dst, const uint8_t* src) {
+#pragma unroll
+    for (int i = 0; i < N * kPlane / 16 / kThreads; ++i) {
+        const int o = 16 * (threadIdx.x + i * kThreads);
         copy16(dst + o, src + o);
     }
 }
@@ -196,39 +257,50 @@ __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"
 template <int N>
 __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// ---- the inputs: up to 64 rows x 64 columns of a strided tensor as a tile, zero outside rows x cols. `vec`: rows
-// start on 16 bytes and cols is whole vectors.
+// ---- the inputs: up to 64 rows x 64 columns of a strided tensor as planes (one of bf16, three of fp32), zero outside
+// rows x cols. `vec`: rows start on 16 bytes and cols is whole vectors; bf16 then goes by asynchronous copies, which the
+// caller commits and waits for.
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 
-template <typename E>
-__device__ __forceinline__ void load_tile(float* dst, const E* src, long long st, int rows, int cols, bool vec) {
+__device__ __forceinline__ void load_planes(uint8_t* dst, const bf16* src, long long st, int rows, int cols, bool vec) {
     if (vec) {
-        constexpr int W = 16 / sizeof(E), PER = kC / W, N = kC * PER / kThreads;
-        uint4 v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = threadIdx.x + i * kThreads, row = c / PER, col = (c % PER) * W;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (row < rows && col < cols) v[i] = *reinterpret_cast<const uint4*>(src + row * st + col);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = threadIdx.x + i * kThreads, row = c / PER, col = (c % PER) * W;
-            float* p = dst + at(row, col);
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            if (sizeof(E) == 4) {
-                *reinterpret_cast<uint4*>(p) = v[i];
-            } else {
-                *reinterpret_cast<uint4*>(p) = make_uint4(u[0] << 16, u[0] & 0xffff0000u, u[1] << 16, u[1] & 0xffff0000u);
-                *reinterpret_cast<uint4*>(p + 4) = make_uint4(u[2] << 16, u[2] & 0xffff0000u, u[3] << 16, u[3] & 0xffff0000u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int c = threadIdx.x + i * kThreads, row = c >> 3, col = (c & 7) * 8;
+            const bool in = row < rows && col < cols;
+            copy16(saddr(dst) + pat(row, col), in ? src + row * st + col : src, in);
         }
     } else {
 #pragma unroll 4
         for (int c = threadIdx.x; c < kTile; c += kThreads) {
             const int row = c >> 6, col = c & 63;
-            dst[at(row, col)] = row < rows && col < cols ? to_f(src[row * st + col]) : 0.f;
+            *reinterpret_cast<bf16*>(dst + pat(row, col)) = row < rows && col < cols ? src[row * st + col] : __float2bfloat16_rn(0.f);
+        }
+    }
+}
+__device__ __forceinline__ void load_planes(uint8_t* dst, const float* src, long long st, int rows, int cols, bool vec) {
+    if (vec) {
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+            const int c = threadIdx.x + i * kThreads, row = c >> 4, col = (c & 15) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows && col < cols) v = *reinterpret_cast<const float4*>(src + row * st + col);
+            uint32_t x[3], y[3];
+            split<3>(v.x, v.y, x);
+            split<3>(v.z, v.w, y);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) *reinterpret_cast<uint2*>(dst + m * kPlane + pat(row, col)) = make_uint2(x[m], y[m]);
+        }
+    } else {
+#pragma unroll 2
+        for (int c = threadIdx.x; c < kTile / 2; c += kThreads) {
+            const int row = c >> 5, col = (c & 31) * 2;
+            const float* p = src + row * st + col;
+            uint32_t x[3];
+            split<3>(row < rows && col < cols ? p[0] : 0.f, row < rows && col + 1 < cols ? p[1] : 0.f, x);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) *reinterpret_cast<uint32_t*>(dst + m * kPlane + pat(row, col)) = x[m];
         }
     }
 }
@@ -296,15 +368,20 @@ __device__ __forceinline__ void write_rows(E* p, long long st, bool pair, int rb
 
 // ---- a chunk's gains and decays
 struct Scal {
-    float beta[kC], hi[kC], lo[kC];  // G = hi + lo: a difference of two keeps fp32's relative precision
+    float beta[kC], hi[kC], lo[kC];  // G / ln 2 = hi + lo: a difference of two keeps fp32's relative precision
     float eG[kC], w[kC], bw[kC];     // e^G, e^{G_C - G}, beta w
     float eC;
 };
-__device__ __forceinline__ float exp_sum(float hi, float lo) {
-    const float e = expf(hi);
-    return fmaf(e, lo, e);
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-__device__ __forceinline__ float decay(const Scal& s, int i, int j) { return expf((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j])); }
+__device__ __forceinline__ float exp_sum(double x) {
+    const float hi = (float)x, e = expf(hi);
+    return fmaf(e, (float)(x - hi), e);
+}
+__device__ __forceinline__ float decay(const Scal& s, int i, int j) { return ex2((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j])); }
 
 // Below this a log decay's factor is 0 in fp32 and so are all that contain it; sums of 64 stay exact enough in double.
 constexpr float kLeast = -1e5f;
@@ -337,22 +414,31 @@ __device__ __forceinline__ void load_scal(Scal& s, const Ten<float>& beta, const
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
-        const float hi = (float)G[e], lo = (float)(G[e] - hi);
-        const double left = all - G[e];
-        const float lh = (float)left, w = exp_sum(lh, (float)(left - lh));
+        const double g2 = G[e] * 1.4426950408889634074;
+        const float hi = (float)g2, w = exp_sum(all - G[e]);
         s.beta[t] = v[e];
         s.hi[t] = hi;
-        s.lo[t] = lo;
-        s.eG[t] = exp_sum(hi, lo);
+        s.lo[t] = (float)(g2 - hi);
+        s.eG[t] = exp_sum(G[e]);
         s.w[t] = w;
         s.bw[t] = v[e] * w;
     }
-    if (l == 31) s.eC = exp_sum((float)all, (float)(all - (float)all));
+    if (l == 31) s.eC = exp_sum(all);
 }
 
 // ---- the inverse of I + A, A strictly lower triangular in tile T, in its place: 16 x 16 diagonal blocks by
-// substitution, then twice the corner of a block pair, -Y22 A21 Y11, as products. They are formed transposed,
-// Y11^T A21^T first: its result is then the next product's A in registers.
+// substitution, then twice the corner of a block pair, -Y22 A21 Y11, as products of tf32 pairs (the blocks are
+// too small for planes to pay). They are formed transposed, Y11^T A21^T first: its result is then the next product's A in registers.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = h + l, h its nearest tf32. The carry of a NaN's mantissa may leave the NaN out of h, never out of l.
+__device__ __forceinline__ void split(float x, uint32_t& h, uint32_t& l) {
+    h = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    l = __float_as_uint(x - __uint_as_float(h));
+}
 __device__ __forceinline__ void corner(const float* T, int o, int n, int mb, float (&res)[4][4], const Lane& ln) {
     // columns o + 16 mb .. + 15 of the corner below the block of n rows at o, transposed: res[nt][e] is column
     // 16 mb + r + 8 (e / 2), row 8 nt + 2j + e % 2 of it
@@ -377,9 +463,9 @@ __device__ __forceinline__ void corner(const float* T, int o, int n, int mb, flo
             uint32_t h0, l0, h1, l1;
             split(v.x, h0, l0);
             split(v.y, h1, l1);
-            mma(x[nt], al, h0, h1);
-            mma(x[nt], ah, l0, l1);
-            mma(x[nt], ah, h0, h1);
+            mma_tf32(x[nt], al, h0, h1);
+            mma_tf32(x[nt], ah, l0, l1);
+            mma_tf32(x[nt], ah, h0, h1);
         }
     }
 #pragma unroll
@@ -396,9 +482,9 @@ __device__ __forceinline__ void corner(const float* T, int o, int n, int mb, flo
             uint32_t h0, l0, h1, l1;
             split(v.x, h0, l0);
             split(v.y, h1, l1);
-            mma(res[nt], al, h0, h1);
-            mma(res[nt], ah, l0, l1);
-            mma(res[nt], ah, h0, h1);
+            mma_tf32(res[nt], al, h0, h1);
+            mma_tf32(res[nt], ah, l0, l1);
+            mma_tf32(res[nt], ah, h0, h1);
         }
     }
 }
@@ -464,43 +550,38 @@ __device__ __forceinline__ int length_of(const Sizes& n, long long b) {
     return l < 0 ? 0 : l > n.T ? n.T : l;
 }
 
-// Where a chunk's tiles lie, in floats: X [BH][NC] tiles, M [BH][NC][NK][NK] (M[i][j]: rows 64 i of the new state,
-// columns 64 j of the old), states transposed [BH][NC + 1][NV][NK] (tile (s, i): rows 64 s of dv, columns 64 i of dk).
+// Where a chunk's tiles lie in the workspace: X [BH][NC], M [BH][NC][NK][NK] (M[i][j]: rows 64 i of the new state,
+// columns 64 j of the old) in planes, A [BH][NC][NV][NK] in fp32, the states transposed like A (tile (s, i): rows 64 s of
+// dv, columns 64 i of dk), [BH][NC + 1], in planes.
+template <typename E>
+__host__ __device__ constexpr int planes() { return sizeof(E) == 2 ? 1 : 3; }
+// Planes of X and of the states that a pass reads: from bf16 inputs the forward's output, a bf16 value, needs two.
+template <typename E, bool BWD>
+__host__ __device__ constexpr int state_planes() { return sizeof(E) == 2 && !BWD ? 2 : 3; }
+
 template <typename E>
 struct PrepArgs {
     Sizes n;
     Ten<const E> q, k, v, dout;
     Ten<float> beta, g;
-    float *X, *M, *A, *dA;  // dA: backward, what the chunk adds to the adjoint of the state before it
+    uint8_t *X, *M;
+    float *A, *dA;  // dA: backward, what the chunk adds to the adjoint of the state before it
 };
 
-// Strict lower triangle of D * (K K^T) * beta_col into tile T (rows 16 rb ..).
-template <int PI, int NK>
-__device__ __forceinline__ void gram(float* T, const float* K, const Scal& s, int rb, const Lane& ln) {
-    float acc[8][4];
-    zero(acc);
-#pragma unroll 1
-    for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(acc, K + kb * kTile, rb, K + kb * kTile, ln, 0, 8, 0, 2 * rb + 2);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
-            acc[nt][e] = j < i ? acc[nt][e] * decay(s, i, j) * s.beta[j] : 0.f;
-        }
-    put(T, rb, acc, ln);
-}
+template <typename E, int NK, bool BWD>
+__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 2 + 3 + (BWD ? (NK + 1) * planes<E>() : 0)) * kPlane; }
 
 template <typename E, int NK, bool BWD>
 __global__ void __launch_bounds__(kThreads) gdr_prep(const PrepArgs<E> a) {
-    constexpr int PI = sizeof(E) == 2 ? kExact : kFull;
-    extern __shared__ __align__(16) float smem[];
+    constexpr int PI = planes<E>(), PX = state_planes<E, BWD>();
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
-    float* K = smem;
-    float* T = K + NK * kTile;
-    float* Y = T + kTile;
-    float* Q = Y + kTile;      // BWD
-    float* dO = Q + NK * kTile;
+    uint8_t* K = smem;
+    float* T = reinterpret_cast<float*>(K + NK * PI * kPlane);
+    uint8_t* Y = K + (NK * PI + 2) * kPlane;
+    uint8_t* Q = Y + 3 * kPlane;  // BWD
+    uint8_t* dO = Q + NK * PI * kPlane;
+    const uint32_t Ks = saddr(K), Ys = saddr(Y), Qs = saddr(Q), Os = saddr(dO);
     const Lane ln;
     const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
@@ -509,122 +590,129 @@ __global__ void __launch_bounds__(kThreads) gdr_prep(const PrepArgs<E> a) {
     // the CTAs of an SM put the longest rows of a triangle on different quarters of it
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
     const long long t0 = (long long)c * kC;
-    load_scal(s, a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
-    for (int kb = 0; kb < NK; ++kb) load_tile(K + kb * kTile, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
-    if (BWD) {
-#pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) load_tile(Q + kb * kTile, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
+    for (int kb = 0; kb < NK; ++kb) {
+        load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
+        if (BWD) load_planes(Q + kb * PI * kPlane, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
     }
+    commit();
+    load_scal(s, a.beta, a.g, b, h, t0, live);
+    wait<0>();
     __syncthreads();
-    gram<PI, NK>(T, K, s, rb, ln);
+    float acc[8][4];
+    {  // N diag(beta)
+        zero(acc);
+#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(acc, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
+                acc[nt][e] = j < i ? acc[nt][e] * decay(s, i, j) * s.beta[j] : 0.f;
+            }
+        put(T, rb, acc, ln);
+    }
     invert(T, ln);
     const long long item = bh * a.n.NC + c;
-    {
-        float* out = a.X + item * kTile;
-        // a forward call reads X as a tf32 operand only
-        constexpr bool ROUND = !BWD && PI == kExact;
-#pragma unroll
-        for (int i = 0; i < kTile / 4 / kThreads; ++i) {
-            const int o = 4 * (threadIdx.x + i * kThreads);
-            float4 v = *reinterpret_cast<const float4*>(T + o);
-            if (ROUND) {
-                v.x = __uint_as_float(tf32(v.x)), v.y = __uint_as_float(tf32(v.y));
-                v.z = __uint_as_float(tf32(v.z)), v.w = __uint_as_float(tf32(v.w));
-            }
-            *reinterpret_cast<float4*>(out + o) = v;
-        }
-    }
-    float acc[8][4];
-    const int k1 = 2 * rb + 2;  // X's rows end on the diagonal
+    float t[8][4];
+    get(T, rb, t, ln);
+    put_planes<PX>(a.X + item * (PX * kPlane), rb, t, ln);
+    const int k1 = rb + 1;  // X's rows end on the diagonal
 #pragma unroll 1
     for (int cb = 0; cb < NK; ++cb) {  // M's columns 64 cb ..
+        float f[8][4];
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[nt][e] = t[nt][e] * s.eG[8 * nt + 2 * ln.j + (e & 1)];
         zero(acc);
-        mm<kFull, PI, false, true>(acc, T, rb, K + cb * kTile, ln, 0, k1, 0, 8, s.eG);
+        mmr<3, PI, true>(acc, f, Ks + cb * PI * kPlane, ln, 0, k1);
         if (cb > 0) __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.bw[16 * rb + ln.r + 8 * (e >> 1)];
-        put(Y, rb, acc, ln);
+        put_planes<3>(Y, rb, acc, ln);
         __syncthreads();
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) {
             zero(acc);
-            mm<PI, kFull, true, true>(acc, K + kb * kTile, rb, Y, ln);
+            mm<PI, 3, true, true>(acc, Ks + kb * PI * kPlane, rb, Ys, ln);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     acc[nt][e] = (kb == cb && 16 * rb + ln.r + 8 * (e >> 1) == 8 * nt + 2 * ln.j + (e & 1) ? s.eC : 0.f) - acc[nt][e];
-            put(a.M + ((item * NK + kb) * NK + cb) * kTile, rb, acc, ln);
+            put_planes<3>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), rb, acc, ln);
         }
     }
     const int NV = (a.n.dv + kC - 1) / kC;
-    float P[8][4];  // BWD: scale D_ij q_i.k_j, transposed: rows j, columns i >= j
-    if (BWD) {
-        zero(P);
-#pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, K + kb * kTile, rb, Q + kb * kTile, ln, 0, 8, 2 * rb, 8);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
-                P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
-            }
-    }
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         __syncthreads();
-        load_tile(Y, a.v.row0(b, h, t0) + sb * kC, a.v.st, live, a.n.dv - sb * kC, a.v.vec);
-        if (BWD) load_tile(dO, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, a.n.dv - sb * kC, a.dout.vec);
+        load_planes(Y, a.v.row0(b, h, t0) + sb * kC, a.v.st, live, a.n.dv - sb * kC, a.v.vec);
+        if (BWD) load_planes(dO, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, a.n.dv - sb * kC, a.dout.vec);
+        commit();
+        wait<0>();
         __syncthreads();
         zero(acc);
-        mm<kFull, PI, false, true>(acc, T, rb, Y, ln, 0, k1);
+        mmr<3, PI, true>(acc, t, Ys, ln, 0, k1);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.bw[16 * rb + ln.r + 8 * (e >> 1)];
-        put(Y, rb, acc, ln);
+        put_planes<3>(Y, rb, acc, ln);
         __syncthreads();
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) {
             zero(acc);
-            mm<kFull, PI, true, true>(acc, Y, rb, K + kb * kTile, ln);
-            put(a.A + (((bh * (a.n.NC + 1) + c) * NV + sb) * NK + kb) * kTile, rb, acc, ln);
+            mm<3, PI, true, true>(acc, Ys, rb, Ks + kb * PI * kPlane, ln);
+            put(a.A + ((item * NV + sb) * NK + kb) * kTile, rb, acc, ln);
         }
         if (BWD) {
             // local part of the adjoints: Z = X^T diag(beta) P^T dO; adds scale Q^T diag(e^G) dO - K^T diag(e^G) Z
+            float P[8][4];  // scale D_ij q_i.k_j, transposed: rows j, columns i >= j
+            zero(P);
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4);
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
+                    P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
+                }
             zero(acc);
-            mmr<kFull, PI, true>(acc, P, dO, ln, 2 * rb, 8);
+            mmr<3, PI, true>(acc, P, Os, ln, rb, 4);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][e] *= s.beta[16 * rb + ln.r + 8 * (e >> 1)];
             __syncthreads();
-            put(Y, rb, acc, ln);
+            put_planes<3>(Y, rb, acc, ln);
             __syncthreads();
+            get_cols(T, rb, P, ln);
             zero(acc);
-            mm<kFull, kFull, true, true>(acc, T, rb, Y, ln, 2 * rb, 8);
+            mmr<3, 3, true>(acc, P, Ys, ln, rb, 4);
             __syncthreads();
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][e] *= -s.eG[16 * rb + ln.r + 8 * (e >> 1)];
-            put(Y, rb, acc, ln);
+            put_planes<3>(Y, rb, acc, ln);
             __syncthreads();
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
                 zero(acc);
-                mm<kFull, PI, true, true>(acc, dO, rb, Q + kb * kTile, ln, 0, 8, 0, 8, s.eG);
+                mms<PI, PI, true>(acc, Os, s.eG, rb, Qs + kb * PI * kPlane, ln);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[nt][e] *= a.n.scale;
-                mm<kFull, PI, true, true>(acc, Y, rb, K + kb * kTile, ln);
-                put(a.dA + (((bh * a.n.NC + c) * NV + sb) * NK + kb) * kTile, rb, acc, ln);
+                mm<3, PI, true, true>(acc, Ys, rb, Ks + kb * PI * kPlane, ln);
+                put(a.dA + ((item * NV + sb) * NK + kb) * kTile, rb, acc, ln);
             }
         }
     }
@@ -632,35 +720,35 @@ __global__ void __launch_bounds__(kThreads) gdr_prep(const PrepArgs<E> a) {
 
 // ---- the scan over items (chunks, or segments of them): state = M_i state + A_i, or with REV state = M_i^T state +
 // A_i from the last item to the first. A warp holds 16 rows of the transposed state, 16 x 64 NK, in registers: its own
-// result is the next step's operand, and nothing but M goes through shared memory. A_i's place takes the state before
-// the item (REV: behind it). With MAP a segment's own map is left instead of states: the state that it makes of
-// nothing, and (rows NV ..) the product of its M.
+// result is the next step's operand, and nothing but M goes through shared memory. S_i takes the state before the item
+// (REV: behind it). With MAP a segment's own map is left instead of states: the state that it makes of nothing, and (rows
+// NV ..) the product of its M.
 struct ScanArgs {
     Sizes n;
     int NV;
-    const float* M;        // [BH][items][NK][NK]
-    float* A;              // [BH][stride][NV][NK]
-    long long stride;      // items of A a sequence
+    const uint8_t* M;      // [BH][items][NK][NK]
+    const float* A;        // [BH][items][NV][NK]
+    uint8_t* S;            // [BH][stride][NV][NK]
+    long long stride;
     int items;             // items of a sequence (at most)
     int chunks;            // 1: an item is a chunk, and sequence lengths count; 0: an item is a segment
     int L, nseg;           // items of a segment (L * nseg >= items)
-    const float* init;     // [BH][dk][dv], null: zero; with nseg > 1 the segments' states
-    const float* init_tiles;  // [BH][init_stride][NV][NK]
-    long long init_stride;
+    const float* init;     // [BH][dk][dv], null: zero
+    const uint8_t* init_tiles;  // or, of segments, [BH][nseg][NV][NK] in three planes
     float* last;           // [BH][dk][dv] or null
-    int end_tile;          // leave the state behind the last chunk in A's place after it, too
-    int round;             // states are read as tf32 operands only
-    float *mapM, *mapA;    // MAP: [BH][nseg][NK][NK], [BH][map_stride][NV][NK]
-    long long map_stride;
+    int end_tile;          // leave the state behind the last chunk behind S's others, too
+    uint8_t* mapM;         // MAP: [BH][nseg][NK][NK]
+    float* mapA;           // MAP: [BH][nseg][NV][NK]
+    const uint8_t* fwd;    // REV: the states [BH][NC + 1][NV][NK] in three planes, for
+    float* ends;           // [BH][NC][NV][4]: parts of <state behind the item, its adjoint>; or null
 };
 
-__host__ __device__ constexpr int scan_stages(int NK) { return NK == 1 ? 3 : 2; }
-__host__ __device__ constexpr int scan_smem(int NK) { return scan_stages(NK) * NK * NK * kTile * 4; }
+constexpr int kScanStages = 2;
+__host__ __device__ constexpr int scan_smem(int NK) { return kScanStages * NK * NK * 3 * kPlane; }
 
-template <int NK, bool REV, bool MAP>
+template <int NK, bool REV, bool MAP, int PS>
 __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
-    constexpr int STAGES = scan_stages(NK);
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const Lane ln;
     const int w = threadIdx.x >> 5;
     const long long bh = blockIdx.x / (unsigned)a.nseg, b = bh / a.n.H;
@@ -681,7 +769,7 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
                         if (16 * w + ln.r + 8 * (e >> 1) == 8 * nt + 2 * ln.j + (e & 1)) acc[kb][nt][e] = 1.f;
             }
         } else if (a.init_tiles) {
-            get(a.init_tiles + (((bh * a.init_stride + seg) * a.NV + sb) * NK + kb) * kTile, w, acc[kb], ln);
+            get_planes<3>(a.init_tiles + (((bh * a.nseg + seg) * a.NV + sb) * NK + kb) * (3 * kPlane), w, acc[kb], ln);
         } else if (a.init) {
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
@@ -694,51 +782,51 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
     }
     auto item = [&](int i) { return REV ? i1 - 1 - i : i0 + i; };
     auto fetch = [&](int i) {
-        if (i < n) {
-            const float* src = a.M + (bh * a.items + item(i)) * (NK * NK * kTile);
-            float* dst = smem + (i % STAGES) * (NK * NK * kTile);
-#pragma unroll 1
-            for (int t = 0; t < NK * NK; ++t) copy_tile(dst + t * kTile, src + t * kTile);
-        }
+        if (i < n) copy_planes<3 * NK * NK>(saddr(smem) + (i % kScanStages) * (3 * NK * NK * kPlane), a.M + (bh * a.items + item(i)) * (3 * NK * NK * kPlane));
         commit();
     };
-    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < kScanStages - 1; ++i) fetch(i);
     for (int i = 0; i < n; ++i) {
-        float* tile = ident ? nullptr : a.A + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * kTile);
-        float add[NK][8][4];
+        float add[NK][8][4], sum = 0.f;
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             if (ident) zero(add[kb]);
-            else get(tile + kb * kTile, w, add[kb], ln);
+            else get(a.A + (((bh * a.items + item(i)) * a.NV + sb) * NK + kb) * kTile, w, add[kb], ln);
         }
-        wait<STAGES - 2>();
+        wait<kScanStages - 2>();
         __syncthreads();  // item i has arrived for every warp, and item i - 1 is read by every warp
-        fetch(i + STAGES - 1);
+        fetch(i + kScanStages - 1);
         if (!MAP) {
 #pragma unroll
-            for (int kb = 0; kb < NK; ++kb) {
-                if (a.round) {
+            for (int kb = 0; kb < NK; ++kb)
+                put_planes<PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
+            if (REV && a.ends) {
+#pragma unroll
+                for (int kb = 0; kb < NK; ++kb) {
                     float t[8][4];
+                    get_planes<3>(a.fwd + (((bh * (a.n.NC + 1) + item(i) + 1) * a.NV + sb) * NK + kb) * (3 * kPlane), w, t, ln);
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) t[nt][e] = __uint_as_float(tf32(acc[kb][nt][e]));
-                    put(tile + kb * kTile, w, t, ln);
-                } else {
-                    put(tile + kb * kTile, w, acc[kb], ln);
+                        for (int e = 0; e < 4; ++e) sum = fmaf(t[nt][e], acc[kb][nt][e], sum);
                 }
             }
         }
-        const float* M = smem + (i % STAGES) * (NK * NK * kTile);
+        const uint32_t M = saddr(smem) + (i % kScanStages) * (3 * NK * NK * kPlane);
         float nw[NK][8][4];
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             zero(nw[kb]);
 #pragma unroll
             for (int kc = 0; kc < NK; ++kc) {
-                if (!REV) mmr<kFull, kFull, false>(nw[kb], acc[kc], M + (kb * NK + kc) * kTile, ln);
-                else mmr<kFull, kFull, true>(nw[kb], acc[kc], M + (kc * NK + kb) * kTile, ln);
+                if (!REV) mmr<3, 3, false>(nw[kb], acc[kc], M + (kb * NK + kc) * (3 * kPlane), ln);
+                else mmr<3, 3, true>(nw[kb], acc[kc], M + (kc * NK + kb) * (3 * kPlane), ln);
             }
+        }
+        if (!MAP && REV && a.ends) {
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if ((threadIdx.x & 31) == 0) a.ends[((bh * a.n.NC + item(i)) * a.NV + sb) * 4 + w] = sum;
         }
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb)
@@ -751,23 +839,31 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             if (!ident) {
-                put(a.mapA + (((bh * a.map_stride + seg) * a.NV + sb) * NK + kb) * kTile, w, acc[kb], ln);
+                put(a.mapA + (((bh * a.nseg + seg) * a.NV + sb) * NK + kb) * kTile, w, acc[kb], ln);
             } else {
                 // rows of the transposed product: element (m, k) of the map is acc[k][m]
-                float* t = a.mapM + (((bh * a.nseg + seg) * NK + kb) * NK + (sb - a.NV)) * kTile;
+                uint8_t* t = a.mapM + (((bh * a.nseg + seg) * NK + kb) * NK + (sb - a.NV)) * (3 * kPlane);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        t[at(8 * nt + 2 * ln.j + (e & 1), 16 * w + ln.r + 8 * (e >> 1))] = acc[kb][nt][e];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[3];
+                        split<3>(acc[kb][nt][2 * h], acc[kb][nt][2 * h + 1], p);
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) {
+                            const int row = 8 * nt + 2 * ln.j, col = 16 * w + ln.r + 8 * h;
+                            *reinterpret_cast<uint16_t*>(t + m * kPlane + pat(row, col)) = (uint16_t)p[m];
+                            *reinterpret_cast<uint16_t*>(t + m * kPlane + pat(row + 1, col)) = (uint16_t)(p[m] >> 16);
+                        }
+                    }
             }
         }
         return;
     }
+    const bool ends = i1 == count && (n > 0 || seg == 0);
 #pragma unroll
     for (int kb = 0; kb < NK; ++kb) {
-        const bool ends = i1 == count && (n > 0 || seg == 0);
-        if (a.end_tile && ends) put(a.A + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * kTile, w, acc[kb], ln);
+        if (a.end_tile && ends) put_planes<PS>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
         if (!a.last) continue;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -797,35 +893,41 @@ inline Cut cut_of(long long BH, int NC, int NK, int NV) {
     return best;
 }
 
-// The workspace of one call, in floats from its start.
+// The workspace of one call, in bytes from its start.
 struct Layout {
     int NK, NV, NC;
     Cut cut;
-    long long X, M, S, P, Z, dA, dZ, dq, dk, total;
+    long long X, M, A, S, P, Z, G, dA, dS, dZ, dG, ends, dq, dk, total;
 };
 inline Layout layout_of(const GdrSizes& n, bool bwd) {
     Layout l = {};
     l.NK = (n.dk + kC - 1) / kC;
     l.NV = (n.dv + kC - 1) / kC;
     l.NC = (n.T + kC - 1) / kC;
-    const long long BH = n.B * n.H, sq = (long long)l.NK * l.NK * kTile, st = (long long)l.NV * l.NK * kTile;
+    const long long BH = n.B * n.H, sq = (long long)l.NK * l.NK, st = (long long)l.NV * l.NK;
+    const int ps = n.bf16 && !bwd ? 2 : 3;
     l.cut = cut_of(BH, l.NC, l.NK, l.NV);
     long long at = 0;
-    auto take = [&](long long count) {
+    auto take = [&](long long bytes) {
         const long long o = at;
-        at += (count + 63) / 64 * 64;
+        at += (bytes + 255) / 256 * 256;
         return o;
     };
-    const long long seg = l.cut.nseg > 1 ? l.cut.nseg : 0;
-    l.X = take(BH * l.NC * kTile);
-    l.M = take(BH * l.NC * sq);
-    l.S = take(BH * (l.NC + 1) * st);
-    l.P = take(BH * seg * sq);
-    l.Z = take(BH * seg * st);
+    const long long seg = l.cut.nseg > 1 ? l.cut.nseg : 0, tile = kTile * 4;
+    l.X = take(BH * l.NC * ps * kPlane);
+    l.M = take(BH * l.NC * sq * 3 * kPlane);
+    l.A = take(BH * l.NC * st * tile);
+    l.S = take(BH * (l.NC + 1) * st * ps * kPlane);
+    l.P = take(BH * seg * sq * 3 * kPlane);
+    l.Z = take(BH * seg * st * tile);
+    l.G = take(BH * seg * st * 3 * kPlane);
     if (bwd) {
-        l.dA = take(BH * l.NC * st);
-        l.dZ = take(BH * seg * st);
-        const long long shared = n.H != n.Hk ? BH * n.T * n.dk : 0;
+        l.dA = take(BH * l.NC * st * tile);
+        l.dS = take(BH * l.NC * st * 3 * kPlane);
+        l.dZ = take(BH * seg * st * tile);
+        l.dG = take(BH * seg * st * 3 * kPlane);
+        l.ends = take(BH * l.NC * l.NV * 16);
+        const long long shared = n.H != n.Hk ? BH * n.T * n.dk * 4 : 0;
         l.dq = take(shared);
         l.dk = take(shared);
     }
@@ -843,45 +945,49 @@ inline Sizes sizes_of(const GdrArgs& a, const Layout& l) {
 
 // The states' scan (REV: the adjoints'), in one pass or by segments. The segments' products of M are the forward
 // pass's: the backward one reads them transposed.
-template <int NK, bool REV>
-bool run_scan(const Sizes& n, const Layout& l, float* ws, const float* init, float* last, bool end_tile, bool round, cudaStream_t s) {
+template <int NK, bool REV, int PS>
+bool run_scan(const Sizes& n, const Layout& l, uint8_t* ws, const float* init, float* last, bool end_tile, cudaStream_t s) {
     ScanArgs c = {};
     c.n = n;
     c.NV = l.NV;
     c.M = ws + l.M;
-    c.A = ws + (REV ? l.dA : l.S);
+    c.A = reinterpret_cast<const float*>(ws + (REV ? l.dA : l.A));
+    c.S = ws + (REV ? l.dS : l.S);
     c.stride = l.NC + (REV ? 0 : 1);
     c.items = l.NC;
     c.chunks = 1;
     c.L = l.cut.L;
     c.nseg = l.cut.nseg;
     const int smem = scan_smem(NK);
-    if (!want_smem(gdr_scan<NK, REV, false>, smem) || !want_smem(gdr_scan<NK, REV, true>, smem)) return false;
+    if (!want_smem(gdr_scan<NK, REV, false, PS>, smem)) return false;
     const unsigned x = (unsigned)(n.BH * l.cut.nseg);
     if (l.cut.nseg > 1) {
+        if (!want_smem(gdr_scan<NK, REV, true, 3>, smem) || !want_smem(gdr_scan<NK, REV, false, 3>, smem)) return false;
         ScanArgs m = c;
         m.mapM = ws + l.P;
-        m.mapA = ws + (REV ? l.dZ : l.Z);
-        m.map_stride = l.cut.nseg;
-        gdr_scan<NK, REV, true><<<dim3(x, l.NV + (REV ? 0 : NK)), kThreads, smem, s>>>(m);
+        m.mapA = reinterpret_cast<float*>(ws + (REV ? l.dZ : l.Z));
+        gdr_scan<NK, REV, true, 3><<<dim3(x, l.NV + (REV ? 0 : NK)), kThreads, smem, s>>>(m);
         ScanArgs t = c;
         t.M = ws + l.P;
-        t.A = ws + (REV ? l.dZ : l.Z);
+        t.A = m.mapA;
+        t.S = ws + (REV ? l.dG : l.G);
         t.stride = t.items = t.L = l.cut.nseg;
         t.chunks = 0;
         t.nseg = 1;
         t.init = init;
         t.last = last;
-        gdr_scan<NK, REV, false><<<dim3((unsigned)n.BH, l.NV), kThreads, smem, s>>>(t);
-        c.init_tiles = t.A;
-        c.init_stride = l.cut.nseg;
+        gdr_scan<NK, REV, false, 3><<<dim3((unsigned)n.BH, l.NV), kThreads, smem, s>>>(t);
+        c.init_tiles = t.S;
     } else {
         c.init = init;
         c.last = last;
     }
     c.end_tile = end_tile;
-    c.round = round;
-    gdr_scan<NK, REV, false><<<dim3(x, l.NV), kThreads, smem, s>>>(c);
+    if (REV) {
+        c.fwd = ws + l.S;
+        c.ends = reinterpret_cast<float*>(ws + l.ends);
+    }
+    gdr_scan<NK, REV, false, PS><<<dim3(x, l.NV), kThreads, smem, s>>>(c);
     return true;
 }
 

@@ -7,7 +7,8 @@
 //   dK = dP^T Q + H K - diag(e^G) Z S^T + diag(w beta) E dS'^T,
 //   dbeta_j = E_j.(dU - N^T Z)_j.
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
-// writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
+// writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides (the adjoints' scan sums
+// it); dg is the sum of dG
 // from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
 // gdr_grad takes the gradients, all chunks at once.
 
@@ -26,13 +27,18 @@ struct GradArgs {
     Ten<float> beta, g, dbeta, dg;
     Ten<E> dq, dk, dv;
     float *pq, *pk;  // [B,H,T,dk] instead of dq and dk where heads share theirs, or null
-    const float *X, *S, *dS;
+    const uint8_t *X, *S, *dS;
+    const float* ends;
 };
 
-template <int NK, int NV>
-constexpr int grad_smem() { return (NK + 3 * NV + 2) * kTile * 4; }
+// K, dO, E, Z and what comes and goes. With one tile of S and dS' (and bf16) all of it is on its way early: S and dS'
+// in E's and Z's places, X and Q in the last; else these come one after the other in three planes.
+template <typename E, int NK, int NV>
+__host__ __device__ constexpr bool grad_one() { return NK * NV == 1 && sizeof(E) == 2; }
+template <typename E, int NK, int NV>
+__host__ __device__ constexpr int grad_smem() { return ((NK + NV) * planes<E>() + 6 * NV + (grad_one<E, NK, NV>() ? 5 : 3)) * kPlane; }
 
-// x and y summed over the four lanes that hold a row.
+// Summed over the four lanes that hold a row.
 __device__ __forceinline__ float row_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -40,19 +46,19 @@ __device__ __forceinline__ float row_sum(float x) {
 
 template <typename E, int NK, int NV>
 __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
-    constexpr bool ONE = NK * NV == 1;  // one tile of S and dS': both stay
-    constexpr int PI = sizeof(E) == 2 ? kExact : kFull;
-    // operands that reach only dK, rounded to bf16: its steps are eight of tf32's
-    constexpr int PL = sizeof(E) == 2 ? kRound : kFull;
-    extern __shared__ __align__(16) float smem[];
+    constexpr bool ONE = grad_one<E, NK, NV>();
+    constexpr int PI = planes<E>();
+    // planes of operands that reach only dK, rounded to bf16: two where the other has one
+    constexpr int PL = sizeof(E) == 2 ? 2 : 3, P1 = sizeof(E) == 2 ? 1 : 3;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
-    __shared__ float own[kC], dbe[kC], part[kThreads / 32];
-    float* K = smem;
-    float* dO = K + NK * kTile;
-    float* Et = dO + NV * kTile;
-    float* Zt = Et + NV * kTile;
-    float* W0 = Zt + NV * kTile;
-    float* W1 = W0 + kTile;
+    __shared__ float own[kC], dbe[kC];
+    uint8_t* K = smem;
+    uint8_t* dO = K + NK * PI * kPlane;
+    uint8_t* Et = dO + NV * PI * kPlane;
+    uint8_t* Zt = Et + NV * 3 * kPlane;
+    uint8_t* W = Zt + NV * 3 * kPlane;
+    const uint32_t Ks = saddr(K), Os = saddr(dO), Es0 = saddr(Et), Zs0 = saddr(Zt), Ws = saddr(W);
     const Lane ln;
     const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
@@ -78,27 +84,50 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         }
         return;
     }
-    const long long st = (long long)NV * NK * kTile;
-    const float* St = a.S + (bh * (a.n.NC + 1) + c) * st;  // the state behind the chunk lies st further
-    const float* dSt = a.dS + (bh * a.n.NC + c) * st;
-    const float* Xt = a.X + (bh * a.n.NC + c) * kTile;
-    copy_tile(W0, St);
-    copy_tile(W1, dSt);
+    const long long st = (long long)NV * NK * 3 * kPlane;
+    const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * st;
+    const uint8_t* dSt = a.dS + (bh * a.n.NC + c) * st;
+    const uint8_t* Xt = a.X + (bh * a.n.NC + c) * (3 * kPlane);
+    auto load_q = [&](uint8_t* to, int kb) {
+        load_planes(to, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
+    };
+    // a tile of planes that every warp then reads
+    auto bring = [&](uint32_t to, const uint8_t* from) {
+        __syncthreads();
+        copy_planes<3>(to, from);
+        commit();
+        wait<0>();
+        __syncthreads();
+    };
+    const uint32_t Xs = ONE ? Ws + 2 * kPlane : Ws;
+#pragma unroll 1
+    for (int kb = 0; kb < NK; ++kb) load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, dk - kb * kC, a.k.vec);
+    if (ONE) load_q(W, 0);
+    commit();
+#pragma unroll 1
+    for (int sb = 0; sb < NV; ++sb) load_planes(dO + sb * PI * kPlane, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
+    if (ONE) {
+        copy_planes<3>(Es0, St);
+        copy_planes<3>(Zs0, dSt);
+        copy_planes<3>(Xs, Xt);
+    }
     commit();
     load_scal(s, a.beta, a.g, b, h, t0, live);
-#pragma unroll 1
-    for (int kb = 0; kb < NK; ++kb) load_tile(K + kb * kTile, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, dk - kb * kC, a.k.vec);
-#pragma unroll 1
-    for (int sb = 0; sb < NV; ++sb) load_tile(dO + sb * kTile, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
     // P transposed: rows j, columns i >= j
     float P[8][4];
     zero(P);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
-        if (kb > 0) __syncthreads();
-        load_tile(Et, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
+        if (!ONE) {
+            if (kb > 0) __syncthreads();
+            load_q(W, kb);
+            commit();
+            wait<0>();
+        } else {
+            wait<1>();
+        }
         __syncthreads();
-        mm<PI, PI, false, false>(P, K + kb * kTile, rb, Et, ln, 0, 8, 2 * rb, 8);
+        mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Ws, ln, 0, 4, rb, 4);
     }
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -107,40 +136,34 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
             const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
             P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
         }
-    float ends = 0.f;                               // <dS', S'>
+    float q1[8][4];                                 // ONE: dO S^T, taken while S is there
     float sb_[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};  // the rows' dbeta and dV.V
+    zero(q1);
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
+        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
         zero(x);
         zero(d);
-#pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) {
-            if (sb + kb > 0) {
-                __syncthreads();
-                copy_tile(W0, St + (sb * NK + kb) * kTile);
-                copy_tile(W1, dSt + (sb * NK + kb) * kTile);
-                commit();
-            }
+        if (ONE) {
             wait<0>();
             __syncthreads();
-            mm<PI, kFull, false, false>(x, K + kb * kTile, rb, W0, ln);
-            mm<PI, kFull, false, false>(d, K + kb * kTile, rb, W1, ln);
-            const float* S1 = St + st + (sb * NK + kb) * kTile;
-#pragma unroll
-            for (int i = 0; i < kTile / 4 / kThreads; ++i) {
-                const int o = 4 * (threadIdx.x + i * kThreads);
-                const float4 u = *reinterpret_cast<const float4*>(S1 + o), v = *reinterpret_cast<const float4*>(W1 + o);
-                ends += (u.x * v.x + u.y * v.y) + (u.z * v.z + u.w * v.w);
+            mm<PI, 3, false, false>(x, Ks, rb, Es, ln);
+            mm<PI, 3, false, true>(q1, Ob, rb, Es, ln);
+            mm<PI, 3, false, false>(d, Ks, rb, Zs, ln);
+        } else {
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) {
+                bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
+                mm<PI, 3, false, false>(x, Ks + kb * PI * kPlane, rb, Ws, ln);
+                bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
+                mm<PI, 3, false, false>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
             }
         }
-        __syncthreads();  // Q in E's place, dS' and the states are read
-        copy_tile(W1, Xt);
-        commit();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<kFull, PI, true>(d, P, dO + sb * kTile, ln, 2 * rb, 8);  // dU
+        mmr<3, PI, true>(d, P, Ob, ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int row = 16 * rb + ln.r + 8 * hf;
@@ -153,28 +176,29 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
                 x[nt][2 * hf + 1] = fmaf(-s.eG[row], x[nt][2 * hf + 1], v.y);
             }
         }
-        float* Es = Et + sb * kTile;
-        float* Zs = Zt + sb * kTile;
-        put(Es, rb, x, ln);
+        if (ONE) __syncthreads();  // S and dS' are read
+        else bring(Xs, Xt);
+        put_planes<3>(Et + sb * 3 * kPlane, rb, x, ln);
         float z[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[nt][e] = d[nt][e] * s.beta[16 * rb + ln.r + 8 * (e >> 1)];
-        put(Zs, rb, z, ln);
-        wait<0>();
+        put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
         __syncthreads();
         zero(x);
         zero(z);
-        mm<kFull, kFull, false, true>(x, W1, rb, Es, ln, 0, 2 * rb + 2);  // E
-        mm<kFull, kFull, true, true>(z, W1, rb, Zs, ln, 2 * rb, 8);       // Z
+        mm<3, 3, false, true>(x, Xs, rb, Es, ln, 0, rb + 1);  // E
+        mm<3, 3, true, true>(z, Xs, rb, Zs, ln, rb, 4);       // Z
         __syncthreads();
-        put(Es, rb, x, ln);
-        put(Zs, rb, z, ln);
-        if (ONE) {
-            copy_tile(W1, dSt);
+        if (ONE) {  // for dK: two planes each, and Q behind them
+            copy_planes<2>(Ws, St);
+            copy_planes<2>(Ws + 2 * kPlane, dSt);
+            load_q(W + 4 * kPlane, 0);
             commit();
         }
+        put_planes<3>(Et + sb * 3 * kPlane, rb, x, ln);
+        put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
         write_rows(a.dv.row0(b, h, t0) + sb * kC, a.dv.st, a.dv.pair, rb, z, ln, rows, live, dv - sb * kC);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -192,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         float N[8][4];
         zero(N);
 #pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(N, K + kb * kTile, rb, K + kb * kTile, ln, 0, 8, 2 * rb, 8);
+        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(N, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, rb, 4);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -201,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
                 N[nt][e] = j < i ? N[nt][e] * decay(s, i, j) : 0.f;
             }
         zero(z);
-        mmr<kFull, kFull, true>(z, N, Zs, ln, 2 * rb, 8);
+        mmr<3, 3, true>(z, N, Zs, ln, rb, 4);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -215,11 +239,11 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
     zero(x);
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
-        const float *Es = Et + sb * kTile, *Zs = Zt + sb * kTile, *Os = dO + sb * kTile;
-        mm<PI, kFull, false, false>(A1, Os, rb, Es, ln, 0, 8, 0, 2 * rb + 2);
-        mm<PL, PI, false, false>(A3, Es, rb, Os, ln, 0, 8, 2 * rb, 8);
-        mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 8, 0, 2 * rb + 2);
-        mm<PL, PL, false, false>(x, Es, rb, Zs, ln, 0, 8, 2 * rb, 8);
+        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
+        mm<PI, 3, false, false>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
+        mm<PL, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
+        mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
+        mm<PL, PL, false, false>(x, Es, rb, Zs, ln, 0, 4, rb, 4);
     }
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -234,26 +258,32 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
     float sq[2] = {0.f, 0.f};
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
-        zero(x);
-        zero(d);
         float t[8][4];
+        zero(d);
         zero(t);
-#pragma unroll 1
-        for (int sb = 0; sb < NV; ++sb) {
-            if (!ONE) {
-                __syncthreads();
-                copy_tile(W0, St + (sb * NK + kb) * kTile);
-                copy_tile(W1, dSt + (sb * NK + kb) * kTile);
-                commit();
-            }
+        if (ONE) {
             wait<0>();
             __syncthreads();
-            mm<PI, kFull, false, true>(x, dO + sb * kTile, rb, W0, ln);
-            mm<PL, PL, false, true>(d, Zt + sb * kTile, rb, W0, ln);
-            mm<PL, PL, false, true>(t, Et + sb * kTile, rb, W1, ln);
+            mm<PL, PL, false, true>(d, Zs0, rb, Ws, ln);
+            mm<PL, PL, false, true>(t, Es0, rb, Ws + 2 * kPlane, ln);
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[nt][e] = q1[nt][e];
+        } else {
+            zero(x);
+#pragma unroll 1
+            for (int sb = 0; sb < NV; ++sb) {
+                bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
+                mm<PI, 3, false, true>(x, Os + sb * PI * kPlane, rb, Ws, ln);
+                mm<PL, PL, false, true>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
+                bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
+                mm<PL, PL, false, true>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
+            }
+            __syncthreads();
+            load_q(W, kb);
+            commit();
         }
-        __syncthreads();
-        load_tile(W0, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -262,28 +292,29 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
                 x[nt][e] *= s.eG[row] * a.n.scale;
                 d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
             }
-        mmr<kFull, PI, true>(x, A1, K + kb * kTile, ln, 0, 2 * rb + 2);
+        mmr<3, PI, true>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
         write_qk(a.dq, a.pq, x, kb);
-        mmr<PL, PI, true>(d, H, K + kb * kTile, ln);
-        __syncthreads();
-        mmr<PL, PI, true>(d, A3, W0, ln, 2 * rb, 8);
+        mmr<PL, P1, true>(d, H, Ks + kb * PI * kPlane, ln);
+        uint8_t* Qt = ONE ? W + 4 * kPlane : W;
+        if (!ONE) {
+            wait<0>();
+            __syncthreads();
+        }
+        mmr<PL, P1, true>(d, A3, saddr(Qt), ln, rb, 4);
         write_qk(a.dk, a.pk, d, kb);
-        get(W0, rb, t, ln);
+        get_planes<PI>(Qt, rb, t, ln);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sq[e >> 1] = fmaf(x[nt][e], t[nt][e], sq[e >> 1]);
     }
-    // the rows' sums: own = dQ.Q - dV.V, and the ends'
+    // the rows' sums: own = dQ.Q - dV.V
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         const int row = 16 * rb + ln.r + 8 * hf;
         const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]);
         if (ln.j == 0) own[row] = o, dbe[row] = e;
     }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) ends += __shfl_xor_sync(0xffffffffu, ends, m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ends;
     __syncthreads();
     if (threadIdx.x >= 32) return;
     const int l = threadIdx.x;
@@ -293,7 +324,10 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         const double o = __shfl_down_sync(0xffffffffu, sum, m);
         if (l + m < 32) sum += o;
     }
-    const double all = ((double)part[0] + part[1]) + ((double)part[2] + part[3]);
+    double all = 0.;
+    const float* ends = a.ends + (bh * a.n.NC + c) * (NV * 4);
+#pragma unroll
+    for (int i = 0; i < NV * 4; ++i) all += ends[i];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
@@ -347,17 +381,18 @@ int launch_bwd(const GdrArgs& a, cudaStream_t st) {
     p.dout = ten<const E>(a.dout, a.n.dv);
     p.beta = ten<float>(a.beta, 1);
     p.g = ten<float>(a.g, 1);
-    p.X = a.ws + l.X;
-    p.M = a.ws + l.M;
-    p.A = a.ws + l.S;
-    p.dA = a.ws + l.dA;
-    const int prep = (2 * NK + 3) * kTile * 4;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(a.ws);
+    p.X = ws + l.X;
+    p.M = ws + l.M;
+    p.A = reinterpret_cast<float*>(ws + l.A);
+    p.dA = reinterpret_cast<float*>(ws + l.dA);
+    constexpr int prep = prep_smem<E, NK, true>();
     if (!want_smem(gdr_prep<E, NK, true>, prep)) return FALCON_ERR_CUDA;
     if (grid) {
         gdr_prep<E, NK, true><<<grid, kThreads, prep, st>>>(p);
-        if (!run_scan<NK, false>(n, l, a.ws, a.S0, nullptr, true, false, st)) return FALCON_ERR_CUDA;
+        if (!run_scan<NK, false, 3>(n, l, ws, a.S0, nullptr, true, st)) return FALCON_ERR_CUDA;
     }
-    if (!run_scan<NK, true>(n, l, a.ws, a.dS_final, a.dS0, false, false, st)) return FALCON_ERR_CUDA;
+    if (!run_scan<NK, true, 3>(n, l, ws, a.dS_final, a.dS0, false, st)) return FALCON_ERR_CUDA;
     if (grid) {
         GradArgs<E> g = {};
         g.n = n;
@@ -368,21 +403,22 @@ int launch_bwd(const GdrArgs& a, cudaStream_t st) {
         g.dk = ten<E>(a.dk, a.n.dk);
         g.dv = ten<E>(a.dv, a.n.dv);
         const bool shared = n.group > 1;
-        g.pq = shared ? a.ws + l.dq : nullptr;
-        g.pk = shared ? a.ws + l.dk : nullptr;
+        g.pq = shared ? reinterpret_cast<float*>(ws + l.dq) : nullptr;
+        g.pk = shared ? reinterpret_cast<float*>(ws + l.dk) : nullptr;
         g.X = p.X;
-        g.S = p.A;
-        g.dS = p.dA;
+        g.S = ws + l.S;
+        g.dS = ws + l.dS;
+        g.ends = reinterpret_cast<const float*>(ws + l.ends);
         if (l.NV == 1) {
-            if (!want_smem(gdr_grad<E, NK, 1>, grad_smem<NK, 1>())) return FALCON_ERR_CUDA;
-            gdr_grad<E, NK, 1><<<grid, kThreads, grad_smem<NK, 1>(), st>>>(g);
+            if (!want_smem(gdr_grad<E, NK, 1>, grad_smem<E, NK, 1>())) return FALCON_ERR_CUDA;
+            gdr_grad<E, NK, 1><<<grid, kThreads, grad_smem<E, NK, 1>(), st>>>(g);
         } else {
-            if (!want_smem(gdr_grad<E, NK, 2>, grad_smem<NK, 2>())) return FALCON_ERR_CUDA;
-            gdr_grad<E, NK, 2><<<grid, kThreads, grad_smem<NK, 2>(), st>>>(g);
+            if (!want_smem(gdr_grad<E, NK, 2>, grad_smem<E, NK, 2>())) return FALCON_ERR_CUDA;
+            gdr_grad<E, NK, 2><<<grid, kThreads, grad_smem<E, NK, 2>(), st>>>(g);
         }
         if (shared) {
-            SumArgs<E> q = {a.ws + l.dq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
-            k.part = a.ws + l.dk;
+            SumArgs<E> q = {g.pq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
+            k.part = g.pk;
             k.to = g.dk;
             gdr_sum<E><<<dim3((unsigned)((q.count + 7) / 8), 2), 256, 0, st>>>(q, k);
         }
