@@ -24,7 +24,7 @@ template <typename E, int NK>
 __host__ __device__ constexpr int out_smem() { return (2 * NK * planes<E>() + 2 * state_planes<E, false>()) * kPlane; }
 
 template <typename E, int NK>
-__global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(const OutArgs<E> a) {
     constexpr int PI = planes<E>(), PS = state_planes<E, false>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
@@ -34,7 +34,8 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
     uint8_t* W = X + PS * kPlane;
     const uint32_t Ks = saddr(K), Qs = saddr(Q), Xs = saddr(X), Ws = saddr(W);
     const Lane ln;
-    const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
+    const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
     const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
         return;
     }
     const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * PS * kPlane);
+    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
         load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
     copy_planes<PS>(Ws, St);
     copy_planes<PS>(Xs, a.X + (bh * a.n.NC + c) * (PS * kPlane));
     commit();
-    load_scal(s, a.beta, a.g, b, h, t0, live);
+    make_scal(s, gates);
     wait<1>();
     __syncthreads();
     float P[8][4];
@@ -74,6 +76,8 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         float o[8][4];
+        Rows<E> v;
+        load_rows(v, a.v.row0(b, h, t0) + sb * kC, a.v.st, a.v.pair, rb, ln, live, a.n.dv - sb * kC);
         zero(acc);
         zero(o);
 #pragma unroll 1
@@ -91,15 +95,12 @@ __global__ void __launch_bounds__(kThreads) gdr_out(const OutArgs<E> a) {
         __syncthreads();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const int row = 16 * rb + ln.r + 8 * hf;
-            const float eG = s.eG[row];
-            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+            const float eG = s.eG[16 * rb + ln.r + 8 * hf];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
-                const int col = 8 * nt + 2 * ln.j;
-                const float2 v = row < live ? load2(pv + col, a.n.dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
-                acc[nt][2 * hf] = fmaf(-eG, acc[nt][2 * hf], v.x);
-                acc[nt][2 * hf + 1] = fmaf(-eG, acc[nt][2 * hf + 1], v.y);
+                const float2 x = v.of(nt, hf);
+                acc[nt][2 * hf] = fmaf(-eG, acc[nt][2 * hf], x.x);
+                acc[nt][2 * hf + 1] = fmaf(-eG, acc[nt][2 * hf + 1], x.y);
                 o[nt][2 * hf] *= eG * a.n.scale;
                 o[nt][2 * hf + 1] *= eG * a.n.scale;
             }

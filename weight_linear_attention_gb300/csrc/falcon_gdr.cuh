@@ -209,7 +209,8 @@ __device__ __forceinline__ void get_cols(const float* T, int rb, float (&acc)[8]
         for (int e = 0; e < 4; ++e) acc[nt][e] = T[at(8 * nt + 2 * ln.j + (e & 1), 16 * rb + ln.r + 8 * (e >> 1))];
 }
 // Rows 16 rb .. of N planes, in shared or global memory.
-template <int N>
+// OUT: as many of them are written.
+template <int N, int OUT = N>
 __device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc)[8][4], const Lane& ln) {
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -219,7 +220,7 @@ __device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc
             split<N>(acc[nt][2 * h], acc[nt][2 * h + 1], p);
             uint8_t* to = T + (16 * rb + ln.r + 8 * h) * 128 + ((nt ^ ln.r) << 4) + 4 * ln.j;
 #pragma unroll
-            for (int m = 0; m < N; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
+            for (int m = 0; m < OUT; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
         }
 }
 template <int N>
@@ -335,6 +336,40 @@ __device__ __forceinline__ void store2(bf16* p, float x, float y, int left, bool
     }
 }
 
+// Rows 16 rb .. of a tensor as a product's registers have them, kept as they come: on their way while a product runs.
+template <typename E>
+struct Rows;
+template <>
+struct Rows<float> {
+    float2 v[8][2];
+    __device__ __forceinline__ float2 of(int nt, int h) const { return v[nt][h]; }
+    __device__ __forceinline__ void take(const float* p, int left, bool pair, int nt, int h) { v[nt][h] = load2(p, left, pair); }
+};
+template <>
+struct Rows<bf16> {
+    uint32_t v[8][2];
+    __device__ __forceinline__ float2 of(int nt, int h) const {
+        return make_float2(__uint_as_float(v[nt][h] << 16), __uint_as_float(v[nt][h] & 0xffff0000u));
+    }
+    __device__ __forceinline__ void take(const bf16* p, int left, bool pair, int nt, int h) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        if (pair && left >= 2) v[nt][h] = *reinterpret_cast<const uint32_t*>(p);
+        else v[nt][h] = (left > 0 ? q[0] : 0u) | (left > 1 ? (uint32_t)q[1] << 16 : 0u);
+    }
+};
+template <typename E>
+__device__ __forceinline__ void load_rows(Rows<E>& r, const E* p, long long st, bool pair, int rb, const Lane& ln, int live, int cols) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = 16 * rb + ln.r + 8 * h;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const int col = 8 * nt + 2 * ln.j;
+            r.take(p + row * st + col, row < live ? cols - col : 0, pair, nt, h);
+        }
+    }
+}
+
 // A tensor of the call. vec: 16-byte accesses hold everywhere, pair: those of two elements.
 template <typename E>
 struct Ten {
@@ -366,9 +401,10 @@ __device__ __forceinline__ void write_rows(E* p, long long st, bool pair, int rb
     }
 }
 
-// ---- a chunk's gains and decays
+// ---- a chunk's gains and decays. Sums of log decays are pairs of floats, hi + lo, 48 bits: a difference of two, at whatever
+// size, keeps fp32's relative precision. (In double, whose units are few, this took 10 us of a chunk's 18.)
 struct Scal {
-    float beta[kC], hi[kC], lo[kC];  // G / ln 2 = hi + lo: a difference of two keeps fp32's relative precision
+    float beta[kC], hi[kC], lo[kC];  // G / ln 2 = hi + lo
     float eG[kC], w[kC], bw[kC];     // e^G, e^{G_C - G}, beta w
     float eC;
 };
@@ -377,53 +413,75 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float exp_sum(double x) {
-    const float hi = (float)x, e = expf(hi);
-    return fmaf(e, (float)(x - hi), e);
+// 2^(hi + lo), lo being small.
+__device__ __forceinline__ float ex2(float hi, float lo) {
+    const float e = ex2(hi);
+    return fmaf(e, lo * 0.69314718f, e);
 }
 __device__ __forceinline__ float decay(const Scal& s, int i, int j) { return ex2((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j])); }
 
-// Below this a log decay's factor is 0 in fp32 and so are all that contain it; sums of 64 stay exact enough in double.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    const float h = s + e;
+    return Two{h, e - (h - s)};
+}
+
+// Below this a log decay's factor is 0 in fp32 and so are all that contain it; sums of 64 keep their lesser parts.
 constexpr float kLeast = -1e5f;
 
-__device__ __forceinline__ void load_scal(Scal& s, const Ten<float>& beta, const Ten<float>& g, long long b, long long h,
-                                          long long t0, int live) {
+// The gains and log decays of tokens 2 l and 2 l + 1, in the lanes of the first warp: read early, summed late.
+struct Gates {
+    float beta[2], g[2];
+};
+__device__ __forceinline__ Gates load_gates(const Ten<float>& beta, const Ten<float>& g, long long b, long long h, long long t0, int live) {
+    Gates r = {};
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = 2 * threadIdx.x + e;
+            if (t < live) {
+                r.beta[e] = beta.row0(b, h, t0)[t * beta.st];
+                r.g[e] = g.row0(b, h, t0)[t * g.st];
+            }
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ void make_scal(Scal& s, const Gates& r) {
     if (threadIdx.x >= 32) return;
     const int l = threadIdx.x;
-    const float* pb = beta.row0(b, h, t0);
-    const float* pg = g.row0(b, h, t0);
-    float v[2];
-    double x[2];
+    Two x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int t = 2 * l + e;
-        const bool in = t < live;
-        v[e] = in ? pb[t * beta.st] : 0.f;
-        float y = in ? pg[t * g.st] : 0.f;
-        y = y < kLeast ? kLeast : y;
-        x[e] = y;
+        const float g = r.g[e] < kLeast ? kLeast : r.g[e];
+        x[e].hi = g * 1.44269502f;  // 1 / ln 2 = 1.44269502 + 1.92596299e-8
+        x[e].lo = fmaf(g, 1.44269502f, -x[e].hi) + g * 1.92596299e-8f;
     }
-    double sum = x[0] + x[1];
+    Two sum = add(x[0], x[1]);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (l >= d) sum += o;
+        const Two o = {__shfl_up_sync(0xffffffffu, sum.hi, d), __shfl_up_sync(0xffffffffu, sum.lo, d)};
+        if (l >= d) sum = add(o, sum);
     }
-    const double all = __shfl_sync(0xffffffffu, sum, 31);
-    const double G[2] = {sum - x[1], sum};
+    const Two all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+    const Two G[2] = {add(sum, Two{-x[1].hi, -x[1].lo}), sum};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
-        const double g2 = G[e] * 1.4426950408889634074;
-        const float hi = (float)g2, w = exp_sum(all - G[e]);
-        s.beta[t] = v[e];
-        s.hi[t] = hi;
-        s.lo[t] = (float)(g2 - hi);
-        s.eG[t] = exp_sum(G[e]);
+        const Two left = add(all, Two{-G[e].hi, -G[e].lo});
+        const float w = ex2(left.hi, left.lo);
+        s.beta[t] = r.beta[e];
+        s.hi[t] = G[e].hi;
+        s.lo[t] = G[e].lo;
+        s.eG[t] = ex2(G[e].hi, G[e].lo);
         s.w[t] = w;
-        s.bw[t] = v[e] * w;
+        s.bw[t] = r.beta[e] * w;
     }
-    if (l == 31) s.eC = exp_sum(all);
+    if (l == 31) s.eC = ex2(all.hi, all.lo);
 }
 
 // ---- the inverse of I + A, A strictly lower triangular in tile T, in its place: 16 x 16 diagonal blocks by
@@ -439,27 +497,28 @@ __device__ __forceinline__ void split(float x, uint32_t& h, uint32_t& l) {
     h = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     l = __float_as_uint(x - __uint_as_float(h));
 }
-__device__ __forceinline__ void corner(const float* T, int o, int n, int mb, float (&res)[4][4], const Lane& ln) {
-    // columns o + 16 mb .. + 15 of the corner below the block of n rows at o, transposed: res[nt][e] is column
-    // 16 mb + r + 8 (e / 2), row 8 nt + 2j + e % 2 of it
-    float x[4][4];
+// Columns o + 16 mb .. + 15 of the corner below the block of N rows at o, its rows 16 half .. + 15, transposed: res[nt][e]
+// is column 16 mb + r + 8 (e / 2), row 16 half + 8 nt + 2 j + e % 2 of it.
+template <int N>
+__device__ __forceinline__ void corner(const float* T, int o, int mb, int half, float (&res)[2][4], const Lane& ln) {
+    float x[N / 8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N / 8; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] = 0.f, res[i][e] = 0.f;
-    const int nn = n / 8;
-    for (int kk = 2 * mb; kk < nn; ++kk) {  // Y11[k][m] is 0 for k < m
-        float a[4];
+        for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) res[e >> 2][e & 3] = 0.f;
+    const int rows = 2 * half + 2;  // Y22[n][k] is 0 for k > n: rows of A21 Y11 that count, by 8
+#pragma unroll
+    for (int kk = 0; kk < N / 8; ++kk) {
+        if (kk < 2 * mb) continue;  // Y11[k][m] is 0 for k < m
         uint32_t ah[4], al[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            a[e] = T[at(o + 8 * kk + 2 * ln.j + (e >> 1), o + 16 * mb + ln.r + 8 * (e & 1))];
-            split(a[e], ah[e], al[e]);
-        }
+        for (int e = 0; e < 4; ++e) split(T[at(o + 8 * kk + 2 * ln.j + (e >> 1), o + 16 * mb + ln.r + 8 * (e & 1))], ah[e], al[e]);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            if (nt >= nn) continue;
-            const float2 v = *reinterpret_cast<const float2*>(T + at(o + n + 8 * nt + ln.r, o + 8 * kk + 2 * ln.j));
+        for (int nt = 0; nt < N / 8; ++nt) {
+            if (nt >= rows) continue;
+            const float2 v = *reinterpret_cast<const float2*>(T + at(o + N + 8 * nt + ln.r, o + 8 * kk + 2 * ln.j));
             uint32_t h0, l0, h1, l1;
             split(v.x, h0, l0);
             split(v.y, h1, l1);
@@ -469,16 +528,15 @@ __device__ __forceinline__ void corner(const float* T, int o, int n, int mb, flo
         }
     }
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        if (kk >= nn) continue;
+    for (int kk = 0; kk < N / 8; ++kk) {
+        if (kk >= rows) continue;
         const float a[4] = {-x[kk][0], -x[kk][2], -x[kk][1], -x[kk][3]};
         uint32_t ah[4], al[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split(a[e], ah[e], al[e]);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            if (nt >= nn || nt < kk) continue;  // Y22[n][k] is 0 for k > n
-            const float2 v = *reinterpret_cast<const float2*>(T + at(o + n + 8 * nt + ln.r, o + n + 8 * kk + 2 * ln.j));
+        for (int nt = 0; nt < 2; ++nt) {
+            const float2 v = *reinterpret_cast<const float2*>(T + at(o + N + 16 * half + 8 * nt + ln.r, o + N + 8 * kk + 2 * ln.j));
             uint32_t h0, l0, h1, l1;
             split(v.x, h0, l0);
             split(v.y, h1, l1);
@@ -488,13 +546,13 @@ __device__ __forceinline__ void corner(const float* T, int o, int n, int mb, flo
         }
     }
 }
-__device__ __forceinline__ void put_corner(float* T, int o, int n, int mb, const float (&res)[4][4], const Lane& ln) {
+template <int N>
+__device__ __forceinline__ void put_corner(float* T, int o, int mb, int half, const float (&res)[2][4], const Lane& ln) {
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        if (nt >= n / 8) continue;
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) T[at(o + n + 8 * nt + 2 * ln.j + (e & 1), o + 16 * mb + ln.r + 8 * (e >> 1))] = res[nt][e];
-    }
+        for (int e = 0; e < 4; ++e)
+            T[at(o + N + 16 * half + 8 * nt + 2 * ln.j + (e & 1), o + 16 * mb + ln.r + 8 * (e >> 1))] = res[nt][e];
 }
 // All threads; the tile is written and read between barriers of its own.
 __device__ __forceinline__ void invert(float* T, const Lane& ln) {
@@ -505,16 +563,16 @@ __device__ __forceinline__ void invert(float* T, const Lane& ln) {
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = i == c ? 1.f : 0.f;
+            float s[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < (i + 3) / 4; ++q) {
                 const float4 v = *reinterpret_cast<const float4*>(T + at(o + i, o + 4 * q));
                 const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (4 * q + e < i) s = fmaf(-a[e], y[4 * q + e], s);
+                    if (4 * q + e < i) s[e] = fmaf(-a[e], y[4 * q + e], s[e]);
             }
-            y[i] = s;
+            y[i] = (s[0] + s[1]) + (s[2] + s[3]);
         }
         __syncwarp();
         if (l < 16) {
@@ -523,16 +581,16 @@ __device__ __forceinline__ void invert(float* T, const Lane& ln) {
         }
     }
     __syncthreads();
-    float res[4][4];
+    float res[2][4];
     if (!(w & 1)) {
-        corner(T, 16 * w, 16, 0, res, ln);
+        corner<16>(T, 16 * w, 0, 0, res, ln);
         __syncwarp();
-        put_corner(T, 16 * w, 16, 0, res, ln);
+        put_corner<16>(T, 16 * w, 0, 0, res, ln);
     }
     __syncthreads();
-    if (w < 2) corner(T, 0, 32, w, res, ln);
+    corner<32>(T, 0, w & 1, w >> 1, res, ln);
     __syncthreads();
-    if (w < 2) put_corner(T, 0, 32, w, res, ln);
+    put_corner<32>(T, 0, w & 1, w >> 1, res, ln);
     __syncthreads();
 }
 
@@ -571,8 +629,11 @@ struct PrepArgs {
 template <typename E, int NK, bool BWD>
 __host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 2 + 3 + (BWD ? (NK + 1) * planes<E>() : 0)) * kPlane; }
 
+// CTAs that the shared memory of an SM holds, up to four: what the registers are to allow.
+__host__ __device__ constexpr int ctas_of(int smem) { return 226 * 1024 / (smem + 3072) < 4 ? 226 * 1024 / (smem + 3072) : 4; }
+
 template <typename E, int NK, bool BWD>
-__global__ void __launch_bounds__(kThreads) gdr_prep(const PrepArgs<E> a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gdr_prep(const PrepArgs<E> a) {
     constexpr int PI = planes<E>(), PX = state_planes<E, BWD>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
@@ -583,20 +644,22 @@ __global__ void __launch_bounds__(kThreads) gdr_prep(const PrepArgs<E> a) {
     uint8_t* dO = Q + NK * PI * kPlane;
     const uint32_t Ks = saddr(K), Ys = saddr(Y), Qs = saddr(Q), Os = saddr(dO);
     const Lane ln;
-    const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
+    const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
     const int live = min(kC, length_of(a.n, b) - c * kC);
     if (live <= 0) return;
     // the CTAs of an SM put the longest rows of a triangle on different quarters of it
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
     const long long t0 = (long long)c * kC;
+    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
         load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
         if (BWD) load_planes(Q + kb * PI * kPlane, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
     }
     commit();
-    load_scal(s, a.beta, a.g, b, h, t0, live);
+    make_scal(s, gates);
     wait<0>();
     __syncthreads();
     float acc[8][4];
@@ -751,7 +814,8 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const Lane ln;
     const int w = threadIdx.x >> 5;
-    const long long bh = blockIdx.x / (unsigned)a.nseg, b = bh / a.n.H;
+    const unsigned ubh = blockIdx.x / (unsigned)a.nseg;
+    const long long bh = ubh, b = ubh / (unsigned)a.n.H;
     const int seg = (int)(blockIdx.x % (unsigned)a.nseg), sb = blockIdx.y;
     const bool ident = MAP && sb >= a.NV;
     const int count = a.chunks ? (length_of(a.n, b) + kC - 1) / kC : a.items;
@@ -799,7 +863,7 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
         if (!MAP) {
 #pragma unroll
             for (int kb = 0; kb < NK; ++kb)
-                put_planes<PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
+                put_planes<3, PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
             if (REV && a.ends) {
 #pragma unroll
                 for (int kb = 0; kb < NK; ++kb) {

@@ -45,7 +45,7 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <typename E, int NK, int NV>
-__global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr_grad(const GradArgs<E> a) {
     constexpr bool ONE = grad_one<E, NK, NV>();
     constexpr int PI = planes<E>();
     // planes of operands that reach only dK, rounded to bf16: two where the other has one
@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
     uint8_t* W = Zt + NV * 3 * kPlane;
     const uint32_t Ks = saddr(K), Os = saddr(dO), Es0 = saddr(Et), Zs0 = saddr(Zt), Ws = saddr(W);
     const Lane ln;
-    const long long bh = blockIdx.x / (unsigned)a.n.NC, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
+    const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
+    const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
     const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         __syncthreads();
     };
     const uint32_t Xs = ONE ? Ws + 2 * kPlane : Ws;
+    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, dk - kb * kC, a.k.vec);
     if (ONE) load_q(W, 0);
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         copy_planes<3>(Xs, Xt);
     }
     commit();
-    load_scal(s, a.beta, a.g, b, h, t0, live);
+    make_scal(s, gates);
     // P transposed: rows j, columns i >= j
     float P[8][4];
     zero(P);
@@ -142,6 +144,8 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
+        Rows<E> v;
+        load_rows(v, a.v.row0(b, h, t0) + sb * kC, a.v.st, a.v.pair, rb, ln, live, dv - sb * kC);
         zero(x);
         zero(d);
         if (ONE) {
@@ -166,14 +170,12 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         mmr<3, PI, true>(d, P, Ob, ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const int row = 16 * rb + ln.r + 8 * hf;
-            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+            const float eG = s.eG[16 * rb + ln.r + 8 * hf];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
-                const int col = 8 * nt + 2 * ln.j;
-                const float2 v = row < live ? load2(pv + col, dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
-                x[nt][2 * hf] = fmaf(-s.eG[row], x[nt][2 * hf], v.x);
-                x[nt][2 * hf + 1] = fmaf(-s.eG[row], x[nt][2 * hf + 1], v.y);
+                const float2 u = v.of(nt, hf);
+                x[nt][2 * hf] = fmaf(-eG, x[nt][2 * hf], u.x);
+                x[nt][2 * hf + 1] = fmaf(-eG, x[nt][2 * hf + 1], u.y);
             }
         }
         if (ONE) __syncthreads();  // S and dS' are read
@@ -201,16 +203,12 @@ __global__ void __launch_bounds__(kThreads) gdr_grad(const GradArgs<E> a) {
         put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
         write_rows(a.dv.row0(b, h, t0) + sb * kC, a.dv.st, a.dv.pair, rb, z, ln, rows, live, dv - sb * kC);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int row = 16 * rb + ln.r + 8 * hf;
-            const E* pv = a.v.row0(b, h, t0 + row) + sb * kC;
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
-                const int col = 8 * nt + 2 * ln.j;
-                const float2 v = row < live ? load2(pv + col, dv - sb * kC - col, a.v.pair) : make_float2(0.f, 0.f);
-                sv[hf] = fmaf(z[nt][2 * hf], v.x, fmaf(z[nt][2 * hf + 1], v.y, sv[hf]));
+                const float2 u = v.of(nt, hf);
+                sv[hf] = fmaf(z[nt][2 * hf], u.x, fmaf(z[nt][2 * hf + 1], u.y, sv[hf]));
             }
-        }
         __syncthreads();
         // N transposed: rows j, columns i > j
         float N[8][4];
