@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
     const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
     const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
     const long long t0 = (long long)c * kC;
@@ -121,8 +123,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
     }
 }
 
-// ---- short sequences: a warp holds 16 columns of a head's state, 8 groups of R rows x 4 columns, and walks the
-// tokens. Bound by the state's bytes, read and written once; every load of them is in flight before the first use.
+// ---- short sequences: a CTA holds 64 columns of a head's state, a thread R rows x 4 columns of them (16 threads a row),
+// and walks the tokens. Bound by the state's bytes, read and written once: every load of them is in flight before the
+// first use, and a warp's reach over whole rows (columns of 16 a warp, without barriers, took 10 % longer).
 template <typename E>
 struct StepArgs {
     Sizes n;
@@ -131,18 +134,20 @@ struct StepArgs {
     Ten<float> beta, g;
     const float* S0;
     float* S;
-    long long tiles;  // warps
-    int cols;         // of 16 a head
+    int cols;         // of 64 a head
     bool vec;         // states in 16-byte pieces
 };
 
 template <typename E, int R>
-__global__ void __launch_bounds__(kThreads) gdr_step(const StepArgs<E> a) {
-    const long long id = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (id >= a.tiles) return;
-    const int l = threadIdx.x & 31, c0 = 16 * (int)(id % a.cols) + 4 * (l & 3), rg = l >> 2;
-    const long long bh = id / a.cols, b = bh / a.n.H, h = bh % a.n.H, hk = h / a.n.group;
-    const int live = length_of(a.n, b), dk = a.n.dk, dv = a.n.dv;
+__global__ void __launch_bounds__(kThreads, R == 8 ? 6 : 4) gdr_step(const StepArgs<E> a) {
+    __shared__ float part[2][kThreads / 32][9 * 16];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31, rg = threadIdx.x >> 4, c = l & 15;
+    const unsigned ubh = blockIdx.x / (unsigned)a.cols, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
+    const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
+    const int c0 = 64 * (int)(blockIdx.x % (unsigned)a.cols) + 4 * c;
+    const int dk = a.n.dk, dv = a.n.dv;
     float S[R][4];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) gdr_step(const StepArgs<E> a) {
                 if (c0 + e < dv) S[i][e] = p[e];
         }
     }
+    const int live = length_of(a.n, b);
     for (int t = 0; t < a.n.T; ++t) {
         E* po = a.out.row0(b, h, t) + c0;
         if (t >= live) {
@@ -168,36 +174,48 @@ __global__ void __launch_bounds__(kThreads) gdr_step(const StepArgs<E> a) {
         const E* pk = a.k.row0(b, hk, t);
         const E* pq = a.q.row0(b, hk, t);
         const E* pv = a.v.row0(b, h, t) + c0;
-        const float2 v0 = load2(pv, dv - c0, a.v.pair), v1 = load2(pv + 2, dv - c0 - 2, a.v.pair);
-        const float v[4] = {v0.x, v0.y, v1.x, v1.y};
-        const float beta = *a.beta.row0(b, h, t), dec = expf(*a.g.row0(b, h, t));
-        float k[R], x[9];  // S^T k, S^T q, k.q
-#pragma unroll
-        for (int e = 0; e < 9; ++e) x[e] = 0.f;
+        float k[R], q[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int row = 8 * i + rg;
             k[i] = row < dk ? to_f(pk[row]) : 0.f;
-            const float q = row < dk ? to_f(pq[row]) : 0.f;
+            q[i] = row < dk ? to_f(pq[row]) : 0.f;
+        }
+        const float2 v0 = load2(pv, dv - c0, a.v.pair), v1 = load2(pv + 2, dv - c0 - 2, a.v.pair);
+        const float v[4] = {v0.x, v0.y, v1.x, v1.y};
+        const float beta = *a.beta.row0(b, h, t), dec = expf(*a.g.row0(b, h, t));
+        float x[9];  // S^T k, S^T q, k.q
+#pragma unroll
+        for (int e = 0; e < 9; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 S[i][e] *= dec;
                 x[e] = fmaf(S[i][e], k[i], x[e]);
-                x[4 + e] = fmaf(S[i][e], q, x[4 + e]);
+                x[4 + e] = fmaf(S[i][e], q[i], x[4 + e]);
             }
-            x[8] = fmaf(k[i], q, x[8]);
+            x[8] = fmaf(k[i], q[i], x[8]);
         }
+        float* mine = part[t & 1][w];  // the other half is still read for the token before
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1)
+        for (int e = 0; e < 9; ++e) {
+            x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
+            if (l < 16) mine[16 * e + c] = x[e];
+        }
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 9; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], d);
-        float u[4], o[4];
+        for (int e = 0; e < 9; ++e) {
+            const float* p = part[t & 1][0] + 16 * e + c;
+            x[e] = (p[0] + p[9 * 16]) + (p[18 * 16] + p[27 * 16]);
+        }
+        float o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            u[e] = beta * (v[e] - x[e]);
-            o[e] = a.n.scale * fmaf(x[8], u[e], x[4 + e]);
+            const float u = beta * (v[e] - x[e]);
+            o[e] = a.n.scale * fmaf(x[8], u, x[4 + e]);
 #pragma unroll
-            for (int i = 0; i < R; ++i) S[i][e] = fmaf(k[i], u[e], S[i][e]);
+            for (int i = 0; i < R; ++i) S[i][e] = fmaf(k[i], u, S[i][e]);
         }
         if (rg == 0) store2(po, o[0], o[1], dv - c0, a.out.pair), store2(po + 2, o[2], o[3], dv - c0 - 2, a.out.pair);
     }
@@ -231,13 +249,10 @@ int launch_step(const GdrArgs& a, cudaStream_t st) {
     p.g = ten<float>(a.g, 1);
     p.S0 = a.S0;
     p.S = a.S_final;
-    p.cols = (a.n.dv + 15) / 16;
-    p.tiles = p.n.BH * p.cols;
+    p.cols = (a.n.dv + 63) / 64;
     p.vec = a.n.dv % 4 == 0 && al16(a.S0) && al16(a.S_final);
-    const unsigned grid = (unsigned)((p.tiles + kThreads / 32 - 1) / (kThreads / 32));
-    if (a.n.dk <= 64) gdr_step<E, 8><<<grid, kThreads, 0, st>>>(p);
-    else gdr_step<E, 16><<<grid, kThreads, 0, st>>>(p);
-    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+    const unsigned grid = (unsigned)(p.n.BH * p.cols);
+    return a.n.dk <= 64 ? launch_ahead<gdr_step<E, 8>>(grid, kThreads, 0, st, p) : launch_ahead<gdr_step<E, 16>>(grid, kThreads, 0, st, p);
 }
 
 template <typename E, int NK>
@@ -263,13 +278,10 @@ int launch_chunks(const GdrArgs& a, const Layout& l, cudaStream_t st) {
     o.g = p.g;
     o.X = p.X;
     o.S = ws + l.S;
-    constexpr int prep = prep_smem<E, NK, false>(), out = out_smem<E, NK>();
-    if (!want_smem(gdr_prep<E, NK, false>, prep) || !want_smem(gdr_out<E, NK>, out)) return FALCON_ERR_CUDA;
     const unsigned grid = (unsigned)(n.BH * l.NC);
-    gdr_prep<E, NK, false><<<grid, kThreads, prep, st>>>(p);
-    if (!run_scan<NK, false, state_planes<E, false>()>(n, l, ws, a.S0, a.S_final, false, st)) return FALCON_ERR_CUDA;
-    gdr_out<E, NK><<<grid, kThreads, out, st>>>(o);
-    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+    int r = launch_ahead<gdr_prep<E, NK, false>>(grid, kThreads, prep_smem<E, NK, false>(), st, p);
+    r |= run_scan<NK, state_planes<E, false>()>(n, l, ws, a.S0, a.S_final, st);
+    return r | launch_ahead<gdr_out<E, NK>>(grid, kThreads, out_smem<E, NK>(), st, o);
 }
 
 template <typename E>

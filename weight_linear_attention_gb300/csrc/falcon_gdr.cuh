@@ -22,6 +22,8 @@
 #include <stdint.h>
 
 #include "falcon_gdr.h"
+#include "falcon_launch.h"
+#include "sm103_ptx.cuh"
 
 namespace falcon {
 namespace gdr {
@@ -647,6 +649,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
     const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
     const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
+    // what the grids before this one wrote may be read from here on; the scan behind it is not let in early, or its few
+    // CTAs share the first SMs that are free (144 us a forward call against 125)
+    ptx::pdl_wait();
     const int live = min(kC, length_of(a.n, b) - c * kC);
     if (live <= 0) return;
     // the CTAs of an SM put the longest rows of a triangle on different quarters of it
@@ -802,16 +807,15 @@ struct ScanArgs {
     int end_tile;          // leave the state behind the last chunk behind S's others, too
     uint8_t* mapM;         // MAP: [BH][nseg][NK][NK]
     float* mapA;           // MAP: [BH][nseg][NV][NK]
-    const uint8_t* fwd;    // REV: the states [BH][NC + 1][NV][NK] in three planes, for
-    float* ends;           // [BH][NC][NV][4]: parts of <state behind the item, its adjoint>; or null
 };
 
-constexpr int kScanStages = 2;
-__host__ __device__ constexpr int scan_smem(int NK) { return kScanStages * NK * NK * 3 * kPlane; }
+// Items of M on their way: as many as the shared memory of an SM has room for.
+__host__ __device__ constexpr int scan_stages(int NK) { return NK == 1 ? 3 : 2; }
+__host__ __device__ constexpr int scan_smem(int NK) { return scan_stages(NK) * NK * NK * 3 * kPlane; }
 
 template <int NK, bool REV, bool MAP, int PS>
-__global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
-    extern __shared__ __align__(128) uint8_t smem[];
+__device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
+    constexpr int STAGES = scan_stages(NK);
     const Lane ln;
     const int w = threadIdx.x >> 5;
     const unsigned ubh = blockIdx.x / (unsigned)a.nseg;
@@ -846,37 +850,26 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
     }
     auto item = [&](int i) { return REV ? i1 - 1 - i : i0 + i; };
     auto fetch = [&](int i) {
-        if (i < n) copy_planes<3 * NK * NK>(saddr(smem) + (i % kScanStages) * (3 * NK * NK * kPlane), a.M + (bh * a.items + item(i)) * (3 * NK * NK * kPlane));
+        if (i < n) copy_planes<3 * NK * NK>(saddr(smem) + (i % STAGES) * (3 * NK * NK * kPlane), a.M + (bh * a.items + item(i)) * (3 * NK * NK * kPlane));
         commit();
     };
-    for (int i = 0; i < kScanStages - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
     for (int i = 0; i < n; ++i) {
-        float add[NK][8][4], sum = 0.f;
+        float add[NK][8][4];
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             if (ident) zero(add[kb]);
             else get(a.A + (((bh * a.items + item(i)) * a.NV + sb) * NK + kb) * kTile, w, add[kb], ln);
         }
-        wait<kScanStages - 2>();
+        wait<STAGES - 2>();
         __syncthreads();  // item i has arrived for every warp, and item i - 1 is read by every warp
-        fetch(i + kScanStages - 1);
+        fetch(i + STAGES - 1);
         if (!MAP) {
 #pragma unroll
             for (int kb = 0; kb < NK; ++kb)
                 put_planes<3, PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
-            if (REV && a.ends) {
-#pragma unroll
-                for (int kb = 0; kb < NK; ++kb) {
-                    float t[8][4];
-                    get_planes<3>(a.fwd + (((bh * (a.n.NC + 1) + item(i) + 1) * a.NV + sb) * NK + kb) * (3 * kPlane), w, t, ln);
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum = fmaf(t[nt][e], acc[kb][nt][e], sum);
-                }
-            }
         }
-        const uint32_t M = saddr(smem) + (i % kScanStages) * (3 * NK * NK * kPlane);
+        const uint32_t M = saddr(smem) + (i % STAGES) * (3 * NK * NK * kPlane);
         float nw[NK][8][4];
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
@@ -886,11 +879,6 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
                 if (!REV) mmr<3, 3, false>(nw[kb], acc[kc], M + (kb * NK + kc) * (3 * kPlane), ln);
                 else mmr<3, 3, true>(nw[kb], acc[kc], M + (kc * NK + kb) * (3 * kPlane), ln);
             }
-        }
-        if (!MAP && REV && a.ends) {
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if ((threadIdx.x & 31) == 0) a.ends[((bh * a.n.NC + item(i)) * a.NV + sb) * 4 + w] = sum;
         }
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb)
@@ -939,6 +927,24 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
     }
 }
 
+// The states' scan.
+template <int NK, bool MAP, int PS>
+__global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    ptx::pdl_wait();
+    if (!MAP && a.chunks) ptx::pdl_launch_dependents();
+    scan<NK, false, MAP, PS>(a, smem);
+}
+// The states' and the adjoints', side by side: neither needs the other.
+template <int NK, bool MAP>
+__global__ void __launch_bounds__(kThreads) gdr_scans(const ScanArgs a, const ScanArgs r) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    ptx::pdl_wait();
+    if (!MAP && a.chunks) ptx::pdl_launch_dependents();
+    if (blockIdx.z == 0) scan<NK, false, MAP, 3>(a, smem);
+    else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP, 3>(r, smem);
+}
+
 // The scan's segments. In units of 1000 cycles: a step along the chain takes 1.7 alone, and an SM's tensor cores take
 // 1.55 for each CTA's step. Cut into segments, the segments' maps come first (as many steps, for dk more rows), then a
 // scan over them, then the segments' own states. 8: what two more launches cost.
@@ -961,7 +967,7 @@ inline Cut cut_of(long long BH, int NC, int NK, int NV) {
 struct Layout {
     int NK, NV, NC;
     Cut cut;
-    long long X, M, A, S, P, Z, G, dA, dS, dZ, dG, ends, dq, dk, total;
+    long long X, M, A, S, P, Z, G, dA, dS, dZ, dG, dq, dk, total;
 };
 inline Layout layout_of(const GdrSizes& n, bool bwd) {
     Layout l = {};
@@ -990,7 +996,6 @@ inline Layout layout_of(const GdrSizes& n, bool bwd) {
         l.dS = take(BH * l.NC * st * 3 * kPlane);
         l.dZ = take(BH * seg * st * tile);
         l.dG = take(BH * seg * st * 3 * kPlane);
-        l.ends = take(BH * l.NC * l.NV * 16);
         const long long shared = n.H != n.Hk ? BH * n.T * n.dk * 4 : 0;
         l.dq = take(shared);
         l.dk = take(shared);
@@ -999,60 +1004,71 @@ inline Layout layout_of(const GdrSizes& n, bool bwd) {
     return l;
 }
 
-template <typename K>
-inline bool want_smem(K* kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
 inline Sizes sizes_of(const GdrArgs& a, const Layout& l) {
     return Sizes{a.n.B * a.n.H, (int)a.n.H, (int)(a.n.H / a.n.Hk), a.n.T, a.n.dk, a.n.dv, l.NC, a.lengths, a.scale};
 }
 
-// The states' scan (REV: the adjoints'), in one pass or by segments. The segments' products of M are the forward
-// pass's: the backward one reads them transposed.
-template <int NK, bool REV, int PS>
-bool run_scan(const Sizes& n, const Layout& l, uint8_t* ws, const float* init, float* last, bool end_tile, cudaStream_t s) {
-    ScanArgs c = {};
+// Arguments of the scan's three launches: the segments' maps, the scan over them, the states. Uncut, the last alone.
+struct ScanSteps {
+    ScanArgs map, over, own;
+};
+inline ScanSteps scan_steps(const Sizes& n, const Layout& l, uint8_t* ws, bool rev, const float* init, float* last) {
+    ScanSteps r = {};
+    ScanArgs& c = r.own;
     c.n = n;
     c.NV = l.NV;
     c.M = ws + l.M;
-    c.A = reinterpret_cast<const float*>(ws + (REV ? l.dA : l.A));
-    c.S = ws + (REV ? l.dS : l.S);
-    c.stride = l.NC + (REV ? 0 : 1);
+    c.A = reinterpret_cast<const float*>(ws + (rev ? l.dA : l.A));
+    c.S = ws + (rev ? l.dS : l.S);
+    c.stride = l.NC + (rev ? 0 : 1);
     c.items = l.NC;
     c.chunks = 1;
     c.L = l.cut.L;
     c.nseg = l.cut.nseg;
-    const int smem = scan_smem(NK);
-    if (!want_smem(gdr_scan<NK, REV, false, PS>, smem)) return false;
-    const unsigned x = (unsigned)(n.BH * l.cut.nseg);
     if (l.cut.nseg > 1) {
-        if (!want_smem(gdr_scan<NK, REV, true, 3>, smem) || !want_smem(gdr_scan<NK, REV, false, 3>, smem)) return false;
-        ScanArgs m = c;
-        m.mapM = ws + l.P;
-        m.mapA = reinterpret_cast<float*>(ws + (REV ? l.dZ : l.Z));
-        gdr_scan<NK, REV, true, 3><<<dim3(x, l.NV + (REV ? 0 : NK)), kThreads, smem, s>>>(m);
-        ScanArgs t = c;
+        r.map = r.over = c;
+        r.map.mapM = ws + l.P;
+        r.map.mapA = reinterpret_cast<float*>(ws + (rev ? l.dZ : l.Z));
+        ScanArgs& t = r.over;
         t.M = ws + l.P;
-        t.A = m.mapA;
-        t.S = ws + (REV ? l.dG : l.G);
+        t.A = r.map.mapA;
+        t.S = ws + (rev ? l.dG : l.G);
         t.stride = t.items = t.L = l.cut.nseg;
         t.chunks = 0;
         t.nseg = 1;
         t.init = init;
         t.last = last;
-        gdr_scan<NK, REV, false, 3><<<dim3((unsigned)n.BH, l.NV), kThreads, smem, s>>>(t);
         c.init_tiles = t.S;
     } else {
         c.init = init;
         c.last = last;
     }
-    c.end_tile = end_tile;
-    if (REV) {
-        c.fwd = ws + l.S;
-        c.ends = reinterpret_cast<float*>(ws + l.ends);
+    return r;
+}
+// The states' scan of a forward call.
+template <int NK, int PS>
+int run_scan(const Sizes& n, const Layout& l, uint8_t* ws, const float* init, float* last, cudaStream_t s) {
+    const ScanSteps f = scan_steps(n, l, ws, false, init, last);
+    const unsigned x = (unsigned)(n.BH * l.cut.nseg);
+    int st = 0;
+    if (l.cut.nseg > 1) {
+        st |= launch_ahead<gdr_scan<NK, true, 3>>(dim3(x, l.NV + NK), kThreads, scan_smem(NK), s, f.map);
+        st |= launch_ahead<gdr_scan<NK, false, 3>>(dim3((unsigned)n.BH, l.NV), kThreads, scan_smem(NK), s, f.over);
     }
-    gdr_scan<NK, REV, false, PS><<<dim3(x, l.NV), kThreads, smem, s>>>(c);
-    return true;
+    return st | launch_ahead<gdr_scan<NK, false, PS>>(dim3(x, l.NV), kThreads, scan_smem(NK), s, f.own);
+}
+// Both of a backward call's. The segments' products of M are the forward's: the other reads them transposed.
+template <int NK>
+int run_scans(const Sizes& n, const Layout& l, uint8_t* ws, const float* S0, const float* dS_final, float* dS0, cudaStream_t s) {
+    ScanSteps f = scan_steps(n, l, ws, false, S0, nullptr), r = scan_steps(n, l, ws, true, dS_final, dS0);
+    f.own.end_tile = 1;  // the state behind the last chunk, too
+    const unsigned x = (unsigned)(n.BH * l.cut.nseg);
+    int st = 0;
+    if (l.cut.nseg > 1) {
+        st |= launch_ahead<gdr_scans<NK, true>>(dim3(x, l.NV + NK, 2), kThreads, scan_smem(NK), s, f.map, r.map);
+        st |= launch_ahead<gdr_scans<NK, false>>(dim3((unsigned)n.BH, l.NV, 2), kThreads, scan_smem(NK), s, f.over, r.over);
+    }
+    return st | launch_ahead<gdr_scans<NK, false>>(dim3(x, l.NV, 2), kThreads, scan_smem(NK), s, f.own, r.own);
 }
 
 }  // namespace gdr

@@ -7,8 +7,7 @@
 //   dK = dP^T Q + H K - diag(e^G) Z S^T + diag(w beta) E dS'^T,
 //   dbeta_j = E_j.(dU - N^T Z)_j.
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
-// writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides (the adjoints' scan sums
-// it); dg is the sum of dG
+// writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
 // from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
 // gdr_grad takes the gradients, all chunks at once.
 
@@ -28,7 +27,6 @@ struct GradArgs {
     Ten<E> dq, dk, dv;
     float *pq, *pk;  // [B,H,T,dk] instead of dq and dk where heads share theirs, or null
     const uint8_t *X, *S, *dS;
-    const float* ends;
 };
 
 // K, dO, E, Z and what comes and goes. With one tile of S and dS' (and bf16) all of it is on its way early: S and dS'
@@ -52,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     constexpr int PL = sizeof(E) == 2 ? 2 : 3, P1 = sizeof(E) == 2 ? 1 : 3;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
-    __shared__ float own[kC], dbe[kC];
+    __shared__ float own[kC], dbe[kC], part[kThreads / 32];
     uint8_t* K = smem;
     uint8_t* dO = K + NK * PI * kPlane;
     uint8_t* Et = dO + NV * PI * kPlane;
@@ -63,6 +61,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
     const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const int rows = min(kC, a.n.T - c * kC), live = min(kC, length_of(a.n, b) - c * kC);
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
     const int dk = a.n.dk, dv = a.n.dv;
@@ -99,6 +99,27 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         commit();
         wait<0>();
         __syncthreads();
+    };
+    // <dS', S'>: a tile of dS' in shared memory against the state's behind the chunk
+    float ends = 0.f;
+    auto meet = [&](const uint8_t* t, const uint8_t* S1) {
+#pragma unroll
+        for (int i = 0; i < kPlane / 16 / kThreads; ++i) {
+            float x[8] = {}, y[8] = {};
+#pragma unroll
+            for (int m = 2; m >= 0; --m) {
+                const int o = m * kPlane + 16 * (threadIdx.x + i * kThreads);
+                const uint4 u = *reinterpret_cast<const uint4*>(t + o), v = *reinterpret_cast<const uint4*>(S1 + o);
+                const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] += __uint_as_float(p[e] << 16), x[2 * e + 1] += __uint_as_float(p[e] & 0xffff0000u);
+                    y[2 * e] += __uint_as_float(q[e] << 16), y[2 * e + 1] += __uint_as_float(q[e] & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ends = fmaf(x[e], y[e], ends);
+        }
     };
     const uint32_t Xs = ONE ? Ws + 2 * kPlane : Ws;
     const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
@@ -154,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             mm<PI, 3, false, false>(x, Ks, rb, Es, ln);
             mm<PI, 3, false, true>(q1, Ob, rb, Es, ln);
             mm<PI, 3, false, false>(d, Ks, rb, Zs, ln);
+            meet(Zt, St + st);
         } else {
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
@@ -161,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 mm<PI, 3, false, false>(x, Ks + kb * PI * kPlane, rb, Ws, ln);
                 bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
                 mm<PI, 3, false, false>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
+                meet(W, St + st + (sb * NK + kb) * (3 * kPlane));
             }
         }
 #pragma unroll
@@ -313,19 +336,19 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]);
         if (ln.j == 0) own[row] = o, dbe[row] = e;
     }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) ends += __shfl_xor_sync(0xffffffffu, ends, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ends;
     __syncthreads();
     if (threadIdx.x >= 32) return;
     const int l = threadIdx.x;
-    double sum = (double)own[2 * l] + own[2 * l + 1];
+    Two sum = add(Two{own[2 * l], 0.f}, Two{own[2 * l + 1], 0.f});  // pairs of floats: the sums may cancel
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const double o = __shfl_down_sync(0xffffffffu, sum, m);
-        if (l + m < 32) sum += o;
+        const Two o = {__shfl_down_sync(0xffffffffu, sum.hi, m), __shfl_down_sync(0xffffffffu, sum.lo, m)};
+        if (l + m < 32) sum = add(sum, o);
     }
-    double all = 0.;
-    const float* ends = a.ends + (bh * a.n.NC + c) * (NV * 4);
-#pragma unroll
-    for (int i = 0; i < NV * 4; ++i) all += ends[i];
+    sum = add(sum, Two{(part[0] + part[1]) + (part[2] + part[3]), 0.f});
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         *a.dbeta.row0(b, h, t0 + t) = in ? dbe[t] : 0.f;
         // a decay of 0 keeps nothing: its gradient is 0, not what rounding leaves of the sum
         const bool kept = in && !(expf(*a.g.row0(b, h, t0 + t)) == 0.f);
-        *a.dg.row0(b, h, t0 + t) = kept ? (float)((e ? sum - own[2 * l] : sum) + all) : 0.f;
+        *a.dg.row0(b, h, t0 + t) = kept ? (e ? add(sum, Two{-own[2 * l], 0.f}) : sum).hi : 0.f;
     }
 }
 
@@ -348,6 +371,8 @@ struct SumArgs {
 };
 template <typename E>
 __global__ void __launch_bounds__(256) gdr_sum(const SumArgs<E> a, const SumArgs<E> a2) {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const SumArgs<E>& p = blockIdx.y ? a2 : a;
     const int l = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -384,44 +409,33 @@ int launch_bwd(const GdrArgs& a, cudaStream_t st) {
     p.M = ws + l.M;
     p.A = reinterpret_cast<float*>(ws + l.A);
     p.dA = reinterpret_cast<float*>(ws + l.dA);
-    constexpr int prep = prep_smem<E, NK, true>();
-    if (!want_smem(gdr_prep<E, NK, true>, prep)) return FALCON_ERR_CUDA;
-    if (grid) {
-        gdr_prep<E, NK, true><<<grid, kThreads, prep, st>>>(p);
-        if (!run_scan<NK, false, 3>(n, l, ws, a.S0, nullptr, true, st)) return FALCON_ERR_CUDA;
+    int r = 0;
+    if (grid) r |= launch_ahead<gdr_prep<E, NK, true>>(grid, kThreads, prep_smem<E, NK, true>(), st, p);
+    r |= run_scans<NK>(n, l, ws, a.S0, a.dS_final, a.dS0, st);
+    if (!grid) return r;
+    GradArgs<E> g = {};
+    g.n = n;
+    g.q = p.q, g.k = p.k, g.v = p.v, g.dout = p.dout, g.beta = p.beta, g.g = p.g;
+    g.dbeta = ten<float>(a.dbeta, 1);
+    g.dg = ten<float>(a.dg, 1);
+    g.dq = ten<E>(a.dq, a.n.dk);
+    g.dk = ten<E>(a.dk, a.n.dk);
+    g.dv = ten<E>(a.dv, a.n.dv);
+    const bool shared = n.group > 1;
+    g.pq = shared ? reinterpret_cast<float*>(ws + l.dq) : nullptr;
+    g.pk = shared ? reinterpret_cast<float*>(ws + l.dk) : nullptr;
+    g.X = p.X;
+    g.S = ws + l.S;
+    g.dS = ws + l.dS;
+    r |= l.NV == 1 ? launch_ahead<gdr_grad<E, NK, 1>>(grid, kThreads, grad_smem<E, NK, 1>(), st, g)
+                   : launch_ahead<gdr_grad<E, NK, 2>>(grid, kThreads, grad_smem<E, NK, 2>(), st, g);
+    if (shared) {
+        SumArgs<E> q = {g.pq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
+        k.part = g.pk;
+        k.to = g.dk;
+        r |= launch_ahead<gdr_sum<E>>(dim3((unsigned)((q.count + 7) / 8), 2), 256, 0, st, q, k);
     }
-    if (!run_scan<NK, true, 3>(n, l, ws, a.dS_final, a.dS0, false, st)) return FALCON_ERR_CUDA;
-    if (grid) {
-        GradArgs<E> g = {};
-        g.n = n;
-        g.q = p.q, g.k = p.k, g.v = p.v, g.dout = p.dout, g.beta = p.beta, g.g = p.g;
-        g.dbeta = ten<float>(a.dbeta, 1);
-        g.dg = ten<float>(a.dg, 1);
-        g.dq = ten<E>(a.dq, a.n.dk);
-        g.dk = ten<E>(a.dk, a.n.dk);
-        g.dv = ten<E>(a.dv, a.n.dv);
-        const bool shared = n.group > 1;
-        g.pq = shared ? reinterpret_cast<float*>(ws + l.dq) : nullptr;
-        g.pk = shared ? reinterpret_cast<float*>(ws + l.dk) : nullptr;
-        g.X = p.X;
-        g.S = ws + l.S;
-        g.dS = ws + l.dS;
-        g.ends = reinterpret_cast<const float*>(ws + l.ends);
-        if (l.NV == 1) {
-            if (!want_smem(gdr_grad<E, NK, 1>, grad_smem<E, NK, 1>())) return FALCON_ERR_CUDA;
-            gdr_grad<E, NK, 1><<<grid, kThreads, grad_smem<E, NK, 1>(), st>>>(g);
-        } else {
-            if (!want_smem(gdr_grad<E, NK, 2>, grad_smem<E, NK, 2>())) return FALCON_ERR_CUDA;
-            gdr_grad<E, NK, 2><<<grid, kThreads, grad_smem<E, NK, 2>(), st>>>(g);
-        }
-        if (shared) {
-            SumArgs<E> q = {g.pq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
-            k.part = g.pk;
-            k.to = g.dk;
-            gdr_sum<E><<<dim3((unsigned)((q.count + 7) / 8), 2), 256, 0, st>>>(q, k);
-        }
-    }
-    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+    return r;
 }
 
 // One translation unit for each, to be compiled side by side.

@@ -3,9 +3,9 @@
 // with elements (l + LPR k) VW .. + VW - 1 for k < NCH.
 #pragma once
 
-#include <atomic>
 #include <type_traits>
 
+#include "falcon_launch.h"
 #include "falcon_seq.cuh"
 #include "falcon_seq.h"
 #include "sm103_ptx.cuh"
@@ -341,39 +341,12 @@ struct Rows {
 
 constexpr int kSms = 152;
 
-constexpr int kMaxDevices = 64;
 constexpr int kSmem = 220 * 1024;  // of an SM, for the CTAs that it is given
 
 // The rows a ring has: three (more gain nothing: 60.5 us either way for [16,16,4096,64] bf16 forward), or two where
 // that is too much for the shared memory of `ctas` CTAs with `other` bytes besides.
 constexpr int depth(int row, int ctas, int other) {
     return ctas * (3 * row + other) <= kSmem ? 3 : ctas * (2 * row + other) <= kSmem ? 2 : 0;
-}
-
-// Launches kernel FN with programmatic stream serialisation: the launch overlaps the end of the kernel before it, so
-// it waits (pdl_wait) before it reads or writes.
-template <auto FN, typename... Args>
-inline int launch_ahead(dim3 grid, int threads, int bytes, cudaStream_t s, Args... args) {
-    if (bytes > 0) {
-        static std::atomic<bool> ready[kMaxDevices];  // the kernel may have `bytes` of shared memory there
-        int dev;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 4;
-        if (!ready[dev].load(std::memory_order_acquire)) {
-            if (cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return 4;
-            ready[dev].store(true, std::memory_order_release);
-        }
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, FN, args...) == cudaSuccess ? 0 : 4;
 }
 
 }  // namespace gn

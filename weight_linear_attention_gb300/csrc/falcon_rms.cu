@@ -8,8 +8,10 @@
 #include <cuda_fp8.h>
 
 #include "falcon.h"
+#include "falcon_launch.h"
 #include "falcon_rms.h"
 #include "falcon_seq.cuh"
+#include "sm103_ptx.cuh"
 
 namespace falcon {
 namespace rms {
@@ -20,10 +22,12 @@ using namespace seq;
 constexpr int kWarps = 4;       // of a CTA whose warps have a token each
 constexpr int kMost = 512;      // threads of a CTA that has one token
 constexpr int kSms = 152;
+constexpr int kSums = 4096;     // bytes: the sums of a token's channels in one warp, 1024 at most
 
 struct Args {
     RmsArgs a;
     long long rows;
+    bool weight16;  // the weights start on 16 bytes
 };
 
 // The place of a token, and whether it lies inside its sequence.
@@ -108,6 +112,8 @@ __device__ __forceinline__ void store8(uint8_t* p, const float* v) {
 template <typename E, int W, int N, bool MULTI, bool EIGHT>
 __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Args g) {
     __shared__ float slots[2][2][32];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const RmsArgs& a = g.a;
     const int step = MULTI ? blockDim.x : 32, first = MULTI ? threadIdx.x : threadIdx.x & 31;
     const int count = a.d / W;
@@ -194,63 +200,72 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Arg
 }
 
 // dweight's sums: a lane adds up its own channels over the CTA's tokens, then the CTA's warps in their order, and
-// rms_sum the CTAs in theirs.
+// rms_sum the CTAs in theirs. What a lane holds (32 channels at most where a warp has a token) leaves room for 16 warps an
+// SM, whose loads cover one another: fetching a token ahead takes the registers of half of them.
 template <typename E, int W, int N, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_bwd(const Args g) {
+__global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps, MULTI ? 1 : 4) rms_bwd(const Args g) {
     extern __shared__ __align__(16) float sums[];
     __shared__ float slots[2][2 * 32];
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
     const RmsArgs& a = g.a;
     const int step = MULTI ? blockDim.x : 32, first = MULTI ? threadIdx.x : threadIdx.x & 31;
     const int count = a.d / W;
     const long long stride = MULTI ? gridDim.x : (long long)gridDim.x * kWarps;
-    long long row = MULTI ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    float wt[N * W], acc[N * W];
+    float acc[N * W];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const int c = (first + i * step) * W + e;
-            wt[i * W + e] = a.weight && c < a.d ? a.weight[c] : 1.f;
-            acc[i * W + e] = 0.f;
-        }
+    for (int i = 0; i < N * W; ++i) acc[i] = 0.f;
     const float inv_d = 1.f / a.d;
-    Line<E, W, N> x, dy, dh;
-    Row at = {};
-    auto fetch = [&] {
-        if (row >= g.rows) return;
-        at = row_of(a, row);
+    // the weights of vector i, from the first-level cache
+    auto weights = [&](int i, float* w) {
+        const int c = (first + i * step) * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = 1.f;
+        if (!a.weight || c >= a.d) return;
+        if (W % 4 == 0 && g.weight16) {
+#pragma unroll
+            for (int e = 0; e < W / 4; ++e) {
+                const float4 v = *reinterpret_cast<const float4*>(a.weight + c + 4 * e);
+                w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) w[e] = a.weight[c + e];
+        }
+    };
+    int turn = 0;
+    for (long long row = MULTI ? blockIdx.x : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); row < g.rows; row += stride, turn ^= 1) {
+        const Row at = row_of(a, row);
+        Line<E, W, N> x, dy, dh;
         x.fetch(a.x.p, offset(a.x, at), first, step, count, at.live);
         dy.fetch(a.dy.p, offset(a.dy, at), first, step, count, at.live);
         if (a.dh.p) dh.fetch(a.dh.p, offset(a.dh, at), first, step, count, at.live);
-    };
-    fetch();
-    for (int turn = 0; row < g.rows; turn ^= 1) {
-        const Line<E, W, N> cx = x, cy = dy, ch = dh;
-        const Row now = at;
-        row += stride;
-        fetch();
         float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+            float w[W];
+            weights(i, w);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float h = elem(cx.v[i], e), p = elem(cy.v[i], e) * wt[i * W + e];
+                const float h = elem(x.v[i], e), p = elem(dy.v[i], e) * w[e];
                 s[0] = fmaf(h, h, s[0]);
                 s[1] = fmaf(p, h, s[1]);
             }
+        }
         reduce<MULTI, false>(s, slots[turn]);
         const float rstd = 1.f / sqrtf(fmaf(s[0], inv_d, a.eps)), k = rstd * rstd * (s[1] * inv_d);
-        const long long o = offset(a.dx, now);
+        const long long o = offset(a.dx, at);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float v[W];
+            float v[W], w[W];
+            weights(i, w);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float h = elem(cx.v[i], e), y = elem(cy.v[i], e);
-                if (now.live) acc[i * W + e] = fmaf(y, h * rstd, acc[i * W + e]);
-                v[e] = rstd * fmaf(-h, k, y * wt[i * W + e]);
-                if (a.dh.p) v[e] += elem(ch.v[i], e);
-                if (!now.live) v[e] = 0.f;
+                const float h = elem(x.v[i], e), y = elem(dy.v[i], e);
+                if (at.live) acc[i * W + e] = fmaf(y, h * rstd, acc[i * W + e]);
+                v[e] = rstd * fmaf(-h, k, y * w[e]);
+                if (a.dh.p) v[e] += elem(dh.v[i], e);
+                if (!at.live) v[e] = 0.f;
             }
             if (first + i * step >= count) continue;
             Pack<E, W> u;
@@ -285,19 +300,23 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_bwd(const Arg
     }
 }
 
-__global__ void __launch_bounds__(256) rms_sum(const float* part, int splits, int d, float* out) {
-    __shared__ float s[8][33];
+// A CTA has 32 channels, its warps every 32nd of the sums.
+__global__ void __launch_bounds__(1024) rms_sum(const float* part, int splits, int d, float* out) {
+    __shared__ float s[32][33];
+    ptx::pdl_wait();  // launched while the CTAs whose sums it adds still run
+    ptx::pdl_launch_dependents();
     const int l = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
     float v = 0.f;
-    if (c < d)
-        for (int i = w; i < splits; i += 8) v += part[(long long)i * d + c];
-    s[w][l] = v;
-    __syncthreads();
-    if (w == 0 && c < d) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][l];
-        out[c] = v;
+    if (c < d) {
+#pragma unroll 8
+        for (int i = w; i < splits; i += 32) v += part[(long long)i * d + c];
     }
+    s[l][w] = v;
+    __syncthreads();
+    v = s[w][l];  // warp w: channel w
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (l == 0 && blockIdx.x * 32 + w < d) out[blockIdx.x * 32 + w] = v;
 }
 
 // Lanes of a token. A vector is 16 bytes where every access can be one, else an element, and a lane holds N of them: as
@@ -308,8 +327,9 @@ bool vec_ok(const RowView& v, int bytes, int es) {
 }
 int lanes_of(int d, int per) { return ((d + per - 1) / per + 31) / 32 * 32; }
 
-template <typename E, int W, int N>
-void fwd(const Args& g, cudaStream_t s) {
+// ONE: such tokens may fit a warp.
+template <typename E, int W, int N, bool ONE = true>
+int fwd(const Args& g, cudaStream_t s) {
     const int lanes = lanes_of(g.a.d, W * N);
     const bool multi = lanes > 32;
     const int threads = multi ? lanes : 32 * kWarps;
@@ -317,27 +337,31 @@ void fwd(const Args& g, cudaStream_t s) {
     const long long most = (long long)kSms * (512 / threads);
     const long long want = multi ? g.rows : (g.rows + kWarps - 1) / kWarps;
     const unsigned grid = (unsigned)(want < most ? want : most);
-    if (g.a.eight) {
-        if (multi) rms_fwd<E, W, N, true, true><<<grid, threads, 0, s>>>(g);
-        else rms_fwd<E, W, N, false, true><<<grid, threads, 0, s>>>(g);
-    } else {
-        if (multi) rms_fwd<E, W, N, true, false><<<grid, threads, 0, s>>>(g);
-        else rms_fwd<E, W, N, false, false><<<grid, threads, 0, s>>>(g);
+    if constexpr (ONE) {
+        if (!multi) return g.a.eight ? launch_ahead<rms_fwd<E, W, N, false, true>>(grid, threads, 0, s, g)
+                                     : launch_ahead<rms_fwd<E, W, N, false, false>>(grid, threads, 0, s, g);
     }
+    return g.a.eight ? launch_ahead<rms_fwd<E, W, N, true, true>>(grid, threads, 0, s, g)
+                     : launch_ahead<rms_fwd<E, W, N, true, false>>(grid, threads, 0, s, g);
 }
-template <typename E, int W, int N>
-void bwd(const Args& g, cudaStream_t s) {
+template <typename E, int W, int N, bool ONE = true>
+int bwd(const Args& g, cudaStream_t s) {
     const int lanes = lanes_of(g.a.d, W * N);
-    const unsigned grid = (unsigned)rms_bwd_splits(g.rows);
-    if (lanes > 32) rms_bwd<E, W, N, true><<<grid, lanes, 0, s>>>(g);
-    else rms_bwd<E, W, N, false><<<grid, 32 * kWarps, g.a.d * 4, s>>>(g);
+    const unsigned grid = (unsigned)rms_bwd_splits(g.rows, g.a.d);
+    if constexpr (ONE) {
+        if (lanes == 32) return launch_ahead<rms_bwd<E, W, N, false>>(grid, 32 * kWarps, kSums, s, g);
+    }
+    return launch_ahead<rms_bwd<E, W, N, true>>(grid, lanes, 0, s, g);
 }
+
+bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
 }  // namespace rms
 
-int rms_bwd_splits(long long rows) {
-    const long long most = 2 * rms::kSms;  // two CTAs an SM; what rms_sum reads grows with them
+int rms_bwd_splits(long long rows, int d) {
+    // as many CTAs as are resident: 16 warps an SM where a warp has a token; wider tokens have 2 to 16 warps each
+    const long long most = (long long)rms::kSms * (d <= 2048 ? 4 : 2);
     return (int)(rows < most ? rows : most);
 }
 
@@ -346,26 +370,31 @@ int launch_rms_fwd(const RmsArgs& a, cudaStream_t s) {
     const int es = a.bf16 ? 2 : 4, w = 16 / es;
     const bool vec = a.d % w == 0 && vec_ok(a.x, 16, es) && vec_ok(a.residual, 16, es) && vec_ok(a.h, 16, es) &&
                      (a.eight ? vec_ok(a.y, w, 1) : vec_ok(a.y, 16, es));
-    const Args g = {a, a.B * a.T};
+    const Args g = {a, a.B * a.T, al16(a.weight)};
     const bool wide = a.d > kMost * 16;
-    if (a.bf16) vec ? fwd<bf16, 8, 4>(g, s) : wide ? fwd<bf16, 1, 32>(g, s) : fwd<bf16, 1, 16>(g, s);
-    else if (vec) wide ? fwd<float, 4, 8>(g, s) : fwd<float, 4, 4>(g, s);
-    else wide ? fwd<float, 1, 32>(g, s) : fwd<float, 1, 16>(g, s);
-    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+    if (a.bf16) return vec ? fwd<bf16, 8, 4>(g, s) : wide ? fwd<bf16, 1, 32, false>(g, s) : fwd<bf16, 1, 16>(g, s);
+    if (vec) return wide ? fwd<float, 4, 8, false>(g, s) : fwd<float, 4, 4>(g, s);
+    return wide ? fwd<float, 1, 32, false>(g, s) : fwd<float, 1, 16>(g, s);
 }
 
 int launch_rms_bwd(const RmsArgs& a, cudaStream_t s) {
     using namespace rms;
-    const int es = a.bf16 ? 2 : 4, w = 16 / es;
-    const bool vec = a.d % w == 0 && vec_ok(a.x, 16, es) && vec_ok(a.dy, 16, es) && vec_ok(a.dh, 16, es) && vec_ok(a.dx, 16, es);
-    const Args g = {a, a.B * a.T};
-    const bool wide = a.d > kMost * 16;
-    if (a.bf16 && vec) wide || a.d <= 1024 ? bwd<bf16, 8, 4>(g, s) : bwd<bf16, 8, 2>(g, s);
-    else if (a.bf16) wide ? bwd<bf16, 1, 32>(g, s) : bwd<bf16, 1, 16>(g, s);
-    else if (vec) wide ? bwd<float, 4, 8>(g, s) : bwd<float, 4, 4>(g, s);
-    else wide ? bwd<float, 1, 32>(g, s) : bwd<float, 1, 16>(g, s);
-    if (a.ws) rms_sum<<<(a.d + 31) / 32, 256, 0, s>>>(a.ws, rms_bwd_splits(g.rows), a.d, a.dweight);
-    return cudaPeekAtLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+    const int es = a.bf16 ? 2 : 4, w = 16 / es, d = a.d;
+    const bool vec = d % w == 0 && vec_ok(a.x, 16, es) && vec_ok(a.dy, 16, es) && vec_ok(a.dh, 16, es) && vec_ok(a.dx, 16, es);
+    const Args g = {a, a.B * a.T, al16(a.weight)};
+    const bool mid = d <= kMost * 8, wide = d > kMost * 16;  // 8, 16 or 32 channels a lane, in a CTA's most threads
+    int st;
+    if (a.bf16 && vec) {
+        st = wide ? bwd<bf16, 8, 4, false>(g, s) : d > 1024 || d <= 512 ? bwd<bf16, 8, 2>(g, s) : d <= 768 ? bwd<bf16, 8, 3>(g, s) : bwd<bf16, 8, 4>(g, s);
+    } else if (a.bf16) {
+        st = mid ? bwd<bf16, 1, 8>(g, s) : wide ? bwd<bf16, 1, 32, false>(g, s) : bwd<bf16, 1, 16, false>(g, s);
+    } else if (vec) {
+        st = mid ? bwd<float, 4, 2>(g, s) : wide ? bwd<float, 4, 8, false>(g, s) : bwd<float, 4, 4, false>(g, s);
+    } else {
+        st = mid ? bwd<float, 1, 8>(g, s) : wide ? bwd<float, 1, 32, false>(g, s) : bwd<float, 1, 16, false>(g, s);
+    }
+    if (!a.ws || st != 0) return st;
+    return launch_ahead<rms_sum>((d + 31) / 32, 1024, 0, s, (const float*)a.ws, rms_bwd_splits(g.rows, d), d, a.dweight);
 }
 
 }  // namespace falcon

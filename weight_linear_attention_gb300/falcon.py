@@ -688,7 +688,7 @@ def falcon_rms_bwd_workspace_bytes(dims: FalconRmsDims) -> int:
 
 _PACK_GDR = struct.Struct("=6q2i").pack
 _PACK_RMS = struct.Struct("=3q2i").pack
-_PACK_N = functools.lru_cache(maxsize=None)(lambda n: struct.Struct(f"={n}q").pack)
+_PACK_8, _PACK_18, _PACK_33 = (struct.Struct(f"={n}q").pack for n in (8, 18, 33))
 
 
 def _refuse(name, t, shape, dtype, device, what="contiguous channels"):
@@ -696,21 +696,29 @@ def _refuse(name, t, shape, dtype, device, what="contiguous channels"):
                      f"{t.device} with strides {t.stride()}")
 
 
-def _view(name, t, shape, dtype, index, x, pointers, strides):
-    """Checks one strided tensor (the last axis contiguous) and notes its pointer and its other axes' strides."""
-    layout = t.stride()
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or layout[-1] != 1 and shape[-1] > 1:
-        _refuse(name, t, shape, dtype, x.device)
-    strides += layout[:-1]
-    pointers.append(t.data_ptr())
+def _views(names, tensors, shapes, dtype, index, x, pointers, strides):
+    """Checks strided tensors (the last axis contiguous), None for one that is not there, and notes their pointers and
+    their other axes' strides."""
+    for name, t, shape in zip(names, tensors, shapes):
+        if t is None:
+            pointers.append(None)
+            strides += (0,) * (len(shape) - 1)
+            continue
+        layout = t.stride()
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index or layout[-1] != 1 and shape[-1] > 1:
+            _refuse(name, t, shape, dtype, x.device)
+        strides += layout[:-1]
+        pointers.append(t.data_ptr())
 
 
-def _gate_view(name, t, shape, index, x, pointers, strides):
-    """The same for an fp32 [B,H,T] tensor, whose tokens may lie apart."""
-    if t.shape != shape or t.dtype is not _t().float32 or t.get_device() != index:
-        _refuse(name, t, shape, "torch.float32", x.device, "any strides")
-    strides += t.stride()
-    pointers.append(t.data_ptr())
+def _gate_views(names, tensors, shape, index, x, pointers, strides):
+    """The same for fp32 [B,H,T] tensors, whose tokens may lie apart."""
+    f32 = _t().float32
+    for name, t in zip(names, tensors):
+        if t.shape != shape or t.dtype is not f32 or t.get_device() != index:
+            _refuse(name, t, shape, f32, x.device, "any strides")
+        strides += t.stride()
+        pointers.append(t.data_ptr())
 
 
 def _dense(name, t, shape, dtype, index, x):
@@ -787,19 +795,17 @@ def gdr_forward(q, k, v, beta, g, S0=None, *, scale=None, lengths=None, out=None
     if S_final is None and want_state:
         S_final = _empty(v, (B, H, dk, dv), t.float32, stream)
     pointers, strides = [], []
-    _view("q", q, (B, Hk, T, dk), dtype, index, q, pointers, strides)
-    _view("k", k, (B, Hk, T, dk), dtype, index, q, pointers, strides)
-    _view("v", v, (B, H, T, dv), dtype, index, q, pointers, strides)
-    _gate_view("beta", beta, (B, H, T), index, q, pointers, strides)
-    _gate_view("g", g, (B, H, T), index, q, pointers, strides)
-    _view("out", out, (B, H, T, dv), dtype, index, q, pointers, strides)
+    of_qk, of_v = (B, Hk, T, dk), (B, H, T, dv)
+    _views(("q", "k", "v"), (q, k, v), (of_qk, of_qk, of_v), dtype, index, q, pointers, strides)
+    _gate_views(("beta", "g"), (beta, g), (B, H, T), index, q, pointers, strides)
+    _views(("out",), (out,), (of_v,), dtype, index, q, pointers, strides)
     p_out = pointers.pop()
     state = (B, H, dk, dv)
     p_S0 = _dense("S0", S0, state, t.float32, index, q)
     p_last = _dense("S_final", S_final, state, t.float32, index, q)
     p_len = _dense("lengths", lengths, (B,), t.torch.int32, index, q)
     workspace, size = _workspace(workspace, _gdr_bytes(dims, 0), q, stream)
-    _launch("falcon_gdr_fwd", index, (*pointers, p_S0, p_len, p_out, p_last, dims, _PACK_N(18)(*strides),
+    _launch("falcon_gdr_fwd", index, (*pointers, p_S0, p_len, p_out, p_last, dims, _PACK_18(*strides),
                                       dk ** -0.5 if scale is None else scale, _ptr(workspace), size,
                                       t.raw_stream(index) if stream is None else _handle(stream, q.device)))
     return out, S_final
@@ -820,24 +826,18 @@ def gdr_backward(q, k, v, beta, g, dout, S0=None, dS_final=None, *, scale=None, 
     dg = _empty(q, (B, H, T), f32, stream) if dg is None else dg
     dS0 = _empty(q, state, f32, stream) if dS0 is None else dS0
     pointers, strides = [], []
-    _view("q", q, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
-    _view("k", k, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
-    _view("v", v, (B, H, T, n_v), dtype, index, q, pointers, strides)
-    _gate_view("beta", beta, (B, H, T), index, q, pointers, strides)
-    _gate_view("g", g, (B, H, T), index, q, pointers, strides)
-    _view("dout", dout, (B, H, T, n_v), dtype, index, q, pointers, strides)
-    _view("dq", dq, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
-    _view("dk", dk, (B, Hk, T, n_k), dtype, index, q, pointers, strides)
-    _view("dv", dv, (B, H, T, n_v), dtype, index, q, pointers, strides)
-    _gate_view("dbeta", dbeta, (B, H, T), index, q, pointers, strides)
-    _gate_view("dg", dg, (B, H, T), index, q, pointers, strides)
+    of_qk, of_v, of_t = (B, Hk, T, n_k), (B, H, T, n_v), (B, H, T)
+    _views(("q", "k", "v"), (q, k, v), (of_qk, of_qk, of_v), dtype, index, q, pointers, strides)
+    _gate_views(("beta", "g"), (beta, g), of_t, index, q, pointers, strides)
+    _views(("dout", "dq", "dk", "dv"), (dout, dq, dk, dv), (of_v, of_qk, of_qk, of_v), dtype, index, q, pointers, strides)
+    _gate_views(("dbeta", "dg"), (dbeta, dg), of_t, index, q, pointers, strides)
     p_S0 = _dense("S0", S0, state, f32, index, q)
     p_dS = _dense("dS_final", dS_final, state, f32, index, q)
     p_dS0 = _dense("dS0", dS0, state, f32, index, q)
     p_len = _dense("lengths", lengths, (B,), t.torch.int32, index, q)
     workspace, size = _workspace(workspace, _gdr_bytes(dims, 1), q, stream)
     _launch("falcon_gdr_bwd", index, (*pointers[:5], p_S0, p_len, pointers[5], p_dS, *pointers[6:], p_dS0, dims,
-                                      _PACK_N(33)(*strides), n_k ** -0.5 if scale is None else scale, _ptr(workspace),
+                                      _PACK_33(*strides), n_k ** -0.5 if scale is None else scale, _ptr(workspace),
                                       size, t.raw_stream(index) if stream is None else _handle(stream, q.device)))
     return {"dq": dq, "dk": dk, "dv": dv, "dbeta": dbeta, "dg": dg, "dS0": dS0}
 
@@ -855,12 +855,13 @@ def _rms_sizes(x):
     return index, code, (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
 
 
-def _row_view(name, t, x, dtype, index, pointers, strides):
-    layout = t.stride()
-    if t.shape != x.shape or t.dtype is not dtype or t.get_device() != index or layout[-1] != 1 and x.shape[-1] > 1:
-        _refuse(name, t, x.shape, dtype, x.device)
-    strides += (0, *layout[:-1]) if len(layout) == 2 else layout[:-1]
-    pointers.append(t.data_ptr())
+def _row_strides(strides, flat):
+    """(batch, token) strides per tensor from the tensors' own: flat tokens are one sequence."""
+    if not flat:
+        return strides
+    out = [0] * (2 * len(strides))
+    out[1::2] = strides
+    return out
 
 
 def rmsnorm_forward(x, weight=None, residual=None, *, eps=1e-6, lengths=None, y=None, h=None, scales=None,
@@ -891,19 +892,14 @@ def rmsnorm_forward(x, weight=None, residual=None, *, eps=1e-6, lengths=None, y=
         h = _empty(x, x.shape, x.dtype, stream)
     if eight and scales is None:
         scales = _empty(x, x.shape[:-1], t.float32, stream)
-    pointers, strides = [], []
-    for name, v in (("x", x), ("residual", residual), ("h", h)):
-        if v is None:
-            pointers.append(None)
-            strides += (0, 0)
-        else:
-            _row_view(name, v, x, x.dtype, index, pointers, strides)
-    _row_view("y", y, x, kind, index, pointers, strides)
+    pointers, strides, shape = [], [], x.shape
+    _views(("x", "residual", "h"), (x, residual, h), (shape, shape, shape), x.dtype, index, x, pointers, strides)
+    _views(("y",), (y,), (shape,), kind, index, x, pointers, strides)
     p_x, p_r, p_h, p_y = pointers
     _launch("falcon_rms_fwd", index, (
         p_x, p_r, _dense("weight", weight, (d,), t.float32, index, x), _dense("lengths", lengths, (B,), torch.int32, index, x),
         p_h, p_y, _dense("scales", scales, x.shape[:-1], t.float32, index, x),
-        _PACK_RMS(B, T, d, code, FALCON_E4M3 if eight else code), _PACK_N(8)(*strides), eps,
+        _PACK_RMS(B, T, d, code, FALCON_E4M3 if eight else code), _PACK_8(*_row_strides(strides, len(shape) == 2)), eps,
         t.raw_stream(index) if stream is None else _handle(stream, x.device)))
     return y, x if residual is None else h, scales
 
@@ -919,13 +915,8 @@ def rmsnorm_backward(h, dy, weight=None, dh=None, *, eps=1e-6, lengths=None, dx=
     dx = _empty(h, h.shape, h.dtype, stream) if dx is None else dx
     if want_params and dweight is None:
         dweight = _empty(h, (d,), t.float32, stream)
-    pointers, strides = [], []
-    for name, v in (("h", h), ("dy", dy), ("dh", dh), ("dx", dx)):
-        if v is None:
-            pointers.append(None)
-            strides += (0, 0)
-        else:
-            _row_view(name, v, h, h.dtype, index, pointers, strides)
+    pointers, strides, shape = [], [], h.shape
+    _views(("h", "dy", "dh", "dx"), (h, dy, dh, dx), (shape, shape, shape, shape), h.dtype, index, h, pointers, strides)
     p_h, p_dy, p_dh, p_dx = pointers
     dims, size = _PACK_RMS(B, T, d, code, code), 0
     if dweight is not None:
@@ -933,6 +924,7 @@ def rmsnorm_backward(h, dy, weight=None, dh=None, *, eps=1e-6, lengths=None, dx=
     _launch("falcon_rms_bwd", index, (
         p_h, _dense("weight", weight, (d,), t.float32, index, h),
         _dense("lengths", lengths, (B,), t.torch.int32, index, h), p_dy, p_dh, p_dx,
-        _dense("dweight", dweight, (d,), t.float32, index, h), dims, _PACK_N(8)(*strides), eps, _ptr(workspace), size,
+        _dense("dweight", dweight, (d,), t.float32, index, h), dims, _PACK_8(*_row_strides(strides, len(shape) == 2)),
+        eps, _ptr(workspace), size,
         t.raw_stream(index) if stream is None else _handle(stream, h.device)))
     return {"dx": dx, "dweight": dweight}
