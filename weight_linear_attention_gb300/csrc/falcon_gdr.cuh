@@ -58,14 +58,15 @@ struct Lane {
 };
 
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Not a barrier to the compiler: what is read was written before a barrier of all threads, and is overwritten behind one.
 template <bool TRANS>
 __device__ __forceinline__ void ldm(uint32_t (&v)[4], uint32_t addr) {
     if (TRANS)
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
     else
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -134,21 +135,84 @@ __device__ __forceinline__ void mm(float (&acc)[8][4], uint32_t A, int rb, uint3
         step<PA, PB, BCOL>(acc, a, B, ln, kk, p0, p1);
     }
 }
-// The same with A in registers, as a product leaves it.
-template <int PA, int PB, bool BCOL>
+// Registers of a product's result as one k step's operand.
+template <int PA>
+__device__ __forceinline__ void split_a(uint32_t (&a)[PA][4], const float (&x)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t s[PA];
+        split<PA>(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1], s);
+#pragma unroll
+        for (int m = 0; m < PA; ++m) a[m][i] = s[m];
+    }
+}
+// The same with A in registers, as a product leaves it. ROLL: the loop stays one, its registers chosen by selection, for the
+// backward's long kernels, which wait for instructions as long as for anything else (gradients 220 us unrolled, 209 so;
+// the forward's are shorter and lose 5 % by it).
+template <int PA, int PB, bool BCOL, bool ROLL = false>
 __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4) {
+    if (!ROLL) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        if (kk < k0 || kk >= k1) continue;
-        uint32_t a[PA][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t s[PA];
-            split<PA>(A[2 * kk + (i >> 1)][2 * (i & 1)], A[2 * kk + (i >> 1)][2 * (i & 1) + 1], s);
-#pragma unroll
-            for (int m = 0; m < PA; ++m) a[m][i] = s[m];
+        for (int kk = 0; kk < 4; ++kk) {
+            if (kk < k0 || kk >= k1) continue;
+            const float x[2][4] = {{A[2 * kk][0], A[2 * kk][1], A[2 * kk][2], A[2 * kk][3]}, {A[2 * kk + 1][0], A[2 * kk + 1][1], A[2 * kk + 1][2], A[2 * kk + 1][3]}};
+            uint32_t a[PA][4];
+            split_a<PA>(a, x);
+            step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
         }
+        return;
+    }
+#pragma unroll 1
+    for (int kk = k0; kk < k1; ++kk) {
+        float x[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float lo = kk & 1 ? A[2 + i][e] : A[i][e], hi = kk & 1 ? A[6 + i][e] : A[4 + i][e];
+                x[i][e] = kk & 2 ? hi : lo;
+            }
+        uint32_t a[PA][4];
+        split_a<PA>(a, x);
         step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
+    }
+}
+// The scan's product, all of fp32: its warps have their quarter of the SM to themselves, so that the matrices of a step are
+// fetched a step ahead here.
+template <bool BCOL>
+__device__ __forceinline__ void mmr_ahead(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln) {
+    uint32_t v[2][2][3][4];
+    auto fetch = [&](int g) {  // k step g / 2, column groups 32 (g % 2)
+        const int kk = g >> 1, q = g & 1;
+        const uint32_t row = BCOL ? B + (16 * kk + ln.l7 + 8 * ln.l8) * 128 : B + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                const int p = 2 * q + i;
+                ldm<BCOL>(v[g & 1][i][m], row + m * kPlane + (BCOL ? (((2 * p + ln.l16) ^ ln.l7) << 4) : p * 2048));
+            }
+    };
+    fetch(0);
+    uint32_t a[3][4];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        if (g < 7) fetch(g + 1);
+        if (!(g & 1)) {
+            const int kk = g >> 1;
+            const float x[2][4] = {{A[2 * kk][0], A[2 * kk][1], A[2 * kk][2], A[2 * kk][3]}, {A[2 * kk + 1][0], A[2 * kk + 1][1], A[2 * kk + 1][2], A[2 * kk + 1][3]}};
+            split_a<3>(a, x);
+        }
+#pragma unroll
+        for (int s = 2; s >= 0; --s)
+#pragma unroll
+            for (int ma = 0; ma <= s; ++ma)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int q = g & 1;
+                    mma(acc[4 * q + 2 * i], a[ma], v[g & 1][i][s - ma][0], v[g & 1][i][s - ma][1]);
+                    mma(acc[4 * q + 2 * i + 1], a[ma], v[g & 1][i][s - ma][2], v[g & 1][i][s - ma][3]);
+                }
     }
 }
 // The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
@@ -629,19 +693,21 @@ struct PrepArgs {
 };
 
 template <typename E, int NK, bool BWD>
-__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 2 + 3 + (BWD ? (NK + 1) * planes<E>() : 0)) * kPlane; }
+__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 3 + (BWD ? 2 + (NK + 1) * planes<E>() : 0)) * kPlane; }
 
-// CTAs that the shared memory of an SM holds, up to four: what the registers are to allow.
-__host__ __device__ constexpr int ctas_of(int smem) { return 226 * 1024 / (smem + 3072) < 4 ? 226 * 1024 / (smem + 3072) : 4; }
+// CTAs that the shared memory of an SM holds, up to `most`: what the registers are to allow.
+__host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
+    return 226 * 1024 / (smem + 3072) < most ? 226 * 1024 / (smem + 3072) : most;
+}
 
 template <typename E, int NK, bool BWD>
-__global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gdr_prep(const PrepArgs<E> a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD ? 4 : 4)) gdr_prep(const PrepArgs<E> a) {
     constexpr int PI = planes<E>(), PX = state_planes<E, BWD>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     uint8_t* K = smem;
     float* T = reinterpret_cast<float*>(K + NK * PI * kPlane);
-    uint8_t* Y = K + (NK * PI + 2) * kPlane;
+    uint8_t* Y = K + (NK * PI + (BWD ? 2 : 0)) * kPlane;  // forward: X, in registers by then, leaves its place
     uint8_t* Q = Y + 3 * kPlane;  // BWD
     uint8_t* dO = Q + NK * PI * kPlane;
     const uint32_t Ks = saddr(K), Ys = saddr(Y), Qs = saddr(Q), Os = saddr(dO);
@@ -673,12 +739,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(acc, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt >= 2 * rb + 2) continue;  // 0 there
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
                 acc[nt][e] = j < i ? acc[nt][e] * decay(s, i, j) * s.beta[j] : 0.f;
             }
+        }
         put(T, rb, acc, ln);
     }
     invert(T, ln);
@@ -686,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
     float t[8][4];
     get(T, rb, t, ln);
     put_planes<PX>(a.X + item * (PX * kPlane), rb, t, ln);
+    if (!BWD) __syncthreads();
     const int k1 = rb + 1;  // X's rows end on the diagonal
 #pragma unroll 1
     for (int cb = 0; cb < NK; ++cb) {  // M's columns 64 cb ..
@@ -695,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[nt][e] = t[nt][e] * s.eG[8 * nt + 2 * ln.j + (e & 1)];
         zero(acc);
-        mmr<3, PI, true>(acc, f, Ks + cb * PI * kPlane, ln, 0, k1);
+        mmr<3, PI, true, BWD>(acc, f, Ks + cb * PI * kPlane, ln, 0, k1);
         if (cb > 0) __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -725,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
         wait<0>();
         __syncthreads();
         zero(acc);
-        mmr<3, PI, true>(acc, t, Ys, ln, 0, k1);
+        mmr<3, PI, true, BWD>(acc, t, Ys, ln, 0, k1);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -746,14 +815,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int nt = 0; nt < 8; ++nt) {
+                if (nt < 2 * rb) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
                     P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
                 }
+            }
             zero(acc);
-            mmr<3, PI, true>(acc, P, Os, ln, rb, 4);
+            mmr<3, PI, true, BWD>(acc, P, Os, ln, rb, 4);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -763,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
             __syncthreads();
             get_cols(T, rb, P, ln);
             zero(acc);
-            mmr<3, 3, true>(acc, P, Ys, ln, rb, 4);
+            mmr<3, 3, true, BWD>(acc, P, Ys, ln, rb, 4);
             __syncthreads();
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
@@ -854,13 +925,16 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
         commit();
     };
     for (int i = 0; i < STAGES - 1; ++i) fetch(i);
-    for (int i = 0; i < n; ++i) {
-        float add[NK][8][4];
+    float add[NK][8][4];
+    auto fetch_add = [&](int i) {
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            if (ident) zero(add[kb]);
+            if (ident || i >= n) zero(add[kb]);
             else get(a.A + (((bh * a.items + item(i)) * a.NV + sb) * NK + kb) * kTile, w, add[kb], ln);
         }
+    };
+    for (int i = 0; i < n; ++i) {
+        fetch_add(i);
         wait<STAGES - 2>();
         __syncthreads();  // item i has arrived for every warp, and item i - 1 is read by every warp
         fetch(i + STAGES - 1);
@@ -869,6 +943,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
             for (int kb = 0; kb < NK; ++kb)
                 put_planes<3, PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
         }
+        // (one tile: A starts the sum, and the next one's is on its way while the products run)
         const uint32_t M = saddr(smem) + (i % STAGES) * (3 * NK * NK * kPlane);
         float nw[NK][8][4];
 #pragma unroll
@@ -876,8 +951,8 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
             zero(nw[kb]);
 #pragma unroll
             for (int kc = 0; kc < NK; ++kc) {
-                if (!REV) mmr<3, 3, false>(nw[kb], acc[kc], M + (kb * NK + kc) * (3 * kPlane), ln);
-                else mmr<3, 3, true>(nw[kb], acc[kc], M + (kc * NK + kb) * (3 * kPlane), ln);
+                if (!REV) mmr_ahead<false>(nw[kb], acc[kc], M + (kb * NK + kc) * (3 * kPlane), ln);
+                else mmr_ahead<true>(nw[kb], acc[kc], M + (kc * NK + kb) * (3 * kPlane), ln);
             }
         }
 #pragma unroll
@@ -945,19 +1020,22 @@ __global__ void __launch_bounds__(kThreads) gdr_scans(const ScanArgs a, const Sc
     else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP, 3>(r, smem);
 }
 
-// The scan's segments. In units of 1000 cycles: a step along the chain takes 1.7 alone, and an SM's tensor cores take
-// 1.55 for each CTA's step. Cut into segments, the segments' maps come first (as many steps, for dk more rows), then a
-// scan over them, then the segments' own states. 8: what two more launches cost.
+// The scan's segments, for as few microseconds as the steps make: one of the states takes 1.95 with a CTA an SM and 1.15
+// more with each other one there, one of a segment's map, which writes nothing, 1.1 for each but 1.6 at least (three fit
+// an SM); wide heads have an SM to themselves, 5.1 and 4.5. A scan over the segments' maps and two more launches come on
+// top. (12 heads, 1024 chunks: 12 segments.)
 struct Cut {
     int L, nseg;
 };
 inline Cut cut_of(long long BH, int NC, int NK, int NV) {
-    auto steps = [](double ctas) { return ctas / 152 * 1.55 > 1.7 ? ctas / 152 * 1.55 : 1.7; };
+    auto per_sm = [](long long ctas) { return (double)((ctas + 151) / 152); };
+    auto own = [&](long long ctas) { return NK == 1 ? 0.8 + 1.15 * per_sm(ctas) : 5.1 * per_sm(ctas); };
+    auto map = [&](long long ctas) { return NK == 1 ? (1.1 * per_sm(ctas) > 1.6 ? 1.1 * per_sm(ctas) : 1.6) : 4.5 * per_sm(ctas); };
     Cut best = {NC > 0 ? NC : 1, 1};
-    double least = NC * steps((double)BH * NV);
-    for (int s = 2; s <= 128 && s * 4 <= NC; s += s < 16 ? 1 : 8) {
+    double least = NC * own(BH * NV);
+    for (int s = 2; s <= 64 && s * 4 <= NC; ++s) {
         const int L = (NC + s - 1) / s, nseg = (NC + L - 1) / L;
-        const double c = L * (steps((double)BH * nseg * (NV + NK)) + steps((double)BH * nseg * NV)) + 1.7 * nseg + 8;
+        const double c = L * (map(BH * nseg * (NV + NK)) + own(BH * nseg * NV)) + own(BH * NV) * nseg + 8;
         if (c < least) least = c, best = Cut{L, nseg};
     }
     return best;

@@ -153,12 +153,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Ws, ln, 0, 4, rb, 4);
     }
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt < 2 * rb) continue;  // 0 there
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
             P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
         }
+    }
     float q1[8][4];                                 // ONE: dO S^T, taken while S is there
     float sb_[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};  // the rows' dbeta and dV.V
     zero(q1);
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<3, PI, true>(d, P, Ob, ln, rb, 4);  // dU
+        mmr<3, PI, true, true>(d, P, Ob, ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const float eG = s.eG[16 * rb + ln.r + 8 * hf];
@@ -239,14 +241,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(N, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, rb, 4);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt < 2 * rb) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
                 N[nt][e] = j < i ? N[nt][e] * decay(s, i, j) : 0.f;
             }
+        }
         zero(z);
-        mmr<3, 3, true>(z, N, Zs, ln, rb, 4);
+        mmr<3, 3, true, true>(z, N, Zs, ln, rb, 4);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -313,15 +317,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 x[nt][e] *= s.eG[row] * a.n.scale;
                 d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
             }
-        mmr<3, PI, true>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
+        mmr<3, PI, true, true>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
         write_qk(a.dq, a.pq, x, kb);
-        mmr<PL, P1, true>(d, H, Ks + kb * PI * kPlane, ln);
+        mmr<PL, P1, true, true>(d, H, Ks + kb * PI * kPlane, ln);
         uint8_t* Qt = ONE ? W + 4 * kPlane : W;
         if (!ONE) {
             wait<0>();
             __syncthreads();
         }
-        mmr<PL, P1, true>(d, A3, saddr(Qt), ln, rb, 4);
+        mmr<PL, P1, true, true>(d, A3, saddr(Qt), ln, rb, 4);
         write_qk(a.dk, a.pk, d, kb);
         get_planes<PI>(Qt, rb, t, ln);
 #pragma unroll
