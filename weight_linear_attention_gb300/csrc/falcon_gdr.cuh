@@ -177,44 +177,6 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
         step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
     }
 }
-// The scan's product, all of fp32: its warps have their quarter of the SM to themselves, so that the matrices of a step are
-// fetched a step ahead here.
-template <bool BCOL>
-__device__ __forceinline__ void mmr_ahead(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln) {
-    uint32_t v[2][2][3][4];
-    auto fetch = [&](int g) {  // k step g / 2, column groups 32 (g % 2)
-        const int kk = g >> 1, q = g & 1;
-        const uint32_t row = BCOL ? B + (16 * kk + ln.l7 + 8 * ln.l8) * 128 : B + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int m = 0; m < 3; ++m) {
-                const int p = 2 * q + i;
-                ldm<BCOL>(v[g & 1][i][m], row + m * kPlane + (BCOL ? (((2 * p + ln.l16) ^ ln.l7) << 4) : p * 2048));
-            }
-    };
-    fetch(0);
-    uint32_t a[3][4];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        if (g < 7) fetch(g + 1);
-        if (!(g & 1)) {
-            const int kk = g >> 1;
-            const float x[2][4] = {{A[2 * kk][0], A[2 * kk][1], A[2 * kk][2], A[2 * kk][3]}, {A[2 * kk + 1][0], A[2 * kk + 1][1], A[2 * kk + 1][2], A[2 * kk + 1][3]}};
-            split_a<3>(a, x);
-        }
-#pragma unroll
-        for (int s = 2; s >= 0; --s)
-#pragma unroll
-            for (int ma = 0; ma <= s; ++ma)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int q = g & 1;
-                    mma(acc[4 * q + 2 * i], a[ma], v[g & 1][i][s - ma][0], v[g & 1][i][s - ma][1]);
-                    mma(acc[4 * q + 2 * i + 1], a[ma], v[g & 1][i][s - ma][2], v[g & 1][i][s - ma][3]);
-                }
-    }
-}
 // The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
 template <int PI, int PB, bool BCOL>
 __device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float* f, int rb, uint32_t B, const Lane& ln) {
@@ -307,7 +269,40 @@ __device__ __forceinline__ void get_planes(const uint8_t* T, int rb, float (&acc
         }
 }
 
-// ---- asynchronous copies, global to shared
+// ---- asynchronous copies
+// A warp's 16 rows of a result into the workspace: by bulk copies of 2 or 4 KB from its own rows of a tile in shared memory,
+// or, DIRECT, as they lie in registers, a quarter of eight lines an instruction. The copies need the tile: with wide heads
+// they save the forward 8 %; the backward's kernel, which has no room for it beside a third CTA, loses 15 % by it.
+__device__ __forceinline__ void bulk_out(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+template <int N, bool DIRECT>
+__device__ __forceinline__ void leave_planes(uint8_t* dst, uint8_t* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
+    if (DIRECT) return put_planes<N>(dst, rb, acc, ln);
+    if (ln.r + ln.j == 0) ptx::bulk_wait_read<0>();  // what these rows held before has left
+    __syncwarp();
+    put_planes<N>(stage, rb, acc, ln);
+    ptx::fence_async_smem();
+    __syncwarp();
+    if (ln.r + ln.j == 0) {
+#pragma unroll
+        for (int m = 0; m < N; ++m) bulk_out(dst + m * kPlane + rb * 2048, saddr(stage) + m * kPlane + rb * 2048, 2048);
+        ptx::bulk_commit();
+    }
+}
+template <bool DIRECT>
+__device__ __forceinline__ void leave_tile(float* dst, float* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
+    if (DIRECT) return put(dst, rb, acc, ln);
+    if (ln.r + ln.j == 0) ptx::bulk_wait_read<0>();
+    __syncwarp();
+    put(stage, rb, acc, ln);
+    ptx::fence_async_smem();
+    __syncwarp();
+    if (ln.r + ln.j == 0) {
+        bulk_out(dst + rb * 1024, saddr(stage + rb * 1024), 4096);
+        ptx::bulk_commit();
+    }
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in = true) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -693,7 +688,7 @@ struct PrepArgs {
 };
 
 template <typename E, int NK, bool BWD>
-__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 3 + (BWD ? 2 + (NK + 1) * planes<E>() : 0)) * kPlane; }
+__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 3 + (BWD ? 2 + (NK + 1) * planes<E>() : 3)) * kPlane; }
 
 // CTAs that the shared memory of an SM holds, up to `most`: what the registers are to allow.
 __host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
@@ -708,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     uint8_t* K = smem;
     float* T = reinterpret_cast<float*>(K + NK * PI * kPlane);
     uint8_t* Y = K + (NK * PI + (BWD ? 2 : 0)) * kPlane;  // forward: X, in registers by then, leaves its place
-    uint8_t* Q = Y + 3 * kPlane;  // BWD
+    uint8_t* Q = Y + 3 * kPlane;  // BWD; forward: results on their way out
     uint8_t* dO = Q + NK * PI * kPlane;
     const uint32_t Ks = saddr(K), Ys = saddr(Y), Qs = saddr(Q), Os = saddr(dO);
     const Lane ln;
@@ -753,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     const long long item = bh * a.n.NC + c;
     float t[8][4];
     get(T, rb, t, ln);
-    put_planes<PX>(a.X + item * (PX * kPlane), rb, t, ln);
+    leave_planes<PX, BWD>(a.X + item * (PX * kPlane), Q, rb, t, ln);
     if (!BWD) __syncthreads();
     const int k1 = rb + 1;  // X's rows end on the diagonal
 #pragma unroll 1
@@ -781,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     acc[nt][e] = (kb == cb && 16 * rb + ln.r + 8 * (e >> 1) == 8 * nt + 2 * ln.j + (e & 1) ? s.eC : 0.f) - acc[nt][e];
-            put_planes<3>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), rb, acc, ln);
+            leave_planes<3, BWD>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), Q, rb, acc, ln);
         }
     }
     const int NV = (a.n.dv + kC - 1) / kC;
@@ -806,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
         for (int kb = 0; kb < NK; ++kb) {
             zero(acc);
             mm<3, PI, true, true>(acc, Ys, rb, Ks + kb * PI * kPlane, ln);
-            put(a.A + ((item * NV + sb) * NK + kb) * kTile, rb, acc, ln);
+            leave_tile<BWD>(a.A + ((item * NV + sb) * NK + kb) * kTile, reinterpret_cast<float*>(Q), rb, acc, ln);
         }
         if (BWD) {
             // local part of the adjoints: Z = X^T diag(beta) P^T dO; adds scale Q^T diag(e^G) dO - K^T diag(e^G) Z
@@ -855,13 +850,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
             }
         }
     }
+    if (!BWD) ptx::bulk_wait_all();
 }
 
 // ---- the scan over items (chunks, or segments of them): state = M_i state + A_i, or with REV state = M_i^T state +
 // A_i from the last item to the first. A warp holds 16 rows of the transposed state, 16 x 64 NK, in registers: its own
-// result is the next step's operand, and nothing but M goes through shared memory. S_i takes the state before the item
-// (REV: behind it). With MAP a segment's own map is left instead of states: the state that it makes of nothing, and (rows
-// NV ..) the product of its M.
+// result is the next step's operand. S_i takes the state before the item (REV: behind it). With MAP a segment's own map is
+// left instead of states: the state that it makes of nothing, and (rows NV ..) the product of its M.
+// The chain of steps is what takes the time, so four warps do nothing but products and two bring M, block by block into a
+// ring, and A, and carry the states away: with loads and stores in the products' warps a step took 1.95 us, its 192
+// products a warp 0.8.
 struct ScanArgs {
     Sizes n;
     int NV;
@@ -880,14 +878,17 @@ struct ScanArgs {
     float* mapA;           // MAP: [BH][nseg][NV][NK]
 };
 
-// Items of M on their way: as many as the shared memory of an SM has room for.
-__host__ __device__ constexpr int scan_stages(int NK) { return NK == 1 ? 3 : 2; }
-__host__ __device__ constexpr int scan_smem(int NK) { return scan_stages(NK) * NK * NK * 3 * kPlane; }
+// Blocks of M in the ring; A's and S's places follow it. Two CTAs of one block a step fit an SM, one of four.
+__host__ __device__ constexpr int ring_of(int NK) { return NK == 1 ? 2 : 6; }
+__host__ __device__ constexpr int scan_smem(int NK) { return (ring_of(NK) * 3 + NK * 2 + NK * 3) * kPlane; }
+constexpr int kScanThreads = kThreads + 64;
 
 template <int NK, bool REV, bool MAP, int PS>
 __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
-    constexpr int STAGES = scan_stages(NK);
+    constexpr int R = ring_of(NK), NB = NK * NK;
     const Lane ln;
+    uint8_t* At = smem + R * 3 * kPlane;
+    uint8_t* St = At + NK * 2 * kPlane;
     const int w = threadIdx.x >> 5;
     const unsigned ubh = blockIdx.x / (unsigned)a.nseg;
     const long long bh = ubh, b = ubh / (unsigned)a.n.H;
@@ -895,6 +896,41 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     const bool ident = MAP && sb >= a.NV;
     const int count = a.chunks ? (length_of(a.n, b) + kC - 1) / kC : a.items;
     const int i0 = min(count, seg * a.L), i1 = min(count, i0 + a.L), n = i1 - i0;
+    auto item = [&](int i) { return REV ? i1 - 1 - i : i0 + i; };
+    // block t of a step: rows kb, columns kc of M (REV: of its transpose)
+    auto block = [&](int t) { return REV ? (t % NK) * NK + t / NK : t; };
+    if (threadIdx.x >= kThreads) {
+        const int id = threadIdx.x - kThreads;
+        auto bring = [&](uint8_t* dst, const uint8_t* src, int bytes) {
+            const uint32_t d = saddr(dst);
+            for (int o = 16 * id; o < bytes; o += 16 * 64) copy16(d + o, src + o);
+        };
+        auto fetch = [&](int g) {
+            const int i = g / NB;
+            if (i < n) bring(smem + (g % R) * (3 * kPlane), a.M + ((bh * a.items + item(i)) * NB + block(g % NB)) * (3 * kPlane), 3 * kPlane);
+        };
+        for (int g = 0; g < R - 1; ++g) {
+            fetch(g);
+            commit();
+        }
+        for (int i = 0; i < n; ++i) {
+            for (int t = 0; t < NB; ++t) {
+                wait<R - 2>();
+                __syncthreads();  // block t has arrived, and the one before it is read
+                fetch(i * NB + t + R - 1);
+                if (t == 0 && !ident)
+                    bring(At, reinterpret_cast<const uint8_t*>(a.A + ((bh * a.items + item(i)) * a.NV + sb) * (NK * kTile)), NK * kTile * 4);
+                commit();
+            }
+            wait<NB - 1>();
+            __syncthreads();  // A has arrived, and the state is in its place
+            if (MAP) continue;
+            uint8_t* dst = a.S + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * PS * kPlane);
+#pragma unroll 6
+            for (int o = 16 * id; o < NK * PS * kPlane; o += 16 * 64) *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(St + o);
+        }
+        return;
+    }
     float acc[NK][8][4];
 #pragma unroll
     for (int kb = 0; kb < NK; ++kb) {
@@ -919,48 +955,31 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
                 }
         }
     }
-    auto item = [&](int i) { return REV ? i1 - 1 - i : i0 + i; };
-    auto fetch = [&](int i) {
-        if (i < n) copy_planes<3 * NK * NK>(saddr(smem) + (i % STAGES) * (3 * NK * NK * kPlane), a.M + (bh * a.items + item(i)) * (3 * NK * NK * kPlane));
-        commit();
-    };
-    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
-    float add[NK][8][4];
-    auto fetch_add = [&](int i) {
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-            if (ident || i >= n) zero(add[kb]);
-            else get(a.A + (((bh * a.items + item(i)) * a.NV + sb) * NK + kb) * kTile, w, add[kb], ln);
-        }
-    };
     for (int i = 0; i < n; ++i) {
-        fetch_add(i);
-        wait<STAGES - 2>();
-        __syncthreads();  // item i has arrived for every warp, and item i - 1 is read by every warp
-        fetch(i + STAGES - 1);
-        if (!MAP) {
-#pragma unroll
-            for (int kb = 0; kb < NK; ++kb)
-                put_planes<3, PS>(a.S + (((bh * a.stride + item(i)) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
-        }
-        // (one tile: A starts the sum, and the next one's is on its way while the products run)
-        const uint32_t M = saddr(smem) + (i % STAGES) * (3 * NK * NK * kPlane);
         float nw[NK][8][4];
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-            zero(nw[kb]);
+        for (int t = 0; t < NB; ++t) {
+            const int kb = t / NK, kc = t % NK;
+            __syncthreads();
+            if (t == 0) {
 #pragma unroll
-            for (int kc = 0; kc < NK; ++kc) {
-                if (!REV) mmr_ahead<false>(nw[kb], acc[kc], M + (kb * NK + kc) * (3 * kPlane), ln);
-                else mmr_ahead<true>(nw[kb], acc[kc], M + (kc * NK + kb) * (3 * kPlane), ln);
+                for (int k = 0; k < NK; ++k) {
+                    if (!MAP) put_planes<3, PS>(St + k * (PS * kPlane), w, acc[k], ln);
+                    zero(nw[k]);
+                }
             }
+            mmr<3, 3, REV>(nw[kb], acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln);
         }
+        __syncthreads();
 #pragma unroll
-        for (int kb = 0; kb < NK; ++kb)
+        for (int kb = 0; kb < NK; ++kb) {
+            if (ident) zero(acc[kb]);
+            else get(reinterpret_cast<const float*>(At) + kb * kTile, w, acc[kb], ln);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[kb][nt][e] = nw[kb][nt][e] + add[kb][nt][e];
+                for (int e = 0; e < 4; ++e) acc[kb][nt][e] += nw[kb][nt][e];
+        }
     }
     if (MAP) {
 #pragma unroll
@@ -990,7 +1009,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     const bool ends = i1 == count && (n > 0 || seg == 0);
 #pragma unroll
     for (int kb = 0; kb < NK; ++kb) {
-        if (a.end_tile && ends) put_planes<PS>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
+        if (a.end_tile && ends) put_planes<3, PS>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
         if (!a.last) continue;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -1004,7 +1023,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
 
 // The states' scan.
 template <int NK, bool MAP, int PS>
-__global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scan(const ScanArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::pdl_wait();
     if (!MAP && a.chunks) ptx::pdl_launch_dependents();
@@ -1012,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads) gdr_scan(const ScanArgs a) {
 }
 // The states' and the adjoints', side by side: neither needs the other.
 template <int NK, bool MAP>
-__global__ void __launch_bounds__(kThreads) gdr_scans(const ScanArgs a, const ScanArgs r) {
+__global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scans(const ScanArgs a, const ScanArgs r) {
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::pdl_wait();
     if (!MAP && a.chunks) ptx::pdl_launch_dependents();
@@ -1130,10 +1149,10 @@ int run_scan(const Sizes& n, const Layout& l, uint8_t* ws, const float* init, fl
     const unsigned x = (unsigned)(n.BH * l.cut.nseg);
     int st = 0;
     if (l.cut.nseg > 1) {
-        st |= launch_ahead<gdr_scan<NK, true, 3>>(dim3(x, l.NV + NK), kThreads, scan_smem(NK), s, f.map);
-        st |= launch_ahead<gdr_scan<NK, false, 3>>(dim3((unsigned)n.BH, l.NV), kThreads, scan_smem(NK), s, f.over);
+        st |= launch_ahead<gdr_scan<NK, true, 3>>(dim3(x, l.NV + NK), kScanThreads, scan_smem(NK), s, f.map);
+        st |= launch_ahead<gdr_scan<NK, false, 3>>(dim3((unsigned)n.BH, l.NV), kScanThreads, scan_smem(NK), s, f.over);
     }
-    return st | launch_ahead<gdr_scan<NK, false, PS>>(dim3(x, l.NV), kThreads, scan_smem(NK), s, f.own);
+    return st | launch_ahead<gdr_scan<NK, false, PS>>(dim3(x, l.NV), kScanThreads, scan_smem(NK), s, f.own);
 }
 // Both of a backward call's. The segments' products of M are the forward's: the other reads them transposed.
 template <int NK>
@@ -1143,10 +1162,10 @@ int run_scans(const Sizes& n, const Layout& l, uint8_t* ws, const float* S0, con
     const unsigned x = (unsigned)(n.BH * l.cut.nseg);
     int st = 0;
     if (l.cut.nseg > 1) {
-        st |= launch_ahead<gdr_scans<NK, true>>(dim3(x, l.NV + NK, 2), kThreads, scan_smem(NK), s, f.map, r.map);
-        st |= launch_ahead<gdr_scans<NK, false>>(dim3((unsigned)n.BH, l.NV, 2), kThreads, scan_smem(NK), s, f.over, r.over);
+        st |= launch_ahead<gdr_scans<NK, true>>(dim3(x, l.NV + NK, 2), kScanThreads, scan_smem(NK), s, f.map, r.map);
+        st |= launch_ahead<gdr_scans<NK, false>>(dim3((unsigned)n.BH, l.NV, 2), kScanThreads, scan_smem(NK), s, f.over, r.over);
     }
-    return st | launch_ahead<gdr_scans<NK, false>>(dim3(x, l.NV, 2), kThreads, scan_smem(NK), s, f.own, r.own);
+    return st | launch_ahead<gdr_scans<NK, false>>(dim3(x, l.NV, 2), kScanThreads, scan_smem(NK), s, f.own, r.own);
 }
 
 }  // namespace gdr
