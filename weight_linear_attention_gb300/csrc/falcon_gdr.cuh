@@ -879,8 +879,8 @@ struct ScanArgs {
 };
 
 // Blocks of M in the ring; A's and S's places follow it. Two CTAs of one block a step fit an SM, one of four.
-__host__ __device__ constexpr int ring_of(int NK) { return NK == 1 ? 2 : 6; }
-__host__ __device__ constexpr int scan_smem(int NK) { return (ring_of(NK) * 3 + NK * 2 + NK * 3) * kPlane; }
+__host__ __device__ constexpr int ring_of(int NK) { return NK == 1 ? 2 : 4; }
+__host__ __device__ constexpr int scan_smem(int NK) { return (ring_of(NK) * 3 + 2 * NK * 2 + NK * 3) * kPlane; }
 constexpr int kScanThreads = kThreads + 64;
 
 template <int NK, bool REV, bool MAP, int PS>
@@ -888,7 +888,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     constexpr int R = ring_of(NK), NB = NK * NK;
     const Lane ln;
     uint8_t* At = smem + R * 3 * kPlane;
-    uint8_t* St = At + NK * 2 * kPlane;
+    uint8_t* St = At + 2 * NK * 2 * kPlane;
     const int w = threadIdx.x >> 5;
     const unsigned ubh = blockIdx.x / (unsigned)a.nseg;
     const long long bh = ubh, b = ubh / (unsigned)a.n.H;
@@ -909,6 +909,11 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
             const int i = g / NB;
             if (i < n) bring(smem + (g % R) * (3 * kPlane), a.M + ((bh * a.items + item(i)) * NB + block(g % NB)) * (3 * kPlane), 3 * kPlane);
         };
+        auto fetch_a = [&](int i) {  // two places, each a step's
+            if (i < n && !ident)
+                bring(At + (i & 1) * (NK * 2 * kPlane), reinterpret_cast<const uint8_t*>(a.A + ((bh * a.items + item(i)) * a.NV + sb) * (NK * kTile)), NK * kTile * 4);
+        };
+        fetch_a(0);
         for (int g = 0; g < R - 1; ++g) {
             fetch(g);
             commit();
@@ -916,18 +921,16 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
         for (int i = 0; i < n; ++i) {
             for (int t = 0; t < NB; ++t) {
                 wait<R - 2>();
-                __syncthreads();  // block t has arrived, and the one before it is read
+                __syncthreads();  // block t has arrived (and A, a step ago), the one before it is read, and so is the state
                 fetch(i * NB + t + R - 1);
-                if (t == 0 && !ident)
-                    bring(At, reinterpret_cast<const uint8_t*>(a.A + ((bh * a.items + item(i)) * a.NV + sb) * (NK * kTile)), NK * kTile * 4);
+                if (t == 0) fetch_a(i + 1);
                 commit();
+                if (t > 0 || MAP) continue;
+                ptx::named_bar(1, kScanThreads);  // the state is in its place
+                uint8_t* dst = a.S + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * PS * kPlane);
+#pragma unroll 8
+                for (int o = 16 * id; o < NK * PS * kPlane; o += 16 * 64) *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(St + o);
             }
-            wait<NB - 1>();
-            __syncthreads();  // A has arrived, and the state is in its place
-            if (MAP) continue;
-            uint8_t* dst = a.S + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * PS * kPlane);
-#pragma unroll 6
-            for (int o = 16 * id; o < NK * PS * kPlane; o += 16 * 64) *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(St + o);
         }
         return;
     }
@@ -967,14 +970,14 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
                     if (!MAP) put_planes<3, PS>(St + k * (PS * kPlane), w, acc[k], ln);
                     zero(nw[k]);
                 }
+                if (!MAP) asm volatile("bar.arrive 1, %0;" ::"n"(kScanThreads) : "memory");
             }
             mmr<3, 3, REV>(nw[kb], acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln);
         }
-        __syncthreads();
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             if (ident) zero(acc[kb]);
-            else get(reinterpret_cast<const float*>(At) + kb * kTile, w, acc[kb], ln);
+            else get(reinterpret_cast<const float*>(At) + ((i & 1) * NK + kb) * kTile, w, acc[kb], ln);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
