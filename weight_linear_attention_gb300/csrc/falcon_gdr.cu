@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
         return;
     }
     const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * PS * kPlane);
-    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
+    const Gates gates = load_gates<false>(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
         load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
@@ -68,15 +68,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
     zero(P);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Qs + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        if (nt >= 2 * rb + 2) continue;  // 0 there
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
-            P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
-        }
-    }
+    times_decay<false, false>(P, s, rb, ln, nullptr, a.n.scale);
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         float o[8][4];

@@ -74,23 +74,33 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two values as N planes of packed pairs (x in the low half).
+// Two values as N planes of packed pairs (x in the low half). A plane is the upper half of what is left, cut off: 8 bits
+// each, so that three are the value itself; the last of fewer is rounded.
 template <int N>
 __device__ __forceinline__ void split(float x, float y, uint32_t (&p)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        p[i] = *reinterpret_cast<const uint32_t*>(&h);
+        if (i + 1 == N && N < 3) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            p[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            p[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+        }
         if (i + 1 < N) {
-            x -= __uint_as_float(p[i] << 16);
-            y -= __uint_as_float(p[i] & 0xffff0000u);
+            x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+            y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
         }
     }
 }
 
+// Which products of planes: all of them, or those below the first two's, or theirs alone. The tensor cores cut sums off, a
+// unit at a time: of fp32 operands the small products of all k steps come first, while the sums are small, and leave four
+// cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm instead of 6e-7).
+enum { kAll = 0, kSmall = 1, kGreat = 2 };
+
 // One k step of 16: acc (16 rows x 64 columns, column groups of 16 in [p0, p1)) += a B. B, its planes at `b`, is stored
 // [n][k], or [k][n] (BCOL).
-template <int PA, int PB, bool BCOL>
+template <int PA, int PB, bool BCOL, int WHICH = kAll>
 __device__ __forceinline__ void step(float (&acc)[8][4], const uint32_t (&a)[PA][4], uint32_t b, const Lane& ln, int kk, int p0, int p1) {
     const uint32_t row = BCOL ? b + (16 * kk + ln.l7 + 8 * ln.l8) * 128 : b + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
 #pragma unroll
@@ -100,12 +110,12 @@ __device__ __forceinline__ void step(float (&acc)[8][4], const uint32_t (&a)[PA]
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int m = 0; m < PB; ++m) {
+            for (int m = 0; m < (WHICH == kGreat ? 1 : PB); ++m) {
                 const int p = 2 * q + i;
                 ldm<BCOL>(v[i][m], row + m * kPlane + (BCOL ? (((2 * p + ln.l16) ^ ln.l7) << 4) : p * 2048));
             }
 #pragma unroll
-        for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
+        for (int s = WHICH == kGreat ? 0 : (PA > PB ? PA : PB) - 1; s >= (WHICH == kSmall ? 1 : 0); --s)
 #pragma unroll
             for (int ma = 0; ma < PA; ++ma) {
                 const int mb = s - ma;
@@ -120,19 +130,24 @@ __device__ __forceinline__ void step(float (&acc)[8][4], const uint32_t (&a)[PA]
 }
 
 // acc += A[16 rb ..][k] B over k steps [k0, k1). ACOL: A is stored [k][m].
-template <int PA, int PB, bool ACOL, bool BCOL>
+template <int PA, int PB, bool ACOL, bool BCOL, int WHICH = kAll>
 __device__ __forceinline__ void mm(float (&acc)[8][4], uint32_t A, int rb, uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4,
                                    int p0 = 0, int p1 = 4) {
+    if constexpr (PA * PB == 9 && WHICH == kAll) {
+        mm<PA, PB, ACOL, BCOL, kSmall>(acc, A, rb, B, ln, k0, k1, p0, p1);
+        mm<PA, PB, ACOL, BCOL, kGreat>(acc, A, rb, B, ln, k0, k1, p0, p1);
+        return;
+    }
 #pragma unroll 1
     for (int kk = k0; kk < k1; ++kk) {
         uint32_t a[PA][4];
 #pragma unroll
-        for (int m = 0; m < PA; ++m) {
+        for (int m = 0; m < (WHICH == kGreat ? 1 : PA); ++m) {
             const uint32_t p = ACOL ? A + (16 * kk + ln.l7 + 8 * ln.l16) * 128 + (((2 * rb + ln.l8) ^ ln.l7) << 4)
                                     : A + (16 * rb + ln.l7 + 8 * ln.l8) * 128 + (((2 * kk + ln.l16) ^ ln.l7) << 4);
             ldm<ACOL>(a[m], p + m * kPlane);
         }
-        step<PA, PB, BCOL>(acc, a, B, ln, kk, p0, p1);
+        step<PA, PB, BCOL, WHICH>(acc, a, B, ln, kk, p0, p1);
     }
 }
 // Registers of a product's result as one k step's operand.
@@ -149,8 +164,13 @@ __device__ __forceinline__ void split_a(uint32_t (&a)[PA][4], const float (&x)[2
 // The same with A in registers, as a product leaves it. ROLL: the loop stays one, its registers chosen by selection, for the
 // backward's long kernels, which wait for instructions as long as for anything else (gradients 220 us unrolled, 209 so;
 // the forward's are shorter and lose 5 % by it).
-template <int PA, int PB, bool BCOL, bool ROLL = false>
+template <int PA, int PB, bool BCOL, bool ROLL = false, int WHICH = kAll>
 __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4) {
+    if constexpr (PA * PB == 9 && WHICH == kAll) {
+        mmr<PA, PB, BCOL, ROLL, kSmall>(acc, A, B, ln, k0, k1);
+        mmr<PA, PB, BCOL, ROLL, kGreat>(acc, A, B, ln, k0, k1);
+        return;
+    }
     if (!ROLL) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -158,7 +178,7 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
             const float x[2][4] = {{A[2 * kk][0], A[2 * kk][1], A[2 * kk][2], A[2 * kk][3]}, {A[2 * kk + 1][0], A[2 * kk + 1][1], A[2 * kk + 1][2], A[2 * kk + 1][3]}};
             uint32_t a[PA][4];
             split_a<PA>(a, x);
-            step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
+            step<PA, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
         }
         return;
     }
@@ -174,12 +194,17 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
             }
         uint32_t a[PA][4];
         split_a<PA>(a, x);
-        step<PA, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
+        step<PA, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
     }
 }
 // The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
-template <int PI, int PB, bool BCOL>
+template <int PI, int PB, bool BCOL, int WHICH = kAll>
 __device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float* f, int rb, uint32_t B, const Lane& ln) {
+    if constexpr (PB == 3 && WHICH == kAll) {
+        mms<PI, PB, BCOL, kSmall>(acc, A, f, rb, B, ln);
+        mms<PI, PB, BCOL, kGreat>(acc, A, f, rb, B, ln);
+        return;
+    }
 #pragma unroll 1
     for (int kk = 0; kk < 4; ++kk) {
         float x[4][2];
@@ -201,7 +226,7 @@ __device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float*
 #pragma unroll
             for (int m = 0; m < 3; ++m) a[m][i] = p[m];
         }
-        step<3, PB, BCOL>(acc, a, B, ln, kk, 0, 4);
+        step<3, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
     }
 }
 
@@ -465,8 +490,11 @@ __device__ __forceinline__ void write_rows(E* p, long long st, bool pair, int rb
 // ---- a chunk's gains and decays. Sums of log decays are pairs of floats, hi + lo, 48 bits: a difference of two, at whatever
 // size, keeps fp32's relative precision. (In double, whose units are few, this took 10 us of a chunk's 18.)
 struct Scal {
-    float beta[kC], hi[kC], lo[kC];  // G / ln 2 = hi + lo
+    float beta[kC], hi[kC], lo[kC];  // (backward: no gain below kTiny), G / ln 2 = hi + lo
     float eG[kC], w[kC], bw[kC];     // e^G, e^{G_C - G}, beta w
+    // D_ij of a row block of 16 and columns before it as a product: with R the sum before the block, since[i] = e^{G_i - R}
+    // and until[block][j] = e^{R - G_j}, neither above 1 where the decays are not
+    float since[kC], until[4][kC];
     float eC;
 };
 __device__ __forceinline__ float ex2(float x) {
@@ -491,6 +519,10 @@ __device__ __forceinline__ Two add(Two a, Two b) {
     return Two{h, e - (h - s)};
 }
 
+// The backward divides by the gain what has it as a factor: where it is (nearly) 0, this takes its place, which moves nothing
+// else, and dV is scaled back.
+constexpr float kTiny = 5.421010862427522e-20f;  // 2^-64
+
 // Below this a log decay's factor is 0 in fp32 and so are all that contain it; sums of 64 keep their lesser parts.
 constexpr float kLeast = -1e5f;
 
@@ -498,6 +530,7 @@ constexpr float kLeast = -1e5f;
 struct Gates {
     float beta[2], g[2];
 };
+template <bool BWD>
 __device__ __forceinline__ Gates load_gates(const Ten<float>& beta, const Ten<float>& g, long long b, long long h, long long t0, int live) {
     Gates r = {};
     if (threadIdx.x < 32) {
@@ -506,6 +539,7 @@ __device__ __forceinline__ Gates load_gates(const Ten<float>& beta, const Ten<fl
             const int t = 2 * threadIdx.x + e;
             if (t < live) {
                 r.beta[e] = beta.row0(b, h, t0)[t * beta.st];
+                if (BWD && fabsf(r.beta[e]) < kTiny) r.beta[e] = kTiny;
                 r.g[e] = g.row0(b, h, t0)[t * g.st];
             }
         }
@@ -543,6 +577,48 @@ __device__ __forceinline__ void make_scal(Scal& s, const Gates& r) {
         s.bw[t] = r.beta[e] * w;
     }
     if (l == 31) s.eC = ex2(all.hi, all.lo);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int t = l + 32 * h, first = t & ~15;
+        const float rh = first ? s.hi[first - 1] : 0.f, rl = first ? s.lo[first - 1] : 0.f;
+        s.since[t] = ex2((s.hi[t] - rh) + (s.lo[t] - rl));
+#pragma unroll
+        for (int b = 1; b < 4; ++b)
+            if (t < 16 * b) s.until[b][t] = ex2((s.hi[16 * b - 1] - s.hi[t]) + (s.lo[16 * b - 1] - s.lo[t]));
+    }
+}
+
+// A product's rows times D, and times f of the column (of the row, UPPER) or f itself: rows i and columns j <= i, or rows
+// j and columns i >= j (UPPER), STRICT without the diagonal; 0 elsewhere.
+template <bool UPPER, bool STRICT>
+__device__ __forceinline__ void times_decay(float (&acc)[8][4], const Scal& s, int rb, const Lane& ln, const float* f, float one) {
+    const int r0 = 16 * rb + ln.r;
+    const float a0 = UPPER ? (f ? f[r0] * one : one) : s.since[r0] * one, a1 = UPPER ? (f ? f[r0 + 8] * one : one) : s.since[r0 + 8] * one;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        const int c = 8 * nt + 2 * ln.j;
+        if ((nt >> 1) == rb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = r0 + 8 * (e >> 1), col = c + (e & 1), i = UPPER ? col : row, j = UPPER ? row : col;
+                const bool in = STRICT ? j < i : j <= i;
+                acc[nt][e] = in ? acc[nt][e] * (decay(s, i, j) * (f ? f[j] * one : one)) : 0.f;
+            }
+        } else if (UPPER ? nt > 2 * rb : nt < 2 * rb) {
+            float2 v = *reinterpret_cast<const float2*>(UPPER ? s.since + c : s.until[rb] + c);
+            if (!UPPER && f) {
+                const float2 u = *reinterpret_cast<const float2*>(f + c);
+                v.x *= u.x, v.y *= u.y;
+            }
+            const float b0 = UPPER ? a0 * s.until[nt >> 1][r0] : a0, b1 = UPPER ? a1 * s.until[nt >> 1][r0 + 8] : a1;
+            acc[nt][0] *= b0 * v.x, acc[nt][1] *= b0 * v.y;
+            acc[nt][2] *= b1 * v.x, acc[nt][3] *= b1 * v.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+        }
+    }
 }
 
 // ---- the inverse of I + A, A strictly lower triangular in tile T, in its place: 16 x 16 diagonal blocks by
@@ -718,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     // the CTAs of an SM put the longest rows of a triangle on different quarters of it
     const int rb = ((threadIdx.x >> 5) + blockIdx.x) & 3;
     const long long t0 = (long long)c * kC;
-    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
+    const Gates gates = load_gates<BWD>(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
         load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, a.n.dk - kb * kC, a.k.vec);
@@ -733,15 +809,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
         zero(acc);
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(acc, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt >= 2 * rb + 2) continue;  // 0 there
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * rb + ln.r + 8 * (e >> 1), j = 8 * nt + 2 * ln.j + (e & 1);
-                acc[nt][e] = j < i ? acc[nt][e] * decay(s, i, j) * s.beta[j] : 0.f;
-            }
-        }
+        times_decay<false, true>(acc, s, rb, ln, s.beta, 1.f);
         put(T, rb, acc, ln);
     }
     invert(T, ln);
@@ -772,10 +840,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
             zero(acc);
             mm<PI, 3, true, true>(acc, Ks + kb * PI * kPlane, rb, Ys, ln);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int nt = 0; nt < 8; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][e] = -acc[nt][e];
+                if (kb != cb || (nt >> 1) != rb) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[nt][e] = (kb == cb && 16 * rb + ln.r + 8 * (e >> 1) == 8 * nt + 2 * ln.j + (e & 1) ? s.eC : 0.f) - acc[nt][e];
+                    if (ln.r + 8 * (e >> 1) == 8 * (nt & 1) + 2 * ln.j + (e & 1)) acc[nt][e] += s.eC;
+            }
             leave_planes<3, BWD>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), Q, rb, acc, ln);
         }
     }
@@ -809,15 +881,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
             zero(P);
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4);
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                if (nt < 2 * rb) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
-                    P[nt][e] = j <= i ? P[nt][e] * decay(s, i, j) * a.n.scale : 0.f;
-                }
-            }
+            times_decay<true, false>(P, s, rb, ln, nullptr, a.n.scale);
             zero(acc);
             mmr<3, PI, true, BWD>(acc, P, Os, ln, rb, 4);
 #pragma unroll
@@ -840,12 +904,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
                 zero(acc);
+                zero(P);
                 mms<PI, PI, true>(acc, Os, s.eG, rb, Qs + kb * PI * kPlane, ln);
+                mm<3, PI, true, true>(P, Ys, rb, Ks + kb * PI * kPlane, ln);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][e] *= a.n.scale;
-                mm<3, PI, true, true>(acc, Ys, rb, Ks + kb * PI * kPlane, ln);
+                    for (int e = 0; e < 4; ++e) acc[nt][e] = fmaf(acc[nt][e], a.n.scale, P[nt][e]);
                 put(a.dA + ((item * NV + sb) * NK + kb) * kTile, rb, acc, ln);
             }
         }
@@ -858,8 +923,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
 // result is the next step's operand. S_i takes the state before the item (REV: behind it). With MAP a segment's own map is
 // left instead of states: the state that it makes of nothing, and (rows NV ..) the product of its M.
 // The chain of steps is what takes the time, so four warps do nothing but products and two bring M, block by block into a
-// ring, and A, and carry the states away: with loads and stores in the products' warps a step took 1.95 us, its 192
-// products a warp 0.8.
+// ring, and A, and carry the states away: a step takes 1.5 us, 1.95 with loads and stores in the products' warps (its
+// 192 products a warp are 0.8).
 struct ScanArgs {
     Sizes n;
     int NV;
@@ -1042,17 +1107,19 @@ __global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scans(const
     else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP, 3>(r, smem);
 }
 
-// The scan's segments, for as few microseconds as the steps make: one of the states takes 1.95 with a CTA an SM and 1.15
-// more with each other one there, one of a segment's map, which writes nothing, 1.1 for each but 1.6 at least (three fit
-// an SM); wide heads have an SM to themselves, 5.1 and 4.5. A scan over the segments' maps and two more launches come on
-// top. (12 heads, 1024 chunks: 12 segments.)
+// The scan's segments, for as few microseconds as the steps make: one of the states takes 1.5 with a CTA an SM, 2.6 with the
+// two that fit, one of a segment's map, which writes nothing, 1.3 and 2.1; wide heads have an SM to themselves, 4.5 and 4. A
+// scan over the segments' maps and two more launches come on top. (12 heads, 1024 chunks: 25 segments.)
 struct Cut {
     int L, nseg;
 };
 inline Cut cut_of(long long BH, int NC, int NK, int NV) {
-    auto per_sm = [](long long ctas) { return (double)((ctas + 151) / 152); };
-    auto own = [&](long long ctas) { return NK == 1 ? 0.8 + 1.15 * per_sm(ctas) : 5.1 * per_sm(ctas); };
-    auto map = [&](long long ctas) { return NK == 1 ? (1.1 * per_sm(ctas) > 1.6 ? 1.1 * per_sm(ctas) : 1.6) : 4.5 * per_sm(ctas); };
+    auto step = [&](long long ctas, double one, double two, double wide) {
+        const long long n = (ctas + 151) / 152;  // of the fullest SM
+        return NK == 1 ? (double)(n / 2) * two + (double)(n % 2) * one : (double)n * wide;
+    };
+    auto own = [&](long long ctas) { return step(ctas, 1.5, 2.6, 4.5); };
+    auto map = [&](long long ctas) { return step(ctas, 1.3, 2.1, 4.0); };
     Cut best = {NC > 0 ? NC : 1, 1};
     double least = NC * own(BH * NV);
     for (int s = 2; s <= 64 && s * 4 <= NC; ++s) {

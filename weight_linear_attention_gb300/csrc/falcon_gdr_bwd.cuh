@@ -5,7 +5,7 @@
 //   dP_ij = scale D_ij beta_j dO_i.E_j (j <= i),   H_ij = -D_ij beta_j Z_i.E_j (j < i), H symmetric,
 //   dQ = scale diag(e^G) dO S^T + dP K,
 //   dK = dP^T Q + H K - diag(e^G) Z S^T + diag(w beta) E dS'^T,
-//   dbeta_j = E_j.(dU - N^T Z)_j.
+//   dbeta_j = E_j.(dU - N^T Z)_j = E_j.Z_j / beta_j.
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
 // writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
 // from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     // <dS', S'>: a tile of dS' in shared memory against the state's behind the chunk
     float ends = 0.f;
     auto meet = [&](const uint8_t* t, const uint8_t* S1) {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPlane / 16 / kThreads; ++i) {
             float x[8] = {}, y[8] = {};
 #pragma unroll
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         }
     };
     const uint32_t Xs = ONE ? Ws + 2 * kPlane : Ws;
-    const Gates gates = load_gates(a.beta, a.g, b, h, t0, live);
+    const Gates gates = load_gates<true>(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) load_planes(K + kb * PI * kPlane, a.k.row0(b, hk, t0) + kb * kC, a.k.st, live, dk - kb * kC, a.k.vec);
     if (ONE) load_q(W, 0);
@@ -162,8 +162,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         }
     }
     float q1[8][4];                                 // ONE: dO S^T, taken while S is there
-    float sb_[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};  // the rows' dbeta and dV.V
+    float sb_[2] = {0.f, 0.f}, sv[2] = {0.f, 0.f};  // the rows' E.Z and dV.V
+    float back[2];                                  // what takes a gain's substitute out of Z again
     zero(q1);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int row = 16 * rb + ln.r + 8 * hf;
+        const float t = row < live ? a.beta.row0(b, h, t0)[row * a.beta.st] : 0.f;
+        back[hf] = fabsf(t) < kTiny ? t / kTiny : 1.f;
+    }
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
@@ -226,6 +233,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         }
         put_planes<3>(Et + sb * 3 * kPlane, rb, x, ln);
         put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sb_[e >> 1] = fmaf(x[nt][e], z[nt][e], sb_[e >> 1]);  // Z has beta as a factor
+                z[nt][e] *= back[e >> 1];
+            }
         write_rows(a.dv.row0(b, h, t0) + sb * kC, a.dv.st, a.dv.pair, rb, z, ln, rows, live, dv - sb * kC);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
@@ -235,26 +249,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 sv[hf] = fmaf(z[nt][2 * hf], u.x, fmaf(z[nt][2 * hf + 1], u.y, sv[hf]));
             }
         __syncthreads();
-        // N transposed: rows j, columns i > j
-        float N[8][4];
-        zero(N);
-#pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(N, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, rb, 4);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt < 2 * rb) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 16 * rb + ln.r + 8 * (e >> 1), i = 8 * nt + 2 * ln.j + (e & 1);
-                N[nt][e] = j < i ? N[nt][e] * decay(s, i, j) : 0.f;
-            }
-        }
-        zero(z);
-        mmr<3, 3, true, true>(z, N, Zs, ln, rb, 4);
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sb_[e >> 1] = fmaf(x[nt][e], d[nt][e] - z[nt][e], sb_[e >> 1]);
     }
     // dP, its transpose, and H
     float A1[8][4], A3[8][4], H[8][4];
@@ -275,10 +269,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int m = 16 * rb + ln.r + 8 * (e >> 1), n = 8 * nt + 2 * ln.j + (e & 1);
-            const float f = m >= n ? decay(s, m, n) * s.beta[n] : decay(s, n, m) * s.beta[m];
-            A1[nt][e] = m >= n ? A1[nt][e] * f * a.n.scale : 0.f;
+            const bool low = m >= n;
+            const float f = decay(s, low ? m : n, low ? n : m) * s.beta[low ? n : m];
+            A1[nt][e] = low ? A1[nt][e] * f * a.n.scale : 0.f;
             A3[nt][e] = m <= n ? A3[nt][e] * f * a.n.scale : 0.f;
-            H[nt][e] = m == n ? 0.f : (m > n ? H[nt][e] : x[nt][e]) * -f;
+            H[nt][e] = m == n ? 0.f : (low ? H[nt][e] : x[nt][e]) * -f;
         }
     float sq[2] = {0.f, 0.f};
 #pragma unroll 1
@@ -337,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         const int row = 16 * rb + ln.r + 8 * hf;
-        const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]);
+        const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]) / s.beta[row];
         if (ln.j == 0) own[row] = o, dbe[row] = e;
     }
 #pragma unroll
