@@ -195,7 +195,7 @@ int falcon_rms_fwd(const void* x, const void* residual, const float* weight, con
 size_t falcon_rms_bwd_workspace_bytes(const falcon_rms_dims_t* dims) {
     falcon::RmsArgs a = {};
     if (sizes_of(dims, &a) != FALCON_OK || a.B * a.T == 0) return 0;
-    return (size_t)falcon::rms_bwd_splits(a.B * a.T, a.d) * a.d * sizeof(float);
+    return (size_t)falcon::rms_bwd_splits(a.B * a.T, a.d, a.bf16) * a.d * sizeof(float);
 }
 
 int falcon_rms_bwd(const void* h, const float* weight, const int32_t* lengths, const void* dy, const void* dh, void* dx,

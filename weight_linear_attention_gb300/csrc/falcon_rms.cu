@@ -22,7 +22,7 @@ using namespace seq;
 constexpr int kWarps = 4;       // of a CTA whose warps have a token each
 constexpr int kMost = 512;      // threads of a CTA that has one token
 constexpr int kSms = 152;
-constexpr int kSums = 4096;     // bytes: the sums of a token's channels in one warp, 1024 at most
+constexpr int kSums = kWarps * 4096;  // bytes: a warp's sums of a token's channels, 1024 at most
 
 struct Args {
     RmsArgs a;
@@ -276,19 +276,21 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps, MULTI ? 1 : 4) rm
     if (!a.ws) return;
     float* to = a.ws + (long long)blockIdx.x * a.d;
     if (!MULTI) {
-        for (int w = 0; w < kWarps; ++w) {
-            if ((int)(threadIdx.x >> 5) == w) {
+        float* mine = sums + (threadIdx.x >> 5) * a.d;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        const int c = (first + i * step) * W + e;
-                        if (c < a.d) sums[c] = (w > 0 ? sums[c] : 0.f) + acc[i * W + e];
-                    }
+            for (int e = 0; e < W; ++e) {
+                const int c = (first + i * step) * W + e;
+                if (c < a.d) mine[c] = acc[i * W + e];
             }
-            __syncthreads();
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.d; c += 32 * kWarps) {
+            float v = sums[c];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) v += sums[w * a.d + c];
+            to[c] = v;
         }
-        for (int c = threadIdx.x; c < a.d; c += blockDim.x) to[c] = sums[c];
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -347,7 +349,7 @@ int fwd(const Args& g, cudaStream_t s) {
 template <typename E, int W, int N, bool ONE = true>
 int bwd(const Args& g, cudaStream_t s) {
     const int lanes = lanes_of(g.a.d, W * N);
-    const unsigned grid = (unsigned)rms_bwd_splits(g.rows, g.a.d);
+    const unsigned grid = (unsigned)rms_bwd_splits(g.rows, g.a.d, g.a.bf16);
     if constexpr (ONE) {
         if (lanes == 32) return launch_ahead<rms_bwd<E, W, N, false>>(grid, 32 * kWarps, kSums, s, g);
     }
@@ -359,9 +361,11 @@ bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 }  // namespace
 }  // namespace rms
 
-int rms_bwd_splits(long long rows, int d) {
-    // as many CTAs as are resident: 16 warps an SM where a warp has a token; wider tokens have 2 to 16 warps each
-    const long long most = (long long)rms::kSms * (d <= 2048 ? 4 : 2);
+int rms_bwd_splits(long long rows, int d, int bf16) {
+    // as many CTAs as are resident, by the lanes of a token: one warp each, or 2 to 16 (fp32 of 1000 channels, four warps: 45 us
+    // with 4 CTAs an SM, 39 with 6)
+    const int per_sm = bf16 ? (d <= 2048 ? 4 : 2) : d <= 256 ? 4 : d <= 1024 ? 6 : d <= 2048 ? 3 : 2;
+    const long long most = (long long)rms::kSms * per_sm;
     return (int)(rows < most ? rows : most);
 }
 
@@ -394,7 +398,7 @@ int launch_rms_bwd(const RmsArgs& a, cudaStream_t s) {
         st = mid ? bwd<float, 1, 8>(g, s) : wide ? bwd<float, 1, 32, false>(g, s) : bwd<float, 1, 16, false>(g, s);
     }
     if (!a.ws || st != 0) return st;
-    return launch_ahead<rms_sum>((d + 31) / 32, 1024, 0, s, (const float*)a.ws, rms_bwd_splits(g.rows, d), d, a.dweight);
+    return launch_ahead<rms_sum>((d + 31) / 32, 1024, 0, s, (const float*)a.ws, rms_bwd_splits(g.rows, d, a.bf16), d, a.dweight);
 }
 
 }  // namespace falcon

@@ -31,6 +31,6 @@ struct RmsArgs {
 int launch_rms_fwd(const RmsArgs& a, cudaStream_t s);
 int launch_rms_bwd(const RmsArgs& a, cudaStream_t s);
 // CTAs of the backward pass; a function of the sizes alone, so that sums keep their order.
-int rms_bwd_splits(long long rows, int d);
+int rms_bwd_splits(long long rows, int d, int bf16);
 
 }  // namespace falcon
