@@ -691,12 +691,14 @@ __device__ __forceinline__ void put_corner(float* T, int o, int mb, int half, co
         for (int e = 0; e < 4; ++e)
             T[at(o + N + 16 * half + 8 * nt + 2 * ln.j + (e & 1), o + 16 * mb + ln.r + 8 * (e >> 1))] = res[nt][e];
 }
-// All threads; the tile is written and read between barriers of its own.
-__device__ __forceinline__ void invert(float* T, const Lane& ln) {
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+// All threads, w a warp's turn; the tile is written and read between barriers of its own. Two warps have a pair of diagonal
+// blocks each, 16 lanes a block, and the corner between them; four share the last.
+__device__ __forceinline__ void invert(float* T, int w, const Lane& ln) {
+    const int l = threadIdx.x & 31;
+    float res[2][4];
     __syncthreads();
-    {
-        const int o = 16 * w, c = l & 15;
+    if (w < 2) {
+        const int o = 32 * w + (l & 16), c = l & 15;
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -712,17 +714,12 @@ __device__ __forceinline__ void invert(float* T, const Lane& ln) {
             y[i] = (s[0] + s[1]) + (s[2] + s[3]);
         }
         __syncwarp();
-        if (l < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) T[at(o + i, o + c)] = y[i];
-        }
-    }
-    __syncthreads();
-    float res[2][4];
-    if (!(w & 1)) {
-        corner<16>(T, 16 * w, 0, 0, res, ln);
+        for (int i = 0; i < 16; ++i) T[at(o + i, o + c)] = y[i];
         __syncwarp();
-        put_corner<16>(T, 16 * w, 0, 0, res, ln);
+        corner<16>(T, 32 * w, 0, 0, res, ln);
+        __syncwarp();
+        put_corner<16>(T, 32 * w, 0, 0, res, ln);
     }
     __syncthreads();
     corner<32>(T, 0, w & 1, w >> 1, res, ln);
@@ -812,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
         times_decay<false, true>(acc, s, rb, ln, s.beta, 1.f);
         put(T, rb, acc, ln);
     }
-    invert(T, ln);
+    invert(T, rb, ln);
     const long long item = bh * a.n.NC + c;
     float t[8][4];
     get(T, rb, t, ln);
