@@ -374,7 +374,7 @@ typedef struct {
  * and are as well conditioned as the update itself where beta |k|^2 stays below 2 (keys of unit length, a gain
  * below 1). Sums over more than 2^24 log decays' worth are not formed: a chunk's are, in double.
  * T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
- * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or B*H*ceil(T/64) = 2^31.
+ * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or from B*H*ceil(T/64) = 2^27 on with more than 16 tokens.
  */
 int falcon_gdr_fwd(const void* q, const void* k, const void* v, const float* beta, const float* g, const float* S0,
                    const int32_t* lengths, void* out, float* S_final, const falcon_gdr_dims_t* dims,

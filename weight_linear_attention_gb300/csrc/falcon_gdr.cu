@@ -291,9 +291,8 @@ unsigned long long gdr_fwd_workspace(const GdrSizes& n) {
 }
 
 bool gdr_fits(const GdrSizes& n) {
-    const long long BH = n.B * n.H, most = 0x7fffffff;
-    const long long NC = (n.T + gdr::kC - 1) / gdr::kC;
-    return BH <= most / 8 && BH * (NC > 0 ? NC : 1) <= most;
+    const long long BH = n.B * n.H, NC = (n.T + gdr::kC - 1) / gdr::kC;
+    return BH < 1ll << 28 && (n.T <= kGdrStepT || BH * NC < 1ll << 27);
 }
 
 int launch_gdr_fwd(const GdrArgs& a, cudaStream_t s) { return a.n.bf16 ? gdr::launch_fwd<gdr::bf16>(a, s) : gdr::launch_fwd<float>(a, s); }

@@ -760,8 +760,14 @@ struct PrepArgs {
     float *A, *dA;  // dA: backward, what the chunk adds to the adjoint of the state before it
 };
 
+// Whether the inverse keeps a tile of its own: else it leaves its place to Y, its rows, and backward its columns, being in
+// registers (of which fp32's kernel, two CTAs an SM instead of one then, has enough).
+template <typename E, bool BWD>
+__host__ __device__ constexpr bool prep_keeps() { return BWD && sizeof(E) == 2; }
 template <typename E, int NK, bool BWD>
-__host__ __device__ constexpr int prep_smem() { return (NK * planes<E>() + 3 + (BWD ? 2 + (NK + 1) * planes<E>() : 3)) * kPlane; }
+__host__ __device__ constexpr int prep_smem() {
+    return (NK * planes<E>() + 3 + (prep_keeps<E, BWD>() ? 2 : 0) + (BWD ? (NK + 1) * planes<E>() : 3)) * kPlane;
+}
 
 // CTAs that the shared memory of an SM holds, up to `most`: what the registers are to allow.
 __host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
@@ -775,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     __shared__ Scal s;
     uint8_t* K = smem;
     float* T = reinterpret_cast<float*>(K + NK * PI * kPlane);
-    uint8_t* Y = K + (NK * PI + (BWD ? 2 : 0)) * kPlane;  // forward: X, in registers by then, leaves its place
+    constexpr bool KEEPS = prep_keeps<E, BWD>();
+    uint8_t* Y = K + (NK * PI + (KEEPS ? 2 : 0)) * kPlane;
     uint8_t* Q = Y + 3 * kPlane;  // BWD; forward: results on their way out
     uint8_t* dO = Q + NK * PI * kPlane;
     const uint32_t Ks = saddr(K), Ys = saddr(Y), Qs = saddr(Q), Os = saddr(dO);
@@ -814,7 +821,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     float t[8][4];
     get(T, rb, t, ln);
     leave_planes<PX, BWD>(a.X + item * (PX * kPlane), Q, rb, t, ln);
-    if (!BWD) __syncthreads();
+    float tc[8][4];
+    if (BWD && !KEEPS) get_cols(T, rb, tc, ln);
+    if (!KEEPS) __syncthreads();
     const int k1 = rb + 1;  // X's rows end on the diagonal
 #pragma unroll 1
     for (int cb = 0; cb < NK; ++cb) {  // M's columns 64 cb ..
@@ -888,9 +897,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
             __syncthreads();
             put_planes<3>(Y, rb, acc, ln);
             __syncthreads();
-            get_cols(T, rb, P, ln);
+            if (KEEPS) get_cols(T, rb, P, ln);
             zero(acc);
-            mmr<3, 3, true, BWD>(acc, P, Ys, ln, rb, 4);
+            mmr<3, 3, true, BWD>(acc, KEEPS ? P : tc, Ys, ln, rb, 4);
             __syncthreads();
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)

@@ -30,11 +30,14 @@ struct GradArgs {
 };
 
 // K, dO, E, Z and what comes and goes. With one tile of S and dS' (and bf16) all of it is on its way early: S and dS'
-// in E's and Z's places, X and Q in the last; else these come one after the other in three planes.
+// in E's and Z's places, X and Q in the last; else these come one after the other in three planes. So does fp32's dO:
+// 96 KB then let two CTAs of heads up to 64 run on an SM.
+template <typename E>
+__host__ __device__ constexpr bool grad_keeps() { return sizeof(E) == 2; }
 template <typename E, int NK, int NV>
 __host__ __device__ constexpr bool grad_one() { return NK * NV == 1 && sizeof(E) == 2; }
 template <typename E, int NK, int NV>
-__host__ __device__ constexpr int grad_smem() { return ((NK + NV) * planes<E>() + 6 * NV + (grad_one<E, NK, NV>() ? 5 : 3)) * kPlane; }
+__host__ __device__ constexpr int grad_smem() { return ((NK + (grad_keeps<E>() ? NV : 0)) * planes<E>() + 6 * NV + (grad_one<E, NK, NV>() ? 5 : 3)) * kPlane; }
 
 // Summed over the four lanes that hold a row.
 __device__ __forceinline__ float row_sum(float x) {
@@ -44,7 +47,7 @@ __device__ __forceinline__ float row_sum(float x) {
 
 template <typename E, int NK, int NV>
 __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr_grad(const GradArgs<E> a) {
-    constexpr bool ONE = grad_one<E, NK, NV>();
+    constexpr bool ONE = grad_one<E, NK, NV>(), KEEPS = grad_keeps<E>();
     constexpr int PI = planes<E>();
     // planes of operands that reach only dK, rounded to bf16: two where the other has one
     constexpr int PL = sizeof(E) == 2 ? 2 : 3, P1 = sizeof(E) == 2 ? 1 : 3;
@@ -53,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     __shared__ float own[kC], dbe[kC], part[kThreads / 32];
     uint8_t* K = smem;
     uint8_t* dO = K + NK * PI * kPlane;
-    uint8_t* Et = dO + NV * PI * kPlane;
+    uint8_t* Et = dO + (KEEPS ? NV * PI : 0) * kPlane;
     uint8_t* Zt = Et + NV * 3 * kPlane;
     uint8_t* W = Zt + NV * 3 * kPlane;
     const uint32_t Ks = saddr(K), Os = saddr(dO), Es0 = saddr(Et), Zs0 = saddr(Zt), Ws = saddr(W);
@@ -121,6 +124,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             for (int e = 0; e < 8; ++e) ends = fmaf(x[e], y[e], ends);
         }
     };
+    // dO's tile sb, where it is or brought
+    auto adjoint = [&](int sb) {
+        if (KEEPS) return Os + sb * PI * kPlane;
+        __syncthreads();
+        load_planes(W, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
+        commit();
+        wait<0>();
+        __syncthreads();
+        return Ws;
+    };
     const uint32_t Xs = ONE ? Ws + 2 * kPlane : Ws;
     const Gates gates = load_gates<true>(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
@@ -128,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     if (ONE) load_q(W, 0);
     commit();
 #pragma unroll 1
-    for (int sb = 0; sb < NV; ++sb) load_planes(dO + sb * PI * kPlane, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
+    for (int sb = 0; KEEPS && sb < NV; ++sb) load_planes(dO + sb * PI * kPlane, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, live, dv - sb * kC, a.dout.vec);
     if (ONE) {
         copy_planes<3>(Es0, St);
         copy_planes<3>(Zs0, dSt);
@@ -173,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     }
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
-        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
+        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane;
         Rows<E> v;
         load_rows(v, a.v.row0(b, h, t0) + sb * kC, a.v.st, a.v.pair, rb, ln, live, dv - sb * kC);
         zero(x);
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             wait<0>();
             __syncthreads();
             mm<PI, 3, false, false>(x, Ks, rb, Es, ln);
-            mm<PI, 3, false, true>(q1, Ob, rb, Es, ln);
+            mm<PI, 3, false, true>(q1, Os, rb, Es, ln);
             mm<PI, 3, false, false>(d, Ks, rb, Zs, ln);
             meet(Zt, St + st);
         } else {
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<3, PI, true, true>(d, P, Ob, ln, rb, 4);  // dU
+        mmr<3, PI, true, true>(d, P, adjoint(sb), ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const float eG = s.eG[16 * rb + ln.r + 8 * hf];
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     zero(x);
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
-        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = Os + sb * PI * kPlane;
+        const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = adjoint(sb);
         mm<PI, 3, false, false>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
         mm<PL, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
         mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
@@ -294,8 +307,19 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             zero(x);
 #pragma unroll 1
             for (int sb = 0; sb < NV; ++sb) {
+                Rows<E> o;
+                if (!KEEPS) load_rows(o, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, a.dout.pair, rb, ln, live, dv - sb * kC);
                 bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
-                mm<PI, 3, false, true>(x, Os + sb * PI * kPlane, rb, Ws, ln);
+                if (KEEPS) {
+                    mm<PI, 3, false, true>(x, Os + sb * PI * kPlane, rb, Ws, ln);
+                } else {
+                    float f[8][4];
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
+                    mmr<3, 3, true, true>(x, f, Ws, ln);
+                }
                 mm<PL, PL, false, true>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
                 bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
                 mm<PL, PL, false, true>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
@@ -373,21 +397,28 @@ __global__ void __launch_bounds__(256) gdr_sum(const SumArgs<E> a, const SumArgs
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const SumArgs<E>& p = blockIdx.y ? a2 : a;
-    const int l = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const unsigned per = (p.dk + 3) / 4;  // of four channels, a thread each
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x, row = id / per;
     if (row >= p.count) return;
-    const long long bk = row / p.T, t = row % p.T;
-    const float* src = p.part + (bk * p.group * p.T + t) * p.dk;
-    E* dst = p.to.row0(bk / p.Hk, bk % p.Hk, t);
-    for (int i = 2 * l; i < p.dk; i += 64) {
-        float2 s = make_float2(0.f, 0.f);
-        for (int m = 0; m < p.group; ++m) {
-            const float2 v = load2(src + (long long)m * p.T * p.dk + i, p.dk - i, p.dk % 2 == 0);
-            s.x += v.x;
-            s.y += v.y;
+    const int i = 4 * (int)(id % per), left = p.dk - i;
+    const long long bk = row / p.T, t = row % p.T, next = (long long)p.T * p.dk;
+    const float* src = p.part + (bk * p.group * p.T + t) * p.dk + i;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool vec = p.dk % 4 == 0;
+#pragma unroll 4
+    for (int m = 0; m < p.group; ++m, src += next) {
+        if (vec) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) s[e] += src[e];
         }
-        store2(dst + i, s.x, s.y, p.dk - i, p.to.pair);
     }
+    E* dst = p.to.row0(bk / p.Hk, bk % p.Hk, t) + i;
+    store2(dst, s[0], s[1], left, p.to.pair);
+    store2(dst + 2, s[2], s[3], left - 2, p.to.pair);
 }
 
 template <typename E, int NK>
@@ -432,7 +463,7 @@ int launch_bwd(const GdrArgs& a, cudaStream_t st) {
         SumArgs<E> q = {g.pq, g.dq, a.n.B * a.n.Hk * a.n.T, (int)a.n.Hk, n.group, a.n.T, a.n.dk}, k = q;
         k.part = g.pk;
         k.to = g.dk;
-        r |= launch_ahead<gdr_sum<E>>(dim3((unsigned)((q.count + 7) / 8), 2), 256, 0, st, q, k);
+        r |= launch_ahead<gdr_sum<E>>(dim3((unsigned)((q.count * ((a.n.dk + 3) / 4) + 255) / 256), 2), 256, 0, st, q, k);
     }
     return r;
 }
