@@ -360,7 +360,8 @@ typedef struct {
  *   S_t = a_t S_{t-1} + k_t (beta_t (v_t - a_t S_{t-1}^T k_t))^T,   out_t = scale S_t^T q_t.
  *   q, k      [B,Hk,T,dk] dtype
  *   v, out    [B,H,T,dv] dtype
- *   beta, g   fp32 [B,H,T]            gain, and log decay (-inf forgets all before its token)
+ *   beta, g   fp32 [B,H,T]            gain, and log decay (-inf forgets all before its token; above 0 it is taken as
+ *                                     it is, and where products of 64 tokens' decays overflow results are inf or NaN)
  *   S0        fp32 [B,H,dk,dv] or NULL (zero state)
  *   S_final   fp32 [B,H,dk,dv] or NULL: the state behind each sequence's last token (S0 when it has none);
  *             may be the same pointer as S0
@@ -372,7 +373,7 @@ typedef struct {
  * Up to 16 tokens are walked one by one, in fp32. Longer sequences go in chunks of 64, whose maps of the state are
  * formed first: their products, (I + N diag(beta))^-1 with N_ij = e^{..} k_i.k_j among them, have fp32's precision,
  * and are as well conditioned as the update itself where beta |k|^2 stays below 2 (keys of unit length, a gain
- * below 1). Sums over more than 2^24 log decays' worth are not formed: a chunk's are, in double.
+ * below 1). From bf16 inputs the output's operands have 16 bits, the state's 24. Where B*H is 0 nothing is written.
  * T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
  * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or from B*H*ceil(T/64) = 2^27 on with more than 16 tokens.
  */

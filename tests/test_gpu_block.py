@@ -244,6 +244,38 @@ def test_gdr_nan_stays_in_its_head_and_behind_its_token(T):
     assert not torch.isnan(S[0, ::2]).any() and not torch.isnan(out[0, ::2]).any()
 
 
+def test_gdr_without_tokens():
+    """No tokens, or none in any sequence: the states pass through."""
+    p, a = inputs(2, 3, 0, 40, 64, torch.bfloat16, 27)
+    out, S = F.gdr_forward(*(p[n].cuda() for n in ("q", "k", "v", "beta", "g")), p["S0"].cuda())
+    assert out.shape == (2, 3, 0, 64) and torch.equal(S.cpu(), p["S0"])
+    got = F.gdr_backward(*(p[n].cuda() for n in ("q", "k", "v", "beta", "g")), a["dout"].cuda(), p["S0"].cuda(), a["dS_final"].cuda())
+    assert torch.equal(got["dS0"].cpu(), a["dS_final"]) and got["dq"].shape == (2, 3, 0, 40)
+    p, a = inputs(2, 2, 100, 64, 64, torch.float32, 28, Hk=1)
+    n = torch.zeros(2, dtype=torch.int32)
+    out, S = forward(p, n)
+    assert not out.any() and torch.equal(S.cpu(), p["S0"])
+    got = backward(p, a, n)
+    assert torch.equal(got["dS0"].cpu(), a["dS_final"])
+    assert not any(got[x].any() for x in ("dq", "dk", "dv", "dbeta", "dg"))
+
+
+def test_gdr_gains_of_every_size():
+    """dbeta is formed from what has the gain as a factor: gains from 0 through 1e-30 and 1e-12 to 1, and below 0."""
+    p, a = inputs(1, 2, 100, 64, 64, torch.float32, 29)
+    p["beta"][0, 0] = torch.logspace(-38, 0, 100)
+    p["beta"][0, 1, ::2] *= -1
+    out, S = forward(p)
+    check_forward(out, S, p)
+    got = backward(p, a)
+    check_backward(got, p, a)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    # each token's own: rows of dv carry their gain, however small
+    for t in range(100):
+        check(f"dv of token {t}", got["dv"][:, :1, t:t + 1], want["dv"][:, :1, t:t + 1], 4 * R.GDR)
+        check(f"dbeta of token {t}", got["dbeta"][:, :1, t:t + 1, None], want["dbeta"][:, :1, t:t + 1, None], 40 * R.GDR)
+
+
 def test_gdr_scale():
     p, a = inputs(1, 2, 70, 64, 64, torch.float32, 12)
     for scale in (1.0, 0.0, -2.5):

@@ -1,5 +1,5 @@
-// Device code that the gated delta rule's chunk kernels share: 64 x 64 fp32 tiles in shared memory, products of
-// them in three tf32 passes, a chunk's decays, and the kernels of the chunk maps and of the scan over them.
+// Device code that the gated delta rule's kernels share: tiles of 64 x 64, their products on the tensor cores, a chunk's
+// decays, the inverse of a triangle, and the kernels of the chunk maps and of the scan over them.
 //
 // Per head, S [dk, dv]: S_t = a_t S_{t-1} + k_t (beta_t (v_t - a_t S_{t-1}^T k_t))^T, a_t = e^{g_t}. In a chunk of
 // 64 tokens (rows i, j), G_i the sum of its log decays up to i, S the state before it, D_ij = e^{G_i - G_j}:
@@ -10,11 +10,15 @@
 // So S' = M S + A with M = e^{G_C} I - K^T diag(w beta) X diag(e^G) K and A = K^T diag(w beta) X V: the chunk
 // kernels run for all chunks at once, and only S' = M S + A goes along the sequence.
 //
-// Products: an fp32 operand x enters as bf16 planes, x = h + m + l (each the nearest bf16 of what the ones before
-// leave: 24 bits), and a product of two as h h + h m + m h + m m + h l + l h with fp32 sums, what is left out being
-// below 2^-24 of it; with two planes as h h + h m + m h (2^-16). bf16 inputs are their own single plane. An operand is
-// split once, where it is made, and the warps' products are loads of matrices and nothing else. (As tf32 pairs, split by
-// every warp that reads them, the same products took 2.2 to 3 times as long.)
+// Products: an fp32 operand x enters as bf16 planes of 8 bits each, x = h + m + l, and a product of two as h h + h m +
+// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it; with two planes as h h + h m +
+// m h (2^-16). bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
+// loads of matrices and nothing else. (As tf32 pairs, split by every warp that reads them, the gradient kernel took 306 us
+// for 8 x 12 x 1024 x 64, so 246.)
+// They are mma.sync products. A chunk is a row of dependent ones of 64 x 64 x 64 with its own arithmetic between them, and
+// what follows a product finds its result in registers; no pipe is busy more than half of the time, the tensor cores 30 %.
+// On tcgen05, results in tensor memory, the chunk kernels of Falcon-1's backward do the same work with two planes an
+// operand in 89 and 117 ns a chunk (the map, the gradients); these take 66 and 107.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -488,7 +492,7 @@ __device__ __forceinline__ void write_rows(E* p, long long st, bool pair, int rb
 }
 
 // ---- a chunk's gains and decays. Sums of log decays are pairs of floats, hi + lo, 48 bits: a difference of two, at whatever
-// size, keeps fp32's relative precision. (In double, whose units are few, this took 10 us of a chunk's 18.)
+// size, keeps fp32's relative precision. (In double, whose units are few, this took 10,900 of a chunk's 36,600 cycles.)
 struct Scal {
     float beta[kC], hi[kC], lo[kC];  // (backward: no gain below kTiny), G / ln 2 = hi + lo
     float eG[kC], w[kC], bw[kC];     // e^G, e^{G_C - G}, beta w
@@ -589,6 +593,8 @@ __device__ __forceinline__ void make_scal(Scal& s, const Gates& r) {
     }
 }
 
+// (The far blocks so, and not by exponentials, save the chunk maps' kernel 2 us of 54 and the outputs' 2 of 38; the gradients'
+// kernel, which waits for its instructions, does better with fewer of them: 211 us against 241.)
 // A product's rows times D, and times f of the column (of the row, UPPER) or f itself: rows i and columns j <= i, or rows
 // j and columns i >= j (UPPER), STRICT without the diagonal; 0 elsewhere.
 template <bool UPPER, bool STRICT>
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
     const long long bh = ubh, b = ub, h = uh, hk = uh / (unsigned)a.n.group;
     const int c = (int)(blockIdx.x % (unsigned)a.n.NC);
     // what the grids before this one wrote may be read from here on; the scan behind it is not let in early, or its few
-    // CTAs share the first SMs that are free (144 us a forward call against 125)
+    // CTAs share the first SMs that are free (144 us a forward call against 121)
     ptx::pdl_wait();
     const int live = min(kC, length_of(a.n, b) - c * kC);
     if (live <= 0) return;

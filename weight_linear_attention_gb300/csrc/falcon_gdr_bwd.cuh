@@ -9,7 +9,8 @@
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
 // writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
 // from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
-// gdr_grad takes the gradients, all chunks at once.
+// gdr_grad takes the gradients, all chunks at once: 18 products a chunk, two CTAs an SM (of their operands' 104 KB), bound
+// by latency and by fetching its own instructions (8 x 12 x 1024 x 64 bf16: maps 102, scans 45, gradients 164 us).
 
 #pragma once
 

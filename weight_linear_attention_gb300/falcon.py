@@ -771,7 +771,7 @@ def _gdr_sizes(q, v):
         raise ValueError(f"unsupported dtype {dtype}: float32 or bfloat16")
     B, Hk, T, dk = q.shape
     H, dv = v.shape[1], v.shape[3]
-    if H > 0 and (Hk == 0 or H % Hk):
+    if Hk != H and (Hk == 0 or H == 0 or H % Hk):
         raise ValueError(f"the heads of q and k must divide those of v, got {Hk} and {H}")
     return index, dtype, B, H, Hk, T, dk, dv, _PACK_GDR(B, H, Hk, T, dk, dv, code, 0)
 
