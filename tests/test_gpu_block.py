@@ -104,7 +104,7 @@ def check_backward(got, p, a, lengths=None, scale=None):
             check(name, g, w, R.GDR_BF16_DK if name == "dk" and dt != torch.float32 else R.GDR, dt)
 
 
-SIZES = [(1, 1, 1, 64, 64), (2, 3, 1, 33, 40), (1, 2, 16, 128, 128), (2, 2, 17, 64, 64), (1, 1, 63, 16, 16),
+SIZES = [(1, 1, 1, 64, 64), (2, 3, 1, 33, 40), (1, 2, 16, 128, 128), (2, 2, 17, 64, 64), (2, 1, 32, 64, 64), (1, 2, 33, 64, 64), (1, 1, 63, 16, 16),
          (2, 1, 64, 64, 64), (1, 3, 65, 64, 64), (1, 2, 128, 1, 1), (2, 2, 200, 40, 100), (1, 2, 130, 128, 64),
          (1, 2, 130, 64, 128), (1, 1, 300, 128, 128), (1, 2, 129, 65, 65), (3, 1, 90, 7, 3)]
 
@@ -188,7 +188,7 @@ def test_gdr_continues_from_its_state(dt):
     cut = lambda a, b: {n: (t[:, :, a:b] if n != "S0" else t) for n, t in p.items()}  # noqa: E731
     S = p["S0"].cuda()
     outs, at = [], 0
-    for n in (70, 1, 1, 5, 16, 7):
+    for n in (50, 1, 1, 5, 33, 10):
         q = cut(at, at + n)
         o, s = F.gdr_forward(*(q[x].cuda() for x in ("q", "k", "v", "beta", "g")), S, S_final=S)
         assert s is S
@@ -342,7 +342,7 @@ def test_gdr_offsets_past_32_bits():
 def test_gdr_many_sequences():
     p, a = inputs(700, 3, 2, 16, 16, torch.bfloat16, 16)
     check_forward(*forward(p), p)
-    p, a = inputs(300, 2, 20, 16, 16, torch.bfloat16, 17)
+    p, a = inputs(300, 2, 40, 16, 16, torch.bfloat16, 17)
     check_forward(*forward(p), p)
     check_backward(backward(p, a), p, a)
 
@@ -655,7 +655,7 @@ def test_two_host_threads():
 
 
 def test_wrappers_refuse():
-    p, a = inputs(1, 2, 20, 16, 16, torch.bfloat16, 26)
+    p, a = inputs(1, 2, 40, 16, 16, torch.bfloat16, 26)
     d = {n: t.cuda() for n, t in p.items()}
     ok = [d[n] for n in ("q", "k", "v", "beta", "g")]
 
@@ -675,7 +675,7 @@ def test_wrappers_refuse():
         F.gdr_forward(*ok, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(F.FalconError):
         F.gdr_forward(*ok, scale=math.inf)
-    three = torch.zeros(1, 3, 20, 16, dtype=torch.bfloat16, device="cuda")
+    three = torch.zeros(1, 3, 40, 16, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError, match="divide"):
         F.gdr_forward(d["q"], d["k"], three, ok[3], ok[4])
     x = torch.zeros(2, 4, 32, device="cuda")

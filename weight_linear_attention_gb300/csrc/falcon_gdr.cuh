@@ -97,10 +97,12 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&p)[N]) {
     }
 }
 
-// Which products of planes: all of them, or those below the first two's, or theirs alone. The tensor cores cut sums off, a
+// Which products of planes: all of them, or those below the first two's, or theirs alone, or first the ones and then the other. The tensor cores cut sums off, a
 // unit at a time: of fp32 operands the small products of all k steps come first, while the sums are small, and leave four
-// cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm instead of 6e-7).
-enum { kAll = 0, kSmall = 1, kGreat = 2 };
+// cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm instead of 6e-7). kOrdered: so for other
+// operands, too, where a product goes into dg, in which what it is made of cancels (5e-7 instead of 1e-6; 4 % of the
+// gradients' kernel).
+enum { kAll = 0, kSmall = 1, kGreat = 2, kOrdered = 3 };
 
 // One k step of 16: acc (16 rows x 64 columns, column groups of 16 in [p0, p1)) += a B. B, its planes at `b`, is stored
 // [n][k], or [k][n] (BCOL).
@@ -137,7 +139,7 @@ __device__ __forceinline__ void step(float (&acc)[8][4], const uint32_t (&a)[PA]
 template <int PA, int PB, bool ACOL, bool BCOL, int WHICH = kAll>
 __device__ __forceinline__ void mm(float (&acc)[8][4], uint32_t A, int rb, uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4,
                                    int p0 = 0, int p1 = 4) {
-    if constexpr (PA * PB == 9 && WHICH == kAll) {
+    if constexpr ((PA * PB == 9 && WHICH == kAll) || WHICH == kOrdered) {
         mm<PA, PB, ACOL, BCOL, kSmall>(acc, A, rb, B, ln, k0, k1, p0, p1);
         mm<PA, PB, ACOL, BCOL, kGreat>(acc, A, rb, B, ln, k0, k1, p0, p1);
         return;
@@ -170,7 +172,7 @@ __device__ __forceinline__ void split_a(uint32_t (&a)[PA][4], const float (&x)[2
 // the forward's are shorter and lose 5 % by it).
 template <int PA, int PB, bool BCOL, bool ROLL = false, int WHICH = kAll>
 __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4) {
-    if constexpr (PA * PB == 9 && WHICH == kAll) {
+    if constexpr ((PA * PB == 9 && WHICH == kAll) || WHICH == kOrdered) {
         mmr<PA, PB, BCOL, ROLL, kSmall>(acc, A, B, ln, k0, k1);
         mmr<PA, PB, BCOL, ROLL, kGreat>(acc, A, B, ln, k0, k1);
         return;

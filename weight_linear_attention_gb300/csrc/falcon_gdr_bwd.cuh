@@ -195,17 +195,17 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         if (ONE) {
             wait<0>();
             __syncthreads();
-            mm<PI, 3, false, false>(x, Ks, rb, Es, ln);
-            mm<PI, 3, false, true>(q1, Os, rb, Es, ln);
-            mm<PI, 3, false, false>(d, Ks, rb, Zs, ln);
+            mm<PI, 3, false, false, kOrdered>(x, Ks, rb, Es, ln);
+            mm<PI, 3, false, true, kOrdered>(q1, Os, rb, Es, ln);
+            mm<PI, 3, false, false, kOrdered>(d, Ks, rb, Zs, ln);
             meet(Zt, St + st);
         } else {
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
                 bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
-                mm<PI, 3, false, false>(x, Ks + kb * PI * kPlane, rb, Ws, ln);
+                mm<PI, 3, false, false, kOrdered>(x, Ks + kb * PI * kPlane, rb, Ws, ln);
                 bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
-                mm<PI, 3, false, false>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
+                mm<PI, 3, false, false, kOrdered>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
                 meet(W, St + st + (sb * NK + kb) * (3 * kPlane));
             }
         }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<3, PI, true, true>(d, P, adjoint(sb), ln, rb, 4);  // dU
+        mmr<3, PI, true, true, kOrdered>(d, P, adjoint(sb), ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const float eG = s.eG[16 * rb + ln.r + 8 * hf];
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = adjoint(sb);
-        mm<PI, 3, false, false>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
+        mm<PI, 3, false, false, kOrdered>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
         mm<PL, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
         mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
         mm<PL, PL, false, false>(x, Es, rb, Zs, ln, 0, 4, rb, 4);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 if (!KEEPS) load_rows(o, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, a.dout.pair, rb, ln, live, dv - sb * kC);
                 bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
                 if (KEEPS) {
-                    mm<PI, 3, false, true>(x, Os + sb * PI * kPlane, rb, Ws, ln);
+                    mm<PI, 3, false, true, kOrdered>(x, Os + sb * PI * kPlane, rb, Ws, ln);
                 } else {
                     float f[8][4];
 #pragma unroll
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 x[nt][e] *= s.eG[row] * a.n.scale;
                 d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
             }
-        mmr<3, PI, true, true>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
+        mmr<3, PI, true, true, kOrdered>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
         write_qk(a.dq, a.pq, x, kb);
         mmr<PL, P1, true, true>(d, H, Ks + kb * PI * kPlane, ln);
         uint8_t* Qt = ONE ? W + 4 * kPlane : W;

@@ -180,9 +180,12 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Arg
             }
         } else {
             reduce<MULTI, true>(top, slots[turn][1]);
-            const float scale = now.live ? top[0] * (1.f / 448.f) : 0.f;
+            const float near = top[0] * (1.f / 448.f);
+            const float exact = near < 3.4e38f ? fmaf(fmaf(-near, 448.f, top[0]), 1.f / 448.f, near) : near;  // its last bit
+            const float scale = now.live ? exact : 0.f;
             if (first == 0) a.scales[here] = scale;
-            // 1 / scale where it is not near overflow (NaN too), else the quotients themselves; a row of zeros stays 0
+            // 1 / scale where it is not near overflow (NaN too), else the quotients themselves; a row of zeros stays 0. (The
+            // quotients everywhere, 89 us for 16384 x 4096 against 80, meet the nearest value as often.)
             const bool tiny = scale < 1e-37f;
             const float inv = tiny ? 0.f : 1.f / scale;
 #pragma unroll

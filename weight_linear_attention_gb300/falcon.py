@@ -787,7 +787,7 @@ def gdr_forward(q, k, v, beta, g, S0=None, *, scale=None, lengths=None, out=None
     or None (zero). scale: dk ** -0.5 unless given. lengths: int32 [B] or None; rows behind them come back as zeros.
     out (a [B,H,T,dv] view) and S_final (may be S0: updated in place) are written where given; out is else allocated
     in the output projection's layout, a view of a dense [B,T,H,dv]. workspace: uint8 of falcon_gdr_workspace_bytes,
-    allocated unless given (up to 16 tokens need none). stream: as for glr_forward."""
+    allocated unless given (up to 32 tokens need none). stream: as for glr_forward."""
     index, dtype, B, H, Hk, T, dk, dv, dims = _gdr_sizes(q, v)
     t = _t()
     if out is None:
