@@ -20,6 +20,38 @@ struct OutArgs {
     const uint8_t *X, *S;
 };
 
+// acc += K S and o += Q S (S stored [n][k]): S is fetched once.
+template <int PA, int PB>
+__device__ __forceinline__ void mm_both(float (&acc)[8][4], float (&o)[8][4], uint32_t K, uint32_t Q, int rb, uint32_t S, const Lane& ln) {
+#pragma unroll 1
+    for (int kk = 0; kk < 4; ++kk) {
+        uint32_t a[PA][4], q[PA][4];
+        const uint32_t at = (16 * rb + ln.l7 + 8 * ln.l8) * 128 + (((2 * kk + ln.l16) ^ ln.l7) << 4);
+#pragma unroll
+        for (int m = 0; m < PA; ++m) {
+            ldm<false>(a[m], K + at + m * kPlane);
+            ldm<false>(q[m], Q + at + m * kPlane);
+        }
+        const uint32_t row = S + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t v[PB][4];
+#pragma unroll
+            for (int m = 0; m < PB; ++m) ldm<false>(v[m], row + m * kPlane + p * 2048);
+#pragma unroll
+            for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
+#pragma unroll
+                for (int ma = 0; ma < PA; ++ma) {
+                    if (s < ma || s - ma >= PB) continue;
+                    mma(acc[2 * p], a[ma], v[s - ma][0], v[s - ma][1]);
+                    mma(acc[2 * p + 1], a[ma], v[s - ma][2], v[s - ma][3]);
+                    mma(o[2 * p], q[ma], v[s - ma][0], v[s - ma][1]);
+                    mma(o[2 * p + 1], q[ma], v[s - ma][2], v[s - ma][3]);
+                }
+        }
+    }
+}
+
 template <typename E, int NK>
 __host__ __device__ constexpr int out_smem() { return (2 * NK * planes<E>() + 2 * state_planes<E, false>()) * kPlane; }
 
@@ -85,8 +117,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
             }
             wait<0>();
             __syncthreads();
-            mm<PI, PS, false, false>(acc, Ks + kb * PI * kPlane, rb, Ws, ln);
-            mm<PI, PS, false, false>(o, Qs + kb * PI * kPlane, rb, Ws, ln);
+            mm_both<PI, PS>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
         }
         __syncthreads();
 #pragma unroll

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(1024) rms_sum(const float* part, int splits, i
     const int l = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
     float v = 0.f;
     if (c < d) {
-#pragma unroll 8
+#pragma unroll 16
         for (int i = w; i < splits; i += 32) v += part[(long long)i * d + c];
     }
     s[l][w] = v;
