@@ -675,6 +675,9 @@ def test_wrappers_refuse():
         F.gdr_forward(*ok, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(F.FalconError):
         F.gdr_forward(*ok, scale=math.inf)
+    for args in (swapped(2, d["v"][..., :0]), [t[..., :0] if t.dim() == 4 else t for t in ok]):
+        with pytest.raises(ValueError, match="channels"):
+            F.gdr_forward(*args)
     three = torch.zeros(1, 3, 40, 16, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError, match="divide"):
         F.gdr_forward(d["q"], d["k"], three, ok[3], ok[4])

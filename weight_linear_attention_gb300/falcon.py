@@ -773,6 +773,8 @@ def _gdr_sizes(q, v):
     H, dv = v.shape[1], v.shape[3]
     if Hk != H and (Hk == 0 or H == 0 or H % Hk):
         raise ValueError(f"the heads of q and k must divide those of v, got {Hk} and {H}")
+    if dk == 0 or dv == 0:
+        raise ValueError(f"q and v must have channels, got {tuple(q.shape)} and {tuple(v.shape)}")
     return index, dtype, B, H, Hk, T, dk, dv, _PACK_GDR(B, H, Hk, T, dk, dv, code, 0)
 
 
