@@ -276,6 +276,34 @@ def test_gdr_gains_of_every_size():
         check(f"dbeta of token {t}", got["dbeta"][:, :1, t:t + 1, None], want["dbeta"][:, :1, t:t + 1, None], 40 * R.GDR)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("gain", [1.0, 1.9])
+def test_gdr_one_key_for_all_tokens(dt, gain):
+    """Every token writes where the one before it wrote: the triangle is full, its inverse's signs alternate."""
+    p, a = inputs(1, 2, 200, 64, 64, DT[dt], 30)
+    p["k"] = torch.zeros_like(p["k"])
+    p["k"][..., 5] = 1.0
+    p["beta"] = torch.full_like(p["beta"], gain)
+    p["g"] = torch.full_like(p["g"], -1e-3)
+    out, S = forward(p)
+    check_forward(out, S, p)
+    check_backward(backward(p, a), p, a)
+
+
+@pytest.mark.parametrize("T", [20, 70])
+def test_gdr_strong_decays(T):
+    """Decays that leave e^-6 of a state: dg is small beside the sums it comes from."""
+    p, a = inputs(2, 2, T, 64, 64, torch.float32, 31)
+    p["g"] = torch.full_like(p["g"], -6.0)
+    out, S = forward(p)
+    check_forward(out, S, p)
+    got = backward(p, a)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    terms = (want["dq"] * p["q"]).sum(-1).abs() + (want["dv"] * p["v"]).sum(-1).abs()
+    off = (got["dg"].cpu().double() - want["dg"]).norm(dim=-1)
+    assert (off <= R.GDR * terms.norm(dim=-1)).all()
+
+
 def test_gdr_scale():
     p, a = inputs(1, 2, 70, 64, 64, torch.float32, 12)
     for scale in (1.0, 0.0, -2.5):
@@ -630,6 +658,37 @@ def test_side_streams_at_the_same_time():
     for g in got:
         for u, v in zip(g.values(), want):
             assert torch.equal(u, v)
+
+
+PENDING = 40_000_000  # cycles of a kernel that does nothing, some 20 ms
+
+
+def test_memory_belongs_to_the_given_stream():
+    """The current stream allocates and writes while a call on another stream still waits: what the call allocated, its
+    workspace too, is not among it."""
+    p, a = inputs(2, 2, 300, 64, 64, torch.bfloat16, 27)
+    dev, da = ({n: t.cuda() for n, t in x.items()} for x in (p, a))
+    ok = [dev[n] for n in ("q", "k", "v", "beta", "g")]
+    x, w = torch.randn(2000, 200, device="cuda"), torch.randn(200, device="cuda")
+
+    def calls(stream):
+        out = [*F.gdr_forward(*ok, dev["S0"], stream=stream)]
+        out += F.gdr_backward(*ok, da["dout"], dev["S0"], da["dS_final"], stream=stream).values()
+        out += F.rmsnorm_forward(x, w, x, out_dtype=E4M3, stream=stream)
+        return out + [*F.rmsnorm_backward(x, x, w, x, stream=stream).values()]
+
+    want = calls(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):  # the second time from memory that the first gave back
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(PENDING)
+        got = calls(side)
+        over = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in (1 << k for k in range(9, 25)) for _ in range(4)]
+        torch.cuda.synchronize()
+        for u, v in zip(got, want):
+            assert torch.equal(u.float(), v.float())
+        del got, over
 
 
 def test_two_host_threads():

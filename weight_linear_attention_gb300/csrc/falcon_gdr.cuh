@@ -777,9 +777,10 @@ __host__ __device__ constexpr int prep_smem() {
     return (NK * planes<E>() + 3 + (prep_keeps<E, BWD>() ? 2 : 0) + (BWD ? (NK + 1) * planes<E>() : 3)) * kPlane;
 }
 
-// CTAs that the shared memory of an SM holds, up to `most`: what the registers are to allow.
+// CTAs that the shared memory of an SM holds, up to `most`: what the registers are to allow. 3 KiB a CTA are for its
+// static arrays and what the system keeps.
 __host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
-    return 226 * 1024 / (smem + 3072) < most ? 226 * 1024 / (smem + 3072) : most;
+    return 226 * 1024 / (smem + 3 * 1024) < most ? 226 * 1024 / (smem + 3 * 1024) : most;
 }
 
 template <typename E, int NK, bool BWD>
