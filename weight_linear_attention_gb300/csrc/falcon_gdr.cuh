@@ -301,14 +301,28 @@ __device__ __forceinline__ void get_planes(const uint8_t* T, int rb, float (&acc
 }
 
 // ---- asynchronous copies
-// A warp's 16 rows of a result into the workspace: by bulk copies of 2 or 4 KB from its own rows of a tile in shared memory,
-// or, DIRECT, as they lie in registers, a quarter of eight lines an instruction. The copies need the tile: with wide heads
-// they save the forward 8 %; the backward's kernel, which has no room for it beside a third CTA, loses 15 % by it.
+// A warp's 16 rows of a result into the workspace: by bulk copies from a place in shared memory, or, DIRECT, as they lie in
+// registers, a quarter of eight lines an instruction. The copies need the place: with wide heads they save the forward 8 %;
+// the backward's kernel, which has no room for it beside a third CTA, loses 15 % by it.
+// A copy still reads its place when the warp goes on, and only the thread that sent it can wait for that. So a warp's
+// pieces are its own whatever they hold, rows of a plane or half of its rows of an fp32 tile, and no barrier is needed for them.
+constexpr int kPiece = 2048, kPieces = 3;
+__host__ __device__ constexpr int piece(int rb, int i) { return i * kPlane + rb * kPiece; }
+constexpr bool pieces_apart() {
+    for (int a = 0; a < 4 * kPieces; ++a)
+        for (int b = 0; b < a; ++b) {
+            const int x = piece(a & 3, a >> 2), y = piece(b & 3, b >> 2);
+            if (x < y + kPiece && y < x + kPiece) return false;
+        }
+    return true;
+}
+static_assert(pieces_apart() && piece(3, kPieces - 1) + kPiece <= kPieces * kPlane && 2 * kPiece == 16 * kC * 4, "stages overlap");
 __device__ __forceinline__ void bulk_out(void* dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 template <int N, bool DIRECT>
 __device__ __forceinline__ void leave_planes(uint8_t* dst, uint8_t* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
+    static_assert(N <= kPieces, "pieces of a stage");
     if (DIRECT) return put_planes<N>(dst, rb, acc, ln);
     if (ln.r + ln.j == 0) ptx::bulk_wait_read<0>();  // what these rows held before has left
     __syncwarp();
@@ -317,20 +331,27 @@ __device__ __forceinline__ void leave_planes(uint8_t* dst, uint8_t* stage, int r
     __syncwarp();
     if (ln.r + ln.j == 0) {
 #pragma unroll
-        for (int m = 0; m < N; ++m) bulk_out(dst + m * kPlane + rb * 2048, saddr(stage) + m * kPlane + rb * 2048, 2048);
+        for (int m = 0; m < N; ++m) bulk_out(dst + m * kPlane + rb * kPiece, saddr(stage) + piece(rb, m), kPiece);
         ptx::bulk_commit();
     }
 }
 template <bool DIRECT>
-__device__ __forceinline__ void leave_tile(float* dst, float* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
+__device__ __forceinline__ void leave_tile(float* dst, uint8_t* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
     if (DIRECT) return put(dst, rb, acc, ln);
     if (ln.r + ln.j == 0) ptx::bulk_wait_read<0>();
     __syncwarp();
-    put(stage, rb, acc, ln);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // rows 8 h .. 8 h + 7 of the 16
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            float* p = reinterpret_cast<float*>(stage + piece(rb, h)) + ln.r * kC + (((nt & 3) ^ ln.fr) << 3) + ((nt >> 2) << 5) + 2 * ln.j;
+            *reinterpret_cast<float2*>(p) = make_float2(acc[nt][2 * h], acc[nt][2 * h + 1]);
+        }
     ptx::fence_async_smem();
     __syncwarp();
     if (ln.r + ln.j == 0) {
-        bulk_out(dst + rb * 1024, saddr(stage + rb * 1024), 4096);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) bulk_out(dst + rb * (16 * kC) + h * (8 * kC), saddr(stage) + piece(rb, h), kPiece);
         ptx::bulk_commit();
     }
 }
@@ -784,7 +805,7 @@ __host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
 }
 
 template <typename E, int NK, bool BWD>
-__global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD ? 4 : 4)) gdr_prep(const PrepArgs<E> a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gdr_prep(const PrepArgs<E> a) {
     constexpr int PI = planes<E>(), PX = state_planes<E, BWD>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
@@ -888,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>(), BWD
         for (int kb = 0; kb < NK; ++kb) {
             zero(acc);
             mm<3, PI, true, true>(acc, Ys, rb, Ks + kb * PI * kPlane, ln);
-            leave_tile<BWD>(a.A + ((item * NV + sb) * NK + kb) * kTile, reinterpret_cast<float*>(Q), rb, acc, ln);
+            leave_tile<BWD>(a.A + ((item * NV + sb) * NK + kb) * kTile, Q, rb, acc, ln);
         }
         if (BWD) {
             // local part of the adjoints: Z = X^T diag(beta) P^T dO; adds scale Q^T diag(e^G) dO - K^T diag(e^G) Z
