@@ -15,9 +15,10 @@ def test_gdr_maps_leave_in_order(dt, size):
     """A chunk's tiles leave shared memory one after another, in planes and then as fp32, while the next is formed in their
     place: calls in a row, beside copies that keep the memory busy, have the same bits."""
     p, _ = inputs(*size, DT[dt], 1)
-    out, S = forward(p)
     busy = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())  # its memory may have been a call's until now
+    out, S = forward(p)
     for _ in range(20):
         with torch.cuda.stream(side):
             busy[1 << 27:].copy_(busy[:1 << 27])
