@@ -371,9 +371,9 @@ typedef struct {
  *             (up to 32 tokens). Contents ignored on entry, unspecified on return; calls that may run at the same
  *             time must not share one
  * Up to 32 tokens are walked one by one, in fp32. Longer sequences go in chunks of 64, whose maps of the state are
- * formed first: their products, (I + N diag(beta))^-1 with N_ij = e^{..} k_i.k_j among them, have fp32's precision,
- * and are as well conditioned as the update itself where beta |k|^2 stays below 2 (keys of unit length, a gain
- * below 1). From bf16 inputs the output's operands have 16 bits, the state's 24. Where B*H is 0 nothing is written.
+ * formed first: their products, (I + N diag(beta))^-1 with N_ij = e^{..} k_i.k_j among them, have fp32's precision
+ * (bf16 inputs, too: out is rounded once), and are as well conditioned as the update itself where beta |k|^2 stays below 2
+ * (keys of unit length, a gain below 1). Where B*H is 0 nothing is written.
  * T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
  * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or from B*H*ceil(T/64) = 2^27 on with more than 32 tokens.
  */

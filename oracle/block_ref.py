@@ -8,16 +8,23 @@ import torch
 
 U = 2.0 ** -24
 
-# What fp32 arithmetic may make of a delta rule result, relative to the largest norm of what is summed for it. A product
-# over 64 or 128 terms is at most 48 sums on the tensor cores (16 steps of 8 in three passes), each of which may drop
+# What fp32 arithmetic may make of a delta rule result at worst, relative to the largest norm of what is summed for it. A
+# product over 64 or 128 terms is at most 48 sums on the tensor cores (16 steps of 8 in three passes), each of which may drop
 # a unit (2 U); at most eight products follow one another from the inputs to a gradient (the Gram matrix, the inverse's
 # two levels of two, E, a score, the result), and the errors of at most three of the operands of one meet: 48 x 2 x 8 x 3 U.
 GDR = 2304 * U
-# From bf16 inputs the forward's output is of operands rounded to tf32 (11 bits, half a step 2^-11 of the value): state,
-# prediction, inverse, score and update, five of them.
-GDR_BF16 = 5 * 2.0 ** -11 + GDR
-# and dk of the scores, the adjoint and the error rounded so: three.
+# From bf16 inputs the forward's output, too: its operands have fp32's 24 bits.
+GDR_BF16 = GDR
+# dk of bf16 calls, of the scores, the adjoint and the error rounded to 11 bits: three.
 GDR_BF16_DK = 3 * 2.0 ** -11 + GDR
+
+# What it makes of a whole head's tensor, in the 2-norm, where no error is at its worst and few have one sign: a product leaves
+# about 4 U (its operands' 24 bits and the planes' products that are left out, 2^-24 each, and sums that are cut four times),
+# eight in a row sqrt(8) times that, 11 U. Three times that is the bound; operands of 16 bits leave 2^-17 = 128 U and more.
+NEAR = 32 * U
+# dg adds up to 64 terms of its chunk, 32 in the middle, whose errors add as their root: six times a term's, of which
+# each has that of one product of fp32 results, 8 U; half as much again.
+NEAR_DG = 72 * U
 
 
 def _live(lengths, B, T):
@@ -106,6 +113,27 @@ def gdr_close(got, want, room, dtype=torch.float32):
     bound = half_step(dtype) * norm + room * top + 1e-30
     share = ((got - want).norm(dim=-1) / bound).max().item()
     return share <= 1, share
+
+
+def gdr_near(got, want, dtype=torch.float32, room=NEAR, size=None):
+    """The share that the error of a [B,H,...] tensor has of `room`, head by head in the 2-norm; `size` [B,H]: the norm of
+    what was summed for it, where that is more than the result.
+
+    What is rounded to bf16 is compared with the rounded reference. An error e moves a value to the neighbour, a step u
+    away, with probability |e| / u, so that the square expected is the sum of |e| u, u up to 2^-7 |x|, and |e| is 0.8 of its
+    root mean square: 0.8 room rms 2^-7 sum |x|, and the same again (three standard deviations where 10 values or more move)."""
+    got, want = got.detach().cpu().double().flatten(2), want.double().flatten(2)
+    norm = want.norm(dim=-1) if size is None else size
+    if dtype == torch.float32:
+        return ((got - want).norm(dim=-1) / (room * norm + 1e-300)).max().item()
+    rms = norm / want.shape[-1] ** 0.5
+    square = 2 * 0.8 * room * rms * 2.0 ** -7 * want.abs().sum(-1)
+    return ((got - want.to(dtype).double()).norm(dim=-1) / (square.sqrt() + 1e-300)).max().item()
+
+
+def cut(x, bits):
+    """x in fp32 with that many leading bits of its mantissa (the first of them implied), the others cut off."""
+    return (x.float().contiguous().view(torch.int32) & -(1 << (24 - bits))).view(torch.float32)
 
 
 def rms_forward(x, weight=None, residual=None, *, eps=1e-6, lengths=None):

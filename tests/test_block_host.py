@@ -58,6 +58,25 @@ def test_delta_rule_by_hand():
     assert out.flatten().tolist() == pytest.approx([4.0, 3.5]) and S.item() == pytest.approx(3.5)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_bound_sees_operands_of_16_bits(dt):
+    """The bound of a whole head in its norm: a state, or any input, cut to 16 bits goes past it in what is made of it."""
+    r = torch.Generator().manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=r)  # noqa: E731
+    B, H, T, d = 2, 2, 70, 64
+    p = dict(q=n(B, H, T, d), k=n(B, H, T, d), v=n(B, H, T, d).to(dt), beta=torch.sigmoid(n(B, H, T)),
+             g=-torch.exp(n(B, H, T) - 3), S0=n(B, H, d, d) / 8)
+    p["q"], p["k"] = ((x / x.norm(dim=-1, keepdim=True)).to(dt) for x in (p["q"], p["k"]))
+    out, S = R.gdr_forward(**p)
+    assert R.gdr_near(out.to(dt), out, dt) < 1 and R.gdr_near(S.float(), S) < 1
+    for name in ("S0", "beta") if dt == torch.bfloat16 else ("q", "k", "v", "S0", "beta"):
+        o, s = R.gdr_forward(**dict(p, **{name: R.cut(p[name], 16)}))
+        t = 20 if name == "S0" else T  # little is left of it behind
+        assert R.gdr_near(o[:, :, :t].to(dt), out[:, :, :t], dt) > 1, name
+        if name in ("k", "v", "beta"):
+            assert R.gdr_near(s.float(), S) > 1, name
+
+
 def test_norm_gradients_by_differences():
     r = torch.Generator().manual_seed(2)
     n = lambda *s: torch.randn(*s, generator=r, dtype=torch.double)  # noqa: E731

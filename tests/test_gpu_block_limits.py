@@ -4,6 +4,7 @@ another, values that are not finite, operands' bits, decays of every strength.""
 import pytest
 import torch
 
+from oracle import block_ref as R
 from tests.test_gpu_block import DT, forward, inputs
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +26,23 @@ def test_gdr_maps_leave_in_order(dt, size):
         o, s = forward(p)
         assert torch.equal(o, out) and torch.equal(s, S)
     torch.cuda.synchronize()
+
+
+def near(what, got, want, dtype=torch.float32, room=R.NEAR, size=None):
+    share = R.gdr_near(got, want, dtype, room, size)
+    print(f"NEAR {what}: {share:.3f} of the bound")
+    assert share <= 1, f"{what}: {share:.3f} of the bound"
+
+
+LONG = [(2, 2, 33, 64, 64), (2, 2, 200, 64, 64), (1, 2, 130, 40, 100), (1, 3, 500, 128, 128), (1, 1, 2500, 64, 64)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", LONG, ids=str)
+def test_gdr_forward_keeps_fp32s_bits(dt, size):
+    """Operands of 16 bits in the place of 24 would not pass: test_block_host.py shows it of the bound."""
+    p, _ = inputs(*size, DT[dt], 40)
+    out, S = forward(p)
+    ro, rs = R.gdr_forward(**p)
+    near("out", out, ro, DT[dt])
+    near("S_final", S, rs)

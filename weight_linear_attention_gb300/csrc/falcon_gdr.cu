@@ -9,8 +9,8 @@ namespace falcon {
 namespace gdr {
 namespace {
 
-// ---- outputs of one chunk: out = scale diag(e^G) Q S + P U, U = diag(beta) X (V - diag(e^G) K S). From bf16 inputs
-// every fp32 operand enters in two planes, 16 bits where the result has 8; from fp32 ones in three.
+// ---- outputs of one chunk: out = scale diag(e^G) Q S + P U, U = diag(beta) X (V - diag(e^G) K S), every
+// fp32 operand in three planes.
 template <typename E>
 struct OutArgs {
     Sizes n;
@@ -53,17 +53,17 @@ __device__ __forceinline__ void mm_both(float (&acc)[8][4], float (&o)[8][4], ui
 }
 
 template <typename E, int NK>
-__host__ __device__ constexpr int out_smem() { return (2 * NK * planes<E>() + 2 * state_planes<E, false>()) * kPlane; }
+__host__ __device__ constexpr int out_smem() { return (2 * NK * planes<E>() + 6) * kPlane; }
 
 template <typename E, int NK>
 __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(const OutArgs<E> a) {
-    constexpr int PI = planes<E>(), PS = state_planes<E, false>();
+    constexpr int PI = planes<E>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     uint8_t* K = smem;
     uint8_t* Q = K + NK * PI * kPlane;
     uint8_t* X = Q + NK * PI * kPlane;
-    uint8_t* W = X + PS * kPlane;
+    uint8_t* W = X + 3 * kPlane;
     const uint32_t Ks = saddr(K), Qs = saddr(Q), Xs = saddr(X), Ws = saddr(W);
     const Lane ln;
     const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
             write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, acc, ln, rows, 0, a.n.dv - sb * kC);
         return;
     }
-    const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * PS * kPlane);
+    const uint8_t* St = a.S + (bh * (a.n.NC + 1) + c) * ((long long)NV * NK * 3 * kPlane);
     const Gates gates = load_gates<false>(a.beta, a.g, b, h, t0, live);
 #pragma unroll 1
     for (int kb = 0; kb < NK; ++kb) {
@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
         load_planes(Q + kb * PI * kPlane, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, a.n.dk - kb * kC, a.q.vec);
     }
     commit();
-    copy_planes<PS>(Ws, St);
-    copy_planes<PS>(Xs, a.X + (bh * a.n.NC + c) * (PS * kPlane));
+    copy_planes<3>(Ws, St);
+    copy_planes<3>(Xs, a.X + (bh * a.n.NC + c) * (3 * kPlane));
     commit();
     make_scal(s, gates);
     wait<1>();
@@ -112,12 +112,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
         for (int kb = 0; kb < NK; ++kb) {
             if (sb + kb > 0) {
                 __syncthreads();
-                copy_planes<PS>(Ws, St + (sb * NK + kb) * (PS * kPlane));
+                copy_planes<3>(Ws, St + (sb * NK + kb) * (3 * kPlane));
                 commit();
             }
             wait<0>();
             __syncthreads();
-            mm_both<PI, PS>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+            mm_both<PI, 3>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
         }
         __syncthreads();
 #pragma unroll
@@ -132,18 +132,18 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
                 o[nt][2 * hf + 1] *= eG * a.n.scale;
             }
         }
-        put_planes<PS>(W, rb, acc, ln);
+        put_planes<3>(W, rb, acc, ln);
         __syncthreads();
         zero(acc);
-        mm<PS, PS, false, true>(acc, Xs, rb, Ws, ln, 0, rb + 1);
+        mm<3, 3, false, true>(acc, Xs, rb, Ws, ln, 0, rb + 1);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.beta[16 * rb + ln.r + 8 * (e >> 1)];
-        put_planes<PS>(W, rb, acc, ln);
+        put_planes<3>(W, rb, acc, ln);
         __syncthreads();
-        mmr<PS, PS, true>(o, P, Ws, ln, 0, rb + 1);
+        mmr<3, 3, true>(o, P, Ws, ln, 0, rb + 1);
         write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, o, ln, rows, live, a.n.dv - sb * kC);
     }
 }
@@ -303,7 +303,7 @@ int launch_chunks(const GdrArgs& a, const Layout& l, cudaStream_t st) {
     o.S = ws + l.S;
     const unsigned grid = (unsigned)(n.BH * l.NC);
     int r = launch_ahead<gdr_prep<E, NK, false>>(grid, kThreads, prep_smem<E, NK, false>(), st, p);
-    r |= run_scan<NK, state_planes<E, false>()>(n, l, ws, a.S0, a.S_final, st);
+    r |= run_scan<NK>(n, l, ws, a.S0, a.S_final, st);
     return r | launch_ahead<gdr_out<E, NK>>(grid, kThreads, out_smem<E, NK>(), st, o);
 }
 

@@ -11,8 +11,8 @@
 // kernels run for all chunks at once, and only S' = M S + A goes along the sequence.
 //
 // Products: an fp32 operand x enters as bf16 planes of 8 bits each, x = h + m + l, and a product of two as h h + h m +
-// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it; with two planes as h h + h m +
-// m h (2^-16). bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
+// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it; with two planes (of
+// operands that reach only a bf16 dk) as h h + h m + m h (2^-16). bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
 // loads of matrices and nothing else. (As tf32 pairs, split by every warp that reads them, the gradient kernel took 306 us
 // for 8 x 12 x 1024 x 64, so 246.)
 // They are mma.sync products. A chunk is a row of dependent ones of 64 x 64 x 64 with its own arithmetic between them, and
@@ -268,8 +268,7 @@ __device__ __forceinline__ void get_cols(const float* T, int rb, float (&acc)[8]
         for (int e = 0; e < 4; ++e) acc[nt][e] = T[at(8 * nt + 2 * ln.j + (e & 1), 16 * rb + ln.r + 8 * (e >> 1))];
 }
 // Rows 16 rb .. of N planes, in shared or global memory.
-// OUT: as many of them are written.
-template <int N, int OUT = N>
+template <int N>
 __device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc)[8][4], const Lane& ln) {
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -279,7 +278,7 @@ __device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc
             split<N>(acc[nt][2 * h], acc[nt][2 * h + 1], p);
             uint8_t* to = T + (16 * rb + ln.r + 8 * h) * 128 + ((nt ^ ln.r) << 4) + 4 * ln.j;
 #pragma unroll
-            for (int m = 0; m < OUT; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
+            for (int m = 0; m < N; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
         }
 }
 template <int N>
@@ -776,10 +775,6 @@ __device__ __forceinline__ int length_of(const Sizes& n, long long b) {
 // dv, columns 64 i of dk), [BH][NC + 1], in planes.
 template <typename E>
 __host__ __device__ constexpr int planes() { return sizeof(E) == 2 ? 1 : 3; }
-// Planes of X and of the states that a pass reads: from bf16 inputs the forward's output, a bf16 value, needs two.
-template <typename E, bool BWD>
-__host__ __device__ constexpr int state_planes() { return sizeof(E) == 2 && !BWD ? 2 : 3; }
-
 template <typename E>
 struct PrepArgs {
     Sizes n;
@@ -806,7 +801,7 @@ __host__ __device__ constexpr int ctas_of(int smem, int most = 4) {
 
 template <typename E, int NK, bool BWD>
 __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gdr_prep(const PrepArgs<E> a) {
-    constexpr int PI = planes<E>(), PX = state_planes<E, BWD>();
+    constexpr int PI = planes<E>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     uint8_t* K = smem;
@@ -850,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
     const long long item = bh * a.n.NC + c;
     float t[8][4];
     get(T, rb, t, ln);
-    leave_planes<PX, BWD>(a.X + item * (PX * kPlane), Q, rb, t, ln);
+    leave_planes<3, BWD>(a.X + item * (3 * kPlane), Q, rb, t, ln);
     float tc[8][4];
     if (BWD && !KEEPS) get_cols(T, rb, tc, ln);
     if (!KEEPS) __syncthreads();
@@ -984,7 +979,7 @@ __host__ __device__ constexpr int ring_of(int NK) { return NK == 1 ? 2 : 4; }
 __host__ __device__ constexpr int scan_smem(int NK) { return (ring_of(NK) * 3 + 2 * NK * 2 + NK * 3) * kPlane; }
 constexpr int kScanThreads = kThreads + 64;
 
-template <int NK, bool REV, bool MAP, int PS>
+template <int NK, bool REV, bool MAP>
 __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     constexpr int R = ring_of(NK), NB = NK * NK;
     const Lane ln;
@@ -1028,9 +1023,9 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
                 commit();
                 if (t > 0 || MAP) continue;
                 ptx::named_bar(1, kScanThreads);  // the state is in its place
-                uint8_t* dst = a.S + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * PS * kPlane);
+                uint8_t* dst = a.S + ((bh * a.stride + item(i)) * a.NV + sb) * (NK * 3 * kPlane);
 #pragma unroll 8
-                for (int o = 16 * id; o < NK * PS * kPlane; o += 16 * 64) *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(St + o);
+                for (int o = 16 * id; o < NK * 3 * kPlane; o += 16 * 64) *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(St + o);
             }
         }
         return;
@@ -1068,7 +1063,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
             if (t == 0) {
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
-                    if (!MAP) put_planes<3, PS>(St + k * (PS * kPlane), w, acc[k], ln);
+                    if (!MAP) put_planes<3>(St + k * (3 * kPlane), w, acc[k], ln);
                     zero(nw[k]);
                 }
                 if (!MAP) asm volatile("bar.arrive 1, %0;" ::"n"(kScanThreads) : "memory");
@@ -1113,7 +1108,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     const bool ends = i1 == count && (n > 0 || seg == 0);
 #pragma unroll
     for (int kb = 0; kb < NK; ++kb) {
-        if (a.end_tile && ends) put_planes<3, PS>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (PS * kPlane), w, acc[kb], ln);
+        if (a.end_tile && ends) put_planes<3>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (3 * kPlane), w, acc[kb], ln);
         if (!a.last) continue;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -1126,12 +1121,12 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
 }
 
 // The states' scan.
-template <int NK, bool MAP, int PS>
+template <int NK, bool MAP>
 __global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scan(const ScanArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::pdl_wait();
     if (!MAP && a.chunks) ptx::pdl_launch_dependents();
-    scan<NK, false, MAP, PS>(a, smem);
+    scan<NK, false, MAP>(a, smem);
 }
 // The states' and the adjoints', side by side: neither needs the other.
 template <int NK, bool MAP>
@@ -1139,8 +1134,8 @@ __global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scans(const
     extern __shared__ __align__(128) uint8_t smem[];
     ptx::pdl_wait();
     if (!MAP && a.chunks) ptx::pdl_launch_dependents();
-    if (blockIdx.z == 0) scan<NK, false, MAP, 3>(a, smem);
-    else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP, 3>(r, smem);
+    if (blockIdx.z == 0) scan<NK, false, MAP>(a, smem);
+    else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP>(r, smem);
 }
 
 // The scan's segments, for as few microseconds as the steps make: one of the states takes 1.5 with a CTA an SM, 2.6 with the
@@ -1178,7 +1173,6 @@ inline Layout layout_of(const GdrSizes& n, bool bwd) {
     l.NV = (n.dv + kC - 1) / kC;
     l.NC = (n.T + kC - 1) / kC;
     const long long BH = n.B * n.H, sq = (long long)l.NK * l.NK, st = (long long)l.NV * l.NK;
-    const int ps = n.bf16 && !bwd ? 2 : 3;
     l.cut = cut_of(BH, l.NC, l.NK, l.NV);
     long long at = 0;
     auto take = [&](long long bytes) {
@@ -1187,10 +1181,10 @@ inline Layout layout_of(const GdrSizes& n, bool bwd) {
         return o;
     };
     const long long seg = l.cut.nseg > 1 ? l.cut.nseg : 0, tile = kTile * 4;
-    l.X = take(BH * l.NC * ps * kPlane);
+    l.X = take(BH * l.NC * 3 * kPlane);
     l.M = take(BH * l.NC * sq * 3 * kPlane);
     l.A = take(BH * l.NC * st * tile);
-    l.S = take(BH * (l.NC + 1) * st * ps * kPlane);
+    l.S = take(BH * (l.NC + 1) * st * 3 * kPlane);
     l.P = take(BH * seg * sq * 3 * kPlane);
     l.Z = take(BH * seg * st * tile);
     l.G = take(BH * seg * st * 3 * kPlane);
@@ -1249,16 +1243,16 @@ inline ScanSteps scan_steps(const Sizes& n, const Layout& l, uint8_t* ws, bool r
     return r;
 }
 // The states' scan of a forward call.
-template <int NK, int PS>
+template <int NK>
 int run_scan(const Sizes& n, const Layout& l, uint8_t* ws, const float* init, float* last, cudaStream_t s) {
     const ScanSteps f = scan_steps(n, l, ws, false, init, last);
     const unsigned x = (unsigned)(n.BH * l.cut.nseg);
     int st = 0;
     if (l.cut.nseg > 1) {
-        st |= launch_ahead<gdr_scan<NK, true, 3>>(dim3(x, l.NV + NK), kScanThreads, scan_smem(NK), s, f.map);
-        st |= launch_ahead<gdr_scan<NK, false, 3>>(dim3((unsigned)n.BH, l.NV), kScanThreads, scan_smem(NK), s, f.over);
+        st |= launch_ahead<gdr_scan<NK, true>>(dim3(x, l.NV + NK), kScanThreads, scan_smem(NK), s, f.map);
+        st |= launch_ahead<gdr_scan<NK, false>>(dim3((unsigned)n.BH, l.NV), kScanThreads, scan_smem(NK), s, f.over);
     }
-    return st | launch_ahead<gdr_scan<NK, false, PS>>(dim3(x, l.NV), kScanThreads, scan_smem(NK), s, f.own);
+    return st | launch_ahead<gdr_scan<NK, false>>(dim3(x, l.NV), kScanThreads, scan_smem(NK), s, f.own);
 }
 // Both of a backward call's. The segments' products of M are the forward's: the other reads them transposed.
 template <int NK>
