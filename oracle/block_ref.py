@@ -13,10 +13,8 @@ U = 2.0 ** -24
 # a unit (2 U); at most eight products follow one another from the inputs to a gradient (the Gram matrix, the inverse's
 # two levels of two, E, a score, the result), and the errors of at most three of the operands of one meet: 48 x 2 x 8 x 3 U.
 GDR = 2304 * U
-# From bf16 inputs the forward's output, too: its operands have fp32's 24 bits.
-GDR_BF16 = GDR
-# dk of bf16 calls, of the scores, the adjoint and the error rounded to 11 bits: three.
-GDR_BF16_DK = 3 * 2.0 ** -11 + GDR
+# From bf16 inputs, too: all operands have fp32's 24 bits.
+GDR_BF16 = GDR_BF16_DK = GDR
 
 # What it makes of a whole head's tensor, in the 2-norm, where no error is at its worst and few have one sign: a product leaves
 # about 4 U (its operands' 24 bits and the planes' products that are left out, 2^-24 each, and sums that are cut four times),
@@ -119,16 +117,17 @@ def gdr_near(got, want, dtype=torch.float32, room=NEAR, size=None):
     """The share that the error of a [B,H,...] tensor has of `room`, head by head in the 2-norm; `size` [B,H]: the norm of
     what was summed for it, where that is more than the result.
 
-    What is rounded to bf16 is compared with the rounded reference. An error e moves a value to the neighbour, a step u
-    away, with probability |e| / u, so that the square expected is the sum of |e| u, u up to 2^-7 |x|, and |e| is 0.8 of its
-    root mean square: 0.8 room rms 2^-7 sum |x|, and the same again (three standard deviations where 10 values or more move)."""
-    got, want = got.detach().cpu().double().flatten(2), want.double().flatten(2)
-    norm = want.norm(dim=-1) if size is None else size
+    Of what is rounded to bf16 only that shows which goes past half a step of the rounding: value by value that is at most
+    the error before it, five standard deviations of 11 U of its row (of its head, where that has more): 2 room."""
+    got, want = got.detach().cpu().double(), want.double()
+    norm = want.flatten(2).norm(dim=-1) if size is None else size
     if dtype == torch.float32:
-        return ((got - want).norm(dim=-1) / (room * norm + 1e-300)).max().item()
-    rms = norm / want.shape[-1] ** 0.5
-    square = 2 * 0.8 * room * rms * 2.0 ** -7 * want.abs().sum(-1)
-    return ((got - want.to(dtype).double()).norm(dim=-1) / (square.sqrt() + 1e-300)).max().item()
+        return ((got - want).flatten(2).norm(dim=-1) / (room * norm + 1e-300)).max().item()
+    top = torch.maximum(got.abs(), want.abs()).clamp(min=2.0 ** -126)
+    past = (got - want).abs() - torch.exp2(torch.floor(torch.log2(top))) * half_step(dtype)
+    d = want.shape[-1]
+    rms = torch.maximum(want.norm(dim=-1) / d ** 0.5, norm[..., None] / (want[0, 0].numel()) ** 0.5)[..., None]
+    return (past / (2 * room * rms + 1e-300)).max().item()
 
 
 def cut(x, bits):

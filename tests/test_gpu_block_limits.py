@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import block_ref as R
-from tests.test_gpu_block import DT, forward, inputs
+from tests.test_gpu_block import DT, backward, forward, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,20 @@ def test_gdr_forward_keeps_fp32s_bits(dt, size):
     ro, rs = R.gdr_forward(**p)
     near("out", out, ro, DT[dt])
     near("S_final", S, rs)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", LONG, ids=str)
+@pytest.mark.parametrize("shared", [False, True])
+def test_gdr_backward_keeps_fp32s_bits(dt, size, shared):
+    p, a = inputs(*size, DT[dt], 41, 1 if shared else None)
+    got = backward(p, a)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    for name in ("dq", "dk", "dv", "dbeta", "dS0"):
+        near(name, got[name], want[name], DT[dt] if name in ("dq", "dk", "dv") else torch.float32)
+    # dg is summed from dq.q and dv.v, of heads that share a key each for itself
+    own = R.gdr_backward(*(p[x].repeat_interleave(size[1] // p[x].shape[1], 1) for x in ("q", "k")), p["v"], p["beta"], p["g"],
+                         a["dout"], p["S0"], a["dS_final"])["dq"]
+    q = p["q"].repeat_interleave(size[1] // p["q"].shape[1], 1)
+    terms = torch.stack([(own * q).sum(-1), (want["dv"] * p["v"]).sum(-1)])
+    near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms.square().sum((0, -1)).sqrt())

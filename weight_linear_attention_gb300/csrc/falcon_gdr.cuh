@@ -11,8 +11,7 @@
 // kernels run for all chunks at once, and only S' = M S + A goes along the sequence.
 //
 // Products: an fp32 operand x enters as bf16 planes of 8 bits each, x = h + m + l, and a product of two as h h + h m +
-// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it; with two planes (of
-// operands that reach only a bf16 dk) as h h + h m + m h (2^-16). bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
+// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it. bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
 // loads of matrices and nothing else. (As tf32 pairs, split by every warp that reads them, the gradient kernel took 306 us
 // for 8 x 12 x 1024 x 64, so 246.)
 // They are mma.sync products. A chunk is a row of dependent ones of 64 x 64 x 64 with its own arithmetic between them, and
@@ -78,22 +77,14 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two values as N planes of packed pairs (x in the low half). A plane is the upper half of what is left, cut off: 8 bits
-// each, so that three are the value itself; the last of fewer is rounded.
-template <int N>
-__device__ __forceinline__ void split(float x, float y, uint32_t (&p)[N]) {
+// Two values as planes of packed pairs (x in the low half). A plane is the upper half of what is left, cut off: 8 bits
+// each, so that three are the value itself.
+__device__ __forceinline__ void split(float x, float y, uint32_t (&p)[3]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (i + 1 == N && N < 3) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-            p[i] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-            p[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-        }
-        if (i + 1 < N) {
-            x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-            y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-        }
+    for (int i = 0; i < 3; ++i) {
+        p[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+        x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+        y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
     }
 }
 
@@ -157,24 +148,23 @@ __device__ __forceinline__ void mm(float (&acc)[8][4], uint32_t A, int rb, uint3
     }
 }
 // Registers of a product's result as one k step's operand.
-template <int PA>
-__device__ __forceinline__ void split_a(uint32_t (&a)[PA][4], const float (&x)[2][4]) {
+__device__ __forceinline__ void split_a(uint32_t (&a)[3][4], const float (&x)[2][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t s[PA];
-        split<PA>(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1], s);
+        uint32_t s[3];
+        split(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1], s);
 #pragma unroll
-        for (int m = 0; m < PA; ++m) a[m][i] = s[m];
+        for (int m = 0; m < 3; ++m) a[m][i] = s[m];
     }
 }
 // The same with A in registers, as a product leaves it. ROLL: the loop stays one, its registers chosen by selection, for the
 // backward's long kernels, which wait for instructions as long as for anything else (gradients 220 us unrolled, 209 so;
 // the forward's are shorter and lose 5 % by it).
-template <int PA, int PB, bool BCOL, bool ROLL = false, int WHICH = kAll>
+template <int PB, bool BCOL, bool ROLL = false, int WHICH = kAll>
 __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, const Lane& ln, int k0 = 0, int k1 = 4) {
-    if constexpr ((PA * PB == 9 && WHICH == kAll) || WHICH == kOrdered) {
-        mmr<PA, PB, BCOL, ROLL, kSmall>(acc, A, B, ln, k0, k1);
-        mmr<PA, PB, BCOL, ROLL, kGreat>(acc, A, B, ln, k0, k1);
+    if constexpr ((PB == 3 && WHICH == kAll) || WHICH == kOrdered) {
+        mmr<PB, BCOL, ROLL, kSmall>(acc, A, B, ln, k0, k1);
+        mmr<PB, BCOL, ROLL, kGreat>(acc, A, B, ln, k0, k1);
         return;
     }
     if (!ROLL) {
@@ -182,9 +172,9 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
         for (int kk = 0; kk < 4; ++kk) {
             if (kk < k0 || kk >= k1) continue;
             const float x[2][4] = {{A[2 * kk][0], A[2 * kk][1], A[2 * kk][2], A[2 * kk][3]}, {A[2 * kk + 1][0], A[2 * kk + 1][1], A[2 * kk + 1][2], A[2 * kk + 1][3]}};
-            uint32_t a[PA][4];
-            split_a<PA>(a, x);
-            step<PA, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
+            uint32_t a[3][4];
+            split_a(a, x);
+            step<3, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
         }
         return;
     }
@@ -198,9 +188,9 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
                 const float lo = kk & 1 ? A[2 + i][e] : A[i][e], hi = kk & 1 ? A[6 + i][e] : A[4 + i][e];
                 x[i][e] = kk & 2 ? hi : lo;
             }
-        uint32_t a[PA][4];
-        split_a<PA>(a, x);
-        step<PA, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
+        uint32_t a[3][4];
+        split_a(a, x);
+        step<3, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
     }
 }
 // The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
@@ -228,7 +218,7 @@ __device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float*
         for (int i = 0; i < 4; ++i) {
             const float2 s = *reinterpret_cast<const float2*>(f + 16 * kk + 8 * (i >> 1) + 2 * ln.j);
             uint32_t p[3];
-            split<3>(x[i][0] * s.x, x[i][1] * s.y, p);
+            split(x[i][0] * s.x, x[i][1] * s.y, p);
 #pragma unroll
             for (int m = 0; m < 3; ++m) a[m][i] = p[m];
         }
@@ -267,18 +257,17 @@ __device__ __forceinline__ void get_cols(const float* T, int rb, float (&acc)[8]
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[nt][e] = T[at(8 * nt + 2 * ln.j + (e & 1), 16 * rb + ln.r + 8 * (e >> 1))];
 }
-// Rows 16 rb .. of N planes, in shared or global memory.
-template <int N>
+// Rows 16 rb .. of planes, in shared or global memory: as they are made, three; as they are read, N.
 __device__ __forceinline__ void put_planes(uint8_t* T, int rb, const float (&acc)[8][4], const Lane& ln) {
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t p[N];
-            split<N>(acc[nt][2 * h], acc[nt][2 * h + 1], p);
+            uint32_t p[3];
+            split(acc[nt][2 * h], acc[nt][2 * h + 1], p);
             uint8_t* to = T + (16 * rb + ln.r + 8 * h) * 128 + ((nt ^ ln.r) << 4) + 4 * ln.j;
 #pragma unroll
-            for (int m = 0; m < N; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
+            for (int m = 0; m < 3; ++m) *reinterpret_cast<uint32_t*>(to + m * kPlane) = p[m];
         }
 }
 template <int N>
@@ -319,18 +308,17 @@ static_assert(pieces_apart() && piece(3, kPieces - 1) + kPiece <= kPieces * kPla
 __device__ __forceinline__ void bulk_out(void* dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
-template <int N, bool DIRECT>
+template <bool DIRECT>
 __device__ __forceinline__ void leave_planes(uint8_t* dst, uint8_t* stage, int rb, const float (&acc)[8][4], const Lane& ln) {
-    static_assert(N <= kPieces, "pieces of a stage");
-    if (DIRECT) return put_planes<N>(dst, rb, acc, ln);
+    if (DIRECT) return put_planes(dst, rb, acc, ln);
     if (ln.r + ln.j == 0) ptx::bulk_wait_read<0>();  // what these rows held before has left
     __syncwarp();
-    put_planes<N>(stage, rb, acc, ln);
+    put_planes(stage, rb, acc, ln);
     ptx::fence_async_smem();
     __syncwarp();
     if (ln.r + ln.j == 0) {
 #pragma unroll
-        for (int m = 0; m < N; ++m) bulk_out(dst + m * kPlane + rb * kPiece, saddr(stage) + piece(rb, m), kPiece);
+        for (int m = 0; m < kPieces; ++m) bulk_out(dst + m * kPlane + rb * kPiece, saddr(stage) + piece(rb, m), kPiece);
         ptx::bulk_commit();
     }
 }
@@ -400,8 +388,8 @@ __device__ __forceinline__ void load_planes(uint8_t* dst, const float* src, long
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (row < rows && col < cols) v = *reinterpret_cast<const float4*>(src + row * st + col);
             uint32_t x[3], y[3];
-            split<3>(v.x, v.y, x);
-            split<3>(v.z, v.w, y);
+            split(v.x, v.y, x);
+            split(v.z, v.w, y);
 #pragma unroll
             for (int m = 0; m < 3; ++m) *reinterpret_cast<uint2*>(dst + m * kPlane + pat(row, col)) = make_uint2(x[m], y[m]);
         }
@@ -411,7 +399,7 @@ __device__ __forceinline__ void load_planes(uint8_t* dst, const float* src, long
             const int row = c >> 5, col = (c & 31) * 2;
             const float* p = src + row * st + col;
             uint32_t x[3];
-            split<3>(row < rows && col < cols ? p[0] : 0.f, row < rows && col + 1 < cols ? p[1] : 0.f, x);
+            split(row < rows && col < cols ? p[0] : 0.f, row < rows && col + 1 < cols ? p[1] : 0.f, x);
 #pragma unroll
             for (int m = 0; m < 3; ++m) *reinterpret_cast<uint32_t*>(dst + m * kPlane + pat(row, col)) = x[m];
         }
@@ -845,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
     const long long item = bh * a.n.NC + c;
     float t[8][4];
     get(T, rb, t, ln);
-    leave_planes<3, BWD>(a.X + item * (3 * kPlane), Q, rb, t, ln);
+    leave_planes<BWD>(a.X + item * (3 * kPlane), Q, rb, t, ln);
     float tc[8][4];
     if (BWD && !KEEPS) get_cols(T, rb, tc, ln);
     if (!KEEPS) __syncthreads();
@@ -858,13 +846,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[nt][e] = t[nt][e] * s.eG[8 * nt + 2 * ln.j + (e & 1)];
         zero(acc);
-        mmr<3, PI, true, BWD>(acc, f, Ks + cb * PI * kPlane, ln, 0, k1);
+        mmr<PI, true, BWD>(acc, f, Ks + cb * PI * kPlane, ln, 0, k1);
         if (cb > 0) __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.bw[16 * rb + ln.r + 8 * (e >> 1)];
-        put_planes<3>(Y, rb, acc, ln);
+        put_planes(Y, rb, acc, ln);
         __syncthreads();
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) {
@@ -879,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
                 for (int e = 0; e < 4; ++e)
                     if (ln.r + 8 * (e >> 1) == 8 * (nt & 1) + 2 * ln.j + (e & 1)) acc[nt][e] += s.eC;
             }
-            leave_planes<3, BWD>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), Q, rb, acc, ln);
+            leave_planes<BWD>(a.M + ((item * NK + kb) * NK + cb) * (3 * kPlane), Q, rb, acc, ln);
         }
     }
     const int NV = (a.n.dv + kC - 1) / kC;
@@ -892,13 +880,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
         wait<0>();
         __syncthreads();
         zero(acc);
-        mmr<3, PI, true, BWD>(acc, t, Ys, ln, 0, k1);
+        mmr<PI, true, BWD>(acc, t, Ys, ln, 0, k1);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.bw[16 * rb + ln.r + 8 * (e >> 1)];
-        put_planes<3>(Y, rb, acc, ln);
+        put_planes(Y, rb, acc, ln);
         __syncthreads();
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) {
@@ -914,23 +902,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
             for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4);
             times_decay<true, false>(P, s, rb, ln, nullptr, a.n.scale);
             zero(acc);
-            mmr<3, PI, true, BWD>(acc, P, Os, ln, rb, 4);
+            mmr<PI, true, BWD>(acc, P, Os, ln, rb, 4);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][e] *= s.beta[16 * rb + ln.r + 8 * (e >> 1)];
             __syncthreads();
-            put_planes<3>(Y, rb, acc, ln);
+            put_planes(Y, rb, acc, ln);
             __syncthreads();
             if (KEEPS) get_cols(T, rb, P, ln);
             zero(acc);
-            mmr<3, 3, true, BWD>(acc, KEEPS ? P : tc, Ys, ln, rb, 4);
+            mmr<3, true, BWD>(acc, KEEPS ? P : tc, Ys, ln, rb, 4);
             __syncthreads();
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][e] *= -s.eG[16 * rb + ln.r + 8 * (e >> 1)];
-            put_planes<3>(Y, rb, acc, ln);
+            put_planes(Y, rb, acc, ln);
             __syncthreads();
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
@@ -1063,12 +1051,12 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
             if (t == 0) {
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
-                    if (!MAP) put_planes<3>(St + k * (3 * kPlane), w, acc[k], ln);
+                    if (!MAP) put_planes(St + k * (3 * kPlane), w, acc[k], ln);
                     zero(nw[k]);
                 }
                 if (!MAP) asm volatile("bar.arrive 1, %0;" ::"n"(kScanThreads) : "memory");
             }
-            mmr<3, 3, REV>(nw[kb], acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln);
+            mmr<3, REV>(nw[kb], acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln);
         }
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
@@ -1093,7 +1081,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t p[3];
-                        split<3>(acc[kb][nt][2 * h], acc[kb][nt][2 * h + 1], p);
+                        split(acc[kb][nt][2 * h], acc[kb][nt][2 * h + 1], p);
 #pragma unroll
                         for (int m = 0; m < 3; ++m) {
                             const int row = 8 * nt + 2 * ln.j, col = 16 * w + ln.r + 8 * h;
@@ -1108,7 +1096,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
     const bool ends = i1 == count && (n > 0 || seg == 0);
 #pragma unroll
     for (int kb = 0; kb < NK; ++kb) {
-        if (a.end_tile && ends) put_planes<3>(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (3 * kPlane), w, acc[kb], ln);
+        if (a.end_tile && ends) put_planes(a.S + (((bh * a.stride + count) * a.NV + sb) * NK + kb) * (3 * kPlane), w, acc[kb], ln);
         if (!a.last) continue;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)

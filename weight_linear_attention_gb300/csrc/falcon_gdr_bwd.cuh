@@ -30,9 +30,9 @@ struct GradArgs {
     const uint8_t *X, *S, *dS;
 };
 
-// K, dO, E, Z and what comes and goes. With one tile of S and dS' (and bf16) all of it is on its way early: S and dS'
-// in E's and Z's places, X and Q in the last; else these come one after the other in three planes. So does fp32's dO:
-// 96 KB then let two CTAs of heads up to 64 run on an SM.
+// K, E, Z, what comes and goes, and dO. With one tile of S and dS' (and bf16) all of it is on its way early: S and dS'
+// in E's and Z's places, X and Q in W, then S and dS' in W, whose last plane is dO's, and Q again; else these come one
+// after the other. So does fp32's dO: 96 KB then let two CTAs of heads up to 64 run on an SM.
 template <typename E>
 __host__ __device__ constexpr bool grad_keeps() { return sizeof(E) == 2; }
 template <typename E, int NK, int NV>
@@ -50,16 +50,14 @@ template <typename E, int NK, int NV>
 __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr_grad(const GradArgs<E> a) {
     constexpr bool ONE = grad_one<E, NK, NV>(), KEEPS = grad_keeps<E>();
     constexpr int PI = planes<E>();
-    // planes of operands that reach only dK, rounded to bf16: two where the other has one
-    constexpr int PL = sizeof(E) == 2 ? 2 : 3, P1 = sizeof(E) == 2 ? 1 : 3;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     __shared__ float own[kC], dbe[kC], part[kThreads / 32];
     uint8_t* K = smem;
-    uint8_t* dO = K + NK * PI * kPlane;
-    uint8_t* Et = dO + (KEEPS ? NV * PI : 0) * kPlane;
+    uint8_t* Et = K + NK * PI * kPlane;
     uint8_t* Zt = Et + NV * 3 * kPlane;
     uint8_t* W = Zt + NV * 3 * kPlane;
+    uint8_t* dO = W + (ONE ? 5 : 3) * kPlane;  // KEEPS
     const uint32_t Ks = saddr(K), Os = saddr(dO), Es0 = saddr(Et), Zs0 = saddr(Zt), Ws = saddr(W);
     const Lane ln;
     const unsigned ubh = blockIdx.x / (unsigned)a.n.NC, ub = ubh / (unsigned)a.n.H, uh = ubh % (unsigned)a.n.H;
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<3, PI, true, true, kOrdered>(d, P, adjoint(sb), ln, rb, 4);  // dU
+        mmr<PI, true, true, kOrdered>(d, P, adjoint(sb), ln, rb, 4);  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const float eG = s.eG[16 * rb + ln.r + 8 * hf];
@@ -226,27 +224,26 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         }
         if (ONE) __syncthreads();  // S and dS' are read
         else bring(Xs, Xt);
-        put_planes<3>(Et + sb * 3 * kPlane, rb, x, ln);
+        put_planes(Et + sb * 3 * kPlane, rb, x, ln);
         float z[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[nt][e] = d[nt][e] * s.beta[16 * rb + ln.r + 8 * (e >> 1)];
-        put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
+        put_planes(Zt + sb * 3 * kPlane, rb, z, ln);
         __syncthreads();
         zero(x);
         zero(z);
         mm<3, 3, false, true>(x, Xs, rb, Es, ln, 0, rb + 1);  // E
         mm<3, 3, true, true>(z, Xs, rb, Zs, ln, rb, 4);       // Z
         __syncthreads();
-        if (ONE) {  // for dK: two planes each, and Q behind them
-            copy_planes<2>(Ws, St);
-            copy_planes<2>(Ws + 2 * kPlane, dSt);
-            load_q(W + 4 * kPlane, 0);
+        if (ONE) {  // for dK: what there is room for
+            copy_planes<3>(Ws, St);
+            copy_planes<2>(Ws + 3 * kPlane, dSt);
             commit();
         }
-        put_planes<3>(Et + sb * 3 * kPlane, rb, x, ln);
-        put_planes<3>(Zt + sb * 3 * kPlane, rb, z, ln);
+        put_planes(Et + sb * 3 * kPlane, rb, x, ln);
+        put_planes(Zt + sb * 3 * kPlane, rb, z, ln);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -274,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     for (int sb = 0; sb < NV; ++sb) {
         const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = adjoint(sb);
         mm<PI, 3, false, false, kOrdered>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
-        mm<PL, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
-        mm<PL, PL, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
-        mm<PL, PL, false, false>(x, Es, rb, Zs, ln, 0, 4, rb, 4);
+        mm<3, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
+        mm<3, 3, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
+        mm<3, 3, false, false>(x, Es, rb, Zs, ln, 0, 4, rb, 4);
     }
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -298,8 +295,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         if (ONE) {
             wait<0>();
             __syncthreads();
-            mm<PL, PL, false, true>(d, Zs0, rb, Ws, ln);
-            mm<PL, PL, false, true>(t, Es0, rb, Ws + 2 * kPlane, ln);
+            copy_planes<1>(Ws + 5 * kPlane, dSt + 2 * kPlane);  // dO is read
+            commit();
+            mm<3, 3, false, true>(d, Zs0, rb, Ws, ln);
+            wait<0>();
+            __syncthreads();
+            load_q(W, 0);
+            commit();
+            mm<3, 3, false, true>(t, Es0, rb, Ws + 3 * kPlane, ln);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -319,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
-                    mmr<3, 3, true, true>(x, f, Ws, ln);
+                    mmr<3, true, true>(x, f, Ws, ln);
                 }
-                mm<PL, PL, false, true>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
+                mm<3, 3, false, true>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
                 bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
-                mm<PL, PL, false, true>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
+                mm<3, 3, false, true>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
             }
             __syncthreads();
             load_q(W, kb);
@@ -337,17 +340,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 x[nt][e] *= s.eG[row] * a.n.scale;
                 d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
             }
-        mmr<3, PI, true, true, kOrdered>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
+        mmr<PI, true, true, kOrdered>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
         write_qk(a.dq, a.pq, x, kb);
-        mmr<PL, P1, true, true>(d, H, Ks + kb * PI * kPlane, ln);
-        uint8_t* Qt = ONE ? W + 4 * kPlane : W;
-        if (!ONE) {
-            wait<0>();
-            __syncthreads();
-        }
-        mmr<PL, P1, true, true>(d, A3, saddr(Qt), ln, rb, 4);
+        mmr<PI, true, true>(d, H, Ks + kb * PI * kPlane, ln);
+        wait<0>();
+        __syncthreads();
+        mmr<PI, true, true>(d, A3, Ws, ln, rb, 4);
         write_qk(a.dk, a.pk, d, kb);
-        get_planes<PI>(Qt, rb, t, ln);
+        get_planes<PI>(W, rb, t, ln);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
