@@ -278,7 +278,8 @@ typedef enum {
  *   h_final   fp32 [B,H,d] or NULL: the state behind each sequence's last token (h0 when it has none);
  *             may be the same pointer as h0
  *   strides   of x, g, out (9 values) or NULL
- * T = 1 is a decoding step; calls that continue from h_final equal one call over all tokens.
+ * A value that is not finite reaches what its token and those behind it make of it (a v of its own channel alone), no token
+ * before it. T = 1 is a decoding step; calls that continue from h_final equal one call over all tokens.
  */
 int falcon_glr_fwd(int gate, const void* x, const void* g, const float* h0, const int32_t* lengths, void* out,
                    float* h_final, const falcon_seq_dims_t* dims, const int64_t* strides, void* stream);
@@ -374,7 +375,8 @@ typedef struct {
  * formed first: their products, (I + N diag(beta))^-1 with N_ij = e^{..} k_i.k_j among them, have fp32's precision
  * (bf16 inputs, too: out is rounded once), and are as well conditioned as the update itself where beta |k|^2 stays below 2
  * (keys of unit length, a gain below 1). Where B*H is 0 nothing is written.
- * T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
+ * A value that is not finite reaches what its token and those behind it make of it (a v of its own channel alone), no token
+ * before it. T = 1 is a decoding step; calls that continue from S_final equal one call over all tokens.
  * FALCON_ERR_UNSUPPORTED from B*H = 2^28 on, or from B*H*ceil(T/64) = 2^27 on with more than 32 tokens.
  */
 int falcon_gdr_fwd(const void* q, const void* k, const void* v, const float* beta, const float* g, const float* S0,
@@ -383,7 +385,8 @@ int falcon_gdr_fwd(const void* q, const void* k, const void* v, const float* bet
 
 /*
  * falcon_gdr_bwd — gradients of L = sum(out * dout) + sum(S_final * dS_final) of one falcon_gdr_fwd call, from its
- * inputs alone (the states are formed again).
+ * inputs alone (the states are formed again). A value that is not finite may reach any gradient of its head and of those
+ * that share its key.
  *   dout      [B,H,T,dv] dtype
  *   dS_final  fp32 [B,H,dk,dv] or NULL (zero)
  *   dq, dk    [B,Hk,T,dk] dtype       summed over the heads that share them, rounded once

@@ -1,6 +1,8 @@
 """Where the gated delta rule and the root-mean-square norm can go wrong beside their parity: what a call's parts leave for one
 another, values that are not finite, operands' bits, decays of every strength."""
 
+import math
+
 import pytest
 import torch
 
@@ -63,3 +65,29 @@ def test_gdr_backward_keeps_fp32s_bits(dt, size, shared):
     q = p["q"].repeat_interleave(size[1] // p["q"].shape[1], 1)
     terms = torch.stack([(own * q).sum(-1), (want["dv"] * p["v"]).sum(-1)])
     near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms.square().sum((0, -1)).sqrt())
+
+
+BAD = [("v", math.nan), ("v", math.inf), ("k", math.nan), ("k", -math.inf), ("q", math.nan), ("q", math.inf),
+       ("beta", math.nan), ("beta", math.inf), ("g", math.nan), ("g", math.inf)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,dk,dv", [(20, 64, 64), (130, 64, 64), (200, 128, 72)])
+@pytest.mark.parametrize("name,value", BAD, ids=lambda x: str(x))
+def test_gdr_tokens_before_a_value_that_is_not_finite(dt, T, dk, dv, name, value):
+    """Each head has one such value at another token: what the definition makes of it is not finite either, all else is, and
+    right."""
+    at = [t for t in (0, 3, 15, 16, 17, 31, 33, 47, 48, 63, 64, 79, 100, T - 1) if t < T]
+    p, _ = inputs(1, len(at), T, dk, dv, DT[dt], 42)
+    for h, t in enumerate(at):
+        if p[name].dim() == 4:
+            p[name][0, h, t, 5] = value
+        else:
+            p[name][0, h, t] = value
+    out, S = forward(p)
+    ro, rs = R.gdr_forward(**p)
+    for got, want, dtype in ((out.cpu(), ro, DT[dt]), (S.cpu(), rs, torch.float32)):
+        there = torch.isfinite(want)
+        assert torch.equal(torch.isfinite(got), there)
+        ok, share = R.gdr_close(torch.where(there, got, 0), torch.where(there, want, 0), R.GDR, dtype)
+        assert ok, share

@@ -132,18 +132,20 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
                 o[nt][2 * hf + 1] *= eG * a.n.scale;
             }
         }
+        const bool predicted = all_finite(acc);
         put_planes(W, rb, acc, ln);
         __syncthreads();
         zero(acc);
-        mm<3, 3, false, true>(acc, Xs, rb, Ws, ln, 0, rb + 1);
+        mm_lower(acc, Xs, rb, Ws, ln, predicted);
         __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] *= s.beta[16 * rb + ln.r + 8 * (e >> 1)];
+        const bool written = all_finite(acc);
         put_planes(W, rb, acc, ln);
         __syncthreads();
-        mmr<3, true>(o, P, Ws, ln, 0, rb + 1);
+        mmr_lower(o, P, Ws, rb, ln, written);
         write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, o, ln, rows, live, a.n.dv - sb * kC);
     }
 }

@@ -193,6 +193,76 @@ __device__ __forceinline__ void mmr(float (&acc)[8][4], const float (&A)[8][4], 
         step<3, PB, BCOL, WHICH>(acc, a, B, ln, kk, 0, 4);
     }
 }
+// ---- values that are not finite. A row i of a triangle's product depends on rows j <= i of B, but the zeros above the diagonal
+// meet the others' NaN in the k step on the diagonal. So where a warp's own 16 rows of B hold such a value, that step is
+// made without it, and what a product of ones below the diagonal with ones in its places counts is made NaN.
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028234e38f; }
+__device__ __forceinline__ bool all_finite(const float (&x)[8][4]) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = fmaf(x[i][e], 0.f, s);
+    return __all_sync(0xffffffffu, s == 0.f);
+}
+// acc += A B for the k step kk that holds the rows of acc, A (lower triangular) in registers, B stored [k][n].
+__device__ __forceinline__ void step_diagonal(float (&acc)[8][4], const uint32_t (&a)[3][4], uint32_t b, const Lane& ln, int kk) {
+    const uint32_t row = b + (16 * kk + ln.l7 + 8 * ln.l8) * 128;
+    uint32_t ones[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = ln.r + 8 * (i & 1), k = 2 * ln.j + 8 * (i >> 1);
+        ones[i] = (k <= m ? 0x3f80u : 0u) | (k + 1 <= m ? 0x3f800000u : 0u);
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        uint32_t v[3][4], bad[4];
+#pragma unroll
+        for (int m = 0; m < 3; ++m) ldm<true>(v[m], row + m * kPlane + (((2 * p + ln.l16) ^ ln.l7) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the first plane has the value's exponent
+            const uint32_t lo = (v[0][i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (v[0][i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+            bad[i] = (lo | hi) & 0x3f803f80u;
+#pragma unroll
+            for (int m = 0; m < 3; ++m) v[m][i] &= ~(lo | hi);
+        }
+#pragma unroll
+        for (int s = 2; s >= 0; --s)
+#pragma unroll
+            for (int m = 0; m <= s; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma(acc[2 * p + i], a[m], v[s - m][2 * i], v[s - m][2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float n[4] = {0.f, 0.f, 0.f, 0.f};
+            mma(n, ones, bad[2 * i], bad[2 * i + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n[e] > 0.f) acc[2 * p + i][e] = __int_as_float(0x7fc00000);
+        }
+    }
+}
+// acc += A B, A's rows 16 rb .. lower triangular; `whole`: all of B's rows 16 rb .. are finite.
+__device__ __forceinline__ void mm_lower(float (&acc)[8][4], uint32_t A, int rb, uint32_t B, const Lane& ln, bool whole) {
+    mm<3, 3, false, true>(acc, A, rb, B, ln, 0, whole ? rb + 1 : rb);
+    if (whole) return;
+    uint32_t a[3][4];
+#pragma unroll
+    for (int m = 0; m < 3; ++m) ldm<false>(a[m], A + m * kPlane + (16 * rb + ln.l7 + 8 * ln.l8) * 128 + (((2 * rb + ln.l16) ^ ln.l7) << 4));
+    step_diagonal(acc, a, B, ln, rb);
+}
+__device__ __forceinline__ void mmr_lower(float (&acc)[8][4], const float (&A)[8][4], uint32_t B, int rb, const Lane& ln, bool whole) {
+    mmr<3, true>(acc, A, B, ln, 0, whole ? rb + 1 : rb);
+    if (whole) return;
+    float x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] = rb == 0 ? A[i][e] : rb == 1 ? A[2 + i][e] : rb == 2 ? A[4 + i][e] : A[6 + i][e];
+    uint32_t a[3][4];
+    split_a(a, x);
+    step_diagonal(acc, a, B, ln, rb);
+}
 // The same with A[k][m] one plane in shared memory, each k scaled by f[k]: the products of planes are made here.
 template <int PI, int PB, bool BCOL, int WHICH = kAll>
 __device__ __forceinline__ void mms(float (&acc)[8][4], uint32_t A, const float* f, int rb, uint32_t B, const Lane& ln) {
@@ -577,7 +647,9 @@ __device__ __forceinline__ void make_scal(Scal& s, const Gates& r) {
         if (l >= d) sum = add(o, sum);
     }
     const Two all = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
-    const Two G[2] = {add(sum, Two{-x[1].hi, -x[1].lo}), sum};
+    Two prev = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+    if (l == 0) prev = Two{0.f, 0.f};
+    const Two G[2] = {add(prev, x[0]), sum};  // (not sum - x[1], which a decay that is not finite would carry back)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
@@ -683,12 +755,20 @@ __device__ __forceinline__ void corner(const float* T, int o, int mb, int half, 
 #pragma unroll
     for (int kk = 0; kk < N / 8; ++kk) {
         if (kk >= rows) continue;
-        const float a[4] = {-x[kk][0], -x[kk][2], -x[kk][1], -x[kk][3]};
-        uint32_t ah[4], al[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split(a[e], ah[e], al[e]);
+        float a[4] = {-x[kk][0], -x[kk][2], -x[kk][1], -x[kk][3]};
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
+            const int below = 2 * half + nt - kk;  // Y22's block
+            if (below < 0) continue;
+            uint32_t bad[4] = {0, 0, 0, 0};  // on the diagonal a row that is not finite leaves those before it alone
+            if (below == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!finite(a[e])) bad[e] = __float_as_uint(1.f);
+            }
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(bad[e] ? 0.f : a[e], ah[e], al[e]);
             const float2 v = *reinterpret_cast<const float2*>(T + at(o + N + 16 * half + 8 * nt + ln.r, o + N + 8 * kk + 2 * ln.j));
             uint32_t h0, l0, h1, l1;
             split(v.x, h0, l0);
@@ -696,6 +776,13 @@ __device__ __forceinline__ void corner(const float* T, int o, int mb, int half, 
             mma_tf32(res[nt], al, h0, h1);
             mma_tf32(res[nt], ah, l0, l1);
             mma_tf32(res[nt], ah, h0, h1);
+            if (below == 0 && __any_sync(0xffffffffu, bad[0] | bad[1] | bad[2] | bad[3])) {
+                float n[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_tf32(n, bad, __float_as_uint(2 * ln.j <= ln.r ? 1.f : 0.f), __float_as_uint(2 * ln.j + 1 <= ln.r ? 1.f : 0.f));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n[e] > 0.f) res[nt][e] = __int_as_float(0x7fc00000);
+            }
         }
     }
 }
