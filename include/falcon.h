@@ -391,10 +391,10 @@ int falcon_gdr_fwd(const void* q, const void* k, const void* v, const float* bet
  *   dS_final  fp32 [B,H,dk,dv] or NULL (zero)
  *   dq, dk    [B,Hk,T,dk] dtype       summed over the heads that share them, rounded once
  *   dv        [B,H,T,dv] dtype
- *   dbeta, dg fp32 [B,H,T]            (dg is 0 where e^g is; it is a difference of dq.q and dv.v, with <S, dS>, and
- *                                     its error is about 1e-6 of the norm of these terms. Where decays are strong dg
- *                                     is small beside them: off by 3e-4 of itself at a g of -6 for every token, by
- *                                     0.05 to 0.2 at -12)
+ *   dbeta, dg fp32 [B,H,T]            (dg is 0 where e^g is below fp32's normal numbers. It is a difference of dq.q and
+ *                                     dv.v, with <S, dS>, and its error about 1e-6 of the norm of these terms; where a
+ *                                     decay of its 64 tokens is below -2 it is summed from what has the decay as a factor,
+ *                                     and its error about 1e-6 of that)
  *   dS0       fp32 [B,H,dk,dv] or NULL
  *   strides   of q, k, v, beta, g, dout, dq, dk, dv, dbeta, dg (33 values) or NULL
  *   workspace at least falcon_gdr_workspace_bytes(dims, 1) bytes, as above

@@ -59,12 +59,14 @@ def test_gdr_backward_keeps_fp32s_bits(dt, size, shared):
     want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
     for name in ("dq", "dk", "dv", "dbeta", "dS0"):
         near(name, got[name], want[name], DT[dt] if name in ("dq", "dk", "dv") else torch.float32)
-    # dg is summed from dq.q and dv.v, of heads that share a key each for itself
-    own = R.gdr_backward(*(p[x].repeat_interleave(size[1] // p[x].shape[1], 1) for x in ("q", "k")), p["v"], p["beta"], p["g"],
-                         a["dout"], p["S0"], a["dS_final"])["dq"]
-    q = p["q"].repeat_interleave(size[1] // p["q"].shape[1], 1)
-    terms = torch.stack([(own * q).sum(-1), (want["dv"] * p["v"]).sum(-1)])
-    near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms.square().sum((0, -1)).sqrt())
+    near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms_of_dg(p, a, want))
+
+
+def terms_of_dg(p, a, want):
+    """The norm of what dg is summed from: dq.q (of heads that share a key each for itself) and dv.v."""
+    q, k = (p[x].repeat_interleave(p["v"].shape[1] // p[x].shape[1], 1) for x in ("q", "k"))
+    own = R.gdr_backward(q, k, p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])["dq"]
+    return torch.stack([(own * q).sum(-1), (want["dv"] * p["v"]).sum(-1)]).square().sum((0, -1)).sqrt()
 
 
 BAD = [("v", math.nan), ("v", math.inf), ("k", math.nan), ("k", -math.inf), ("q", math.nan), ("q", math.inf),
@@ -91,3 +93,51 @@ def test_gdr_tokens_before_a_value_that_is_not_finite(dt, T, dk, dv, name, value
         assert torch.equal(torch.isfinite(got), there)
         ok, share = R.gdr_close(torch.where(there, got, 0), torch.where(there, want, 0), R.GDR, dtype)
         assert ok, share
+
+
+STRONG = [-3.9, -4.5, -6.0, -9.0, -12.0, -20.0, -60.0, -80.0]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,dk,dv", [(20, 64, 64), (150, 64, 64), (100, 128, 40), (130, 48, 100), (90, 128, 128)])
+def test_gdr_dg_of_strong_decays(dt, T, dk, dv):
+    """All tokens of a head decay alike, down to e^-80: the error of dg is one of dg itself."""
+    p, a = inputs(2, len(STRONG), T, dk, dv, DT[dt], 43)
+    p["g"] = torch.tensor(STRONG)[None, :, None].expand(2, -1, T).contiguous()
+    got = backward(p, a)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    for h, g in enumerate(STRONG):
+        # above -4 a difference of terms that are e^3.9 as great
+        room = R.NEAR_DG * (math.exp(3.9) if g > -4 else 1)
+        near(f"dg at {g}", got["dg"][:, h:h + 1], want["dg"][:, h:h + 1], room=room)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [-1.9, -2.1])
+def test_gdr_dg_on_both_sides_of_its_rule(dt, d, g):
+    p, a = inputs(1, 4, 200, d, d, DT[dt], 45)
+    p["g"] = torch.full_like(p["g"], g)
+    got = backward(p, a)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms_of_dg(p, a, want) if g > -2 else None)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_gdr_dg_of_strong_decays_among_weak_ones(dt, shared):
+    """Every seventh token forgets (and one in a sequence that ends early, gains of 0 beside it): its dg by itself."""
+    T, n = 300, torch.tensor([300, 170], dtype=torch.int32)
+    p, a = inputs(2, len(STRONG), T, 64, 64, DT[dt], 44, 2 if shared else None)
+    strong = torch.arange(T) % 7 == 3
+    p["g"] = torch.where(strong, torch.tensor(STRONG)[:, None], torch.tensor(-0.05)).expand(2, -1, -1).contiguous()
+    p["beta"][:, :, 5::14] = 0
+    p["g"][0, :, 101] = -math.inf
+    got = backward(p, a, n)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"], lengths=n)
+    assert not got["dg"][0, :, 101].any() and not got["dg"][1, :, 170:].any()
+    for h, g in enumerate(STRONG):
+        room = R.NEAR_DG * (math.exp(3.9) if g > -4 else 1)
+        near(f"dg at {g}", got["dg"][:, h:h + 1, strong], want["dg"][:, h:h + 1, strong], room=room)
+        weak = ~strong & (torch.arange(T) != 101)
+        near(f"dg beside {g}", got["dg"][:, h:h + 1, weak], want["dg"][:, h:h + 1, weak], room=R.NEAR_DG)

@@ -8,7 +8,8 @@
 //   dbeta_j = E_j.(dU - N^T Z)_j = E_j.Z_j / beta_j.
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
 // writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
-// from its token to the chunk's end. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
+// from its token to the chunk's end. Its error is 1e-6 of these terms, of which dg is the part e^g: where a token's decay is
+// below kSteep, the chunk takes dg from what passes that token. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
 // gdr_grad takes the gradients, all chunks at once: 18 products a chunk, two CTAs an SM (of their operands' 104 KB), bound
 // by latency and by fetching its own instructions (8 x 12 x 1024 x 64 bf16: maps 102, scans 45, gradients 164 us).
 
@@ -40,6 +41,10 @@ __host__ __device__ constexpr bool grad_one() { return NK * NV == 1 && sizeof(E)
 template <typename E, int NK, int NV>
 __host__ __device__ constexpr int grad_smem() { return ((NK + (grad_keeps<E>() ? NV : 0)) * planes<E>() + 6 * NV + (grad_one<E, NK, NV>() ? 5 : 3)) * kPlane; }
 
+// The sums are right to 1e-6 of their terms, that is of dg to e^2 as much or so; at -4 it would be 2e-4, at -12 a tenth. What passes a
+// token takes a third more of a call (8 x 12 x 1024 x 64 with all tokens below: 390 to 509 us).
+constexpr float kSteep = -2.f;
+
 // Summed over the four lanes that hold a row.
 __device__ __forceinline__ float row_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -53,6 +58,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     __shared__ float own[kC], dbe[kC], part[kThreads / 32];
+    __shared__ bool steep;
     uint8_t* K = smem;
     uint8_t* Et = K + NK * PI * kPlane;
     uint8_t* Zt = Et + NV * 3 * kPlane;
@@ -148,6 +154,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     }
     commit();
     make_scal(s, gates);
+    if (threadIdx.x < 32) {
+        const bool any = __any_sync(0xffffffffu, gates.g[0] < kSteep || gates.g[1] < kSteep);
+        if (threadIdx.x == 0) steep = any;
+    }
     // P transposed: rows j, columns i >= j
     float P[8][4];
     zero(P);
@@ -353,26 +363,150 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll
             for (int e = 0; e < 4; ++e) sq[e >> 1] = fmaf(x[nt][e], t[nt][e], sq[e >> 1]);
     }
-    // the rows' sums: own = dQ.Q - dV.V
+    // dg of tokens 2 l and 2 l + 1 in the first warp
+    float dg[2];
+    const int l = threadIdx.x;
+    auto sum_ends = [&] {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) ends += __shfl_xor_sync(0xffffffffu, ends, m);
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ends;
+    };
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         const int row = 16 * rb + ln.r + 8 * hf;
         const float o = row_sum(sq[hf] - sv[hf]), e = row_sum(sb_[hf]) / s.beta[row];
-        if (ln.j == 0) own[row] = o, dbe[row] = e;
+        if (ln.j == 0) own[row] = o, dbe[row] = e;  // own = dQ.Q - dV.V
     }
+    if (!steep) {
+        sum_ends();
+        __syncthreads();
+        if (threadIdx.x >= 32) return;
+        Two sum = add(Two{own[2 * l], 0.f}, Two{own[2 * l + 1], 0.f});  // pairs of floats: the sums may cancel
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) ends += __shfl_xor_sync(0xffffffffu, ends, m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ends;
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    const int l = threadIdx.x;
-    Two sum = add(Two{own[2 * l], 0.f}, Two{own[2 * l + 1], 0.f});  // pairs of floats: the sums may cancel
+        for (int m = 1; m < 32; m <<= 1) {
+            const Two o = {__shfl_down_sync(0xffffffffu, sum.hi, m), __shfl_down_sync(0xffffffffu, sum.lo, m)};
+            if (l + m < 32) sum = add(sum, o);
+        }
+        sum = add(sum, Two{(part[0] + part[1]) + (part[2] + part[3]), 0.f});
+        dg[0] = sum.hi;
+        dg[1] = add(sum, Two{-own[2 * l], 0.f}).hi;
+    } else {
+        // What passes token t, of which each part has e^g as a factor: with F_ij what token j writes and i > j reads,
+        // F_i what i reads of the state before the chunk, F^j what is left of j's at the end, F that state's rest there,
+        // dg_t = sum over i >= t, j < t of F_ij + sum over i >= t of F_i + sum over j < t of F^j + F.
+        ends = 0.f;
+        float f0[2] = {0.f, 0.f}, f1[2] = {0.f, 0.f};  // F_i, F^j
+        auto as_rows = [&](float (&f)[8][4], const Ten<const E>& t, long long head, int blk, int width) {
+            Rows<E> o;
+            load_rows(o, t.row0(b, head, t0) + blk * kC, t.st, t.pair, rb, ln, live, width - blk * kC);
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const Two o = {__shfl_down_sync(0xffffffffu, sum.hi, m), __shfl_down_sync(0xffffffffu, sum.lo, m)};
-        if (l + m < 32) sum = add(sum, o);
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
+        };
+        auto dot = [&](float (&to)[2], const float (&p)[8][4], const float (&q)[8][4], const float* f, float one) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float u = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) u = fmaf(p[nt][2 * hf], q[nt][2 * hf], fmaf(p[nt][2 * hf + 1], q[nt][2 * hf + 1], u));
+                to[hf] = fmaf(u, f[16 * rb + ln.r + 8 * hf] * one, to[hf]);
+            }
+        };
+        float f[8][4], t[8][4];
+#pragma unroll 1
+        for (int sb = 0; sb < NV; ++sb) {
+            zero(x);
+            zero(d);
+            zero(t);
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) {
+                as_rows(f, a.q, hk, kb, dk);
+                bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
+                mmr<3, false, true>(x, f, Ws, ln);
+                mm<PI, 3, false, false>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
+                bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
+                mm<PI, 3, false, false>(t, Ks + kb * PI * kPlane, rb, Ws, ln);
+                meet(W, St + (sb * NK + kb) * (3 * kPlane));
+            }
+            as_rows(f, a.dout, h, sb, dv);
+            dot(f0, x, f, s.eG, a.n.scale);
+            get_planes<3>(Zt + sb * 3 * kPlane, rb, f, ln);
+            dot(f0, d, f, s.eG, -1.f);
+            get_planes<3>(Et + sb * 3 * kPlane, rb, f, ln);
+            dot(f1, t, f, s.bw, 1.f);
+        }
+        ends *= s.eC;
+        sum_ends();
+        zero(x);
+        zero(d);
+#pragma unroll 1
+        for (int kb = 0; kb < NK; ++kb) {
+            as_rows(f, a.q, hk, kb, dk);
+            mmr<PI, false, true>(x, f, Ks + kb * PI * kPlane, ln);
+            mm<PI, PI, false, false>(d, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
+        }
+        zero(t);
+        zero(H);
+#pragma unroll 1
+        for (int sb = 0; sb < NV; ++sb) {
+            as_rows(f, a.dout, h, sb, dv);
+            mmr<3, false, true>(t, f, Es0 + sb * 3 * kPlane, ln);
+            mm<3, 3, false, false>(H, Zs0 + sb * 3 * kPlane, rb, Es0 + sb * 3 * kPlane, ln, 0, 4, 0, rb + 1);
+        }
+        f0[0] = row_sum(f0[0]), f0[1] = row_sum(f0[1]), f1[0] = row_sum(f1[0]), f1[1] = row_sum(f1[1]);
+        __syncthreads();  // W is read
+        float* at_t = reinterpret_cast<float*>(W);  // [4][kC], a warp's rows' part of dg
+        float before[2] = {f0[0], f0[1]};           // F_i and the sum over columns before nt's
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = 16 * rb + ln.r + 8 * hf, j = 8 * nt + 2 * ln.j;
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    v[e] = j + e < i ? decay(s, i, j + e) * s.beta[j + e] * fmaf(t[nt][2 * hf + e] * a.n.scale, x[nt][2 * hf + e], -H[nt][2 * hf + e] * d[nt][2 * hf + e]) : 0.f;
+                float upto = v[0] + v[1];
+#pragma unroll
+                for (int m = 1; m < 4; m <<= 1) {
+                    const float o = __shfl_up_sync(0xffffffffu, upto, m, 4);
+                    if (ln.j >= m) upto += o;
+                }
+                const float all = __shfl_sync(0xffffffffu, upto, 3, 4), prev = __shfl_up_sync(0xffffffffu, upto, 1, 4);
+                const float c0 = before[hf] + (ln.j ? prev : 0.f);
+                if (j <= i) sum[0] += c0;
+                if (j + 1 <= i) sum[1] += c0 + v[0];
+                before[hf] += all;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int m = 4; m < 32; m <<= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], m);
+                if (ln.r == 0) at_t[rb * kC + 8 * nt + 2 * ln.j + e] = sum[e];
+            }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+            if (ln.j == 0) own[16 * rb + ln.r + 8 * hf] = f1[hf];
+        __syncthreads();
+        if (threadIdx.x >= 32) return;
+        float upto = own[2 * l] + own[2 * l + 1];
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float o = __shfl_up_sync(0xffffffffu, upto, m);
+            if (l >= m) upto += o;
+        }
+        float left = __shfl_up_sync(0xffffffffu, upto, 1);
+        if (l == 0) left = 0.f;
+        left += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float* p = at_t + 2 * l + e;
+            dg[e] = (p[0] + p[kC]) + (p[2 * kC] + p[3 * kC]) + left + (e ? own[2 * l] : 0.f);
+        }
     }
-    sum = add(sum, Two{(part[0] + part[1]) + (part[2] + part[3]), 0.f});
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int t = 2 * l + e;
@@ -381,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         *a.dbeta.row0(b, h, t0 + t) = in ? dbe[t] : 0.f;
         // a decay of 0 keeps nothing: its gradient is 0, not what rounding leaves of the sum
         const bool kept = in && !(expf(*a.g.row0(b, h, t0 + t)) == 0.f);
-        *a.dg.row0(b, h, t0 + t) = kept ? (e ? add(sum, Two{-own[2 * l], 0.f}) : sum).hi : 0.f;
+        *a.dg.row0(b, h, t0 + t) = kept ? dg[e] : 0.f;
     }
 }
 
