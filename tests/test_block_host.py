@@ -171,6 +171,26 @@ def test_delta_rule_workspace():
     assert F.falcon_gdr_workspace_bytes(_dims(hk=4), True) < m
 
 
+def test_delta_rule_segments():
+    """Whether a sequence is cut shows in the workspace: two scans side by side fill the GPU with half the sequences."""
+    kib, up = 1024, lambda n: (n + 255) // 256 * 256  # noqa: E731
+
+    def uncut(bh, chunks, tiles, rows, bwd):  # X, M, A, S; dA, dS
+        per = 24 + 24 * tiles * tiles + 16 * tiles * rows + (16 + 24) * tiles * rows * bwd
+        return up(bh * chunks * per * kib) + up(bh * (chunks + 1) * 24 * tiles * rows * kib)
+
+    def whole(bh, chunks, d, bwd):
+        n = F.falcon_gdr_workspace_bytes(_dims(b=1, h=bh, hk=bh, t=64 * chunks, dk=d, dv=d), bwd)
+        least = uncut(bh, chunks, (d + 63) // 64, (d + 63) // 64, bwd)
+        assert n >= least
+        return n == least
+
+    # 64 chunks of one scan, a step 1.5 us alone on an SM and 2.6 where two share it: 96 us uncut
+    assert whole(48, 64, 64, True) and whole(16, 128, 128, True)
+    assert whole(96, 16, 64, False) and whole(96, 16, 64, True)
+    assert not whole(2, 64, 64, True) and not whole(12, 1024, 64, False) and not whole(12, 1024, 64, True)
+
+
 def test_delta_rule_written_buffers_overlap_nothing():
     assert fwd(out=A) == INV and fwd(S_final=A + 5 * GB) == INV
     assert fwd(S0=A + 11 * GB, S_final=A + 11 * GB + 16) == INV

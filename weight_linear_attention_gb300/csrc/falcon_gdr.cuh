@@ -1215,11 +1215,12 @@ __global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scans(const
 
 // The scan's segments, for as few microseconds as the steps make: one of the states takes 1.5 with a CTA an SM, 2.6 with the
 // two that fit, one of a segment's map, which writes nothing, 1.3 and 2.1; wide heads have an SM to themselves, 4.5 and 4. A
-// scan over the segments' maps and two more launches come on top. (12 heads, 1024 chunks: 25 segments.)
+// scan over the segments' maps and two more launches come on top. (12 heads, 1024 chunks: 25 segments.) A backward call has two
+// scans side by side, which share the map's product of M.
 struct Cut {
     int L, nseg;
 };
-inline Cut cut_of(long long BH, int NC, int NK, int NV) {
+inline Cut cut_of(long long BH, int NC, int NK, int NV, int scans) {
     auto step = [&](long long ctas, double one, double two, double wide) {
         const long long n = (ctas + 151) / 152;  // of the fullest SM
         return NK == 1 ? (double)(n / 2) * two + (double)(n % 2) * one : (double)n * wide;
@@ -1227,10 +1228,10 @@ inline Cut cut_of(long long BH, int NC, int NK, int NV) {
     auto own = [&](long long ctas) { return step(ctas, 1.5, 2.6, 4.5); };
     auto map = [&](long long ctas) { return step(ctas, 1.3, 2.1, 4.0); };
     Cut best = {NC > 0 ? NC : 1, 1};
-    double least = NC * own(BH * NV);
+    double least = NC * own(BH * NV * scans);
     for (int s = 2; s <= 64 && s * 4 <= NC; ++s) {
         const int L = (NC + s - 1) / s, nseg = (NC + L - 1) / L;
-        const double c = L * (map(BH * nseg * (NV + NK)) + own(BH * nseg * NV)) + own(BH * NV) * nseg + 8;
+        const double c = L * (map(BH * nseg * (NV * scans + NK)) + own(BH * nseg * NV * scans)) + own(BH * NV * scans) * nseg + 8;
         if (c < least) least = c, best = Cut{L, nseg};
     }
     return best;
@@ -1248,7 +1249,7 @@ inline Layout layout_of(const GdrSizes& n, bool bwd) {
     l.NV = (n.dv + kC - 1) / kC;
     l.NC = (n.T + kC - 1) / kC;
     const long long BH = n.B * n.H, sq = (long long)l.NK * l.NK, st = (long long)l.NV * l.NK;
-    l.cut = cut_of(BH, l.NC, l.NK, l.NV);
+    l.cut = cut_of(BH, l.NC, l.NK, l.NV, bwd ? 2 : 1);
     long long at = 0;
     auto take = [&](long long bytes) {
         const long long o = at;
