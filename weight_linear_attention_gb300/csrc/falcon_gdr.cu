@@ -20,29 +20,35 @@ struct OutArgs {
     const uint8_t *X, *S;
 };
 
-// acc += K S and o += Q S (S stored [n][k]): S is fetched once.
-template <int PA, int PB>
+// acc += K S and o += Q S (S stored [n][k]): S is fetched once; twice from fp32 inputs, whose small products come first.
+template <int PA, int WHICH = kAll>
 __device__ __forceinline__ void mm_both(float (&acc)[8][4], float (&o)[8][4], uint32_t K, uint32_t Q, int rb, uint32_t S, const Lane& ln) {
+    if constexpr (PA == 3 && WHICH == kAll) {
+        mm_both<PA, kSmall>(acc, o, K, Q, rb, S, ln);
+        mm_both<PA, kGreat>(acc, o, K, Q, rb, S, ln);
+        return;
+    }
+    constexpr int NA = WHICH == kGreat ? 1 : PA, NB = WHICH == kGreat ? 1 : 3;
 #pragma unroll 1
     for (int kk = 0; kk < 4; ++kk) {
-        uint32_t a[PA][4], q[PA][4];
+        uint32_t a[NA][4], q[NA][4];
         const uint32_t at = (16 * rb + ln.l7 + 8 * ln.l8) * 128 + (((2 * kk + ln.l16) ^ ln.l7) << 4);
 #pragma unroll
-        for (int m = 0; m < PA; ++m) {
+        for (int m = 0; m < NA; ++m) {
             ldm<false>(a[m], K + at + m * kPlane);
             ldm<false>(q[m], Q + at + m * kPlane);
         }
         const uint32_t row = S + (8 * ln.l16 + ln.l7) * 128 + (((2 * kk + ln.l8) ^ ln.l7) << 4);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            uint32_t v[PB][4];
+            uint32_t v[NB][4];
 #pragma unroll
-            for (int m = 0; m < PB; ++m) ldm<false>(v[m], row + m * kPlane + p * 2048);
+            for (int m = 0; m < NB; ++m) ldm<false>(v[m], row + m * kPlane + p * 2048);
 #pragma unroll
-            for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
+            for (int s = NB - 1; s >= (WHICH == kSmall ? 1 : 0); --s)
 #pragma unroll
-                for (int ma = 0; ma < PA; ++ma) {
-                    if (s < ma || s - ma >= PB) continue;
+                for (int ma = 0; ma < NA; ++ma) {
+                    if (s < ma) continue;
                     mma(acc[2 * p], a[ma], v[s - ma][0], v[s - ma][1]);
                     mma(acc[2 * p + 1], a[ma], v[s - ma][2], v[s - ma][3]);
                     mma(o[2 * p], q[ma], v[s - ma][0], v[s - ma][1]);
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
             }
             wait<0>();
             __syncthreads();
-            mm_both<PI, 3>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+            mm_both<PI>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
         }
         __syncthreads();
 #pragma unroll
