@@ -426,7 +426,8 @@ typedef struct {
  *   weight    fp32 [d] or NULL (1)
  *   h         [B,T,d] dtype or NULL; only with a residual. May be x or residual (same pointer and strides)
  *   scales    fp32 [B,T] if y is FALCON_E4M3, else NULL: a token's scale is its largest |y| / 448, and y holds the
- *             nearest values of y / scale (ties to even; zeros, and scale 0, where all are 0; NaN stays NaN)
+ *             nearest values of y / scale as fp32 has that quotient (ties to even; zeros, and scale 0, where all
+ *             are 0; NaN stays NaN)
  *   strides   of x, residual, h, y (8 values) or NULL
  * Rows behind a sequence's length are written as zeros, their h and scales too. Statistics are fp32: where a row's
  * squares' sum overflows, y is 0.

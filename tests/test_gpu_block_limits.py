@@ -8,6 +8,7 @@ import torch
 
 from oracle import block_ref as R
 from tests.test_gpu_block import DT, backward, forward, inputs
+from weight_linear_attention_gb300 import falcon as F
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +142,26 @@ def test_gdr_dg_of_strong_decays_among_weak_ones(dt, shared):
         near(f"dg at {g}", got["dg"][:, h:h + 1, strong], want["dg"][:, h:h + 1, strong], room=room)
         weak = ~strong & (torch.arange(T) != 101)
         near(f"dg beside {g}", got["dg"][:, h:h + 1, weak], want["dg"][:, h:h + 1, weak], room=R.NEAR_DG)
+
+
+@pytest.mark.parametrize("d", [100, 768, 4096, 8200])
+def test_rms_8_bits_are_those_of_the_quotient(d):
+    """Value by value: the fp32 call's y by the scale, rounded once more. Rows of every size, one with an infinity."""
+    r = torch.Generator().manual_seed(d)
+    x = torch.randn(1, 4000, d, generator=r).cuda()
+    x[0, 7] = 0
+    w = torch.randn(d, generator=r) * 2.0 ** torch.randint(-20, 20, (d,), generator=r)
+    for w in (w, w * 1e31, w * 1e-32):
+        y, _, _ = F.rmsnorm_forward(x, w.cuda())
+        y8, _, s = F.rmsnorm_forward(x, w.cuda(), out_dtype=torch.float8_e4m3fn)
+        top = y.abs().amax(-1)
+        # the scale is the nearest fp32 value of the largest |y| / 448 but for subnormal ones (torch multiplies by 1 / 448 where
+        # 448 is a number)
+        assert torch.equal(s, top / torch.full_like(top, 448)) if top[top > 0].min() > 1e-35 else torch.allclose(s, top / 448, rtol=1e-6, atol=1e-44)
+        want = torch.where(s[..., None] > 0, y / s[..., None], 0.0).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert torch.equal(y8.view(torch.uint8) & 0x7f, want.view(torch.uint8) & 0x7f) and torch.equal(y8.float(), want.float())
+    w = torch.ones(d)
+    w[3] = math.inf
+    y8, _, s = F.rmsnorm_forward(x[:, :5], w.cuda(), out_dtype=torch.float8_e4m3fn)
+    y8 = y8.float()
+    assert torch.isinf(s).all() and torch.isnan(y8[..., 3]).all() and not y8[..., :3].any() and not y8[..., 4:].any()

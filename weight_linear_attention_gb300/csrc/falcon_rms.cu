@@ -184,17 +184,29 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Arg
             const float exact = near < 3.4e38f ? fmaf(fmaf(-near, 448.f, top[0]), 1.f / 448.f, near) : near;  // its last bit
             const float scale = now.live ? exact : 0.f;
             if (first == 0) a.scales[here] = scale;
-            // 1 / scale where it is not near overflow (NaN too), else the quotients themselves; a row of zeros stays 0. (The
-            // quotients everywhere, 89 us for 16384 x 4096 against 80, meet the nearest value as often.)
-            const bool tiny = scale < 1e-37f;
-            const float inv = tiny ? 0.f : 1.f / scale;
+            // The quotient, correctly rounded: by 1 / scale and what is left of it where both are finite (80 us for 16384 x 4096,
+            // 89 by division), else by division; a row of zeros stays 0.
+            const bool plain = !(scale >= 1e-37f && scale < 3.4e38f);
+            const float inv = plain ? 0.f : 1.f / scale;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (first + i * step >= count) continue;
                 float q[W];
+                const float* v = h + i * W;
+                if (plain) {
 #pragma unroll
-                for (int e = 0; e < W; ++e)
-                    q[e] = !now.live ? 0.f : !tiny ? h[i * W + e] * inv : scale > 0.f ? h[i * W + e] / scale : 0.f;
+                    for (int e = 0; e < W; ++e) q[e] = !now.live || scale == 0.f ? 0.f : v[e] / scale;
+                } else if (W == 1) {
+                    q[0] = v[0] * inv;
+                    q[0] = fmaf(fmaf(-q[0], scale, v[0]), inv, q[0]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e + 1 < W; e += 2) {
+                        const float2 x2 = pair(v[e], v[e + 1]), f = pair(inv, inv), near2 = mul2(x2, f);
+                        const float2 r2 = fma2(fma2(near2, pair(-scale, -scale), x2), f, near2);
+                        q[e] = r2.x, q[e + 1] = r2.y;
+                    }
+                }
                 store8<W>(static_cast<uint8_t*>(a.y.p) + oy + (long long)(first + i * step) * W, q);
             }
         }
