@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Arg
             const float exact = near < 3.4e38f ? fmaf(fmaf(-near, 448.f, top[0]), 1.f / 448.f, near) : near;  // its last bit
             const float scale = now.live ? exact : 0.f;
             if (first == 0) a.scales[here] = scale;
-            // The quotient, correctly rounded: by 1 / scale and what is left of it where both are finite (80 us for 16384 x 4096,
+            // The quotient, correctly rounded: by 1 / scale and what is left of it where both are finite (73 us for 16384 x 4096,
             // 89 by division), else by division; a row of zeros stays 0.
             const bool plain = !(scale >= 1e-37f && scale < 3.4e38f);
             const float inv = plain ? 0.f : 1.f / scale;
