@@ -144,6 +144,11 @@ def test_delta_rule_nothing_to_do():
         assert fwd(scale=s) == INV and bwd(scale=s) == INV
 
 
+def test_delta_rule_takes_every_finite_scale():
+    for x in (3.4028234e38, -3.4028234e38, 1e-45, 0.0):
+        assert fwd(dims=_dims(b=0), ws=None, scale=x) == OK and bwd(dims=_dims(b=0), ws=None, scale=x) == OK
+
+
 def test_delta_rule_missing_and_misaligned():
     for name in ("q", "k", "v", "beta", "g", "out"):
         assert fwd(**{name: None}) == INV, name

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "falcon.h"
 #include "falcon_check.h"
 #include "falcon_gdr.h"
@@ -51,7 +53,7 @@ struct GdrChecker : Checker {
     }
 };
 
-bool good_scale(float s) { return s > -3.4e38f && s < 3.4e38f; }
+bool good_scale(float s) { return std::isfinite(s); }
 
 int sizes_of(const falcon_rms_dims_t* d, falcon::RmsArgs* a) {
     if (!d || d->batch < 0 || d->seqlen < 0 || d->d <= 0) return FALCON_ERR_INVALID_ARG;
