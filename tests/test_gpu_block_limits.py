@@ -63,6 +63,19 @@ def test_gdr_backward_keeps_fp32s_bits(dt, size, shared):
     near("dg", got["dg"], want["dg"], room=R.NEAR_DG, size=terms_of_dg(p, a, want))
 
 
+@pytest.mark.parametrize("size", [(1, 2, 156, 128, 128), (2, 1, 459, 32, 128), (2, 3, 66, 100, 64), (1, 2, 300, 64, 64)], ids=str)
+def test_gdr_sums_of_products_keep_fp32s_bits(size):
+    """Results that are sums of products (two blocks of a wide head, dk's four terms): half of the bound, 16 U, which is one and
+    a half of the 11 U that it stands on. Small products that were added to a whole sum left 12 to 20 U."""
+    p, a = inputs(*size, torch.float32, 46)
+    out, S = forward(p)
+    got = dict(backward(p, a), out=out, S_final=S)
+    want = R.gdr_backward(p["q"], p["k"], p["v"], p["beta"], p["g"], a["dout"], p["S0"], a["dS_final"])
+    want["out"], want["S_final"] = R.gdr_forward(**p)
+    for name in ("out", "S_final", "dq", "dk", "dv", "dbeta", "dS0"):
+        near(name, got[name], want[name], room=R.NEAR / 2)
+
+
 def terms_of_dg(p, a, want):
     """The norm of what dg is summed from: dq.q (of heads that share a key each for itself) and dv.v."""
     q, k = (p[x].repeat_interleave(p["v"].shape[1] // p[x].shape[1], 1) for x in ("q", "k"))

@@ -1,6 +1,8 @@
 // Gated delta rule, forward: the chunks' maps (gdr_prep), the scan over them (gdr_scan), the outputs (gdr_out), and
 // short sequences token by token (gdr_step). The algebra is in falcon_gdr.cuh.
 
+#include <type_traits>
+
 #include "falcon.h"
 #include "falcon_gdr.cuh"
 #include "falcon_gdr_bwd.cuh"
@@ -105,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
     float P[8][4];
     zero(P);
 #pragma unroll 1
-    for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Qs + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
+    for (int kb = 0; kb < NK; ++kb)
+        sum<NK * PI == 6>(P, [&](float (&x)[8][4]) { mm<PI, PI, false, false>(x, Qs + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1); });
     times_decay<false, false>(P, s, rb, ln, nullptr, a.n.scale);
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
@@ -114,16 +117,33 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
         load_rows(v, a.v.row0(b, h, t0) + sb * kC, a.v.st, a.v.pair, rb, ln, live, a.n.dv - sb * kC);
         zero(acc);
         zero(o);
-#pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) {
-            if (sb + kb > 0) {
+        auto state = [&](int kb, auto planes) {  // its tile (sb, kb) in W
+            constexpr int N = decltype(planes)::value;
+            if (sb + kb > 0 || N == 1) {
                 __syncthreads();
-                copy_planes<3>(Ws, St + (sb * NK + kb) * (3 * kPlane));
+                copy_planes<N>(Ws, St + (sb * NK + kb) * (3 * kPlane));
                 commit();
             }
             wait<0>();
             __syncthreads();
-            mm_both<PI>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+        };
+        if constexpr (NK * PI == 6) {  // fp32's wide heads: both tiles' small products first
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) {
+                state(kb, std::integral_constant<int, 3>{});
+                mm_both<PI, kSmall>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+            }
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) {
+                state(kb, std::integral_constant<int, 1>{});
+                mm_both<PI, kGreat>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+            }
+        } else {
+#pragma unroll 1
+            for (int kb = 0; kb < NK; ++kb) {
+                state(kb, std::integral_constant<int, 3>{});
+                mm_both<PI>(acc, o, Ks + kb * PI * kPlane, Qs + kb * PI * kPlane, rb, Ws, ln);
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -151,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
         const bool written = all_finite(acc);
         put_planes(W, rb, acc, ln);
         __syncthreads();
-        mmr_lower(o, P, Ws, rb, ln, written);
+        sum<PI == 3>(o, [&](float (&x)[8][4]) { mmr_lower(x, P, Ws, rb, ln, written); });
         write_rows(a.out.row0(b, h, t0) + sb * kC, a.out.st, a.out.pair, rb, o, ln, rows, live, a.n.dv - sb * kC);
     }
 }

@@ -88,11 +88,12 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&p)[3]) {
     }
 }
 
-// Which products of planes: all of them, or those below the first two's, or theirs alone, or first the ones and then the other. The tensor cores cut sums off, a
-// unit at a time: of fp32 operands the small products of all k steps come first, while the sums are small, and leave four
-// cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm instead of 6e-7). kOrdered: so for other
-// operands, too, where a product goes into dg, in which what it is made of cancels (5e-7 instead of 1e-6; 4 % of the
-// gradients' kernel).
+// Which products of planes: all of them, or those below the first two's, or theirs alone, or first the ones and then the
+// other. The tensor cores cut sums off, a unit at a time: of fp32 operands the small products of all k steps come first,
+// while the sums are small, and leave four cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm
+// instead of 6e-7). What is added to such a result is made by itself and added in fp32 (`sum`), for what its small products cut off
+// would be units of the whole (wide heads' results 7e-7 to 1.2e-6 so, 2 to 4e-7 by itself). kOrdered: the order for other operands, too,
+// where a product goes into dg, in which what it is made of cancels (5e-7 instead of 1e-6; 4 % of the gradients' kernel).
 enum { kAll = 0, kSmall = 1, kGreat = 2, kOrdered = 3 };
 
 // One k step of 16: acc (16 rows x 64 columns, column groups of 16 in [p0, p1)) += a B. B, its planes at `b`, is stored
@@ -301,6 +302,21 @@ __device__ __forceinline__ void zero(float (&acc)[8][4]) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+}
+// acc += make(t), t from zero: SEP, or into acc.
+template <bool SEP, typename F>
+__device__ __forceinline__ void sum(float (&acc)[8][4], F make) {
+    if constexpr (!SEP) {
+        make(acc);
+    } else {
+        float t[8][4];
+        zero(t);
+        make(t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] += t[i][e];
+    }
 }
 // Rows 16 rb .. of an fp32 tile from and to a product's registers: acc[nt][e] is row 16 rb + r + 8 (e / 2), column
 // 8 nt + 2 j + e % 2.
@@ -912,7 +928,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
     {  // N diag(beta)
         zero(acc);
 #pragma unroll 1
-        for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(acc, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
+        for (int kb = 0; kb < NK; ++kb)
+            sum<NK * PI == 6>(acc, [&](float (&t)[8][4]) { mm<PI, PI, false, false>(t, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1); });
         times_decay<false, true>(acc, s, rb, ln, s.beta, 1.f);
         put(T, rb, acc, ln);
     }
@@ -986,7 +1003,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(prep_smem<E, NK, BWD>())) gd
             float P[8][4];  // scale D_ij q_i.k_j, transposed: rows j, columns i >= j
             zero(P);
 #pragma unroll 1
-            for (int kb = 0; kb < NK; ++kb) mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4);
+            for (int kb = 0; kb < NK; ++kb)
+                sum<NK * PI == 6>(P, [&](float (&x)[8][4]) { mm<PI, PI, false, false>(x, Ks + kb * PI * kPlane, rb, Qs + kb * PI * kPlane, ln, 0, 4, rb, 4); });
             times_decay<true, false>(P, s, rb, ln, nullptr, a.n.scale);
             zero(acc);
             mmr<PI, true, BWD>(acc, P, Os, ln, rb, 4);
@@ -1143,7 +1161,7 @@ __device__ __forceinline__ void scan(const ScanArgs& a, uint8_t* smem) {
                 }
                 if (!MAP) asm volatile("bar.arrive 1, %0;" ::"n"(kScanThreads) : "memory");
             }
-            mmr<3, REV>(nw[kb], acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln);
+            sum<(NK > 1)>(nw[kb], [&](float (&x)[8][4]) { mmr<3, REV>(x, acc[kc], saddr(smem) + ((i * NB + t) % R) * (3 * kPlane), ln); });
         }
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {

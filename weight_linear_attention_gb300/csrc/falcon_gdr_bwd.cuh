@@ -15,6 +15,8 @@
 
 #pragma once
 
+#include <type_traits>
+
 #include "falcon.h"
 #include "falcon_gdr.cuh"
 
@@ -55,6 +57,7 @@ template <typename E, int NK, int NV>
 __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr_grad(const GradArgs<E> a) {
     constexpr bool ONE = grad_one<E, NK, NV>(), KEEPS = grad_keeps<E>();
     constexpr int PI = planes<E>();
+    constexpr bool SEP = PI == 3;  // what is added to a product's result is made by itself
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scal s;
     __shared__ float own[kC], dbe[kC], part[kThreads / 32];
@@ -99,6 +102,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
     const uint8_t* Xt = a.X + (bh * a.n.NC + c) * (3 * kPlane);
     auto load_q = [&](uint8_t* to, int kb) {
         load_planes(to, a.q.row0(b, hk, t0) + kb * kC, a.q.st, live, dk - kb * kC, a.q.vec);
+    };
+    // a warp's own rows, 64 channels of them
+    auto rows_of = [&](float (&f)[8][4], const Ten<const E>& t, long long head, int blk, int width) {
+        Rows<E> o;
+        load_rows(o, t.row0(b, head, t0) + blk * kC, t.st, t.pair, rb, ln, live, width - blk * kC);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
     };
     // a tile of planes that every warp then reads
     auto bring = [&](uint32_t to, const uint8_t* from) {
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             wait<1>();
         }
         __syncthreads();
-        mm<PI, PI, false, false>(P, Ks + kb * PI * kPlane, rb, Ws, ln, 0, 4, rb, 4);
+        sum<SEP && NK == 2>(P, [&](float (&t)[8][4]) { mm<PI, PI, false, false>(t, Ks + kb * PI * kPlane, rb, Ws, ln, 0, 4, rb, 4); });
     }
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
@@ -211,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
                 bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
-                mm<PI, 3, false, false, kOrdered>(x, Ks + kb * PI * kPlane, rb, Ws, ln);
+                sum<SEP && NK == 2>(x, [&](float (&t)[8][4]) { mm<PI, 3, false, false, kOrdered>(t, Ks + kb * PI * kPlane, rb, Ws, ln); });
                 bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
-                mm<PI, 3, false, false, kOrdered>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
+                sum<SEP && NK == 2>(d, [&](float (&t)[8][4]) { mm<PI, 3, false, false, kOrdered>(t, Ks + kb * PI * kPlane, rb, Ws, ln); });
                 meet(W, St + st + (sb * NK + kb) * (3 * kPlane));
             }
         }
@@ -221,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[nt][e] *= s.w[16 * rb + ln.r + 8 * (e >> 1)];
-        mmr<PI, true, true, kOrdered>(d, P, adjoint(sb), ln, rb, 4);  // dU
+        const uint32_t Ob = adjoint(sb);
+        sum<SEP>(d, [&](float (&t)[8][4]) { mmr<PI, true, true, kOrdered>(t, P, Ob, ln, rb, 4); });  // dU
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const float eG = s.eG[16 * rb + ln.r + 8 * hf];
@@ -280,10 +293,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
 #pragma unroll 1
     for (int sb = 0; sb < NV; ++sb) {
         const uint32_t Es = Es0 + sb * 3 * kPlane, Zs = Zs0 + sb * 3 * kPlane, Ob = adjoint(sb);
-        mm<PI, 3, false, false, kOrdered>(A1, Ob, rb, Es, ln, 0, 4, 0, rb + 1);
-        mm<3, PI, false, false>(A3, Es, rb, Ob, ln, 0, 4, rb, 4);
-        mm<3, 3, false, false>(H, Zs, rb, Es, ln, 0, 4, 0, rb + 1);
-        mm<3, 3, false, false>(x, Es, rb, Zs, ln, 0, 4, rb, 4);
+        sum<SEP && NV == 2>(A1, [&](float (&t)[8][4]) { mm<PI, 3, false, false, kOrdered>(t, Ob, rb, Es, ln, 0, 4, 0, rb + 1); });
+        sum<SEP && NV == 2>(A3, [&](float (&t)[8][4]) { mm<3, PI, false, false>(t, Es, rb, Ob, ln, 0, 4, rb, 4); });
+        sum<SEP && NV == 2>(H, [&](float (&t)[8][4]) { mm<3, 3, false, false>(t, Zs, rb, Es, ln, 0, 4, 0, rb + 1); });
+        sum<SEP && NV == 2>(x, [&](float (&t)[8][4]) { mm<3, 3, false, false>(t, Es, rb, Zs, ln, 0, 4, rb, 4); });
     }
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
@@ -319,24 +332,26 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 for (int e = 0; e < 4; ++e) x[nt][e] = q1[nt][e];
         } else {
             zero(x);
+            // SEP and two tiles: the small products of both come first (in registers of their own there is no room for them)
+            auto tiles = [&](auto which) {
+                constexpr int WH = decltype(which)::value;
 #pragma unroll 1
-            for (int sb = 0; sb < NV; ++sb) {
-                Rows<E> o;
-                if (!KEEPS) load_rows(o, a.dout.row0(b, h, t0) + sb * kC, a.dout.st, a.dout.pair, rb, ln, live, dv - sb * kC);
-                bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
-                if (KEEPS) {
-                    mm<PI, 3, false, true, kOrdered>(x, Os + sb * PI * kPlane, rb, Ws, ln);
-                } else {
+                for (int sb = 0; sb < NV; ++sb) {
                     float f[8][4];
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
-                    mmr<3, true, true>(x, f, Ws, ln);
+                    if (!KEEPS) rows_of(f, a.dout, h, sb, dv);
+                    bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
+                    if (KEEPS) mm<PI, 3, false, true, WH == kAll ? kOrdered : WH>(x, Os + sb * PI * kPlane, rb, Ws, ln);
+                    else mmr<3, true, true, WH>(x, f, Ws, ln);
+                    mm<3, 3, false, true, WH>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
+                    bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
+                    mm<3, 3, false, true, WH>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
                 }
-                mm<3, 3, false, true>(d, Zs0 + sb * 3 * kPlane, rb, Ws, ln);
-                bring(Ws, dSt + (sb * NK + kb) * (3 * kPlane));
-                mm<3, 3, false, true>(t, Es0 + sb * 3 * kPlane, rb, Ws, ln);
+            };
+            if constexpr (SEP && NV == 2) {
+                tiles(std::integral_constant<int, kSmall>{});
+                tiles(std::integral_constant<int, kGreat>{});
+            } else {
+                tiles(std::integral_constant<int, kAll>{});
             }
             __syncthreads();
             load_q(W, kb);
@@ -350,12 +365,19 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 x[nt][e] *= s.eG[row] * a.n.scale;
                 d[nt][e] = fmaf(s.bw[row], t[nt][e], -s.eG[row] * d[nt][e]);
             }
-        mmr<PI, true, true, kOrdered>(x, A1, Ks + kb * PI * kPlane, ln, 0, rb + 1);
+        const uint32_t Kb = Ks + kb * PI * kPlane;
+        sum<SEP>(x, [&](float (&u)[8][4]) { mmr<PI, true, true, kOrdered>(u, A1, Kb, ln, 0, rb + 1); });
         write_qk(a.dq, a.pq, x, kb);
-        mmr<PI, true, true>(d, H, Ks + kb * PI * kPlane, ln);
-        wait<0>();
-        __syncthreads();
-        mmr<PI, true, true>(d, A3, Ws, ln, rb, 4);
+        sum<SEP>(d, [&](float (&u)[8][4]) {
+            mmr<PI, true, true, SEP ? kSmall : kAll>(u, H, Kb, ln);
+            wait<0>();
+            __syncthreads();
+            mmr<PI, true, true, SEP ? kSmall : kAll>(u, A3, Ws, ln, rb, 4);
+            if constexpr (SEP) {
+                mmr<PI, true, true, kGreat>(u, H, Kb, ln);
+                mmr<PI, true, true, kGreat>(u, A3, Ws, ln, rb, 4);
+            }
+        });
         write_qk(a.dk, a.pk, d, kb);
         get_planes<PI>(W, rb, t, ln);
 #pragma unroll
@@ -396,14 +418,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         // dg_t = sum over i >= t, j < t of F_ij + sum over i >= t of F_i + sum over j < t of F^j + F.
         ends = 0.f;
         float f0[2] = {0.f, 0.f}, f1[2] = {0.f, 0.f};  // F_i, F^j
-        auto as_rows = [&](float (&f)[8][4], const Ten<const E>& t, long long head, int blk, int width) {
-            Rows<E> o;
-            load_rows(o, t.row0(b, head, t0) + blk * kC, t.st, t.pair, rb, ln, live, width - blk * kC);
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[nt][e] = e & 1 ? o.of(nt, e >> 1).y : o.of(nt, e >> 1).x;
-        };
         auto dot = [&](float (&to)[2], const float (&p)[8][4], const float (&q)[8][4], const float* f, float one) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
             zero(t);
 #pragma unroll 1
             for (int kb = 0; kb < NK; ++kb) {
-                as_rows(f, a.q, hk, kb, dk);
+                rows_of(f, a.q, hk, kb, dk);
                 bring(Ws, St + (sb * NK + kb) * (3 * kPlane));
                 mmr<3, false, true>(x, f, Ws, ln);
                 mm<PI, 3, false, false>(d, Ks + kb * PI * kPlane, rb, Ws, ln);
@@ -429,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
                 mm<PI, 3, false, false>(t, Ks + kb * PI * kPlane, rb, Ws, ln);
                 meet(W, St + (sb * NK + kb) * (3 * kPlane));
             }
-            as_rows(f, a.dout, h, sb, dv);
+            rows_of(f, a.dout, h, sb, dv);
             dot(f0, x, f, s.eG, a.n.scale);
             get_planes<3>(Zt + sb * 3 * kPlane, rb, f, ln);
             dot(f0, d, f, s.eG, -1.f);
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         zero(d);
 #pragma unroll 1
         for (int kb = 0; kb < NK; ++kb) {
-            as_rows(f, a.q, hk, kb, dk);
+            rows_of(f, a.q, hk, kb, dk);
             mmr<PI, false, true>(x, f, Ks + kb * PI * kPlane, ln);
             mm<PI, PI, false, false>(d, Ks + kb * PI * kPlane, rb, Ks + kb * PI * kPlane, ln, 0, 4, 0, rb + 1);
         }
@@ -450,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(grad_smem<E, NK, NV>())) gdr
         zero(H);
 #pragma unroll 1
         for (int sb = 0; sb < NV; ++sb) {
-            as_rows(f, a.dout, h, sb, dv);
+            rows_of(f, a.dout, h, sb, dv);
             mmr<3, false, true>(t, f, Es0 + sb * 3 * kPlane, ln);
             mm<3, 3, false, false>(H, Zs0 + sb * 3 * kPlane, rb, Es0 + sb * 3 * kPlane, ln, 0, 4, 0, rb + 1);
         }
