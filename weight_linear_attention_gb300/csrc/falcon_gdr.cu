@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(out_smem<E, NK>())) gdr_out(
 
 // ---- short sequences: a CTA holds 64 columns of a head's state, a thread R rows x 4 columns of them (16 threads a row, a
 // warp 2 R whole rows that lie together), and walks the tokens, k and q in shared memory. Bound by the state's bytes, read
-// and written once: 256 x 12 states of 64 x 64 take 17.6 us, 85 % of the copy rate (with a warp's rows 8 apart and k and q
-// in registers 21.7).
+// and written once: 256 x 12 states of 64 x 64 take 19.3 us, 78 % of the copy rate (a warp's rows 8 apart and k and q in
+// registers took 23 % more).
 template <typename E>
 struct StepArgs {
     Sizes n;

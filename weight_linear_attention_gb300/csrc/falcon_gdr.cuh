@@ -11,13 +11,13 @@
 // kernels run for all chunks at once, and only S' = M S + A goes along the sequence.
 //
 // Products: an fp32 operand x enters as bf16 planes of 8 bits each, x = h + m + l, and a product of two as h h + h m +
-// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it. bf16 inputs are their own single plane. An operand is split once, where it is made; the warps' products are
-// loads of matrices and nothing else. (As tf32 pairs, split by every warp that reads them, the gradient kernel took 306 us
-// for 8 x 12 x 1024 x 64, so 246.)
+// m h + m m + h l + l h with fp32 sums, what is left out being a few units of 2^-24 of it. bf16 inputs are their own single
+// plane. An operand is split once, where it is made; the warps' products are loads of matrices and nothing else. (As tf32
+// pairs, split by every warp that reads them, the gradient kernel took 306 us for 8 x 12 x 1024 x 64, so 246.)
 // They are mma.sync products. A chunk is a row of dependent ones of 64 x 64 x 64 with its own arithmetic between them, and
-// what follows a product finds its result in registers; no pipe is busy more than half of the time, the tensor cores 30 %.
+// what follows a product finds its result in registers; no pipe is busy more than half of the time, the tensor cores 30 % (44 with wide heads).
 // On tcgen05, results in tensor memory, the chunk kernels of Falcon-1's backward do the same work with two planes an
-// operand in 89 and 117 ns a chunk (the map, the gradients); these take 66 and 107.
+// operand in 89 and 117 ns a chunk (the map, the gradients); these, with three, take 67 and 137.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -91,9 +91,9 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&p)[3]) {
 // Which products of planes: all of them, or those below the first two's, or theirs alone, or first the ones and then the
 // other. The tensor cores cut sums off, a unit at a time: of fp32 operands the small products of all k steps come first,
 // while the sums are small, and leave four cuts of the result instead of 24 (fp32's forward is off by 3e-7 of its norm
-// instead of 6e-7). What is added to such a result is made by itself and added in fp32 (`sum`), for what its small products cut off
-// would be units of the whole (wide heads' results 7e-7 to 1.2e-6 so, 2 to 4e-7 by itself). kOrdered: the order for other operands, too,
-// where a product goes into dg, in which what it is made of cancels (5e-7 instead of 1e-6; 4 % of the gradients' kernel).
+// instead of 6e-7). What is added to such a result is made by itself and added in fp32 (`sum`), or its small products would
+// be cut by units of the whole (wide heads' results 7e-7 to 1.2e-6 so, 2 to 4e-7 by itself). kOrdered: the order for other
+// operands, too, where a product goes into dg, in which what it is made of cancels (5e-7 instead of 1e-6; 4 % of the gradients' kernel).
 enum { kAll = 0, kSmall = 1, kGreat = 2, kOrdered = 3 };
 
 // One k step of 16: acc (16 rows x 64 columns, column groups of 16 in [p0, p1)) += a B. B, its planes at `b`, is stored
@@ -691,7 +691,7 @@ __device__ __forceinline__ void make_scal(Scal& s, const Gates& r) {
     }
 }
 
-// (The far blocks so, and not by exponentials, save the chunk maps' kernel 2 us of 54 and the outputs' 2 of 38; the gradients'
+// (The far blocks so, and not by exponentials, save the chunk maps' kernel 2 us of 54 and the outputs' 2 as well; the gradients'
 // kernel, which waits for its instructions, does better with fewer of them: 211 us against 241.)
 // A product's rows times D, and times f of the column (of the row, UPPER) or f itself: rows i and columns j <= i, or rows
 // j and columns i >= j (UPPER), STRICT without the diagonal; 0 elsewhere.
@@ -1231,8 +1231,8 @@ __global__ void __launch_bounds__(kScanThreads, NK == 1 ? 2 : 1) gdr_scans(const
     else if (!MAP || (int)blockIdx.y < r.NV) scan<NK, true, MAP>(r, smem);
 }
 
-// The scan's segments, for as few microseconds as the steps make: one of the states takes 1.5 with a CTA an SM, 2.6 with the
-// two that fit, one of a segment's map, which writes nothing, 1.3 and 2.1; wide heads have an SM to themselves, 4.5 and 4. A
+// The scan's segments, for as few microseconds as the steps make: one of the states takes 1.5 with a CTA an SM, 2.8 with the
+// two that fit, one of a segment's map, which writes nothing, 1.3 and 2.1; wide heads have an SM to themselves, 5.1 and 5.2. A
 // scan over the segments' maps and two more launches come on top. (12 heads, 1024 chunks: 25 segments.) A backward call has two
 // scans side by side, which share the map's product of M.
 struct Cut {
@@ -1243,8 +1243,8 @@ inline Cut cut_of(long long BH, int NC, int NK, int NV, int scans) {
         const long long n = (ctas + 151) / 152;  // of the fullest SM
         return NK == 1 ? (double)(n / 2) * two + (double)(n % 2) * one : (double)n * wide;
     };
-    auto own = [&](long long ctas) { return step(ctas, 1.5, 2.6, 4.5); };
-    auto map = [&](long long ctas) { return step(ctas, 1.3, 2.1, 4.0); };
+    auto own = [&](long long ctas) { return step(ctas, 1.5, 2.8, 5.1); };
+    auto map = [&](long long ctas) { return step(ctas, 1.3, 2.1, 5.2); };
     Cut best = {NC > 0 ? NC : 1, 1};
     double least = NC * own(BH * NV * scans);
     for (int s = 2; s <= 64 && s * 4 <= NC; ++s) {

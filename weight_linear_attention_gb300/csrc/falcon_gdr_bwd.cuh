@@ -9,9 +9,10 @@
 // The factor e^{G_i} stands before all that token i reads (out_i, what it predicts), e^{-G_i} before all that it
 // writes, so dG_i = dO_i.out_i - dV_i.V_i = dQ_i.Q_i - dV_i.V_i, and G_C has <dS', S'> besides; dg is the sum of dG
 // from its token to the chunk's end. Its error is 1e-6 of these terms, of which dg is the part e^g: where a token's decay is
-// below kSteep, the chunk takes dg from what passes that token. gdr_prep leaves X, M, A and dA, two scans the states S and adjoints dS', and
-// gdr_grad takes the gradients, all chunks at once: 18 products a chunk, two CTAs an SM (of their operands' 104 KB), bound
-// by latency and by fetching its own instructions (8 x 12 x 1024 x 64 bf16: maps 102, scans 45, gradients 164 us).
+// below kSteep, the chunk takes dg from what passes that token. gdr_prep leaves X, M, A and dA, two scans the states S and
+// adjoints dS', and gdr_grad takes the gradients, all chunks at once: 18 products a chunk, two CTAs an SM (of their
+// operands' 104 KB), bound by latency and by fetching its own instructions (8 x 12 x 1024 x 64 bf16: maps 103, scans 45,
+// gradients 211 us).
 
 #pragma once
 
@@ -43,8 +44,8 @@ __host__ __device__ constexpr bool grad_one() { return NK * NV == 1 && sizeof(E)
 template <typename E, int NK, int NV>
 __host__ __device__ constexpr int grad_smem() { return ((NK + (grad_keeps<E>() ? NV : 0)) * planes<E>() + 6 * NV + (grad_one<E, NK, NV>() ? 5 : 3)) * kPlane; }
 
-// The sums are right to 1e-6 of their terms, that is of dg to e^2 as much or so; at -4 it would be 2e-4, at -12 a tenth. What passes a
-// token takes a third more of a call (8 x 12 x 1024 x 64 with all tokens below: 390 to 509 us).
+// Above it the sums' 1e-6 of their terms is e^2 times that of dg at most or so (at -4 it was 2e-4 of dg, at -12 a tenth). What
+// passes a token takes a third more of a call (8 x 12 x 1024 x 64 with all tokens below: 389 to 514 us).
 constexpr float kSteep = -2.f;
 
 // Summed over the four lanes that hold a row.
