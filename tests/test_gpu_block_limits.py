@@ -164,7 +164,7 @@ def test_rms_8_bits_are_those_of_the_quotient(d):
     x = torch.randn(1, 4000, d, generator=r).cuda()
     x[0, 7] = 0
     w = torch.randn(d, generator=r) * 2.0 ** torch.randint(-20, 20, (d,), generator=r)
-    for w in (w, w * 1e31, w * 1e-32):
+    for w in (w, w * 1e31, w * 1e-32, w * 1e-36):
         y, _, _ = F.rmsnorm_forward(x, w.cuda())
         y8, _, s = F.rmsnorm_forward(x, w.cuda(), out_dtype=torch.float8_e4m3fn)
         top = y.abs().amax(-1)

@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(MULTI ? kMost : 32 * kWarps) rms_fwd(const Arg
             const float exact = near < 3.4e38f ? fmaf(fmaf(-near, 448.f, top[0]), 1.f / 448.f, near) : near;  // its last bit
             const float scale = now.live ? exact : 0.f;
             if (first == 0) a.scales[here] = scale;
-            // The quotient, correctly rounded: by 1 / scale and what is left of it where both are finite (73 us for 16384 x 4096,
-            // 89 by division), else by division; a row of zeros stays 0.
-            const bool plain = !(scale >= 1e-37f && scale < 3.4e38f);
+            // The quotient, correctly rounded: by 1 / scale and what is left of the value (73 us for 16384 x 4096, 89 by division)
+            // where that is exact, 2^-48 of values down to scale / 1024 being no less than 2^-149; else by division. A row of
+            // zeros stays 0.
+            const bool plain = !(scale >= 1e-27f && scale < 3.4e38f);
             const float inv = plain ? 0.f : 1.f / scale;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
