@@ -727,7 +727,8 @@ __device__ __forceinline__ void times_decay(float (&acc)[8][4], const Scal& s, i
 
 // ---- the inverse of I + A, A strictly lower triangular in tile T, in its place: 16 x 16 diagonal blocks by
 // substitution, then twice the corner of a block pair, -Y22 A21 Y11, as products of tf32 pairs (the blocks are
-// too small for planes to pay; 22 bits, and with the product of both low parts no result's error is another). They are formed transposed, Y11^T A21^T first: its result is then the next product's A in registers.
+// too small for planes to pay; 22 bits, and with the product of both low parts no result's error is another). They are
+// formed transposed, Y11^T A21^T first: its result is then the next product's A in registers.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
